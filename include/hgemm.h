@@ -391,6 +391,132 @@ HGEMM_API int hgemm_trsm_noalloc(const hgemm_half_t *A, int64_t lda, const hgemm
                        cudaStream_t stream);
 
 /*
+ * The operators of a transformer's feed-forward block, y = x + W2·act(W1·LN(x) + b1) + b2:
+ * products whose epilogue carries the bias, the activation and the residual,
+ * their gradients, the layer norm in front of them, and activations kept in
+ * 8 bits for the backward pass. All matrices are row-major with a row pitch
+ * in elements; a weight W is N×K with one output feature per row (hgemm's
+ * column-major B). Values are FP16, statistics and the gradients of vectors
+ * FP32; sums and all arithmetic are FP32, each FP16 output is rounded once.
+ * Streams, ownership, status codes and the watchdog are those of hgemm;
+ * sizes are at most HGEMM_MAX_DIM, pitches at least a row; outputs may
+ * overlap neither inputs nor each other (HGEMM_ERR_ALIAS) except where a
+ * call says so; FP16 pointers are 2-byte and FP32 pointers 4-byte aligned.
+ * Any pitch and alignment is computed; pitches that are multiples of 8
+ * elements and 16-byte-aligned bases take the faster paths.
+ *
+ * Activations f, on FP32 values: NONE u; RELU max(u, 0) (a NaN stays one,
+ * derivative 0 at 0); GELU u·(1 + tanh(√(2/π)·(u + 0.044715·u³)))/2;
+ * SILU u/(1 + e⁻ᵘ); GELU_ERF u·Φ(u), Φ the normal distribution function.
+ *
+ * The 8-bit form of an M×N matrix U (a "checkpoint"): codes, M×N signed
+ * bytes with row pitch ldq, and scales, ⌈N/64⌉×M FP32 values with pitch
+ * lds ≥ M. Columns 64g .. 64g+63 of row m share s = scales[g·lds + m] =
+ * max|u| / 127, and codes hold rint(u · (127 / max|u|)) (FP32 operations in
+ * that order, to nearest even): a value read back, code·s, is within s/2 of
+ * u up to FP32 rounding. A group whose largest magnitude is below 2^-100 has
+ * s = 0 and codes 0; a group that holds an infinity or a NaN has s = NaN and
+ * codes 0, so all of it reads back as NaN.
+ */
+#define HGEMM_ACT_NONE 0
+#define HGEMM_ACT_RELU 1
+#define HGEMM_ACT_GELU 2
+#define HGEMM_ACT_SILU 3
+#define HGEMM_ACT_GELU_ERF 4
+#define HGEMM_CKPT8_GROUP 64 /* columns that share a scale */
+
+/*
+ * hgemm_linear — Y = f(U) + R with U = X·Wᵀ + bias, X M×K, W N×K, Y M×N:
+ *
+ *   bias    N FP16 values, or NULL
+ *   act     HGEMM_ACT_*
+ *   R       M×N, added after the activation, or NULL; R = Y with ldr = ldy
+ *           adds in place
+ *   codes, ldq, scales, lds
+ *           where U (before the activation, FP32) is kept in 8 bits, or NULL
+ *           both
+ *
+ * K = 0: U is the bias. M = 0 or N = 0: nothing to do.
+ * Returns HGEMM_OK, HGEMM_ERR_INVALID_ARG, HGEMM_ERR_ALIAS,
+ * HGEMM_ERR_UNSUPPORTED_DEVICE or HGEMM_ERR_CUDA, as hgemm does.
+ */
+HGEMM_API int hgemm_linear(const hgemm_half_t *X, int64_t ldx, const hgemm_half_t *W, int64_t ldw,
+                 const hgemm_half_t *bias, int act, const hgemm_half_t *R, int64_t ldr,
+                 hgemm_half_t *Y, int64_t ldy, int8_t *codes, int64_t ldq, float *scales,
+                 int64_t lds, int64_t M, int64_t N, int64_t K, cudaStream_t stream);
+
+/*
+ * hgemm_linear_dgrad — the gradient of a linear layer's input, carried
+ * through the activation that made that input. With dY M×N, W N×K and the
+ * 8-bit pre-activations Û (M×K) of the layer below:
+ *
+ *     dU = (dY·W) ⊙ f'(Û)      M×K
+ *     H  = f(Û)                 M×K, the layer's input rebuilt for
+ *                               hgemm_linear_wgrad; NULL: not wanted
+ *
+ * codes and scales NULL: dU = dY·W (act must be HGEMM_ACT_NONE and H NULL).
+ * N = 0: dY·W is 0. M = 0 or K = 0: nothing to do. Same return values.
+ */
+HGEMM_API int hgemm_linear_dgrad(const hgemm_half_t *dY, int64_t lddy, const hgemm_half_t *W, int64_t ldw,
+                       const int8_t *codes, int64_t ldq, const float *scales, int64_t lds, int act,
+                       hgemm_half_t *dU, int64_t lddu, hgemm_half_t *H, int64_t ldh, int64_t M,
+                       int64_t N, int64_t K, cudaStream_t stream);
+
+/*
+ * hgemm_linear_wgrad — the gradients of a linear layer's weight and bias:
+ * dW = dYᵀ·X (N×K FP16; with accumulate != 0, dW = dYᵀ·X + dW) and, unless
+ * dbias is NULL, dbias[n] = Σ_m dY(m, n) (N FP32 values; with accumulate
+ * added to). dY is M×N, X M×K. M = 0: the sums are empty (0, or unchanged
+ * with accumulate). The order of every sum is fixed: equal calls give equal
+ * bits. Same return values.
+ */
+HGEMM_API int hgemm_linear_wgrad(const hgemm_half_t *dY, int64_t lddy, const hgemm_half_t *X, int64_t ldx,
+                       hgemm_half_t *dW, int64_t lddw, float *dbias, int accumulate, int64_t M,
+                       int64_t N, int64_t K, cudaStream_t stream);
+
+/*
+ * hgemm_layernorm_forward — Y(m, d) = (X(m, d) − μ)·ρ·gamma[d] + beta[d], over
+ * rows of D values: μ the row's mean and ρ = 1/√(variance + eps), the
+ * variance that of the whole row (divided by D). gamma and beta hold D FP16
+ * values. mean and rstd receive μ and ρ, M FP32 values each, or are both
+ * NULL. eps ≥ 0. Y = X with ldy = ldx normalises in place. Same return
+ * values.
+ */
+HGEMM_API int hgemm_layernorm_forward(const hgemm_half_t *X, int64_t ldx, const hgemm_half_t *gamma,
+                            const hgemm_half_t *beta, float eps, hgemm_half_t *Y, int64_t ldy,
+                            float *mean, float *rstd, int64_t M, int64_t D, cudaStream_t stream);
+
+/*
+ * hgemm_layernorm_backward — with x̂ = (X − mean)·rstd and g = dY·gamma, rows
+ * of D values and mean(·) over a row:
+ *
+ *     dX     = rstd·(g − mean(g) − x̂·mean(g·x̂)) + R
+ *     dgamma = Σ_m dY ⊙ x̂,   dbeta = Σ_m dY        (D FP32 values each)
+ *
+ * R is the gradient that reaches X around the norm (the residual branch),
+ * M×D, or NULL; dX may be R or dY (same pitch). workspace: caller-owned,
+ * 16-byte aligned, at least hgemm_layernorm_backward_workspace_size(M, D)
+ * bytes, not used by other work until the stream has passed this call. The
+ * order of every sum is fixed. M = 0: dgamma = dbeta = 0. Same return values.
+ */
+HGEMM_API size_t hgemm_layernorm_backward_workspace_size(int64_t M, int64_t D);
+HGEMM_API int hgemm_layernorm_backward(const hgemm_half_t *dY, int64_t lddy, const hgemm_half_t *X, int64_t ldx,
+                             const hgemm_half_t *gamma, const float *mean, const float *rstd,
+                             const hgemm_half_t *R, int64_t ldr, hgemm_half_t *dX, int64_t lddx,
+                             float *dgamma, float *dbeta, void *workspace, size_t workspace_bytes,
+                             int64_t M, int64_t D, cudaStream_t stream);
+
+/*
+ * hgemm_ckpt8_save — X (M×N FP16) into its 8-bit form.
+ * hgemm_ckpt8_load — Y = f(Û) (M×N FP16, rounded once) from it, f an
+ * HGEMM_ACT_*. Same return values.
+ */
+HGEMM_API int hgemm_ckpt8_save(const hgemm_half_t *X, int64_t ldx, int8_t *codes, int64_t ldq, float *scales,
+                     int64_t lds, int64_t M, int64_t N, cudaStream_t stream);
+HGEMM_API int hgemm_ckpt8_load(const int8_t *codes, int64_t ldq, const float *scales, int64_t lds, int act,
+                     hgemm_half_t *Y, int64_t ldy, int64_t M, int64_t N, cudaStream_t stream);
+
+/*
  * hgemm_host — the same product for operands held in HOST memory.
  *
  * Copies hA -> dA (M*K values) and hB -> dB (N*K values), computes

@@ -34,6 +34,10 @@ __all__ = [
     "HGEMM_TRSM_RECURSIVE", "HGEMM_TRSM_CHAIN", "HGEMM_TRSM_CHAIN_FUSED", "HGEMM_TRSM_CHAIN_SPLIT",
     "HGEMM_A_ROW_MAJOR", "HGEMM_A_COL_MAJOR", "HGEMM_B_COL_MAJOR", "HGEMM_B_ROW_MAJOR",
     "HGEMM_INJECT_NONE", "HGEMM_INJECT_DROP_ARRIVAL", "matmul",
+    "hgemm_linear", "hgemm_linear_dgrad", "hgemm_linear_wgrad", "hgemm_layernorm_forward",
+    "hgemm_layernorm_backward", "hgemm_layernorm_backward_workspace_size", "hgemm_ckpt8_save", "hgemm_ckpt8_load",
+    "HGEMM_ACT_NONE", "HGEMM_ACT_RELU", "HGEMM_ACT_GELU", "HGEMM_ACT_SILU", "HGEMM_ACT_GELU_ERF",
+    "HGEMM_CKPT8_GROUP",
 ]
 
 HGEMM_OK = 0
@@ -57,6 +61,13 @@ HGEMM_A_ROW_MAJOR = 0
 HGEMM_A_COL_MAJOR = 1
 HGEMM_B_COL_MAJOR = 0
 HGEMM_B_ROW_MAJOR = 1
+
+HGEMM_ACT_NONE = 0
+HGEMM_ACT_RELU = 1
+HGEMM_ACT_GELU = 2
+HGEMM_ACT_SILU = 3
+HGEMM_ACT_GELU_ERF = 4
+HGEMM_CKPT8_GROUP = 64
 
 HGEMM_PATH_NONE = 0
 HGEMM_PATH_ZERO = 1
@@ -154,6 +165,20 @@ def load():
     lib.hgemm_launch_floor.restype = i32
     lib.hgemm_force_trsm_schedule.argtypes = [i32]
     lib.hgemm_force_trsm_schedule.restype = i32
+    f32 = ctypes.c_float
+    lib.hgemm_linear.argtypes = [vp, i64, vp, i64, vp, i32, vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i64, vp]
+    lib.hgemm_linear_dgrad.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, i32, vp, i64, vp, i64, i64, i64, i64, vp]
+    lib.hgemm_linear_wgrad.argtypes = [vp, i64, vp, i64, vp, i64, vp, i32, i64, i64, i64, vp]
+    lib.hgemm_layernorm_forward.argtypes = [vp, i64, vp, vp, f32, vp, i64, vp, vp, i64, i64, vp]
+    lib.hgemm_layernorm_backward.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp, vp, vp,
+                                             ctypes.c_size_t, i64, i64, vp]
+    lib.hgemm_ckpt8_save.argtypes = [vp, i64, vp, i64, vp, i64, i64, i64, vp]
+    lib.hgemm_ckpt8_load.argtypes = [vp, i64, vp, i64, i32, vp, i64, i64, i64, vp]
+    for name in ("hgemm_linear", "hgemm_linear_dgrad", "hgemm_linear_wgrad", "hgemm_layernorm_forward",
+                 "hgemm_layernorm_backward", "hgemm_ckpt8_save", "hgemm_ckpt8_load"):
+        getattr(lib, name).restype = i32
+    lib.hgemm_layernorm_backward_workspace_size.argtypes = [i64, i64]
+    lib.hgemm_layernorm_backward_workspace_size.restype = ctypes.c_size_t
     for name in ("hgemm_debug_build", "hgemm_debug_code", "hgemm_debug_selftest", "hgemm_trsm_last_schedule"):
         getattr(lib, name).argtypes = []
         getattr(lib, name).restype = i32
@@ -412,3 +437,101 @@ def matmul(a, b_cols, out=None, stream=None):
         raise ValueError(f"out must be ({M}, {N})")
     hgemm(a, b_cols, out, M, N, K, stream)
     return out
+
+
+# ------------------------------------------- the feed-forward block's operators
+
+def _typed(name, dtype, *tensors) -> None:
+    """Each tensor (None or a raw address passes) is on the device and of `dtype`."""
+    for x in tensors:
+        if x is None or isinstance(x, int):
+            continue
+        if x.dtype != dtype:
+            raise TypeError(f"{name}: expected {dtype}, got {x.dtype}")
+        if not x.is_cuda:
+            raise ValueError(f"{name}: expected a CUDA tensor")
+
+
+def hgemm_linear(X, ldx: int, W, ldw: int, bias, act: int, R, ldr: int, Y, ldy: int, M: int, N: int, K: int,
+                 codes=None, ldq: int = 0, scales=None, lds: int = 0, stream=None) -> None:
+    """Y = f(X·Wᵀ + bias) + R, f an HGEMM_ACT_*; with codes and scales the
+    pre-activations are kept in 8 bits too (see hgemm.h)."""
+    import torch
+    _typed("hgemm_linear", torch.float16, X, W, bias, R, Y)
+    _typed("hgemm_linear codes", torch.int8, codes)
+    _typed("hgemm_linear scales", torch.float32, scales)
+    _raise_on(load().hgemm_linear(_ptr(X), ldx, _ptr(W), ldw, _ptr(bias), act, _ptr(R), ldr, _ptr(Y), ldy,
+                                  _ptr(codes), ldq, _ptr(scales), lds, M, N, K, _stream(stream)), "hgemm_linear")
+
+
+def hgemm_linear_dgrad(dY, lddy: int, W, ldw: int, codes, ldq: int, scales, lds: int, act: int, dU, lddu: int,
+                       H, ldh: int, M: int, N: int, K: int, stream=None) -> None:
+    """dU = (dY·W) ⊙ f'(Û) and H = f(Û), Û the 8-bit pre-activations (see hgemm.h)."""
+    import torch
+    _typed("hgemm_linear_dgrad", torch.float16, dY, W, dU, H)
+    _typed("hgemm_linear_dgrad codes", torch.int8, codes)
+    _typed("hgemm_linear_dgrad scales", torch.float32, scales)
+    _raise_on(load().hgemm_linear_dgrad(_ptr(dY), lddy, _ptr(W), ldw, _ptr(codes), ldq, _ptr(scales), lds, act,
+                                        _ptr(dU), lddu, _ptr(H), ldh, M, N, K, _stream(stream)),
+              "hgemm_linear_dgrad")
+
+
+def hgemm_linear_wgrad(dY, lddy: int, X, ldx: int, dW, lddw: int, dbias, accumulate: bool, M: int, N: int, K: int,
+                       stream=None) -> None:
+    """dW = dYᵀ·X and dbias = Σ_rows dY, or added to both (see hgemm.h)."""
+    import torch
+    _typed("hgemm_linear_wgrad", torch.float16, dY, X, dW)
+    _typed("hgemm_linear_wgrad dbias", torch.float32, dbias)
+    _raise_on(load().hgemm_linear_wgrad(_ptr(dY), lddy, _ptr(X), ldx, _ptr(dW), lddw, _ptr(dbias),
+                                        int(bool(accumulate)), M, N, K, _stream(stream)), "hgemm_linear_wgrad")
+
+
+def hgemm_layernorm_forward(X, ldx: int, gamma, beta, eps: float, Y, ldy: int, mean, rstd, M: int, D: int,
+                            stream=None) -> None:
+    """Y = (X − mean)·rstd·gamma + beta over rows of D values (see hgemm.h)."""
+    import torch
+    _typed("hgemm_layernorm_forward", torch.float16, X, gamma, beta, Y)
+    _typed("hgemm_layernorm_forward statistics", torch.float32, mean, rstd)
+    _raise_on(load().hgemm_layernorm_forward(_ptr(X), ldx, _ptr(gamma), _ptr(beta), eps, _ptr(Y), ldy, _ptr(mean),
+                                             _ptr(rstd), M, D, _stream(stream)), "hgemm_layernorm_forward")
+
+
+def hgemm_layernorm_backward_workspace_size(M: int, D: int) -> int:
+    """Bytes of device workspace hgemm_layernorm_backward needs."""
+    return int(load().hgemm_layernorm_backward_workspace_size(M, D))
+
+
+def hgemm_layernorm_backward(dY, lddy: int, X, ldx: int, gamma, mean, rstd, R, ldr: int, dX, lddx: int, dgamma,
+                             dbeta, workspace, M: int, D: int, workspace_bytes: int | None = None,
+                             stream=None) -> None:
+    """dX, dgamma and dbeta of a layer norm, R added to dX (see hgemm.h); the
+    workspace's size defaults to the tensor's bytes."""
+    import torch
+    _typed("hgemm_layernorm_backward", torch.float16, dY, X, gamma, R, dX)
+    _typed("hgemm_layernorm_backward statistics", torch.float32, mean, rstd, dgamma, dbeta)
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size() if hasattr(workspace, "numel") else 0
+    _raise_on(load().hgemm_layernorm_backward(_ptr(dY), lddy, _ptr(X), ldx, _ptr(gamma), _ptr(mean), _ptr(rstd),
+                                              _ptr(R), ldr, _ptr(dX), lddx, _ptr(dgamma), _ptr(dbeta),
+                                              _ptr(workspace), workspace_bytes, M, D, _stream(stream)),
+              "hgemm_layernorm_backward")
+
+
+def hgemm_ckpt8_save(X, ldx: int, codes, ldq: int, scales, lds: int, M: int, N: int, stream=None) -> None:
+    """X into its 8-bit form (see hgemm.h)."""
+    import torch
+    _typed("hgemm_ckpt8_save", torch.float16, X)
+    _typed("hgemm_ckpt8_save codes", torch.int8, codes)
+    _typed("hgemm_ckpt8_save scales", torch.float32, scales)
+    _raise_on(load().hgemm_ckpt8_save(_ptr(X), ldx, _ptr(codes), ldq, _ptr(scales), lds, M, N, _stream(stream)),
+              "hgemm_ckpt8_save")
+
+
+def hgemm_ckpt8_load(codes, ldq: int, scales, lds: int, act: int, Y, ldy: int, M: int, N: int, stream=None) -> None:
+    """Y = f(Û) from the 8-bit form, f an HGEMM_ACT_* (see hgemm.h)."""
+    import torch
+    _typed("hgemm_ckpt8_load codes", torch.int8, codes)
+    _typed("hgemm_ckpt8_load scales", torch.float32, scales)
+    _typed("hgemm_ckpt8_load", torch.float16, Y)
+    _raise_on(load().hgemm_ckpt8_load(_ptr(codes), ldq, _ptr(scales), lds, act, _ptr(Y), ldy, M, N,
+                                      _stream(stream)), "hgemm_ckpt8_load")

@@ -72,7 +72,9 @@ cudaError_t debug_words(int* (&out)[hg::kDebugWords]) {
   cudaError_t (*const get[hg::kDebugWords])(int**) = {hg::debug_word_tc,      hg::debug_word_tc2,
                                                       hg::debug_word_tc2w,    hg::debug_word_skinny,
                                                       hg::debug_word_generic, hg::debug_word_trsm,
-                                                      hg::debug_word_trileaf, hg::debug_word_chain};
+                                                      hg::debug_word_trileaf, hg::debug_word_chain,
+                                                      hg::debug_word_linear,  hg::debug_word_norm,
+                                                      hg::debug_word_ckpt8};
   for (int i = 0; i < hg::kDebugWords; ++i) {
     const cudaError_t e = get[i](&out[i]);
     if (e != cudaSuccess) return e;
@@ -266,6 +268,15 @@ int choose_path(const Gemm& g, const hg::DeviceProfile& prof, bool fused, int* s
 }  // namespace
 
 namespace hg {
+
+int call_device(CallDevice* out) {
+  DeviceState* dev = nullptr;
+  const int rc = current_device(&dev);
+  if (rc == HGEMM_OK) *out = CallDevice{dev->num_sms, t_ctx.status, g_timeout_ns.load(std::memory_order_relaxed)};
+  return rc;
+}
+
+int cuda_status(cudaError_t e) { return e == cudaSuccess ? HGEMM_OK : cuda_fail(e); }
 
 int choose_tma_path(int64_t M, int64_t N, int64_t K, const DeviceProfile& dev, int forced,
                     int forced_split, int forced_tile_n, bool fused, int* split, int* tile_n) {

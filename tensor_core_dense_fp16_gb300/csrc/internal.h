@@ -182,6 +182,75 @@ cudaError_t launch_trsm_leaf(const uint16_t* A, int64_t lda, uint16_t* X, int64_
                              int s, int64_t m, int num_sms, bool chained, bool fwd, cudaStream_t stream);
 
 
+// ------------------------------------------- feed-forward block operators
+
+// The epilogue of a linear layer's product (forward) or of its input's
+// gradient (backward); the definitions are in linear_epilogue.cuh.
+struct LinEpi {
+  int backward;              // 0: y = f(acc + bias) + res, u kept in 8 bits; 1: acc·f'(û), h = f(û)
+  int act;                   // HGEMM_ACT_*
+  const uint16_t* bias;      // forward: N values, or null
+  const uint16_t* res;       // forward: M×N, or null
+  int64_t ldr;
+  int8_t* codes;             // forward: written; backward: read; null: none
+  int64_t ldq;
+  float* scales;             // scales[g·lds + m]
+  int64_t lds;
+  uint16_t* h;               // backward: f(û), or null
+  int64_t ldh;
+};
+
+// Σ over the rows of dY (M×N): out[n], or out[n] + the sum.
+cudaError_t launch_column_sums(const uint16_t* dy, int64_t ld, int64_t M, int64_t N, float* out,
+                               bool accumulate, cudaStream_t stream);
+// C = epilogue(A·B): A(i,k) at A[i·sai + k·sak], B(k,j) at B[k·sbk + j·sbj].
+struct SimpleProduct {
+  const uint16_t* A;
+  const uint16_t* B;
+  uint16_t* C;
+  int64_t M, N, K, sai, sak, sbk, sbj, ldc;
+  LinEpi epi;
+};
+cudaError_t launch_linear_simple(const SimpleProduct& p, cudaStream_t stream);
+
+struct NormArgs {
+  const uint16_t* x;
+  int64_t ldx;
+  const uint16_t* gamma;
+  const uint16_t* beta;      // forward
+  float eps;                 // forward
+  uint16_t* y;               // forward: y; backward: dx
+  int64_t ldy;
+  float* mean;               // forward: written, or null; backward: read
+  float* rstd;
+  const uint16_t* dy;        // backward
+  int64_t lddy;
+  const uint16_t* res;       // backward, or null
+  int64_t ldr;
+  float* dgamma;             // backward
+  float* dbeta;
+  float* work;               // backward: partial sums
+  int64_t M, D;
+};
+cudaError_t launch_layernorm_forward(const NormArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_layernorm_backward(const NormArgs& a, int num_sms, cudaStream_t stream);
+size_t layernorm_backward_workspace(int64_t M, int64_t D);
+
+cudaError_t launch_ckpt8_save(const uint16_t* x, int64_t ldx, int8_t* codes, int64_t ldq, float* scales,
+                              int64_t lds, int64_t M, int64_t N, cudaStream_t stream);
+cudaError_t launch_ckpt8_load(const int8_t* codes, int64_t ldq, const float* scales, int64_t lds, int act,
+                              uint16_t* y, int64_t ldy, int64_t M, int64_t N, cudaStream_t stream);
+
+// What an entry point outside hgemm_api.cu needs of a call: the current
+// device checked (HGEMM_OK or an error status), and a CUDA error as a status.
+struct CallDevice {
+  int num_sms;
+  int* status;
+  unsigned long long timeout_ns;
+};
+int call_device(CallDevice* out);
+int cuda_status(cudaError_t e);
+
 // Address of the device watchdog word on the current device.
 cudaError_t status_word_address(int** addr);
 
@@ -195,7 +264,10 @@ cudaError_t debug_word_generic(int** out);
 cudaError_t debug_word_trsm(int** out);
 cudaError_t debug_word_trileaf(int** out);
 cudaError_t debug_word_chain(int** out);
-constexpr int kDebugWords = 8;
+cudaError_t debug_word_linear(int** out);
+cudaError_t debug_word_norm(int** out);
+cudaError_t debug_word_ckpt8(int** out);
+constexpr int kDebugWords = 11;
 
 // Co-residency limits of the cluster kernels on one device, measured once
 // (or nominal GB300 figures when no device has been queried).
