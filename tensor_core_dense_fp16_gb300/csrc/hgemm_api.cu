@@ -121,6 +121,12 @@ struct Gemm {
   // itself: the TMA paths only (the generic kernel reads C_old from C)
   const void* c_src = nullptr;
   int64_t ld_src = 0;
+  // a linear layer's epilogue instead of EpiArgs (null: none)
+  const hg::LinEpi* lin = nullptr;
+  hg::Epilogue kind(const hg::EpiArgs& epi) const {
+    if (lin) return lin->backward ? hg::kEpiLinearGrad : hg::kEpiLinear;
+    return epi.mode != 0 ? hg::kEpiFused : hg::kEpiPlain;
+  }
 };
 
 Gemm dense(const void* A, const void* B, void* C, int64_t M, int64_t N, int64_t K) {
@@ -239,12 +245,22 @@ int validate(const Gemm& g) {
   return HGEMM_OK;
 }
 
+// The linear epilogue of the TMA paths reads and writes eight columns at a
+// time: 16 bytes of FP16, 8 bytes of codes.
+bool linear_ok(const hg::LinEpi& e) {
+  auto rows = [](const void* p, int64_t ld, uintptr_t bytes) {
+    return !p || ((reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0 && ld % 8 == 0);
+  };
+  return rows(e.res, e.ldr, 16) && rows(e.h, e.ldh, 16) && rows(e.codes, e.ldq, 8);
+}
+
 // TMA needs 16-byte-aligned bases and row pitches; the epilogue's 16-byte
 // reads of C need N to be a multiple of 8 as well.
 bool tma_ok(const Gemm& g) {
   auto al16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
   return al16(g.A) && al16(g.B) && al16(g.C) && g.lda % 8 == 0 && g.ldb % 8 == 0 &&
-         g.ldc % 8 == 0 && g.N % 8 == 0 && (!g.c_src || (al16(g.c_src) && g.ld_src % 8 == 0));
+         g.ldc % 8 == 0 && g.N % 8 == 0 && (!g.c_src || (al16(g.c_src) && g.ld_src % 8 == 0)) &&
+         (!g.lin || linear_ok(*g.lin));
 }
 
 int choose_path(const Gemm& g, const hg::DeviceProfile& prof, bool fused, int* split, int* tile_n) {
@@ -262,6 +278,8 @@ int choose_path(const Gemm& g, const hg::DeviceProfile& prof, bool fused, int* s
   // them as MN-major tiles; the single-CTA kernel takes K-major ones only
   if ((g.a_mn || g.b_mn) && (path == HGEMM_PATH_TC || path == HGEMM_PATH_TC_NARROW))
     return HGEMM_PATH_TC_PAIR;
+  // the wide kernel has no linear epilogue (only a forced path gets here)
+  if (g.lin && path == HGEMM_PATH_TC_WIDE) return HGEMM_PATH_TC_PAIR;
   return path;
 }
 
@@ -445,8 +463,9 @@ int run_tc(const Gemm& g, const hg::EpiArgs& epi, const DeviceState& dev, cudaSt
   args.epi = epi;
   args.C = static_cast<const uint16_t*>(g.c_src ? g.c_src : C);  // C_old, for a fused epilogue
   args.ldc = g.c_src ? g.ld_src : g.ldc;
-  cudaError_t e = bn == hg::kNarrowBN ? hg::launch_tc_128x64(ma, mb, mc, args, stream)
-                                      : hg::launch_tc_128x256(ma, mb, mc, args, stream);
+  if (g.lin) args.lin = *g.lin;
+  cudaError_t e = bn == hg::kNarrowBN ? hg::launch_tc_128x64(ma, mb, mc, args, g.kind(epi), stream)
+                                      : hg::launch_tc_128x256(ma, mb, mc, args, g.kind(epi), stream);
   return e == cudaSuccess ? HGEMM_OK : cuda_fail(e);
 }
 
@@ -512,6 +531,7 @@ int run_tc_pair(const Gemm& g, const hg::EpiArgs& epi, const DeviceState& dev,
   args.epi = epi;
   args.C = static_cast<const uint16_t*>(g.c_src ? g.c_src : C);  // C_old, for a fused epilogue
   args.ldc = g.c_src ? g.ld_src : g.ldc;
+  if (g.lin) args.lin = *g.lin;
   args.a_mn = g.a_mn ? 1 : 0;
   args.b_mn = g.b_mn ? 1 : 0;
   CUtensorMap ma, mb, mbp, mc;
@@ -530,7 +550,7 @@ int run_tc_pair(const Gemm& g, const hg::EpiArgs& epi, const DeviceState& dev,
     if ((rc = encode_map(&mbp, B, N, K, g.ldb, args.part_cols / 2, hg::kTcBK)) != HGEMM_OK) return rc;
   }
   if ((rc = encode_map(&mc, C, M, N, g.ldc, hg::kEpiRows, hg::kEpiCols)) != HGEMM_OK) return rc;
-  cudaError_t e = hg::launch_tc_pair(ma, mb, mbp, mc, args, stream);
+  cudaError_t e = hg::launch_tc_pair(ma, mb, mbp, mc, args, g.kind(epi), stream);
   return e == cudaSuccess ? HGEMM_OK : cuda_fail(e);
 }
 
@@ -570,6 +590,7 @@ int run_tc_wide(const Gemm& g, const hg::EpiArgs& epi, const DeviceState& dev,
   args.epi = epi;
   args.C = static_cast<const uint16_t*>(g.c_src ? g.c_src : C);  // C_old, for a fused epilogue
   args.ldc = g.c_src ? g.ld_src : g.ldc;
+  if (g.lin) args.lin = *g.lin;
   args.a_mn = g.a_mn ? 1 : 0;
   args.b_mn = g.b_mn ? 1 : 0;
   cudaError_t e = hg::launch_tc_wide(ma, mb, mc, args, stream);
@@ -611,20 +632,22 @@ int run_skinny(const Gemm& g, int split, int tile_n, const hg::EpiArgs& epi, con
   args.epi = epi;
   args.C = static_cast<const uint16_t*>(g.c_src ? g.c_src : C);  // C_old, for a fused epilogue
   args.ldc = g.c_src ? g.ld_src : g.ldc;
+  if (g.lin) args.lin = *g.lin;
   args.a_mn = g.a_mn ? 1 : 0;
   args.b_mn = g.b_mn ? 1 : 0;
-  cudaError_t e = hg::launch_skinny(split, tile_n, ma, mb, mc, args, stream);
+  cudaError_t e = hg::launch_skinny(split, tile_n, ma, mb, mc, args, g.kind(epi), stream);
   return e == cudaSuccess ? HGEMM_OK : cuda_fail(e);
 }
 
 int dispatch(const Gemm& g, const hg::EpiArgs& epi, const DeviceState& dev, cudaStream_t stream) {
   cudaError_t e;
   int split = 1, tile_n = hg::kPairBN;
-  switch (choose_path(g, dev.prof, epi.mode != 0, &split, &tile_n)) {
+  switch (choose_path(g, dev.prof, g.kind(epi) != hg::kEpiPlain, &split, &tile_n)) {
     case HGEMM_PATH_NONE:
       return HGEMM_OK;
     case HGEMM_PATH_ZERO:
       if (g.c_src) return HGEMM_ERR_INVALID_ARG;  // the empty sum reads C_old from C
+      if (g.lin) return hg::cuda_status(hg::launch_linear_empty(static_cast<uint16_t*>(g.C), g.ldc, g.M, g.N, *g.lin, stream));
       e = hg::launch_empty_sum(static_cast<uint16_t*>(g.C), g.M, g.N, g.ldc, epi, stream);
       return e == cudaSuccess ? HGEMM_OK : cuda_fail(e);
     case HGEMM_PATH_TC:
@@ -642,6 +665,10 @@ int dispatch(const Gemm& g, const hg::EpiArgs& epi, const DeviceState& dev, cuda
       hg::PlainArgs pa{static_cast<const uint16_t*>(g.A), static_cast<const uint16_t*>(g.B),
                        static_cast<uint16_t*>(g.C), g.M, g.N, g.K, g.lda, g.ldb, g.ldc,
                        t_ctx.status, g_timeout_ns.load(), epi, g.a_mn ? 1 : 0, g.b_mn ? 1 : 0};
+      if (g.lin) {
+        pa.kind = g.kind(epi);
+        pa.lin = *g.lin;
+      }
       e = hg::launch_generic(pa, dev.num_sms, stream);
       return e == cudaSuccess ? HGEMM_OK : cuda_fail(e);
     }
@@ -706,6 +733,20 @@ int trmm_pipe(int dev, TrmmPipe** out) {
 }
 
 }  // namespace
+
+namespace hg {
+
+int run_linear(const LinearProduct& p, cudaStream_t stream) {
+  DeviceState* dev = nullptr;
+  const int rc = current_device(&dev);
+  if (rc != HGEMM_OK) return rc;
+  Gemm g{p.A, p.B, p.C, p.M, p.N, p.K, p.lda, p.ldb, p.ldc};
+  g.b_mn = p.b_mn;
+  g.lin = &p.epi;
+  return dispatch(g, kPlainEpilogue, *dev, stream);
+}
+
+}  // namespace hg
 
 extern "C" {
 

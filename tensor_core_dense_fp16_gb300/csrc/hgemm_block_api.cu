@@ -70,12 +70,9 @@ int hgemm_linear(const hgemm_half_t* X, int64_t ldx, const hgemm_half_t* W, int6
   if ((overlap(y, r) && !same(y, r)) || overlap(q, r) || overlap(s, r)) return HGEMM_ERR_ALIAS;
   if (overlap(y, q) || overlap(y, s) || overlap(q, s)) return HGEMM_ERR_ALIAS;
   if (M == 0 || N == 0) return HGEMM_OK;
-  hg::CallDevice dev;
-  const int rc = hg::call_device(&dev);
-  if (rc != HGEMM_OK) return rc;
-  hg::SimpleProduct p{X, W, Y, M, N, K, ldx, 1, 1, ldw, ldy,
-                      hg::LinEpi{0, act, bias, R, ldr, codes, ldq, scales, lds, nullptr, 0}};
-  return hg::cuda_status(hg::launch_linear_simple(p, stream));
+  const hg::LinearProduct p{X, ldx, W, ldw, false, Y, ldy, M, N, K,
+                            hg::LinEpi{0, act, bias, R, ldr, codes, ldq, scales, lds, nullptr, 0}};
+  return hg::run_linear(p, stream);
 }
 
 int hgemm_linear_dgrad(const hgemm_half_t* dY, int64_t lddy, const hgemm_half_t* W, int64_t ldw,
@@ -96,13 +93,10 @@ int hgemm_linear_dgrad(const hgemm_half_t* dY, int64_t lddy, const hgemm_half_t*
       if (overlap(o, v)) return HGEMM_ERR_ALIAS;
   if (overlap(du, h)) return HGEMM_ERR_ALIAS;
   if (M == 0 || K == 0) return HGEMM_OK;
-  hg::CallDevice dev;
-  const int rc = hg::call_device(&dev);
-  if (rc != HGEMM_OK) return rc;
-  hg::SimpleProduct p{dY, W, dU, M, K, N, lddy, 1, ldw, 1, lddu,
-                      hg::LinEpi{1, act, nullptr, nullptr, 0, const_cast<int8_t*>(codes), ldq,
-                                 const_cast<float*>(scales), lds, H, ldh}};
-  return hg::cuda_status(hg::launch_linear_simple(p, stream));
+  const hg::LinearProduct p{dY, lddy, W, ldw, true, dU, lddu, M, K, N,
+                            hg::LinEpi{1, act, nullptr, nullptr, 0, const_cast<int8_t*>(codes), ldq,
+                                       const_cast<float*>(scales), lds, H, ldh}};
+  return hg::run_linear(p, stream);
 }
 
 int hgemm_linear_wgrad(const hgemm_half_t* dY, int64_t lddy, const hgemm_half_t* X, int64_t ldx, hgemm_half_t* dW,

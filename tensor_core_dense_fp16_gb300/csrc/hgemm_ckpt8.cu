@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int64_t n = g * kCkptGroup + lane + 32 * i;
-      if (n < N) codes[m * ldq + n] = static_cast<int8_t>(ckpt_code(u[i], inv));
+      if (n < N) codes[m * ldq + n] = static_cast<int8_t>(inv == 0.f ? 0u : ckpt_code(u[i], inv));
     }
     if (lane == 0) scales[g * lds + m] = scale;
   }

@@ -33,6 +33,7 @@
 
 #include "internal.h"
 #include "kernel_common.cuh"
+#include "linear_epilogue.cuh"
 #include "ptx.cuh"
 
 namespace hg {
@@ -100,7 +101,7 @@ __device__ __forceinline__ uint32_t f32_block_offset(int r, int c, int cols) {
   return static_cast<uint32_t>(r * cols * 4 + ((c ^ (r & 7)) << 4));
 }
 
-template <int SPLIT, int BN, bool FUSED>
+template <int SPLIT, int BN, int EPI>
 __global__ void __launch_bounds__(192, 1)
     hgemm_skinny_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                         const __grid_constant__ CUtensorMap tmC, const TcArgs p) {
@@ -273,7 +274,12 @@ __global__ void __launch_bounds__(192, 1)
   const int q = warp & 3;  // TMEM lanes / tile rows 32q .. 32q+31 of this CTA
   const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
   const int row = q * 32 + lane;
-  if (FUSED && warp >= 2)
+  if constexpr (EPI >= kEpiLinear) {
+    if (warp >= 2)
+      lin_prefetch_row<EPI>(p.lin, p.M, p.N, static_cast<int64_t>(mb) * Cfg::BM + half * Cfg::ROWS + row,
+                            static_cast<int64_t>(nb) * Cfg::BN + own_c0, own_cols);
+  }
+  if (EPI == kEpiFused && warp >= 2)
     prefetch_c_row(p.epi, p.C, p.M, p.N, p.ldc, static_cast<int64_t>(mb) * Cfg::BM + half * Cfg::ROWS + row,
                    static_cast<int64_t>(nb) * Cfg::BN + own_c0, own_cols);
   // ring layout for the exchange: receive slots first, then send staging
@@ -328,12 +334,11 @@ __global__ void __launch_bounds__(192, 1)
       const int x0 = nb * Cfg::BN + own_c0;
       const int y0 = mb * Cfg::BM + half * Cfg::ROWS + q * kEpiRows;
       uint8_t* cbuf = smem + Cfg::OFF_C + q * Cfg::C_WARP_BYTES;
-#pragma unroll 1
-      for (int c32 = 0; c32 < own_cols / 32; ++c32) {
+      // 32 columns of this CTA's range: the S partials added in slice order
+      auto sum32 = [&](int c32, float (&acc)[32]) {
         uint32_t own[32];
         tmem_ld_32x32b_x32(t_row + own_c0 + c32 * 32, own);
         tmem_ld_wait(own);
-        float acc[32];
         for (int sl = 0; sl < SPLIT; ++sl) {
           if (sl == slice) {
 #pragma unroll
@@ -360,11 +365,26 @@ __global__ void __launch_bounds__(192, 1)
             }
           }
         }
+      };
+#pragma unroll 1
+      for (int c64 = 0; EPI >= kEpiLinear && c64 < own_cols / 64; ++c64) {
+        float a0[32], a1[32];
+        sum32(2 * c64, a0);
+        sum32(2 * c64 + 1, a1);
+        if constexpr (EPI >= kEpiLinear)
+          lin_stage_row64<EPI>(cbuf + c64 * (kEpiRows * 128) + lane * 128, lane,
+                               reinterpret_cast<uint32_t(&)[32]>(a0), reinterpret_cast<uint32_t(&)[32]>(a1), p.lin,
+                               p.M, p.N, static_cast<int64_t>(y0) + lane, x0 + c64 * 64);
+      }
+#pragma unroll 1
+      for (int c32 = 0; EPI < kEpiLinear && c32 < own_cols / 32; ++c32) {
+        float acc[32];
+        sum32(c32, acc);
         // 32 FP16 columns (64 bytes) into the 128-byte-swizzled staging box
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           uint4 pk;
-          if constexpr (!FUSED) {
+          if constexpr (EPI == kEpiPlain) {
             pk.x = pack_half2(__float_as_uint(acc[8 * u]), __float_as_uint(acc[8 * u + 1]));
             pk.y = pack_half2(__float_as_uint(acc[8 * u + 2]), __float_as_uint(acc[8 * u + 3]));
             pk.z = pack_half2(__float_as_uint(acc[8 * u + 4]), __float_as_uint(acc[8 * u + 5]));
@@ -375,7 +395,7 @@ __global__ void __launch_bounds__(192, 1)
             for (int i = 0; i < 8; ++i) vb[i] = __float_as_uint(acc[8 * u + i]);
             const int64_t col0 = static_cast<int64_t>(x0) + c32 * 32 + 8 * u;
             pk = epi_pack8(vb, p.epi, load_c_old8(p.epi, p.C, p.M, p.N, p.ldc, y0 + lane, col0),
-                           load_bias8(p.epi, col0, p.N));
+                           load_bias8(p.epi.bias, col0, p.N));
           }
           const int chunk = c32 * 4 + u;  // 16-byte chunk within the row
           const int box = chunk >> 3;     // 64-column box
@@ -411,18 +431,20 @@ __global__ void __launch_bounds__(192, 1)
 
 template <int SPLIT, int BN>
 cudaError_t launch_split(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c,
-                         const TcArgs& args, cudaStream_t stream) {
+                         const TcArgs& args, Epilogue kind, cudaStream_t stream) {
   using Cfg = SkCfg<SPLIT, BN>;
-  static std::atomic<bool> attr_done[2][64];
-  const int fused = args.epi.mode != 0 ? 1 : 0;
-  auto kern = fused ? hgemm_skinny_kernel<SPLIT, BN, true> : hgemm_skinny_kernel<SPLIT, BN, false>;
+  static std::atomic<bool> attr_done[4][64];
+  auto kern = kind == kEpiPlain    ? hgemm_skinny_kernel<SPLIT, BN, kEpiPlain>
+              : kind == kEpiFused  ? hgemm_skinny_kernel<SPLIT, BN, kEpiFused>
+              : kind == kEpiLinear ? hgemm_skinny_kernel<SPLIT, BN, kEpiLinear>
+                                   : hgemm_skinny_kernel<SPLIT, BN, kEpiLinearGrad>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || !attr_done[fused][dev]) {
+  if (dev < 0 || dev >= 64 || !attr_done[kind][dev]) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) attr_done[fused][dev] = true;
+    if (dev >= 0 && dev < 64) attr_done[kind][dev] = true;
   }
   PdlLaunch l(dim3(static_cast<unsigned>(args.num_tiles * 2 * SPLIT)), dim3(Cfg::THREADS), Cfg::SMEM_BYTES,
               stream);
@@ -433,7 +455,7 @@ cudaError_t launch_split(const CUtensorMap& a, const CUtensorMap& b, const CUten
 template <int SPLIT, int BN>
 int max_clusters_split(int num_sms) {
   using Cfg = SkCfg<SPLIT, BN>;
-  auto kern = hgemm_skinny_kernel<SPLIT, BN, false>;
+  auto kern = hgemm_skinny_kernel<SPLIT, BN, kEpiPlain>;
   int n = 0;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES) ==
       cudaSuccess) {
@@ -471,16 +493,16 @@ int skinny_max_clusters(int split, int tile_n, int num_sms) {
 }
 
 cudaError_t launch_skinny(int split, int tile_n, const CUtensorMap& a, const CUtensorMap& b,
-                          const CUtensorMap& c, const TcArgs& args, cudaStream_t stream) {
-  if (tile_n == 128) return split == 2 ? launch_split<2, 128>(a, b, c, args, stream) : cudaErrorInvalidValue;
+                          const CUtensorMap& c, const TcArgs& args, Epilogue kind, cudaStream_t stream) {
+  if (tile_n == 128) return split == 2 ? launch_split<2, 128>(a, b, c, args, kind, stream) : cudaErrorInvalidValue;
   if (tile_n != 256) return cudaErrorInvalidValue;
   switch (split) {
     case 2:
-      return launch_split<2, 256>(a, b, c, args, stream);
+      return launch_split<2, 256>(a, b, c, args, kind, stream);
     case 3:
-      return launch_split<3, 256>(a, b, c, args, stream);
+      return launch_split<3, 256>(a, b, c, args, kind, stream);
     case 4:
-      return launch_split<4, 256>(a, b, c, args, stream);
+      return launch_split<4, 256>(a, b, c, args, kind, stream);
     default:
       return cudaErrorInvalidValue;
   }

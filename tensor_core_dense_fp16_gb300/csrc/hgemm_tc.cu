@@ -31,6 +31,7 @@
 
 #include "internal.h"
 #include "kernel_common.cuh"
+#include "linear_epilogue.cuh"
 #include "ptx.cuh"
 
 namespace hg {
@@ -79,7 +80,7 @@ struct TcCfg {
   static_assert(SMEM_BYTES <= 232448, "exceeds 227 KB of shared memory per CTA");
 };
 
-template <int BN, int STAGES, bool FUSED>
+template <int BN, int STAGES, int EPI>
 __global__ void __launch_bounds__(192, 1)
     hgemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmC, const TcArgs p) {
@@ -228,9 +229,12 @@ __global__ void __launch_bounds__(192, 1)
     for (int t = blockIdx.x; t < p.num_tiles; t += gridDim.x) {
       int mb, nb;
       tile_coords(t, p.num_m, p.num_n, p.group_m, mb, nb);
-      if constexpr (FUSED)
+      if constexpr (EPI == kEpiFused)
         prefetch_c_row(p.epi, p.C, p.M, p.N, p.ldc, static_cast<int64_t>(mb) * Cfg::BM + q * kEpiRows + lane,
                        static_cast<int64_t>(nb) * BN, BN);
+      else if constexpr (EPI == kEpiLinear)
+        lin_prefetch_row<EPI>(p.lin, p.M, p.N, static_cast<int64_t>(mb) * Cfg::BM + q * kEpiRows + lane,
+                              static_cast<int64_t>(nb) * BN, BN);
       int ok = 1;
       if (lane == 0) ok = wait_phase(accf_bar(acc), acc_phase, wd, kWdEpiAccFull) ? 1 : 0;
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -260,7 +264,11 @@ __global__ void __launch_bounds__(192, 1)
         uint8_t* buf = cbuf_base + cb * Cfg::C_BOX_BYTES;
         uint8_t* row = buf + lane * 128;
         // 128-byte swizzle: 16-byte chunk j of row r sits at chunk j ^ (r % 8)
-        stage_row64<FUSED>(row, lane, v0, v1, p.epi, p.C, p.M, p.N, p.ldc, static_cast<int64_t>(y0) + lane, x0);
+        if constexpr (EPI == kEpiLinear)
+          lin_stage_row64<EPI>(row, lane, v0, v1, p.lin, p.M, p.N, static_cast<int64_t>(y0) + lane, x0);
+        else
+          stage_row64<EPI == kEpiFused>(row, lane, v0, v1, p.epi, p.C, p.M, p.N, p.ldc,
+                                        static_cast<int64_t>(y0) + lane, x0);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -326,24 +334,28 @@ cudaError_t ensure_smem_attr(Kern kern, int bytes, std::atomic<bool>* done_per_d
 }  // namespace
 
 cudaError_t launch_tc_128x256(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c,
-                              const TcArgs& args, cudaStream_t stream) {
+                              const TcArgs& args, Epilogue kind, cudaStream_t stream) {
   using Cfg = TcCfg<256, 4>;
-  static std::atomic<bool> attr_done[2][64];
-  const bool fused = args.epi.mode != 0;
-  auto kern = fused ? hgemm_tc_kernel<256, 4, true> : hgemm_tc_kernel<256, 4, false>;
-  cudaError_t e = ensure_smem_attr(kern, Cfg::SMEM_BYTES, attr_done[fused ? 1 : 0]);
+  static std::atomic<bool> attr_done[3][64];
+  if (kind == kEpiLinearGrad) return cudaErrorInvalidValue;  // K-major operands only: the pair kernel's
+  auto kern = kind == kEpiPlain   ? hgemm_tc_kernel<256, 4, kEpiPlain>
+              : kind == kEpiFused ? hgemm_tc_kernel<256, 4, kEpiFused>
+                                  : hgemm_tc_kernel<256, 4, kEpiLinear>;
+  cudaError_t e = ensure_smem_attr(kern, Cfg::SMEM_BYTES, attr_done[kind]);
   if (e != cudaSuccess) return e;
   PdlLaunch l(dim3(static_cast<unsigned>(args.grid)), dim3(Cfg::THREADS), Cfg::SMEM_BYTES, stream);
   return cudaLaunchKernelEx(&l.cfg, kern, a, b, c, args);
 }
 
 cudaError_t launch_tc_128x64(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c,
-                             const TcArgs& args, cudaStream_t stream) {
+                             const TcArgs& args, Epilogue kind, cudaStream_t stream) {
   using Cfg = TcCfg<64, 8>;
-  static std::atomic<bool> attr_done[2][64];
-  const bool fused = args.epi.mode != 0;
-  auto kern = fused ? hgemm_tc_kernel<64, 8, true> : hgemm_tc_kernel<64, 8, false>;
-  cudaError_t e = ensure_smem_attr(kern, Cfg::SMEM_BYTES, attr_done[fused ? 1 : 0]);
+  static std::atomic<bool> attr_done[3][64];
+  if (kind == kEpiLinearGrad) return cudaErrorInvalidValue;  // K-major operands only: the pair kernel's
+  auto kern = kind == kEpiPlain   ? hgemm_tc_kernel<64, 8, kEpiPlain>
+              : kind == kEpiFused ? hgemm_tc_kernel<64, 8, kEpiFused>
+                                  : hgemm_tc_kernel<64, 8, kEpiLinear>;
+  cudaError_t e = ensure_smem_attr(kern, Cfg::SMEM_BYTES, attr_done[kind]);
   if (e != cudaSuccess) return e;
   PdlLaunch l(dim3(static_cast<unsigned>(args.grid)), dim3(Cfg::THREADS), Cfg::SMEM_BYTES, stream);
   return cudaLaunchKernelEx(&l.cfg, kern, a, b, c, args);

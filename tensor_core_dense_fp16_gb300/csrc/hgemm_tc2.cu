@@ -38,6 +38,7 @@
 
 #include "internal.h"
 #include "kernel_common.cuh"
+#include "linear_epilogue.cuh"
 #include "ptx.cuh"
 
 namespace hg {
@@ -117,12 +118,12 @@ __device__ __forceinline__ PairTile pair_tile(int t, const TcArgs& p) {
   return w;
 }
 
-template <int MAX_STAGES, bool FUSED>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FUSED ? 320 : 192, 1)
+template <int MAX_STAGES, int EPI>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EPI != kEpiPlain ? 320 : 192, 1)
     hgemm_tc2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmBh, const __grid_constant__ CUtensorMap tmC,
                      const TcArgs p) {
-  using Cfg = PairCfg<MAX_STAGES, FUSED ? 8 : 4>;
+  using Cfg = PairCfg<MAX_STAGES, EPI != kEpiPlain ? 8 : 4>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
@@ -300,7 +301,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FUSED ? 320 : 192, 1
       wait_drain(drain_bar, 0, wd);
     }
     __syncwarp();
-  } else if constexpr (FUSED) {
+  } else if constexpr (EPI != kEpiPlain) {
     // --------------------------------------- fused epilogue (both CTAs)
     // warps 2..5 take the even 64-column boxes of a tile, warps 6..9 the odd
     // ones; warp w reads TMEM lanes 32·(w % 4) .. +31
@@ -314,7 +315,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FUSED ? 320 : 192, 1
       const int chunks = w.ncols / kEpiCols;
       const int64_t grow = static_cast<int64_t>(w.mb) * Cfg::BM + static_cast<int>(rank) * Cfg::ROWS +
                            q * kEpiRows + lane;  // this lane's row of C
-      prefetch_c_row(p.epi, p.C, p.M, p.N, p.ldc, grow, w.n0, w.ncols);
+      if constexpr (EPI == kEpiFused)
+        prefetch_c_row(p.epi, p.C, p.M, p.N, p.ldc, grow, w.n0, w.ncols);
+      else
+        lin_prefetch_row<EPI>(p.lin, p.M, p.N, grow, w.n0, w.ncols);
       int ok = 1;
       if (lane == 0) ok = wait_phase(accf_bar(acc), acc_phase, wd, kWdEpiAccFull) ? 1 : 0;
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -350,7 +354,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FUSED ? 320 : 192, 1
         if (lane == 0) bulk_wait_group_read<0>();  // the previous store has read the box
         __syncwarp();
         // 128-byte swizzle: 16-byte chunk j of row r sits at chunk j ^ (r % 8)
-        stage_row64<true>(buf + lane * 128, lane, v0, v1, p.epi, p.C, p.M, p.N, p.ldc, grow, x0);
+        if constexpr (EPI == kEpiFused)
+          stage_row64<true>(buf + lane * 128, lane, v0, v1, p.epi, p.C, p.M, p.N, p.ldc, grow, x0);
+        else
+          lin_stage_row64<EPI>(buf + lane * 128, lane, v0, v1, p.lin, p.M, p.N, grow, x0);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -373,10 +380,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FUSED ? 320 : 192, 1
     for (int t = cluster_id; t < p.num_tiles; t += num_clusters) {
       const PairTile w = pair_tile(t, p);
       const int chunks = w.ncols / kEpiCols;
-      if constexpr (FUSED)
-        prefetch_c_row(p.epi, p.C, p.M, p.N, p.ldc,
-                       static_cast<int64_t>(w.mb) * Cfg::BM + static_cast<int>(rank) * Cfg::ROWS + q * kEpiRows + lane,
-                       w.n0, w.ncols);
       int ok = 1;
       if (lane == 0)
         ok = wait_phase(accf_bar(acc), acc_phase, wd, kWdEpiAccFull) ? 1 : 0;
@@ -406,7 +409,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FUSED ? 320 : 192, 1
         uint8_t* buf = cbuf_base + cb * Cfg::C_BOX_BYTES;
         uint8_t* row = buf + lane * 128;
         // 128-byte swizzle: 16-byte chunk j of row r sits at chunk j ^ (r % 8)
-        stage_row64<FUSED>(row, lane, v0, v1, p.epi, p.C, p.M, p.N, p.ldc, static_cast<int64_t>(y0) + lane, x0);
+        stage_row64<false>(row, lane, v0, v1, p.epi, p.C, p.M, p.N, p.ldc, static_cast<int64_t>(y0) + lane, x0);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -443,7 +446,7 @@ int pair_max_clusters(int num_sms) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return num_sms / 2;
   if (cached[dev] > 0) return cached[dev];
-  auto kern = hgemm_tc2_kernel<kPairStages, false>;
+  auto kern = hgemm_tc2_kernel<kPairStages, kEpiPlain>;
   int n = 0;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES) ==
       cudaSuccess) {
@@ -462,21 +465,23 @@ int pair_max_clusters(int num_sms) {
 int pair_smem_bytes() { return PairCfg<kPairStages>::SMEM_BYTES; }
 
 cudaError_t launch_tc_pair(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& b_part,
-                           const CUtensorMap& c, const TcArgs& args, cudaStream_t stream) {
+                           const CUtensorMap& c, const TcArgs& args, Epilogue kind, cudaStream_t stream) {
   using Cfg = PairCfg<kPairStages, 4>;
   using FusedCfg = PairCfg<kPairStages, 8>;
   static_assert(Cfg::SMEM_BYTES == FusedCfg::SMEM_BYTES, "both instantiations have the same footprint");
-  static std::atomic<bool> attr_done[2][64];
-  const int fused = args.epi.mode != 0 ? 1 : 0;
-  auto kern = fused ? hgemm_tc2_kernel<kPairStages, true> : hgemm_tc2_kernel<kPairStages, false>;
-  const int threads = fused ? FusedCfg::THREADS : Cfg::THREADS;
+  static std::atomic<bool> attr_done[4][64];
+  auto kern = kind == kEpiPlain    ? hgemm_tc2_kernel<kPairStages, kEpiPlain>
+              : kind == kEpiFused  ? hgemm_tc2_kernel<kPairStages, kEpiFused>
+              : kind == kEpiLinear ? hgemm_tc2_kernel<kPairStages, kEpiLinear>
+                                   : hgemm_tc2_kernel<kPairStages, kEpiLinearGrad>;
+  const int threads = kind != kEpiPlain ? FusedCfg::THREADS : Cfg::THREADS;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || !attr_done[fused][dev]) {
+  if (dev < 0 || dev >= 64 || !attr_done[kind][dev]) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) attr_done[fused][dev] = true;
+    if (dev >= 0 && dev < 64) attr_done[kind][dev] = true;
   }
   PdlLaunch l(dim3(static_cast<unsigned>(args.grid)), dim3(static_cast<unsigned>(threads)), Cfg::SMEM_BYTES,
               stream);

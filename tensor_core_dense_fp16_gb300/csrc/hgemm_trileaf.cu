@@ -385,7 +385,7 @@ __device__ __forceinline__ void store_row64(const uint32_t (&v0)[32], const uint
     const uint32_t* v = (j < 4) ? (v0 + 8 * j) : (v1 + 8 * (j - 4));
     uint4 pk;
     if constexpr (FUSED) {
-      pk = epi_pack8(v, e, load_c_old8(e, C, M, N, ldc, grow, x0 + 8 * j), load_bias8(e, x0 + 8 * j, N));
+      pk = epi_pack8(v, e, load_c_old8(e, C, M, N, ldc, grow, x0 + 8 * j), load_bias8(e.bias, x0 + 8 * j, N));
     } else {
       pk.x = pack_half2(v[0], v[1]);
       pk.y = pack_half2(v[2], v[3]);

@@ -33,6 +33,26 @@ struct EpiArgs {
   int mode;
 };
 
+// Which epilogue a product kernel is instantiated with: the accumulator
+// stored as it is, EpiArgs, or LinEpi forward or backward.
+enum Epilogue : int { kEpiPlain = 0, kEpiFused = 1, kEpiLinear = 2, kEpiLinearGrad = 3 };
+
+// The epilogue of a linear layer's product (forward) or of its input's
+// gradient (backward); the definitions are in linear_epilogue.cuh.
+struct LinEpi {
+  int backward;              // 0: y = f(acc + bias) + res, u kept in 8 bits; 1: acc·f'(û), h = f(û)
+  int act;                   // HGEMM_ACT_*
+  const uint16_t* bias;      // forward: N values, or null
+  const uint16_t* res;       // forward: M×N, or null
+  int64_t ldr;
+  int8_t* codes;             // forward: written; backward: read; null: none
+  int64_t ldq;
+  float* scales;             // scales[g·lds + m]
+  int64_t lds;
+  uint16_t* h;               // backward: f(û), or null
+  int64_t ldh;
+};
+
 // Everything a tensor-core launch needs besides the tensor maps.
 struct TcArgs {
   int M, N, K;
@@ -52,6 +72,7 @@ struct TcArgs {
   int64_t ldc;               // C's row pitch in elements
   int a_mn, b_mn;            // pair kernel: A stored M-contiguous (K×M), B stored
                              // N-contiguous (K×N); else K-contiguous
+  LinEpi lin;                // kEpiLinear and kEpiLinearGrad
   int batch_tiles;           // pair kernel: whole tiles per product of a batch of
                              // equal products in one launch (0: a single product)
   int batch_shift;           // product j of the batch is the first one with A's K,
@@ -69,6 +90,8 @@ struct PlainArgs {
   unsigned long long timeout_ns;
   EpiArgs epi;
   int a_mn = 0, b_mn = 0;    // A(i,k) at A[k*lda + i]; B(k,j) at B[k*ldb + j]
+  Epilogue kind = kEpiFused;  // kEpiFused (any EpiArgs mode), or one of the linear ones
+  LinEpi lin = {};
 };
 
 // The diagonal blocks ("leaves") of a triangular product, for one batched
@@ -110,12 +133,12 @@ struct PdlLaunch {
 // Launchers (each enqueues one kernel on `stream` and returns the launch
 // error, if any). Shared-memory attributes are set on first use per device.
 cudaError_t launch_tc_128x256(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c,
-                              const TcArgs& args, cudaStream_t stream);
+                              const TcArgs& args, Epilogue kind, cudaStream_t stream);
 cudaError_t launch_tc_128x64(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c,
-                             const TcArgs& args, cudaStream_t stream);
+                             const TcArgs& args, Epilogue kind, cudaStream_t stream);
 // b_part: the B map with part_cols / 2-row boxes, for the tile parts of the last wave.
 cudaError_t launch_tc_pair(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& b_part,
-                           const CUtensorMap& c, const TcArgs& args, cudaStream_t stream);
+                           const CUtensorMap& c, const TcArgs& args, Epilogue kind, cudaStream_t stream);
 // Largest number of co-resident 2-CTA clusters of the pair kernel.
 int pair_max_clusters(int num_sms);
 // Wide pair kernel: 256×512 tiles per CTA pair.
@@ -126,7 +149,7 @@ int wide_max_clusters(int num_sms);
 // of 2*split CTAs per 256×tile_n tile (args.num_tiles of them); tile_n 256
 // with 2, 3 or 4 slices, or tile_n 128 with 2.
 cudaError_t launch_skinny(int split, int tile_n, const CUtensorMap& a, const CUtensorMap& b,
-                          const CUtensorMap& c, const TcArgs& args, cudaStream_t stream);
+                          const CUtensorMap& c, const TcArgs& args, Epilogue kind, cudaStream_t stream);
 // Largest number of co-resident clusters of the split-K kernel.
 int skinny_max_clusters(int split, int tile_n, int num_sms);
 // K = 0: C := f(beta·C_old + bias) elementwise (plain mode: +0).
@@ -184,34 +207,26 @@ cudaError_t launch_trsm_leaf(const uint16_t* A, int64_t lda, uint16_t* X, int64_
 
 // ------------------------------------------- feed-forward block operators
 
-// The epilogue of a linear layer's product (forward) or of its input's
-// gradient (backward); the definitions are in linear_epilogue.cuh.
-struct LinEpi {
-  int backward;              // 0: y = f(acc + bias) + res, u kept in 8 bits; 1: acc·f'(û), h = f(û)
-  int act;                   // HGEMM_ACT_*
-  const uint16_t* bias;      // forward: N values, or null
-  const uint16_t* res;       // forward: M×N, or null
-  int64_t ldr;
-  int8_t* codes;             // forward: written; backward: read; null: none
-  int64_t ldq;
-  float* scales;             // scales[g·lds + m]
-  int64_t lds;
-  uint16_t* h;               // backward: f(û), or null
-  int64_t ldh;
-};
-
 // Σ over the rows of dY (M×N): out[n], or out[n] + the sum.
 cudaError_t launch_column_sums(const uint16_t* dy, int64_t ld, int64_t M, int64_t N, float* out,
                                bool accumulate, cudaStream_t stream);
-// C = epilogue(A·B): A(i,k) at A[i·sai + k·sak], B(k,j) at B[k·sbk + j·sbj].
-struct SimpleProduct {
+// K = 0: C = the epilogue of zeros.
+cudaError_t launch_linear_empty(uint16_t* C, int64_t ldc, int64_t M, int64_t N, const LinEpi& epi,
+                                cudaStream_t stream);
+
+// One product with a linear layer's epilogue, C (M×N) = epilogue(A·B) with B
+// N×K, or K×N when b_mn.
+struct LinearProduct {
   const uint16_t* A;
+  int64_t lda;
   const uint16_t* B;
+  int64_t ldb;
+  bool b_mn;
   uint16_t* C;
-  int64_t M, N, K, sai, sak, sbk, sbj, ldc;
+  int64_t ldc, M, N, K;
   LinEpi epi;
 };
-cudaError_t launch_linear_simple(const SimpleProduct& p, cudaStream_t stream);
+int run_linear(const LinearProduct& p, cudaStream_t stream);
 
 struct NormArgs {
   const uint16_t* x;

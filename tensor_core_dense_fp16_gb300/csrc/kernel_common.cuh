@@ -139,13 +139,13 @@ __device__ __forceinline__ void prefetch_c_row(const EpiArgs& e, const uint16_t*
 
 // The biases of columns col0 .. col0+7 (zeros past N or without a bias);
 // col0 is a multiple of 8, so with a 16-byte-aligned bias one vector load.
-__device__ __forceinline__ uint4 load_bias8(const EpiArgs& e, int64_t col0, int64_t N) {
-  if (!e.bias || col0 >= N) return make_uint4(0u, 0u, 0u, 0u);
-  if ((reinterpret_cast<uintptr_t>(e.bias) & 15u) == 0 && col0 + 8 <= N)
-    return __ldg(reinterpret_cast<const uint4*>(e.bias + col0));
+__device__ __forceinline__ uint4 load_bias8(const uint16_t* bias, int64_t col0, int64_t N) {
+  if (!bias || col0 >= N) return make_uint4(0u, 0u, 0u, 0u);
+  if ((reinterpret_cast<uintptr_t>(bias) & 15u) == 0 && col0 + 8 <= N)
+    return __ldg(reinterpret_cast<const uint4*>(bias + col0));
   uint16_t h[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) h[i] = col0 + i < N ? __ldg(e.bias + col0 + i) : static_cast<uint16_t>(0);
+  for (int i = 0; i < 8; ++i) h[i] = col0 + i < N ? __ldg(bias + col0 + i) : static_cast<uint16_t>(0);
   return make_uint4(h[0] | (static_cast<uint32_t>(h[1]) << 16), h[2] | (static_cast<uint32_t>(h[3]) << 16),
                     h[4] | (static_cast<uint32_t>(h[5]) << 16), h[6] | (static_cast<uint32_t>(h[7]) << 16));
 }
@@ -201,7 +201,7 @@ __device__ __forceinline__ void stage_row64(uint8_t* row, int lane, const uint32
   for (int j = 0; j < 8; ++j) {
     const uint32_t* v = (j < 4) ? (v0 + 8 * j) : (v1 + 8 * (j - 4));
     *reinterpret_cast<uint4*>(row + ((j ^ (lane & 7)) << 4)) =
-        epi_pack8(v, e, c_old[j], load_bias8(e, x0 + 8 * j, N));
+        epi_pack8(v, e, c_old[j], load_bias8(e.bias, x0 + 8 * j, N));
   }
 }
 
