@@ -187,6 +187,7 @@ int hgemm_layernorm_backward(const hgemm_half_t* dY, int64_t lddy, const hgemm_h
   a.mean = const_cast<float*>(mean), a.rstd = const_cast<float*>(rstd);
   a.dy = dY, a.lddy = lddy, a.res = R, a.ldr = ldr, a.dgamma = dgamma, a.dbeta = dbeta;
   a.work = static_cast<float*>(workspace), a.M = M, a.D = D;
+  a.status = dev.status, a.timeout_ns = dev.timeout_ns;
   return hg::cuda_status(hg::launch_layernorm_backward(a, dev.num_sms, stream));
 }
 

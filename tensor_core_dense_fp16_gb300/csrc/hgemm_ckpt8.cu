@@ -1,5 +1,10 @@
 // hgemm_ckpt8.cu — a matrix into its 8-bit form and back (hgemm_ckpt8_save,
 // hgemm_ckpt8_load; the form is defined in hgemm.h).
+//
+// Both are bound by memory: 2 bytes read and 1.06 written per value, or the
+// other way round. A warp takes 8 rows of a few groups at once, so that it
+// has eight independent loads in flight per lane and so that the scales of 8
+// rows, neighbours in memory, form one 32-byte sector per group.
 #include "debug.cuh"
 #include "linear_epilogue.cuh"
 #include "ptx.cuh"
@@ -7,36 +12,135 @@
 namespace hg {
 namespace {
 
-// One warp per group of 64 columns of a row, two columns per lane.
+constexpr int kRows = 8;      // rows of a warp's piece
+constexpr int kVecCols = 256;  // its columns, eight per lane: four groups of eight lanes
+
+// A warp's piece: rows [m0, m0 + 8), columns from n0.
+struct Piece {
+  int64_t m0, n0;
+};
+
+// Pieces are numbered along the columns first, so that neighbouring warps
+// read neighbouring memory.
+__device__ __forceinline__ bool piece_of(int64_t M, int64_t N, int cols, Piece& p) {
+  const int64_t per_row = (N + cols - 1) / cols;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  p.m0 = t / per_row * kRows;
+  p.n0 = t % per_row * cols;
+  return p.m0 < M;
+}
+
+// N, the pitches and the bases let eight columns be moved at once.
+__global__ void __launch_bounds__(256)
+    ckpt8_save_vec_kernel(const uint16_t* __restrict__ x, int64_t ldx, int8_t* __restrict__ codes, int64_t ldq,
+                          float* __restrict__ scales, int64_t lds, int64_t M, int64_t N) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  Piece p;
+  if (!piece_of(M, N, kVecCols, p)) return;
+  const int lane = threadIdx.x & 31;
+  const int64_t n = p.n0 + 8 * lane;
+  const bool in_n = n < N;
+  uint4 v[kRows];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r)
+    v[r] = in_n && p.m0 + r < M ? __ldg(reinterpret_cast<const uint4*>(x + (p.m0 + r) * ldx + n))
+                                : make_uint4(0u, 0u, 0u, 0u);
+  float mine = 0.f;  // lane 8g + r keeps the scale of group g, row r
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    const __half2* h = reinterpret_cast<const __half2*>(&v[r]);
+    float u[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(h[i]);
+      u[2 * i] = f.x;
+      u[2 * i + 1] = f.y;
+    }
+    float top = max_abs3(u[0], u[1], u[2]);
+    top = max_abs3(top, u[3], u[4]);
+    top = max_abs3(top, u[5], u[6]);
+    top = max_abs3(top, u[7], 0.f);
+    uint32_t bits = magnitude_bits(top);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, o));
+    float scale, inv;
+    ckpt_scale(bits, scale, inv);
+    if ((lane & 7) == r) mine = scale;
+    if (in_n && p.m0 + r < M)
+      *reinterpret_cast<uint2*>(codes + (p.m0 + r) * ldq + n) =
+          make_uint2(ckpt_word(u[0], u[1], u[2], u[3], inv), ckpt_word(u[4], u[5], u[6], u[7], inv));
+  }
+  const int64_t m = p.m0 + (lane & 7);
+  const int64_t g = n / kCkptGroup;  // (its last lanes may be past N)
+  if (g * kCkptGroup < N && m < M) scales[g * lds + m] = mine;
+}
+
+// Any pitch and alignment: one group per warp, two columns per lane.
 __global__ void __launch_bounds__(256)
     ckpt8_save_kernel(const uint16_t* __restrict__ x, int64_t ldx, int8_t* __restrict__ codes, int64_t ldq,
                       float* __restrict__ scales, int64_t lds, int64_t M, int64_t N) {
   grid_dependency_wait();
   grid_launch_dependents();
+  Piece p;
+  if (!piece_of(M, N, kCkptGroup, p)) return;
   const int lane = threadIdx.x & 31;
-  const int64_t groups = (N + kCkptGroup - 1) / kCkptGroup;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); t < M * groups;
-       t += warps) {
-    const int64_t m = t / groups, g = t - m * groups;
-    float u[2];
-    uint32_t top = 0;
+  float u[kRows][2];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int64_t n = g * kCkptGroup + lane + 32 * i;
-      u[i] = n < N ? __half2float(__ushort_as_half(x[m * ldx + n])) : 0.f;
-      top = max(top, magnitude_bits(u[i]));
+      const int64_t n = p.n0 + lane + 32 * i;
+      u[r][i] = n < N && p.m0 + r < M ? __half2float(__ushort_as_half(x[(p.m0 + r) * ldx + n])) : 0.f;
     }
-    top = __reduce_max_sync(0xffffffffu, top);
+  float mine = 0.f;
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
     float scale, inv;
-    ckpt_scale(top, scale, inv);
+    ckpt_scale(__reduce_max_sync(0xffffffffu, max(magnitude_bits(u[r][0]), magnitude_bits(u[r][1]))), scale, inv);
+    if (lane == r) mine = scale;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int64_t n = g * kCkptGroup + lane + 32 * i;
-      if (n < N) codes[m * ldq + n] = static_cast<int8_t>(inv == 0.f ? 0u : ckpt_code(u[i], inv));
+      const int64_t n = p.n0 + lane + 32 * i;
+      if (n < N && p.m0 + r < M)
+        codes[(p.m0 + r) * ldq + n] = static_cast<int8_t>(inv == 0.f ? 0u : ckpt_code(u[r][i], inv));
     }
-    if (lane == 0) scales[g * lds + m] = scale;
   }
+  if (lane < kRows && p.m0 + lane < M) scales[p.n0 / kCkptGroup * lds + p.m0 + lane] = mine;
+}
+
+__global__ void __launch_bounds__(256)
+    ckpt8_load_vec_kernel(const int8_t* __restrict__ codes, int64_t ldq, const float* __restrict__ scales,
+                          int64_t lds, int act, uint16_t* __restrict__ y, int64_t ldy, int64_t M, int64_t N) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  Piece p;
+  if (!piece_of(M, N, kVecCols, p)) return;
+  const int lane = threadIdx.x & 31;
+  const int64_t n = p.n0 + 8 * lane;
+  const bool in_n = n < N;
+  uint2 w[kRows];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r)
+    w[r] = in_n && p.m0 + r < M ? __ldg(reinterpret_cast<const uint2*>(codes + (p.m0 + r) * ldq + n))
+                                : make_uint2(0u, 0u);
+  const int64_t m = p.m0 + (lane & 7);
+  const int64_t g = n / kCkptGroup;  // (its last lanes may be past N)
+  const float mine = g * kCkptGroup < N && m < M ? __ldg(scales + g * lds + m) : 0.f;
+  with_activation(act, [&](auto a) {
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const float scale = __shfl_sync(0xffffffffu, mine, (lane & 24) | r);
+      uint32_t f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float v, df;
+        activate<decltype(a)::value, false>(ckpt_byte(i < 4 ? w[r].x : w[r].y, i & 3) * scale, v, df);
+        f[i] = __float_as_uint(v);
+      }
+      if (in_n && p.m0 + r < M) *reinterpret_cast<uint4*>(y + (p.m0 + r) * ldy + n) = pack8(f);
+    }
+  });
 }
 
 __global__ void __launch_bounds__(256)
@@ -44,32 +148,63 @@ __global__ void __launch_bounds__(256)
                       int act, uint16_t* __restrict__ y, int64_t ldy, int64_t M, int64_t N) {
   grid_dependency_wait();
   grid_launch_dependents();
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < M * N; i += stride) {
-    const int64_t m = i / N, n = i - m * N;
-    const float u = static_cast<float>(codes[m * ldq + n]) * scales[n / kCkptGroup * lds + m];
-    y[m * ldy + n] = __half_as_ushort(__float2half_rn(activate(u, act)));
+  Piece p;
+  if (!piece_of(M, N, kCkptGroup, p)) return;
+  const int lane = threadIdx.x & 31;
+  int8_t c[kRows][2];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t n = p.n0 + lane + 32 * i;
+      c[r][i] = n < N && p.m0 + r < M ? codes[(p.m0 + r) * ldq + n] : static_cast<int8_t>(0);
+    }
+  const int64_t m = p.m0 + (lane & 7);
+  const float mine = m < M ? scales[p.n0 / kCkptGroup * lds + m] : 0.f;
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    const float scale = __shfl_sync(0xffffffffu, mine, r);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t n = p.n0 + lane + 32 * i;
+      if (n < N && p.m0 + r < M)
+        y[(p.m0 + r) * ldy + n] =
+            __half_as_ushort(__float2half_rn(activate(static_cast<float>(c[r][i]) * scale, act)));
+    }
   }
 }
 
-unsigned blocks_for(int64_t items, int64_t per_block) {
-  const int64_t b = (items + per_block - 1) / per_block;
-  return static_cast<unsigned>(b < 1 ? 1 : (b > 65536 ? 65536 : b));
+bool aligned(const void* p, int64_t ld, uintptr_t bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0 && ld % 8 == 0;
+}
+
+// Blocks of eight warps over the pieces; 0: more than a grid holds.
+unsigned pieces_grid(int64_t M, int64_t N, int cols) {
+  const int64_t pieces = ((M + kRows - 1) / kRows) * ((N + cols - 1) / cols);
+  const int64_t blocks = (pieces + 7) / 8;
+  return blocks > 0x7FFFFFFF ? 0u : static_cast<unsigned>(blocks);
 }
 
 }  // namespace
 
 cudaError_t launch_ckpt8_save(const uint16_t* x, int64_t ldx, int8_t* codes, int64_t ldq, float* scales,
                               int64_t lds, int64_t M, int64_t N, cudaStream_t stream) {
-  const int64_t groups = (N + kCkptGroup - 1) / kCkptGroup;
-  PdlLaunch l(dim3(blocks_for(M * groups, 8)), dim3(256), 0, stream);
-  return cudaLaunchKernelEx(&l.cfg, ckpt8_save_kernel, x, ldx, codes, ldq, scales, lds, M, N);
+  const bool vec = N % 8 == 0 && aligned(x, ldx, 16) && aligned(codes, ldq, 8);
+  const unsigned grid = pieces_grid(M, N, vec ? kVecCols : kCkptGroup);
+  if (grid == 0) return cudaErrorInvalidValue;
+  PdlLaunch l(dim3(grid), dim3(256), 0, stream);
+  return cudaLaunchKernelEx(&l.cfg, vec ? ckpt8_save_vec_kernel : ckpt8_save_kernel, x, ldx, codes, ldq, scales, lds,
+                            M, N);
 }
 
 cudaError_t launch_ckpt8_load(const int8_t* codes, int64_t ldq, const float* scales, int64_t lds, int act,
                               uint16_t* y, int64_t ldy, int64_t M, int64_t N, cudaStream_t stream) {
-  PdlLaunch l(dim3(blocks_for(M * N, 256)), dim3(256), 0, stream);
-  return cudaLaunchKernelEx(&l.cfg, ckpt8_load_kernel, codes, ldq, scales, lds, act, y, ldy, M, N);
+  const bool vec = N % 8 == 0 && aligned(y, ldy, 16) && aligned(codes, ldq, 8);
+  const unsigned grid = pieces_grid(M, N, vec ? kVecCols : kCkptGroup);
+  if (grid == 0) return cudaErrorInvalidValue;
+  PdlLaunch l(dim3(grid), dim3(256), 0, stream);
+  return cudaLaunchKernelEx(&l.cfg, vec ? ckpt8_load_vec_kernel : ckpt8_load_kernel, codes, ldq, scales, lds, act, y,
+                            ldy, M, N);
 }
 
 // The -DHGEMM_DEBUG build's check word of this file (null otherwise).

@@ -20,6 +20,7 @@ enum WatchdogCode : int {
   kWdReduce = 6,          // split-K owner waiting for the other slices' partials
   kWdGridBarrier = 7,     // a CTA of a cooperative launch waiting for all others at a phase boundary
   kWdRowGroup = 8,        // an epilogue waiting for the CTAs that read the rows it overwrites
+  kWdRows = 9,            // the layer norm's backward pass waiting for a row
 };
 
 // The fused epilogue ("GPU架构与CUDA", 核函数融合): each FP32 accumulator
@@ -246,6 +247,8 @@ struct NormArgs {
   float* dbeta;
   float* work;               // backward: partial sums
   int64_t M, D;
+  int* status;               // device watchdog word
+  unsigned long long timeout_ns;
 };
 cudaError_t launch_layernorm_forward(const NormArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_layernorm_backward(const NormArgs& a, int num_sms, cudaStream_t stream);

@@ -127,6 +127,13 @@ __device__ __forceinline__ uint32_t ckpt_code(float u, float inv) {
   return __float_as_uint(__fadd_rn(__fmul_rn(u, inv), 12582912.f));
 }
 
+// Four codes packed (the first in the low byte); all 0 where inv is 0.
+__device__ __forceinline__ uint32_t ckpt_word(float a, float b, float c, float d, float inv) {
+  const uint32_t w = __byte_perm(__byte_perm(ckpt_code(a, inv), ckpt_code(b, inv), 0x0040u),
+                                 __byte_perm(ckpt_code(c, inv), ckpt_code(d, inv), 0x0040u), 0x5410u);
+  return inv == 0.f ? 0u : w;
+}
+
 // The FP32 value of the signed byte at position `i` of `word`: the byte,
 // offset by 128, placed in the mantissa of 2^23.
 __device__ __forceinline__ float ckpt_byte(uint32_t word, int i) {
@@ -229,11 +236,8 @@ __device__ __forceinline__ void lin_stage_row64(uint8_t* row, int lane, uint32_t
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         const uint32_t* v = j < 8 ? v0 + 4 * j : v1 + 4 * (j - 8);
-        uint32_t c[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = ckpt_code(__uint_as_float(v[i]), inv);
-        w[j] = __byte_perm(__byte_perm(c[0], c[1], 0x0040u), __byte_perm(c[2], c[3], 0x0040u), 0x5410u);
-        if (inv == 0.f) w[j] = 0u;
+        w[j] = ckpt_word(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]), __uint_as_float(v[3]),
+                         inv);
       }
       if (in_m) {
         int8_t* q = e.codes + grow * e.ldq + x0;

@@ -437,6 +437,24 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t cluster_addr, uint32_t a,
                : "memory");
 }
 
+// 4-byte load from shared memory of any CTA of the cluster.
+__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
+// Bulk copy of `bytes` (a multiple of 16; both addresses 16-byte aligned)
+// from global memory to this CTA's shared memory, counted as transaction
+// bytes on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  if (!HG_DBG_SMEM(dst, bytes) || !HG_DBG_SMEM(bar, 8) || !HG_DBG_ALIGN(src, 16)) return;
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
 // Bulk copy of `bytes` (a multiple of 16) from this CTA's shared memory to a
 // cluster CTA's shared memory; completion is counted as transaction bytes on
 // the destination CTA's barrier `bar` (a shared::cluster address).
