@@ -225,10 +225,25 @@ def _check_tensor(x, name: str, on_device: bool | None):
             raise ValueError(f"{name} must be device memory, got a numpy array")
 
 
+_torch = None              # torch, once a call has needed it
+_raw_current_stream = None  # device index -> handle of torch's current stream
+
+
+def _import_torch():
+    global _torch, _raw_current_stream
+    import torch
+    torch.cuda.current_stream()  # initialises CUDA
+    # the handle alone: torch.cuda.current_stream() makes a Stream object, 2.8 us against 0.1
+    _raw_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _torch = torch
+    return torch
+
+
 def _stream(stream) -> int:
     if stream is None:
-        import torch
-        return int(torch.cuda.current_stream().cuda_stream)
+        torch = _torch or _import_torch()
+        return int(_raw_current_stream(torch.cuda.current_device()))
     if isinstance(stream, int):
         return stream
     if hasattr(stream, "cuda_stream"):
@@ -441,59 +456,56 @@ def matmul(a, b_cols, out=None, stream=None):
 
 # ------------------------------------------- the feed-forward block's operators
 
-def _typed(name, dtype, *tensors) -> None:
-    """Each tensor (None or a raw address passes) is on the device and of `dtype`."""
-    for x in tensors:
-        if x is None or isinstance(x, int):
-            continue
-        if x.dtype != dtype:
-            raise TypeError(f"{name}: expected {dtype}, got {x.dtype}")
-        if not x.is_cuda:
-            raise ValueError(f"{name}: expected a CUDA tensor")
+_F16, _F32, _I8 = "torch.float16", "torch.float32", "torch.int8"
+_dtypes: dict = {}  # torch's dtype objects and their names
+
+
+def _dev(x, dtype: str, name: str):
+    """Address of a CUDA tensor of `dtype`; None and raw addresses pass."""
+    if x is None or type(x) is int:
+        return x
+    if _dtypes.get(x.dtype) is not dtype:
+        if str(x.dtype) != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
+        _dtypes[x.dtype] = dtype
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return x.data_ptr()
 
 
 def hgemm_linear(X, ldx: int, W, ldw: int, bias, act: int, R, ldr: int, Y, ldy: int, M: int, N: int, K: int,
                  codes=None, ldq: int = 0, scales=None, lds: int = 0, stream=None) -> None:
     """Y = f(X·Wᵀ + bias) + R, f an HGEMM_ACT_*; with codes and scales the
     pre-activations are kept in 8 bits too (see hgemm.h)."""
-    import torch
-    _typed("hgemm_linear", torch.float16, X, W, bias, R, Y)
-    _typed("hgemm_linear codes", torch.int8, codes)
-    _typed("hgemm_linear scales", torch.float32, scales)
-    _raise_on(load().hgemm_linear(_ptr(X), ldx, _ptr(W), ldw, _ptr(bias), act, _ptr(R), ldr, _ptr(Y), ldy,
-                                  _ptr(codes), ldq, _ptr(scales), lds, M, N, K, _stream(stream)), "hgemm_linear")
+    _raise_on((_lib or load()).hgemm_linear(
+        _dev(X, _F16, "X"), ldx, _dev(W, _F16, "W"), ldw, _dev(bias, _F16, "bias"), act, _dev(R, _F16, "R"), ldr,
+        _dev(Y, _F16, "Y"), ldy, _dev(codes, _I8, "codes"), ldq, _dev(scales, _F32, "scales"), lds, M, N, K,
+        _stream(stream)), "hgemm_linear")
 
 
 def hgemm_linear_dgrad(dY, lddy: int, W, ldw: int, codes, ldq: int, scales, lds: int, act: int, dU, lddu: int,
                        H, ldh: int, M: int, N: int, K: int, stream=None) -> None:
     """dU = (dY·W) ⊙ f'(Û) and H = f(Û), Û the 8-bit pre-activations (see hgemm.h)."""
-    import torch
-    _typed("hgemm_linear_dgrad", torch.float16, dY, W, dU, H)
-    _typed("hgemm_linear_dgrad codes", torch.int8, codes)
-    _typed("hgemm_linear_dgrad scales", torch.float32, scales)
-    _raise_on(load().hgemm_linear_dgrad(_ptr(dY), lddy, _ptr(W), ldw, _ptr(codes), ldq, _ptr(scales), lds, act,
-                                        _ptr(dU), lddu, _ptr(H), ldh, M, N, K, _stream(stream)),
-              "hgemm_linear_dgrad")
+    _raise_on((_lib or load()).hgemm_linear_dgrad(
+        _dev(dY, _F16, "dY"), lddy, _dev(W, _F16, "W"), ldw, _dev(codes, _I8, "codes"), ldq,
+        _dev(scales, _F32, "scales"), lds, act, _dev(dU, _F16, "dU"), lddu, _dev(H, _F16, "H"), ldh, M, N, K,
+        _stream(stream)), "hgemm_linear_dgrad")
 
 
 def hgemm_linear_wgrad(dY, lddy: int, X, ldx: int, dW, lddw: int, dbias, accumulate: bool, M: int, N: int, K: int,
                        stream=None) -> None:
     """dW = dYᵀ·X and dbias = Σ_rows dY, or added to both (see hgemm.h)."""
-    import torch
-    _typed("hgemm_linear_wgrad", torch.float16, dY, X, dW)
-    _typed("hgemm_linear_wgrad dbias", torch.float32, dbias)
-    _raise_on(load().hgemm_linear_wgrad(_ptr(dY), lddy, _ptr(X), ldx, _ptr(dW), lddw, _ptr(dbias),
-                                        int(bool(accumulate)), M, N, K, _stream(stream)), "hgemm_linear_wgrad")
+    _raise_on((_lib or load()).hgemm_linear_wgrad(
+        _dev(dY, _F16, "dY"), lddy, _dev(X, _F16, "X"), ldx, _dev(dW, _F16, "dW"), lddw, _dev(dbias, _F32, "dbias"),
+        1 if accumulate else 0, M, N, K, _stream(stream)), "hgemm_linear_wgrad")
 
 
 def hgemm_layernorm_forward(X, ldx: int, gamma, beta, eps: float, Y, ldy: int, mean, rstd, M: int, D: int,
                             stream=None) -> None:
     """Y = (X − mean)·rstd·gamma + beta over rows of D values (see hgemm.h)."""
-    import torch
-    _typed("hgemm_layernorm_forward", torch.float16, X, gamma, beta, Y)
-    _typed("hgemm_layernorm_forward statistics", torch.float32, mean, rstd)
-    _raise_on(load().hgemm_layernorm_forward(_ptr(X), ldx, _ptr(gamma), _ptr(beta), eps, _ptr(Y), ldy, _ptr(mean),
-                                             _ptr(rstd), M, D, _stream(stream)), "hgemm_layernorm_forward")
+    _raise_on((_lib or load()).hgemm_layernorm_forward(
+        _dev(X, _F16, "X"), ldx, _dev(gamma, _F16, "gamma"), _dev(beta, _F16, "beta"), eps, _dev(Y, _F16, "Y"), ldy,
+        _dev(mean, _F32, "mean"), _dev(rstd, _F32, "rstd"), M, D, _stream(stream)), "hgemm_layernorm_forward")
 
 
 def hgemm_layernorm_backward_workspace_size(M: int, D: int) -> int:
@@ -506,32 +518,24 @@ def hgemm_layernorm_backward(dY, lddy: int, X, ldx: int, gamma, mean, rstd, R, l
                              stream=None) -> None:
     """dX, dgamma and dbeta of a layer norm, R added to dX (see hgemm.h); the
     workspace's size defaults to the tensor's bytes."""
-    import torch
-    _typed("hgemm_layernorm_backward", torch.float16, dY, X, gamma, R, dX)
-    _typed("hgemm_layernorm_backward statistics", torch.float32, mean, rstd, dgamma, dbeta)
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size() if hasattr(workspace, "numel") else 0
-    _raise_on(load().hgemm_layernorm_backward(_ptr(dY), lddy, _ptr(X), ldx, _ptr(gamma), _ptr(mean), _ptr(rstd),
-                                              _ptr(R), ldr, _ptr(dX), lddx, _ptr(dgamma), _ptr(dbeta),
-                                              _ptr(workspace), workspace_bytes, M, D, _stream(stream)),
-              "hgemm_layernorm_backward")
+    _raise_on((_lib or load()).hgemm_layernorm_backward(
+        _dev(dY, _F16, "dY"), lddy, _dev(X, _F16, "X"), ldx, _dev(gamma, _F16, "gamma"), _dev(mean, _F32, "mean"),
+        _dev(rstd, _F32, "rstd"), _dev(R, _F16, "R"), ldr, _dev(dX, _F16, "dX"), lddx, _dev(dgamma, _F32, "dgamma"),
+        _dev(dbeta, _F32, "dbeta"), _ptr(workspace), workspace_bytes, M, D, _stream(stream)),
+        "hgemm_layernorm_backward")
 
 
 def hgemm_ckpt8_save(X, ldx: int, codes, ldq: int, scales, lds: int, M: int, N: int, stream=None) -> None:
     """X into its 8-bit form (see hgemm.h)."""
-    import torch
-    _typed("hgemm_ckpt8_save", torch.float16, X)
-    _typed("hgemm_ckpt8_save codes", torch.int8, codes)
-    _typed("hgemm_ckpt8_save scales", torch.float32, scales)
-    _raise_on(load().hgemm_ckpt8_save(_ptr(X), ldx, _ptr(codes), ldq, _ptr(scales), lds, M, N, _stream(stream)),
-              "hgemm_ckpt8_save")
+    _raise_on((_lib or load()).hgemm_ckpt8_save(
+        _dev(X, _F16, "X"), ldx, _dev(codes, _I8, "codes"), ldq, _dev(scales, _F32, "scales"), lds, M, N,
+        _stream(stream)), "hgemm_ckpt8_save")
 
 
 def hgemm_ckpt8_load(codes, ldq: int, scales, lds: int, act: int, Y, ldy: int, M: int, N: int, stream=None) -> None:
     """Y = f(Û) from the 8-bit form, f an HGEMM_ACT_* (see hgemm.h)."""
-    import torch
-    _typed("hgemm_ckpt8_load codes", torch.int8, codes)
-    _typed("hgemm_ckpt8_load scales", torch.float32, scales)
-    _typed("hgemm_ckpt8_load", torch.float16, Y)
-    _raise_on(load().hgemm_ckpt8_load(_ptr(codes), ldq, _ptr(scales), lds, act, _ptr(Y), ldy, M, N,
-                                      _stream(stream)), "hgemm_ckpt8_load")
+    _raise_on((_lib or load()).hgemm_ckpt8_load(
+        _dev(codes, _I8, "codes"), ldq, _dev(scales, _F32, "scales"), lds, act, _dev(Y, _F16, "Y"), ldy, M, N,
+        _stream(stream)), "hgemm_ckpt8_load")

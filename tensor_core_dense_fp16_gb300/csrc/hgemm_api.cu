@@ -743,6 +743,8 @@ int run_linear(const LinearProduct& p, cudaStream_t stream) {
   Gemm g{p.A, p.B, p.C, p.M, p.N, p.K, p.lda, p.ldb, p.ldc};
   g.b_mn = p.b_mn;
   g.lin = &p.epi;
+  if (g_forced_path.load(std::memory_order_relaxed) < 0 && linear_rows_suits(p))
+    return cuda_status(launch_linear_rows(p, dev->num_sms, stream));
   return dispatch(g, kPlainEpilogue, *dev, stream);
 }
 

@@ -40,6 +40,131 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+// ------------------------------------------------------------ few rows of X
+
+// Loads of weights that this launch reads once: past L1, which keeps X.
+__device__ __forceinline__ uint4 load_once16(const uint16_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// D (16×8, FP32) += A (16×16) · B (16×8).
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Y for at most 8·MT rows of X (a step of token generation), bound by reading
+// W once. A block takes 16 features, its warps interleaved 32-wide pieces of
+// K. Weights go from memory straight into the fragments of a 16×8×16 matrix
+// instruction with the features as its rows and the rows of X as its columns:
+// a sum does not depend on which k stands in which slot, so lane 4g + t takes
+// the 16 contiguous bytes at k = 8t of a piece (of features g and g + 8, and
+// of row g of X), which are its slots of two instructions, and nothing passes
+// through shared memory. One row of X costs as much as eight. The warps'
+// partial sums are added in order through shared memory. VEC: pitches and
+// bases allow the 16-byte loads; otherwise the slots are filled by 2-byte
+// loads.
+struct RowsArgs {
+  const uint16_t* X;
+  int64_t ldx;
+  const uint16_t* W;
+  int64_t ldw;
+  uint16_t* Y;
+  int64_t ldy;
+  int M, N, K;
+  LinEpi epi;
+};
+
+constexpr int kRowsFeatures = 16;
+template <int MT, int WARPS, bool VEC>
+__global__ void __launch_bounds__(WARPS * 32) linear_rows_kernel(const RowsArgs p) {
+  constexpr int AHEAD = 4;  // pieces in flight per warp: 64 bytes of each feature per lane pair
+  constexpr int PITCH = kRowsFeatures + 1;
+  __shared__ float part[WARPS][8 * MT][PITCH];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int n0 = static_cast<int>(blockIdx.x) * kRowsFeatures;
+  // features past N are computed as copies of the last one and not stored
+  const uint16_t* w0 = p.W + min(n0 + g, p.N - 1) * p.ldw;
+  const uint16_t* w1 = p.W + min(n0 + g + 8, p.N - 1) * p.ldw;
+  auto load = [&](const uint16_t* row, int k, bool weights) {
+    if constexpr (VEC) {
+      if (k >= p.K) return make_uint4(0u, 0u, 0u, 0u);
+      return weights ? load_once16(row + k) : __ldg(reinterpret_cast<const uint4*>(row + k));
+    } else {
+      uint32_t v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = k + 2 * i < p.K ? __ldg(row + k + 2 * i) : 0u;
+        const uint32_t hi = k + 2 * i + 1 < p.K ? __ldg(row + k + 2 * i + 1) : 0u;
+        v[i] = lo | hi << 16;
+      }
+      return make_uint4(v[0], v[1], v[2], v[3]);
+    }
+  };
+  float acc[MT][4] = {};
+  for (int k0 = warp * 32 + 8 * t; k0 - 8 * t < p.K; k0 += AHEAD * WARPS * 32) {
+    uint4 a0[AHEAD], a1[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      a0[u] = load(w0, k0 + u * WARPS * 32, true);
+      a1[u] = load(w1, k0 + u * WARPS * 32, true);
+    }
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const int m = 8 * i + g;
+        uint4 b = make_uint4(0u, 0u, 0u, 0u);
+        if (m < p.M) b = load(p.X + m * p.ldx, k0 + u * WARPS * 32, false);
+        mma_16816(acc[i], a0[u].x, a1[u].x, a0[u].y, a1[u].y, b.x, b.y);
+        mma_16816(acc[i], a0[u].z, a1[u].z, a0[u].w, a1[u].w, b.z, b.w);
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    part[warp][8 * i + 2 * t][g] = acc[i][0];
+    part[warp][8 * i + 2 * t + 1][g] = acc[i][1];
+    part[warp][8 * i + 2 * t][g + 8] = acc[i][2];
+    part[warp][8 * i + 2 * t + 1][g + 8] = acc[i][3];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.M * kRowsFeatures; i += WARPS * 32) {
+    const int m = i / kRowsFeatures, f = i % kRowsFeatures;
+    if (n0 + f >= p.N) continue;
+    float u = part[0][m][f];
+#pragma unroll
+    for (int w = 1; w < WARPS; ++w) u += part[w][m][f];
+    if (p.epi.bias) u += __half2float(__ushort_as_half(p.epi.bias[n0 + f]));
+    lin_scalar<false>(p.epi, u, m, n0 + f, 0.f, 0.f, p.Y + m * p.ldy + n0 + f);
+  }
+}
+
+template <int MT, int WARPS>
+cudaError_t rows_with(const RowsArgs& p, bool vec, cudaStream_t stream) {
+  PdlLaunch l(dim3(static_cast<unsigned>((p.N + kRowsFeatures - 1) / kRowsFeatures)), dim3(WARPS * 32), 0, stream);
+  return cudaLaunchKernelEx(&l.cfg, vec ? linear_rows_kernel<MT, WARPS, true> : linear_rows_kernel<MT, WARPS, false>,
+                            p);
+}
+
+template <int MT>
+cudaError_t rows_tiles(const RowsArgs& p, bool vec, int num_sms, cudaStream_t stream) {
+  // 16 warps where there are few blocks, so that each SM still has enough
+  // loads in flight
+  const int64_t blocks = (p.N + kRowsFeatures - 1) / kRowsFeatures;
+  return blocks <= 2 * num_sms ? rows_with<MT, 16>(p, vec, stream) : rows_with<MT, 8>(p, vec, stream);
+}
+
 // Column sums, in a fixed order. A cluster of CTAs takes 64 columns (128
 // bytes of a row, so that every row's piece is whole sectors), each CTA a run
 // of rows; within a CTA a thread takes VEC neighbouring columns of every
@@ -102,6 +227,27 @@ __global__ void __launch_bounds__(256)
 }
 
 }  // namespace
+
+bool linear_rows_suits(const LinearProduct& p) {
+  return p.M <= kLinearRows && p.K > 0 && !p.b_mn && !p.epi.backward && !p.epi.codes;
+}
+
+cudaError_t launch_linear_rows(const LinearProduct& q, int num_sms, cudaStream_t stream) {
+  const RowsArgs p{q.A, q.lda, q.B, q.ldb, q.C, q.ldc, static_cast<int>(q.M), static_cast<int>(q.N),
+                   static_cast<int>(q.K), q.epi};
+  auto rows16 = [](const void* b, int64_t ld) { return (reinterpret_cast<uintptr_t>(b) & 15u) == 0 && ld % 8 == 0; };
+  const bool vec = q.K % 8 == 0 && rows16(q.A, q.lda) && rows16(q.B, q.ldb);
+  switch ((q.M + 7) / 8) {
+    case 1:
+      return rows_tiles<1>(p, vec, num_sms, stream);
+    case 2:
+      return rows_tiles<2>(p, vec, num_sms, stream);
+    case 3:
+      return rows_tiles<3>(p, vec, num_sms, stream);
+    default:
+      return rows_tiles<4>(p, vec, num_sms, stream);
+  }
+}
 
 cudaError_t launch_linear_empty(uint16_t* C, int64_t ldc, int64_t M, int64_t N, const LinEpi& epi,
                                 cudaStream_t stream) {

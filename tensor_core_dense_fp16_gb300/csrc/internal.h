@@ -228,6 +228,10 @@ struct LinearProduct {
   LinEpi epi;
 };
 int run_linear(const LinearProduct& p, cudaStream_t stream);
+// The kernel for at most kLinearRows rows of A, and whether it computes p.
+constexpr int kLinearRows = 32;
+bool linear_rows_suits(const LinearProduct& p);
+cudaError_t launch_linear_rows(const LinearProduct& p, int num_sms, cudaStream_t stream);
 
 struct NormArgs {
   const uint16_t* x;
