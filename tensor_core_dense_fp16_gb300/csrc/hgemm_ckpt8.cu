@@ -49,18 +49,14 @@ __global__ void __launch_bounds__(256)
   float mine = 0.f;  // lane 8g + r keeps the scale of group g, row r
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
-    const __half2* h = reinterpret_cast<const __half2*>(&v[r]);
-    float u[8];
+    const f32x2 u[4] = {unpack_half2(v[r].x), unpack_half2(v[r].y), unpack_half2(v[r].z), unpack_half2(v[r].w)};
+    float top = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(h[i]);
-      u[2 * i] = f.x;
-      u[2 * i + 1] = f.y;
+      float a, b;
+      unpair(u[i], a, b);
+      top = max_abs3(top, a, b);
     }
-    float top = max_abs3(u[0], u[1], u[2]);
-    top = max_abs3(top, u[3], u[4]);
-    top = max_abs3(top, u[5], u[6]);
-    top = max_abs3(top, u[7], 0.f);
     uint32_t bits = magnitude_bits(top);
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, o));
@@ -69,7 +65,7 @@ __global__ void __launch_bounds__(256)
     if ((lane & 7) == r) mine = scale;
     if (in_n && p.m0 + r < M)
       *reinterpret_cast<uint2*>(codes + (p.m0 + r) * ldq + n) =
-          make_uint2(ckpt_word(u[0], u[1], u[2], u[3], inv), ckpt_word(u[4], u[5], u[6], u[7], inv));
+          make_uint2(ckpt_word(u[0], u[1], inv), ckpt_word(u[2], u[3], inv));
   }
   const int64_t m = p.m0 + (lane & 7);
   const int64_t g = n / kCkptGroup;  // (its last lanes may be past N)
@@ -131,13 +127,11 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       const float scale = __shfl_sync(0xffffffffu, mine, (lane & 24) | r);
-      uint32_t f[8];
+      f32x2 f[4], df;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float v, df;
-        activate<decltype(a)::value, false>(ckpt_byte(i < 4 ? w[r].x : w[r].y, i & 3) * scale, v, df);
-        f[i] = __float_as_uint(v);
-      }
+      for (int i = 0; i < 4; ++i)
+        activate<decltype(a)::value, false>(
+            mul2(ckpt_pair((i < 2 ? w[r].x : w[r].y) ^ 0x80808080u, i & 1), pair_of(scale)), f[i], df);
       if (in_n && p.m0 + r < M) *reinterpret_cast<uint4*>(y + (p.m0 + r) * ldy + n) = pack8(f);
     }
   });

@@ -368,13 +368,17 @@ __global__ void __launch_bounds__(192, 1)
       };
 #pragma unroll 1
       for (int c64 = 0; EPI >= kEpiLinear && c64 < own_cols / 64; ++c64) {
-        float a0[32], a1[32];
-        sum32(2 * c64, a0);
-        sum32(2 * c64 + 1, a1);
+        f32x2 v[32];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float a[32];
+          sum32(2 * c64 + i, a);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) v[16 * i + k] = pair_of(a[2 * k], a[2 * k + 1]);
+        }
         if constexpr (EPI >= kEpiLinear)
-          lin_stage_row64<EPI>(cbuf + c64 * (kEpiRows * 128) + lane * 128, lane,
-                               reinterpret_cast<uint32_t(&)[32]>(a0), reinterpret_cast<uint32_t(&)[32]>(a1), p.lin,
-                               p.M, p.N, static_cast<int64_t>(y0) + lane, x0 + c64 * 64);
+          lin_row64<EPI>(cbuf + c64 * (kEpiRows * 128) + lane * 128, lane, v, p.lin, p.M, p.N,
+                         static_cast<int64_t>(y0) + lane, x0 + c64 * 64);
       }
 #pragma unroll 1
       for (int c32 = 0; EPI < kEpiLinear && c32 < own_cols / 32; ++c32) {

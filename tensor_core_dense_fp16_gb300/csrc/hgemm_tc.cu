@@ -245,30 +245,41 @@ __global__ void __launch_bounds__(192, 1)
       const int y0 = mb * Cfg::BM + q * kEpiRows;
 #pragma unroll 1
       for (int c = 0; c < BN / kEpiCols; ++c) {
-        uint32_t v0[32], v1[32];
-        tmem_ld_32x32b_x32(t_row + c * kEpiCols, v0);
-        tmem_ld_32x32b_x32(t_row + c * kEpiCols + 32, v1);
-        tmem_ld_wait(v0);
-        tmem_ld_wait(v1);
-        if (c == BN / kEpiCols - 1) {
-          // the whole accumulator has been read: hand it back to the MMA warp
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(acce_bar(acc));
-        }
         const int x0 = nb * BN + c * kEpiCols;
-        if (x0 >= p.N || y0 >= p.M) continue;  // box entirely outside C
-        // the store issued from this buffer two boxes ago must have read it
-        if (lane == 0) bulk_wait_group_read<1>();
-        __syncwarp();
+        const bool inside = x0 < p.N && y0 < p.M;  // else the box is entirely outside C
+        auto release = [&]() {
+          if (c == BN / kEpiCols - 1) {
+            // the whole accumulator has been read: hand it back to the MMA warp
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acce_bar(acc));
+          }
+        };
         uint8_t* buf = cbuf_base + cb * Cfg::C_BOX_BYTES;
         uint8_t* row = buf + lane * 128;
-        // 128-byte swizzle: 16-byte chunk j of row r sits at chunk j ^ (r % 8)
-        if constexpr (EPI == kEpiLinear)
-          lin_stage_row64<EPI>(row, lane, v0, v1, p.lin, p.M, p.N, static_cast<int64_t>(y0) + lane, x0);
-        else
+        if constexpr (EPI == kEpiLinear) {
+          f32x2 v[32];
+          tmem_row64(t_row + c * kEpiCols, v);
+          release();
+          if (!inside) continue;
+          if (lane == 0) bulk_wait_group_read<1>();
+          __syncwarp();
+          lin_row64<EPI>(row, lane, v, p.lin, p.M, p.N, static_cast<int64_t>(y0) + lane, x0);
+        } else {
+          uint32_t v0[32], v1[32];
+          tmem_ld_32x32b_x32(t_row + c * kEpiCols, v0);
+          tmem_ld_32x32b_x32(t_row + c * kEpiCols + 32, v1);
+          tmem_ld_wait(v0);
+          tmem_ld_wait(v1);
+          release();
+          if (!inside) continue;
+          // the store issued from this buffer two boxes ago must have read it
+          if (lane == 0) bulk_wait_group_read<1>();
+          __syncwarp();
+          // 128-byte swizzle: 16-byte chunk j of row r sits at chunk j ^ (r % 8)
           stage_row64<EPI == kEpiFused>(row, lane, v0, v1, p.epi, p.C, p.M, p.N, p.ldc,
                                         static_cast<int64_t>(y0) + lane, x0);
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {

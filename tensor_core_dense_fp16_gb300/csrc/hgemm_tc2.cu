@@ -118,12 +118,15 @@ __device__ __forceinline__ PairTile pair_tile(int t, const TcArgs& p) {
   return w;
 }
 
+// Epilogue warps of each instantiation.
+constexpr int epi_warps(int epi) { return epi == kEpiPlain ? 4 : 8; }
+
 template <int MAX_STAGES, int EPI>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EPI != kEpiPlain ? 320 : 192, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * epi_warps(EPI), 1)
     hgemm_tc2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmBh, const __grid_constant__ CUtensorMap tmC,
                      const TcArgs p) {
-  using Cfg = PairCfg<MAX_STAGES, EPI != kEpiPlain ? 8 : 4>;
+  using Cfg = PairCfg<MAX_STAGES, epi_warps(EPI)>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
@@ -252,8 +255,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EPI != kEpiPlain ? 3
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------- MMA issuer (even CTA)
-    if (rank == 0 && lane == 0) {
+    // The whole warp walks the loop and one lane issues: what the issue needs
+    // (descriptors, barrier addresses) then stays in uniform registers. The
+    // issue of a stage takes a large part of the stage's MMA time, so with
+    // epilogue warps beside it every instruction less shows (8192×8192
+    // outputs, contraction 2048, GELU: 188 us, 180 with this).
+    if (rank == 0) {
+      const uint32_t on = lane == 0 ? 1u : 0u;
+      // K-major: 16 K elements are 32 bytes along the row; MN-major: 16 K
+      // rows of 128 bytes
+      const uint64_t a_base = p.a_mn ? sdesc_mnmajor_sw128(sA) : sdesc_kmajor_sw128(sA);
+      const uint64_t b_base = p.b_mn ? sdesc_mnmajor_sw128(sB) : sdesc_kmajor_sw128(sB);
+      const uint32_t a_step = p.a_mn ? 128u : 2u, b_step = p.b_mn ? 128u : 2u;
       int stage = 0;
+      uint32_t offset = 0;  // of the stage, in the descriptors' 16-byte units
       uint32_t phase = 0;
       int acc = 0;
       uint32_t acc_phase = 0;
@@ -261,43 +276,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EPI != kEpiPlain ? 3
       for (int t = cluster_id; ok && t < p.num_tiles; t += num_clusters) {
         const uint32_t idesc = (t < p.full_tiles ? Cfg::IDESC : idesc_f16_f32acc(Cfg::BM, p.part_cols)) |
                                idesc_major_bits(p.a_mn != 0, p.b_mn != 0);
-        if (!wait_phase_cluster(acce_bar(acc), acc_phase ^ 1u, wd, kWdMmaAccEmpty)) {
-          ok = false;
-          break;
-        }
+        ok = wait_phase_cluster(acce_bar(acc), acc_phase ^ 1u, wd, kWdMmaAccEmpty);
+        if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after_sync();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * Cfg::ACC_COLS);
         for (int kb = 0; kb < p.num_kb; ++kb) {
-          if (!wait_phase(full_bar(stage), phase, wd, kWdMmaFull)) {
-            ok = false;
-            break;
-          }
+          ok = __all_sync(0xffffffffu, wait_phase(full_bar(stage), phase, wd, kWdMmaFull));
+          if (!ok) break;
           tc_fence_after_sync();
-          // K-major: 16 K elements are 32 bytes along the row; MN-major: 16 K
-          // rows of 128 bytes
-          const uint64_t a_desc = p.a_mn ? sdesc_mnmajor_sw128(sA + stage * stage_bytes)
-                                         : sdesc_kmajor_sw128(sA + stage * stage_bytes);
-          const uint64_t b_desc = p.b_mn ? sdesc_mnmajor_sw128(sB + stage * stage_bytes)
-                                         : sdesc_kmajor_sw128(sB + stage * stage_bytes);
-          const uint32_t a_step = p.a_mn ? 128u : 2u, b_step = p.b_mn ? 128u : 2u;
 #pragma unroll
           for (int k = 0; k < Cfg::BK / Cfg::UMMA_K; ++k)
             // kb counts the tile's K steps in load order (the producer may walk
             // K backwards); the first step overwrites the accumulator
-            mma_f16_ss_cg2(d_tmem, a_desc + a_step * k, b_desc + b_step * k, idesc,
-                           (kb > 0 || k > 0) ? 1u : 0u);
-          mma_commit_cg2_multicast(empty_bar(stage), 0x3);  // frees the stage in both CTAs
+            mma_f16_ss_cg2_if(on, d_tmem, a_base + offset + a_step * k, b_base + offset + b_step * k, idesc,
+                              (kb > 0 || k > 0) ? 1u : 0u);
+          mma_commit_cg2_multicast_if(on, empty_bar(stage), 0x3);  // frees the stage in both CTAs
+          offset += stage_bytes >> 4;
           if (++stage == STAGES) {
             stage = 0;
+            offset = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        mma_commit_cg2_multicast(accf_bar(acc), 0x3);  // both TMEM halves complete
+        mma_commit_cg2_multicast_if(on, accf_bar(acc), 0x3);  // both TMEM halves complete
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       }
-      mma_commit_cg2_multicast(drain_bar, 0x1);
+      mma_commit_cg2_multicast_if(on, drain_bar, 0x1);
       wait_drain(drain_bar, 0, wd);
     }
     __syncwarp();
@@ -339,25 +345,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EPI != kEpiPlain ? 3
       }
 #pragma unroll 1
       for (int c = h; c < chunks; c += 2) {
-        uint32_t v0[32], v1[32];
-        tmem_ld_32x32b_x32(t_row + c * kEpiCols, v0);
-        tmem_ld_32x32b_x32(t_row + c * kEpiCols + 32, v1);
-        tmem_ld_wait(v0);
-        tmem_ld_wait(v1);
-        if (c == last && reused) {
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa_shared(acce_bar(acc), 0));
-        }
         const int x0 = w.n0 + c * kEpiCols;
-        if (x0 >= p.N || y0 >= p.M) continue;
-        if (lane == 0) bulk_wait_group_read<0>();  // the previous store has read the box
-        __syncwarp();
-        // 128-byte swizzle: 16-byte chunk j of row r sits at chunk j ^ (r % 8)
-        if constexpr (EPI == kEpiFused)
+        const bool inside = x0 < p.N && y0 < p.M;
+        // hands the accumulator back once its last box has been read
+        auto release = [&]() {
+          if (c == last && reused) {
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(mapa_shared(acce_bar(acc), 0));
+          }
+        };
+        if constexpr (EPI == kEpiFused) {
+          uint32_t v0[32], v1[32];
+          tmem_ld_32x32b_x32(t_row + c * kEpiCols, v0);
+          tmem_ld_32x32b_x32(t_row + c * kEpiCols + 32, v1);
+          tmem_ld_wait(v0);
+          tmem_ld_wait(v1);
+          release();
+          if (!inside) continue;
+          if (lane == 0) bulk_wait_group_read<0>();  // the previous store has read the box
+          __syncwarp();
+          // 128-byte swizzle: 16-byte chunk j of row r sits at chunk j ^ (r % 8)
           stage_row64<true>(buf + lane * 128, lane, v0, v1, p.epi, p.C, p.M, p.N, p.ldc, grow, x0);
-        else
-          lin_stage_row64<EPI>(buf + lane * 128, lane, v0, v1, p.lin, p.M, p.N, grow, x0);
+        } else {
+          f32x2 v[32];
+          tmem_row64(t_row + c * kEpiCols, v);
+          release();
+          if (!inside) continue;
+          if (lane == 0) bulk_wait_group_read<0>();
+          __syncwarp();
+          lin_row64<EPI>(buf + lane * 128, lane, v, p.lin, p.M, p.N, grow, x0);
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -467,14 +485,13 @@ int pair_smem_bytes() { return PairCfg<kPairStages>::SMEM_BYTES; }
 cudaError_t launch_tc_pair(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& b_part,
                            const CUtensorMap& c, const TcArgs& args, Epilogue kind, cudaStream_t stream) {
   using Cfg = PairCfg<kPairStages, 4>;
-  using FusedCfg = PairCfg<kPairStages, 8>;
-  static_assert(Cfg::SMEM_BYTES == FusedCfg::SMEM_BYTES, "both instantiations have the same footprint");
+  static_assert(Cfg::SMEM_BYTES == PairCfg<kPairStages, 8>::SMEM_BYTES, "all instantiations have the same footprint");
   static std::atomic<bool> attr_done[4][64];
   auto kern = kind == kEpiPlain    ? hgemm_tc2_kernel<kPairStages, kEpiPlain>
               : kind == kEpiFused  ? hgemm_tc2_kernel<kPairStages, kEpiFused>
               : kind == kEpiLinear ? hgemm_tc2_kernel<kPairStages, kEpiLinear>
                                    : hgemm_tc2_kernel<kPairStages, kEpiLinearGrad>;
-  const int threads = kind != kEpiPlain ? FusedCfg::THREADS : Cfg::THREADS;
+  const int threads = 64 + 32 * epi_warps(kind);
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;

@@ -29,37 +29,60 @@ constexpr float kGeluC = 0.044715f;
 constexpr float kInvSqrt2 = 0.7071067811865476f;
 constexpr float kInvSqrt2Pi = 0.3989422804014327f;
 
-// σ(x) = 1 / (1 + e^-x), from the approximate 2^x and reciprocal (two
-// special-function instructions, relative error ~2^-22: an FP16 output's
-// rounding is 2^-11). x = ±∞ gives 1 and 0.
-__device__ __forceinline__ float sigmoid_f(float x) { return rcp_approx(1.f + ex2_approx(-kLog2e * x)); }
+// The approximate 2^x and reciprocal, one special-function instruction each,
+// have a relative error of ~2^-22 (an FP16 output's rounding is 2^-11); at
+// ±∞ they give the limits 0, ∞ and 0.
 
-// f(u), and f'(u) when GRAD, f the activation ACT. The tanh form of GELU is u·σ(2z),
-// z = √(2/π)·(u + 0.044715·u³), with derivative
-// σ + u·σ·(1 − σ)·2z'. Beyond |u| = 16 σ is 0 or 1 in FP32, so z is taken
-// at u clamped to ±16, where no power of u overflows.
+// A pair of f(u), and of f'(u) when GRAD, f the activation ACT. The tanh form
+// of GELU is u·σ(2z), z = √(2/π)·(u + 0.044715·u³), with derivative
+// σ + u·σ·(1 − σ)·2z'. Where σ has become 0 or 1 its factor u·σ·(1 − σ) is 0,
+// and no power of u overflows below |u| = 2^62: products of FP16 values stay
+// far below.
 template <int ACT, bool GRAD>
-__device__ __forceinline__ void activate(float u, float& f, float& df) {
+__device__ __forceinline__ void activate(f32x2 u, f32x2& f, f32x2& df) {
   if constexpr (ACT == HGEMM_ACT_RELU) {
-    f = u < 0.f ? 0.f : u;
-    if (GRAD) df = u > 0.f ? 1.f : (u <= 0.f ? 0.f : u);  // NaN stays NaN
-  } else if constexpr (ACT == HGEMM_ACT_GELU) {
-    const float c = fminf(fmaxf(u, -16.f), 16.f);  // (a NaN is dropped from s, not from f)
-    const float c2 = c * c;
-    const float s = sigmoid_f(2.f * kGeluZ * c * fmaf(kGeluC, c2, 1.f));
-    f = u * s;
-    if (GRAD) df = fmaf(f * (1.f - s), 2.f * kGeluZ * fmaf(3.f * kGeluC, c2, 1.f), s);
-  } else if constexpr (ACT == HGEMM_ACT_SILU) {
-    const float s = sigmoid_f(u);
-    f = u * s;
-    if (GRAD) df = fmaf(f, 1.f - s, s);
+    float a, b;
+    unpair(u, a, b);
+    float fa, fb;  // max(u, 0); a NaN stays one, in f and in f'
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(fa) : "f"(a));
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(fb) : "f"(b));
+    f = pair_of(fa, fb);
+    if (GRAD) df = pair_of(a > 0.f ? 1.f : fa, b > 0.f ? 1.f : fb);
+  } else if constexpr (ACT == HGEMM_ACT_GELU || ACT == HGEMM_ACT_SILU) {
+    // σ(x) = 1 / (1 + 2^(-x·log2 e))
+    f32x2 x, u2 = 0;
+    if constexpr (ACT == HGEMM_ACT_GELU) {
+      u2 = mul2(u, u);
+      x = mul2(u, fma2(u2, pair_of(-2.f * kLog2e * kGeluZ * kGeluC), pair_of(-2.f * kLog2e * kGeluZ)));
+    } else {
+      x = mul2(u, pair_of(-kLog2e));
+    }
+    float a, b;
+    unpair(x, a, b);
+    unpair(add2(pair_of(ex2_approx(a), ex2_approx(b)), pair_of(1.f)), a, b);
+    const f32x2 s = pair_of(rcp_approx(a), rcp_approx(b));
+    f = mul2(u, s);
+    if constexpr (GRAD) {
+      const f32x2 minus_f = mul2(u, mul2(s, pair_of(-1.f)));
+      const f32x2 w = fma2(minus_f, s, f);  // u·σ·(1 − σ)
+      if constexpr (ACT == HGEMM_ACT_GELU)
+        df = fma2(w, fma2(u2, pair_of(6.f * kGeluZ * kGeluC), pair_of(2.f * kGeluZ)), s);
+      else
+        df = add2(w, s);
+    }
   } else if constexpr (ACT == HGEMM_ACT_GELU_ERF) {
-    const float phi = fmaf(0.5f, erff(u * kInvSqrt2), 0.5f);  // Φ(u)
-    f = u * phi;
-    if (GRAD) df = fmaf(u * kInvSqrt2Pi, ex2_approx(-0.5f * kLog2e * u * u), phi);
+    float a, b;
+    unpair(u, a, b);
+    const f32x2 phi = fma2(pair_of(erff(a * kInvSqrt2), erff(b * kInvSqrt2)), pair_of(0.5f), pair_of(0.5f));  // Φ(u)
+    f = mul2(u, phi);
+    if constexpr (GRAD) {
+      float c, d;
+      unpair(mul2(mul2(u, u), pair_of(-0.5f * kLog2e)), c, d);
+      df = fma2(mul2(u, pair_of(kInvSqrt2Pi)), pair_of(ex2_approx(c), ex2_approx(d)), phi);
+    }
   } else {
     f = u;
-    if (GRAD) df = 1.f;
+    if (GRAD) df = pair_of(1.f);
   }
 }
 
@@ -85,9 +108,16 @@ __device__ __forceinline__ void with_activation(int act, Body body) {
   }
 }
 
+// One value at a time.
 template <bool GRAD>
 __device__ __forceinline__ void activate(float u, int act, float& f, float& df) {
-  with_activation(act, [&](auto a) { activate<decltype(a)::value, GRAD>(u, f, df); });
+  with_activation(act, [&](auto a) {
+    f32x2 f2, df2 = 0;
+    activate<decltype(a)::value, GRAD>(pair_of(u), f2, df2);
+    float other;
+    unpair(f2, f, other);
+    if (GRAD) unpair(df2, df, other);
+  });
 }
 
 __device__ __forceinline__ float activate(float u, int act) {
@@ -128,17 +158,27 @@ __device__ __forceinline__ uint32_t ckpt_code(float u, float inv) {
 }
 
 // Four codes packed (the first in the low byte); all 0 where inv is 0.
-__device__ __forceinline__ uint32_t ckpt_word(float a, float b, float c, float d, float inv) {
-  const uint32_t w = __byte_perm(__byte_perm(ckpt_code(a, inv), ckpt_code(b, inv), 0x0040u),
-                                 __byte_perm(ckpt_code(c, inv), ckpt_code(d, inv), 0x0040u), 0x5410u);
+__device__ __forceinline__ uint32_t ckpt_word(f32x2 u01, f32x2 u23, float inv) {
+  // (scalar products: a packed product and sum are contracted into one
+  // rounding, which the form's definition does not have)
+  float c[4];
+  unpair(u01, c[0], c[1]);
+  unpair(u23, c[2], c[3]);
+  const f32x2 magic = pair_of(12582912.f);
+  unpair(add2(pair_of(__fmul_rn(c[0], inv), __fmul_rn(c[1], inv)), magic), c[0], c[1]);
+  unpair(add2(pair_of(__fmul_rn(c[2], inv), __fmul_rn(c[3], inv)), magic), c[2], c[3]);
+  const uint32_t w = __byte_perm(__byte_perm(__float_as_uint(c[0]), __float_as_uint(c[1]), 0x0040u),
+                                 __byte_perm(__float_as_uint(c[2]), __float_as_uint(c[3]), 0x0040u), 0x5410u);
   return inv == 0.f ? 0u : w;
 }
 
-// The FP32 value of the signed byte at position `i` of `word`: the byte,
-// offset by 128, placed in the mantissa of 2^23.
-__device__ __forceinline__ float ckpt_byte(uint32_t word, int i) {
-  const uint32_t biased = __byte_perm(word ^ 0x80808080u, 0x4B000000u, 0x7440u + static_cast<uint32_t>(i));
-  return __uint_as_float(biased) - 8388736.f;  // 2^23 + 128
+// The FP32 values of the signed bytes 2·i and 2·i + 1 of a word: a byte,
+// offset by 128 (`flipped`: the word with every top bit inverted), placed in
+// the mantissa of 2^23.
+__device__ __forceinline__ f32x2 ckpt_pair(uint32_t flipped, int i) {
+  const uint32_t a = __byte_perm(flipped, 0x4B000000u, 0x7440u + static_cast<uint32_t>(2 * i));
+  const uint32_t b = __byte_perm(flipped, 0x4B000000u, 0x7441u + static_cast<uint32_t>(2 * i));
+  return add2(pair_of(__uint_as_float(a), __uint_as_float(b)), pair_of(-8388736.f));  // 2^23 + 128
 }
 
 // The largest of three magnitudes; a NaN wins.
@@ -196,49 +236,68 @@ __device__ __forceinline__ void lin_prefetch_row(const LinEpi& e, int64_t M, int
   }
 }
 
-// Eight FP32 values (bits), rounded and packed, into chunk j of the
-// 128-byte-swizzled staging row of `lane`.
-__device__ __forceinline__ uint4 pack8(const uint32_t* v) {
-  return make_uint4(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]), pack_half2(v[4], v[5]), pack_half2(v[6], v[7]));
+__device__ __forceinline__ uint32_t pack_half2(f32x2 v) {
+  float a, b;
+  unpair(v, a, b);
+  return pack_half2(__float_as_uint(a), __float_as_uint(b));
+}
+__device__ __forceinline__ f32x2 unpack_half2(uint32_t h) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return pair_of(f.x, f.y);
+}
+// Eight FP32 values, rounded and packed.
+__device__ __forceinline__ uint4 pack8(const f32x2* v) {
+  return make_uint4(pack_half2(v[0]), pack_half2(v[1]), pack_half2(v[2]), pack_half2(v[3]));
+}
+// v[0..3] += eight FP16 values.
+__device__ __forceinline__ void add8(f32x2* v, uint4 h) {
+  v[0] = add2(v[0], unpack_half2(h.x));
+  v[1] = add2(v[1], unpack_half2(h.y));
+  v[2] = add2(v[2], unpack_half2(h.z));
+  v[3] = add2(v[3], unpack_half2(h.w));
 }
 
-// Row `lane` of a staged 32×64 box, columns x0 .. x0+63 (one 8-bit group):
-// the 64 accumulators of row `grow` (v0: the first 32) through the epilogue
-// into the staging row, as stage_row64 does. N, the pitches and x0 are
-// multiples of 8, so eight columns are inside the matrix or none.
+// The 64 accumulators of a TMEM row as pairs.
+__device__ __forceinline__ void tmem_row64(uint32_t taddr, f32x2 (&v)[32]) {
+  uint32_t a[32], b[32];
+  tmem_ld_32x32b_x32(taddr, a);
+  tmem_ld_32x32b_x32(taddr + 32, b);
+  tmem_ld_wait(a);
+  tmem_ld_wait(b);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    v[i] = pair_of(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1]));
+    v[16 + i] = pair_of(__uint_as_float(b[2 * i]), __uint_as_float(b[2 * i + 1]));
+  }
+}
+
+// Row `lane` of a staged 32×64 box, columns x0 .. x0+63 (one 8-bit group) of
+// row `grow`: its 64 accumulators v through the epilogue into the
+// 128-byte-swizzled staging row, as stage_row64 does. N, the pitches and x0
+// are multiples of 8, so eight columns are inside the matrix or none.
 template <int EPI>
-__device__ __forceinline__ void lin_stage_row64(uint8_t* row, int lane, uint32_t (&v0)[32], uint32_t (&v1)[32],
-                                                const LinEpi& e, int64_t M, int64_t N, int64_t grow, int64_t x0) {
+__device__ __forceinline__ void lin_row64(uint8_t* row, int lane, f32x2 (&v)[32], const LinEpi& e, int64_t M,
+                                          int64_t N, int64_t grow, int64_t x0) {
   const bool in_m = grow < M;
-  auto half_of = [&](int j) -> uint32_t* { return j < 4 ? v0 + 8 * j : v1 + 8 * (j - 4); };
   if constexpr (EPI == kEpiLinear) {
     if (e.bias) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint4 b8 = load_bias8(e.bias, x0 + 8 * j, N);
-        const __half* b = reinterpret_cast<const __half*>(&b8);
-        uint32_t* v = half_of(j);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __half2float(b[i]));
-      }
+      for (int j = 0; j < 8; ++j) add8(v + 4 * j, load_bias8(e.bias, x0 + 8 * j, N));
     }
     if (e.codes) {
-      // columns past N hold 0: zero-filled operands and no bias
-      float t0 = 0.f, t1 = 0.f;
+      // (columns past N hold 0: zero-filled operands and no bias)
+      float top = 0.f;
 #pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        t0 = max_abs3(t0, __uint_as_float(v0[i]), __uint_as_float(v0[i + 1]));
-        t1 = max_abs3(t1, __uint_as_float(v1[i]), __uint_as_float(v1[i + 1]));
+      for (int i = 0; i < 32; ++i) {
+        float a, b;
+        unpair(v[i], a, b);
+        top = max_abs3(top, a, b);
       }
       float scale, inv;
-      ckpt_scale(magnitude_bits(max_abs3(t0, t1, 0.f)), scale, inv);
+      ckpt_scale(magnitude_bits(top), scale, inv);
       uint32_t w[16];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const uint32_t* v = j < 8 ? v0 + 4 * j : v1 + 4 * (j - 8);
-        w[j] = ckpt_word(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]), __uint_as_float(v[3]),
-                         inv);
-      }
+      for (int j = 0; j < 16; ++j) w[j] = ckpt_word(v[2 * j], v[2 * j + 1], inv);
       if (in_m) {
         int8_t* q = e.codes + grow * e.ldq + x0;
         if (x0 + 64 <= N && (reinterpret_cast<uintptr_t>(q) & 15u) == 0) {
@@ -254,15 +313,11 @@ __device__ __forceinline__ void lin_stage_row64(uint8_t* row, int lane, uint32_t
       }
     }
     with_activation(e.act, [&](auto a) {
-      if constexpr (decltype(a)::value != HGEMM_ACT_NONE) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float f, df;
-          activate<decltype(a)::value, false>(__uint_as_float(v0[i]), f, df);
-          v0[i] = __float_as_uint(f);
-          activate<decltype(a)::value, false>(__uint_as_float(v1[i]), f, df);
-          v1[i] = __float_as_uint(f);
-        }
+      for (int i = 0; i < 32; ++i) {
+        f32x2 f, df;
+        activate<decltype(a)::value, false>(v[i], f, df);
+        v[i] = f;
       }
     });
     if (e.res && in_m) {
@@ -272,12 +327,7 @@ __device__ __forceinline__ void lin_stage_row64(uint8_t* row, int lane, uint32_t
       for (int j = 0; j < 8; ++j)
         r8[j] = x0 + 8 * j < N ? *reinterpret_cast<const uint4*>(r + 8 * j) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const __half* h = reinterpret_cast<const __half*>(&r8[j]);
-        uint32_t* v = half_of(j);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __half2float(h[i]));
-      }
+      for (int j = 0; j < 8; ++j) add8(v + 4 * j, r8[j]);
     }
   } else if (e.codes) {
     uint32_t w[16];
@@ -302,30 +352,23 @@ __device__ __forceinline__ void lin_stage_row64(uint8_t* row, int lane, uint32_t
       }
       scale = e.scales[x0 / kCkptGroup * e.lds + grow];
     }
-    uint32_t hid[32];
+    uint16_t* h = e.h + grow * e.ldh + x0;
     with_activation(e.act, [&](auto a) {
 #pragma unroll
-      for (int i = 0; i < 64; i += 2) {
-        float f[2], df;
+      for (int j = 0; j < 8; ++j) {
+        f32x2 f[4], df;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t& v = i < 32 ? v0[i + k] : v1[i - 32 + k];
-          activate<decltype(a)::value, true>(ckpt_byte(w[i / 4], (i + k) & 3) * scale, f[k], df);
-          v = __float_as_uint(__uint_as_float(v) * df);
+        for (int i = 0; i < 4; ++i) {
+          const f32x2 u = mul2(ckpt_pair(w[2 * j + i / 2] ^ 0x80808080u, i & 1), pair_of(scale));
+          activate<decltype(a)::value, true>(u, f[i], df);
+          v[4 * j + i] = mul2(v[4 * j + i], df);
         }
-        hid[i / 2] = pack_half2(__float_as_uint(f[0]), __float_as_uint(f[1]));
+        if (e.h && in_m && x0 + 8 * j < N) *reinterpret_cast<uint4*>(h + 8 * j) = pack8(f);
       }
     });
-    if (e.h && in_m) {
-      uint16_t* h = e.h + grow * e.ldh + x0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (x0 + 8 * j < N)
-          reinterpret_cast<uint4*>(h)[j] = make_uint4(hid[4 * j], hid[4 * j + 1], hid[4 * j + 2], hid[4 * j + 3]);
-    }
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(row + ((j ^ (lane & 7)) << 4)) = pack8(half_of(j));
+  for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(row + ((j ^ (lane & 7)) << 4)) = pack8(v + 4 * j);
 }
 
 }  // namespace hg
