@@ -165,40 +165,39 @@ cudaError_t rows_tiles(const RowsArgs& p, bool vec, int num_sms, cudaStream_t st
   return blocks <= 2 * num_sms ? rows_with<MT, 16>(p, vec, stream) : rows_with<MT, 8>(p, vec, stream);
 }
 
-// Column sums, in a fixed order. A cluster of CTAs takes 64 columns (128
-// bytes of a row, so that every row's piece is whole sectors), each CTA a run
-// of rows; within a CTA a thread takes VEC neighbouring columns of every
-// 256·VEC/64-th row, kUnroll rows in flight, then the threads of a column are
-// added in order through shared memory, and the CTAs in rank order through
-// distributed shared memory by rank 0. Bound by reading dY once.
-constexpr int kSumCols = 64;
+// Column sums, in a fixed order. A cluster of CTAs takes a strip of columns,
+// each CTA a run of rows; within a CTA `across` threads lie along a row, VEC
+// neighbouring columns each, the others down the rows, kUnroll rows in
+// flight per thread. The threads of a column are added in order through
+// shared memory, and the CTAs in rank order through distributed shared memory
+// by rank 0. Bound by reading dY once; a strip is as wide as leaves enough
+// CTAs, because the longer a row's piece the better memory delivers it.
+constexpr int kSumThreads = 512;
 constexpr int kUnroll = 8;
 template <int VEC>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kSumThreads)
     column_sums_kernel(const uint16_t* __restrict__ dy, int64_t ld, int64_t M, int64_t N, float* __restrict__ out,
-                       int accumulate, int cluster) {
-  constexpr int ACROSS = kSumCols / VEC;  // threads across the columns
-  constexpr int DOWN = 256 / ACROSS;      // threads down the rows
-  __shared__ float s[DOWN][kSumCols + 1];
-  __shared__ float part[kSumCols + 2];
+                       int accumulate, int across, int cluster) {
+  __shared__ float s[kSumThreads * VEC];  // [down][columns]
   grid_dependency_wait();
   grid_launch_dependents();
+  const int columns = across * VEC, down = kSumThreads / across;
   const int rank = static_cast<int>(blockIdx.x) % cluster;
-  const int c = threadIdx.x % ACROSS * VEC, r = threadIdx.x / ACROSS;
-  const int64_t n = static_cast<int64_t>(blockIdx.x) / cluster * kSumCols + c;
-  const int64_t m0 = M * rank / cluster, m1 = M * (rank + 1) / cluster;
+  const int c = threadIdx.x % across * VEC, r = threadIdx.x / across;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) / cluster * columns;
+  const int64_t m1 = M * (rank + 1) / cluster;
   float sum[VEC] = {};
-  if (n < N) {
-    for (int64_t m = m0 + r; m < m1; m += DOWN * kUnroll) {
+  if (n0 + c < N) {
+    for (int64_t m = M * rank / cluster + r; m < m1; m += down * kUnroll) {
       uint16_t v[kUnroll][VEC];
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) {
-        const int64_t row = m + k * DOWN;
+        const int64_t row = m + k * down;
         if constexpr (VEC == 8)
-          *reinterpret_cast<uint4*>(v[k]) =
-              row < m1 ? __ldg(reinterpret_cast<const uint4*>(dy + row * ld + n)) : make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(v[k]) = row < m1 ? __ldg(reinterpret_cast<const uint4*>(dy + row * ld + n0 + c))
+                                                     : make_uint4(0u, 0u, 0u, 0u);
         else
-          v[k][0] = row < m1 ? __ldg(dy + row * ld + n) : static_cast<uint16_t>(0);
+          v[k][0] = row < m1 ? __ldg(dy + row * ld + n0 + c) : static_cast<uint16_t>(0);
       }
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k)
@@ -207,23 +206,23 @@ __global__ void __launch_bounds__(256)
     }
   }
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) s[r][c + i] = sum[i];
+  for (int i = 0; i < VEC; ++i) s[r * columns + c + i] = sum[i];
   __syncthreads();
   float total = 0.f;
-  if (threadIdx.x < kSumCols) {
-#pragma unroll
-    for (int i = 0; i < DOWN; ++i) total += s[i][threadIdx.x];
-    part[threadIdx.x] = total;
+  const bool mine = static_cast<int>(threadIdx.x) < columns;
+  if (mine) {
+    for (int i = 0; i < down; ++i) total += s[i * columns + threadIdx.x];
+    s[threadIdx.x] = total;  // (only this thread reads its column)
   }
   if (cluster > 1) {
     cluster_sync();
-    if (rank == 0 && threadIdx.x < kSumCols)
+    if (rank == 0 && mine)
       for (int i = 1; i < cluster; ++i)
-        total += ld_cluster_f32(mapa_shared(smem_u32(&part[threadIdx.x]), static_cast<uint32_t>(i)));
+        total += ld_cluster_f32(mapa_shared(smem_u32(&s[threadIdx.x]), static_cast<uint32_t>(i)));
     cluster_sync();  // the other ranks' shared memory stays until rank 0 has read it
   }
-  const int64_t col = static_cast<int64_t>(blockIdx.x) / cluster * kSumCols + threadIdx.x;
-  if (rank == 0 && threadIdx.x < kSumCols && col < N) out[col] = accumulate ? out[col] + total : total;
+  const int64_t n = n0 + threadIdx.x;
+  if (rank == 0 && mine && n < N) out[n] = accumulate ? out[n] + total : total;
 }
 
 }  // namespace
@@ -260,15 +259,20 @@ cudaError_t launch_linear_empty(uint16_t* C, int64_t ldc, int64_t M, int64_t N, 
 cudaError_t launch_column_sums(const uint16_t* dy, int64_t ld, int64_t M, int64_t N, float* out, bool accumulate,
                                cudaStream_t stream) {
   const bool vec = N % 8 == 0 && ld % 8 == 0 && (reinterpret_cast<uintptr_t>(dy) & 15u) == 0;
-  // up to 8 CTAs (the portable cluster size) per 64 columns, 256 rows or more each
+  const int vec_cols = vec ? 8 : 1;
+  // up to 8 CTAs (the portable cluster size) per strip, 128 rows or more each
   int cluster = 1;
-  while (cluster < 8 && M >= 512 * cluster) cluster *= 2;
-  const int64_t blocks = (N + kSumCols - 1) / kSumCols * cluster;
-  if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  PdlLaunch l(dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream);
+  while (cluster < 8 && M >= 256 * cluster) cluster *= 2;
+  // from 512 bytes of a row down to 64, while a strip's CTAs are fewer than
+  // would fill most of the GPU
+  int across = vec ? 32 : 256;
+  auto blocks = [&] { return (N + across * vec_cols - 1) / (across * vec_cols) * cluster; };
+  while (across > (vec ? 4 : 32) && blocks() < 128) across /= 2;
+  if (blocks() > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  PdlLaunch l(dim3(static_cast<unsigned>(blocks())), dim3(kSumThreads), 0, stream);
   l.cluster(static_cast<unsigned>(cluster));
   return cudaLaunchKernelEx(&l.cfg, vec ? column_sums_kernel<8> : column_sums_kernel<1>, dy, ld, M, N, out,
-                            accumulate ? 1 : 0, cluster);
+                            accumulate ? 1 : 0, across, cluster);
 }
 
 // The -DHGEMM_DEBUG build's check word of this file (null otherwise).

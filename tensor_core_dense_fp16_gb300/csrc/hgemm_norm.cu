@@ -8,6 +8,7 @@
 #include "debug.cuh"
 #include "internal.h"
 #include "kernel_common.cuh"
+#include "linear_epilogue.cuh"
 #include "ptx.cuh"
 
 namespace hg {
@@ -27,6 +28,13 @@ __device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
   }
 }
 
+__device__ __forceinline__ void unpack8(uint4 v, f32x2 (&f)[4]) {
+  f[0] = unpack_half2(v.x);
+  f[1] = unpack_half2(v.y);
+  f[2] = unpack_half2(v.z);
+  f[3] = unpack_half2(v.w);
+}
+
 __device__ __forceinline__ uint4 pack8f(const float (&f)[8]) {
   uint32_t w[4];
 #pragma unroll
@@ -38,6 +46,19 @@ __device__ __forceinline__ float warp_sum(float a) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
   return a;
+}
+
+// Both sums over a warp, in every lane, in 6 shuffles instead of 10: after the
+// first the lower lanes go on with a and the upper with b.
+__device__ __forceinline__ void warp_sum2(float& a, float& b) {
+  const bool upper = (threadIdx.x & 16) != 0;
+  const float other = __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
+  float v = (upper ? b : a) + other;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const float w = __shfl_xor_sync(0xffffffffu, v, 16);
+  a = upper ? w : v;
+  b = upper ? v : w;
 }
 
 // A sum over the G threads that share a row, in each of them. `s` holds one
@@ -184,8 +205,7 @@ struct RingCfg {
   static constexpr int OFF_MISC = OFF_EXCHANGE + 2 * (THREADS / 32) * 8;  // two buffers of one float2 per warp
   static constexpr int SMEM_BYTES = OFF_MISC + 16;
   static_assert(SMEM_BYTES <= 232448 - 1024, "fits an SM");
-  // the groups' sums are added through the ring, 8 columns at a time per thread
-  static_assert(GROUPS == 1 || THREADS * 8 * 4 * NV * 2 <= RING_BYTES, "final sums fit the ring");
+  static_assert(GROUPS == 1 || THREADS * 8 * 4 * NV * 2 <= RING_BYTES, "the groups' sums fit the ring");
 };
 
 template <int G, int NV, bool RES>
@@ -229,14 +249,14 @@ __global__ void __launch_bounds__(512, 1) layernorm_backward_ring_kernel(const N
       if (first + i * step < a.M) copy_row(first + i * step, i);
 
   uint4 gamma[NV];
-  float dgamma[NV][8], dbeta[NV][8];
+  f32x2 dgamma[NV][4], dbeta[NV][4];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (t + i * G) * 8;
     gamma[i] = make_uint4(0u, 0u, 0u, 0u);
     if (c < D) gamma[i] = __ldg(reinterpret_cast<const uint4*>(a.gamma + c));
 #pragma unroll
-    for (int k = 0; k < 8; ++k) dgamma[i][k] = dbeta[i][k] = 0.f;
+    for (int k = 0; k < 4; ++k) dgamma[i][k] = dbeta[i][k] = 0;  // a pair of +0
   }
 
   const float inv_d = 1.f / static_cast<float>(D);
@@ -261,29 +281,35 @@ __global__ void __launch_bounds__(512, 1) layernorm_backward_ring_kernel(const N
     const uint4* sdy = reinterpret_cast<const uint4*>(ring + static_cast<uint32_t>(stage) * stage_bytes + row_bytes);
     const uint4* sres =
         reinterpret_cast<const uint4*>(ring + static_cast<uint32_t>(stage) * stage_bytes + 2 * row_bytes);
-    const float shift = -mu * rs;
-    float s1 = 0.f, s2 = 0.f;
+    const f32x2 scale = pair_of(rs), shift = pair_of(-mu * rs);
+    f32x2 p1 = 0, p2 = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = t + i * G;
       if (v * 8 < D) {
-        float x[8], dy[8], g[8];
+        f32x2 x[4], dy[4], g[4];
         unpack8(sx[v], x);
         unpack8(sdy[v], dy);
         unpack8(gamma[i], g);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float xh = fmaf(x[k], rs, shift);
-          const float gy = dy[k] * g[k];
-          s1 += gy;
-          s2 = fmaf(gy, xh, s2);
-          dgamma[i][k] = fmaf(dy[k], xh, dgamma[i][k]);
-          dbeta[i][k] += dy[k];
+        for (int k = 0; k < 4; ++k) {
+          const f32x2 xh = fma2(x[k], scale, shift), gy = mul2(dy[k], g[k]);
+          p1 = add2(p1, gy);
+          p2 = fma2(gy, xh, p2);
+          dgamma[i][k] = fma2(dy[k], xh, dgamma[i][k]);
+          dbeta[i][k] = add2(dbeta[i][k], dy[k]);
         }
       }
     }
-    s1 = warp_sum(s1);
-    s2 = warp_sum(s2);
+    float s1, s2;
+    {
+      float lo, hi;
+      unpair(p1, lo, hi);
+      s1 = lo + hi;
+      unpair(p2, lo, hi);
+      s2 = lo + hi;
+    }
+    warp_sum2(s1, s2);
     if constexpr (Cfg::WARPS > 1) {
       float2* ex = exchange + flip * (Cfg::THREADS / 32) + group * Cfg::WARPS;
       if (lane == 0) ex[warp - group * Cfg::WARPS] = make_float2(s1, s2);
@@ -304,26 +330,24 @@ __global__ void __launch_bounds__(512, 1) layernorm_backward_ring_kernel(const N
       const int64_t ahead = m + (stages - 1) * step;
       if (ahead < a.M && !*abort_flag) copy_row(ahead, stage == 0 ? stages - 1 : stage - 1);
     }
-    const float k1 = -rs * (s1 * inv_d), k2 = -rs * (s2 * inv_d);
+    const f32x2 k1 = pair_of(-rs * (s1 * inv_d)), k2 = pair_of(-rs * (s2 * inv_d));
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = t + i * G;
       if (v * 8 < D) {
-        float x[8], dy[8], g[8];
+        f32x2 x[4], dy[4], g[4];
         unpack8(sx[v], x);
         unpack8(sdy[v], dy);
         unpack8(gamma[i], g);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float xh = fmaf(x[k], rs, shift);
-          x[k] = fmaf(dy[k] * g[k], rs, fmaf(xh, k2, k1));
-        }
+        for (int k = 0; k < 4; ++k)
+          x[k] = fma2(mul2(dy[k], g[k]), scale, fma2(fma2(x[k], scale, shift), k2, k1));
         if (RES) {
           unpack8(sres[v], dy);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) x[k] += dy[k];
+          for (int k = 0; k < 4; ++k) x[k] = add2(x[k], dy[k]);
         }
-        *reinterpret_cast<uint4*>(a.y + m * a.ldy + v * 8) = pack8f(x);
+        *reinterpret_cast<uint4*>(a.y + m * a.ldy + v * 8) = pack8(x);
       }
     }
     mu = next_mu;
@@ -352,12 +376,10 @@ __global__ void __launch_bounds__(512, 1) layernorm_backward_ring_kernel(const N
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int k = 0; k < 8; k += 4) {
-        const int c = (t + i * G) * 8 + k;
-        *reinterpret_cast<float4*>(mine + c) =
-            make_float4(dgamma[i][k], dgamma[i][k + 1], dgamma[i][k + 2], dgamma[i][k + 3]);
-        *reinterpret_cast<float4*>(mine + NV * 8 * G + c) =
-            make_float4(dbeta[i][k], dbeta[i][k + 1], dbeta[i][k + 2], dbeta[i][k + 3]);
+      for (int k = 0; k < 2; ++k) {
+        const int c = (t + i * G) * 8 + 4 * k;
+        *reinterpret_cast<ulonglong2*>(mine + c) = make_ulonglong2(dgamma[i][2 * k], dgamma[i][2 * k + 1]);
+        *reinterpret_cast<ulonglong2*>(mine + NV * 8 * G + c) = make_ulonglong2(dbeta[i][2 * k], dbeta[i][2 * k + 1]);
       }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * NV * 8 * G; i += Cfg::THREADS) {
@@ -374,11 +396,9 @@ __global__ void __launch_bounds__(512, 1) layernorm_backward_ring_kernel(const N
       const int c = (t + i * G) * 8;
       if (c < D) {
 #pragma unroll
-        for (int k = 0; k < 8; k += 4) {
-          *reinterpret_cast<float4*>(out + c + k) =
-              make_float4(dgamma[i][k], dgamma[i][k + 1], dgamma[i][k + 2], dgamma[i][k + 3]);
-          *reinterpret_cast<float4*>(out + D + c + k) =
-              make_float4(dbeta[i][k], dbeta[i][k + 1], dbeta[i][k + 2], dbeta[i][k + 3]);
+        for (int k = 0; k < 2; ++k) {
+          *reinterpret_cast<ulonglong2*>(out + c + 4 * k) = make_ulonglong2(dgamma[i][2 * k], dgamma[i][2 * k + 1]);
+          *reinterpret_cast<ulonglong2*>(out + D + c + 4 * k) = make_ulonglong2(dbeta[i][2 * k], dbeta[i][2 * k + 1]);
         }
       }
     }
@@ -551,14 +571,16 @@ cudaError_t launch_layernorm_backward(const NormArgs& a, int num_sms, cudaStream
   if (a.M == 0) {
     // no rows: the sums of nothing
   } else if (ring) {
-    // 16 columns per thread, so that two rows of 512 sums fit its registers
-    // (32 for rows past 8192): the fewer threads a row needs, the more rows
-    // a CTA has under way
+    // 16 columns per thread, and 32 where a row would otherwise take the whole
+    // CTA: the fewer threads a row needs, the more rows a CTA has under way,
+    // each waiting for its own copies and exchanges. With residual, 16384
+    // rows: 8192 columns on 512 threads (one row at a time) 207 us, on 256
+    // (two rows) 171; 4096 columns on 256 threads 83 us, on 128 88.
     e = a.D <= 512    ? ring_group<32, 2>(a, num_sms, &partials, stream)
         : a.D <= 1024 ? ring_group<64, 2>(a, num_sms, &partials, stream)
         : a.D <= 2048 ? ring_group<128, 2>(a, num_sms, &partials, stream)
         : a.D <= 4096 ? ring_group<256, 2>(a, num_sms, &partials, stream)
-        : a.D <= 8192 ? ring_group<512, 2>(a, num_sms, &partials, stream)
+        : a.D <= 8192 ? ring_group<256, 4>(a, num_sms, &partials, stream)
                       : ring_group<512, 4>(a, num_sms, &partials, stream);
   } else {
     PdlLaunch p(dim3(static_cast<unsigned>((a.D + 31) / 32), kSlices), dim3(kThreads), 0, stream);
