@@ -74,7 +74,7 @@ cudaError_t debug_words(int* (&out)[hg::kDebugWords]) {
                                                       hg::debug_word_generic, hg::debug_word_trsm,
                                                       hg::debug_word_trileaf, hg::debug_word_chain,
                                                       hg::debug_word_linear,  hg::debug_word_norm,
-                                                      hg::debug_word_ckpt8};
+                                                      hg::debug_word_ckpt8,   hg::debug_word_linear_any};
   for (int i = 0; i < hg::kDebugWords; ++i) {
     const cudaError_t e = get[i](&out[i]);
     if (e != cudaSuccess) return e;
@@ -665,10 +665,6 @@ int dispatch(const Gemm& g, const hg::EpiArgs& epi, const DeviceState& dev, cuda
       hg::PlainArgs pa{static_cast<const uint16_t*>(g.A), static_cast<const uint16_t*>(g.B),
                        static_cast<uint16_t*>(g.C), g.M, g.N, g.K, g.lda, g.ldb, g.ldc,
                        t_ctx.status, g_timeout_ns.load(), epi, g.a_mn ? 1 : 0, g.b_mn ? 1 : 0};
-      if (g.lin) {
-        pa.kind = g.kind(epi);
-        pa.lin = *g.lin;
-      }
       e = hg::launch_generic(pa, dev.num_sms, stream);
       return e == cudaSuccess ? HGEMM_OK : cuda_fail(e);
     }
@@ -740,12 +736,35 @@ int run_linear(const LinearProduct& p, cudaStream_t stream) {
   DeviceState* dev = nullptr;
   const int rc = current_device(&dev);
   if (rc != HGEMM_OK) return rc;
+  const int forced = g_forced_path.load(std::memory_order_relaxed);
+  if (forced < 0 && linear_rows_suits(p)) return cuda_status(launch_linear_rows(p, dev->num_sms, stream));
   Gemm g{p.A, p.B, p.C, p.M, p.N, p.K, p.lda, p.ldb, p.ldc};
+  g.a_mn = p.a_mn;
   g.b_mn = p.b_mn;
   g.lin = &p.epi;
-  if (g_forced_path.load(std::memory_order_relaxed) < 0 && linear_rows_suits(p))
-    return cuda_status(launch_linear_rows(p, dev->num_sms, stream));
+  if (p.K > 0 && (forced == HGEMM_PATH_GENERIC || !tma_ok(g))) {
+    const CallDevice cd{dev->num_sms, t_ctx.status, g_timeout_ns.load(std::memory_order_relaxed)};
+    return cuda_status(launch_linear_any(p, cd, stream));
+  }
   return dispatch(g, kPlainEpilogue, *dev, stream);
+}
+
+int run_wgrad(const LinearProduct& p, cudaStream_t stream) {
+  Gemm g{p.A, p.B, p.C, p.M, p.N, p.K, p.lda, p.ldb, p.ldc};
+  g.a_mn = p.a_mn;
+  g.b_mn = p.b_mn;
+  const int forced = g_forced_path.load(std::memory_order_relaxed);
+  if (p.K > 0 && (forced == HGEMM_PATH_GENERIC || !tma_ok(g))) return run_linear(p, stream);
+  DeviceState* dev = nullptr;
+  const int rc = current_device(&dev);
+  if (rc != HGEMM_OK) return rc;
+  // (the plain and the accumulating product; the sum of an old value is the residual's)
+  EpiArgs epi = kPlainEpilogue;
+  if (p.epi.res) {
+    epi.beta = 1.0f;
+    epi.mode = 2;
+  }
+  return dispatch(g, epi, *dev, stream);
 }
 
 }  // namespace hg

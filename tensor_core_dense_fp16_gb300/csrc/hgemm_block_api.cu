@@ -70,7 +70,7 @@ int hgemm_linear(const hgemm_half_t* X, int64_t ldx, const hgemm_half_t* W, int6
   if ((overlap(y, r) && !same(y, r)) || overlap(q, r) || overlap(s, r)) return HGEMM_ERR_ALIAS;
   if (overlap(y, q) || overlap(y, s) || overlap(q, s)) return HGEMM_ERR_ALIAS;
   if (M == 0 || N == 0) return HGEMM_OK;
-  const hg::LinearProduct p{X, ldx, W, ldw, false, Y, ldy, M, N, K,
+  const hg::LinearProduct p{X, ldx, false, W, ldw, false, Y, ldy, M, N, K,
                             hg::LinEpi{0, act, bias, R, ldr, codes, ldq, scales, lds, nullptr, 0}};
   return hg::run_linear(p, stream);
 }
@@ -93,7 +93,7 @@ int hgemm_linear_dgrad(const hgemm_half_t* dY, int64_t lddy, const hgemm_half_t*
       if (overlap(o, v)) return HGEMM_ERR_ALIAS;
   if (overlap(du, h)) return HGEMM_ERR_ALIAS;
   if (M == 0 || K == 0) return HGEMM_OK;
-  const hg::LinearProduct p{dY, lddy, W, ldw, true, dU, lddu, M, K, N,
+  const hg::LinearProduct p{dY, lddy, false, W, ldw, true, dU, lddu, M, K, N,
                             hg::LinEpi{1, act, nullptr, nullptr, 0, const_cast<int8_t*>(codes), ldq,
                                        const_cast<float*>(scales), lds, H, ldh}};
   return hg::run_linear(p, stream);
@@ -120,9 +120,10 @@ int hgemm_linear_wgrad(const hgemm_half_t* dY, int64_t lddy, const hgemm_half_t*
     if (rc != HGEMM_OK) return rc;
   }
   if (K == 0) return HGEMM_OK;
-  // dWᵀ's layouts are hgemm_layout's: dYᵀ is N×M with the rows contiguous in M's pitch
-  return hgemm_layout(HGEMM_A_COL_MAJOR, HGEMM_B_ROW_MAJOR, dY, lddy, X, ldx, dW, lddw, N, K, M, 1.0f,
-                      accumulate ? 1.0f : 0.0f, nullptr, 0, stream);
+  const uint16_t* old = accumulate ? dW : nullptr;
+  const hg::LinearProduct p{dY, lddy, true, X, ldx, true, dW, lddw, N, K, M,
+                            hg::LinEpi{0, HGEMM_ACT_NONE, nullptr, old, lddw, nullptr, 0, nullptr, 0, nullptr, 0}};
+  return hg::run_wgrad(p, stream);
 }
 
 int hgemm_layernorm_forward(const hgemm_half_t* X, int64_t ldx, const hgemm_half_t* gamma, const hgemm_half_t* beta,

@@ -32,7 +32,6 @@
 
 #include "internal.h"
 #include "kernel_common.cuh"
-#include "linear_epilogue.cuh"
 #include "ptx.cuh"
 
 namespace hg {
@@ -54,13 +53,7 @@ struct GenCfg {
   static constexpr int THREADS = 9 * 32;
   static constexpr int TMEM_COLS = 2 * BN;  // two accumulators: two CTAs per SM fill TMEM
   static constexpr uint32_t IDESC = idesc_f16_f32acc(BM, BN);
-  // linear epilogues: each epilogue warp turns 32 rows × 16 columns around in
-  // shared memory (rows of 17 words), with the rows' scales
-  static constexpr int TURN_COLS = 16;
-  static constexpr int TURN_WORDS = 32 * (TURN_COLS + 1) + 2 * 32;
-  static constexpr int OFF_TURN = (OFF_MISC + 16 + 15) / 16 * 16;
-  static constexpr int LIN_SMEM_BYTES = OFF_TURN + EPI_WARPS * TURN_WORDS * 4 + 1024;
-  static_assert(2 * (LIN_SMEM_BYTES + 1024) <= 233472, "two CTAs per SM");
+  static_assert(2 * (SMEM_BYTES + 1024) <= 233472, "two CTAs per SM");
 };
 
 // Row r of a K block (the values of `src` with index in [first, n); zeros
@@ -213,7 +206,7 @@ __device__ __forceinline__ GenUnit gen_unit(const PlainArgs& p, const TriLeaves&
 // operand of each unit is the lower triangle of a square block (column i of
 // the triangle, i.e. operand row gj, holds its values from index gj on), so
 // values at k < gj are replaced by zero as they are loaded.
-template <bool TRI_B, int EPI = kEpiFused>
+template <bool TRI_B>
 __device__ __forceinline__ void generic_units(const PlainArgs& p, const TriLeaves& leaves, int64_t units,
                                               int64_t tiles_m, int64_t tiles_n) {
   using Cfg = GenCfg;
@@ -406,76 +399,8 @@ __device__ __forceinline__ void generic_units(const PlainArgs& p, const TriLeave
       const int64_t gi = u.m0 + q * 32 + lane;
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * Cfg::BN);
       const PlainArgs& c = u.q;
-      if constexpr (EPI >= kEpiLinear) {
-        // A lane holds a row of the accumulator, but rows of unaligned
-        // outputs are best read and written along the columns: 16 columns
-        // at a time go through shared memory, so that a warp's accesses are
-        // two runs of 16 neighbouring elements.
-        constexpr bool BACKWARD = EPI == kEpiLinearGrad;
-        const LinEpi& e = c.lin;
-        float* turn = reinterpret_cast<float*>(smem + Cfg::OFF_TURN) + q * Cfg::TURN_WORDS;
-        float* row_scale = turn + 32 * (Cfg::TURN_COLS + 1);
-        float* row_inv = row_scale + 32;
-        const __half* bias = reinterpret_cast<const __half*>(e.bias);
-        auto biased = [&](uint32_t v, int64_t n) {
-          const float x = __uint_as_float(v);
-          return !BACKWARD && bias && n < c.N ? x + __half2float(bias[n]) : x;
-        };
 #pragma unroll 1
-        for (int64_t col0 = u.n0; col0 < u.n0 + Cfg::BN && col0 < c.N; col0 += kCkptGroup) {
-          const uint32_t t_group = t_row + static_cast<uint32_t>(col0 - u.n0);
-          float scale = 0.f, inv = 0.f;
-          if (e.codes) {
-            float* s = e.scales + col0 / kCkptGroup * e.lds + gi;
-            if constexpr (BACKWARD) {
-              if (gi < c.M) scale = *s;
-            } else {
-              float top = 0.f;
-#pragma unroll 1
-              for (int ch = 0; ch < 2; ++ch) {
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(t_group + ch * 32, v);
-                tmem_ld_wait(v);
-#pragma unroll
-                for (int j = 0; j < 32; j += 2) {
-                  const int64_t n = col0 + ch * 32 + j;
-                  top = max_abs3(top, n < c.N ? biased(v[j], n) : 0.f, n + 1 < c.N ? biased(v[j + 1], n + 1) : 0.f);
-                }
-              }
-              ckpt_scale(magnitude_bits(top), scale, inv);
-              if (gi < c.M) *s = scale;
-            }
-          }
-          row_scale[lane] = scale;
-          row_inv[lane] = inv;
-#pragma unroll 1
-          for (int ch = 0; ch < 2; ++ch) {
-            uint32_t v[32];
-            tmem_ld_32x32b_x32(t_group + ch * 32, v);
-            tmem_ld_wait(v);
-#pragma unroll
-            for (int part = 0; part < 2; ++part) {
-              const int64_t n0 = col0 + ch * 32 + part * Cfg::TURN_COLS;
-              __syncwarp();
-#pragma unroll
-              for (int j = 0; j < Cfg::TURN_COLS; ++j)
-                turn[lane * (Cfg::TURN_COLS + 1) + j] = biased(v[part * Cfg::TURN_COLS + j], n0 + j);
-              __syncwarp();
-              const int j = lane & (Cfg::TURN_COLS - 1);
-#pragma unroll 1
-              for (int r = lane >> 4; r < 32; r += 2) {
-                const int64_t m = u.m0 + q * 32 + r;
-                if (m < c.M && n0 + j < c.N)
-                  lin_scalar<BACKWARD>(e, turn[r * (Cfg::TURN_COLS + 1) + j], m, n0 + j, row_scale[r], row_inv[r],
-                                       c.C + m * c.ldc + n0 + j);
-              }
-            }
-          }
-          __syncwarp();
-        }
-      }
-#pragma unroll 1
-      for (int ch = 0; EPI < kEpiLinear && ch < Cfg::BN / 32; ++ch) {
+      for (int ch = 0; ch < Cfg::BN / 32; ++ch) {
         uint32_t v[32];
         tmem_ld_32x32b_x32(t_row + ch * 32, v);
         tmem_ld_wait(v);
@@ -536,13 +461,6 @@ __global__ void __launch_bounds__(GenCfg::THREADS, 2)
   generic_units<false>(p, none, tiles_m * tiles_n, tiles_m, tiles_n);
 }
 
-template <int EPI>
-__global__ void __launch_bounds__(GenCfg::THREADS, 2)
-    hgemm_generic_linear_kernel(const PlainArgs p, int64_t tiles_m, int64_t tiles_n) {
-  const TriLeaves none{};
-  generic_units<false, EPI>(p, none, tiles_m * tiles_n, tiles_m, tiles_n);
-}
-
 // The diagonal blocks of a triangular product: leaf b is the product of p's
 // A operand shifted by off columns (M × s) with the lower triangle of p's B
 // operand at (off, off) (s × s), into C shifted by off columns, where
@@ -553,12 +471,12 @@ __global__ void __launch_bounds__(GenCfg::THREADS, 2)
 }
 
 template <typename Kern>
-cudaError_t prepare(Kern kern, std::atomic<bool>* done, int smem_bytes = GenCfg::SMEM_BYTES) {
+cudaError_t prepare(Kern kern, std::atomic<bool>* done) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !done[dev]) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GenCfg::SMEM_BYTES);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) done[dev] = true;
   }
@@ -588,18 +506,14 @@ cudaError_t launch_tri_leaves(const PlainArgs& args, const TriLeaves& leaves, in
 }
 
 cudaError_t launch_generic(const PlainArgs& args, int num_sms, cudaStream_t stream) {
-  static std::atomic<bool> attr_done[3][64];
-  auto kern = args.kind == kEpiLinear       ? hgemm_generic_linear_kernel<kEpiLinear>
-              : args.kind == kEpiLinearGrad ? hgemm_generic_linear_kernel<kEpiLinearGrad>
-                                            : hgemm_generic_kernel;
-  const int smem = args.kind >= kEpiLinear ? GenCfg::LIN_SMEM_BYTES : GenCfg::SMEM_BYTES;
-  cudaError_t e = prepare(kern, attr_done[args.kind >= kEpiLinear ? args.kind - kEpiLinear + 1 : 0], smem);
+  static std::atomic<bool> attr_done[64];
+  cudaError_t e = prepare(hgemm_generic_kernel, attr_done);
   if (e != cudaSuccess) return e;
   const int64_t tiles_n = (args.N + GenCfg::BN - 1) / GenCfg::BN;
   const int64_t tiles_m = (args.M + GenCfg::BM - 1) / GenCfg::BM;
-  PdlLaunch l(dim3(persistent_grid(tiles_m * tiles_n, num_sms)), dim3(GenCfg::THREADS),
-              static_cast<size_t>(smem), stream);
-  return cudaLaunchKernelEx(&l.cfg, kern, args, tiles_m, tiles_n);
+  PdlLaunch l(dim3(persistent_grid(tiles_m * tiles_n, num_sms)), dim3(GenCfg::THREADS), GenCfg::SMEM_BYTES,
+              stream);
+  return cudaLaunchKernelEx(&l.cfg, hgemm_generic_kernel, args, tiles_m, tiles_n);
 }
 
 // The -DHGEMM_DEBUG build's check word of this file (null otherwise).

@@ -1,0 +1,479 @@
+// hgemm_linear_any.cu — products with a linear layer's epilogue (forward,
+// input gradient, weight gradient) for operands and outputs that TMA cannot
+// describe: odd feature counts, pitches that are not multiples of 8, bases
+// that are not 16-byte aligned.
+//
+// The tensor-core pipeline is the usual one: a ring of 64-wide K blocks in
+// 128-byte-swizzled shared memory, tcgen05.mma into one of two FP32
+// accumulators, an epilogue that drains the other. What differs is who fills
+// the ring. An operand's tile of a K block is 128 segments of 128 bytes: rows
+// of 64 k, or (an M- or N-contiguous operand) for each of 64 k two runs of 64
+// rows, which is TMA's MN-major layout. Eight lanes read a segment, each the
+// two aligned 16-byte pieces that its 16 bytes lie in, so that a read is one
+// run of memory whatever the pitch, and shift them together. How far is the
+// same in every K block (a block is 128 bytes on, or 64 pitches), so a lane
+// keeps its pointers and its shift for a whole output tile, and a K block
+// costs a warp some 130 instructions: the loaders are bound by those.
+// Nothing outside a matrix is read: what a tile has there is zeros.
+#include <atomic>
+
+#include <cuda_fp16.h>
+
+#include "internal.h"
+#include "kernel_common.cuh"
+#include "linear_epilogue.cuh"
+#include "ptx.cuh"
+
+namespace hg {
+namespace {
+
+struct AnyCfg {
+  static constexpr int BM = 128, BN = 128, BK = 64, STAGES = 5, UMMA_K = 16;
+  static constexpr int TILE_BYTES = 128 * BK * 2;  // of either operand
+  static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
+  static constexpr int LOADERS = 16;                // warps 0 .. 15
+  static constexpr int SEGMENTS = 128 / LOADERS;    // of each operand, per loader warp
+  static constexpr int EPI_WARPS = 4;               // warps 16 .. 19: TMEM lanes 32·(w % 4)
+  static constexpr int MMA_WARP = LOADERS + EPI_WARPS;
+  static constexpr int THREADS = (MMA_WARP + 1) * 32;
+  static constexpr int TMEM_COLS = 2 * BN;
+  // the epilogue turns 32 rows × 16 columns around per warp (rows of 17
+  // words), beside the rows' scales
+  static constexpr int TURN_COLS = 16;
+  static constexpr int TURN_WORDS = 32 * (TURN_COLS + 1) + 2 * 32;
+  static constexpr int OFF_TURN = STAGES * STAGE_BYTES;
+  static constexpr int OFF_BAR = OFF_TURN + EPI_WARPS * TURN_WORDS * 4;
+  static constexpr int NUM_BARS = 2 * STAGES + 5;  // full, empty, accumulator full ×2 and empty ×2, drain
+  static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
+  static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
+  static constexpr uint32_t IDESC = idesc_f16_f32acc(BM, BN);
+  static_assert(OFF_BAR % 8 == 0, "aligned barriers");
+  static_assert(SMEM_BYTES <= 232448, "exceeds 227 KB of shared memory per CTA");
+};
+
+struct AnyArgs {
+  LinearProduct p;
+  int64_t num_m, num_n, units;
+  int num_kb;
+  int* status;
+  unsigned long long timeout_ns;
+};
+
+// One operand: element (i, k) at p[i·ld + k], or p[k·ld + i] when mn.
+struct AnyOperand {
+  const uint16_t* p;
+  const uint16_t* end;  // past its last element
+  int64_t ld, rows, K;
+  bool mn;
+  bool vec;  // 16-byte-aligned segments
+};
+
+constexpr int kAnyGroups = AnyCfg::SEGMENTS / 4;  // of four segments, eight lanes each
+
+// A loader warp's way along K: its segment j of the current block starts at
+// src + j·ld. at, shift: for each group, the aligned piece this lane reads
+// first and how many elements into it the lane's own eight begin.
+struct AnyCursor {
+  const uint16_t* src;
+  int64_t left;  // K that remains: of the segments' elements, or (mn) of the segments
+  int fixed;     // rows that are inside: segments, or (mn) elements
+  const uint16_t* at[kAnyGroups];
+  int shift[kAnyGroups];
+};
+__device__ __forceinline__ int any_clamp(int64_t v, int most) {
+  return v < 0 ? 0 : (v < most ? static_cast<int>(v) : most);
+}
+__device__ __forceinline__ AnyCursor any_start(const AnyOperand& o, int warp, int lane, int64_t i0) {
+  const int s = warp * AnyCfg::SEGMENTS;
+  const int64_t i = o.mn ? i0 + (s & 64) : i0 + s, k = o.mn ? s & 63 : 0;
+  AnyCursor c;
+  c.src = o.p + (o.mn ? k * o.ld + i : i * o.ld);
+  c.left = o.K - k;
+  c.fixed = any_clamp(o.rows - i, o.mn ? 64 : AnyCfg::SEGMENTS);
+#pragma unroll
+  for (int g = 0; g < kAnyGroups; ++g) {
+    const uint16_t* mine = c.src + (4 * g + (lane >> 3)) * o.ld + 8 * (lane & 7);
+    c.shift[g] = static_cast<int>(reinterpret_cast<uintptr_t>(mine) >> 1) & 7;
+    c.at[g] = mine - c.shift[g];
+  }
+  return c;
+}
+// The next K block: a multiple of 16 bytes on, so that the shifts stay.
+__device__ __forceinline__ void any_advance(const AnyOperand& o, AnyCursor& c) {
+  const int64_t step = o.mn ? AnyCfg::BK * o.ld : AnyCfg::BK;
+  c.src += step;
+  c.left -= AnyCfg::BK;
+#pragma unroll
+  for (int g = 0; g < kAnyGroups; ++g) c.at[g] += step;
+}
+
+// A warp's part of one operand's block, on its way to shared memory.
+struct AnyPieces {
+  uint4 lo[kAnyGroups], hi[kAnyGroups];
+  bool joined;  // lo is what goes into the tile
+};
+
+__device__ __forceinline__ void load_pieces(const AnyOperand& o, const AnyCursor& c, int lane, AnyPieces& r) {
+  using Cfg = AnyCfg;
+  const int count = o.mn ? c.fixed : any_clamp(c.left, 64);
+  const int valid = o.mn ? any_clamp(c.left, Cfg::SEGMENTS) : c.fixed;
+  r.joined = o.vec;
+  if (count == 64 && valid == Cfg::SEGMENTS &&
+      (o.vec || (c.src - 7 >= o.p && c.src + (Cfg::SEGMENTS - 1) * o.ld + 72 <= o.end))) {
+    // every piece lies inside the matrix
+#pragma unroll
+    for (int g = 0; g < kAnyGroups; ++g) r.lo[g] = __ldg(reinterpret_cast<const uint4*>(c.at[g]));
+    if (!o.vec) {
+#pragma unroll
+      for (int g = 0; g < kAnyGroups; ++g) r.hi[g] = __ldg(reinterpret_cast<const uint4*>(c.at[g]) + 1);
+    }
+    return;
+  }
+  r.joined = true;
+#pragma unroll
+  for (int g = 0; g < kAnyGroups; ++g) {
+    const uint16_t* src = c.at[g] + c.shift[g];
+    const int left = 4 * g + (lane >> 3) < valid ? count - 8 * (lane & 7) : 0;
+    uint32_t h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = i < left ? __ldg(src + i) : 0u;
+    r.lo[g] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+  }
+}
+
+__device__ __forceinline__ void store_pieces(const int (&shift)[kAnyGroups], const AnyPieces& r, uint8_t* tile,
+                                             int warp, int lane) {
+  using Cfg = AnyCfg;
+  // (a warp's first segment is a multiple of 8: segment j's swizzle is j % 8)
+  static_assert(Cfg::SEGMENTS % 8 == 0, "the swizzle of a warp's segments");
+#pragma unroll
+  for (int g = 0; g < kAnyGroups; ++g) {
+    const int j = 4 * g + (lane >> 3);
+    uint4 v = r.lo[g];
+    if (!r.joined) {
+      // words shift / 2 .. of the eight, half a word on for an odd shift
+      const uint32_t w[8] = {r.lo[g].x, r.lo[g].y, r.lo[g].z, r.lo[g].w, r.hi[g].x, r.hi[g].y, r.hi[g].z, r.hi[g].w};
+      const bool two = (shift[g] & 4) != 0, one = (shift[g] & 2) != 0;
+      uint32_t x[6], y[5];
+#pragma unroll
+      for (int i = 0; i < 6; ++i) x[i] = two ? w[i + 2] : w[i];
+#pragma unroll
+      for (int i = 0; i < 5; ++i) y[i] = one ? x[i + 1] : x[i];
+      const uint32_t bits = static_cast<uint32_t>(shift[g] & 1) << 4;
+      v = make_uint4(__funnelshift_r(y[0], y[1], bits), __funnelshift_r(y[1], y[2], bits),
+                     __funnelshift_r(y[2], y[3], bits), __funnelshift_r(y[3], y[4], bits));
+    }
+    *reinterpret_cast<uint4*>(tile + (warp * Cfg::SEGMENTS + j) * 128 + (((lane & 7) ^ (j & 7)) << 4)) = v;
+  }
+}
+
+// The first row and column of unit t.
+struct AnyUnit {
+  int64_t m0, n0;
+};
+__device__ __forceinline__ AnyUnit any_unit(const AnyArgs& a, int64_t t) {
+  int mb, nb;
+  tile_coords(static_cast<int>(t), static_cast<int>(a.num_m), static_cast<int>(a.num_n), 12, mb, nb);
+  return AnyUnit{static_cast<int64_t>(mb) * AnyCfg::BM, static_cast<int64_t>(nb) * AnyCfg::BN};
+}
+
+// The epilogue of 32 rows from m0 and 16 columns, turned around in shared
+// memory: this lane's column n, rows m0 + (lane / 16) + 2i.
+template <bool BACKWARD>
+__device__ __noinline__ void any_columns(const LinearProduct& p, const float* turn, const float* row_scale,
+                                         const float* row_inv, int64_t m0, int64_t n, float bias, int lane) {
+  constexpr int PITCH = AnyCfg::TURN_COLS + 1;
+  const LinEpi& e = p.epi;
+  const int r0 = lane >> 4, j = lane & 15;
+  const int rows = n < p.N ? (p.M - m0 < 32 ? static_cast<int>(p.M - m0) : 32) : 0;  // below this a row is inside
+  uint16_t side[16];  // residual, or codes
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int r = r0 + 2 * i;
+    side[i] = 0;
+    if (r >= rows) continue;
+    if (BACKWARD && e.codes)
+      side[i] = static_cast<uint16_t>(static_cast<uint8_t>(e.codes[(m0 + r) * e.ldq + n]));
+    else if (!BACKWARD && e.res)
+      side[i] = e.res[(m0 + r) * e.ldr + n];
+  }
+  const bool act = !BACKWARD || e.codes;
+  with_activation(act ? e.act : HGEMM_ACT_NONE, [&](auto a) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      const int ra = r0 + 2 * i, rb = ra + 2;
+      const float x0 = turn[ra * PITCH + j], x1 = turn[rb * PITCH + j];
+      f32x2 y, f = 0;
+      if constexpr (BACKWARD) {
+        y = pair_of(x0, x1);
+        if (e.codes) {
+          f32x2 df;
+          activate<decltype(a)::value, true>(
+              pair_of(static_cast<float>(static_cast<int8_t>(side[i])) * row_scale[ra],
+                      static_cast<float>(static_cast<int8_t>(side[i + 1])) * row_scale[rb]), f, df);
+          y = mul2(y, df);
+        }
+      } else {
+        const f32x2 u = add2(pair_of(x0, x1), pair_of(bias));
+        if (e.codes) {
+          float ua, ub;
+          unpair(u, ua, ub);
+          const float ia = row_inv[ra], ib = row_inv[rb];
+          if (ra < rows) e.codes[(m0 + ra) * e.ldq + n] = static_cast<int8_t>(ia == 0.f ? 0u : ckpt_code(ua, ia));
+          if (rb < rows) e.codes[(m0 + rb) * e.ldq + n] = static_cast<int8_t>(ib == 0.f ? 0u : ckpt_code(ub, ib));
+        }
+        f32x2 df;
+        activate<decltype(a)::value, false>(u, y, df);
+        y = add2(y, pair_of(__half2float(__ushort_as_half(side[i])), __half2float(__ushort_as_half(side[i + 1]))));
+      }
+      const uint32_t packed = pack_half2(y);
+      if (ra < rows) p.C[(m0 + ra) * p.ldc + n] = static_cast<uint16_t>(packed);
+      if (rb < rows) p.C[(m0 + rb) * p.ldc + n] = static_cast<uint16_t>(packed >> 16);
+      if (BACKWARD && e.h) {
+        const uint32_t hid = pack_half2(f);
+        if (ra < rows) e.h[(m0 + ra) * e.ldh + n] = static_cast<uint16_t>(hid);
+        if (rb < rows) e.h[(m0 + rb) * e.ldh + n] = static_cast<uint16_t>(hid >> 16);
+      }
+    }
+  });
+}
+
+template <bool BACKWARD>
+__global__ void __launch_bounds__(AnyCfg::THREADS, 1) linear_any_kernel(const AnyArgs a) {
+  using Cfg = AnyCfg;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + Cfg::OFF_BAR;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::OFF_MISC + 4);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (Cfg::STAGES + s); };
+  auto accf_bar = [&](int b) { return bar0 + 8u * (2 * Cfg::STAGES + b); };
+  auto acce_bar = [&](int b) { return bar0 + 8u * (2 * Cfg::STAGES + 2 + b); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * Cfg::STAGES + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Watchdog wd{abort_flag, a.status, a.timeout_ns};
+  const LinearProduct& p = a.p;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < Cfg::STAGES; ++s) {
+      mbar_init(full_bar(s), Cfg::LOADERS);  // one arrival per loader warp
+      mbar_init(empty_bar(s), 1);            // tcgen05.commit
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(accf_bar(b), 1);               // tcgen05.commit
+      mbar_init(acce_bar(b), Cfg::EPI_WARPS);  // one arrival per epilogue warp
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == Cfg::MMA_WARP) {
+    tmem_alloc(smem_u32(tmem_slot), Cfg::TMEM_COLS);
+    tmem_relinquish_alloc_permit();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  if (warp < Cfg::LOADERS) {
+    // ------------------------------------------------------------ loaders
+    auto vec = [](const uint16_t* q, int64_t ld) {
+      return (reinterpret_cast<uintptr_t>(q) & 15u) == 0 && ld % 8 == 0;
+    };
+    auto operand = [&](const uint16_t* q, int64_t ld, int64_t rows, bool mn) {
+      const uint16_t* end = q + (mn ? (p.K - 1) * ld + rows : (rows - 1) * ld + p.K);
+      return AnyOperand{q, end, ld, rows, p.K, mn, vec(q, ld)};
+    };
+    const AnyOperand oa = operand(p.A, p.lda, p.M, p.a_mn), ob = operand(p.B, p.ldb, p.N, p.b_mn);
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    AnyPieces pa, pb;
+    for (int64_t t = blockIdx.x; ok && t < a.units; t += gridDim.x) {
+      const AnyUnit u = any_unit(a, t);
+      AnyCursor ca = any_start(oa, warp, lane, u.m0), cb = any_start(ob, warp, lane, u.n0);
+      load_pieces(oa, ca, lane, pa);
+      load_pieces(ob, cb, lane, pb);
+      for (int kb = 0; kb < a.num_kb; ++kb) {
+        int good = 1;
+        if (lane == 0) good = wait_phase(empty_bar(stage), phase ^ 1u, wd, kWdProducerEmpty) ? 1 : 0;
+        ok = __shfl_sync(0xffffffffu, good, 0) != 0;
+        if (!ok) break;
+        uint8_t* tile = smem + stage * Cfg::STAGE_BYTES;
+        store_pieces(ca.shift, pa, tile, warp, lane);
+        store_pieces(cb.shift, pb, tile + Cfg::TILE_BYTES, warp, lane);
+        // the next block's reads start before this one is handed over
+        if (kb + 1 < a.num_kb) {
+          any_advance(oa, ca);
+          any_advance(ob, cb);
+          load_pieces(oa, ca, lane, pa);
+          load_pieces(ob, cb, lane, pb);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full_bar(stage));
+        if (++stage == Cfg::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+  } else if (warp == Cfg::MMA_WARP) {
+    // -------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      const uint32_t idesc = Cfg::IDESC | idesc_major_bits(p.a_mn, p.b_mn);
+      const uint32_t a_step = p.a_mn ? 128u : 2u, b_step = p.b_mn ? 128u : 2u;
+      int stage = 0;
+      uint32_t phase = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      bool ok = true;
+      for (int64_t t = blockIdx.x; ok && t < a.units; t += gridDim.x) {
+        if (!wait_phase(acce_bar(acc), acc_phase ^ 1u, wd, kWdMmaAccEmpty)) break;
+        tc_fence_after_sync();
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * Cfg::BN);
+        for (int kb = 0; kb < a.num_kb; ++kb) {
+          if (!wait_phase(full_bar(stage), phase, wd, kWdMmaFull)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t sa = sbase + stage * Cfg::STAGE_BYTES, sb = sa + Cfg::TILE_BYTES;
+          const uint64_t a_desc = p.a_mn ? sdesc_mnmajor_sw128(sa) : sdesc_kmajor_sw128(sa);
+          const uint64_t b_desc = p.b_mn ? sdesc_mnmajor_sw128(sb) : sdesc_kmajor_sw128(sb);
+#pragma unroll
+          for (int k = 0; k < Cfg::BK / Cfg::UMMA_K; ++k)
+            mma_f16_ss(d_tmem, a_desc + a_step * k, b_desc + b_step * k, idesc, (kb > 0 || k > 0) ? 1u : 0u);
+          mma_commit(empty_bar(stage));
+          if (++stage == Cfg::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        mma_commit(accf_bar(acc));
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      mma_commit(drain_bar);
+      wait_drain(drain_bar, 0, wd);
+    }
+    __syncwarp();
+  } else {
+    // ----------------------------------------------------------- epilogue
+    // A lane holds a row of the accumulator, but unaligned rows are best read
+    // and written along the columns: 16 columns at a time go through shared
+    // memory, so that a lane has 16 rows of one column, and a warp's accesses
+    // are two runs of 16 neighbours. All 16 reads are under way at once.
+    const LinEpi& e = p.epi;
+    const int q = warp & 3;
+    float* turn = reinterpret_cast<float*>(smem + Cfg::OFF_TURN) + (warp - Cfg::LOADERS) * Cfg::TURN_WORDS;
+    float* row_scale = turn + 32 * (Cfg::TURN_COLS + 1);
+    float* row_inv = row_scale + 32;
+    auto bias_at = [&](int64_t n) {
+      return !BACKWARD && e.bias && n < p.N ? __half2float(__ushort_as_half(__ldg(e.bias + n))) : 0.f;
+    };
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int64_t t = blockIdx.x; t < a.units; t += gridDim.x) {
+      const AnyUnit u = any_unit(a, t);
+      lin_prefetch_row<BACKWARD ? kEpiLinearGrad : kEpiLinear>(e, p.M, p.N, u.m0 + q * 32 + lane, u.n0, Cfg::BN);
+      int ok = 1;
+      if (lane == 0) ok = wait_phase(accf_bar(acc), acc_phase, wd, kWdEpiAccFull) ? 1 : 0;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      tc_fence_after_sync();
+      const int64_t gi = u.m0 + q * 32 + lane;
+      for (int64_t col0 = u.n0; col0 < u.n0 + Cfg::BN && col0 < p.N; col0 += kCkptGroup) {
+        const uint32_t t_group = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                                 static_cast<uint32_t>(acc * Cfg::BN + static_cast<int>(col0 - u.n0));
+        float scale = 0.f, inv = 0.f;
+        if (e.codes) {
+          float* s = e.scales + col0 / kCkptGroup * e.lds + gi;
+          if constexpr (BACKWARD) {
+            if (gi < p.M) scale = *s;
+          } else {
+            // (columns past N hold 0: zeros in the tile and no bias)
+            float top = 0.f;
+#pragma unroll 1
+            for (int c = 0; c < kCkptGroup; c += Cfg::TURN_COLS) {
+              float v[16];
+              tmem_ld_32x32b_x16(t_group + c, v);
+#pragma unroll
+              for (int j = 0; j < 16; j += 2)
+                top = max_abs3(top, v[j] + bias_at(col0 + c + j), v[j + 1] + bias_at(col0 + c + j + 1));
+            }
+            ckpt_scale(magnitude_bits(top), scale, inv);
+            if (gi < p.M) *s = scale;
+          }
+        }
+        row_scale[lane] = scale;
+        row_inv[lane] = inv;
+#pragma unroll 1
+        for (int c = 0; c < kCkptGroup; c += Cfg::TURN_COLS) {
+          float v[16];
+          tmem_ld_32x32b_x16(t_group + c, v);
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < Cfg::TURN_COLS; ++j) turn[lane * (Cfg::TURN_COLS + 1) + j] = v[j];
+          __syncwarp();
+          const int64_t n = col0 + c + (lane & (Cfg::TURN_COLS - 1));
+          const float bias = bias_at(n);
+          any_columns<BACKWARD>(p, turn, row_scale, row_inv, u.m0 + q * 32, n, bias, lane);
+        }
+        __syncwarp();
+      }
+      // this accumulator may be overwritten by the unit after next
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acce_bar(acc));
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == Cfg::MMA_WARP) tmem_dealloc(tmem_base, Cfg::TMEM_COLS);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_any(const LinearProduct& p, const CallDevice& dev, cudaStream_t stream) {
+  using Cfg = AnyCfg;
+  static std::atomic<bool> attr_done[2][64];
+  const int back = p.epi.backward ? 1 : 0;
+  auto kern = back ? linear_any_kernel<true> : linear_any_kernel<false>;
+  int id = 0;
+  cudaError_t e = cudaGetDevice(&id);
+  if (e != cudaSuccess) return e;
+  if (id < 0 || id >= 64 || !attr_done[back][id]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    if (id >= 0 && id < 64) attr_done[back][id] = true;
+  }
+  AnyArgs a{};
+  a.p = p;
+  a.num_m = (p.M + Cfg::BM - 1) / Cfg::BM;
+  a.num_n = (p.N + Cfg::BN - 1) / Cfg::BN;
+  a.units = a.num_m * a.num_n;
+  if (a.units > 0x7FFFFFFF - 0xFFFF) return cudaErrorInvalidValue;
+  a.num_kb = static_cast<int>((p.K + Cfg::BK - 1) / Cfg::BK);
+  a.status = dev.status;
+  a.timeout_ns = dev.timeout_ns;
+  PdlLaunch l(dim3(static_cast<unsigned>(a.units < dev.num_sms ? a.units : dev.num_sms)), dim3(Cfg::THREADS),
+              Cfg::SMEM_BYTES, stream);
+  return cudaLaunchKernelEx(&l.cfg, kern, a);
+}
+
+// The -DHGEMM_DEBUG build's check word of this file (null otherwise).
+HG_DEBUG_WORD_ACCESSOR(linear_any)
+
+}  // namespace hg

@@ -91,8 +91,6 @@ struct PlainArgs {
   unsigned long long timeout_ns;
   EpiArgs epi;
   int a_mn = 0, b_mn = 0;    // A(i,k) at A[k*lda + i]; B(k,j) at B[k*ldb + j]
-  Epilogue kind = kEpiFused;  // kEpiFused (any EpiArgs mode), or one of the linear ones
-  LinEpi lin = {};
 };
 
 // The diagonal blocks ("leaves") of a triangular product, for one batched
@@ -215,11 +213,22 @@ cudaError_t launch_column_sums(const uint16_t* dy, int64_t ld, int64_t M, int64_
 cudaError_t launch_linear_empty(uint16_t* C, int64_t ldc, int64_t M, int64_t N, const LinEpi& epi,
                                 cudaStream_t stream);
 
-// One product with a linear layer's epilogue, C (M×N) = epilogue(A·B) with B
-// N×K, or K×N when b_mn.
+// What an entry point outside hgemm_api.cu needs of a call: the current
+// device checked (HGEMM_OK or an error status), and a CUDA error as a status.
+struct CallDevice {
+  int num_sms;
+  int* status;
+  unsigned long long timeout_ns;
+};
+int call_device(CallDevice* out);
+int cuda_status(cudaError_t e);
+
+// One product with a linear layer's epilogue, C (M×N) = epilogue(A·B) with A
+// M×K, or K×M when a_mn, and B N×K, or K×N when b_mn.
 struct LinearProduct {
   const uint16_t* A;
   int64_t lda;
+  bool a_mn;
   const uint16_t* B;
   int64_t ldb;
   bool b_mn;
@@ -232,6 +241,10 @@ int run_linear(const LinearProduct& p, cudaStream_t stream);
 constexpr int kLinearRows = 32;
 bool linear_rows_suits(const LinearProduct& p);
 cudaError_t launch_linear_rows(const LinearProduct& p, int num_sms, cudaStream_t stream);
+// The kernel for operands and outputs of any pitch and alignment; K > 0.
+cudaError_t launch_linear_any(const LinearProduct& p, const CallDevice& dev, cudaStream_t stream);
+// The gradient of a weight: C = A·B, or C + A·B, with an epilogue that says so.
+int run_wgrad(const LinearProduct& p, cudaStream_t stream);
 
 struct NormArgs {
   const uint16_t* x;
@@ -263,15 +276,6 @@ cudaError_t launch_ckpt8_save(const uint16_t* x, int64_t ldx, int8_t* codes, int
 cudaError_t launch_ckpt8_load(const int8_t* codes, int64_t ldq, const float* scales, int64_t lds, int act,
                               uint16_t* y, int64_t ldy, int64_t M, int64_t N, cudaStream_t stream);
 
-// What an entry point outside hgemm_api.cu needs of a call: the current
-// device checked (HGEMM_OK or an error status), and a CUDA error as a status.
-struct CallDevice {
-  int num_sms;
-  int* status;
-  unsigned long long timeout_ns;
-};
-int call_device(CallDevice* out);
-int cuda_status(cudaError_t e);
 
 // Address of the device watchdog word on the current device.
 cudaError_t status_word_address(int** addr);
@@ -289,7 +293,8 @@ cudaError_t debug_word_chain(int** out);
 cudaError_t debug_word_linear(int** out);
 cudaError_t debug_word_norm(int** out);
 cudaError_t debug_word_ckpt8(int** out);
-constexpr int kDebugWords = 11;
+cudaError_t debug_word_linear_any(int** out);
+constexpr int kDebugWords = 12;
 
 // Co-residency limits of the cluster kernels on one device, measured once
 // (or nominal GB300 figures when no device has been queried).
