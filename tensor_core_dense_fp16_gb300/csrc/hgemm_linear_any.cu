@@ -41,8 +41,11 @@ struct AnyCfg {
   // words), beside the rows' scales
   static constexpr int TURN_COLS = 16;
   static constexpr int TURN_WORDS = 32 * (TURN_COLS + 1) + 2 * 32;
+  // ... or, where the outputs are aligned, stages 32 rows × 64 columns
+  static constexpr int BOX_BYTES = 32 * 128;
+  static_assert(BOX_BYTES >= TURN_WORDS * 4, "either fits");
   static constexpr int OFF_TURN = STAGES * STAGE_BYTES;
-  static constexpr int OFF_BAR = OFF_TURN + EPI_WARPS * TURN_WORDS * 4;
+  static constexpr int OFF_BAR = OFF_TURN + EPI_WARPS * BOX_BYTES;
   static constexpr int NUM_BARS = 2 * STAGES + 5;  // full, empty, accumulator full ×2 and empty ×2, drain
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
@@ -55,6 +58,7 @@ struct AnyArgs {
   LinearProduct p;
   int64_t num_m, num_n, units;
   int num_kb;
+  int wide;  // the epilogue can read and write eight columns at a time
   int* status;
   unsigned long long timeout_ns;
 };
@@ -184,55 +188,67 @@ __device__ __noinline__ void any_columns(const LinearProduct& p, const float* tu
                                          const float* row_inv, int64_t m0, int64_t n, float bias, int lane) {
   constexpr int PITCH = AnyCfg::TURN_COLS + 1;
   const LinEpi& e = p.epi;
-  const int r0 = lane >> 4, j = lane & 15;
-  const int rows = n < p.N ? (p.M - m0 < 32 ? static_cast<int>(p.M - m0) : 32) : 0;  // below this a row is inside
-  uint16_t side[16];  // residual, or codes
+  const int r0 = lane >> 4;
+  const int64_t m = m0 + r0;
+  // rows of this lane that are inside: i < count
+  const int count = n < p.N ? any_clamp((p.M - m + 1) / 2, 16) : 0;
+  turn += r0 * PITCH + (lane & 15);
+  row_scale += r0;
+  row_inv += r0;
+  uint32_t side[16];  // residual, or codes
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int r = r0 + 2 * i;
-    side[i] = 0;
-    if (r >= rows) continue;
-    if (BACKWARD && e.codes)
-      side[i] = static_cast<uint16_t>(static_cast<uint8_t>(e.codes[(m0 + r) * e.ldq + n]));
-    else if (!BACKWARD && e.res)
-      side[i] = e.res[(m0 + r) * e.ldr + n];
+  for (int i = 0; i < 16; ++i) side[i] = 0u;
+  if (BACKWARD && e.codes) {
+    const int8_t* q = e.codes + m * e.ldq + n;
+#pragma unroll
+    for (int i = 0; i < 16; ++i, q += 2 * e.ldq)
+      if (i < count) side[i] = static_cast<uint8_t>(*q);
+  } else if (!BACKWARD && e.res) {
+    const uint16_t* r = e.res + m * e.ldr + n;
+#pragma unroll
+    for (int i = 0; i < 16; ++i, r += 2 * e.ldr)
+      if (i < count) side[i] = *r;
   }
-  const bool act = !BACKWARD || e.codes;
-  with_activation(act ? e.act : HGEMM_ACT_NONE, [&](auto a) {
+  uint16_t* c = p.C + m * p.ldc + n;
+  int8_t* q = e.codes + m * e.ldq + n;
+  uint16_t* h = e.h + m * e.ldh + n;
+  with_activation(!BACKWARD || e.codes ? e.act : HGEMM_ACT_NONE, [&](auto a) {
 #pragma unroll
     for (int i = 0; i < 16; i += 2) {
-      const int ra = r0 + 2 * i, rb = ra + 2;
-      const float x0 = turn[ra * PITCH + j], x1 = turn[rb * PITCH + j];
+      const f32x2 x = pair_of(turn[2 * i * PITCH], turn[(2 * i + 2) * PITCH]);
       f32x2 y, f = 0;
       if constexpr (BACKWARD) {
-        y = pair_of(x0, x1);
+        y = x;
         if (e.codes) {
           f32x2 df;
           activate<decltype(a)::value, true>(
-              pair_of(static_cast<float>(static_cast<int8_t>(side[i])) * row_scale[ra],
-                      static_cast<float>(static_cast<int8_t>(side[i + 1])) * row_scale[rb]), f, df);
+              pair_of(static_cast<float>(static_cast<int8_t>(side[i])) * row_scale[2 * i],
+                      static_cast<float>(static_cast<int8_t>(side[i + 1])) * row_scale[2 * i + 2]), f, df);
           y = mul2(y, df);
         }
       } else {
-        const f32x2 u = add2(pair_of(x0, x1), pair_of(bias));
+        const f32x2 u = add2(x, pair_of(bias));
         if (e.codes) {
           float ua, ub;
           unpair(u, ua, ub);
-          const float ia = row_inv[ra], ib = row_inv[rb];
-          if (ra < rows) e.codes[(m0 + ra) * e.ldq + n] = static_cast<int8_t>(ia == 0.f ? 0u : ckpt_code(ua, ia));
-          if (rb < rows) e.codes[(m0 + rb) * e.ldq + n] = static_cast<int8_t>(ib == 0.f ? 0u : ckpt_code(ub, ib));
+          const float ia = row_inv[2 * i], ib = row_inv[2 * i + 2];
+          if (i < count) q[0] = static_cast<int8_t>(ia == 0.f ? 0u : ckpt_code(ua, ia));
+          if (i + 1 < count) q[2 * e.ldq] = static_cast<int8_t>(ib == 0.f ? 0u : ckpt_code(ub, ib));
+          q += 4 * e.ldq;
         }
         f32x2 df;
         activate<decltype(a)::value, false>(u, y, df);
-        y = add2(y, pair_of(__half2float(__ushort_as_half(side[i])), __half2float(__ushort_as_half(side[i + 1]))));
+        y = add2(y, unpack_half2(side[i] | side[i + 1] << 16));
       }
       const uint32_t packed = pack_half2(y);
-      if (ra < rows) p.C[(m0 + ra) * p.ldc + n] = static_cast<uint16_t>(packed);
-      if (rb < rows) p.C[(m0 + rb) * p.ldc + n] = static_cast<uint16_t>(packed >> 16);
+      if (i < count) c[0] = static_cast<uint16_t>(packed);
+      if (i + 1 < count) c[2 * p.ldc] = static_cast<uint16_t>(packed >> 16);
+      c += 4 * p.ldc;
       if (BACKWARD && e.h) {
         const uint32_t hid = pack_half2(f);
-        if (ra < rows) e.h[(m0 + ra) * e.ldh + n] = static_cast<uint16_t>(hid);
-        if (rb < rows) e.h[(m0 + rb) * e.ldh + n] = static_cast<uint16_t>(hid >> 16);
+        if (i < count) h[0] = static_cast<uint16_t>(hid);
+        if (i + 1 < count) h[2 * e.ldh] = static_cast<uint16_t>(hid >> 16);
+        h += 4 * e.ldh;
       }
     }
   });
@@ -373,7 +389,8 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1) linear_any_kernel(const An
     // are two runs of 16 neighbours. All 16 reads are under way at once.
     const LinEpi& e = p.epi;
     const int q = warp & 3;
-    float* turn = reinterpret_cast<float*>(smem + Cfg::OFF_TURN) + (warp - Cfg::LOADERS) * Cfg::TURN_WORDS;
+    uint8_t* box = smem + Cfg::OFF_TURN + (warp - Cfg::LOADERS) * Cfg::BOX_BYTES;
+    float* turn = reinterpret_cast<float*>(box);
     float* row_scale = turn + 32 * (Cfg::TURN_COLS + 1);
     float* row_inv = row_scale + 32;
     auto bias_at = [&](int64_t n) {
@@ -393,6 +410,24 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1) linear_any_kernel(const An
       for (int64_t col0 = u.n0; col0 < u.n0 + Cfg::BN && col0 < p.N; col0 += kCkptGroup) {
         const uint32_t t_group = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                  static_cast<uint32_t>(acc * Cfg::BN + static_cast<int>(col0 - u.n0));
+        if (a.wide) {
+          // aligned rows: the tensor-map kernels' epilogue, eight lanes
+          // writing a row of the box
+          f32x2 v[32];
+          tmem_row64(t_group, v);
+          __syncwarp();
+          lin_row64<BACKWARD ? kEpiLinearGrad : kEpiLinear>(box + lane * 128, lane, v, e, p.M, p.N, gi, col0);
+          __syncwarp();
+          const int64_t n = col0 + 8 * (lane & 7);
+#pragma unroll
+          for (int r = lane >> 3; r < 32; r += 4) {
+            const int64_t m = u.m0 + q * 32 + r;
+            if (m < p.M && n < p.N)
+              *reinterpret_cast<uint4*>(p.C + m * p.ldc + n) =
+                  *reinterpret_cast<const uint4*>(box + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+          }
+          continue;
+        }
         float scale = 0.f, inv = 0.f;
         if (e.codes) {
           float* s = e.scales + col0 / kCkptGroup * e.lds + gi;
@@ -466,6 +501,11 @@ cudaError_t launch_linear_any(const LinearProduct& p, const CallDevice& dev, cud
   a.units = a.num_m * a.num_n;
   if (a.units > 0x7FFFFFFF - 0xFFFF) return cudaErrorInvalidValue;
   a.num_kb = static_cast<int>((p.K + Cfg::BK - 1) / Cfg::BK);
+  auto rows = [](const void* q, int64_t ld, uintptr_t bytes) {
+    return !q || ((reinterpret_cast<uintptr_t>(q) & (bytes - 1)) == 0 && ld % 8 == 0);
+  };
+  a.wide = p.N % 8 == 0 && rows(p.C, p.ldc, 16) && rows(p.epi.res, p.epi.ldr, 16) && rows(p.epi.h, p.epi.ldh, 16) &&
+           rows(p.epi.codes, p.epi.ldq, 8);
   a.status = dev.status;
   a.timeout_ns = dev.timeout_ns;
   PdlLaunch l(dim3(static_cast<unsigned>(a.units < dev.num_sms ? a.units : dev.num_sms)), dim3(Cfg::THREADS),
