@@ -74,7 +74,8 @@ cudaError_t debug_words(int* (&out)[hg::kDebugWords]) {
                                                       hg::debug_word_generic, hg::debug_word_trsm,
                                                       hg::debug_word_trileaf, hg::debug_word_chain,
                                                       hg::debug_word_linear,  hg::debug_word_norm,
-                                                      hg::debug_word_ckpt8,   hg::debug_word_linear_any};
+                                                      hg::debug_word_ckpt8,   hg::debug_word_linear_any,
+                                                      hg::debug_word_linear_small};
   for (int i = 0; i < hg::kDebugWords; ++i) {
     const cudaError_t e = get[i](&out[i]);
     if (e != cudaSuccess) return e;
@@ -732,12 +733,60 @@ int trmm_pipe(int dev, TrmmPipe** out) {
 
 namespace hg {
 
+// Whether the turned-around product for few rows computes p, and is the
+// faster one. Measured (us, weights from memory): against the kernel of
+// matrix fragments, 16 rows, 4096×4096 9.6 to 11.3, 8192×8192 24.3 to 32.6,
+// but 1024×1024 4.3 to 3.6 (so: from 2^21 weights on); against the 128×64
+// tiles, 128 rows, 2048×8192 13.8 to 19.4 and 8192×4096 19.5 to 22.9, but
+// 8192×2048 13.5 to 12.2 and 512×512 8.5 to 5.9 (so: not for more than 64
+// rows where one wave of those tiles covers the output and K is short).
+bool linear_small_suits(const LinearProduct& p, int num_sms) {
+  auto rows = [](const void* q, int64_t ld) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0 && ld % 8 == 0; };
+  if (p.M > kLinearSmall || p.K == 0 || p.a_mn || p.b_mn || p.epi.backward || p.epi.codes || !rows(p.A, p.lda) ||
+      !rows(p.B, p.ldb))
+    return false;
+  if (p.M <= kLinearFragmentRows) return false;
+  if (p.M <= kLinearRows) return p.N * p.K >= int64_t(1) << 21;
+  return p.M <= 64 || p.K > 2048 || p.N > int64_t(kNarrowBN) * num_sms;
+}
+
+int run_linear_small(const LinearProduct& p, const DeviceState& dev, cudaStream_t stream) {
+  CUtensorMap mw, mx;
+  int rc;
+  if ((rc = encode_map(&mw, p.B, p.N, p.K, p.ldb, kTcBM, kTcBK)) != HGEMM_OK) return rc;
+  if ((rc = encode_map(&mx, p.A, p.M, p.K, p.lda, linear_small_rows(p.M), kTcBK)) != HGEMM_OK) return rc;
+  SmallArgs a{};
+  a.Y = p.C;
+  a.ldy = p.ldc;
+  a.M = static_cast<int>(p.M);
+  a.N = static_cast<int>(p.N);
+  a.num_kb = static_cast<int>((p.K + kTcBK - 1) / kTcBK);
+  // The most CTAs per 128 features with which all clusters run at once, four
+  // K blocks or more each: an SM takes in weights at ~112 GB/s, so the more
+  // SMs share them the better, but a second wave costs a whole pass
+  // (2048×8192: clusters of 8, 15 at a time for 16 tiles, 15.1 us; of 4, 10.1).
+  const int64_t tiles = (p.N + kTcBM - 1) / kTcBM;
+  if (tiles * 8 > 0x7FFFFFFF) return HGEMM_ERR_INVALID_ARG;
+  a.split = 1;
+  for (int s = 8; s > 1; --s)
+    if (a.num_kb >= 4 * s && tiles <= linear_small_clusters(s, dev.num_sms)) {
+      a.split = s;
+      break;
+    }
+  a.status = t_ctx.status;
+  a.timeout_ns = g_timeout_ns.load(std::memory_order_relaxed);
+  a.inject = g_inject.load(std::memory_order_relaxed);
+  a.epi = p.epi;
+  return cuda_status(launch_linear_small(mw, mx, a, stream));
+}
+
 int run_linear(const LinearProduct& p, cudaStream_t stream) {
   DeviceState* dev = nullptr;
   const int rc = current_device(&dev);
   if (rc != HGEMM_OK) return rc;
   const int forced = g_forced_path.load(std::memory_order_relaxed);
-  if (forced < 0 && linear_rows_suits(p)) return cuda_status(launch_linear_rows(p, dev->num_sms, stream));
+  if (forced < 0 && linear_small_suits(p, dev->num_sms)) return run_linear_small(p, *dev, stream);
+  if (forced < 0 && linear_rows_suits(p)) return cuda_status(launch_linear_rows(p, stream));
   Gemm g{p.A, p.B, p.C, p.M, p.N, p.K, p.lda, p.ldb, p.ldc};
   g.a_mn = p.a_mn;
   g.b_mn = p.b_mn;

@@ -86,7 +86,7 @@ struct RowsArgs {
 constexpr int kRowsFeatures = 16;
 template <int MT, int WARPS, bool VEC>
 __global__ void __launch_bounds__(WARPS * 32) linear_rows_kernel(const RowsArgs p) {
-  constexpr int AHEAD = 4;  // pieces in flight per warp: 64 bytes of each feature per lane pair
+  constexpr int AHEAD = MT == 1 ? 4 : 2;  // pieces in flight per warp, 64 bytes of each feature
   constexpr int PITCH = kRowsFeatures + 1;
   __shared__ float part[WARPS][8 * MT][PITCH];
   grid_dependency_wait();
@@ -95,8 +95,8 @@ __global__ void __launch_bounds__(WARPS * 32) linear_rows_kernel(const RowsArgs 
   const int g = lane >> 2, t = lane & 3;
   const int n0 = static_cast<int>(blockIdx.x) * kRowsFeatures;
   // features past N are computed as copies of the last one and not stored
-  const uint16_t* w0 = p.W + min(n0 + g, p.N - 1) * p.ldw;
-  const uint16_t* w1 = p.W + min(n0 + g + 8, p.N - 1) * p.ldw;
+  const uint16_t* w0 = p.W + static_cast<int64_t>(min(n0 + g, p.N - 1)) * p.ldw;
+  const uint16_t* w1 = p.W + static_cast<int64_t>(min(n0 + g + 8, p.N - 1)) * p.ldw;
   auto load = [&](const uint16_t* row, int k, bool weights) {
     if constexpr (VEC) {
       if (k >= p.K) return make_uint4(0u, 0u, 0u, 0u);
@@ -113,23 +113,31 @@ __global__ void __launch_bounds__(WARPS * 32) linear_rows_kernel(const RowsArgs 
     }
   };
   float acc[MT][4] = {};
-  for (int k0 = warp * 32 + 8 * t; k0 - 8 * t < p.K; k0 += AHEAD * WARPS * 32) {
-    uint4 a0[AHEAD], a1[AHEAD];
+  // AHEAD pieces in turn: as soon as one has been multiplied, its registers
+  // take the piece AHEAD further on
+  uint4 a0[AHEAD], a1[AHEAD], b[AHEAD][MT];
+  auto fetch = [&](int u, int k) {
+    a0[u] = load(w0, k, true);
+    a1[u] = load(w1, k, true);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const int m = 8 * i + g;
+      b[u][i] = m < p.M ? load(p.X + m * p.ldx, k, false) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  int k0 = warp * 32 + 8 * t;
+#pragma unroll
+  for (int u = 0; u < AHEAD; ++u) fetch(u, k0 + u * WARPS * 32);
+  for (; k0 - 8 * t < p.K; k0 += AHEAD * WARPS * 32) {
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) {
-      a0[u] = load(w0, k0 + u * WARPS * 32, true);
-      a1[u] = load(w1, k0 + u * WARPS * 32, true);
-    }
-#pragma unroll
-    for (int u = 0; u < AHEAD; ++u)
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        const int m = 8 * i + g;
-        uint4 b = make_uint4(0u, 0u, 0u, 0u);
-        if (m < p.M) b = load(p.X + m * p.ldx, k0 + u * WARPS * 32, false);
-        mma_16816(acc[i], a0[u].x, a1[u].x, a0[u].y, a1[u].y, b.x, b.y);
-        mma_16816(acc[i], a0[u].z, a1[u].z, a0[u].w, a1[u].w, b.z, b.w);
+        mma_16816(acc[i], a0[u].x, a1[u].x, a0[u].y, a1[u].y, b[u][i].x, b[u][i].y);
+        mma_16816(acc[i], a0[u].z, a1[u].z, a0[u].w, a1[u].w, b[u][i].z, b[u][i].w);
       }
+      fetch(u, k0 + (AHEAD + u) * WARPS * 32);
+    }
   }
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
@@ -158,11 +166,16 @@ cudaError_t rows_with(const RowsArgs& p, bool vec, cudaStream_t stream) {
 }
 
 template <int MT>
-cudaError_t rows_tiles(const RowsArgs& p, bool vec, int num_sms, cudaStream_t stream) {
-  // 16 warps where there are few blocks, so that each SM still has enough
-  // loads in flight
+cudaError_t rows_tiles(const RowsArgs& p, bool vec, cudaStream_t stream) {
+  // About 2048 warps in all, 13 per SM: enough loads under way, and all
+  // blocks resident at once; four pieces or more per warp. One row, us with 4,
+  // 8 and 16 warps: 8192×2048 8.0, 9.1, 11.0; 4096×4096 10.8, 8.1, 9.2;
+  // 2048×8192 18.6, 11.1, 8.3; 1024×1024 3.3, 2.3, 2.4.
   const int64_t blocks = (p.N + kRowsFeatures - 1) / kRowsFeatures;
-  return blocks <= 2 * num_sms ? rows_with<MT, 16>(p, vec, stream) : rows_with<MT, 8>(p, vec, stream);
+  const int pieces = (p.K + 31) / 32;
+  if (blocks >= 384 || pieces < 32) return rows_with<MT, 4>(p, vec, stream);
+  if (blocks >= 192 || pieces < 64) return rows_with<MT, 8>(p, vec, stream);
+  return rows_with<MT, 16>(p, vec, stream);
 }
 
 // Column sums, in a fixed order. A cluster of CTAs takes a strip of columns,
@@ -231,20 +244,20 @@ bool linear_rows_suits(const LinearProduct& p) {
   return p.M <= kLinearRows && p.K > 0 && !p.b_mn && !p.epi.backward && !p.epi.codes;
 }
 
-cudaError_t launch_linear_rows(const LinearProduct& q, int num_sms, cudaStream_t stream) {
+cudaError_t launch_linear_rows(const LinearProduct& q, cudaStream_t stream) {
   const RowsArgs p{q.A, q.lda, q.B, q.ldb, q.C, q.ldc, static_cast<int>(q.M), static_cast<int>(q.N),
                    static_cast<int>(q.K), q.epi};
   auto rows16 = [](const void* b, int64_t ld) { return (reinterpret_cast<uintptr_t>(b) & 15u) == 0 && ld % 8 == 0; };
   const bool vec = q.K % 8 == 0 && rows16(q.A, q.lda) && rows16(q.B, q.ldb);
   switch ((q.M + 7) / 8) {
     case 1:
-      return rows_tiles<1>(p, vec, num_sms, stream);
+      return rows_tiles<1>(p, vec, stream);
     case 2:
-      return rows_tiles<2>(p, vec, num_sms, stream);
+      return rows_tiles<2>(p, vec, stream);
     case 3:
-      return rows_tiles<3>(p, vec, num_sms, stream);
+      return rows_tiles<3>(p, vec, stream);
     default:
-      return rows_tiles<4>(p, vec, num_sms, stream);
+      return rows_tiles<4>(p, vec, stream);
   }
 }
 

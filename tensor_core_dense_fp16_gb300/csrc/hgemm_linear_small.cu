@@ -1,0 +1,296 @@
+// hgemm_linear_small.cu — a linear layer's forward product for at most 128
+// rows of X (a batch of generated tokens, a short prompt), bound by reading
+// the weights once.
+//
+// The product is computed turned around, Yᵀ = W·Xᵀ: the features are the rows
+// of the matrix instruction (M = 128) and the rows of X its columns (N = 16
+// to 128, as many as there are), so that no part of the instruction is spent
+// on rows that do not exist, and a CTA's ring of stages is almost all
+// weights: 6 to 11 stages, about 200 KB under way per SM. A cluster of CTAs
+// shares 128 features, each a run of K; the FP32 partial sums are left in
+// each CTA's shared memory, and every CTA adds those of its share of the
+// columns in rank order (so the result does not depend on timing) through
+// distributed shared memory. In the accumulator a thread owns a feature:
+// bias, residual and output are read and written along the features, whatever
+// their pitch and alignment.
+#include <atomic>
+
+#include "internal.h"
+#include "kernel_common.cuh"
+#include "linear_epilogue.cuh"
+#include "ptx.cuh"
+
+namespace hg {
+namespace {
+
+template <int NT_>
+struct SmallCfg {
+  static constexpr int NT = NT_;   // rows of X per CTA: columns of the instruction
+  static constexpr int BM = 128;   // features
+  static constexpr int BK = kTcBK, UMMA_K = 16;
+  static constexpr int W_BYTES = BM * BK * 2;
+  static constexpr int X_BYTES = NT * BK * 2;
+  static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
+  static constexpr int STAGES = (208 * 1024) / STAGE_BYTES;
+  static constexpr int PART_BYTES = NT * BM * 4;  // the partial sums, in the ring
+  static constexpr int OFF_BAR = STAGES * STAGE_BYTES;
+  static constexpr int NUM_BARS = 2 * STAGES + 2;  // full, empty, accumulator full, drain
+  static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
+  static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
+  static constexpr int THREADS = 192;
+  static constexpr int TMEM_COLS = NT < 32 ? 32 : NT;
+  static constexpr uint32_t IDESC = idesc_f16_f32acc(BM, NT);
+  static_assert(STAGE_BYTES % 1024 == 0, "swizzled tiles are 1024-byte aligned");
+  static_assert(PART_BYTES <= STAGES * STAGE_BYTES, "the partial sums fit the ring");
+  static_assert(SMEM_BYTES <= 232448, "exceeds 227 KB of shared memory per CTA");
+};
+
+// Outputs of feature f and rows m .. m + R - 1 of X, the first `count` of
+// them inside.
+template <int R>
+__device__ __forceinline__ void put_rows(const SmallArgs& p, const float (&sum)[R], float bias, int m, int f, int count) {
+  const LinEpi& e = p.epi;
+  uint32_t res[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) res[i] = 0u;
+  if (e.res) {
+    const uint16_t* r = e.res + m * e.ldr + f;
+#pragma unroll
+    for (int i = 0; i < R; ++i, r += e.ldr)
+      if (i < count) res[i] = *r;
+  }
+  uint16_t* y = p.Y + m * p.ldy + f;
+  with_activation(e.act, [&](auto a) {
+#pragma unroll
+    for (int i = 0; i < R; i += 2) {
+      f32x2 v, df;
+      activate<decltype(a)::value, false>(add2(pair_of(sum[i], sum[i + 1]), pair_of(bias)), v, df);
+      const uint32_t h = pack_half2(add2(v, unpack_half2(res[i] | res[i + 1] << 16)));
+      if (i < count) y[0] = static_cast<uint16_t>(h);
+      if (i + 1 < count) y[p.ldy] = static_cast<uint16_t>(h >> 16);
+      y += 2 * p.ldy;
+    }
+  });
+}
+
+template <int NT>
+__global__ void __launch_bounds__(192, 1)
+    linear_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                        const SmallArgs p) {
+  using Cfg = SmallCfg<NT>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + Cfg::OFF_BAR;
+  const uint32_t accf_bar = bar0 + 8u * (2 * Cfg::STAGES), drain_bar = accf_bar + 8u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::OFF_MISC + 4);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (Cfg::STAGES + s); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int f0 = static_cast<int>(blockIdx.x) / p.split * Cfg::BM;  // first feature
+  const int kb0 = static_cast<int>(static_cast<long long>(p.num_kb) * rank / p.split);
+  const int kb1 = static_cast<int>(static_cast<long long>(p.num_kb) * (rank + 1) / p.split);
+  const Watchdog wd{abort_flag, p.status, p.timeout_ns};
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < Cfg::STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    mbar_init(accf_bar, 1);
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tensormap(&tmW);
+    prefetch_tensormap(&tmX);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), Cfg::TMEM_COLS);
+    tmem_relinquish_alloc_permit();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  const int q = warp & 3;
+  const int f = f0 + q * 32 + lane;  // this epilogue thread's feature
+  const bool in_f = f < p.N;
+  const float bias =
+      warp >= 2 && p.epi.bias && in_f ? __half2float(__ushort_as_half(__ldg(p.epi.bias + f))) : 0.f;
+  float* part = reinterpret_cast<float*>(smem);  // [row of X][feature]
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int issued = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!wait_phase(empty_bar(stage), phase ^ 1u, wd, kWdProducerEmpty)) break;
+        if (!(p.inject == 1 && issued == 0))  // testing aid: withhold one arrival
+          mbar_arrive_expect_tx(full_bar(stage), Cfg::STAGE_BYTES);
+        const uint32_t dst = sbase + stage * Cfg::STAGE_BYTES;
+        tma_load_2d(dst, &tmW, full_bar(stage), kb * Cfg::BK, f0);
+        tma_load_2d(dst + Cfg::W_BYTES, &tmX, full_bar(stage), kb * Cfg::BK, 0);
+        ++issued;
+        if (++stage == Cfg::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      // the last loads must have landed before the ring is reused or left
+      int s = stage;
+      uint32_t ph = phase;
+      for (int i = 0; i < issued && i < Cfg::STAGES; ++i) {
+        if (s == 0) {
+          s = Cfg::STAGES - 1;
+          ph ^= 1u;
+        } else {
+          --s;
+        }
+        wait_drain(full_bar(s), ph, wd);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!wait_phase(full_bar(stage), phase, wd, kWdMmaFull)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint64_t w_desc = sdesc_kmajor_sw128(sbase + stage * Cfg::STAGE_BYTES);
+        const uint64_t x_desc = sdesc_kmajor_sw128(sbase + stage * Cfg::STAGE_BYTES + Cfg::W_BYTES);
+#pragma unroll
+        for (int k = 0; k < Cfg::BK / Cfg::UMMA_K; ++k)
+          mma_f16_ss(tmem_base, w_desc + 2u * k, x_desc + 2u * k, Cfg::IDESC, (kb > kb0 || k > 0) ? 1u : 0u);
+        mma_commit(empty_bar(stage));
+        if (++stage == Cfg::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (ok) mma_commit(accf_bar);
+      mma_commit(drain_bar);
+      wait_drain(drain_bar, 0, wd);
+    }
+    __syncwarp();
+  } else {
+    int ok = 1;
+    if (lane == 0) ok = wait_phase(accf_bar, 0, wd, kWdEpiAccFull) ? 1 : 0;
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    if (ok) {
+      tc_fence_after_sync();
+      const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll 1
+      for (int c = 0; c < NT && c < p.M; c += 16) {
+        float v[16];
+        tmem_ld_32x32b_x16(t_row + c, v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (p.split > 1) part[(c + i) * Cfg::BM + q * 32 + lane] = v[i];
+        if (p.split == 1) put_rows<16>(p, v, bias, c, f, in_f ? p.M - c : 0);
+      }
+    }
+  }
+  if (p.split > 1) {
+    // (after a wait that gave up the sums are garbage; every CTA still
+    // reaches both barriers)
+    cluster_sync();
+    if (warp >= 2) {
+      const int m0 = NT * rank / p.split, m1 = NT * (rank + 1) / p.split;
+      const uint32_t mine = smem_u32(part + q * 32 + lane);
+      // eight rows at a time: every rank's partial sums of them are under way at once
+#pragma unroll 1
+      for (int m = m0; m < m1 && m < p.M; m += 8) {
+        float sum[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (r < p.split) {
+            const uint32_t from = mapa_shared(mine + static_cast<uint32_t>(m * Cfg::BM * 4), r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float v = m + i < m1 ? ld_cluster_f32(from + static_cast<uint32_t>(i * Cfg::BM * 4)) : 0.f;
+              sum[i] = r == 0 ? v : sum[i] + v;
+            }
+          }
+        const int left = (m1 < p.M ? m1 : p.M) - m;
+        put_rows<8>(p, sum, bias, m, f, in_f ? left : 0);
+      }
+    }
+    cluster_sync();  // the other CTAs' shared memory stays until everybody has read it
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == 1) tmem_dealloc(tmem_base, Cfg::TMEM_COLS);
+}
+
+template <int NT>
+cudaError_t launch_with(const CUtensorMap& w, const CUtensorMap& x, const SmallArgs& a, cudaStream_t stream) {
+  using Cfg = SmallCfg<NT>;
+  static std::atomic<bool> attr_done[64];
+  auto kern = linear_small_kernel<NT>;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !attr_done[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_done[dev] = true;
+  }
+  const unsigned tiles = static_cast<unsigned>((a.N + Cfg::BM - 1) / Cfg::BM);
+  PdlLaunch l(dim3(tiles * static_cast<unsigned>(a.split)), dim3(Cfg::THREADS), Cfg::SMEM_BYTES, stream);
+  l.cluster(static_cast<unsigned>(a.split));
+  return cudaLaunchKernelEx(&l.cfg, kern, w, x, a);
+}
+
+}  // namespace
+
+int linear_small_clusters(int split, int num_sms) {
+  static std::atomic<int> cached[64][9];
+  int dev = 0;
+  if (split < 1 || split > 8 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if (cached[dev][split] > 0) return cached[dev][split];
+  using Cfg = SmallCfg<16>;  // (the others differ by a few KB of shared memory)
+  auto kern = linear_small_kernel<16>;
+  int n = 0;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES) == cudaSuccess) {
+    PdlLaunch l(dim3(static_cast<unsigned>(num_sms / split * split)), dim3(Cfg::THREADS), Cfg::SMEM_BYTES, nullptr);
+    l.cluster(static_cast<unsigned>(split));
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &l.cfg) != cudaSuccess) n = 0;
+  }
+  (void)cudaGetLastError();
+  if (n <= 0) n = 1;
+  cached[dev][split] = n;
+  return n;
+}
+
+int linear_small_rows(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
+
+cudaError_t launch_linear_small(const CUtensorMap& w, const CUtensorMap& x, const SmallArgs& a, cudaStream_t stream) {
+  switch (linear_small_rows(a.M)) {
+    case 16:
+      return launch_with<16>(w, x, a, stream);
+    case 32:
+      return launch_with<32>(w, x, a, stream);
+    case 64:
+      return launch_with<64>(w, x, a, stream);
+    default:
+      return launch_with<128>(w, x, a, stream);
+  }
+}
+
+// The -DHGEMM_DEBUG build's check word of this file (null otherwise).
+HG_DEBUG_WORD_ACCESSOR(linear_small)
+
+}  // namespace hg

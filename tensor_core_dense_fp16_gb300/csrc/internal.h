@@ -239,8 +239,26 @@ struct LinearProduct {
 int run_linear(const LinearProduct& p, cudaStream_t stream);
 // The kernel for at most kLinearRows rows of A, and whether it computes p.
 constexpr int kLinearRows = 32;
+constexpr int kLinearFragmentRows = 8;  // always that kernel: one column fragment
 bool linear_rows_suits(const LinearProduct& p);
-cudaError_t launch_linear_rows(const LinearProduct& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_linear_rows(const LinearProduct& p, cudaStream_t stream);
+// The kernel for at most kLinearSmall rows of A, fed by TMA: w maps the
+// weights (128 × 64 boxes), x the rows of A (linear_small_rows(M) × 64).
+constexpr int kLinearSmall = 128;
+struct SmallArgs {
+  uint16_t* Y;
+  int64_t ldy;
+  int M, N, num_kb;
+  int split;  // CTAs of a cluster, each a run of the K blocks: 1 to 8
+  int* status;
+  unsigned long long timeout_ns;
+  int inject;
+  LinEpi epi;
+};
+int linear_small_rows(int64_t M);
+// How many clusters of `split` CTAs the device holds at once.
+int linear_small_clusters(int split, int num_sms);
+cudaError_t launch_linear_small(const CUtensorMap& w, const CUtensorMap& x, const SmallArgs& a, cudaStream_t stream);
 // The kernel for operands and outputs of any pitch and alignment; K > 0.
 cudaError_t launch_linear_any(const LinearProduct& p, const CallDevice& dev, cudaStream_t stream);
 // The gradient of a weight: C = A·B, or C + A·B, with an epilogue that says so.
@@ -294,7 +312,8 @@ cudaError_t debug_word_linear(int** out);
 cudaError_t debug_word_norm(int** out);
 cudaError_t debug_word_ckpt8(int** out);
 cudaError_t debug_word_linear_any(int** out);
-constexpr int kDebugWords = 12;
+cudaError_t debug_word_linear_small(int** out);
+constexpr int kDebugWords = 13;
 
 // Co-residency limits of the cluster kernels on one device, measured once
 // (or nominal GB300 figures when no device has been queried).
