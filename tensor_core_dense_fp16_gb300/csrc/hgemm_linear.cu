@@ -185,15 +185,24 @@ cudaError_t rows_tiles(const RowsArgs& p, bool vec, cudaStream_t stream) {
 // shared memory, and the CTAs in rank order through distributed shared memory
 // by rank 0. Bound by reading dY once; a strip is as wide as leaves enough
 // CTAs, because the longer a row's piece the better memory delivers it.
+//
+// beside: the launch before this one on the stream is the product with the
+// same dY, and the two may run at the same time, the sums on SMs that the
+// product leaves idle. Nothing here depends on that product, and what it
+// waited for is complete (it lets this launch start only after its own
+// wait), so the sums need not wait; but the first block ends only after the
+// product has, so that whoever waits for this launch waits for both.
 constexpr int kSumThreads = 512;
 constexpr int kUnroll = 8;
 template <int VEC>
 __global__ void __launch_bounds__(kSumThreads)
     column_sums_kernel(const uint16_t* __restrict__ dy, int64_t ld, int64_t M, int64_t N, float* __restrict__ out,
-                       int accumulate, int across, int cluster) {
+                       int accumulate, int across, int cluster, int beside) {
   __shared__ float s[kSumThreads * VEC];  // [down][columns]
-  grid_dependency_wait();
-  grid_launch_dependents();
+  if (!beside) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+  }
   const int columns = across * VEC, down = kSumThreads / across;
   const int rank = static_cast<int>(blockIdx.x) % cluster;
   const int c = threadIdx.x % across * VEC, r = threadIdx.x / across;
@@ -236,6 +245,7 @@ __global__ void __launch_bounds__(kSumThreads)
   }
   const int64_t n = n0 + threadIdx.x;
   if (rank == 0 && mine && n < N) out[n] = accumulate ? out[n] + total : total;
+  if (beside && blockIdx.x == 0) grid_dependency_wait();
 }
 
 }  // namespace
@@ -270,7 +280,7 @@ cudaError_t launch_linear_empty(uint16_t* C, int64_t ldc, int64_t M, int64_t N, 
 }
 
 cudaError_t launch_column_sums(const uint16_t* dy, int64_t ld, int64_t M, int64_t N, float* out, bool accumulate,
-                               cudaStream_t stream) {
+                               bool beside, cudaStream_t stream) {
   const bool vec = N % 8 == 0 && ld % 8 == 0 && (reinterpret_cast<uintptr_t>(dy) & 15u) == 0;
   const int vec_cols = vec ? 8 : 1;
   // up to 8 CTAs (the portable cluster size) per strip, 128 rows or more each
@@ -285,7 +295,7 @@ cudaError_t launch_column_sums(const uint16_t* dy, int64_t ld, int64_t M, int64_
   PdlLaunch l(dim3(static_cast<unsigned>(blocks())), dim3(kSumThreads), 0, stream);
   l.cluster(static_cast<unsigned>(cluster));
   return cudaLaunchKernelEx(&l.cfg, vec ? column_sums_kernel<8> : column_sums_kernel<1>, dy, ld, M, N, out,
-                            accumulate ? 1 : 0, across, cluster);
+                            accumulate ? 1 : 0, across, cluster, beside ? 1 : 0);
 }
 
 // The -DHGEMM_DEBUG build's check word of this file (null otherwise).
