@@ -124,6 +124,9 @@ struct Gemm {
   int64_t ld_src = 0;
   // a linear layer's epilogue instead of EpiArgs (null: none)
   const hg::LinEpi* lin = nullptr;
+  // an M- or N-contiguous product splits K from 8 blocks on where the pair
+  // kernel's tiles would leave most pairs idle
+  bool early_split = false;
   hg::Epilogue kind(const hg::EpiArgs& epi) const {
     if (lin) return lin->backward ? hg::kEpiLinearGrad : hg::kEpiLinear;
     return epi.mode != 0 ? hg::kEpiFused : hg::kEpiPlain;
@@ -275,6 +278,13 @@ int choose_path(const Gemm& g, const hg::DeviceProfile& prof, bool fused, int* s
   if (forced == HGEMM_PATH_GENERIC || !tma) return HGEMM_PATH_GENERIC;
   const int fs = g_forced_split.load(std::memory_order_relaxed);
   const int path = hg::choose_tma_path(M, N, K, prof, forced, fs >> 10, fs & 1023, fused, split, tile_n);
+  // Gradients of linear layers: such operands have no 128×64 tiles, and the
+  // pair kernel keeps 128 columns of a tile, so few tiles leave most pairs
+  // idle unless K is split (1000^3: 9.4 to 7.7 us; 2000×1000, contraction
+  // 1000, 32 tiles: 9.6 to 10.8).
+  if (g.early_split && (g.a_mn || g.b_mn) && forced < 0 && path != HGEMM_PATH_SKINNY && K >= 8 * hg::kTcBK &&
+      4 * ((M + 255) / 256) * ((N + 255) / 256) <= prof.pair_clusters)
+    return hg::choose_tma_path(M, N, K, prof, HGEMM_PATH_SKINNY, fs >> 10, fs & 1023, fused, split, tile_n);
   // M- or N-contiguous operands: the wide, pair and split-K kernels read
   // them as MN-major tiles; the single-CTA kernel takes K-major ones only
   if ((g.a_mn || g.b_mn) && (path == HGEMM_PATH_TC || path == HGEMM_PATH_TC_NARROW))
@@ -733,39 +743,54 @@ int trmm_pipe(int dev, TrmmPipe** out) {
 
 namespace hg {
 
-// Whether the turned-around product for few rows computes p, and is the
-// faster one. Measured (us, weights from memory): against the kernel of
-// matrix fragments, 16 rows, 4096×4096 9.6 to 11.3, 8192×8192 24.3 to 32.6,
-// but 1024×1024 4.3 to 3.6 (so: from 2^21 weights on); against the 128×64
-// tiles, 128 rows, 2048×8192 13.8 to 19.4 and 8192×4096 19.5 to 22.9, but
-// 8192×2048 13.5 to 12.2 and 512×512 8.5 to 5.9 (so: not for more than 64
-// rows where one wave of those tiles covers the output and K is short).
+// Whether the turned-around product for few rows or small outputs computes p,
+// and is the faster kernel. Measured (us, operands from memory):
+//   forward, against the kernel of matrix fragments, 16 rows: 4096×4096 9.6 to
+//   11.3, 8192×8192 24.3 to 32.6, but 1024×1024 4.3 to 3.6 (so: from 2^21
+//   weights on); against the 128×64 tiles, 128 rows: 2048×8192 13.8 to 19.4,
+//   8192×4096 19.5 to 22.9, but 8192×2048 13.5 to 12.2 and 512×512 8.5 to 5.9
+//   (so: not for more than 64 rows where one wave of those tiles covers the
+//   output and K is short);
+//   input gradient, against the split-K kernel: 64 rows 4096×1024 8.3 to 13.1,
+//   16 rows 512×512 5.0 to 6.4, 128 rows 8192×2048 14.2 to 18.5, but 128 rows
+//   1024×4096 10.8 to 8.5;
+//   weight gradient, against the split-K kernel: 16384 rows 512×512 18.2 to
+//   24.9, 5000 rows 200×304 10.4 to 14.9, but 4096 rows 1024×1024 (64 tiles)
+//   16.1 to 13.2 and 512 rows 512×512 8.6 to 5.7.
 bool linear_small_suits(const LinearProduct& p, int num_sms) {
   auto rows = [](const void* q, int64_t ld) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0 && ld % 8 == 0; };
-  if (p.M > kLinearSmall || p.K == 0 || p.a_mn || p.b_mn || p.epi.backward || p.epi.codes || !rows(p.A, p.lda) ||
-      !rows(p.B, p.ldb))
-    return false;
-  if (p.M <= kLinearFragmentRows) return false;
+  if (p.K == 0 || !rows(p.A, p.lda) || !rows(p.B, p.ldb)) return false;
+  if (p.a_mn) return p.K >= 2048 && (p.M + 127) / 128 * ((p.N + 127) / 128) <= 36;
+  if (p.M > kLinearSmall) return false;
+  if (p.epi.backward) return p.M <= 64 || p.K >= 2048;
+  if (p.epi.codes || p.M <= kLinearFragmentRows) return false;
   if (p.M <= kLinearRows) return p.N * p.K >= int64_t(1) << 21;
   return p.M <= 64 || p.K > 2048 || p.N > int64_t(kNarrowBN) * num_sms;
 }
 
 int run_linear_small(const LinearProduct& p, const DeviceState& dev, cudaStream_t stream) {
+  SmallArgs a{};
+  a.tile_rows = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
+  if (p.a_mn && a.tile_rows < 64) a.tile_rows = 64;
   CUtensorMap mw, mx;
   int rc;
-  if ((rc = encode_map(&mw, p.B, p.N, p.K, p.ldb, kTcBM, kTcBK)) != HGEMM_OK) return rc;
-  if ((rc = encode_map(&mx, p.A, p.M, p.K, p.lda, linear_small_rows(p.M), kTcBK)) != HGEMM_OK) return rc;
-  SmallArgs a{};
+  rc = p.b_mn ? encode_map(&mw, p.B, p.K, p.N, p.ldb, kTcBK, 64) : encode_map(&mw, p.B, p.N, p.K, p.ldb, kTcBM, kTcBK);
+  if (rc != HGEMM_OK) return rc;
+  rc = p.a_mn ? encode_map(&mx, p.A, p.K, p.M, p.lda, kTcBK, 64)
+              : encode_map(&mx, p.A, p.M, p.K, p.lda, a.tile_rows, kTcBK);
+  if (rc != HGEMM_OK) return rc;
   a.Y = p.C;
   a.ldy = p.ldc;
   a.M = static_cast<int>(p.M);
   a.N = static_cast<int>(p.N);
   a.num_kb = static_cast<int>((p.K + kTcBK - 1) / kTcBK);
-  // The most CTAs per 128 features with which all clusters run at once, four
+  a.row_tiles = static_cast<int>((p.M + a.tile_rows - 1) / a.tile_rows);
+  a.w_mn = p.b_mn ? 1 : 0;
+  // The most CTAs per output tile with which all clusters run at once, four
   // K blocks or more each: an SM takes in weights at ~112 GB/s, so the more
   // SMs share them the better, but a second wave costs a whole pass
   // (2048×8192: clusters of 8, 15 at a time for 16 tiles, 15.1 us; of 4, 10.1).
-  const int64_t tiles = (p.N + kTcBM - 1) / kTcBM;
+  const int64_t tiles = (p.N + kTcBM - 1) / kTcBM * a.row_tiles;
   if (tiles * 8 > 0x7FFFFFFF) return HGEMM_ERR_INVALID_ARG;
   a.split = 1;
   for (int s = 8; s > 1; --s)
@@ -791,6 +816,7 @@ int run_linear(const LinearProduct& p, cudaStream_t stream) {
   g.a_mn = p.a_mn;
   g.b_mn = p.b_mn;
   g.lin = &p.epi;
+  g.early_split = true;
   if (p.K > 0 && (forced == HGEMM_PATH_GENERIC || !tma_ok(g))) {
     const CallDevice cd{dev->num_sms, t_ctx.status, g_timeout_ns.load(std::memory_order_relaxed)};
     return cuda_status(launch_linear_any(p, cd, stream));
@@ -798,7 +824,7 @@ int run_linear(const LinearProduct& p, cudaStream_t stream) {
   return dispatch(g, kPlainEpilogue, *dev, stream);
 }
 
-int run_wgrad(const LinearProduct& p, cudaStream_t stream) {
+int run_wgrad(const LinearProduct& p, bool alone, cudaStream_t stream) {
   Gemm g{p.A, p.B, p.C, p.M, p.N, p.K, p.lda, p.ldb, p.ldc};
   g.a_mn = p.a_mn;
   g.b_mn = p.b_mn;
@@ -807,6 +833,10 @@ int run_wgrad(const LinearProduct& p, cudaStream_t stream) {
   DeviceState* dev = nullptr;
   const int rc = current_device(&dev);
   if (rc != HGEMM_OK) return rc;
+  // (beside the bias gradient's launch the SMs that a split would take serve
+  // the column sums: 1000^3 with bias 12.6 us split, 11.1 not)
+  g.early_split = alone;
+  if (forced < 0 && linear_small_suits(p, dev->num_sms)) return run_linear_small(p, *dev, stream);
   // (the plain and the accumulating product; the sum of an old value is the residual's)
   EpiArgs epi = kPlainEpilogue;
   if (p.epi.res) {

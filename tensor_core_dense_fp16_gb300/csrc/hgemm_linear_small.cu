@@ -1,18 +1,19 @@
-// hgemm_linear_small.cu — a linear layer's forward product for at most 128
-// rows of X (a batch of generated tokens, a short prompt), bound by reading
-// the weights once.
+// hgemm_linear_small.cu — products of linear layers with few rows or a small
+// output: the forward product and the input gradient of at most 128 rows (a
+// batch of generated tokens, a short prompt), bound by reading the weights
+// once, and the gradient of a small weight over many rows.
 //
-// The product is computed turned around, Yᵀ = W·Xᵀ: the features are the rows
-// of the matrix instruction (M = 128) and the rows of X its columns (N = 16
-// to 128, as many as there are), so that no part of the instruction is spent
-// on rows that do not exist, and a CTA's ring of stages is almost all
-// weights: 6 to 11 stages, about 200 KB under way per SM. A cluster of CTAs
-// shares 128 features, each a run of K; the FP32 partial sums are left in
-// each CTA's shared memory, and every CTA adds those of its share of the
-// columns in rank order (so the result does not depend on timing) through
-// distributed shared memory. In the accumulator a thread owns a feature:
-// bias, residual and output are read and written along the features, whatever
-// their pitch and alignment.
+// The product is computed turned around: the columns of the output (features)
+// are the rows of the matrix instruction (M = 128) and the output's rows its
+// columns (N = 16 to 128, as many as there are), so that no part of the
+// instruction is spent on rows that do not exist, and a CTA's ring of stages
+// is almost all weights: 6 to 11 stages, about 200 KB under way per SM. A
+// cluster of CTAs shares an output tile, each a run of K; the FP32 partial
+// sums are left in each CTA's shared memory, and every CTA adds those of its
+// share of the rows in rank order (so the result does not depend on timing)
+// through distributed shared memory. In the accumulator a thread owns a
+// feature: bias, residual, 8-bit codes and outputs are read and written along
+// the features, whatever their pitch and alignment.
 #include <atomic>
 
 #include "internal.h"
@@ -25,7 +26,7 @@ namespace {
 
 template <int NT_>
 struct SmallCfg {
-  static constexpr int NT = NT_;   // rows of X per CTA: columns of the instruction
+  static constexpr int NT = NT_;   // output rows per CTA: columns of the instruction
   static constexpr int BM = 128;   // features
   static constexpr int BK = kTcBK, UMMA_K = 16;
   static constexpr int W_BYTES = BM * BK * 2;
@@ -45,35 +46,70 @@ struct SmallCfg {
   static_assert(SMEM_BYTES <= 232448, "exceeds 227 KB of shared memory per CTA");
 };
 
-// Outputs of feature f and rows m .. m + R - 1 of X, the first `count` of
-// them inside.
-template <int R>
-__device__ __forceinline__ void put_rows(const SmallArgs& p, const float (&sum)[R], float bias, int m, int f, int count) {
+// Outputs of feature f and rows m .. m + R - 1, the first `count` of them
+// inside.
+template <bool BACKWARD, int R>
+__device__ __forceinline__ void put_rows(const SmallArgs& p, const float (&sum)[R], float bias, int64_t m, int f,
+                                         int count) {
   const LinEpi& e = p.epi;
-  uint32_t res[R];
+  uint32_t side[R];  // residual, or codes
+  float scale[R];
 #pragma unroll
-  for (int i = 0; i < R; ++i) res[i] = 0u;
-  if (e.res) {
+  for (int i = 0; i < R; ++i) {
+    side[i] = 0u;
+    scale[i] = 0.f;
+  }
+  if (BACKWARD && e.codes) {
+    const int8_t* q = e.codes + m * e.ldq + f;
+    const float* s = e.scales + f / kCkptGroup * e.lds + m;
+#pragma unroll
+    for (int i = 0; i < R; ++i, q += e.ldq)
+      if (i < count) {
+        side[i] = static_cast<uint8_t>(*q);
+        scale[i] = s[i];
+      }
+  } else if (!BACKWARD && e.res) {
     const uint16_t* r = e.res + m * e.ldr + f;
 #pragma unroll
     for (int i = 0; i < R; ++i, r += e.ldr)
-      if (i < count) res[i] = *r;
+      if (i < count) side[i] = *r;
   }
   uint16_t* y = p.Y + m * p.ldy + f;
-  with_activation(e.act, [&](auto a) {
+  uint16_t* h = e.h + m * e.ldh + f;
+  with_activation(!BACKWARD || e.codes ? e.act : HGEMM_ACT_NONE, [&](auto a) {
 #pragma unroll
     for (int i = 0; i < R; i += 2) {
-      f32x2 v, df;
-      activate<decltype(a)::value, false>(add2(pair_of(sum[i], sum[i + 1]), pair_of(bias)), v, df);
-      const uint32_t h = pack_half2(add2(v, unpack_half2(res[i] | res[i + 1] << 16)));
-      if (i < count) y[0] = static_cast<uint16_t>(h);
-      if (i + 1 < count) y[p.ldy] = static_cast<uint16_t>(h >> 16);
+      f32x2 v = pair_of(sum[i], sum[i + 1]), df;
+      if constexpr (BACKWARD) {
+        if (e.codes) {
+          f32x2 hid;
+          activate<decltype(a)::value, true>(pair_of(static_cast<float>(static_cast<int8_t>(side[i])) * scale[i],
+                                                     static_cast<float>(static_cast<int8_t>(side[i + 1])) * scale[i + 1]),
+                                             hid, df);
+          v = mul2(v, df);
+          if (e.h) {
+            const uint32_t w = pack_half2(hid);
+            if (i < count) h[0] = static_cast<uint16_t>(w);
+            if (i + 1 < count) h[e.ldh] = static_cast<uint16_t>(w >> 16);
+            h += 2 * e.ldh;
+          }
+        }
+      } else {
+        f32x2 f2;
+        activate<decltype(a)::value, false>(add2(v, pair_of(bias)), f2, df);
+        v = add2(f2, unpack_half2(side[i] | side[i + 1] << 16));
+      }
+      const uint32_t w = pack_half2(v);
+      if (i < count) y[0] = static_cast<uint16_t>(w);
+      if (i + 1 < count) y[p.ldy] = static_cast<uint16_t>(w >> 16);
       y += 2 * p.ldy;
     }
   });
 }
 
-template <int NT>
+// W_MN, X_MN: the operand whose rows are features, or output rows, is stored
+// with those contiguous (K×features, K×rows) and read as MN-major tiles.
+template <int NT, bool W_MN, bool X_MN, bool BACKWARD>
 __global__ void __launch_bounds__(192, 1)
     linear_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                         const SmallArgs p) {
@@ -90,7 +126,10 @@ __global__ void __launch_bounds__(192, 1)
   auto empty_bar = [&](int s) { return bar0 + 8u * (Cfg::STAGES + s); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int f0 = static_cast<int>(blockIdx.x) / p.split * Cfg::BM;  // first feature
+  const int tile = static_cast<int>(blockIdx.x) / p.split;
+  const int f0 = tile / p.row_tiles * Cfg::BM;  // first feature
+  const int r0 = tile % p.row_tiles * NT;       // first output row
+  const int rows = p.M - r0 < NT ? p.M - r0 : NT;
   const int kb0 = static_cast<int>(static_cast<long long>(p.num_kb) * rank / p.split);
   const int kb1 = static_cast<int>(static_cast<long long>(p.num_kb) * (rank + 1) / p.split);
   const Watchdog wd{abort_flag, p.status, p.timeout_ns};
@@ -122,7 +161,7 @@ __global__ void __launch_bounds__(192, 1)
   const int f = f0 + q * 32 + lane;  // this epilogue thread's feature
   const bool in_f = f < p.N;
   const float bias =
-      warp >= 2 && p.epi.bias && in_f ? __half2float(__ushort_as_half(__ldg(p.epi.bias + f))) : 0.f;
+      !BACKWARD && warp >= 2 && p.epi.bias && in_f ? __half2float(__ushort_as_half(__ldg(p.epi.bias + f))) : 0.f;
   float* part = reinterpret_cast<float*>(smem);  // [row of X][feature]
 
   if (warp == 0) {
@@ -135,8 +174,19 @@ __global__ void __launch_bounds__(192, 1)
         if (!(p.inject == 1 && issued == 0))  // testing aid: withhold one arrival
           mbar_arrive_expect_tx(full_bar(stage), Cfg::STAGE_BYTES);
         const uint32_t dst = sbase + stage * Cfg::STAGE_BYTES;
-        tma_load_2d(dst, &tmW, full_bar(stage), kb * Cfg::BK, f0);
-        tma_load_2d(dst + Cfg::W_BYTES, &tmX, full_bar(stage), kb * Cfg::BK, 0);
+        if constexpr (W_MN) {
+          tma_load_2d(dst, &tmW, full_bar(stage), f0, kb * Cfg::BK);
+          tma_load_2d(dst + kMnBoxBytes, &tmW, full_bar(stage), f0 + kMnBox, kb * Cfg::BK);
+        } else {
+          tma_load_2d(dst, &tmW, full_bar(stage), kb * Cfg::BK, f0);
+        }
+        if constexpr (X_MN) {
+#pragma unroll
+          for (int b = 0; b < NT / kMnBox; ++b)
+            tma_load_2d(dst + Cfg::W_BYTES + b * kMnBoxBytes, &tmX, full_bar(stage), r0 + b * kMnBox, kb * Cfg::BK);
+        } else {
+          tma_load_2d(dst + Cfg::W_BYTES, &tmX, full_bar(stage), kb * Cfg::BK, r0);
+        }
         ++issued;
         if (++stage == Cfg::STAGES) {
           stage = 0;
@@ -168,11 +218,13 @@ __global__ void __launch_bounds__(192, 1)
           break;
         }
         tc_fence_after_sync();
-        const uint64_t w_desc = sdesc_kmajor_sw128(sbase + stage * Cfg::STAGE_BYTES);
-        const uint64_t x_desc = sdesc_kmajor_sw128(sbase + stage * Cfg::STAGE_BYTES + Cfg::W_BYTES);
+        const uint32_t sw = sbase + stage * Cfg::STAGE_BYTES, sx = sw + Cfg::W_BYTES;
+        const uint64_t w_desc = W_MN ? sdesc_mnmajor_sw128(sw) : sdesc_kmajor_sw128(sw);
+        const uint64_t x_desc = X_MN ? sdesc_mnmajor_sw128(sx) : sdesc_kmajor_sw128(sx);
 #pragma unroll
         for (int k = 0; k < Cfg::BK / Cfg::UMMA_K; ++k)
-          mma_f16_ss(tmem_base, w_desc + 2u * k, x_desc + 2u * k, Cfg::IDESC, (kb > kb0 || k > 0) ? 1u : 0u);
+          mma_f16_ss(tmem_base, w_desc + (W_MN ? 128u : 2u) * k, x_desc + (X_MN ? 128u : 2u) * k,
+                     Cfg::IDESC | idesc_major_bits(W_MN, X_MN), (kb > kb0 || k > 0) ? 1u : 0u);
         mma_commit(empty_bar(stage));
         if (++stage == Cfg::STAGES) {
           stage = 0;
@@ -192,13 +244,13 @@ __global__ void __launch_bounds__(192, 1)
       tc_fence_after_sync();
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
 #pragma unroll 1
-      for (int c = 0; c < NT && c < p.M; c += 16) {
+      for (int c = 0; c < rows; c += 16) {
         float v[16];
         tmem_ld_32x32b_x16(t_row + c, v);
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           if (p.split > 1) part[(c + i) * Cfg::BM + q * 32 + lane] = v[i];
-        if (p.split == 1) put_rows<16>(p, v, bias, c, f, in_f ? p.M - c : 0);
+        if (p.split == 1) put_rows<BACKWARD, 16>(p, v, bias, r0 + c, f, in_f ? rows - c : 0);
       }
     }
   }
@@ -211,7 +263,7 @@ __global__ void __launch_bounds__(192, 1)
       const uint32_t mine = smem_u32(part + q * 32 + lane);
       // eight rows at a time: every rank's partial sums of them are under way at once
 #pragma unroll 1
-      for (int m = m0; m < m1 && m < p.M; m += 8) {
+      for (int m = m0; m < m1 && m < rows; m += 8) {
         float sum[8];
 #pragma unroll
         for (int r = 0; r < 8; ++r)
@@ -223,8 +275,8 @@ __global__ void __launch_bounds__(192, 1)
               sum[i] = r == 0 ? v : sum[i] + v;
             }
           }
-        const int left = (m1 < p.M ? m1 : p.M) - m;
-        put_rows<8>(p, sum, bias, m, f, in_f ? left : 0);
+        const int left = (m1 < rows ? m1 : rows) - m;
+        put_rows<BACKWARD, 8>(p, sum, bias, r0 + m, f, in_f ? left : 0);
       }
     }
     cluster_sync();  // the other CTAs' shared memory stays until everybody has read it
@@ -235,11 +287,11 @@ __global__ void __launch_bounds__(192, 1)
   if (warp == 1) tmem_dealloc(tmem_base, Cfg::TMEM_COLS);
 }
 
-template <int NT>
+template <int NT, bool W_MN, bool X_MN, bool BACKWARD>
 cudaError_t launch_with(const CUtensorMap& w, const CUtensorMap& x, const SmallArgs& a, cudaStream_t stream) {
   using Cfg = SmallCfg<NT>;
   static std::atomic<bool> attr_done[64];
-  auto kern = linear_small_kernel<NT>;
+  auto kern = linear_small_kernel<NT, W_MN, X_MN, BACKWARD>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -248,10 +300,20 @@ cudaError_t launch_with(const CUtensorMap& w, const CUtensorMap& x, const SmallA
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_done[dev] = true;
   }
-  const unsigned tiles = static_cast<unsigned>((a.N + Cfg::BM - 1) / Cfg::BM);
+  const unsigned tiles = static_cast<unsigned>((a.N + Cfg::BM - 1) / Cfg::BM * a.row_tiles);
   PdlLaunch l(dim3(tiles * static_cast<unsigned>(a.split)), dim3(Cfg::THREADS), Cfg::SMEM_BYTES, stream);
   l.cluster(static_cast<unsigned>(a.split));
   return cudaLaunchKernelEx(&l.cfg, kern, w, x, a);
+}
+
+template <int NT>
+cudaError_t launch_rows(const CUtensorMap& w, const CUtensorMap& x, const SmallArgs& a, cudaStream_t stream) {
+  if (a.epi.backward) return launch_with<NT, true, false, true>(w, x, a, stream);
+  if (!a.w_mn) return launch_with<NT, false, false, false>(w, x, a, stream);
+  if constexpr (NT % kMnBox == 0)
+    return launch_with<NT, true, true, false>(w, x, a, stream);
+  else
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace
@@ -262,7 +324,7 @@ int linear_small_clusters(int split, int num_sms) {
   if (split < 1 || split > 8 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   if (cached[dev][split] > 0) return cached[dev][split];
   using Cfg = SmallCfg<16>;  // (the others differ by a few KB of shared memory)
-  auto kern = linear_small_kernel<16>;
+  auto kern = linear_small_kernel<16, false, false, false>;
   int n = 0;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES) == cudaSuccess) {
     PdlLaunch l(dim3(static_cast<unsigned>(num_sms / split * split)), dim3(Cfg::THREADS), Cfg::SMEM_BYTES, nullptr);
@@ -275,18 +337,18 @@ int linear_small_clusters(int split, int num_sms) {
   return n;
 }
 
-int linear_small_rows(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
-
 cudaError_t launch_linear_small(const CUtensorMap& w, const CUtensorMap& x, const SmallArgs& a, cudaStream_t stream) {
-  switch (linear_small_rows(a.M)) {
+  switch (a.tile_rows) {
     case 16:
-      return launch_with<16>(w, x, a, stream);
+      return launch_rows<16>(w, x, a, stream);
     case 32:
-      return launch_with<32>(w, x, a, stream);
+      return launch_rows<32>(w, x, a, stream);
     case 64:
-      return launch_with<64>(w, x, a, stream);
+      return launch_rows<64>(w, x, a, stream);
+    case 128:
+      return launch_rows<128>(w, x, a, stream);
     default:
-      return launch_with<128>(w, x, a, stream);
+      return cudaErrorInvalidValue;
   }
 }
 

@@ -244,27 +244,33 @@ constexpr int kLinearRows = 32;
 constexpr int kLinearFragmentRows = 8;  // always that kernel: one column fragment
 bool linear_rows_suits(const LinearProduct& p);
 cudaError_t launch_linear_rows(const LinearProduct& p, cudaStream_t stream);
-// The kernel for at most kLinearSmall rows of A, fed by TMA: w maps the
-// weights (128 × 64 boxes), x the rows of A (linear_small_rows(M) × 64).
+// The kernel for few rows or small outputs, fed by TMA: w maps the operand
+// whose rows are the output's N columns, x the one whose rows are its M rows,
+// in boxes of 128 × 64 and tile_rows × 64, or (stored with those contiguous)
+// of 64 × 64. Forward: both K-major, or both contiguous (w_mn: a weight's
+// gradient, tile_rows 64 or 128); backward: w contiguous, x K-major.
 constexpr int kLinearSmall = 128;
 struct SmallArgs {
   uint16_t* Y;
   int64_t ldy;
   int M, N, num_kb;
+  int tile_rows, row_tiles;  // 16, 32, 64 or 128 output rows per CTA
   int split;  // CTAs of a cluster, each a run of the K blocks: 1 to 8
+  int w_mn;
   int* status;
   unsigned long long timeout_ns;
   int inject;
   LinEpi epi;
 };
-int linear_small_rows(int64_t M);
+cudaError_t launch_linear_small(const CUtensorMap& w, const CUtensorMap& x, const SmallArgs& a, cudaStream_t stream);
 // How many clusters of `split` CTAs the device holds at once.
 int linear_small_clusters(int split, int num_sms);
 cudaError_t launch_linear_small(const CUtensorMap& w, const CUtensorMap& x, const SmallArgs& a, cudaStream_t stream);
 // The kernel for operands and outputs of any pitch and alignment; K > 0.
 cudaError_t launch_linear_any(const LinearProduct& p, const CallDevice& dev, cudaStream_t stream);
-// The gradient of a weight: C = A·B, or C + A·B, with an epilogue that says so.
-int run_wgrad(const LinearProduct& p, cudaStream_t stream);
+// The gradient of a weight: C = A·B, or C + A·B, with an epilogue that says
+// so. alone: no column sums follow that may run beside it.
+int run_wgrad(const LinearProduct& p, bool alone, cudaStream_t stream);
 
 struct NormArgs {
   const uint16_t* x;
