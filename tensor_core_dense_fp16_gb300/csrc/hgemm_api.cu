@@ -301,7 +301,9 @@ namespace hg {
 int call_device(CallDevice* out) {
   DeviceState* dev = nullptr;
   const int rc = current_device(&dev);
-  if (rc == HGEMM_OK) *out = CallDevice{dev->num_sms, t_ctx.status, g_timeout_ns.load(std::memory_order_relaxed)};
+  if (rc == HGEMM_OK)
+    *out = CallDevice{dev->num_sms, t_ctx.status, g_timeout_ns.load(std::memory_order_relaxed),
+                      g_inject.load(std::memory_order_relaxed)};
   return rc;
 }
 
@@ -818,7 +820,8 @@ int run_linear(const LinearProduct& p, cudaStream_t stream) {
   g.lin = &p.epi;
   g.early_split = true;
   if (p.K > 0 && (forced == HGEMM_PATH_GENERIC || !tma_ok(g))) {
-    const CallDevice cd{dev->num_sms, t_ctx.status, g_timeout_ns.load(std::memory_order_relaxed)};
+    const CallDevice cd{dev->num_sms, t_ctx.status, g_timeout_ns.load(std::memory_order_relaxed),
+                        g_inject.load(std::memory_order_relaxed)};
     return cuda_status(launch_linear_any(p, cd, stream));
   }
   return dispatch(g, kPlainEpilogue, *dev, stream);

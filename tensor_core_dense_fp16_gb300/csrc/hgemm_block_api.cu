@@ -81,7 +81,7 @@ int hgemm_linear_dgrad(const hgemm_half_t* dY, int64_t lddy, const hgemm_half_t*
                        int64_t K, cudaStream_t stream) {
   if (!dims_ok(M, N, K) || act < HGEMM_ACT_NONE || act > HGEMM_ACT_GELU_ERF || !codes != !scales)
     return HGEMM_ERR_INVALID_ARG;
-  if (!codes && (act != HGEMM_ACT_NONE || H)) return HGEMM_ERR_INVALID_ARG;
+  if (!codes && M > 0 && K > 0 && (act != HGEMM_ACT_NONE || H)) return HGEMM_ERR_INVALID_ARG;
   const Span dy = half_matrix(dY, M, N, lddy), w = half_matrix(W, N, K, ldw), du = half_matrix(dU, M, K, lddu);
   const Span h = H ? half_matrix(H, M, K, ldh) : kNone;
   const Span q = codes ? Span{codes, M, K, ldq, 1} : kNone;
@@ -187,7 +187,7 @@ int hgemm_layernorm_backward(const hgemm_half_t* dY, int64_t lddy, const hgemm_h
   a.mean = const_cast<float*>(mean), a.rstd = const_cast<float*>(rstd);
   a.dy = dY, a.lddy = lddy, a.res = R, a.ldr = ldr, a.dgamma = dgamma, a.dbeta = dbeta;
   a.work = static_cast<float*>(workspace), a.M = M, a.D = D;
-  a.status = dev.status, a.timeout_ns = dev.timeout_ns;
+  a.status = dev.status, a.timeout_ns = dev.timeout_ns, a.inject = dev.inject;
   return hg::cuda_status(hg::launch_layernorm_backward(a, dev.num_sms, stream));
 }
 

@@ -61,6 +61,7 @@ struct AnyArgs {
   int wide;  // the epilogue can read and write eight columns at a time
   int* status;
   unsigned long long timeout_ns;
+  int inject;  // HGEMM_INJECT_* (testing the watchdog)
 };
 
 // One operand: element (i, k) at p[i·ld + k], or p[k·ld + i] when mn.
@@ -333,7 +334,8 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1) linear_any_kernel(const An
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(full_bar(stage));
+        // (testing aid: one warp withholds one arrival)
+        if (lane == 0 && !(a.inject == 1 && warp == 0 && kb == 0 && t == blockIdx.x)) mbar_arrive(full_bar(stage));
         if (++stage == Cfg::STAGES) {
           stage = 0;
           phase ^= 1u;
@@ -508,6 +510,7 @@ cudaError_t launch_linear_any(const LinearProduct& p, const CallDevice& dev, cud
            rows(p.epi.codes, p.epi.ldq, 8);
   a.status = dev.status;
   a.timeout_ns = dev.timeout_ns;
+  a.inject = dev.inject;
   PdlLaunch l(dim3(static_cast<unsigned>(a.units < dev.num_sms ? a.units : dev.num_sms)), dim3(Cfg::THREADS),
               Cfg::SMEM_BYTES, stream);
   return cudaLaunchKernelEx(&l.cfg, kern, a);

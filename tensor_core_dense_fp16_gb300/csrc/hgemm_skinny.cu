@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(192, 1)
         }
       };
 #pragma unroll 1
-      for (int c64 = 0; EPI >= kEpiLinear && c64 < own_cols / 64; ++c64) {
+      for (int c64 = 0; EPI >= kEpiLinear && c64 < own_cols / 64 && x0 + c64 * 64 < p.N; ++c64) {
         f32x2 v[32];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {

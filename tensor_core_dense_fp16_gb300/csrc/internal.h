@@ -221,6 +221,7 @@ struct CallDevice {
   int num_sms;
   int* status;
   unsigned long long timeout_ns;
+  int inject;
 };
 int call_device(CallDevice* out);
 int cuda_status(cudaError_t e);
@@ -292,6 +293,7 @@ struct NormArgs {
   int64_t M, D;
   int* status;               // device watchdog word
   unsigned long long timeout_ns;
+  int inject;                // HGEMM_INJECT_* (testing the watchdog)
 };
 cudaError_t launch_layernorm_forward(const NormArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_layernorm_backward(const NormArgs& a, int num_sms, cudaStream_t stream);

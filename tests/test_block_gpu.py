@@ -402,3 +402,106 @@ def test_equal_calls_give_equal_bits_and_follow_their_stream():
             assert torch.equal(a, b)
     y, _, _, _ = ref.linear(src["x"].cpu().numpy(), src["w"].cpu().numpy(), None, "gelu", None)
     assert np.abs(results[0][0].numpy() - y).max() < 0.1
+
+
+PATHS = {"narrow": tc.HGEMM_PATH_TC_NARROW, "tile": tc.HGEMM_PATH_TC, "pair": tc.HGEMM_PATH_TC_PAIR,
+         "wide": tc.HGEMM_PATH_TC_WIDE, "split": tc.HGEMM_PATH_SKINNY, "any": tc.HGEMM_PATH_GENERIC}
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("M,N,K", [(300, 264, 520), (20, 1000, 1000), (700, 520, 1100)])
+def test_every_kernel_has_the_epilogues(path, M, N, K):
+    """The same products on each product kernel (a forced path that cannot
+    take one leaves it to another)."""
+    tc.hgemm_force_path(PATHS[path])
+    try:
+        run_linear(M, N, K, "gelu", keep=True)
+        run_linear(M, N, K, "silu", in_place=True)
+        run_dgrad(M, N, K, "gelu")
+        run_dgrad(M, N, K, None)
+        run_wgrad(M, N, K, accumulate=True)
+    finally:
+        tc.hgemm_force_path(-1)
+
+
+@pytest.mark.parametrize("M,N,K", [(9, 2048, 1024), (16, 1032, 2048), (40, 2051, 1000), (64, 264, 4096),
+                                   (100, 520, 4104), (128, 9800, 264)])
+def test_few_rows(M, N, K):
+    run_linear(M, N, K, "gelu_erf")
+    run_linear(M, N, K, "none", bias=False, in_place=True)
+    run_dgrad(M, K, N, "silu")
+    run_dgrad(M, K, N, None)
+
+
+@pytest.mark.parametrize("M,N,K", [(2048, 264, 136), (5000, 72, 520), (3000, 130, 128)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_small_weights_of_many_rows(M, N, K, accumulate):
+    run_wgrad(M, N, K, accumulate=accumulate)
+    run_wgrad(M, N, K, bias=False, accumulate=accumulate)
+
+
+def test_bias_gradient_beside_its_product():
+    """The column sums may run beside the product: what comes before the pair
+    of launches on the stream and what comes after keep their order."""
+    torch = torch_cuda()
+    M, N, K = 4096, 1024, 2048
+    rng = np.random.default_rng(12)
+    src = torch.from_numpy(rng_half(rng, (M, N))).cuda()
+    x = torch.from_numpy(rng_half(rng, (M, K))).cuda()
+    dy, dw, db = torch.empty_like(src), torch.empty((N, K), dtype=torch.float16, device="cuda"), torch.empty(N, device="cuda")
+    want = src.double().sum(dim=0)
+    first = None
+    for _ in range(20):
+        dy.fill_(float("nan"))
+        dw.fill_(float("nan"))
+        db.fill_(float("nan"))
+        dy.copy_(src)
+        tc.hgemm_linear_wgrad(dy, N, x, K, dw, K, db, False, M, N, K)
+        copies = dw.clone(), db.clone()
+        dy.zero_()
+        tc.hgemm_linear_wgrad(dy, N, x, K, dw, K, db, True, M, N, K)   # adds nothing
+        dy.fill_(1.0)
+        assert torch.equal(dw, copies[0]) and torch.equal(db, copies[1])
+        assert (copies[1].double() - want).abs().max() < 1e-3 * want.abs().max()
+        first = first or copies
+        assert torch.equal(first[0], copies[0]) and torch.equal(first[1], copies[1])
+    done()
+
+
+@pytest.mark.parametrize("what", ["pair", "narrow", "split", "few rows", "few rows back", "small weight", "any", "norm"])
+def test_withheld_arrival_times_out(what):
+    """Each kernel's waits are bounded: a withheld arrival ends in a timeout
+    the host reads, and the context computes on."""
+    torch = torch_cuda()
+    half = lambda *s: torch.ones(s, dtype=torch.float16, device="cuda")  # noqa: E731
+    y, w = half(2048, 512), half(512, 512)
+    db, ws = torch.empty(512, device="cuda"), torch.empty(tc.hgemm_layernorm_backward_workspace_size(64, 512),
+                                                        dtype=torch.uint8, device="cuda")
+    stats = torch.ones(64, device="cuda")
+    calls = {
+        "pair": lambda: tc.hgemm_linear(y, 512, w, 512, None, 2, None, 0, half(600, 512), 512, 600, 512, 512),
+        "few rows": lambda: tc.hgemm_linear(y, 512, half(8192, 512), 512, None, 2, None, 0, half(40, 8192), 8192, 40,
+                                            8192, 512),
+        "few rows back": lambda: tc.hgemm_linear_dgrad(y, 512, w, 512, None, 0, None, 0, 0, half(20, 512), 512, None, 0,
+                                                       20, 512, 512),
+        "small weight": lambda: tc.hgemm_linear_wgrad(y, 512, y, 512, half(512, 512), 512, None, False, 2048, 512, 512),
+        "any": lambda: tc.hgemm_linear(y, 511, w, 511, None, 2, None, 0, half(600, 512), 511, 600, 511, 511),
+        "norm": lambda: tc.hgemm_layernorm_backward(y, 512, y, 512, w, stats, stats, None, 0, half(64, 512), 512, db,
+                                                    torch.empty(512, device="cuda"), ws, 64, 512),
+    }
+    calls["narrow"] = calls["split"] = calls["pair"]
+    done()
+    tc.hgemm_set_wait_timeout(20_000_000)
+    tc.hgemm_debug_inject(tc.HGEMM_INJECT_DROP_ARRIVAL)
+    if what in ("pair", "narrow", "split"):
+        tc.hgemm_force_path(PATHS[what])
+    try:
+        calls[what]()
+        assert tc.hgemm_device_status() == tc.HGEMM_ERR_TIMEOUT
+        assert tc.hgemm_device_status() == tc.HGEMM_OK
+    finally:
+        tc.hgemm_debug_inject(tc.HGEMM_INJECT_NONE)
+        tc.hgemm_set_wait_timeout(0)
+        tc.hgemm_force_path(-1)
+    run_linear(300, 264, 520, "gelu", keep=True)
+    run_layernorm(40, 512)
