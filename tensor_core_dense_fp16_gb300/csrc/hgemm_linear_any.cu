@@ -415,10 +415,13 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1) linear_any_kernel(const An
         if (a.wide) {
           // aligned rows: the tensor-map kernels' epilogue, eight lanes
           // writing a row of the box
+          constexpr int EPI = BACKWARD ? kEpiLinearGrad : kEpiLinear;
           f32x2 v[32];
           tmem_row64(t_group, v);
           __syncwarp();
-          lin_row64<BACKWARD ? kEpiLinearGrad : kEpiLinear>(box + lane * 128, lane, v, e, p.M, p.N, gi, col0);
+          LinSide<EPI> side;
+          lin_fetch<EPI>(side, e, p.M, p.N, gi, col0);
+          lin_row64<EPI>(box + lane * 128, lane, v, side, e, p.M, p.N, gi, col0);
           __syncwarp();
           const int64_t n = col0 + 8 * (lane & 7);
 #pragma unroll

@@ -282,6 +282,12 @@ __global__ void __launch_bounds__(192, 1)
   if (EPI == kEpiFused && warp >= 2)
     prefetch_c_row(p.epi, p.C, p.M, p.N, p.ldc, static_cast<int64_t>(mb) * Cfg::BM + half * Cfg::ROWS + row,
                    static_cast<int64_t>(nb) * Cfg::BN + own_c0, own_cols);
+  [[maybe_unused]] LinSide<EPI> side;  // of the first 64 of this CTA's columns
+  if constexpr (EPI >= kEpiLinear) {
+    if (warp >= 2)
+      lin_fetch<EPI>(side, p.lin, p.M, p.N, static_cast<int64_t>(mb) * Cfg::BM + half * Cfg::ROWS + row,
+                     static_cast<int64_t>(nb) * Cfg::BN + own_c0);
+  }
   // ring layout for the exchange: receive slots first, then send staging
   const uint32_t recv_base = sbase;
   const uint32_t send_base = sbase + static_cast<uint32_t>((SPLIT - 1) * Cfg::ROWS * own_cols * 4);
@@ -376,9 +382,11 @@ __global__ void __launch_bounds__(192, 1)
 #pragma unroll
           for (int k = 0; k < 16; ++k) v[16 * i + k] = pair_of(a[2 * k], a[2 * k + 1]);
         }
-        if constexpr (EPI >= kEpiLinear)
-          lin_row64<EPI>(cbuf + c64 * (kEpiRows * 128) + lane * 128, lane, v, p.lin, p.M, p.N,
+        if constexpr (EPI >= kEpiLinear) {
+          if (c64 > 0) lin_fetch<EPI>(side, p.lin, p.M, p.N, static_cast<int64_t>(y0) + lane, x0 + c64 * 64);
+          lin_row64<EPI>(cbuf + c64 * (kEpiRows * 128) + lane * 128, lane, v, side, p.lin, p.M, p.N,
                          static_cast<int64_t>(y0) + lane, x0 + c64 * 64);
+        }
       }
 #pragma unroll 1
       for (int c32 = 0; EPI < kEpiLinear && c32 < own_cols / 32; ++c32) {

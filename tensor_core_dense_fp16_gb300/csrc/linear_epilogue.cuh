@@ -63,8 +63,7 @@ __device__ __forceinline__ void activate(f32x2 u, f32x2& f, f32x2& df) {
     const f32x2 s = pair_of(rcp_approx(a), rcp_approx(b));
     f = mul2(u, s);
     if constexpr (GRAD) {
-      const f32x2 minus_f = mul2(u, mul2(s, pair_of(-1.f)));
-      const f32x2 w = fma2(minus_f, s, f);  // u·σ·(1 − σ)
+      const f32x2 w = fma2(f, mul2(s, pair_of(-1.f)), f);  // u·σ·(1 − σ)
       if constexpr (ACT == HGEMM_ACT_GELU)
         df = fma2(w, fma2(u2, pair_of(6.f * kGeluZ * kGeluC), pair_of(2.f * kGeluZ)), s);
       else
@@ -271,18 +270,65 @@ __device__ __forceinline__ void tmem_row64(uint32_t taddr, f32x2 (&v)[32]) {
   }
 }
 
+// What the epilogue of a row's 64 columns reads besides the accumulator:
+// fetched ahead of it, so that the reads wait while the product does.
+template <int EPI>
+struct LinSide {
+  uint4 bias[EPI == kEpiLinear ? 8 : 1];
+  uint4 side[EPI == kEpiLinear ? 8 : 4];  // residual, or codes
+  float scale;
+};
+
+template <int EPI>
+__device__ __forceinline__ void lin_fetch(LinSide<EPI>& s, const LinEpi& e, int64_t M, int64_t N, int64_t grow,
+                                          int64_t x0) {
+  const bool in_m = grow < M;
+  if constexpr (EPI == kEpiLinear) {
+    if (e.bias) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s.bias[j] = load_bias8(e.bias, x0 + 8 * j, N);
+    }
+    if (e.res) {
+      const uint16_t* r = e.res + grow * e.ldr + x0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        s.side[j] = in_m && x0 + 8 * j < N ? *reinterpret_cast<const uint4*>(r + 8 * j) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  } else if (e.codes) {
+    const int8_t* q = e.codes + grow * e.ldq + x0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s.side[j] = make_uint4(0u, 0u, 0u, 0u);
+    s.scale = 0.f;
+    if (in_m && x0 < N) {
+      if (x0 + 64 <= N && (reinterpret_cast<uintptr_t>(q) & 15u) == 0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s.side[j] = reinterpret_cast<const uint4*>(q)[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint2 a = make_uint2(0u, 0u), b = a;
+          if (x0 + 16 * j < N) a = reinterpret_cast<const uint2*>(q)[2 * j];
+          if (x0 + 16 * j + 8 < N) b = reinterpret_cast<const uint2*>(q)[2 * j + 1];
+          s.side[j] = make_uint4(a.x, a.y, b.x, b.y);
+        }
+      }
+      s.scale = e.scales[x0 / kCkptGroup * e.lds + grow];
+    }
+  }
+}
+
 // Row `lane` of a staged 32×64 box, columns x0 .. x0+63 (one 8-bit group) of
 // row `grow`: its 64 accumulators v through the epilogue into the
 // 128-byte-swizzled staging row, as stage_row64 does. N, the pitches and x0
 // are multiples of 8, so eight columns are inside the matrix or none.
 template <int EPI>
-__device__ __forceinline__ void lin_row64(uint8_t* row, int lane, f32x2 (&v)[32], const LinEpi& e, int64_t M,
-                                          int64_t N, int64_t grow, int64_t x0) {
+__device__ __forceinline__ void lin_row64(uint8_t* row, int lane, f32x2 (&v)[32], const LinSide<EPI>& s,
+                                          const LinEpi& e, int64_t M, int64_t N, int64_t grow, int64_t x0) {
   const bool in_m = grow < M;
   if constexpr (EPI == kEpiLinear) {
     if (e.bias) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) add8(v + 4 * j, load_bias8(e.bias, x0 + 8 * j, N));
+      for (int j = 0; j < 8; ++j) add8(v + 4 * j, s.bias[j]);
     }
     if (e.codes) {
       // (columns past N hold 0: zero-filled operands and no bias)
@@ -320,46 +366,20 @@ __device__ __forceinline__ void lin_row64(uint8_t* row, int lane, f32x2 (&v)[32]
         v[i] = f;
       }
     });
-    if (e.res && in_m) {
-      const uint16_t* r = e.res + grow * e.ldr + x0;
-      uint4 r8[8];
+    if (e.res) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        r8[j] = x0 + 8 * j < N ? *reinterpret_cast<const uint4*>(r + 8 * j) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) add8(v + 4 * j, r8[j]);
+      for (int j = 0; j < 8; ++j) add8(v + 4 * j, s.side[j]);
     }
   } else if (e.codes) {
-    uint32_t w[16];
-    float scale = 0.f;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) w[j] = 0u;
-    if (in_m) {
-      const int8_t* q = e.codes + grow * e.ldq + x0;
-      if (x0 + 64 <= N && (reinterpret_cast<uintptr_t>(q) & 15u) == 0) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint4 t = reinterpret_cast<const uint4*>(q)[j];
-          w[4 * j] = t.x, w[4 * j + 1] = t.y, w[4 * j + 2] = t.z, w[4 * j + 3] = t.w;
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (x0 + 8 * j < N) {
-            const uint2 t = reinterpret_cast<const uint2*>(q)[j];
-            w[2 * j] = t.x, w[2 * j + 1] = t.y;
-          }
-      }
-      scale = e.scales[x0 / kCkptGroup * e.lds + grow];
-    }
     uint16_t* h = e.h + grow * e.ldh + x0;
     with_activation(e.act, [&](auto a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
+        const uint32_t w[2] = {j & 1 ? s.side[j / 2].z : s.side[j / 2].x, j & 1 ? s.side[j / 2].w : s.side[j / 2].y};
         f32x2 f[4], df;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const f32x2 u = mul2(ckpt_pair(w[2 * j + i / 2] ^ 0x80808080u, i & 1), pair_of(scale));
+          const f32x2 u = mul2(ckpt_pair(w[i / 2] ^ 0x80808080u, i & 1), pair_of(s.scale));
           activate<decltype(a)::value, true>(u, f[i], df);
           v[4 * j + i] = mul2(v[4 * j + i], df);
         }
