@@ -255,13 +255,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * epi_warps(
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------- MMA issuer (even CTA)
-    // The whole warp walks the loop and one lane issues: what the issue needs
-    // (descriptors, barrier addresses) then stays in uniform registers. The
-    // issue of a stage takes a large part of the stage's MMA time, so with
-    // epilogue warps beside it every instruction less shows (8192×8192
-    // outputs, contraction 2048, GELU: 188 us, 180 with this).
-    if (rank == 0) {
-      const uint32_t on = lane == 0 ? 1u : 0u;
+    // The issue of a stage takes a large part of the stage's MMA time, so what
+    // does not change is kept outside the loop: the descriptors of stage 0 by
+    // operand order, to which a stage adds its offset (8192×8192 outputs,
+    // contraction 2048, GELU and codes: 173 us with descriptors built per
+    // stage or a whole warp in the loop, 166 with these).
+    if (rank == 0 && lane == 0) {
       // K-major: 16 K elements are 32 bytes along the row; MN-major: 16 K
       // rows of 128 bytes
       const uint64_t a_base = p.a_mn ? sdesc_mnmajor_sw128(sA) : sdesc_kmajor_sw128(sA);
@@ -277,20 +276,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * epi_warps(
         const uint32_t idesc = (t < p.full_tiles ? Cfg::IDESC : idesc_f16_f32acc(Cfg::BM, p.part_cols)) |
                                idesc_major_bits(p.a_mn != 0, p.b_mn != 0);
         ok = wait_phase_cluster(acce_bar(acc), acc_phase ^ 1u, wd, kWdMmaAccEmpty);
-        if (!__all_sync(0xffffffffu, ok)) break;
+        if (!ok) break;
         tc_fence_after_sync();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * Cfg::ACC_COLS);
         for (int kb = 0; kb < p.num_kb; ++kb) {
-          ok = __all_sync(0xffffffffu, wait_phase(full_bar(stage), phase, wd, kWdMmaFull));
+          ok = wait_phase(full_bar(stage), phase, wd, kWdMmaFull);
           if (!ok) break;
           tc_fence_after_sync();
 #pragma unroll
           for (int k = 0; k < Cfg::BK / Cfg::UMMA_K; ++k)
             // kb counts the tile's K steps in load order (the producer may walk
             // K backwards); the first step overwrites the accumulator
-            mma_f16_ss_cg2_if(on, d_tmem, a_base + offset + a_step * k, b_base + offset + b_step * k, idesc,
-                              (kb > 0 || k > 0) ? 1u : 0u);
-          mma_commit_cg2_multicast_if(on, empty_bar(stage), 0x3);  // frees the stage in both CTAs
+            mma_f16_ss_cg2(d_tmem, a_base + offset + a_step * k, b_base + offset + b_step * k, idesc,
+                           (kb > 0 || k > 0) ? 1u : 0u);
+          mma_commit_cg2_multicast(empty_bar(stage), 0x3);  // frees the stage in both CTAs
           offset += stage_bytes >> 4;
           if (++stage == STAGES) {
             stage = 0;
@@ -299,11 +298,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * epi_warps(
           }
         }
         if (!ok) break;
-        mma_commit_cg2_multicast_if(on, accf_bar(acc), 0x3);  // both TMEM halves complete
+        mma_commit_cg2_multicast(accf_bar(acc), 0x3);  // both TMEM halves complete
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       }
-      mma_commit_cg2_multicast_if(on, drain_bar, 0x1);
+      mma_commit_cg2_multicast(drain_bar, 0x1);
       wait_drain(drain_bar, 0, wd);
     }
     __syncwarp();

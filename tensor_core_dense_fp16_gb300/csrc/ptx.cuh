@@ -467,28 +467,6 @@ __device__ __forceinline__ void mma_f16_ss_cg2(uint32_t d_tmem, uint64_t a_desc,
       : "memory");
 }
 
-// The same, executed by a whole warp with `on` set in one lane: the warp
-// stays converged, so that the descriptors stay in uniform registers.
-__device__ __forceinline__ void mma_f16_ss_cg2_if(uint32_t on, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                                  uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(on)
-      : "memory");
-}
-__device__ __forceinline__ void mma_commit_cg2_multicast_if(uint32_t on, uint32_t bar, uint16_t cta_mask) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.b32 q, %2, 0;\n\t"
-      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;\n\t}" ::"r"(bar),
-      "h"(cta_mask), "r"(on)
-      : "memory");
-}
-
 // Arrives once on the barrier at offset `bar` in every CTA of `cta_mask`
 // when all prior pair MMAs of this thread have completed.
 __device__ __forceinline__ void mma_commit_cg2_multicast(uint32_t bar, uint16_t cta_mask) {
