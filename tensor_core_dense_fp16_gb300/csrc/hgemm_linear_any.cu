@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1) linear_any_kernel(const An
     }
   } else if (warp == Cfg::MMA_WARP) {
     // -------------------------------------------------------- MMA issuer
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t idesc = Cfg::IDESC | idesc_major_bits(p.a_mn, p.b_mn);
       const uint32_t a_step = p.a_mn ? 128u : 2u, b_step = p.b_mn ? 128u : 2u;
       int stage = 0;

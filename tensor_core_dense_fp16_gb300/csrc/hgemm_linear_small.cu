@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(192, 1)
   float* part = reinterpret_cast<float*>(smem);  // [row of X][feature]
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       int stage = 0;
       uint32_t phase = 0;
       int issued = 0;
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(192, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;

@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(192, 1)
   int ok = 1;
   if (warp == 0) {
     // ------------------------------------------------ TMA producer (all CTAs)
-    if (lane == 0) {
+    if (elect_one()) {
       int stage = 0;
       uint32_t phase = 0;
       long long issued = 0;
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(192, 1)
     __syncwarp();
   } else if (warp == 1) {
     // --------------------------------------------- MMA issuer (even CTAs)
-    if (rank == leader && lane == 0) {
+    if (rank == leader && elect_one()) {
       int stage = 0;
       uint32_t phase = 0;
       bool good = true;

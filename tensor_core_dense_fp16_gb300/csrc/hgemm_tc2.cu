@@ -187,7 +187,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * epi_warps(
 
   if (warp == 0) {
     // ------------------------------------------------ TMA producer (both CTAs)
-    if (lane == 0) {
+    if (elect_one()) {
       int stage = 0;
       uint32_t phase = 0;
       long long issued = 0;
@@ -260,7 +260,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * epi_warps(
     // operand order, to which a stage adds its offset (8192×8192 outputs,
     // contraction 2048, GELU and codes: 173 us with descriptors built per
     // stage or a whole warp in the loop, 166 with these).
-    if (rank == 0 && lane == 0) {
+    if (rank == 0 && elect_one()) {
       // K-major: 16 K elements are 32 bytes along the row; MN-major: 16 K
       // rows of 128 bytes
       const uint64_t a_base = p.a_mn ? sdesc_mnmajor_sw128(sA) : sdesc_kmajor_sw128(sA);

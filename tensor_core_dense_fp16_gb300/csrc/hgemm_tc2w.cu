@@ -134,7 +134,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
 
   if (warp == 0) {
     // ------------------------------------------------ TMA producer (both CTAs)
-    if (lane == 0) {
+    if (elect_one()) {
       int stage = 0;
       uint32_t phase = 0;
       long long issued = 0;
@@ -201,7 +201,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------- MMA issuer (even CTA)
-    if (rank == 0 && lane == 0) {
+    if (rank == 0 && elect_one()) {
       int stage = 0;
       uint32_t phase = 0;
       uint32_t tile_phase = 0;  // parity of this CTA's tile count

