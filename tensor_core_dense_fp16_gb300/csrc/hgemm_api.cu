@@ -75,7 +75,7 @@ cudaError_t debug_words(int* (&out)[hg::kDebugWords]) {
                                                       hg::debug_word_trileaf, hg::debug_word_chain,
                                                       hg::debug_word_linear,  hg::debug_word_norm,
                                                       hg::debug_word_ckpt8,   hg::debug_word_linear_any,
-                                                      hg::debug_word_linear_small};
+                                                      hg::debug_word_linear_small, hg::debug_word_linear_cluster};
   for (int i = 0; i < hg::kDebugWords; ++i) {
     const cudaError_t e = get[i](&out[i]);
     if (e != cudaSuccess) return e;
@@ -124,9 +124,6 @@ struct Gemm {
   int64_t ld_src = 0;
   // a linear layer's epilogue instead of EpiArgs (null: none)
   const hg::LinEpi* lin = nullptr;
-  // an M- or N-contiguous product splits K from 8 blocks on where the pair
-  // kernel's tiles would leave most pairs idle
-  bool early_split = false;
   hg::Epilogue kind(const hg::EpiArgs& epi) const {
     if (lin) return lin->backward ? hg::kEpiLinearGrad : hg::kEpiLinear;
     return epi.mode != 0 ? hg::kEpiFused : hg::kEpiPlain;
@@ -278,13 +275,6 @@ int choose_path(const Gemm& g, const hg::DeviceProfile& prof, bool fused, int* s
   if (forced == HGEMM_PATH_GENERIC || !tma) return HGEMM_PATH_GENERIC;
   const int fs = g_forced_split.load(std::memory_order_relaxed);
   const int path = hg::choose_tma_path(M, N, K, prof, forced, fs >> 10, fs & 1023, fused, split, tile_n);
-  // Gradients of linear layers: such operands have no 128×64 tiles, and the
-  // pair kernel keeps 128 columns of a tile, so few tiles leave most pairs
-  // idle unless K is split (1000^3: 9.4 to 7.7 us; 2000×1000, contraction
-  // 1000, 32 tiles: 9.6 to 10.8).
-  if (g.early_split && (g.a_mn || g.b_mn) && forced < 0 && path != HGEMM_PATH_SKINNY && K >= 8 * hg::kTcBK &&
-      4 * ((M + 255) / 256) * ((N + 255) / 256) <= prof.pair_clusters)
-    return hg::choose_tma_path(M, N, K, prof, HGEMM_PATH_SKINNY, fs >> 10, fs & 1023, fused, split, tile_n);
   // M- or N-contiguous operands: the wide, pair and split-K kernels read
   // them as MN-major tiles; the single-CTA kernel takes K-major ones only
   if ((g.a_mn || g.b_mn) && (path == HGEMM_PATH_TC || path == HGEMM_PATH_TC_NARROW))
@@ -807,6 +797,41 @@ int run_linear_small(const LinearProduct& p, const DeviceState& dev, cudaStream_
   return cuda_status(launch_linear_small(mw, mx, a, stream));
 }
 
+// Whether p is one wave of clusters of four 128×64 tiles.
+bool linear_cluster_suits(const LinearProduct& p, int num_sms) {
+  if (p.M == 0 || p.N == 0 || p.K == 0) return false;
+  const int64_t clusters = (p.M + 2 * kTcBM - 1) / (2 * kTcBM) * ((p.N + 2 * kNarrowBN - 1) / (2 * kNarrowBN));
+  return clusters <= linear_cluster_max(num_sms);
+}
+
+int run_linear_cluster(const LinearProduct& p, const DeviceState& dev, cudaStream_t stream) {
+  CUtensorMap ma, mb, mc;
+  int rc;
+  // halves of tiles: 64 rows of A by 64 of K, or the other way around; 32 rows
+  // of B, or 64 of its columns by 32 of K
+  rc = p.a_mn ? encode_map(&ma, p.A, p.K, p.M, p.lda, kTcBK, 64) : encode_map(&ma, p.A, p.M, p.K, p.lda, kTcBM / 2, kTcBK);
+  if (rc != HGEMM_OK) return rc;
+  rc = p.b_mn ? encode_map(&mb, p.B, p.K, p.N, p.ldb, kTcBK / 2, 64)
+              : encode_map(&mb, p.B, p.N, p.K, p.ldb, kNarrowBN / 2, kTcBK);
+  if (rc != HGEMM_OK) return rc;
+  if ((rc = encode_map(&mc, p.C, p.M, p.N, p.ldc, kEpiRows, kEpiCols)) != HGEMM_OK) return rc;
+  TcArgs args{};
+  args.M = static_cast<int>(p.M);
+  args.N = static_cast<int>(p.N);
+  args.K = static_cast<int>(p.K);
+  args.num_m = static_cast<int>((p.M + kTcBM - 1) / kTcBM);
+  args.num_n = static_cast<int>((p.N + kNarrowBN - 1) / kNarrowBN);
+  args.num_kb = static_cast<int>((p.K + kTcBK - 1) / kTcBK);
+  args.grid = 4 * ((args.num_m + 1) / 2) * ((args.num_n + 1) / 2);
+  args.a_mn = p.a_mn ? 1 : 0;
+  args.b_mn = p.b_mn ? 1 : 0;
+  args.status = t_ctx.status;
+  args.timeout_ns = g_timeout_ns.load(std::memory_order_relaxed);
+  args.inject = g_inject.load(std::memory_order_relaxed);
+  args.lin = p.epi;
+  return cuda_status(launch_linear_cluster(ma, mb, mc, args, p.epi.backward ? kEpiLinearGrad : kEpiLinear, stream));
+}
+
 int run_linear(const LinearProduct& p, cudaStream_t stream) {
   DeviceState* dev = nullptr;
   const int rc = current_device(&dev);
@@ -818,16 +843,16 @@ int run_linear(const LinearProduct& p, cudaStream_t stream) {
   g.a_mn = p.a_mn;
   g.b_mn = p.b_mn;
   g.lin = &p.epi;
-  g.early_split = true;
   if (p.K > 0 && (forced == HGEMM_PATH_GENERIC || !tma_ok(g))) {
     const CallDevice cd{dev->num_sms, t_ctx.status, g_timeout_ns.load(std::memory_order_relaxed),
                         g_inject.load(std::memory_order_relaxed)};
     return cuda_status(launch_linear_any(p, cd, stream));
   }
+  if (forced < 0 && linear_cluster_suits(p, dev->num_sms)) return run_linear_cluster(p, *dev, stream);
   return dispatch(g, kPlainEpilogue, *dev, stream);
 }
 
-int run_wgrad(const LinearProduct& p, bool alone, cudaStream_t stream) {
+int run_wgrad(const LinearProduct& p, cudaStream_t stream) {
   Gemm g{p.A, p.B, p.C, p.M, p.N, p.K, p.lda, p.ldb, p.ldc};
   g.a_mn = p.a_mn;
   g.b_mn = p.b_mn;
@@ -836,10 +861,8 @@ int run_wgrad(const LinearProduct& p, bool alone, cudaStream_t stream) {
   DeviceState* dev = nullptr;
   const int rc = current_device(&dev);
   if (rc != HGEMM_OK) return rc;
-  // (beside the bias gradient's launch the SMs that a split would take serve
-  // the column sums: 1000^3 with bias 12.6 us split, 11.1 not)
-  g.early_split = alone;
   if (forced < 0 && linear_small_suits(p, dev->num_sms)) return run_linear_small(p, *dev, stream);
+  if (forced < 0 && linear_cluster_suits(p, dev->num_sms)) return run_linear_cluster(p, *dev, stream);
   // (the plain and the accumulating product; the sum of an old value is the residual's)
   EpiArgs epi = kPlainEpilogue;
   if (p.epi.res) {

@@ -226,6 +226,12 @@ struct CallDevice {
 int call_device(CallDevice* out);
 int cuda_status(cudaError_t e);
 
+// One wave of 128×64 tiles in clusters of four, and how many clusters the
+// device holds at once (args.grid: 4 per 256×128 outputs).
+cudaError_t launch_linear_cluster(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const TcArgs& args,
+                                  Epilogue kind, cudaStream_t stream);
+int linear_cluster_max(int num_sms);
+
 // One product with a linear layer's epilogue, C (M×N) = epilogue(A·B) with A
 // M×K, or K×M when a_mn, and B N×K, or K×N when b_mn.
 struct LinearProduct {
@@ -270,8 +276,8 @@ cudaError_t launch_linear_small(const CUtensorMap& w, const CUtensorMap& x, cons
 // The kernel for operands and outputs of any pitch and alignment; K > 0.
 cudaError_t launch_linear_any(const LinearProduct& p, const CallDevice& dev, cudaStream_t stream);
 // The gradient of a weight: C = A·B, or C + A·B, with an epilogue that says
-// so. alone: no column sums follow that may run beside it.
-int run_wgrad(const LinearProduct& p, bool alone, cudaStream_t stream);
+// so.
+int run_wgrad(const LinearProduct& p, cudaStream_t stream);
 
 struct NormArgs {
   const uint16_t* x;
@@ -323,7 +329,8 @@ cudaError_t debug_word_norm(int** out);
 cudaError_t debug_word_ckpt8(int** out);
 cudaError_t debug_word_linear_any(int** out);
 cudaError_t debug_word_linear_small(int** out);
-constexpr int kDebugWords = 13;
+cudaError_t debug_word_linear_cluster(int** out);
+constexpr int kDebugWords = 14;
 
 // Co-residency limits of the cluster kernels on one device, measured once
 // (or nominal GB300 figures when no device has been queried).

@@ -433,6 +433,19 @@ def test_few_rows(M, N, K):
     run_dgrad(M, K, N, None)
 
 
+@pytest.mark.parametrize("M,N,K", [(129, 264, 136), (300, 72, 520), (257, 1032, 1000), (1000, 520, 1100), (640, 8, 64),
+                                   (384, 328, 4104)])
+def test_one_wave_of_clusters(M, N, K):
+    """Odd numbers of 128×64 tiles either way, outputs that end inside one,
+    contractions shorter and longer than the ring."""
+    run_linear(M, N, K, "silu", keep=True)
+    run_linear(M, N, K, "gelu", in_place=True)
+    run_dgrad(M, K, N, "gelu")
+    run_dgrad(M, K, N, None)
+    run_wgrad(K, M, N, accumulate=True)
+    run_wgrad(K, M, N, bias=False)
+
+
 @pytest.mark.parametrize("M,N,K", [(2048, 264, 136), (5000, 72, 520), (3000, 130, 128)])
 @pytest.mark.parametrize("accumulate", [False, True])
 def test_small_weights_of_many_rows(M, N, K, accumulate):
@@ -468,7 +481,8 @@ def test_bias_gradient_beside_its_product():
     done()
 
 
-@pytest.mark.parametrize("what", ["pair", "narrow", "split", "few rows", "few rows back", "small weight", "any", "norm"])
+@pytest.mark.parametrize("what", ["pair", "narrow", "split", "few rows", "few rows back", "small weight", "clusters",
+                                  "any", "norm"])
 def test_withheld_arrival_times_out(what):
     """Each kernel's waits are bounded: a withheld arrival ends in a timeout
     the host reads, and the context computes on."""
@@ -485,6 +499,8 @@ def test_withheld_arrival_times_out(what):
         "few rows back": lambda: tc.hgemm_linear_dgrad(y, 512, w, 512, None, 0, None, 0, 0, half(20, 512), 512, None, 0,
                                                        20, 512, 512),
         "small weight": lambda: tc.hgemm_linear_wgrad(y, 512, y, 512, half(512, 512), 512, None, False, 2048, 512, 512),
+        "clusters": lambda: tc.hgemm_linear_dgrad(y, 512, w, 512, None, 0, None, 0, 0, half(600, 512), 512, None, 0, 600,
+                                                  512, 512),
         "any": lambda: tc.hgemm_linear(y, 511, w, 511, None, 2, None, 0, half(600, 512), 511, 600, 511, 511),
         "norm": lambda: tc.hgemm_layernorm_backward(y, 512, y, 512, w, stats, stats, None, 0, half(64, 512), 512, db,
                                                     torch.empty(512, device="cuda"), ws, 64, 512),
