@@ -101,10 +101,11 @@ __device__ __forceinline__ uint32_t f32_block_offset(int r, int c, int cols) {
   return static_cast<uint32_t>(r * cols * 4 + ((c ^ (r & 7)) << 4));
 }
 
-template <int SPLIT, int BN, int EPI>
+template <int SPLIT, int BN, int EPI, Layout LAYOUT>
 __global__ void __launch_bounds__(192, 1)
     hgemm_skinny_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                         const __grid_constant__ CUtensorMap tmC, const TcArgs p) {
+  const bool a_mn = layout_a_mn(LAYOUT, p.a_mn), b_mn = layout_b_mn(LAYOUT, p.b_mn);
   using Cfg = SkCfg<SPLIT, BN>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -184,14 +185,14 @@ __global__ void __launch_bounds__(192, 1)
         const uint32_t fb = mapa_shared(full_bar(stage), leader);
         if (rank == leader && !(p.inject == 1 && issued == 0))  // testing aid: withhold one arrival
           mbar_arrive_expect_tx(full_bar(stage), Cfg::TX_BYTES);
-        if (p.a_mn) {
+        if (a_mn) {
           // A stored K×M: the CTA's 128 rows as two 64-row boxes, 8 KB apart
           tma_load_2d_cg2(sA + stage * Cfg::A_BYTES, &tmA, fb, ya, kb * Cfg::BK);
           tma_load_2d_cg2(sA + stage * Cfg::A_BYTES + kMnBoxBytes, &tmA, fb, ya + kMnBox, kb * Cfg::BK);
         } else {
           tma_load_2d_cg2(sA + stage * Cfg::A_BYTES, &tmA, fb, kb * Cfg::BK, ya);
         }
-        if (p.b_mn) {
+        if (b_mn) {
           // B stored K×N: the CTA's BROWS columns as 64-column boxes, 8 KB apart
 #pragma unroll
           for (int bx = 0; bx < Cfg::BROWS; bx += kMnBox)
@@ -236,12 +237,12 @@ __global__ void __launch_bounds__(192, 1)
         tc_fence_after_sync();
         // K-major: 16 K elements are 32 bytes along the row; MN-major: 16 K
         // rows of 128 bytes
-        const uint64_t a_desc = p.a_mn ? sdesc_mnmajor_sw128(sA + stage * Cfg::A_BYTES)
+        const uint64_t a_desc = a_mn ? sdesc_mnmajor_sw128(sA + stage * Cfg::A_BYTES)
                                        : sdesc_kmajor_sw128(sA + stage * Cfg::A_BYTES);
-        const uint64_t b_desc = p.b_mn ? sdesc_mnmajor_sw128(sB + stage * Cfg::B_BYTES)
+        const uint64_t b_desc = b_mn ? sdesc_mnmajor_sw128(sB + stage * Cfg::B_BYTES)
                                        : sdesc_kmajor_sw128(sB + stage * Cfg::B_BYTES);
-        const uint32_t a_step = p.a_mn ? 128u : 2u, b_step = p.b_mn ? 128u : 2u;
-        const uint32_t idesc = Cfg::IDESC | idesc_major_bits(p.a_mn != 0, p.b_mn != 0);
+        const uint32_t a_step = a_mn ? 128u : 2u, b_step = b_mn ? 128u : 2u;
+        const uint32_t idesc = Cfg::IDESC | idesc_major_bits(a_mn, b_mn);
 #pragma unroll
         for (int k = 0; k < Cfg::BK / Cfg::UMMA_K; ++k)
           mma_f16_ss_cg2(tmem_base, a_desc + a_step * k, b_desc + b_step * k, idesc,
@@ -445,18 +446,25 @@ template <int SPLIT, int BN>
 cudaError_t launch_split(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c,
                          const TcArgs& args, Epilogue kind, cudaStream_t stream) {
   using Cfg = SkCfg<SPLIT, BN>;
-  static std::atomic<bool> attr_done[4][64];
-  auto kern = kind == kEpiPlain    ? hgemm_skinny_kernel<SPLIT, BN, kEpiPlain>
-              : kind == kEpiFused  ? hgemm_skinny_kernel<SPLIT, BN, kEpiFused>
-              : kind == kEpiLinear ? hgemm_skinny_kernel<SPLIT, BN, kEpiLinear>
-                                   : hgemm_skinny_kernel<SPLIT, BN, kEpiLinearGrad>;
+  static std::atomic<bool> attr_done[6][64];
+  const bool mn = args.a_mn || args.b_mn;
+  if ((kind == kEpiLinear && mn) || (kind == kEpiLinearGrad && (args.a_mn || !args.b_mn))) return cudaErrorInvalidValue;
+  using Kern = decltype(&hgemm_skinny_kernel<SPLIT, BN, kEpiPlain, kLayoutK>);
+  const Kern kerns[6] = {hgemm_skinny_kernel<SPLIT, BN, kEpiPlain, kLayoutK>,
+                         hgemm_skinny_kernel<SPLIT, BN, kEpiPlain, kLayoutAny>,
+                         hgemm_skinny_kernel<SPLIT, BN, kEpiFused, kLayoutK>,
+                         hgemm_skinny_kernel<SPLIT, BN, kEpiFused, kLayoutAny>,
+                         hgemm_skinny_kernel<SPLIT, BN, kEpiLinear, kLayoutK>,
+                         hgemm_skinny_kernel<SPLIT, BN, kEpiLinearGrad, kLayoutBn>};
+  const int which = kind == kEpiLinear ? 4 : kind == kEpiLinearGrad ? 5 : (kind == kEpiFused ? 2 : 0) + (mn ? 1 : 0);
+  const Kern kern = kerns[which];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || !attr_done[kind][dev]) {
+  if (dev < 0 || dev >= 64 || !attr_done[which][dev]) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) attr_done[kind][dev] = true;
+    if (dev >= 0 && dev < 64) attr_done[which][dev] = true;
   }
   PdlLaunch l(dim3(static_cast<unsigned>(args.num_tiles * 2 * SPLIT)), dim3(Cfg::THREADS), Cfg::SMEM_BYTES,
               stream);
@@ -467,7 +475,7 @@ cudaError_t launch_split(const CUtensorMap& a, const CUtensorMap& b, const CUten
 template <int SPLIT, int BN>
 int max_clusters_split(int num_sms) {
   using Cfg = SkCfg<SPLIT, BN>;
-  auto kern = hgemm_skinny_kernel<SPLIT, BN, kEpiPlain>;
+  auto kern = hgemm_skinny_kernel<SPLIT, BN, kEpiPlain, kLayoutK>;
   int n = 0;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES) ==
       cudaSuccess) {

@@ -121,11 +121,12 @@ __device__ __forceinline__ PairTile pair_tile(int t, const TcArgs& p) {
 // Epilogue warps of each instantiation.
 constexpr int epi_warps(int epi) { return epi == kEpiPlain ? 4 : 8; }
 
-template <int MAX_STAGES, int EPI>
+template <int MAX_STAGES, int EPI, Layout LAYOUT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * epi_warps(EPI), 1)
     hgemm_tc2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmBh, const __grid_constant__ CUtensorMap tmC,
                      const TcArgs p) {
+  const bool a_mn = layout_a_mn(LAYOUT, p.a_mn), b_mn = layout_b_mn(LAYOUT, p.b_mn);
   using Cfg = PairCfg<MAX_STAGES, epi_warps(EPI)>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -212,14 +213,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * epi_warps(
           const int kx = kb * Cfg::BK + w.koff;
           if (rank == 0 && !(p.inject == 1 && issued == 0))  // testing aid: withhold one arrival
             mbar_arrive_expect_tx(full_bar(stage), tx);
-          if (p.a_mn) {
+          if (a_mn) {
             // A stored K×M: the CTA's 128 rows as two 64-row boxes, 8 KB apart
             tma_load_2d_cg2(sA + stage * stage_bytes, &tmA, fb, ya, kx);
             tma_load_2d_cg2(sA + stage * stage_bytes + kMnBoxBytes, &tmA, fb, ya + kMnBox, kx);
           } else {
             tma_load_2d_cg2(sA + stage * stage_bytes, &tmA, fb, kx, ya);
           }
-          if (p.b_mn) {
+          if (b_mn) {
             // B stored K×N: the CTA's ncols/2 columns as 64-column boxes, 8 KB apart
             for (int bx = 0; bx < w.ncols / 2; bx += kMnBox)
               tma_load_2d_cg2(sB + stage * stage_bytes + (bx / kMnBox) * kMnBoxBytes, &tmB, fb, yb + bx, kx);
@@ -263,9 +264,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * epi_warps(
     if (rank == 0 && elect_one()) {
       // K-major: 16 K elements are 32 bytes along the row; MN-major: 16 K
       // rows of 128 bytes
-      const uint64_t a_base = p.a_mn ? sdesc_mnmajor_sw128(sA) : sdesc_kmajor_sw128(sA);
-      const uint64_t b_base = p.b_mn ? sdesc_mnmajor_sw128(sB) : sdesc_kmajor_sw128(sB);
-      const uint32_t a_step = p.a_mn ? 128u : 2u, b_step = p.b_mn ? 128u : 2u;
+      const uint64_t a_base = a_mn ? sdesc_mnmajor_sw128(sA) : sdesc_kmajor_sw128(sA);
+      const uint64_t b_base = b_mn ? sdesc_mnmajor_sw128(sB) : sdesc_kmajor_sw128(sB);
+      const uint32_t a_step = a_mn ? 128u : 2u, b_step = b_mn ? 128u : 2u;
       int stage = 0;
       uint32_t offset = 0;  // of the stage, in the descriptors' 16-byte units
       uint32_t phase = 0;
@@ -274,7 +275,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * epi_warps(
       bool ok = true;
       for (int t = cluster_id; ok && t < p.num_tiles; t += num_clusters) {
         const uint32_t idesc = (t < p.full_tiles ? Cfg::IDESC : idesc_f16_f32acc(Cfg::BM, p.part_cols)) |
-                               idesc_major_bits(p.a_mn != 0, p.b_mn != 0);
+                               idesc_major_bits(a_mn, b_mn);
         ok = wait_phase_cluster(acce_bar(acc), acc_phase ^ 1u, wd, kWdMmaAccEmpty);
         if (!ok) break;
         tc_fence_after_sync();
@@ -467,7 +468,7 @@ int pair_max_clusters(int num_sms) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return num_sms / 2;
   if (cached[dev] > 0) return cached[dev];
-  auto kern = hgemm_tc2_kernel<kPairStages, kEpiPlain>;
+  auto kern = hgemm_tc2_kernel<kPairStages, kEpiPlain, kLayoutK>;
   int n = 0;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES) ==
       cudaSuccess) {
@@ -489,19 +490,29 @@ cudaError_t launch_tc_pair(const CUtensorMap& a, const CUtensorMap& b, const CUt
                            const CUtensorMap& c, const TcArgs& args, Epilogue kind, cudaStream_t stream) {
   using Cfg = PairCfg<kPairStages, 4>;
   static_assert(Cfg::SMEM_BYTES == PairCfg<kPairStages, 8>::SMEM_BYTES, "all instantiations have the same footprint");
-  static std::atomic<bool> attr_done[4][64];
-  auto kern = kind == kEpiPlain    ? hgemm_tc2_kernel<kPairStages, kEpiPlain>
-              : kind == kEpiFused  ? hgemm_tc2_kernel<kPairStages, kEpiFused>
-              : kind == kEpiLinear ? hgemm_tc2_kernel<kPairStages, kEpiLinear>
-                                   : hgemm_tc2_kernel<kPairStages, kEpiLinearGrad>;
+  static std::atomic<bool> attr_done[8][64];
+  const int order = args.a_mn || args.b_mn ? (args.a_mn && args.b_mn ? 2 : 1) : 0;
+  if ((kind == kEpiLinear && order != 0) || (kind == kEpiLinearGrad && (args.a_mn || !args.b_mn)))
+    return cudaErrorInvalidValue;
+  using Kern = decltype(&hgemm_tc2_kernel<kPairStages, kEpiPlain, kLayoutK>);
+  const Kern kerns[8] = {hgemm_tc2_kernel<kPairStages, kEpiPlain, kLayoutK>,
+                         hgemm_tc2_kernel<kPairStages, kEpiPlain, kLayoutAny>,
+                         hgemm_tc2_kernel<kPairStages, kEpiPlain, kLayoutMn>,
+                         hgemm_tc2_kernel<kPairStages, kEpiFused, kLayoutK>,
+                         hgemm_tc2_kernel<kPairStages, kEpiFused, kLayoutAny>,
+                         hgemm_tc2_kernel<kPairStages, kEpiFused, kLayoutMn>,
+                         hgemm_tc2_kernel<kPairStages, kEpiLinear, kLayoutK>,
+                         hgemm_tc2_kernel<kPairStages, kEpiLinearGrad, kLayoutBn>};
+  const int which = kind == kEpiLinear ? 6 : kind == kEpiLinearGrad ? 7 : (kind == kEpiFused ? 3 : 0) + order;
+  const Kern kern = kerns[which];
   const int threads = 64 + 32 * epi_warps(kind);
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || !attr_done[kind][dev]) {
+  if (dev < 0 || dev >= 64 || !attr_done[which][dev]) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) attr_done[kind][dev] = true;
+    if (dev >= 0 && dev < 64) attr_done[which][dev] = true;
   }
   PdlLaunch l(dim3(static_cast<unsigned>(args.grid)), dim3(static_cast<unsigned>(threads)), Cfg::SMEM_BYTES,
               stream);

@@ -54,6 +54,20 @@ struct LinEpi {
   int64_t ldh;
 };
 
+// The operands' order in memory, a template parameter of the pair and split-K
+// kernels: a branch on it between the copies and between the matrix
+// instructions takes them out of uniform registers (see elect_one).
+enum Layout {
+  kLayoutK,    // both K-contiguous
+  kLayoutBn,   // A K-contiguous, B N-contiguous: a linear layer's input gradient
+  kLayoutMn,   // A M-contiguous, B N-contiguous: its weight's gradient
+  kLayoutAny,  // by TcArgs::a_mn and b_mn
+};
+constexpr bool layout_a_mn(Layout l, int a_mn) { return l == kLayoutMn || (l == kLayoutAny && a_mn != 0); }
+constexpr bool layout_b_mn(Layout l, int b_mn) {
+  return l == kLayoutBn || l == kLayoutMn || (l == kLayoutAny && b_mn != 0);
+}
+
 // Everything a tensor-core launch needs besides the tensor maps.
 struct TcArgs {
   int M, N, K;
