@@ -804,7 +804,7 @@ bool linear_cluster_suits(const LinearProduct& p, int num_sms) {
   return clusters <= linear_cluster_max(num_sms);
 }
 
-int run_linear_cluster(const LinearProduct& p, const DeviceState& dev, cudaStream_t stream) {
+int run_linear_cluster(const LinearProduct& p, float* row_sums, bool add, cudaStream_t stream) {
   CUtensorMap ma, mb, mc;
   int rc;
   // halves of tiles: 64 rows of A by 64 of K, or the other way around; 32 rows
@@ -829,6 +829,8 @@ int run_linear_cluster(const LinearProduct& p, const DeviceState& dev, cudaStrea
   args.timeout_ns = g_timeout_ns.load(std::memory_order_relaxed);
   args.inject = g_inject.load(std::memory_order_relaxed);
   args.lin = p.epi;
+  args.row_sums = row_sums;
+  args.row_sums_add = add ? 1 : 0;
   return cuda_status(launch_linear_cluster(ma, mb, mc, args, p.epi.backward ? kEpiLinearGrad : kEpiLinear, stream));
 }
 
@@ -848,28 +850,35 @@ int run_linear(const LinearProduct& p, cudaStream_t stream) {
                         g_inject.load(std::memory_order_relaxed)};
     return cuda_status(launch_linear_any(p, cd, stream));
   }
-  if (forced < 0 && linear_cluster_suits(p, dev->num_sms)) return run_linear_cluster(p, *dev, stream);
+  if (forced < 0 && linear_cluster_suits(p, dev->num_sms)) return run_linear_cluster(p, nullptr, false, stream);
   return dispatch(g, kPlainEpilogue, *dev, stream);
 }
 
-int run_wgrad(const LinearProduct& p, cudaStream_t stream) {
+int run_wgrad(const LinearProduct& p, float* dbias, bool accumulate, cudaStream_t stream) {
+  const int forced = g_forced_path.load(std::memory_order_relaxed);
+  DeviceState* dev = nullptr;
+  int rc = current_device(&dev);
+  if (rc != HGEMM_OK) return rc;
   Gemm g{p.A, p.B, p.C, p.M, p.N, p.K, p.lda, p.ldb, p.ldc};
   g.a_mn = p.a_mn;
   g.b_mn = p.b_mn;
-  const int forced = g_forced_path.load(std::memory_order_relaxed);
-  if (p.K > 0 && (forced == HGEMM_PATH_GENERIC || !tma_ok(g))) return run_linear(p, stream);
-  DeviceState* dev = nullptr;
-  const int rc = current_device(&dev);
-  if (rc != HGEMM_OK) return rc;
-  if (forced < 0 && linear_small_suits(p, dev->num_sms)) return run_linear_small(p, *dev, stream);
-  if (forced < 0 && linear_cluster_suits(p, dev->num_sms)) return run_linear_cluster(p, *dev, stream);
-  // (the plain and the accumulating product; the sum of an old value is the residual's)
-  EpiArgs epi = kPlainEpilogue;
-  if (p.epi.res) {
-    epi.beta = 1.0f;
-    epi.mode = 2;
+  if (p.K > 0 && (forced == HGEMM_PATH_GENERIC || !tma_ok(g))) {
+    rc = run_linear(p, stream);
+  } else if (forced < 0 && linear_small_suits(p, dev->num_sms)) {
+    rc = run_linear_small(p, *dev, stream);
+  } else if (forced < 0 && linear_cluster_suits(p, dev->num_sms)) {
+    return run_linear_cluster(p, dbias, accumulate, stream);
+  } else {
+    // (the plain and the accumulating product; the sum of an old value is the residual's)
+    EpiArgs epi = kPlainEpilogue;
+    if (p.epi.res) {
+      epi.beta = 1.0f;
+      epi.mode = 2;
+    }
+    rc = dispatch(g, epi, *dev, stream);
   }
-  return dispatch(g, epi, *dev, stream);
+  if (rc != HGEMM_OK || !dbias) return rc;
+  return cuda_status(launch_column_sums(p.A, p.lda, p.K, p.M, dbias, accumulate, true, stream));
 }
 
 }  // namespace hg

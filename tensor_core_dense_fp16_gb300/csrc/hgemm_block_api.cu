@@ -119,10 +119,10 @@ int hgemm_linear_wgrad(const hgemm_half_t* dY, int64_t lddy, const hgemm_half_t*
     const uint16_t* old = accumulate ? dW : nullptr;
     const hg::LinearProduct p{dY, lddy, true, X, ldx, true, dW, lddw, N, K, M,
                               hg::LinEpi{0, HGEMM_ACT_NONE, nullptr, old, lddw, nullptr, 0, nullptr, 0, nullptr, 0}};
-    if ((rc = hg::run_wgrad(p, stream)) != HGEMM_OK) return rc;
+    return hg::run_wgrad(p, dbias, accumulate != 0, stream);
   }
   if (!dbias) return HGEMM_OK;
-  return hg::cuda_status(hg::launch_column_sums(dY, lddy, M, N, dbias, accumulate != 0, K > 0, stream));
+  return hg::cuda_status(hg::launch_column_sums(dY, lddy, M, N, dbias, accumulate != 0, false, stream));
 }
 
 int hgemm_layernorm_forward(const hgemm_half_t* X, int64_t ldx, const hgemm_half_t* gamma, const hgemm_half_t* beta,

@@ -42,7 +42,8 @@ struct ClCfg {
   static constexpr int OFF_A = 0;
   static constexpr int OFF_B = OFF_A + STAGES * A_BYTES;
   static constexpr int OFF_C = OFF_B + STAGES * B_BYTES;
-  static constexpr int OFF_BAR = OFF_C + EPI_WARPS * C_BOX_BYTES;
+  static constexpr int OFF_SUM = OFF_C + EPI_WARPS * C_BOX_BYTES;  // partial row sums of A
+  static constexpr int OFF_BAR = OFF_SUM + EPI_WARPS * (BM / 2) * 4;
   static constexpr int NUM_BARS = 2 * STAGES + 2;  // full, empty, accumulator full, drain
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
@@ -53,6 +54,57 @@ struct ClCfg {
   static_assert(BM == 2 * kMnBox && BN == kMnBox, "half an A tile is one MN-major box");
   static_assert(SMEM_BYTES <= 232448, "exceeds 227 KB of shared memory per CTA");
 };
+
+// The sums over K of the half of the A tile that this CTA loads (64 rows), by
+// the epilogue warps while the product runs: the bias gradient beside the
+// weight's, from the stages in shared memory (MN-major: 64 K rows of 128
+// bytes). A thread adds the eight rows of A of one 16-byte chunk in every
+// 16th K row, and the 16 partial sums of a row are added in a fixed order. (A
+// CTA's own half, because then only its own loads wait for the sums. A kernel
+// of column sums beside the product took 5 us more: 1000^3, 6.0 us without.)
+__device__ __forceinline__ void sum_rows(const TcArgs& p, uint8_t* smem, uint32_t full0, uint32_t empty0, int half,
+                                         int first, const Watchdog& wd) {
+  using Cfg = ClCfg;
+  const int t = static_cast<int>(threadIdx.x) - 64, lane = t & 31;
+  const int chunk = t & 7, k0 = t >> 3;
+  const uint8_t* src = smem + Cfg::OFF_A + half * kMnBoxBytes + k0 * 128 + ((chunk ^ (k0 & 7)) << 4);
+  f32x2 sum[4] = {};
+  int stage = 0;
+  uint32_t phase = 0;
+  for (int kb = 0; kb < p.num_kb; ++kb) {
+    int ok = 1;
+    if (lane == 0) ok = wait_phase(full0 + 8u * stage, phase, wd, kWdRows) ? 1 : 0;
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    if (!ok) break;
+#pragma unroll
+    for (int i = 0; i < Cfg::BK / 16; ++i)
+      add8(sum, *reinterpret_cast<const uint4*>(src + stage * Cfg::A_BYTES + i * 16 * 128));
+    __syncwarp();
+    if (lane == 0) mbar_arrive(empty0 + 8u * stage);
+    if (++stage == Cfg::STAGES) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) unpair(sum[i], v[2 * i], v[2 * i + 1]);
+  float* part = reinterpret_cast<float*>(smem + Cfg::OFF_SUM);  // [warp][row]
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] += __shfl_xor_sync(0xffffffffu, v[i], 8);
+    v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
+    if (lane < 8) part[(t >> 5) * kMnBox + chunk * 8 + i] = v[i];
+  }
+  named_bar_sync(1, 32 * Cfg::EPI_WARPS);
+  if (t < kMnBox && first + t < p.M) {
+    float total = 0.f;
+#pragma unroll
+    for (int w = 0; w < Cfg::EPI_WARPS; ++w) total += part[w * kMnBox + t];
+    float* out = p.row_sums + first + t;
+    *out = p.row_sums_add ? *out + total : total;
+  }
+}
 
 // A_MN, B_MN: the operand is stored with its rows contiguous (K×M, K×N).
 template <int EPI, bool A_MN, bool B_MN>
@@ -81,12 +133,16 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(ClCfg::THREADS, 1)
   const int n0 = (2 * (cluster / clusters_m) + rn) * Cfg::BN;
   const uint16_t same_m = static_cast<uint16_t>(0x5u << rm);       // the two CTAs of these rows
   const uint16_t same_n = static_cast<uint16_t>(0x3u << (2 * rn));  // the two CTAs of these columns
+  // sums of A's rows over K: computed in the first column of tiles
+  const bool summed = A_MN && p.row_sums && cluster / clusters_m == 0;
   const Watchdog wd{abort_flag, p.status, p.timeout_ns};
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < Cfg::STAGES; ++s) {
       mbar_init(full_bar(s), 1);   // the producer's arrive.expect_tx (+ the bytes of three CTAs)
-      mbar_init(empty_bar(s), 3);  // commits of the CTAs that received this CTA's halves
+      // commits of the CTAs that received this CTA's halves, and its own
+      // summing warps
+      mbar_init(empty_bar(s), summed ? 3 + Cfg::EPI_WARPS : 3);
     }
     mbar_init(accf_bar, 1);
     mbar_init(drain_bar, 1);
@@ -204,6 +260,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(ClCfg::THREADS, 1)
     const bool inside = n0 < p.N && y0 < p.M;
     LinSide<EPI> side;
     if (inside) lin_fetch<EPI>(side, p.lin, p.M, p.N, static_cast<int64_t>(y0) + lane, n0);
+    if constexpr (A_MN) {
+      if (summed) sum_rows(p, smem, full_bar(0), empty_bar(0), rn, m0 + rn * kMnBox, wd);
+    }
     int ok = 1;
     if (lane == 0) ok = wait_phase(accf_bar, 0, wd, kWdEpiAccFull) ? 1 : 0;
     ok = __shfl_sync(0xffffffffu, ok, 0);

@@ -88,6 +88,8 @@ struct TcArgs {
   int a_mn, b_mn;            // pair kernel: A stored M-contiguous (K×M), B stored
                              // N-contiguous (K×N); else K-contiguous
   LinEpi lin;                // kEpiLinear and kEpiLinearGrad
+  float* row_sums;           // clusters of 128×64 tiles, kLayoutMn: A's sums over K, or null
+  int row_sums_add;          // added to, instead of written
   int batch_tiles;           // pair kernel: whole tiles per product of a batch of
                              // equal products in one launch (0: a single product)
   int batch_shift;           // product j of the batch is the first one with A's K,
@@ -290,8 +292,9 @@ cudaError_t launch_linear_small(const CUtensorMap& w, const CUtensorMap& x, cons
 // The kernel for operands and outputs of any pitch and alignment; K > 0.
 cudaError_t launch_linear_any(const LinearProduct& p, const CallDevice& dev, cudaStream_t stream);
 // The gradient of a weight: C = A·B, or C + A·B, with an epilogue that says
-// so.
-int run_wgrad(const LinearProduct& p, cudaStream_t stream);
+// so; and, unless dbias is null, the sums of A's rows over K, beside the
+// product or within it.
+int run_wgrad(const LinearProduct& p, float* dbias, bool accumulate, cudaStream_t stream);
 
 struct NormArgs {
   const uint16_t* x;
