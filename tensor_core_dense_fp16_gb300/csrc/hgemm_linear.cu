@@ -89,6 +89,15 @@ __global__ void __launch_bounds__(WARPS * 32) linear_rows_kernel(const RowsArgs 
   constexpr int AHEAD = MT == 1 ? 4 : 2;  // pieces in flight per warp, 64 bytes of each feature
   constexpr int PITCH = kRowsFeatures + 1;
   __shared__ float part[WARPS][8 * MT][PITCH];
+  // The first weights, four lines per thread, into L2 while the previous launch
+  // on the stream ends (only asked for: whatever it still writes there is read
+  // after the wait). A token through 2048→8192→2048, two launches: 16.4 us
+  // without, 14.4 with.
+  const int lines = (p.K + 63) / 64;
+  for (int i = threadIdx.x; i < kRowsFeatures * lines && i < 4 * WARPS * 32; i += WARPS * 32) {
+    const int f = static_cast<int>(blockIdx.x) * kRowsFeatures + i / lines;
+    if (f < p.N) prefetch_l2(p.W + f * p.ldw + i % lines * 64);
+  }
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

@@ -7,11 +7,13 @@
 // are the rows of the matrix instruction (M = 128) and the output's rows its
 // columns (N = 16 to 128, as many as there are), so that no part of the
 // instruction is spent on rows that do not exist, and a CTA's ring of stages
-// is almost all weights: 6 to 11 stages, about 200 KB under way per SM. A
-// cluster of CTAs shares an output tile, each a run of K; the FP32 partial
-// sums are left in each CTA's shared memory, and every CTA adds those of its
-// share of the rows in rank order (so the result does not depend on timing)
-// through distributed shared memory. In the accumulator a thread owns a
+// is almost all weights: 5 to 12 stages, about 200 KB under way per SM. A
+// cluster of CTAs shares an output tile, each a run of K. Each output row has
+// one of them as its owner: the others store their FP32 partial sums into the
+// owner's shared memory, beside its ring, and the owner adds them and its own
+// in rank order, so the result does not depend on timing. (Read by the owner
+// instead, between two barriers of the cluster, they took 3.7 us of 10: 24 rows
+// 2048×8192.) In the accumulator a thread owns a
 // feature: bias, residual, 8-bit codes and outputs are read and written along
 // the features, whatever their pitch and alignment.
 #include <atomic>
@@ -32,17 +34,19 @@ struct SmallCfg {
   static constexpr int W_BYTES = BM * BK * 2;
   static constexpr int X_BYTES = NT * BK * 2;
   static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
-  static constexpr int STAGES = (208 * 1024) / STAGE_BYTES;
-  static constexpr int PART_BYTES = NT * BM * 4;  // the partial sums, in the ring
-  static constexpr int OFF_BAR = STAGES * STAGE_BYTES;
-  static constexpr int NUM_BARS = 2 * STAGES + 2;  // full, empty, accumulator full, drain
+  // four rows of 128 features' partial sums are a unit; the units that a CTA
+  // receives take the end of the ring's space
+  static constexpr int UNITS = NT / 4;
+  static constexpr int UNIT_BYTES = BM * 4 * 4;
+  static constexpr int OFF_BAR = 224 * 1024;
+  static constexpr int STAGES = OFF_BAR / STAGE_BYTES;  // the most, without a cluster
+  static constexpr int NUM_BARS = 2 * STAGES + 3;  // full, empty, accumulator full, drain, received
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
   static constexpr int THREADS = 192;
   static constexpr int TMEM_COLS = NT < 32 ? 32 : NT;
   static constexpr uint32_t IDESC = idesc_f16_f32acc(BM, NT);
   static_assert(STAGE_BYTES % 1024 == 0, "swizzled tiles are 1024-byte aligned");
-  static_assert(PART_BYTES <= STAGES * STAGE_BYTES, "the partial sums fit the ring");
   static_assert(SMEM_BYTES <= 232448, "exceeds 227 KB of shared memory per CTA");
 };
 
@@ -120,6 +124,7 @@ __global__ void __launch_bounds__(192, 1)
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bar0 = sbase + Cfg::OFF_BAR;
   const uint32_t accf_bar = bar0 + 8u * (2 * Cfg::STAGES), drain_bar = accf_bar + 8u;
+  const uint32_t recv_bar = drain_bar + 8u;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::OFF_MISC + 4);
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
@@ -132,6 +137,13 @@ __global__ void __launch_bounds__(192, 1)
   const int rows = p.M - r0 < NT ? p.M - r0 : NT;
   const int kb0 = static_cast<int>(static_cast<long long>(p.num_kb) * rank / p.split);
   const int kb1 = static_cast<int>(static_cast<long long>(p.num_kb) * (rank + 1) / p.split);
+  // units with rows inside; this CTA owns [u0, u1), and its buffer, at the end
+  // of the space, has room for `per` of each other rank
+  const int units = (rows + 3) / 4;
+  const int u0 = units * rank / p.split, u1 = units * (rank + 1) / p.split;
+  const int per = (units + p.split - 1) / p.split;
+  const int off_part = Cfg::OFF_BAR - (p.split - 1) * per * Cfg::UNIT_BYTES;
+  const int stages = off_part / Cfg::STAGE_BYTES;
   const Watchdog wd{abort_flag, p.status, p.timeout_ns};
 
   if (threadIdx.x == 0) {
@@ -141,6 +153,7 @@ __global__ void __launch_bounds__(192, 1)
     }
     mbar_init(accf_bar, 1);
     mbar_init(drain_bar, 1);
+    mbar_init(recv_bar, 4 * (p.split > 1 ? p.split - 1 : 1));  // the other ranks' epilogue warps
     *abort_flag = 0;
     fence_barrier_init();
     prefetch_tensormap(&tmW);
@@ -152,8 +165,21 @@ __global__ void __launch_bounds__(192, 1)
   }
   tc_fence_before_sync();
   __syncthreads();
+  if (p.split > 1) cluster_sync_after_init();  // partial sums reach the other CTAs' barriers
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
+  // As much of the weights as the ring holds, into L2 while the previous
+  // launch on the stream ends (only asked for: whatever it still writes there
+  // is read after the wait). 24 rows 8192×2048 9.6 to 9.1 us, one after another.
+  if (warp == 0 && elect_one())
+    for (int kb = kb0; kb < kb1 && kb < kb0 + stages; ++kb) {
+      if constexpr (W_MN) {
+        tma_prefetch_2d(&tmW, f0, kb * Cfg::BK);
+        tma_prefetch_2d(&tmW, f0 + kMnBox, kb * Cfg::BK);
+      } else {
+        tma_prefetch_2d(&tmW, kb * Cfg::BK, f0);
+      }
+    }
   grid_dependency_wait();
   grid_launch_dependents();
 
@@ -162,7 +188,6 @@ __global__ void __launch_bounds__(192, 1)
   const bool in_f = f < p.N;
   const float bias =
       !BACKWARD && warp >= 2 && p.epi.bias && in_f ? __half2float(__ushort_as_half(__ldg(p.epi.bias + f))) : 0.f;
-  float* part = reinterpret_cast<float*>(smem);  // [row of X][feature]
 
   if (warp == 0) {
     if (elect_one()) {
@@ -188,7 +213,7 @@ __global__ void __launch_bounds__(192, 1)
           tma_load_2d(dst + Cfg::W_BYTES, &tmX, full_bar(stage), kb * Cfg::BK, r0);
         }
         ++issued;
-        if (++stage == Cfg::STAGES) {
+        if (++stage == stages) {
           stage = 0;
           phase ^= 1u;
         }
@@ -196,9 +221,9 @@ __global__ void __launch_bounds__(192, 1)
       // the last loads must have landed before the ring is reused or left
       int s = stage;
       uint32_t ph = phase;
-      for (int i = 0; i < issued && i < Cfg::STAGES; ++i) {
+      for (int i = 0; i < issued && i < stages; ++i) {
         if (s == 0) {
-          s = Cfg::STAGES - 1;
+          s = stages - 1;
           ph ^= 1u;
         } else {
           --s;
@@ -226,7 +251,7 @@ __global__ void __launch_bounds__(192, 1)
           mma_f16_ss(tmem_base, w_desc + (W_MN ? 128u : 2u) * k, x_desc + (X_MN ? 128u : 2u) * k,
                      Cfg::IDESC | idesc_major_bits(W_MN, X_MN), (kb > kb0 || k > 0) ? 1u : 0u);
         mma_commit(empty_bar(stage));
-        if (++stage == Cfg::STAGES) {
+        if (++stage == stages) {
           stage = 0;
           phase ^= 1u;
         }
@@ -243,43 +268,71 @@ __global__ void __launch_bounds__(192, 1)
     if (ok) {
       tc_fence_after_sync();
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+      if (p.split == 1) {
 #pragma unroll 1
-      for (int c = 0; c < rows; c += 16) {
-        float v[16];
-        tmem_ld_32x32b_x16(t_row + c, v);
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (p.split > 1) part[(c + i) * Cfg::BM + q * 32 + lane] = v[i];
-        if (p.split == 1) put_rows<BACKWARD, 16>(p, v, bias, r0 + c, f, in_f ? rows - c : 0);
-      }
-    }
-  }
-  if (p.split > 1) {
-    // (after a wait that gave up the sums are garbage; every CTA still
-    // reaches both barriers)
-    cluster_sync();
-    if (warp >= 2) {
-      const int m0 = NT * rank / p.split, m1 = NT * (rank + 1) / p.split;
-      const uint32_t mine = smem_u32(part + q * 32 + lane);
-      // eight rows at a time: every rank's partial sums of them are under way at once
+        for (int c = 0; c < rows; c += 16) {
+          float v[16];
+          tmem_ld_32x32b_x16(t_row + c, v);
+          put_rows<BACKWARD, 16>(p, v, bias, r0 + c, f, in_f ? rows - c : 0);
+        }
+      } else {
+        const uint32_t column = static_cast<uint32_t>(q * 32 + lane) * 16u;
+        int owner = 0, first = 0, end = units / p.split;  // the owner's units
 #pragma unroll 1
-      for (int m = m0; m < m1 && m < rows; m += 8) {
-        float sum[8];
+        for (int c = 0; c < rows; c += 16) {
+          float v[16];
+          tmem_ld_32x32b_x16(t_row + c, v);
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-          if (r < p.split) {
-            const uint32_t from = mapa_shared(mine + static_cast<uint32_t>(m * Cfg::BM * 4), r);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float v = m + i < m1 ? ld_cluster_f32(from + static_cast<uint32_t>(i * Cfg::BM * 4)) : 0.f;
-              sum[i] = r == 0 ? v : sum[i] + v;
+          for (int i = 0; i < 16; i += 4) {
+            const int u = (c + i) / 4;
+            while (u >= end && owner + 1 < p.split) {
+              first = end;
+              end = units * (++owner + 1) / p.split;
+            }
+            if (u < units && owner != rank) {
+              const int slot = (rank < owner ? rank : rank - 1) * per + u - first;
+              st_cluster_v4(mapa_shared(sbase + static_cast<uint32_t>(off_part + slot * Cfg::UNIT_BYTES) + column, owner),
+                            __float_as_uint(v[i]), __float_as_uint(v[i + 1]), __float_as_uint(v[i + 2]),
+                            __float_as_uint(v[i + 3]));
             }
           }
-        const int left = (m1 < rows ? m1 : rows) - m;
-        put_rows<BACKWARD, 8>(p, sum, bias, r0 + m, f, in_f ? left : 0);
+        }
+        __syncwarp();
+        if (lane < p.split && lane != rank) mbar_arrive_cluster(mapa_shared(recv_bar, static_cast<uint32_t>(lane)));
       }
     }
-    cluster_sync();  // the other CTAs' shared memory stays until everybody has read it
+    if (p.split > 1) {
+      // Nothing is left under way to this CTA's shared memory once the other
+      // ranks have all arrived (after a wait that gave up they are awaited too).
+      if (lane == 0)
+        ok = (ok ? wait_phase_cluster(recv_bar, 0, wd, kWdReduce) : wait_drain_cluster(recv_bar, 0, wd)) ? ok : 0;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      const uint8_t* part = smem + off_part + (q * 32 + lane) * 16;
+      const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll 1
+      for (int u = u0; ok && u < u1; u += 2) {
+        float own[2][4] = {}, sum[8];
+        tmem_ld_32x32b_x4(t_row + 4 * u, own[0]);
+        if (u + 1 < u1) tmem_ld_32x32b_x4(t_row + 4 * u + 4, own[1]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] = 0.f;
+#pragma unroll 1
+        for (int r = 0; r < p.split; ++r) {
+          const uint8_t* from = part + ((r < rank ? r : r - 1) * per + u - u0) * Cfg::UNIT_BYTES;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float4 w = make_float4(own[j][0], own[j][1], own[j][2], own[j][3]);
+            if (r != rank && u + j < u1) w = *reinterpret_cast<const float4*>(from + j * Cfg::UNIT_BYTES);
+            sum[4 * j] += w.x;
+            sum[4 * j + 1] += w.y;
+            sum[4 * j + 2] += w.z;
+            sum[4 * j + 3] += w.w;
+          }
+        }
+        const int left = min(rows, 4 * u1) - 4 * u;
+        put_rows<BACKWARD, 8>(p, sum, bias, r0 + 4 * u, f, in_f ? left : 0);
+      }
+    }
   }
   tc_fence_before_sync();
   __syncthreads();

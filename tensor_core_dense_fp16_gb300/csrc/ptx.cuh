@@ -119,7 +119,15 @@ __device__ __forceinline__ void tma_load_2d_multicast(uint32_t dst, const CUtens
       : "memory");
 }
 
-// The same with an L2 cache-policy hint (a createpolicy result).
+// Asks L2 for the box.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap *map, int32_t x, int32_t y) {
+  if (!HG_DBG_TMA_X(x)) return;
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y)
+               : "memory");
+}
+
+// tma_load_2d with an L2 cache-policy hint (a createpolicy result).
 __device__ __forceinline__ void tma_load_2d_hint(uint32_t dst, const CUtensorMap *map,
                                                  uint32_t bar, int32_t x, int32_t y,
                                                  uint64_t policy) {
@@ -293,6 +301,20 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, float (&r)[16
       "tcgen05.wait::ld.sync.aligned;"
       : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
         "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_32x32b_x4(uint32_t taddr, float (&r)[4]) {
+  if (!HG_DBG_TMEM(taddr, 4)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = 0.f;
+    return;
+  }
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3])
       : "r"(taddr)
       : "memory");
 }
