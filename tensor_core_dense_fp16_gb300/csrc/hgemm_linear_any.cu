@@ -420,8 +420,8 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1) linear_any_kernel(const An
           tmem_row64(t_group, v);
           __syncwarp();
           LinSide<EPI> side;
-          lin_fetch<EPI>(side, e, p.M, p.N, gi, col0);
-          lin_row64<EPI>(box + lane * 128, lane, v, side, e, p.M, p.N, gi, col0);
+          lin_fetch<EPI>(side, e, lane, p.M, p.N, gi, col0);
+          lin_row64<EPI>(box, lane, v, side, e, p.M, p.N, gi, col0);
           __syncwarp();
           const int64_t n = col0 + 8 * (lane & 7);
 #pragma unroll

@@ -259,7 +259,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(ClCfg::THREADS, 1)
     const int y0 = m0 + q * kEpiRows;
     const bool inside = n0 < p.N && y0 < p.M;
     LinSide<EPI> side;
-    if (inside) lin_fetch<EPI>(side, p.lin, p.M, p.N, static_cast<int64_t>(y0) + lane, n0);
+    if (inside) lin_fetch<EPI>(side, p.lin, lane, p.M, p.N, static_cast<int64_t>(y0) + lane, n0);
     if constexpr (A_MN) {
       if (summed) sum_rows(p, smem, full_bar(0), empty_bar(0), rn, m0 + rn * kMnBox, wd);
     }
@@ -270,7 +270,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(ClCfg::THREADS, 1)
       tc_fence_after_sync();
       f32x2 v[32];
       tmem_row64(tmem_base + (static_cast<uint32_t>(q * 32) << 16), v);
-      lin_row64<EPI>(box + lane * 128, lane, v, side, p.lin, p.M, p.N, static_cast<int64_t>(y0) + lane, n0);
+      lin_row64<EPI>(box, lane, v, side, p.lin, p.M, p.N, static_cast<int64_t>(y0) + lane, n0);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {

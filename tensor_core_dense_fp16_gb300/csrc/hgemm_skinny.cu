@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(192, 1)
   [[maybe_unused]] LinSide<EPI> side;  // of the first 64 of this CTA's columns
   if constexpr (EPI >= kEpiLinear) {
     if (warp >= 2)
-      lin_fetch<EPI>(side, p.lin, p.M, p.N, static_cast<int64_t>(mb) * Cfg::BM + half * Cfg::ROWS + row,
+      lin_fetch<EPI>(side, p.lin, lane, p.M, p.N, static_cast<int64_t>(mb) * Cfg::BM + half * Cfg::ROWS + row,
                      static_cast<int64_t>(nb) * Cfg::BN + own_c0);
   }
   // ring layout for the exchange: receive slots first, then send staging
@@ -384,8 +384,8 @@ __global__ void __launch_bounds__(192, 1)
           for (int k = 0; k < 16; ++k) v[16 * i + k] = pair_of(a[2 * k], a[2 * k + 1]);
         }
         if constexpr (EPI >= kEpiLinear) {
-          if (c64 > 0) lin_fetch<EPI>(side, p.lin, p.M, p.N, static_cast<int64_t>(y0) + lane, x0 + c64 * 64);
-          lin_row64<EPI>(cbuf + c64 * (kEpiRows * 128) + lane * 128, lane, v, side, p.lin, p.M, p.N,
+          if (c64 > 0) lin_fetch<EPI>(side, p.lin, lane, p.M, p.N, static_cast<int64_t>(y0) + lane, x0 + c64 * 64);
+          lin_row64<EPI>(cbuf + c64 * (kEpiRows * 128), lane, v, side, p.lin, p.M, p.N,
                          static_cast<int64_t>(y0) + lane, x0 + c64 * 64);
         }
       }

@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(192, 1)
                               static_cast<int64_t>(nb) * BN, BN);
       [[maybe_unused]] LinSide<EPI> side;
       if constexpr (EPI == kEpiLinear)
-        lin_fetch<EPI>(side, p.lin, p.M, p.N, static_cast<int64_t>(mb) * Cfg::BM + q * kEpiRows + lane,
+        lin_fetch<EPI>(side, p.lin, lane, p.M, p.N, static_cast<int64_t>(mb) * Cfg::BM + q * kEpiRows + lane,
                        static_cast<int64_t>(nb) * BN);
       int ok = 1;
       if (lane == 0) ok = wait_phase(accf_bar(acc), acc_phase, wd, kWdEpiAccFull) ? 1 : 0;
@@ -268,8 +268,8 @@ __global__ void __launch_bounds__(192, 1)
           if (!inside) continue;
           if (lane == 0) bulk_wait_group_read<1>();
           __syncwarp();
-          if (c > 0) lin_fetch<EPI>(side, p.lin, p.M, p.N, static_cast<int64_t>(y0) + lane, x0);
-          lin_row64<EPI>(row, lane, v, side, p.lin, p.M, p.N, static_cast<int64_t>(y0) + lane, x0);
+          if (c > 0) lin_fetch<EPI>(side, p.lin, lane, p.M, p.N, static_cast<int64_t>(y0) + lane, x0);
+          lin_row64<EPI>(buf, lane, v, side, p.lin, p.M, p.N, static_cast<int64_t>(y0) + lane, x0);
         } else {
           uint32_t v0[32], v1[32];
           tmem_ld_32x32b_x32(t_row + c * kEpiCols, v0);

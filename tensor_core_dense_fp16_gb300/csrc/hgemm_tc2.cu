@@ -327,7 +327,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * epi_warps(
         lin_prefetch_row<EPI>(p.lin, p.M, p.N, grow, w.n0, w.ncols);
       [[maybe_unused]] LinSide<EPI> side;
       if constexpr (EPI >= kEpiLinear)
-        if (h < chunks) lin_fetch<EPI>(side, p.lin, p.M, p.N, grow, w.n0 + h * kEpiCols);
+        if (h < chunks) lin_fetch<EPI>(side, p.lin, lane, p.M, p.N, grow, w.n0 + h * kEpiCols);
       int ok = 1;
       if (lane == 0) ok = wait_phase(accf_bar(acc), acc_phase, wd, kWdEpiAccFull) ? 1 : 0;
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -377,8 +377,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * epi_warps(
           if (!inside) continue;
           if (lane == 0) bulk_wait_group_read<0>();
           __syncwarp();
-          if (c > h) lin_fetch<EPI>(side, p.lin, p.M, p.N, grow, x0);
-          lin_row64<EPI>(buf + lane * 128, lane, v, side, p.lin, p.M, p.N, grow, x0);
+          if (c > h) lin_fetch<EPI>(side, p.lin, lane, p.M, p.N, grow, x0);
+          lin_row64<EPI>(buf, lane, v, side, p.lin, p.M, p.N, grow, x0);
         }
         fence_proxy_async_smem();
         __syncwarp();

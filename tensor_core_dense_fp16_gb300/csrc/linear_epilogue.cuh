@@ -270,61 +270,86 @@ __device__ __forceinline__ void tmem_row64(uint32_t taddr, f32x2 (&v)[32]) {
   }
 }
 
-// What the epilogue of a row's 64 columns reads besides the accumulator:
+// A lane computes a row of 64 columns, but a warp whose lanes each access a
+// row of their own touches 32 lines per instruction. So residual, codes and
+// f(û) are read and written four or eight rows at a time, neighbouring lanes
+// taking neighbouring 16 bytes, and pass through the warp's staging box on the
+// way to or from the row's lane. (4096×4096 outputs of a contraction of 256,
+// GELU's gradient with f(û): [figures].)
+//
+// The 16-byte chunk j of row r of a box of 128-byte rows and of one of 64-byte
+// rows, permuted so that neither way of access meets bank conflicts.
+__device__ __forceinline__ uint4* box_chunk128(uint8_t* box, int r, int j) {
+  return reinterpret_cast<uint4*>(box + r * 128 + ((j ^ (r & 7)) << 4));
+}
+__device__ __forceinline__ uint4* box_chunk64(uint8_t* box, int r, int j) {
+  return reinterpret_cast<uint4*>(box + r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
+}
+
+// What the epilogue of 32 rows' 64 columns reads besides the accumulator:
 // fetched ahead of it, so that the reads wait while the product does.
 template <int EPI>
 struct LinSide {
   uint4 bias[EPI == kEpiLinear ? 8 : 1];
-  uint4 side[EPI == kEpiLinear ? 8 : 4];  // residual, or codes
-  float scale;
+  uint4 side[EPI == kEpiLinear ? 8 : 4];  // residual: rows 4·j + lane/8; codes: rows 8·j + lane/4
+  float scale;                            // of row `lane`
 };
 
+// Codes are accessed 16 bytes at a time where the matrix allows that.
+__device__ __forceinline__ bool codes16(const LinEpi& e, int64_t N, int64_t x0) {
+  return x0 + 64 <= N && (reinterpret_cast<uintptr_t>(e.codes) & 15u) == 0 && e.ldq % 16 == 0;
+}
+
+// grow: row `lane` of the box.
 template <int EPI>
-__device__ __forceinline__ void lin_fetch(LinSide<EPI>& s, const LinEpi& e, int64_t M, int64_t N, int64_t grow,
-                                          int64_t x0) {
-  const bool in_m = grow < M;
+__device__ __forceinline__ void lin_fetch(LinSide<EPI>& s, const LinEpi& e, int lane, int64_t M, int64_t N,
+                                          int64_t grow, int64_t x0) {
+  const int64_t row0 = grow - lane;
   if constexpr (EPI == kEpiLinear) {
     if (e.bias) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) s.bias[j] = load_bias8(e.bias, x0 + 8 * j, N);
     }
     if (e.res) {
-      const uint16_t* r = e.res + grow * e.ldr + x0;
+      const int64_t m = row0 + (lane >> 3), n = x0 + 8 * (lane & 7);
+      const uint16_t* r = e.res + m * e.ldr + n;
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        s.side[j] = in_m && x0 + 8 * j < N ? *reinterpret_cast<const uint4*>(r + 8 * j) : make_uint4(0u, 0u, 0u, 0u);
+        s.side[j] = m + 4 * j < M && n < N ? *reinterpret_cast<const uint4*>(r + 4 * j * e.ldr)
+                                           : make_uint4(0u, 0u, 0u, 0u);
     }
   } else if (e.codes) {
-    const int8_t* q = e.codes + grow * e.ldq + x0;
+    const int64_t m = row0 + (lane >> 2), n = x0 + 16 * (lane & 3);
+    const int8_t* q = e.codes + m * e.ldq + n;
+    const bool wide = codes16(e, N, x0);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s.side[j] = make_uint4(0u, 0u, 0u, 0u);
-    s.scale = 0.f;
-    if (in_m && x0 < N) {
-      if (x0 + 64 <= N && (reinterpret_cast<uintptr_t>(q) & 15u) == 0) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s.side[j] = reinterpret_cast<const uint4*>(q)[j];
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 4; ++j) {
+      s.side[j] = make_uint4(0u, 0u, 0u, 0u);
+      const int8_t* at = q + 8 * j * e.ldq;
+      if (m + 8 * j < M) {
+        if (wide) {
+          s.side[j] = *reinterpret_cast<const uint4*>(at);
+        } else {
           uint2 a = make_uint2(0u, 0u), b = a;
-          if (x0 + 16 * j < N) a = reinterpret_cast<const uint2*>(q)[2 * j];
-          if (x0 + 16 * j + 8 < N) b = reinterpret_cast<const uint2*>(q)[2 * j + 1];
+          if (n < N) a = reinterpret_cast<const uint2*>(at)[0];
+          if (n + 8 < N) b = reinterpret_cast<const uint2*>(at)[1];
           s.side[j] = make_uint4(a.x, a.y, b.x, b.y);
         }
       }
-      s.scale = e.scales[x0 / kCkptGroup * e.lds + grow];
     }
+    s.scale = grow < M && x0 < N ? e.scales[x0 / kCkptGroup * e.lds + grow] : 0.f;
   }
 }
 
-// Row `lane` of a staged 32×64 box, columns x0 .. x0+63 (one 8-bit group) of
-// row `grow`: its 64 accumulators v through the epilogue into the
-// 128-byte-swizzled staging row, as stage_row64 does. N, the pitches and x0
-// are multiples of 8, so eight columns are inside the matrix or none.
+// Row `lane` of a staging box of 32 rows of 64 columns x0 .. x0+63 (one 8-bit
+// group), row `grow` of the output: its 64 accumulators v through the epilogue
+// into the box, 128-byte swizzled as stage_row64 does. The whole warp calls;
+// the box is free. N, the pitches and x0 are multiples of 8, so eight columns
+// are inside the matrix or none.
 template <int EPI>
-__device__ __forceinline__ void lin_row64(uint8_t* row, int lane, f32x2 (&v)[32], const LinSide<EPI>& s,
+__device__ __forceinline__ void lin_row64(uint8_t* box, int lane, f32x2 (&v)[32], const LinSide<EPI>& s,
                                           const LinEpi& e, int64_t M, int64_t N, int64_t grow, int64_t x0) {
-  const bool in_m = grow < M;
+  const int64_t row0 = grow - lane;
   if constexpr (EPI == kEpiLinear) {
     if (e.bias) {
 #pragma unroll
@@ -341,22 +366,34 @@ __device__ __forceinline__ void lin_row64(uint8_t* row, int lane, f32x2 (&v)[32]
       }
       float scale, inv;
       ckpt_scale(magnitude_bits(top), scale, inv);
-      uint32_t w[16];
+      if (grow < M) e.scales[x0 / kCkptGroup * e.lds + grow] = scale;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) w[j] = ckpt_word(v[2 * j], v[2 * j + 1], inv);
-      if (in_m) {
-        int8_t* q = e.codes + grow * e.ldq + x0;
-        if (x0 + 64 <= N && (reinterpret_cast<uintptr_t>(q) & 15u) == 0) {
+      for (int j = 0; j < 4; ++j)
+        *box_chunk64(box, lane, j) =
+            make_uint4(ckpt_word(v[8 * j], v[8 * j + 1], inv), ckpt_word(v[8 * j + 2], v[8 * j + 3], inv),
+                       ckpt_word(v[8 * j + 4], v[8 * j + 5], inv), ckpt_word(v[8 * j + 6], v[8 * j + 7], inv));
+      __syncwarp();
+      const int64_t m = row0 + (lane >> 2), n = x0 + 16 * (lane & 3);
+      int8_t* q = e.codes + m * e.ldq + n;
+      const bool wide = codes16(e, N, x0);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            reinterpret_cast<uint4*>(q)[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (x0 + 8 * j < N) reinterpret_cast<uint2*>(q)[j] = make_uint2(w[2 * j], w[2 * j + 1]);
+      for (int j = 0; j < 4; ++j) {
+        const uint4 w = *box_chunk64(box, 8 * j + (lane >> 2), lane & 3);
+        int8_t* at = q + 8 * j * e.ldq;
+        if (m + 8 * j < M) {
+          if (wide) {
+            *reinterpret_cast<uint4*>(at) = w;
+          } else {
+            if (n < N) reinterpret_cast<uint2*>(at)[0] = make_uint2(w.x, w.y);
+            if (n + 8 < N) reinterpret_cast<uint2*>(at)[1] = make_uint2(w.z, w.w);
+          }
         }
-        e.scales[x0 / kCkptGroup * e.lds + grow] = scale;
       }
+      __syncwarp();
+    }
+    if (e.res) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) *box_chunk128(box, 4 * j + (lane >> 3), lane & 7) = s.side[j];
     }
     with_activation(e.act, [&](auto a) {
 #pragma unroll
@@ -367,15 +404,23 @@ __device__ __forceinline__ void lin_row64(uint8_t* row, int lane, f32x2 (&v)[32]
       }
     });
     if (e.res) {
+      __syncwarp();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) add8(v + 4 * j, s.side[j]);
+      for (int j = 0; j < 8; ++j) add8(v + 4 * j, *box_chunk128(box, lane, j));
+      // (a lane overwrites below what it alone has read)
     }
   } else if (e.codes) {
-    uint16_t* h = e.h + grow * e.ldh + x0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) *box_chunk64(box, 8 * j + (lane >> 2), lane & 3) = s.side[j];
+    __syncwarp();
+    uint4 codes[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) codes[j] = *box_chunk64(box, lane, j);
+    __syncwarp();
     with_activation(e.act, [&](auto a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const uint32_t w[2] = {j & 1 ? s.side[j / 2].z : s.side[j / 2].x, j & 1 ? s.side[j / 2].w : s.side[j / 2].y};
+        const uint32_t w[2] = {j & 1 ? codes[j / 2].z : codes[j / 2].x, j & 1 ? codes[j / 2].w : codes[j / 2].y};
         f32x2 f[4], df;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -383,12 +428,23 @@ __device__ __forceinline__ void lin_row64(uint8_t* row, int lane, f32x2 (&v)[32]
           activate<decltype(a)::value, true>(u, f[i], df);
           v[4 * j + i] = mul2(v[4 * j + i], df);
         }
-        if (e.h && in_m && x0 + 8 * j < N) *reinterpret_cast<uint4*>(h + 8 * j) = pack8(f);
+        if (e.h) *box_chunk128(box, lane, j) = pack8(f);
       }
     });
+    if (e.h) {
+      __syncwarp();
+      const int64_t m = row0 + (lane >> 3), n = x0 + 8 * (lane & 7);
+      uint16_t* h = e.h + m * e.ldh + n;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint4 w = *box_chunk128(box, 4 * j + (lane >> 3), lane & 7);
+        if (m + 4 * j < M && n < N) *reinterpret_cast<uint4*>(h + 4 * j * e.ldh) = w;
+      }
+      __syncwarp();
+    }
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(row + ((j ^ (lane & 7)) << 4)) = pack8(v + 4 * j);
+  for (int j = 0; j < 8; ++j) *box_chunk128(box, lane, j) = pack8(v + 4 * j);
 }
 
 }  // namespace hg
