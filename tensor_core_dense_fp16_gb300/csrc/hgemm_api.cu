@@ -862,6 +862,7 @@ int run_wgrad(const LinearProduct& p, float* dbias, bool accumulate, cudaStream_
   Gemm g{p.A, p.B, p.C, p.M, p.N, p.K, p.lda, p.ldb, p.ldc};
   g.a_mn = p.a_mn;
   g.b_mn = p.b_mn;
+  bool thin = false;  // the product's kernel leaves room beside it on an SM
   if (p.K > 0 && (forced == HGEMM_PATH_GENERIC || !tma_ok(g))) {
     rc = run_linear(p, stream);
   } else if (forced < 0 && linear_small_suits(p, dev->num_sms)) {
@@ -876,9 +877,10 @@ int run_wgrad(const LinearProduct& p, float* dbias, bool accumulate, cudaStream_
       epi.mode = 2;
     }
     rc = dispatch(g, epi, *dev, stream);
+    thin = !p.epi.res;  // (the epilogue that reads old values takes the registers)
   }
   if (rc != HGEMM_OK || !dbias) return rc;
-  return cuda_status(launch_column_sums(p.A, p.lda, p.K, p.M, dbias, accumulate, true, stream));
+  return cuda_status(launch_column_sums(p.A, p.lda, p.K, p.M, dbias, accumulate, true, thin, stream));
 }
 
 }  // namespace hg

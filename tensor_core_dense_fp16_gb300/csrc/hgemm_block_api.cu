@@ -122,7 +122,7 @@ int hgemm_linear_wgrad(const hgemm_half_t* dY, int64_t lddy, const hgemm_half_t*
     return hg::run_wgrad(p, dbias, accumulate != 0, stream);
   }
   if (!dbias) return HGEMM_OK;
-  return hg::cuda_status(hg::launch_column_sums(dY, lddy, M, N, dbias, accumulate != 0, false, stream));
+  return hg::cuda_status(hg::launch_column_sums(dY, lddy, M, N, dbias, accumulate != 0, false, false, stream));
 }
 
 int hgemm_layernorm_forward(const hgemm_half_t* X, int64_t ldx, const hgemm_half_t* gamma, const hgemm_half_t* beta,

@@ -257,6 +257,77 @@ __global__ void __launch_bounds__(kSumThreads)
   if (beside && blockIdx.x == 0) grid_dependency_wait();
 }
 
+// The same beside a product that fills every SM: blocks small enough for what
+// the pair and wide kernels leave of an SM (1.8 KB of shared memory with the
+// block's own 1 KB, registers for 256 threads of 64), so they read dY while
+// the product, bound by the matrix instructions, runs. A block takes 64 columns
+// (8 lanes along a row, 16 bytes each, 32 rows at a time) of a run of rows; its
+// cluster adds the runs in rank order. With the product, which alone takes the
+// first time, us, and with the wide blocks above: dY 8192×8192, X 8192×2048
+// 157, 162, 180; 4096×8192, 4096×2048 82, 84, 93; 2048 all 14.7, 16.5, 20.3;
+// but 8192×2048, 8192×8192 156, 171, 164.
+constexpr int kThinColumns = 64;
+constexpr int kThinThreads = 256;
+__global__ void __launch_bounds__(kThinThreads)
+    column_sums_thin_kernel(const uint16_t* __restrict__ dy, int64_t ld, int64_t M, int64_t N, float* __restrict__ out,
+                            int accumulate, int cluster) {
+  __shared__ float s[3][kThinColumns];
+  constexpr int WARPS = kThinThreads / 32, STEP = 4 * WARPS;  // rows per step
+  const int rank = static_cast<int>(blockIdx.x) % cluster;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) / cluster * kThinColumns, n = n0 + 8 * (lane & 7);
+  const int64_t m1 = M * (rank + 1) / cluster;
+  f32x2 sum[4] = {};
+  if (n < N) {
+    const uint16_t* p = dy + n;
+    for (int64_t m = M * rank / cluster + warp * 4 + (lane >> 3); m < m1; m += STEP * kUnroll) {
+      uint4 v[kUnroll];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k)
+        v[k] = m + k * STEP < m1 ? __ldg(reinterpret_cast<const uint4*>(p + (m + k * STEP) * ld))
+                                 : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) add8(sum, v[k]);
+    }
+  }
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) unpair(sum[i], v[2 * i], v[2 * i + 1]);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] += __shfl_xor_sync(0xffffffffu, v[i], 8);
+    v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
+  }
+  // warp 0 adds the others' in order, three at a time
+#pragma unroll
+  for (int w0 = 1; w0 < WARPS; w0 += 3) {
+    if (w0 > 1) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (warp >= w0 && warp < w0 + 3 && lane < 8) s[warp - w0][8 * lane + i] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int w = w0; w < w0 + 3 && w < WARPS; ++w)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (warp == 0 && lane < 8) v[i] += s[w - w0][8 * lane + i];
+  }
+  if (warp == 0 && lane < 8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[0][8 * lane + i] = v[i];
+  }
+  cluster_sync();
+  if (rank == 0 && threadIdx.x < kThinColumns && n0 + threadIdx.x < N) {
+    float total = s[0][threadIdx.x];
+    for (int i = 1; i < cluster; ++i)
+      total += ld_cluster_f32(mapa_shared(smem_u32(&s[0][threadIdx.x]), static_cast<uint32_t>(i)));
+    float* o = out + n0 + threadIdx.x;
+    *o = accumulate ? *o + total : total;
+  }
+  cluster_sync();  // the other ranks' shared memory stays until rank 0 has read it
+  if (blockIdx.x == 0) grid_dependency_wait();
+}
+
 }  // namespace
 
 bool linear_rows_suits(const LinearProduct& p) {
@@ -289,8 +360,17 @@ cudaError_t launch_linear_empty(uint16_t* C, int64_t ldc, int64_t M, int64_t N, 
 }
 
 cudaError_t launch_column_sums(const uint16_t* dy, int64_t ld, int64_t M, int64_t N, float* out, bool accumulate,
-                               bool beside, cudaStream_t stream) {
+                               bool beside, bool thin, cudaStream_t stream) {
   const bool vec = N % 8 == 0 && ld % 8 == 0 && (reinterpret_cast<uintptr_t>(dy) & 15u) == 0;
+  if (beside && vec && thin) {
+    int runs = 1;
+    while (runs < 8 && M >= 256 * runs) runs *= 2;
+    const int64_t grid = (N + kThinColumns - 1) / kThinColumns * runs;
+    if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    PdlLaunch l(dim3(static_cast<unsigned>(grid)), dim3(kThinThreads), 0, stream);
+    l.cluster(static_cast<unsigned>(runs));
+    return cudaLaunchKernelEx(&l.cfg, column_sums_thin_kernel, dy, ld, M, N, out, accumulate ? 1 : 0, runs);
+  }
   const int vec_cols = vec ? 8 : 1;
   // up to 8 CTAs (the portable cluster size) per strip, 128 rows or more each
   int cluster = 1;

@@ -224,9 +224,9 @@ cudaError_t launch_trsm_leaf(const uint16_t* A, int64_t lda, uint16_t* X, int64_
 
 // Σ over the rows of dY (M×N): out[n], or out[n] + the sum. beside: the launch
 // before it on the stream is the product that reads the same dY, which the
-// sums may run beside (see the kernel).
+// sums may run beside; thin: on the same SMs (see the kernels).
 cudaError_t launch_column_sums(const uint16_t* dy, int64_t ld, int64_t M, int64_t N, float* out,
-                               bool accumulate, bool beside, cudaStream_t stream);
+                               bool accumulate, bool beside, bool thin, cudaStream_t stream);
 // K = 0: C = the epilogue of zeros.
 cudaError_t launch_linear_empty(uint16_t* C, int64_t ldc, int64_t M, int64_t N, const LinEpi& epi,
                                 cudaStream_t stream);

@@ -453,6 +453,12 @@ def test_small_weights_of_many_rows(M, N, K, accumulate):
     run_wgrad(M, N, K, bias=False, accumulate=accumulate)
 
 
+@pytest.mark.parametrize("M,N,K", [(300, 4360, 2056), (2050, 2600, 2048), (77, 9000, 1032)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_bias_gradient_beside_many_tiles(M, N, K, accumulate):
+    run_wgrad(M, N, K, accumulate=accumulate)
+
+
 def test_bias_gradient_beside_its_product():
     """The column sums may run beside the product: what comes before the pair
     of launches on the stream and what comes after keep their order."""
