@@ -848,7 +848,16 @@ int run_linear(const LinearProduct& p, cudaStream_t stream) {
   if (p.K > 0 && (forced == HGEMM_PATH_GENERIC || !tma_ok(g))) {
     const CallDevice cd{dev->num_sms, t_ctx.status, g_timeout_ns.load(std::memory_order_relaxed),
                         g_inject.load(std::memory_order_relaxed)};
-    return cuda_status(launch_linear_any(p, cd, stream));
+    auto rows = [](const void* q, int64_t ld) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0 && ld % 8 == 0; };
+    if (forced == HGEMM_PATH_GENERIC || !rows(p.A, p.lda) || !rows(p.B, p.ldb))
+      return cuda_status(launch_linear_any(p, nullptr, nullptr, cd, stream));
+    // only the epilogue's side is odd
+    CUtensorMap ma, mb;
+    int e = p.a_mn ? encode_map(&ma, p.A, p.K, p.M, p.lda, kTcBK, 64) : encode_map(&ma, p.A, p.M, p.K, p.lda, 128, kTcBK);
+    if (e != HGEMM_OK) return e;
+    e = p.b_mn ? encode_map(&mb, p.B, p.K, p.N, p.ldb, kTcBK, 64) : encode_map(&mb, p.B, p.N, p.K, p.ldb, 128, kTcBK);
+    if (e != HGEMM_OK) return e;
+    return cuda_status(launch_linear_any(p, &ma, &mb, cd, stream));
   }
   if (forced < 0 && linear_cluster_suits(p, dev->num_sms)) return run_linear_cluster(p, nullptr, false, stream);
   return dispatch(g, kPlainEpilogue, *dev, stream);

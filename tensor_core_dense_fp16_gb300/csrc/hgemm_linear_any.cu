@@ -8,13 +8,20 @@
 // accumulators, an epilogue that drains the other. What differs is who fills
 // the ring. An operand's tile of a K block is 128 segments of 128 bytes: rows
 // of 64 k, or (an M- or N-contiguous operand) for each of 64 k two runs of 64
-// rows, which is TMA's MN-major layout. Eight lanes read a segment, each the
-// two aligned 16-byte pieces that its 16 bytes lie in, so that a read is one
-// run of memory whatever the pitch, and shift them together. How far is the
-// same in every K block (a block is 128 bytes on, or 64 pitches), so a lane
-// keeps its pointers and its shift for a whole output tile, and a K block
-// costs a warp some 130 instructions: the loaders are bound by those.
-// Nothing outside a matrix is read: what a tile has there is zeros.
+// rows, which is TMA's MN-major layout. A loader warp copies the nine aligned
+// 16-byte pieces that each of its segments touches into a buffer of its own,
+// two K blocks ahead (asynchronous copies: what is under way occupies no
+// registers), then shifts them into the tile, eight lanes to a segment. How far
+// is the same in every K block (a block is 128 bytes on, or 64 pitches), so a
+// lane keeps its pointers and its shifts for a whole output tile. Bound by
+// the loaders' instructions: a K block takes them 1.3 us (8192×2049 outputs of
+// a contraction of 2047, GELU and residual: 371 us; 1001^3 46 us, 20 of them
+// the epilogue of the one wave of tiles). Where only the outputs are odd, one
+// thread loads the tiles by TMA instead (2000×2001, contraction 2000: 54 us, by
+// the loader warps 102).
+// Nothing past a matrix's last element is read, and before its first one at
+// most the rest of the same aligned 16 bytes; what a tile has outside the
+// matrix is zeros.
 #include <atomic>
 
 #include <cuda_fp16.h>
@@ -28,7 +35,7 @@ namespace hg {
 namespace {
 
 struct AnyCfg {
-  static constexpr int BM = 128, BN = 128, BK = 64, STAGES = 5, UMMA_K = 16;
+  static constexpr int BM = 128, BN = 128, BK = 64, STAGES = 3, UMMA_K = 16;
   static constexpr int TILE_BYTES = 128 * BK * 2;  // of either operand
   static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
   static constexpr int LOADERS = 16;                // warps 0 .. 15
@@ -44,12 +51,19 @@ struct AnyCfg {
   // ... or, where the outputs are aligned, stages 32 rows × 64 columns
   static constexpr int BOX_BYTES = 32 * 128;
   static_assert(BOX_BYTES >= TURN_WORDS * 4, "either fits");
-  static constexpr int OFF_TURN = STAGES * STAGE_BYTES;
+  // the pieces of a loader warp's segments of either operand
+  static constexpr int PIECES = 2 * SEGMENTS * 9;
+  static constexpr int RAW_STAGES = 3;
+  static constexpr int RAW_BYTES = PIECES * 16;  // of a warp and K block
+  static constexpr int OFF_RAW = STAGES * STAGE_BYTES;
+  static constexpr int TMA_STAGES = 6;           // with tensor maps the buffers are ring as well
+  static constexpr int OFF_TURN = OFF_RAW + LOADERS * RAW_STAGES * RAW_BYTES;
   static constexpr int OFF_BAR = OFF_TURN + EPI_WARPS * BOX_BYTES;
-  static constexpr int NUM_BARS = 2 * STAGES + 5;  // full, empty, accumulator full ×2 and empty ×2, drain
+  static constexpr int NUM_BARS = 2 * TMA_STAGES + 5;  // full, empty, accumulator full ×2 and empty ×2, drain
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
   static constexpr uint32_t IDESC = idesc_f16_f32acc(BM, BN);
+  static_assert(TMA_STAGES * STAGE_BYTES <= OFF_TURN, "the ring of tensor-map loads fits");
   static_assert(OFF_BAR % 8 == 0, "aligned barriers");
   static_assert(SMEM_BYTES <= 232448, "exceeds 227 KB of shared memory per CTA");
 };
@@ -59,6 +73,7 @@ struct AnyArgs {
   int64_t num_m, num_n, units;
   int num_kb;
   int wide;  // the epilogue can read and write eight columns at a time
+  int tma;   // tensor maps describe the operands
   int* status;
   unsigned long long timeout_ns;
   int inject;  // HGEMM_INJECT_* (testing the watchdog)
@@ -70,94 +85,60 @@ struct AnyOperand {
   const uint16_t* end;  // past its last element
   int64_t ld, rows, K;
   bool mn;
-  bool vec;  // 16-byte-aligned segments
+  bool aligned;  // every segment begins on 16 bytes
 };
 
 constexpr int kAnyGroups = AnyCfg::SEGMENTS / 4;  // of four segments, eight lanes each
+constexpr int kAnyCopies = (AnyCfg::PIECES + 31) / 32;
 
-// A loader warp's way along K: its segment j of the current block starts at
-// src + j·ld. at, shift: for each group, the aligned piece this lane reads
-// first and how many elements into it the lane's own eight begin.
-struct AnyCursor {
-  const uint16_t* src;
-  int64_t left;  // K that remains: of the segments' elements, or (mn) of the segments
-  int fixed;     // rows that are inside: segments, or (mn) elements
-  const uint16_t* at[kAnyGroups];
-  int shift[kAnyGroups];
-};
 __device__ __forceinline__ int any_clamp(int64_t v, int most) {
   return v < 0 ? 0 : (v < most ? static_cast<int>(v) : most);
 }
-__device__ __forceinline__ AnyCursor any_start(const AnyOperand& o, int warp, int lane, int64_t i0) {
+
+// A loader warp's segments of an operand's block: segment j starts at
+// src + j·ld.
+struct AnySegments {
+  const uint16_t* src;
+  int64_t left;  // K that remains: of the segments' elements, or (mn) of the segments
+  int fixed;     // rows that are inside: segments, or (mn) elements
+};
+__device__ __forceinline__ AnySegments any_start(const AnyOperand& o, int warp, int64_t i0) {
   const int s = warp * AnyCfg::SEGMENTS;
   const int64_t i = o.mn ? i0 + (s & 64) : i0 + s, k = o.mn ? s & 63 : 0;
-  AnyCursor c;
-  c.src = o.p + (o.mn ? k * o.ld + i : i * o.ld);
-  c.left = o.K - k;
-  c.fixed = any_clamp(o.rows - i, o.mn ? 64 : AnyCfg::SEGMENTS);
-#pragma unroll
-  for (int g = 0; g < kAnyGroups; ++g) {
-    const uint16_t* mine = c.src + (4 * g + (lane >> 3)) * o.ld + 8 * (lane & 7);
-    c.shift[g] = static_cast<int>(reinterpret_cast<uintptr_t>(mine) >> 1) & 7;
-    c.at[g] = mine - c.shift[g];
-  }
-  return c;
+  return AnySegments{o.p + (o.mn ? k * o.ld + i : i * o.ld), o.K - k,
+                     any_clamp(o.rows - i, o.mn ? 64 : AnyCfg::SEGMENTS)};
 }
-// The next K block: a multiple of 16 bytes on, so that the shifts stay.
-__device__ __forceinline__ void any_advance(const AnyOperand& o, AnyCursor& c) {
-  const int64_t step = o.mn ? AnyCfg::BK * o.ld : AnyCfg::BK;
-  c.src += step;
-  c.left -= AnyCfg::BK;
-#pragma unroll
-  for (int g = 0; g < kAnyGroups; ++g) c.at[g] += step;
+// How many elements into its first aligned piece a segment begins.
+__device__ __forceinline__ int any_shift(const uint16_t* segment) {
+  return static_cast<int>(reinterpret_cast<uintptr_t>(segment) >> 1) & 7;
 }
 
-// A warp's part of one operand's block, on its way to shared memory.
-struct AnyPieces {
-  uint4 lo[kAnyGroups], hi[kAnyGroups];
-  bool joined;  // lo is what goes into the tile
-};
-
-__device__ __forceinline__ void load_pieces(const AnyOperand& o, const AnyCursor& c, int lane, AnyPieces& r) {
-  using Cfg = AnyCfg;
-  const int count = o.mn ? c.fixed : any_clamp(c.left, 64);
-  const int valid = o.mn ? any_clamp(c.left, Cfg::SEGMENTS) : c.fixed;
-  r.joined = o.vec;
-  if (count == 64 && valid == Cfg::SEGMENTS &&
-      (o.vec || (c.src - 7 >= o.p && c.src + (Cfg::SEGMENTS - 1) * o.ld + 72 <= o.end))) {
-    // every piece lies inside the matrix
-#pragma unroll
-    for (int g = 0; g < kAnyGroups; ++g) r.lo[g] = __ldg(reinterpret_cast<const uint4*>(c.at[g]));
-    if (!o.vec) {
-#pragma unroll
-      for (int g = 0; g < kAnyGroups; ++g) r.hi[g] = __ldg(reinterpret_cast<const uint4*>(c.at[g]) + 1);
-    }
-    return;
-  }
-  r.joined = true;
-#pragma unroll
-  for (int g = 0; g < kAnyGroups; ++g) {
-    const uint16_t* src = c.at[g] + c.shift[g];
-    const int left = 4 * g + (lane >> 3) < valid ? count - 8 * (lane & 7) : 0;
-    uint32_t h[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = i < left ? __ldg(src + i) : 0u;
-    r.lo[g] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
-  }
+// One aligned piece at an edge on its way into the warp's buffer: what is past
+// the matrix's last element is not read and becomes zeros.
+__device__ __forceinline__ void any_copy_edge(const AnyOperand& o, const uint16_t* at, uint32_t dst) {
+  const int elements = any_clamp(o.end - at, 8);
+  cp_async_16(dst, elements > 0 ? at : o.p - any_shift(o.p), 2 * elements);
 }
 
-__device__ __forceinline__ void store_pieces(const int (&shift)[kAnyGroups], const AnyPieces& r, uint8_t* tile,
-                                             int warp, int lane) {
+// The pieces of an operand's segments from the buffer into its tile. count,
+// valid: the elements of a segment and the segments that are inside.
+__device__ __forceinline__ void any_shift_in(const uint8_t* raw, const int (&shift)[kAnyGroups], bool aligned, int count, int valid,
+                                             uint8_t* tile, int warp, int lane) {
   using Cfg = AnyCfg;
   // (a warp's first segment is a multiple of 8: segment j's swizzle is j % 8)
   static_assert(Cfg::SEGMENTS % 8 == 0, "the swizzle of a warp's segments");
 #pragma unroll
   for (int g = 0; g < kAnyGroups; ++g) {
     const int j = 4 * g + (lane >> 3);
-    uint4 v = r.lo[g];
-    if (!r.joined) {
+    const uint4* from = reinterpret_cast<const uint4*>(raw) + j * 9 + (lane & 7);
+    uint32_t v[4];
+    const uint4 lo = from[0];
+    if (aligned) {
+      v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w;
+    } else {
+      const uint4 hi = from[1];
       // words shift / 2 .. of the eight, half a word on for an odd shift
-      const uint32_t w[8] = {r.lo[g].x, r.lo[g].y, r.lo[g].z, r.lo[g].w, r.hi[g].x, r.hi[g].y, r.hi[g].z, r.hi[g].w};
+      const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
       const bool two = (shift[g] & 4) != 0, one = (shift[g] & 2) != 0;
       uint32_t x[6], y[5];
 #pragma unroll
@@ -165,10 +146,16 @@ __device__ __forceinline__ void store_pieces(const int (&shift)[kAnyGroups], con
 #pragma unroll
       for (int i = 0; i < 5; ++i) y[i] = one ? x[i + 1] : x[i];
       const uint32_t bits = static_cast<uint32_t>(shift[g] & 1) << 4;
-      v = make_uint4(__funnelshift_r(y[0], y[1], bits), __funnelshift_r(y[1], y[2], bits),
-                     __funnelshift_r(y[2], y[3], bits), __funnelshift_r(y[3], y[4], bits));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = __funnelshift_r(y[i], y[i + 1], bits);
     }
-    *reinterpret_cast<uint4*>(tile + (warp * Cfg::SEGMENTS + j) * 128 + (((lane & 7) ^ (j & 7)) << 4)) = v;
+    if (count < 64 || valid < Cfg::SEGMENTS) {
+      const int left = j < valid ? count - 8 * (lane & 7) : 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = 2 * i + 1 < left ? v[i] : 2 * i < left ? v[i] & 0xFFFFu : 0u;
+    }
+    *reinterpret_cast<uint4*>(tile + (warp * Cfg::SEGMENTS + j) * 128 + (((lane & 7) ^ (j & 7)) << 4)) =
+        make_uint4(v[0], v[1], v[2], v[3]);
   }
 }
 
@@ -256,7 +243,8 @@ __device__ __noinline__ void any_columns(const LinearProduct& p, const float* tu
 }
 
 template <bool BACKWARD>
-__global__ void __launch_bounds__(AnyCfg::THREADS, 1) linear_any_kernel(const AnyArgs a) {
+__global__ void __launch_bounds__(AnyCfg::THREADS, 1)
+    linear_any_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const AnyArgs a) {
   using Cfg = AnyCfg;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -266,17 +254,18 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1) linear_any_kernel(const An
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::OFF_MISC + 4);
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
-  auto empty_bar = [&](int s) { return bar0 + 8u * (Cfg::STAGES + s); };
-  auto accf_bar = [&](int b) { return bar0 + 8u * (2 * Cfg::STAGES + b); };
-  auto acce_bar = [&](int b) { return bar0 + 8u * (2 * Cfg::STAGES + 2 + b); };
-  const uint32_t drain_bar = bar0 + 8u * (2 * Cfg::STAGES + 4);
+  auto empty_bar = [&](int s) { return bar0 + 8u * (Cfg::TMA_STAGES + s); };
+  auto accf_bar = [&](int b) { return bar0 + 8u * (2 * Cfg::TMA_STAGES + b); };
+  auto acce_bar = [&](int b) { return bar0 + 8u * (2 * Cfg::TMA_STAGES + 2 + b); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * Cfg::TMA_STAGES + 4);
+  const int stages = a.tma ? Cfg::TMA_STAGES : Cfg::STAGES;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Watchdog wd{abort_flag, a.status, a.timeout_ns};
   const LinearProduct& p = a.p;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < Cfg::STAGES; ++s) {
-      mbar_init(full_bar(s), Cfg::LOADERS);  // one arrival per loader warp
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(full_bar(s), a.tma ? 1 : Cfg::LOADERS);  // the producer, or one arrival per loader warp
       mbar_init(empty_bar(s), 1);            // tcgen05.commit
     }
     for (int b = 0; b < 2; ++b) {
@@ -298,49 +287,144 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1) linear_any_kernel(const An
   grid_dependency_wait();
   grid_launch_dependents();
 
-  if (warp < Cfg::LOADERS) {
+  if (a.tma && warp < Cfg::LOADERS) {
+    // ------------------------------- TMA producer (only the outputs are odd)
+    if (warp == 0 && elect_one()) {
+      int stage = 0;
+      uint32_t phase = 0;
+      long long issued = 0;
+      bool ok = true;
+      for (int64_t t = blockIdx.x; ok && t < a.units; t += gridDim.x) {
+        const AnyUnit u = any_unit(a, t);
+        const int m0 = static_cast<int>(u.m0), n0 = static_cast<int>(u.n0);
+        for (int kb = 0; kb < a.num_kb; ++kb) {
+          ok = wait_phase(empty_bar(stage), phase ^ 1u, wd, kWdProducerEmpty);
+          if (!ok) break;
+          if (!(a.inject == 1 && issued == 0))  // testing aid: withhold one arrival
+            mbar_arrive_expect_tx(full_bar(stage), Cfg::STAGE_BYTES);
+          const uint32_t sa = sbase + stage * Cfg::STAGE_BYTES, sb = sa + Cfg::TILE_BYTES;
+          const int kx = kb * Cfg::BK;
+          if (p.a_mn) {
+            tma_load_2d(sa, &tmA, full_bar(stage), m0, kx);
+            tma_load_2d(sa + kMnBoxBytes, &tmA, full_bar(stage), m0 + kMnBox, kx);
+          } else {
+            tma_load_2d(sa, &tmA, full_bar(stage), kx, m0);
+          }
+          if (p.b_mn) {
+            tma_load_2d(sb, &tmB, full_bar(stage), n0, kx);
+            tma_load_2d(sb + kMnBoxBytes, &tmB, full_bar(stage), n0 + kMnBox, kx);
+          } else {
+            tma_load_2d(sb, &tmB, full_bar(stage), kx, n0);
+          }
+          ++issued;
+          if (++stage == stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // the last loads must have landed before the CTA's memory goes away
+      int s = stage;
+      uint32_t ph = phase;
+      for (long long i = 0; i < issued && i < stages; ++i) {
+        if (s == 0) {
+          s = stages - 1;
+          ph ^= 1u;
+        } else {
+          --s;
+        }
+        wait_drain(full_bar(s), ph, wd);
+      }
+    }
+    __syncwarp();
+  } else if (warp < Cfg::LOADERS) {
     // ------------------------------------------------------------ loaders
-    auto vec = [](const uint16_t* q, int64_t ld) {
-      return (reinterpret_cast<uintptr_t>(q) & 15u) == 0 && ld % 8 == 0;
-    };
     auto operand = [&](const uint16_t* q, int64_t ld, int64_t rows, bool mn) {
       const uint16_t* end = q + (mn ? (p.K - 1) * ld + rows : (rows - 1) * ld + p.K);
-      return AnyOperand{q, end, ld, rows, p.K, mn, vec(q, ld)};
+      return AnyOperand{q, end, ld, rows, p.K, mn, (reinterpret_cast<uintptr_t>(q) & 15u) == 0 && ld % 8 == 0};
     };
     const AnyOperand oa = operand(p.A, p.lda, p.M, p.a_mn), ob = operand(p.B, p.ldb, p.N, p.b_mn);
+    const int64_t step_a = oa.mn ? Cfg::BK * oa.ld : Cfg::BK, step_b = ob.mn ? Cfg::BK * ob.ld : Cfg::BK;
+    uint8_t* raw = smem + Cfg::OFF_RAW + warp * Cfg::RAW_STAGES * Cfg::RAW_BYTES;
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    AnyPieces pa, pb;
     for (int64_t t = blockIdx.x; ok && t < a.units; t += gridDim.x) {
       const AnyUnit u = any_unit(a, t);
-      AnyCursor ca = any_start(oa, warp, lane, u.m0), cb = any_start(ob, warp, lane, u.n0);
-      load_pieces(oa, ca, lane, pa);
-      load_pieces(ob, cb, lane, pb);
+      const AnySegments ca = any_start(oa, warp, u.m0), cb = any_start(ob, warp, u.n0);
+      // this lane's pieces: piece i % 9 of segment i / 9, A's segments first
+      const uint16_t* at[kAnyCopies];
+      int shift_a[kAnyGroups], shift_b[kAnyGroups];
+#pragma unroll
+      for (int c = 0; c < kAnyCopies; ++c) {
+        const int i = lane + 32 * c, j = i / 9;
+        const uint16_t* seg = j < Cfg::SEGMENTS ? ca.src + j * oa.ld : cb.src + (j - Cfg::SEGMENTS) * ob.ld;
+        at[c] = seg - any_shift(seg) + i % 9 * 8;
+      }
+#pragma unroll
+      for (int g = 0; g < kAnyGroups; ++g) {
+        shift_a[g] = any_shift(ca.src + (4 * g + (lane >> 3)) * oa.ld);
+        shift_b[g] = any_shift(cb.src + (4 * g + (lane >> 3)) * ob.ld);
+      }
+      int filled = 0;  // buffer of the next block to copy
+      const uint16_t *src_a = ca.src, *src_b = cb.src;  // of the next block to copy
+      auto inside = [&](const AnyOperand& o, const uint16_t* src) {  // every piece
+        return src + (Cfg::SEGMENTS - 1) * o.ld + 72 <= o.end;
+      };
+      auto copy = [&](bool some) {
+        if (some) {
+          const bool whole = inside(oa, src_a) && inside(ob, src_b);
+          uint8_t* dst = raw + filled * Cfg::RAW_BYTES + lane * 16;
+#pragma unroll
+          for (int c = 0; c < kAnyCopies; ++c) {
+            const int i = lane + 32 * c;
+            const bool of_a = i < Cfg::PIECES / 2;
+            if (i < Cfg::PIECES) {
+              if (whole)
+                cp_async_16(smem_u32(dst + 32 * 16 * c), at[c], 16);
+              else
+                any_copy_edge(of_a ? oa : ob, at[c], smem_u32(dst + 32 * 16 * c));
+            }
+            at[c] += of_a ? step_a : step_b;
+          }
+          src_a += step_a;
+          src_b += step_b;
+        }
+        cp_async_commit();
+        if (++filled == Cfg::RAW_STAGES) filled = 0;
+      };
+      copy(true);
+      copy(a.num_kb > 1);
+      int used = 0;
       for (int kb = 0; kb < a.num_kb; ++kb) {
+        // (every lane has read the buffer that this overwrites)
+        __syncwarp();
+        copy(kb + 2 < a.num_kb);
         int good = 1;
         if (lane == 0) good = wait_phase(empty_bar(stage), phase ^ 1u, wd, kWdProducerEmpty) ? 1 : 0;
         ok = __shfl_sync(0xffffffffu, good, 0) != 0;
         if (!ok) break;
+        cp_async_wait<2>();
+        __syncwarp();
         uint8_t* tile = smem + stage * Cfg::STAGE_BYTES;
-        store_pieces(ca.shift, pa, tile, warp, lane);
-        store_pieces(cb.shift, pb, tile + Cfg::TILE_BYTES, warp, lane);
-        // the next block's reads start before this one is handed over
-        if (kb + 1 < a.num_kb) {
-          any_advance(oa, ca);
-          any_advance(ob, cb);
-          load_pieces(oa, ca, lane, pa);
-          load_pieces(ob, cb, lane, pb);
-        }
+        const uint8_t* from = raw + used * Cfg::RAW_BYTES;
+        const int64_t la = ca.left - static_cast<int64_t>(kb) * Cfg::BK, lb = cb.left - static_cast<int64_t>(kb) * Cfg::BK;
+        any_shift_in(from, shift_a, oa.aligned, oa.mn ? ca.fixed : any_clamp(la, 64),
+                     oa.mn ? any_clamp(la, Cfg::SEGMENTS) : ca.fixed, tile, warp, lane);
+        any_shift_in(from + Cfg::RAW_BYTES / 2, shift_b, ob.aligned, ob.mn ? cb.fixed : any_clamp(lb, 64),
+                     ob.mn ? any_clamp(lb, Cfg::SEGMENTS) : cb.fixed, tile + Cfg::TILE_BYTES, warp, lane);
         fence_proxy_async_smem();
         __syncwarp();
         // (testing aid: one warp withholds one arrival)
         if (lane == 0 && !(a.inject == 1 && warp == 0 && kb == 0 && t == blockIdx.x)) mbar_arrive(full_bar(stage));
-        if (++stage == Cfg::STAGES) {
+        if (++stage == stages) {
           stage = 0;
           phase ^= 1u;
         }
+        if (++used == Cfg::RAW_STAGES) used = 0;
       }
+      cp_async_wait<0>();
+      __syncwarp();
     }
   } else if (warp == Cfg::MMA_WARP) {
     // -------------------------------------------------------- MMA issuer
@@ -369,7 +453,7 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1) linear_any_kernel(const An
           for (int k = 0; k < Cfg::BK / Cfg::UMMA_K; ++k)
             mma_f16_ss(d_tmem, a_desc + a_step * k, b_desc + b_step * k, idesc, (kb > 0 || k > 0) ? 1u : 0u);
           mma_commit(empty_bar(stage));
-          if (++stage == Cfg::STAGES) {
+          if (++stage == stages) {
             stage = 0;
             phase ^= 1u;
           }
@@ -486,7 +570,8 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1) linear_any_kernel(const An
 
 }  // namespace
 
-cudaError_t launch_linear_any(const LinearProduct& p, const CallDevice& dev, cudaStream_t stream) {
+cudaError_t launch_linear_any(const LinearProduct& p, const CUtensorMap* ma, const CUtensorMap* mb,
+                              const CallDevice& dev, cudaStream_t stream) {
   using Cfg = AnyCfg;
   static std::atomic<bool> attr_done[2][64];
   const int back = p.epi.backward ? 1 : 0;
@@ -511,12 +596,14 @@ cudaError_t launch_linear_any(const LinearProduct& p, const CallDevice& dev, cud
   };
   a.wide = p.N % 8 == 0 && rows(p.C, p.ldc, 16) && rows(p.epi.res, p.epi.ldr, 16) && rows(p.epi.h, p.epi.ldh, 16) &&
            rows(p.epi.codes, p.epi.ldq, 8);
+  a.tma = ma ? 1 : 0;
   a.status = dev.status;
   a.timeout_ns = dev.timeout_ns;
   a.inject = dev.inject;
   PdlLaunch l(dim3(static_cast<unsigned>(a.units < dev.num_sms ? a.units : dev.num_sms)), dim3(Cfg::THREADS),
               Cfg::SMEM_BYTES, stream);
-  return cudaLaunchKernelEx(&l.cfg, kern, a);
+  const CUtensorMap none{};
+  return cudaLaunchKernelEx(&l.cfg, kern, ma ? *ma : none, mb ? *mb : none, a);
 }
 
 // The -DHGEMM_DEBUG build's check word of this file (null otherwise).

@@ -290,7 +290,10 @@ cudaError_t launch_linear_small(const CUtensorMap& w, const CUtensorMap& x, cons
 int linear_small_clusters(int split, int num_sms);
 cudaError_t launch_linear_small(const CUtensorMap& w, const CUtensorMap& x, const SmallArgs& a, cudaStream_t stream);
 // The kernel for operands and outputs of any pitch and alignment; K > 0.
-cudaError_t launch_linear_any(const LinearProduct& p, const CallDevice& dev, cudaStream_t stream);
+// ma, mb: tensor maps of the operands (boxes of 128 rows, MN-major 64 by 64),
+// or null where there can be none.
+cudaError_t launch_linear_any(const LinearProduct& p, const CUtensorMap* ma, const CUtensorMap* mb,
+                              const CallDevice& dev, cudaStream_t stream);
 // The gradient of a weight: C = A·B, or C + A·B, with an epilogue that says
 // so; and, unless dbias is null, the sums of A's rows over K, beside the
 // product or within it.
