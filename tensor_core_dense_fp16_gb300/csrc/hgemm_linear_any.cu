@@ -17,8 +17,8 @@
 // the loaders' instructions: a K block takes them 1.3 us (8192×2049 outputs of
 // a contraction of 2047, GELU and residual: 371 us; 1001^3 46 us, 20 of them
 // the epilogue of the one wave of tiles). Where only the outputs are odd, one
-// thread loads the tiles by TMA instead (2000×2001, contraction 2000: 54 us, by
-// the loader warps 102).
+// thread loads the tiles by TMA instead and four of the loader warps join the
+// epilogue (2000×2001, contraction 2000: 38 us, by the loader warps 102).
 // Nothing past a matrix's last element is read, and before its first one at
 // most the rest of the same aligned 16 bytes; what a tile has outside the
 // matrix is zeros.
@@ -56,14 +56,16 @@ struct AnyCfg {
   static constexpr int RAW_STAGES = 3;
   static constexpr int RAW_BYTES = PIECES * 16;  // of a warp and K block
   static constexpr int OFF_RAW = STAGES * STAGE_BYTES;
-  static constexpr int TMA_STAGES = 6;           // with tensor maps the buffers are ring as well
+  // with tensor maps the buffers are ring as well, and staging of four more
+  // epilogue warps, which are otherwise loaders
+  static constexpr int TMA_STAGES = 5;
   static constexpr int OFF_TURN = OFF_RAW + LOADERS * RAW_STAGES * RAW_BYTES;
   static constexpr int OFF_BAR = OFF_TURN + EPI_WARPS * BOX_BYTES;
   static constexpr int NUM_BARS = 2 * TMA_STAGES + 5;  // full, empty, accumulator full ×2 and empty ×2, drain
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
   static constexpr uint32_t IDESC = idesc_f16_f32acc(BM, BN);
-  static_assert(TMA_STAGES * STAGE_BYTES <= OFF_TURN, "the ring of tensor-map loads fits");
+  static_assert(TMA_STAGES * STAGE_BYTES + EPI_WARPS * BOX_BYTES <= OFF_TURN, "the ring of tensor-map loads fits");
   static_assert(OFF_BAR % 8 == 0, "aligned barriers");
   static_assert(SMEM_BYTES <= 232448, "exceeds 227 KB of shared memory per CTA");
 };
@@ -270,7 +272,7 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(accf_bar(b), 1);               // tcgen05.commit
-      mbar_init(acce_bar(b), Cfg::EPI_WARPS);  // one arrival per epilogue warp
+      mbar_init(acce_bar(b), a.tma ? 2 * Cfg::EPI_WARPS : Cfg::EPI_WARPS);  // one arrival per epilogue warp
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -287,7 +289,7 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1)
   grid_dependency_wait();
   grid_launch_dependents();
 
-  if (a.tma && warp < Cfg::LOADERS) {
+  if (a.tma && warp < Cfg::LOADERS - Cfg::EPI_WARPS) {
     // ------------------------------- TMA producer (only the outputs are odd)
     if (warp == 0 && elect_one()) {
       int stage = 0;
@@ -337,7 +339,7 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1)
       }
     }
     __syncwarp();
-  } else if (warp < Cfg::LOADERS) {
+  } else if (!a.tma && warp < Cfg::LOADERS) {
     // ------------------------------------------------------------ loaders
     auto operand = [&](const uint16_t* q, int64_t ld, int64_t rows, bool mn) {
       const uint16_t* end = q + (mn ? (p.K - 1) * ld + rows : (rows - 1) * ld + p.K);
@@ -475,7 +477,10 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1)
     // are two runs of 16 neighbours. All 16 reads are under way at once.
     const LinEpi& e = p.epi;
     const int q = warp & 3;
-    uint8_t* box = smem + Cfg::OFF_TURN + (warp - Cfg::LOADERS) * Cfg::BOX_BYTES;
+    // with tensor maps, warps 12 .. 15 take the second 64 columns of a tile
+    const bool more = warp < Cfg::LOADERS;
+    const int first = more ? kCkptGroup : 0, step = a.tma ? Cfg::BN : kCkptGroup;
+    uint8_t* box = smem + (more ? Cfg::TMA_STAGES * Cfg::STAGE_BYTES : Cfg::OFF_TURN) + q * Cfg::BOX_BYTES;
     float* turn = reinterpret_cast<float*>(box);
     float* row_scale = turn + 32 * (Cfg::TURN_COLS + 1);
     float* row_inv = row_scale + 32;
@@ -493,7 +498,7 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1)
       if (!ok) break;
       tc_fence_after_sync();
       const int64_t gi = u.m0 + q * 32 + lane;
-      for (int64_t col0 = u.n0; col0 < u.n0 + Cfg::BN && col0 < p.N; col0 += kCkptGroup) {
+      for (int64_t col0 = u.n0 + first; col0 < u.n0 + Cfg::BN && col0 < p.N; col0 += step) {
         const uint32_t t_group = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                  static_cast<uint32_t>(acc * Cfg::BN + static_cast<int>(col0 - u.n0));
         if (a.wide) {
