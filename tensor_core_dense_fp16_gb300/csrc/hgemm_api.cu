@@ -736,28 +736,31 @@ int trmm_pipe(int dev, TrmmPipe** out) {
 namespace hg {
 
 // Whether the turned-around product for few rows or small outputs computes p,
-// and is the faster kernel. Measured (us, operands from memory):
-//   forward, against the kernel of matrix fragments, 16 rows: 4096×4096 9.6 to
-//   11.3, 8192×8192 24.3 to 32.6, but 1024×1024 4.3 to 3.6 (so: from 2^21
-//   weights on); against the 128×64 tiles, 128 rows: 2048×8192 13.8 to 19.4,
-//   8192×4096 19.5 to 22.9, but 8192×2048 13.5 to 12.2 and 512×512 8.5 to 5.9
-//   (so: not for more than 64 rows where one wave of those tiles covers the
-//   output and K is short);
-//   input gradient, against the split-K kernel: 64 rows 4096×1024 8.3 to 13.1,
-//   16 rows 512×512 5.0 to 6.4, 128 rows 8192×2048 14.2 to 18.5, but 128 rows
-//   1024×4096 10.8 to 8.5;
-//   weight gradient, against the split-K kernel: 16384 rows 512×512 18.2 to
-//   24.9, 5000 rows 200×304 10.4 to 14.9, but 4096 rows 1024×1024 (64 tiles)
-//   16.1 to 13.2 and 512 rows 512×512 8.6 to 5.7.
+// and is the faster kernel. Measured (us, this kernel | the next one):
+//   forward, 9 to 32 rows, against the kernel of matrix fragments: 16 rows
+//   4096×4096 9.6 | 11.3, 8192×8192 24.3 | 32.6, but 32 rows 1024×1024 4.7 | 3.8
+//   (so: from 2^21 weights on);
+//   more rows, against the clusters of 128×64 tiles: 128 rows 2048×8192 14.1 |
+//   22.5, 4096×4096 12.9 | 13.6, 9800×264, more than one wave, 7.0 | 11.5, but 64
+//   rows 8192×2048 10.6 | 9.9, 1024×1024 5.9 | 5.0 (so: where K is long, or the
+//   output wide; and where rows of many weights start between lines: 48 rows
+//   3000×1000 6.7 | 13.8, though 1000×1000 6.2 | 5.6);
+//   input gradient, against the same, 64 rows over 8192 features 12.7 | 21.2, 128
+//   rows 15.9 | 21.5, 32 rows over 1024 5.2 | 5.7, but 128 rows over 4096 15.5 |
+//   13.6, 64 rows over 1024 6.8 | 5.1;
+//   weight gradient, against the same: 16384 rows 512×512 16.7 | 32.0, 5000 rows
+//   200×304 10.5 | 16.2, 8192 rows 768×768 (36 tiles) 15.7 | 17.6, but 4096 rows
+//   1024×1024 (64 tiles) 14.3 | 11.1, 2048 rows 512×512 9.2 | 6.5.
 bool linear_small_suits(const LinearProduct& p, int num_sms) {
   auto rows = [](const void* q, int64_t ld) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0 && ld % 8 == 0; };
   if (p.K == 0 || !rows(p.A, p.lda) || !rows(p.B, p.ldb)) return false;
-  if (p.a_mn) return p.K >= 2048 && (p.M + 127) / 128 * ((p.N + 127) / 128) <= 36;
+  if (p.a_mn) return p.K >= 4096 && (p.M + 127) / 128 * ((p.N + 127) / 128) <= 36;
   if (p.M > kLinearSmall) return false;
-  if (p.epi.backward) return p.M <= 64 || p.K >= 2048;
+  if (p.epi.backward) return p.M <= 32 || p.K > 4096 || (p.M <= 64 && p.K > 2048);
   if (p.epi.codes || p.M <= kLinearFragmentRows) return false;
   if (p.M <= kLinearRows) return p.N * p.K >= int64_t(1) << 21;
-  return p.M <= 64 || p.K > 2048 || p.N > int64_t(kNarrowBN) * num_sms;
+  if (p.M <= 64 && p.ldb % 32 != 0 && p.N * p.K >= int64_t(1) << 21) return true;
+  return p.K > 2048 || p.N > int64_t(kNarrowBN) * num_sms;
 }
 
 int run_linear_small(const LinearProduct& p, const DeviceState& dev, cudaStream_t stream) {

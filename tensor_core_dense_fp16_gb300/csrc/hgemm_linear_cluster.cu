@@ -15,7 +15,8 @@
 //
 // Measured (us, in a graph, operands in L2), against the kernels of larger
 // outputs: 1000^3 with bias, SiLU and residual 8.8 to 6.6, its input gradient
-// with SiLU's and f(û) 9.6 to 7.0, its weight gradient 7.8 to 5.9; 1024^3
+// with SiLU's and f(û) 9.6 to 7.0, its weight gradient 7.8 to 5.9
+// (with bias 11.1 to 7.1); 1024^3
 // without epilogue 5.1 to 4.8; 1024×1024, contraction 4096, 13.1 to 11.7; the
 // one loss found is 1000×1000 with rows of 4000, 13.1 to 13.9. Of the 6.6 us,
 // 2.5 are launch and set-up, 2.2 the copies of 16 blocks, and 1.2 the epilogue:
@@ -58,33 +59,31 @@ struct ClCfg {
 // The sums over K of the half of the A tile that this CTA loads (64 rows), by
 // the epilogue warps while the product runs: the bias gradient beside the
 // weight's, from the stages in shared memory (MN-major: 64 K rows of 128
-// bytes). A thread adds the eight rows of A of one 16-byte chunk in every
-// 16th K row, and the 16 partial sums of a row are added in a fixed order. (A
-// CTA's own half, because then only its own loads wait for the sums. A kernel
-// of column sums beside the product took 5 us more: 1000^3, 6.0 us without.)
+// bytes). The four warps take K blocks in turn, so that none of them delays the
+// ring. A thread adds the eight rows of A of one 16-byte chunk in every fourth K
+// row of its warp's blocks, and the 16 partial sums of a row are added in a
+// fixed order. (A CTA's own half, because then only its own loads wait for the
+// sums. A kernel of column sums beside the product took 5 us more: 1000^3,
+// 6.0 us without.)
 __device__ __forceinline__ void sum_rows(const TcArgs& p, uint8_t* smem, uint32_t full0, uint32_t empty0, int half,
                                          int first, const Watchdog& wd) {
   using Cfg = ClCfg;
   const int t = static_cast<int>(threadIdx.x) - 64, lane = t & 31;
-  const int chunk = t & 7, k0 = t >> 3;
-  const uint8_t* src = smem + Cfg::OFF_A + half * kMnBoxBytes + k0 * 128 + ((chunk ^ (k0 & 7)) << 4);
+  const int chunk = t & 7, k0 = lane >> 3;
+  const uint8_t* tile = smem + Cfg::OFF_A + half * kMnBoxBytes;
   f32x2 sum[4] = {};
-  int stage = 0;
-  uint32_t phase = 0;
-  for (int kb = 0; kb < p.num_kb; ++kb) {
+  for (int kb = t >> 5; kb < p.num_kb; kb += Cfg::EPI_WARPS) {
+    const int stage = kb % Cfg::STAGES;
     int ok = 1;
-    if (lane == 0) ok = wait_phase(full0 + 8u * stage, phase, wd, kWdRows) ? 1 : 0;
+    if (lane == 0) ok = wait_phase(full0 + 8u * stage, kb / Cfg::STAGES & 1, wd, kWdRows) ? 1 : 0;
     ok = __shfl_sync(0xffffffffu, ok, 0);
     if (!ok) break;
+    const uint8_t* src = tile + stage * Cfg::A_BYTES;
 #pragma unroll
-    for (int i = 0; i < Cfg::BK / 16; ++i)
-      add8(sum, *reinterpret_cast<const uint4*>(src + stage * Cfg::A_BYTES + i * 16 * 128));
+    for (int i = 0; i < Cfg::BK / 4; ++i)
+      add8(sum, *reinterpret_cast<const uint4*>(src + (k0 + 4 * i) * 128 + ((chunk ^ (k0 + 4 * (i & 1))) << 4)));
     __syncwarp();
     if (lane == 0) mbar_arrive(empty0 + 8u * stage);
-    if (++stage == Cfg::STAGES) {
-      stage = 0;
-      phase ^= 1u;
-    }
   }
   float v[8];
 #pragma unroll
@@ -141,8 +140,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(ClCfg::THREADS, 1)
     for (int s = 0; s < Cfg::STAGES; ++s) {
       mbar_init(full_bar(s), 1);   // the producer's arrive.expect_tx (+ the bytes of three CTAs)
       // commits of the CTAs that received this CTA's halves, and its own
-      // summing warps
-      mbar_init(empty_bar(s), summed ? 3 + Cfg::EPI_WARPS : 3);
+      // summing warp
+      mbar_init(empty_bar(s), summed ? 4 : 3);
     }
     mbar_init(accf_bar, 1);
     mbar_init(drain_bar, 1);

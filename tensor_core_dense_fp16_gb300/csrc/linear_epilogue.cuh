@@ -274,8 +274,9 @@ __device__ __forceinline__ void tmem_row64(uint32_t taddr, f32x2 (&v)[32]) {
 // row of their own touches 32 lines per instruction. So residual, codes and
 // f(û) are read and written four or eight rows at a time, neighbouring lanes
 // taking neighbouring 16 bytes, and pass through the warp's staging box on the
-// way to or from the row's lane. (4096×4096 outputs of a contraction of 256,
-// GELU's gradient with f(û): [figures].)
+// way to or from the row's lane. (8192×8192 outputs of a contraction of
+// 2048, GELU's gradient with f(û): 185 us with a row per lane, 173 this way,
+// 150 without codes and f(û).)
 //
 // The 16-byte chunk j of row r of a box of 128-byte rows and of one of 64-byte
 // rows, permuted so that neither way of access meets bank conflicts.
