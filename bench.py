@@ -245,8 +245,10 @@ def load_peaks():
 # The source file of each kernel; with the shared headers and the build
 # flags it determines the compiled kernel, so a recorded ncu traffic figure
 # stays valid while their hash is unchanged.
-KERNEL_SOURCES = {"hgemm_tc_kernel": ("hgemm_tc.cu",), "hgemm_tc2_kernel": ("hgemm_tc2.cu",),
-                  "hgemm_tc2w_kernel": ("hgemm_tc2w.cu",), "hgemm_skinny_kernel": ("hgemm_skinny.cu",),
+KERNEL_SOURCES = {"hgemm_tc_kernel": ("hgemm_tc.cu", "linear_epilogue.cuh"),
+                  "hgemm_tc2_kernel": ("hgemm_tc2.cu", "linear_epilogue.cuh"),
+                  "hgemm_tc2w_kernel": ("hgemm_tc2w.cu",),
+                  "hgemm_skinny_kernel": ("hgemm_skinny.cu", "linear_epilogue.cuh"),
                   "hgemm_generic_kernel": ("hgemm_generic.cu",),
                   "trsm_chain_kernel": ("hgemm_trsm_chain.cu", "trsm_chain.h"),
                   "hgemm_tri_leaves_tc_kernel": ("hgemm_trileaf.cu",),

@@ -15,13 +15,12 @@
 //
 // Measured (us, in a graph, operands in L2), against the kernels of larger
 // outputs: 1000^3 with bias, SiLU and residual 8.8 to 6.6, its input gradient
-// with SiLU's and f(û) 9.6 to 7.0, its weight gradient 7.8 to 5.9
-// (with bias 11.1 to 7.1); 1024^3
-// without epilogue 5.1 to 4.8; 1024×1024, contraction 4096, 13.1 to 11.7; the
-// one loss found is 1000×1000 with rows of 4000, 13.1 to 13.9. Of the 6.6 us,
-// 2.5 are launch and set-up, 2.2 the copies of 16 blocks, and 1.2 the epilogue:
-// its two special-function instructions per SiLU occupy their unit for 1,024
-// cycles.
+// with SiLU's and f(û) 9.6 to 7.0, its weight gradient 7.8 to 5.9 (with bias
+// 11.1 to 7.1); 1024^3 without epilogue 5.1 to 4.8; 1024×1024, contraction 4096,
+// 13.1 to 11.7; the one loss found is 1000×1000 with rows of 4000, 13.1 to 13.9.
+// Of the 6.6 us, about 3 are launch and set-up, 2.2 the copies of 16 blocks, and
+// 1.2 the epilogue: its two special-function instructions per SiLU occupy their
+// unit for 1,024 cycles.
 #include <atomic>
 
 #include "internal.h"

@@ -259,8 +259,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * epi_warps(
     // The issue of a stage takes a large part of the stage's MMA time, so what
     // does not change is kept outside the loop: the descriptors of stage 0 by
     // operand order, to which a stage adds its offset (8192×8192 outputs,
-    // contraction 2048, GELU and codes: 173 us with descriptors built per
-    // stage or a whole warp in the loop, 166 with these).
+    // contraction 2048, GELU and codes: 7 us less than with descriptors built
+    // per stage or a whole warp in the loop, 163 now).
     if (rank == 0 && elect_one()) {
       // K-major: 16 K elements are 32 bytes along the row; MN-major: 16 K
       // rows of 128 bytes
