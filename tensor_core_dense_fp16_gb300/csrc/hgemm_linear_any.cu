@@ -61,7 +61,13 @@ struct AnyCfg {
   static constexpr int TMA_STAGES = 5;
   static constexpr int OFF_TURN = OFF_RAW + LOADERS * RAW_STAGES * RAW_BYTES;
   static constexpr int OFF_BAR = OFF_TURN + EPI_WARPS * BOX_BYTES;
-  static constexpr int NUM_BARS = 2 * TMA_STAGES + 5;  // full, empty, accumulator full ×2 and empty ×2, drain
+  // A cluster that splits K: the first CTA receives the others' accumulators
+  // where its ring and buffers were.
+  static constexpr int MOST_SPLIT = 3;
+  static constexpr int PART_BYTES = BM * BN * 4;
+  static_assert((MOST_SPLIT - 1) * PART_BYTES <= TMA_STAGES * STAGE_BYTES, "before the staging boxes");
+  // full, empty, accumulator full ×2 and empty ×2, drain, ready to receive, received
+  static constexpr int NUM_BARS = 2 * TMA_STAGES + 7;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
   static constexpr uint32_t IDESC = idesc_f16_f32acc(BM, BN);
@@ -76,6 +82,7 @@ struct AnyArgs {
   int num_kb;
   int wide;  // the epilogue can read and write eight columns at a time
   int tma;   // tensor maps describe the operands
+  int split;  // CTAs of a cluster per unit, each a run of K blocks
   int* status;
   unsigned long long timeout_ns;
   int inject;  // HGEMM_INJECT_* (testing the watchdog)
@@ -244,7 +251,8 @@ __device__ __noinline__ void any_columns(const LinearProduct& p, const float* tu
   });
 }
 
-template <bool BACKWARD>
+// SHARED: the CTAs of a cluster share the K of a unit.
+template <bool BACKWARD, bool SHARED>
 __global__ void __launch_bounds__(AnyCfg::THREADS, 1)
     linear_any_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const AnyArgs a) {
   using Cfg = AnyCfg;
@@ -260,6 +268,11 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1)
   auto accf_bar = [&](int b) { return bar0 + 8u * (2 * Cfg::TMA_STAGES + b); };
   auto acce_bar = [&](int b) { return bar0 + 8u * (2 * Cfg::TMA_STAGES + 2 + b); };
   const uint32_t drain_bar = bar0 + 8u * (2 * Cfg::TMA_STAGES + 4);
+  const uint32_t ready_bar = drain_bar + 8u, recv_bar = drain_bar + 16u;
+  const int split = SHARED ? a.split : 1, rank = SHARED ? static_cast<int>(cluster_ctarank()) : 0;
+  const int64_t unit0 = blockIdx.x / split, unit_step = gridDim.x / split;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(a.num_kb) * rank / split);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(a.num_kb) * (rank + 1) / split);
   const int stages = a.tma ? Cfg::TMA_STAGES : Cfg::STAGES;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Watchdog wd{abort_flag, a.status, a.timeout_ns};
@@ -275,6 +288,8 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1)
       mbar_init(acce_bar(b), a.tma ? 2 * Cfg::EPI_WARPS : Cfg::EPI_WARPS);  // one arrival per epilogue warp
     }
     mbar_init(drain_bar, 1);
+    mbar_init(ready_bar, 1);
+    mbar_init(recv_bar, SHARED ? (split - 1) * Cfg::EPI_WARPS : 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -284,6 +299,7 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1)
   }
   tc_fence_before_sync();
   __syncthreads();
+  if (SHARED) cluster_sync_after_init();
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
   grid_dependency_wait();
@@ -296,10 +312,10 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1)
       uint32_t phase = 0;
       long long issued = 0;
       bool ok = true;
-      for (int64_t t = blockIdx.x; ok && t < a.units; t += gridDim.x) {
+      for (int64_t t = unit0; ok && t < a.units; t += unit_step) {
         const AnyUnit u = any_unit(a, t);
         const int m0 = static_cast<int>(u.m0), n0 = static_cast<int>(u.n0);
-        for (int kb = 0; kb < a.num_kb; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           ok = wait_phase(empty_bar(stage), phase ^ 1u, wd, kWdProducerEmpty);
           if (!ok) break;
           if (!(a.inject == 1 && issued == 0))  // testing aid: withhold one arrival
@@ -351,7 +367,7 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1)
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int64_t t = blockIdx.x; ok && t < a.units; t += gridDim.x) {
+    for (int64_t t = unit0; ok && t < a.units; t += unit_step) {
       const AnyUnit u = any_unit(a, t);
       const AnySegments ca = any_start(oa, warp, u.m0), cb = any_start(ob, warp, u.n0);
       // this lane's pieces: piece i % 9 of segment i / 9, A's segments first
@@ -361,7 +377,7 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1)
       for (int c = 0; c < kAnyCopies; ++c) {
         const int i = lane + 32 * c, j = i / 9;
         const uint16_t* seg = j < Cfg::SEGMENTS ? ca.src + j * oa.ld : cb.src + (j - Cfg::SEGMENTS) * ob.ld;
-        at[c] = seg - any_shift(seg) + i % 9 * 8;
+        at[c] = seg - any_shift(seg) + i % 9 * 8 + kb0 * (j < Cfg::SEGMENTS ? step_a : step_b);
       }
 #pragma unroll
       for (int g = 0; g < kAnyGroups; ++g) {
@@ -369,7 +385,7 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1)
         shift_b[g] = any_shift(cb.src + (4 * g + (lane >> 3)) * ob.ld);
       }
       int filled = 0;  // buffer of the next block to copy
-      const uint16_t *src_a = ca.src, *src_b = cb.src;  // of the next block to copy
+      const uint16_t *src_a = ca.src + kb0 * step_a, *src_b = cb.src + kb0 * step_b;  // of the next block to copy
       auto inside = [&](const AnyOperand& o, const uint16_t* src) {  // every piece
         return src + (Cfg::SEGMENTS - 1) * o.ld + 72 <= o.end;
       };
@@ -396,12 +412,12 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1)
         if (++filled == Cfg::RAW_STAGES) filled = 0;
       };
       copy(true);
-      copy(a.num_kb > 1);
+      copy(kb1 - kb0 > 1);
       int used = 0;
-      for (int kb = 0; kb < a.num_kb; ++kb) {
+      for (int kb = kb0; kb < kb1; ++kb) {
         // (every lane has read the buffer that this overwrites)
         __syncwarp();
-        copy(kb + 2 < a.num_kb);
+        copy(kb + 2 < kb1);
         int good = 1;
         if (lane == 0) good = wait_phase(empty_bar(stage), phase ^ 1u, wd, kWdProducerEmpty) ? 1 : 0;
         ok = __shfl_sync(0xffffffffu, good, 0) != 0;
@@ -418,7 +434,7 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1)
         fence_proxy_async_smem();
         __syncwarp();
         // (testing aid: one warp withholds one arrival)
-        if (lane == 0 && !(a.inject == 1 && warp == 0 && kb == 0 && t == blockIdx.x)) mbar_arrive(full_bar(stage));
+        if (lane == 0 && !(a.inject == 1 && warp == 0 && kb == kb0 && t == unit0)) mbar_arrive(full_bar(stage));
         if (++stage == stages) {
           stage = 0;
           phase ^= 1u;
@@ -438,11 +454,11 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1)
       int acc = 0;
       uint32_t acc_phase = 0;
       bool ok = true;
-      for (int64_t t = blockIdx.x; ok && t < a.units; t += gridDim.x) {
+      for (int64_t t = unit0; ok && t < a.units; t += unit_step) {
         if (!wait_phase(acce_bar(acc), acc_phase ^ 1u, wd, kWdMmaAccEmpty)) break;
         tc_fence_after_sync();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * Cfg::BN);
-        for (int kb = 0; kb < a.num_kb; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!wait_phase(full_bar(stage), phase, wd, kWdMmaFull)) {
             ok = false;
             break;
@@ -453,7 +469,7 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1)
           const uint64_t b_desc = p.b_mn ? sdesc_mnmajor_sw128(sb) : sdesc_kmajor_sw128(sb);
 #pragma unroll
           for (int k = 0; k < Cfg::BK / Cfg::UMMA_K; ++k)
-            mma_f16_ss(d_tmem, a_desc + a_step * k, b_desc + b_step * k, idesc, (kb > 0 || k > 0) ? 1u : 0u);
+            mma_f16_ss(d_tmem, a_desc + a_step * k, b_desc + b_step * k, idesc, (kb > kb0 || k > 0) ? 1u : 0u);
           mma_commit(empty_bar(stage));
           if (++stage == stages) {
             stage = 0;
@@ -489,14 +505,70 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1)
     };
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int64_t t = blockIdx.x; t < a.units; t += gridDim.x) {
+    for (int64_t t = unit0; t < a.units; t += unit_step) {
       const AnyUnit u = any_unit(a, t);
       lin_prefetch_row<BACKWARD ? kEpiLinearGrad : kEpiLinear>(e, p.M, p.N, u.m0 + q * 32 + lane, u.n0, Cfg::BN);
       int ok = 1;
       if (lane == 0) ok = wait_phase(accf_bar(acc), acc_phase, wd, kWdEpiAccFull) ? 1 : 0;
       ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
+      if (!ok) {
+        // (the first CTA's signal may still be under way)
+        if (SHARED && rank != 0 && warp == Cfg::LOADERS && lane == 0) wait_drain_cluster(ready_bar, 0, wd);
+        break;
+      }
       tc_fence_after_sync();
+      if constexpr (SHARED) {
+        const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+        // [other rank][quarter][four columns][row]
+        const uint32_t part = static_cast<uint32_t>(q * (Cfg::PART_BYTES / 4) + lane * 16);
+        if (rank != 0) {
+          if (more) break;
+          if (lane == 0) ok = wait_phase_cluster(ready_bar, 0, wd, kWdReduce) ? 1 : 0;
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+          const uint32_t to = mapa_shared(sbase + static_cast<uint32_t>((rank - 1) * Cfg::PART_BYTES) + part, 0);
+#pragma unroll 1
+          for (int c = 0; c < Cfg::BN; c += 16) {
+            float v[16];
+            tmem_ld_32x32b_x16(t_row + c, v);
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+              st_cluster_v4(to + static_cast<uint32_t>((c + i) * 128), __float_as_uint(v[i]), __float_as_uint(v[i + 1]),
+                            __float_as_uint(v[i + 2]), __float_as_uint(v[i + 3]));
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(mapa_shared(recv_bar, 0));
+          break;
+        }
+        // the ring and the buffers have been read: the accumulator is complete
+        if (warp == Cfg::LOADERS && lane > 0 && lane < split)
+          mbar_arrive_cluster_relaxed(mapa_shared(ready_bar, static_cast<uint32_t>(lane)));
+        if (lane == 0) {
+          ok = wait_phase_cluster(recv_bar, 0, wd, kWdReduce) ? 1 : 0;
+          if (!ok) wait_drain_cluster(recv_bar, 0, wd);
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        // the columns that this warp goes on with, summed in rank order in TMEM
+        const int c1 = a.tma ? first + kCkptGroup : Cfg::BN;
+#pragma unroll 1
+        for (int c = first; c < c1; c += 16) {
+          float v[16];
+          tmem_ld_32x32b_x16(t_row + c, v);
+          for (int r = 1; r < split; ++r) {
+            const uint8_t* from = smem + (r - 1) * Cfg::PART_BYTES + part + c * 128;
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+              const float4 w = *reinterpret_cast<const float4*>(from + i * 128);
+              v[i] += w.x;
+              v[i + 1] += w.y;
+              v[i + 2] += w.z;
+              v[i + 3] += w.w;
+            }
+          }
+          tmem_st_32x32b_x16(t_row + c, v);
+        }
+      }
       const int64_t gi = u.m0 + q * 32 + lane;
       for (int64_t col0 = u.n0 + first; col0 < u.n0 + Cfg::BN && col0 < p.N; col0 += step) {
         const uint32_t t_group = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
@@ -578,17 +650,7 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1)
 cudaError_t launch_linear_any(const LinearProduct& p, const CUtensorMap* ma, const CUtensorMap* mb,
                               const CallDevice& dev, cudaStream_t stream) {
   using Cfg = AnyCfg;
-  static std::atomic<bool> attr_done[2][64];
-  const int back = p.epi.backward ? 1 : 0;
-  auto kern = back ? linear_any_kernel<true> : linear_any_kernel<false>;
-  int id = 0;
-  cudaError_t e = cudaGetDevice(&id);
-  if (e != cudaSuccess) return e;
-  if (id < 0 || id >= 64 || !attr_done[back][id]) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
-    if (e != cudaSuccess) return e;
-    if (id >= 0 && id < 64) attr_done[back][id] = true;
-  }
+  static std::atomic<bool> attr_done[4][64];
   AnyArgs a{};
   a.p = p;
   a.num_m = (p.M + Cfg::BM - 1) / Cfg::BM;
@@ -605,8 +667,29 @@ cudaError_t launch_linear_any(const LinearProduct& p, const CUtensorMap* ma, con
   a.status = dev.status;
   a.timeout_ns = dev.timeout_ns;
   a.inject = dev.inject;
-  PdlLaunch l(dim3(static_cast<unsigned>(a.units < dev.num_sms ? a.units : dev.num_sms)), dim3(Cfg::THREADS),
-              Cfg::SMEM_BYTES, stream);
+  // Few tiles and a long K: clusters of two or three share it, eight K blocks or
+  // more each. (The three CTAs of a cluster then exchange 128 KB, some 4 us.)
+  a.split = 1;
+  for (int s = Cfg::MOST_SPLIT; s > 1 && a.split == 1; --s)
+    if (a.units * s <= dev.num_sms - 16 && a.num_kb >= 8 * s) a.split = s;
+  const int which = (p.epi.backward ? 1 : 0) + (a.split > 1 ? 2 : 0);
+  auto kern = which == 0   ? linear_any_kernel<false, false>
+              : which == 1 ? linear_any_kernel<true, false>
+              : which == 2 ? linear_any_kernel<false, true>
+                           : linear_any_kernel<true, true>;
+  int id = 0;
+  cudaError_t e = cudaGetDevice(&id);
+  if (e != cudaSuccess) return e;
+  if (id < 0 || id >= 64 || !attr_done[which][id]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    if (id >= 0 && id < 64) attr_done[which][id] = true;
+  }
+  PdlLaunch l(dim3(static_cast<unsigned>(a.split > 1               ? a.units * a.split
+                                         : a.units < dev.num_sms ? a.units
+                                                                 : dev.num_sms)),
+              dim3(Cfg::THREADS), Cfg::SMEM_BYTES, stream);
+  l.cluster(static_cast<unsigned>(a.split));
   const CUtensorMap none{};
   return cudaLaunchKernelEx(&l.cfg, kern, ma ? *ma : none, mb ? *mb : none, a);
 }

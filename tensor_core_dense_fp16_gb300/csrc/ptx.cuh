@@ -305,6 +305,18 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, float (&r)[16
       : "memory");
 }
 
+// The same the other way round, complete when it returns.
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const float (&r)[16]) {
+  if (!HG_DBG_TMEM(taddr, 16)) return;
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};\n\t"
+      "tcgen05.wait::st.sync.aligned;" ::"f"(r[0]),
+      "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]), "f"(r[9]), "f"(r[10]),
+      "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15]), "r"(taddr)
+      : "memory");
+}
+
 __device__ __forceinline__ void tmem_ld_32x32b_x4(uint32_t taddr, float (&r)[4]) {
   if (!HG_DBG_TMEM(taddr, 4)) {
 #pragma unroll

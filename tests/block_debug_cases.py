@@ -46,6 +46,8 @@ def main() -> int:
         cases.run_linear(150, 131, 77, "silu", keep=True, pad=pad, offset=offset)
         cases.run_dgrad(150, 131, 77, "silu", pad=pad, offset=offset)
         cases.run_wgrad(150, 131, 77, pad=pad, offset=offset)
+    cases.run_linear(150, 131, 2049, "gelu", keep=True)
+    cases.run_linear(150, 131, 1544, "gelu")
     clean("odd sizes")
     for M, D in ((1, 4096), (70, 264), (40, 1000), (30, 2048), (20, 4096), (9, 8192), (5, 16384), (7, 20001)):
         cases.run_layernorm(M, D)

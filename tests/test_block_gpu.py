@@ -446,6 +446,15 @@ def test_one_wave_of_clusters(M, N, K):
     run_wgrad(K, M, N, bias=False)
 
 
+@pytest.mark.parametrize("M,N,K", [(200, 131, 3001), (150, 257, 2049), (300, 129, 1024), (200, 131, 1536)])
+def test_odd_sizes_of_few_tiles_and_a_long_contraction(M, N, K):
+    run_linear(M, N, K, "gelu", keep=True)
+    run_linear(M, N, K, "none", in_place=True)
+    run_dgrad(M, K, N, "silu")
+    run_wgrad(K, N, M, accumulate=True)
+    run_wgrad(K, M, N, pad=3)
+
+
 @pytest.mark.parametrize("M,N,K", [(2048, 264, 136), (5000, 72, 520), (3000, 130, 128)])
 @pytest.mark.parametrize("accumulate", [False, True])
 def test_small_weights_of_many_rows(M, N, K, accumulate):
@@ -488,7 +497,7 @@ def test_bias_gradient_beside_its_product():
 
 
 @pytest.mark.parametrize("what", ["pair", "narrow", "split", "few rows", "few rows back", "small weight", "clusters",
-                                  "any", "norm"])
+                                  "any", "any shared", "norm"])
 def test_withheld_arrival_times_out(what):
     """Each kernel's waits are bounded: a withheld arrival ends in a timeout
     the host reads, and the context computes on."""
@@ -508,6 +517,8 @@ def test_withheld_arrival_times_out(what):
         "clusters": lambda: tc.hgemm_linear_dgrad(y, 512, w, 512, None, 0, None, 0, 0, half(600, 512), 512, None, 0, 600,
                                                   512, 512),
         "any": lambda: tc.hgemm_linear(y, 511, w, 511, None, 2, None, 0, half(600, 512), 511, 600, 511, 511),
+        "any shared": lambda: tc.hgemm_linear(half(200, 2049), 2049, half(199, 2049), 2049, None, 2, None, 0, half(200, 199),
+                                              199, 200, 199, 2049),
         "norm": lambda: tc.hgemm_layernorm_backward(y, 512, y, 512, w, stats, stats, None, 0, half(64, 512), 512, db,
                                                     torch.empty(512, device="cuda"), ws, 64, 512),
     }
