@@ -56,34 +56,47 @@ struct SmallCfg {
   static_assert(SMEM_BYTES <= 232448, "exceeds 227 KB of shared memory per CTA");
 };
 
-// Outputs of feature f and rows m .. m + R - 1, the first `count` of them
-// inside.
-template <bool BACKWARD, int R>
-__device__ __forceinline__ void put_rows(const SmallArgs& p, const float (&sum)[R], float bias, int64_t m, int f,
-                                         int count) {
-  const LinEpi& e = p.epi;
+// What the outputs of feature f and rows m .. m + R - 1, the first `count` of
+// them inside, read besides the sums.
+template <int R>
+struct RowSide {
   uint32_t side[R];  // residual, or codes
   float scale[R];
+};
+template <bool BACKWARD, int R>
+__device__ __forceinline__ RowSide<R> fetch_rows(const SmallArgs& p, int64_t m, int f, int count) {
+  const LinEpi& e = p.epi;
+  RowSide<R> s;
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    side[i] = 0u;
-    scale[i] = 0.f;
+    s.side[i] = 0u;
+    s.scale[i] = 0.f;
   }
   if (BACKWARD && e.codes) {
     const int8_t* q = e.codes + m * e.ldq + f;
-    const float* s = e.scales + f / kCkptGroup * e.lds + m;
+    const float* scale = e.scales + f / kCkptGroup * e.lds + m;
 #pragma unroll
     for (int i = 0; i < R; ++i, q += e.ldq)
       if (i < count) {
-        side[i] = static_cast<uint8_t>(*q);
-        scale[i] = s[i];
+        s.side[i] = static_cast<uint8_t>(*q);
+        s.scale[i] = scale[i];
       }
   } else if (!BACKWARD && e.res) {
     const uint16_t* r = e.res + m * e.ldr + f;
 #pragma unroll
     for (int i = 0; i < R; ++i, r += e.ldr)
-      if (i < count) side[i] = *r;
+      if (i < count) s.side[i] = *r;
   }
+  return s;
+}
+
+// The outputs themselves.
+template <bool BACKWARD, int R>
+__device__ __forceinline__ void put_rows(const SmallArgs& p, const float (&sum)[R], const RowSide<R>& s, float bias,
+                                         int64_t m, int f, int count) {
+  const LinEpi& e = p.epi;
+  const uint32_t(&side)[R] = s.side;
+  const float(&scale)[R] = s.scale;
   uint16_t* y = p.Y + m * p.ldy + f;
   uint16_t* h = e.h + m * e.ldh + f;
   with_activation(!BACKWARD || e.codes ? e.act : HGEMM_ACT_NONE, [&](auto a) {
@@ -279,7 +292,8 @@ __global__ void __launch_bounds__(192, 1)
         for (int c = 0; c < rows; c += 16) {
           float v[16];
           tmem_ld_32x32b_x16(t_row + c, v);
-          put_rows<BACKWARD, 16>(p, v, bias, r0 + c, f, in_f ? rows - c : 0);
+          const int count = in_f ? rows - c : 0;
+          put_rows<BACKWARD, 16>(p, v, fetch_rows<BACKWARD, 16>(p, r0 + c, f, count), bias, r0 + c, f, count);
         }
       } else {
         const uint32_t column = static_cast<uint32_t>(q * 32 + lane) * 16u;
@@ -308,6 +322,9 @@ __global__ void __launch_bounds__(192, 1)
       }
     }
     if (p.split > 1) {
+      // (read while the other ranks' sums are on their way)
+      auto inside = [&](int u) { return in_f ? min(rows, 4 * u1) - 4 * u : 0; };
+      RowSide<8> side = fetch_rows<BACKWARD, 8>(p, r0 + 4 * u0, f, inside(u0));
       // Nothing is left under way to this CTA's shared memory once the other
       // ranks have all arrived (after a wait that gave up they are awaited too).
       if (lane == 0)
@@ -335,8 +352,8 @@ __global__ void __launch_bounds__(192, 1)
             sum[4 * j + 3] += w.w;
           }
         }
-        const int left = min(rows, 4 * u1) - 4 * u;
-        put_rows<BACKWARD, 8>(p, sum, bias, r0 + 4 * u, f, in_f ? left : 0);
+        put_rows<BACKWARD, 8>(p, sum, side, bias, r0 + 4 * u, f, inside(u));
+        if (u + 2 < u1) side = fetch_rows<BACKWARD, 8>(p, r0 + 4 * (u + 2), f, inside(u + 2));
       }
     }
   }
