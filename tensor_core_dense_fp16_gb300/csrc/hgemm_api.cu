@@ -75,7 +75,7 @@ cudaError_t debug_words(int* (&out)[hg::kDebugWords]) {
                                                       hg::debug_word_trileaf, hg::debug_word_chain,
                                                       hg::debug_word_linear,  hg::debug_word_norm,
                                                       hg::debug_word_ckpt8,   hg::debug_word_linear_any,
-                                                      hg::debug_word_linear_small, hg::debug_word_linear_cluster};
+                                                      hg::debug_word_linear_small, hg::debug_word_linear_wave};
   for (int i = 0; i < hg::kDebugWords; ++i) {
     const cudaError_t e = get[i](&out[i]);
     if (e != cudaSuccess) return e;
@@ -124,6 +124,8 @@ struct Gemm {
   int64_t ld_src = 0;
   // a linear layer's epilogue instead of EpiArgs (null: none)
   const hg::LinEpi* lin = nullptr;
+  // K split among clusters if the device holds them, unless a path is forced
+  bool split_k = false;
   hg::Epilogue kind(const hg::EpiArgs& epi) const {
     if (lin) return lin->backward ? hg::kEpiLinearGrad : hg::kEpiLinear;
     return epi.mode != 0 ? hg::kEpiFused : hg::kEpiPlain;
@@ -271,8 +273,9 @@ int choose_path(const Gemm& g, const hg::DeviceProfile& prof, bool fused, int* s
   if (M == 0 || N == 0) return HGEMM_PATH_NONE;
   if (K == 0) return HGEMM_PATH_ZERO;
   const bool tma = tma_ok(g);
-  const int forced = g_forced_path.load(std::memory_order_relaxed);
+  int forced = g_forced_path.load(std::memory_order_relaxed);
   if (forced == HGEMM_PATH_GENERIC || !tma) return HGEMM_PATH_GENERIC;
+  if (forced < 0 && g.split_k) forced = HGEMM_PATH_SKINNY;
   const int fs = g_forced_split.load(std::memory_order_relaxed);
   const int path = hg::choose_tma_path(M, N, K, prof, forced, fs >> 10, fs & 1023, fused, split, tile_n);
   // M- or N-contiguous operands: the wide, pair and split-K kernels read
@@ -800,22 +803,43 @@ int run_linear_small(const LinearProduct& p, const DeviceState& dev, cudaStream_
   return cuda_status(launch_linear_small(mw, mx, a, stream));
 }
 
-// Whether p is one wave of clusters of four 128×64 tiles.
-bool linear_cluster_suits(const LinearProduct& p, int num_sms) {
+// Whether p, with g its product, is one wave of 128×64 tiles that the kernel
+// of a CTA per tile computes. Its time grows by the 128-byte pieces that an SM
+// asks L2 for in a K block, the split-K kernel's by half as many, but that one
+// begins about 3 us later. A piece is two requests where the operand's rows
+// begin inside lines, and a little more where they run along M or N; the sums
+// for a bias gradient delay the ring. Measured (us, this kernel | split K;
+// forward, input gradient with SiLU and f(û), weight gradient, the same with
+// the bias): 1024×1024 outputs of 2048 6.7 | 7.9, 7.8 | 9.6, 6.8 | 7.8, 8.2 | 9.5,
+// of 3328 9.1 | 9.5, 10.3 | 11.2, 9.1 | 9.6, 11.7 | 11.4, of 4096 10.5 | 10.4, 11.7 |
+// 12.2, 10.7 | 10.7; 1000×1000 (pitch 1000) of 1000 7.4 | 7.8, 9.0 | 9.4, 8.5 |
+// 7.7, 8.4 | 9.1, of 2504 13.5 | 11.1, 16.4 | 13.3, 17.3 | 12.2, 17.2 | 13.7;
+// 2048×512 of 8192 19.3 | 15.4, 20.2 | 17.2, 19.1 | 16.3. (The kernels of larger
+// outputs take 1000^3 in 7.8, 11.7, 9.7 and 10.8.) Up to 128 rows split K would
+// leave half of its 256-row tiles empty.
+bool linear_wave_suits(const LinearProduct& p, bool sums, Gemm* g, const DeviceState& dev) {
   if (p.M == 0 || p.N == 0 || p.K == 0) return false;
-  const int64_t clusters = (p.M + 2 * kTcBM - 1) / (2 * kTcBM) * ((p.N + 2 * kNarrowBN - 1) / (2 * kNarrowBN));
-  return clusters <= linear_cluster_max(num_sms);
+  if ((p.M + kTcBM - 1) / kTcBM * ((p.N + kNarrowBN - 1) / kNarrowBN) > dev.num_sms) return false;
+  auto requests = [](const uint16_t* q, int64_t ld, bool mn) {
+    return (reinterpret_cast<uintptr_t>(q) & 127u) == 0 && ld % 64 == 0 ? 1 : mn ? 3 : 2;
+  };
+  // A's pieces are twice as many as B's
+  const int64_t per_block = 2 * requests(p.A, p.lda, p.a_mn) + requests(p.B, p.ldb, p.b_mn) + (sums ? 1 : 0);
+  if (p.M <= kTcBM || (p.K + kTcBK - 1) / kTcBK * per_block <= 192) return true;
+  int split = 1, tile_n = kPairBN;
+  g->split_k = true;
+  if (choose_path(*g, dev.prof, true, &split, &tile_n) == HGEMM_PATH_SKINNY) return false;
+  g->split_k = false;
+  return true;
 }
 
-int run_linear_cluster(const LinearProduct& p, float* row_sums, bool add, cudaStream_t stream) {
+int run_linear_wave(const LinearProduct& p, float* row_sums, bool add, cudaStream_t stream) {
   CUtensorMap ma, mb, mc;
   int rc;
-  // halves of tiles: 64 rows of A by 64 of K, or the other way around; 32 rows
-  // of B, or 64 of its columns by 32 of K
-  rc = p.a_mn ? encode_map(&ma, p.A, p.K, p.M, p.lda, kTcBK, 64) : encode_map(&ma, p.A, p.M, p.K, p.lda, kTcBM / 2, kTcBK);
+  rc = p.a_mn ? encode_map(&ma, p.A, p.K, p.M, p.lda, kTcBK, 64) : encode_map(&ma, p.A, p.M, p.K, p.lda, kTcBM, kTcBK);
   if (rc != HGEMM_OK) return rc;
-  rc = p.b_mn ? encode_map(&mb, p.B, p.K, p.N, p.ldb, kTcBK / 2, 64)
-              : encode_map(&mb, p.B, p.N, p.K, p.ldb, kNarrowBN / 2, kTcBK);
+  rc = p.b_mn ? encode_map(&mb, p.B, p.K, p.N, p.ldb, kTcBK, 64)
+              : encode_map(&mb, p.B, p.N, p.K, p.ldb, kNarrowBN, kTcBK);
   if (rc != HGEMM_OK) return rc;
   if ((rc = encode_map(&mc, p.C, p.M, p.N, p.ldc, kEpiRows, kEpiCols)) != HGEMM_OK) return rc;
   TcArgs args{};
@@ -825,7 +849,7 @@ int run_linear_cluster(const LinearProduct& p, float* row_sums, bool add, cudaSt
   args.num_m = static_cast<int>((p.M + kTcBM - 1) / kTcBM);
   args.num_n = static_cast<int>((p.N + kNarrowBN - 1) / kNarrowBN);
   args.num_kb = static_cast<int>((p.K + kTcBK - 1) / kTcBK);
-  args.grid = 4 * ((args.num_m + 1) / 2) * ((args.num_n + 1) / 2);
+  args.grid = args.num_m * (row_sums && args.num_n == 1 ? 2 : args.num_n);  // (the sums take two columns of tiles)
   args.a_mn = p.a_mn ? 1 : 0;
   args.b_mn = p.b_mn ? 1 : 0;
   args.status = t_ctx.status;
@@ -834,7 +858,7 @@ int run_linear_cluster(const LinearProduct& p, float* row_sums, bool add, cudaSt
   args.lin = p.epi;
   args.row_sums = row_sums;
   args.row_sums_add = add ? 1 : 0;
-  return cuda_status(launch_linear_cluster(ma, mb, mc, args, p.epi.backward ? kEpiLinearGrad : kEpiLinear, stream));
+  return cuda_status(launch_linear_wave(ma, mb, mc, args, p.epi.backward ? kEpiLinearGrad : kEpiLinear, stream));
 }
 
 int run_linear(const LinearProduct& p, cudaStream_t stream) {
@@ -862,7 +886,7 @@ int run_linear(const LinearProduct& p, cudaStream_t stream) {
     if (e != HGEMM_OK) return e;
     return cuda_status(launch_linear_any(p, &ma, &mb, cd, stream));
   }
-  if (forced < 0 && linear_cluster_suits(p, dev->num_sms)) return run_linear_cluster(p, nullptr, false, stream);
+  if (forced < 0 && linear_wave_suits(p, false, &g, *dev)) return run_linear_wave(p, nullptr, false, stream);
   return dispatch(g, kPlainEpilogue, *dev, stream);
 }
 
@@ -879,8 +903,8 @@ int run_wgrad(const LinearProduct& p, float* dbias, bool accumulate, cudaStream_
     rc = run_linear(p, stream);
   } else if (forced < 0 && linear_small_suits(p, dev->num_sms)) {
     rc = run_linear_small(p, *dev, stream);
-  } else if (forced < 0 && linear_cluster_suits(p, dev->num_sms)) {
-    return run_linear_cluster(p, dbias, accumulate, stream);
+  } else if (forced < 0 && linear_wave_suits(p, dbias != nullptr, &g, *dev)) {
+    return run_linear_wave(p, dbias, accumulate, stream);
   } else {
     // (the plain and the accumulating product; the sum of an old value is the residual's)
     EpiArgs epi = kPlainEpilogue;

@@ -1,26 +1,21 @@
-// hgemm_linear_cluster.cu — linear layers and their gradients whose output is
-// a single wave of 128×64 tiles (about a thousand rows and columns), in
-// clusters of four CTAs that share their operands.
+// hgemm_linear_wave.cu — linear layers and their gradients whose output is a
+// single wave of 128×64 tiles (about a thousand rows and columns): a CTA per
+// tile, which loads its own operands, and the bias gradient summed from the
+// weight gradient's staged tiles.
 //
-// Such a product reads each operand many times from L2 (1000^3: 50 MB for 6 MB
-// of operands and output), and rows that start on odd multiples of 16 bytes
-// cost L2 almost twice. Here the CTAs of a cluster compute 2×2 neighbouring
-// tiles. Each loads half of its A tile and half of its B tile and multicasts
-// them to the CTA beside it in its row and in its column, so that half the
-// bytes leave L2. A stage is free for the next loads once the MMAs of all three
-// CTAs that receive them have read it (their commits arrive on the loader's
-// empty barrier). The operand order is a template parameter: a branch on it
-// between the copies took them out of uniform registers (a block of 64 of the
-// contraction: 0.155 us, 0.115 without).
+// Bound by what one SM can ask of L2: about one 128-byte line per cycle, 192 to
+// a block of 64 of the contraction, twice that where rows begin inside lines
+// (an odd multiple of 16 bytes). The operand order is a template parameter: a
+// branch on it between the copies took 0.155 us per block where there was none
+// 0.115.
 //
-// Measured (us, in a graph, operands in L2), against the kernels of larger
-// outputs: 1000^3 with bias, SiLU and residual 8.8 to 6.6, its input gradient
-// with SiLU's and f(û) 9.6 to 7.0, its weight gradient 7.8 to 5.9 (with bias
-// 11.1 to 7.1); 1024^3 without epilogue 5.1 to 4.8; 1024×1024, contraction 4096,
-// 13.1 to 11.7; the one loss found is 1000×1000 with rows of 4000, 13.1 to 13.9.
-// Of the 6.6 us, about 3 are launch and set-up, 2.2 the copies of 16 blocks, and
-// 1.2 the epilogue: its two special-function instructions per SiLU occupy their
-// unit for 1,024 cycles.
+// Measured (us, in a graph, operands in L2): 1024×1024 outputs of a contraction
+// of 1024 4.7, with bias, SiLU and residual 5.5, the input gradient with
+// SiLU's and f(û) 5.9, the weight gradient 4.9, with the bias's 5.5; 1000^3, whose rows
+// begin inside lines, 7.4, 8.2, 9.0, 8.5 and 8.4 (a kernel of column sums beside the
+// product instead of the sums here takes 10.8). Of the 5.5 us, about 3 are
+// launch and set-up, and 1 the epilogue: its two special-function instructions
+// per SiLU occupy their unit for 1,024 cycles.
 #include <atomic>
 
 #include "internal.h"
@@ -31,7 +26,7 @@
 namespace hg {
 namespace {
 
-struct ClCfg {
+struct WaveCfg {
   static constexpr int BM = kTcBM, BN = kNarrowBN, BK = kTcBK, UMMA_K = 16;
   static constexpr int STAGES = 8;
   static constexpr int A_BYTES = BM * BK * 2;
@@ -43,33 +38,30 @@ struct ClCfg {
   static constexpr int OFF_B = OFF_A + STAGES * A_BYTES;
   static constexpr int OFF_C = OFF_B + STAGES * B_BYTES;
   static constexpr int OFF_SUM = OFF_C + EPI_WARPS * C_BOX_BYTES;  // partial row sums of A
-  static constexpr int OFF_BAR = OFF_SUM + EPI_WARPS * (BM / 2) * 4;
+  static constexpr int OFF_BAR = OFF_SUM + EPI_WARPS * kMnBox * 4;
   static constexpr int NUM_BARS = 2 * STAGES + 2;  // full, empty, accumulator full, drain
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
   static constexpr int THREADS = 192;
   static constexpr int TMEM_COLS = BN;
   static constexpr uint32_t IDESC = idesc_f16_f32acc(BM, BN);
-  static_assert(A_BYTES % 2048 == 0 && B_BYTES % 2048 == 0, "halves of tiles are 1024-byte aligned");
-  static_assert(BM == 2 * kMnBox && BN == kMnBox, "half an A tile is one MN-major box");
+  static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0, "swizzled tiles are 1024-byte aligned");
+  static_assert(BM == 2 * kMnBox && BN == kMnBox, "an MN-major A tile is two boxes, a B tile one");
   static_assert(SMEM_BYTES <= 232448, "exceeds 227 KB of shared memory per CTA");
 };
 
-// The sums over K of the half of the A tile that this CTA loads (64 rows), by
-// the epilogue warps while the product runs: the bias gradient beside the
-// weight's, from the stages in shared memory (MN-major: 64 K rows of 128
-// bytes). The four warps take K blocks in turn, so that none of them delays the
-// ring. A thread adds the eight rows of A of one 16-byte chunk in every fourth K
-// row of its warp's blocks, and the 16 partial sums of a row are added in a
-// fixed order. (A CTA's own half, because then only its own loads wait for the
-// sums. A kernel of column sums beside the product took 5 us more: 1000^3,
-// 6.0 us without.)
-__device__ __forceinline__ void sum_rows(const TcArgs& p, uint8_t* smem, uint32_t full0, uint32_t empty0, int half,
+// The sums over K of 64 rows of the A tile, by the epilogue warps while the
+// product runs: the bias gradient beside the weight's, from the stages in
+// shared memory (an MN-major box: 64 K rows of 128 bytes). The four warps take
+// K blocks in turn, so that none of them delays the ring. A thread adds the
+// eight rows of A of one 16-byte chunk in every fourth K row of its warp's
+// blocks, and the 16 partial sums of a row are added in a fixed order.
+__device__ __forceinline__ void sum_rows(const TcArgs& p, uint8_t* smem, uint32_t full0, uint32_t empty0, int box,
                                          int first, const Watchdog& wd) {
-  using Cfg = ClCfg;
+  using Cfg = WaveCfg;
   const int t = static_cast<int>(threadIdx.x) - 64, lane = t & 31;
   const int chunk = t & 7, k0 = lane >> 3;
-  const uint8_t* tile = smem + Cfg::OFF_A + half * kMnBoxBytes;
+  const uint8_t* tile = smem + Cfg::OFF_A + box * kMnBoxBytes;
   f32x2 sum[4] = {};
   for (int kb = t >> 5; kb < p.num_kb; kb += Cfg::EPI_WARPS) {
     const int stage = kb % Cfg::STAGES;
@@ -106,10 +98,10 @@ __device__ __forceinline__ void sum_rows(const TcArgs& p, uint8_t* smem, uint32_
 
 // A_MN, B_MN: the operand is stored with its rows contiguous (K×M, K×N).
 template <int EPI, bool A_MN, bool B_MN>
-__global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(ClCfg::THREADS, 1)
-    linear_cluster_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+__global__ void __launch_bounds__(WaveCfg::THREADS, 1)
+    linear_wave_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                           const __grid_constant__ CUtensorMap tmC, const TcArgs p) {
-  using Cfg = ClCfg;
+  using Cfg = WaveCfg;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
@@ -123,24 +115,17 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(ClCfg::THREADS, 1)
   auto empty_bar = [&](int s) { return bar0 + 8u * (Cfg::STAGES + s); };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = static_cast<int>(cluster_ctarank());
-  const int cluster = static_cast<int>(blockIdx.x) >> 2;
-  const int clusters_m = (p.num_m + 1) >> 1;
-  const int rm = rank & 1, rn = rank >> 1;  // this CTA's tile of the 2×2
-  const int m0 = (2 * (cluster % clusters_m) + rm) * Cfg::BM;
-  const int n0 = (2 * (cluster / clusters_m) + rn) * Cfg::BN;
-  const uint16_t same_m = static_cast<uint16_t>(0x5u << rm);       // the two CTAs of these rows
-  const uint16_t same_n = static_cast<uint16_t>(0x3u << (2 * rn));  // the two CTAs of these columns
-  // sums of A's rows over K: computed in the first column of tiles
-  const bool summed = A_MN && p.row_sums && cluster / clusters_m == 0;
+  const int m0 = static_cast<int>(blockIdx.x) % p.num_m * Cfg::BM;
+  const int nb = static_cast<int>(blockIdx.x) / p.num_m, n0 = nb * Cfg::BN;
+  // sums of A's rows over K: a box of 64 rows each in the first two columns of
+  // tiles (args.grid has both)
+  const bool summed = A_MN && p.row_sums && nb < 2;
   const Watchdog wd{abort_flag, p.status, p.timeout_ns};
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < Cfg::STAGES; ++s) {
-      mbar_init(full_bar(s), 1);   // the producer's arrive.expect_tx (+ the bytes of three CTAs)
-      // commits of the CTAs that received this CTA's halves, and its own
-      // summing warp
-      mbar_init(empty_bar(s), summed ? 4 : 3);
+      mbar_init(full_bar(s), 1);                // the producer's arrive.expect_tx (+ bytes)
+      mbar_init(empty_bar(s), summed ? 2 : 1);  // tcgen05.commit, and the block's summing warp
     }
     mbar_init(accf_bar, 1);
     mbar_init(drain_bar, 1);
@@ -156,7 +141,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(ClCfg::THREADS, 1)
   }
   tc_fence_before_sync();
   __syncthreads();
-  cluster_sync_after_init();  // copies and commits reach the other CTAs' barriers
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
   // operands and the epilogue's inputs may come from the previous launch
@@ -166,13 +150,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(ClCfg::THREADS, 1)
   if (warp == 0) {
     // ------------------------------------------------------ TMA producer
     if (elect_one()) {
-      // this CTA's halves: rows 64·rn.. of the A tile, rows 32·rm.. of the B
-      // tile. K-major they are rows of 128 bytes; MN-major a tile is boxes of
-      // 64 M or N by 64 K rows of 128 bytes, A's two halves being the two boxes
-      // and B's the K rows 32·rm.. of its box.
-      const uint32_t a_dst = sA + static_cast<uint32_t>(rn) * (Cfg::A_BYTES / 2);
-      const uint32_t b_dst = sB + static_cast<uint32_t>(rm) * (Cfg::B_BYTES / 2);
-      const int ya = m0 + rn * (Cfg::BM / 2), yb = n0 + rm * (Cfg::BN / 2);
       int stage = 0;
       uint32_t phase = 0;
       int issued = 0;
@@ -181,22 +158,24 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(ClCfg::THREADS, 1)
         if (!(p.inject == 1 && issued == 0))  // testing aid: withhold one arrival
           mbar_arrive_expect_tx(full_bar(stage), Cfg::STAGE_BYTES);
         const int kx = kb * Cfg::BK;
-        if constexpr (A_MN)
-          tma_load_2d_multicast(a_dst + stage * Cfg::A_BYTES, &tmA, full_bar(stage), ya, kx, same_m);
-        else
-          tma_load_2d_multicast(a_dst + stage * Cfg::A_BYTES, &tmA, full_bar(stage), kx, ya, same_m);
+        const uint32_t a_dst = sA + stage * Cfg::A_BYTES, b_dst = sB + stage * Cfg::B_BYTES;
+        if constexpr (A_MN) {
+          tma_load_2d(a_dst, &tmA, full_bar(stage), m0, kx);
+          tma_load_2d(a_dst + kMnBoxBytes, &tmA, full_bar(stage), m0 + kMnBox, kx);
+        } else {
+          tma_load_2d(a_dst, &tmA, full_bar(stage), kx, m0);
+        }
         if constexpr (B_MN)
-          tma_load_2d_multicast(b_dst + stage * Cfg::B_BYTES, &tmB, full_bar(stage), n0, kx + rm * (Cfg::BK / 2), same_n);
+          tma_load_2d(b_dst, &tmB, full_bar(stage), n0, kx);
         else
-          tma_load_2d_multicast(b_dst + stage * Cfg::B_BYTES, &tmB, full_bar(stage), kx, yb, same_n);
+          tma_load_2d(b_dst, &tmB, full_bar(stage), kx, n0);
         ++issued;
         if (++stage == Cfg::STAGES) {
           stage = 0;
           phase ^= 1u;
         }
       }
-      // Drain: once the last stages are free again, all that this CTA sent has
-      // been read, and nothing more arrives here, bytes or commits.
+      // the last loads must have landed before the CTA's memory goes away
       int s = stage;
       uint32_t ph = phase;
       for (int i = 0; i < issued && i < Cfg::STAGES; ++i) {
@@ -206,14 +185,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(ClCfg::THREADS, 1)
         } else {
           --s;
         }
-        if (!wait_drain(empty_bar(s), ph, wd)) break;
-      }
-      // After a wait that gave up: the other CTAs' last copies and commits to
-      // this one are under way or will never be issued.
-      if (*abort_flag) {
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 100000u) {
-        }
+        wait_drain(full_bar(s), ph, wd);
       }
     }
     __syncwarp();
@@ -224,7 +196,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(ClCfg::THREADS, 1)
       const uint64_t b_base = B_MN ? sdesc_mnmajor_sw128(sB) : sdesc_kmajor_sw128(sB);
       const uint32_t a_step = A_MN ? 128u : 2u, b_step = B_MN ? 128u : 2u;
       constexpr uint32_t idesc = Cfg::IDESC | idesc_major_bits(A_MN, B_MN);
-      const uint16_t readers = same_m | same_n;  // the CTAs whose loads this stage held
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -239,7 +210,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(ClCfg::THREADS, 1)
 #pragma unroll
         for (int k = 0; k < Cfg::BK / Cfg::UMMA_K; ++k)
           mma_f16_ss(tmem_base, a_desc + a_step * k, b_desc + b_step * k, idesc, (kb > 0 || k > 0) ? 1u : 0u);
-        mma_commit_multicast(empty_bar(stage), readers);
+        mma_commit(empty_bar(stage));
         if (++stage == Cfg::STAGES) {
           stage = 0;
           phase ^= 1u;
@@ -259,7 +230,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(ClCfg::THREADS, 1)
     LinSide<EPI> side;
     if (inside) lin_fetch<EPI>(side, p.lin, lane, p.M, p.N, static_cast<int64_t>(y0) + lane, n0);
     if constexpr (A_MN) {
-      if (summed) sum_rows(p, smem, full_bar(0), empty_bar(0), rn, m0 + rn * kMnBox, wd);
+      if (summed) sum_rows(p, smem, full_bar(0), empty_bar(0), nb, m0 + nb * kMnBox, wd);
     }
     int ok = 1;
     if (lane == 0) ok = wait_phase(accf_bar, 0, wd, kWdEpiAccFull) ? 1 : 0;
@@ -287,37 +258,20 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(ClCfg::THREADS, 1)
 }
 
 cudaError_t prepare(const void* kern) {
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ClCfg::SMEM_BYTES);
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, WaveCfg::SMEM_BYTES);
 }
 
 }  // namespace
 
-int linear_cluster_max(int num_sms) {
-  static std::atomic<int> cached[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  if (cached[dev] > 0) return cached[dev];
-  auto kern = linear_cluster_kernel<kEpiLinear, false, false>;
-  int n = 0;
-  if (prepare(reinterpret_cast<const void*>(kern)) == cudaSuccess) {
-    PdlLaunch l(dim3(static_cast<unsigned>(num_sms / 4 * 4)), dim3(ClCfg::THREADS), ClCfg::SMEM_BYTES, nullptr);
-    if (cudaOccupancyMaxActiveClusters(&n, kern, &l.cfg) != cudaSuccess) n = 0;
-  }
-  (void)cudaGetLastError();
-  if (n <= 0) n = 1;
-  cached[dev] = n;
-  return n;
-}
-
-cudaError_t launch_linear_cluster(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const TcArgs& args,
+cudaError_t launch_linear_wave(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const TcArgs& args,
                                   Epilogue kind, cudaStream_t stream) {
   static std::atomic<bool> attr_done[3][64];
   // the forward product, the input gradient, the weight gradient
   const int which = kind == kEpiLinearGrad ? 1 : args.a_mn ? 2 : 0;
   if (args.a_mn != (which == 2) || args.b_mn != (which != 0)) return cudaErrorInvalidValue;
-  auto kern = which == 0   ? linear_cluster_kernel<kEpiLinear, false, false>
-              : which == 1 ? linear_cluster_kernel<kEpiLinearGrad, false, true>
-                           : linear_cluster_kernel<kEpiLinear, true, true>;
+  auto kern = which == 0   ? linear_wave_kernel<kEpiLinear, false, false>
+              : which == 1 ? linear_wave_kernel<kEpiLinearGrad, false, true>
+                           : linear_wave_kernel<kEpiLinear, true, true>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -325,11 +279,11 @@ cudaError_t launch_linear_cluster(const CUtensorMap& a, const CUtensorMap& b, co
     if ((e = prepare(reinterpret_cast<const void*>(kern))) != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_done[which][dev] = true;
   }
-  PdlLaunch l(dim3(static_cast<unsigned>(args.grid)), dim3(ClCfg::THREADS), ClCfg::SMEM_BYTES, stream);
+  PdlLaunch l(dim3(static_cast<unsigned>(args.grid)), dim3(WaveCfg::THREADS), WaveCfg::SMEM_BYTES, stream);
   return cudaLaunchKernelEx(&l.cfg, kern, a, b, c, args);
 }
 
 // The -DHGEMM_DEBUG build's check word of this file (null otherwise).
-HG_DEBUG_WORD_ACCESSOR(linear_cluster)
+HG_DEBUG_WORD_ACCESSOR(linear_wave)
 
 }  // namespace hg

@@ -88,7 +88,7 @@ struct TcArgs {
   int a_mn, b_mn;            // pair kernel: A stored M-contiguous (K×M), B stored
                              // N-contiguous (K×N); else K-contiguous
   LinEpi lin;                // kEpiLinear and kEpiLinearGrad
-  float* row_sums;           // clusters of 128×64 tiles, kLayoutMn: A's sums over K, or null
+  float* row_sums;           // one wave of 128×64 tiles, kLayoutMn: A's sums over K, or null
   int row_sums_add;          // added to, instead of written
   int batch_tiles;           // pair kernel: whole tiles per product of a batch of
                              // equal products in one launch (0: a single product)
@@ -242,11 +242,9 @@ struct CallDevice {
 int call_device(CallDevice* out);
 int cuda_status(cudaError_t e);
 
-// One wave of 128×64 tiles in clusters of four, and how many clusters the
-// device holds at once (args.grid: 4 per 256×128 outputs).
-cudaError_t launch_linear_cluster(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const TcArgs& args,
+// One wave of 128×64 tiles, a CTA each (args.grid).
+cudaError_t launch_linear_wave(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const TcArgs& args,
                                   Epilogue kind, cudaStream_t stream);
-int linear_cluster_max(int num_sms);
 
 // One product with a linear layer's epilogue, C (M×N) = epilogue(A·B) with A
 // M×K, or K×M when a_mn, and B N×K, or K×N when b_mn.
@@ -349,7 +347,7 @@ cudaError_t debug_word_norm(int** out);
 cudaError_t debug_word_ckpt8(int** out);
 cudaError_t debug_word_linear_any(int** out);
 cudaError_t debug_word_linear_small(int** out);
-cudaError_t debug_word_linear_cluster(int** out);
+cudaError_t debug_word_linear_wave(int** out);
 constexpr int kDebugWords = 14;
 
 // Co-residency limits of the cluster kernels on one device, measured once

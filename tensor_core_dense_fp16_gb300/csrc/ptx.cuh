@@ -3,8 +3,7 @@
 //
 // Each wrapper is one PTX instruction (or a short fixed sequence) with the
 // operand conventions of the PTX ISA. Shared-memory operands are 32-bit
-// shared-window addresses (see smem_u32). A load is multicast in one form only
-// (tma_load_2d_multicast), for CTAs of one cluster that read the same tile.
+// shared-window addresses (see smem_u32). No TMA multicast form is used.
 // In the -DHGEMM_DEBUG build every wrapper that takes a shared-memory
 // address of this CTA checks it (and TMA coordinates, TMEM addresses) first
 // and skips the instruction when the check fails (debug.cuh).
@@ -103,19 +102,6 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
-      : "memory");
-}
-
-// The same into every CTA of `cta_mask` (of this cluster): the box lands at
-// the same shared-memory offset in each, and each one's barrier at the offset
-// of `bar` counts its bytes.
-__device__ __forceinline__ void tma_load_2d_multicast(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t x,
-                                                      int32_t y, uint16_t cta_mask) {
-  if (!HG_DBG_SMEM(dst, 16) || !HG_DBG_SMEM(bar, 8) || !HG_DBG_TMA_X(x)) return;
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-      " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "h"(cta_mask)
       : "memory");
 }
 
@@ -243,14 +229,6 @@ __device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uin
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile(
       "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-      : "memory");
-}
-
-// The same on the barrier at offset `bar` in every CTA of `cta_mask`.
-__device__ __forceinline__ void mma_commit_multicast(uint32_t bar, uint16_t cta_mask) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"(cta_mask)
       : "memory");
 }
 
