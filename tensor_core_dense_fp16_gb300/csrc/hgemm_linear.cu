@@ -203,16 +203,19 @@ cudaError_t rows_tiles(const RowsArgs& p, bool vec, cudaStream_t stream) {
 // same dY, and the two may run at the same time, the sums on SMs that the
 // product leaves idle. Nothing here depends on that product, and what it
 // waited for is complete (it lets this launch start only after its own
-// wait), so the sums need not wait; but the first block ends only after the
-// product has, so that whoever waits for this launch waits for both.
+// wait), so the sums need not wait, and read dY and the old sums from L2
+// behind a fence; but the first block ends only after the product has, so
+// that whoever waits for this launch waits for both.
 constexpr int kSumThreads = 512;
 constexpr int kUnroll = 8;
 template <int VEC>
 __global__ void __launch_bounds__(kSumThreads)
-    column_sums_kernel(const uint16_t* __restrict__ dy, int64_t ld, int64_t M, int64_t N, float* __restrict__ out,
+    column_sums_kernel(const uint16_t* dy, int64_t ld, int64_t M, int64_t N, float* out,
                        int accumulate, int across, int cluster, int beside) {
   __shared__ float s[kSumThreads * VEC];  // [down][columns]
-  if (!beside) {
+  if (beside) {
+    fence_gpu();
+  } else {
     grid_dependency_wait();
     grid_launch_dependents();
   }
@@ -229,10 +232,9 @@ __global__ void __launch_bounds__(kSumThreads)
       for (int k = 0; k < kUnroll; ++k) {
         const int64_t row = m + k * down;
         if constexpr (VEC == 8)
-          *reinterpret_cast<uint4*>(v[k]) = row < m1 ? __ldg(reinterpret_cast<const uint4*>(dy + row * ld + n0 + c))
-                                                     : make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(v[k]) = row < m1 ? ld_gpu_16(dy + row * ld + n0 + c) : make_uint4(0u, 0u, 0u, 0u);
         else
-          v[k][0] = row < m1 ? __ldg(dy + row * ld + n0 + c) : static_cast<uint16_t>(0);
+          v[k][0] = row < m1 ? ld_gpu_u16(dy + row * ld + n0 + c) : static_cast<uint16_t>(0);
       }
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k)
@@ -257,7 +259,7 @@ __global__ void __launch_bounds__(kSumThreads)
     cluster_sync();  // the other ranks' shared memory stays until rank 0 has read it
   }
   const int64_t n = n0 + threadIdx.x;
-  if (rank == 0 && mine && n < N) out[n] = accumulate ? out[n] + total : total;
+  if (rank == 0 && mine && n < N) out[n] = accumulate ? ld_gpu_f32(out + n) + total : total;
   if (beside && blockIdx.x == 0) grid_dependency_wait();
 }
 
@@ -268,13 +270,14 @@ __global__ void __launch_bounds__(kSumThreads)
 // (8 lanes along a row, 16 bytes each, 32 rows at a time) of a run of rows; its
 // cluster adds the runs in rank order. With the product, which alone takes the
 // first time, us, and with the wide blocks above: dY 8192×8192, X 8192×2048
-// 157, 162, 180; 4096×8192, 4096×2048 82, 84, 93; 2048 all 14.7, 16.5, 20.3;
-// but 8192×2048, 8192×8192 156, 171, 164.
+// 155, 160, 180; 4096×8192, 8192×2048 87, 89, 93; 2048 all 14.6, 16.1, 20.3;
+// but 8192×2048, 8192×8192 163, 166, 164.
 constexpr int kThinColumns = 64;
 constexpr int kThinThreads = 256;
 __global__ void __launch_bounds__(kThinThreads)
-    column_sums_thin_kernel(const uint16_t* __restrict__ dy, int64_t ld, int64_t M, int64_t N, float* __restrict__ out,
-                            int accumulate, int cluster) {
+    column_sums_thin_kernel(const uint16_t* dy, int64_t ld, int64_t M, int64_t N, float* out, int accumulate,
+                            int cluster) {
+  fence_gpu();
   __shared__ float s[3][kThinColumns];
   constexpr int WARPS = kThinThreads / 32, STEP = 4 * WARPS;  // rows per step
   const int rank = static_cast<int>(blockIdx.x) % cluster;
@@ -288,8 +291,7 @@ __global__ void __launch_bounds__(kThinThreads)
       uint4 v[kUnroll];
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k)
-        v[k] = m + k * STEP < m1 ? __ldg(reinterpret_cast<const uint4*>(p + (m + k * STEP) * ld))
-                                 : make_uint4(0u, 0u, 0u, 0u);
+        v[k] = m + k * STEP < m1 ? ld_gpu_16(p + (m + k * STEP) * ld) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) add8(sum, v[k]);
     }
@@ -326,7 +328,7 @@ __global__ void __launch_bounds__(kThinThreads)
     for (int i = 1; i < cluster; ++i)
       total += ld_cluster_f32(mapa_shared(smem_u32(&s[0][threadIdx.x]), static_cast<uint32_t>(i)));
     float* o = out + n0 + threadIdx.x;
-    *o = accumulate ? *o + total : total;
+    *o = accumulate ? ld_gpu_f32(o) + total : total;
   }
   cluster_sync();  // the other ranks' shared memory stays until rank 0 has read it
   if (blockIdx.x == 0) grid_dependency_wait();

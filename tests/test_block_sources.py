@@ -26,3 +26,27 @@ def test_no_load_is_multicast():
     for name, text in sources().items():
         for call in re.findall(r"asm volatile\((.*?)\);", code(text), flags=re.S):
             assert not ("cp.async.bulk" in call and "multicast" in call), name
+
+
+def kernel(text, name):
+    """A kernel's body."""
+    start = text.index("{", text.index(name + "("))
+    depth, i = 1, start + 1
+    while depth:
+        depth += {"{": 1, "}": -1}.get(text[i], 0)
+        i += 1
+    return text[start:i]
+
+
+def test_sums_beside_a_product_read_behind_a_fence_from_l2():
+    """The column sums do not wait for the launches before them: what these
+    wrote is read with loads that cannot meet an older line."""
+    text = code(sources()["hgemm_linear.cu"])
+    for name in ("column_sums_kernel", "column_sums_thin_kernel"):
+        body = kernel(text, name)
+        loop = body.index("for (")
+        assert 0 <= body.find("fence_gpu()") < loop, name
+        assert "__ldg" not in body and body.count("ld_gpu_16(") == 1, name
+        # dy and the old sums, and nothing else in global memory
+        assert not re.search(r"\bdy\s*\[|\*\s*\(?\s*dy\b|\bout\s*\[[^\]]*\]\s*\+|\*o\s*\+", body), name
+        assert "ld_gpu_f32(" in body, name
