@@ -33,8 +33,8 @@ __device__ __forceinline__ bool piece_of(int64_t M, int64_t N, int cols, Piece& 
 
 // N, the pitches and the bases let eight columns be moved at once.
 __global__ void __launch_bounds__(256)
-    ckpt8_save_vec_kernel(const uint16_t* __restrict__ x, int64_t ldx, int8_t* __restrict__ codes, int64_t ldq,
-                          float* __restrict__ scales, int64_t lds, int64_t M, int64_t N) {
+    ckpt8_save_vec_kernel(const uint16_t* x, int64_t ldx, int8_t* codes, int64_t ldq,
+                          float* scales, int64_t lds, int64_t M, int64_t N) {
   grid_dependency_wait();
   grid_launch_dependents();
   Piece p;
@@ -45,8 +45,7 @@ __global__ void __launch_bounds__(256)
   uint4 v[kRows];
 #pragma unroll
   for (int r = 0; r < kRows; ++r)
-    v[r] = in_n && p.m0 + r < M ? __ldg(reinterpret_cast<const uint4*>(x + (p.m0 + r) * ldx + n))
-                                : make_uint4(0u, 0u, 0u, 0u);
+    v[r] = in_n && p.m0 + r < M ? load16(x + (p.m0 + r) * ldx + n) : make_uint4(0u, 0u, 0u, 0u);
   float mine = 0.f;  // lane 8g + r keeps the scale of group g, row r
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
@@ -75,8 +74,8 @@ __global__ void __launch_bounds__(256)
 
 // Any pitch and alignment: one group per warp, two columns per lane.
 __global__ void __launch_bounds__(256)
-    ckpt8_save_kernel(const uint16_t* __restrict__ x, int64_t ldx, int8_t* __restrict__ codes, int64_t ldq,
-                      float* __restrict__ scales, int64_t lds, int64_t M, int64_t N) {
+    ckpt8_save_kernel(const uint16_t* x, int64_t ldx, int8_t* codes, int64_t ldq,
+                      float* scales, int64_t lds, int64_t M, int64_t N) {
   grid_dependency_wait();
   grid_launch_dependents();
   Piece p;
@@ -107,7 +106,7 @@ __global__ void __launch_bounds__(256)
 }
 
 __global__ void __launch_bounds__(256)
-    ckpt8_load_vec_kernel(const int8_t* __restrict__ codes, int64_t ldq, const float* __restrict__ scales,
+    ckpt8_load_vec_kernel(const int8_t* codes, int64_t ldq, const float* scales,
                           int64_t lds, int act, uint16_t* __restrict__ y, int64_t ldy, int64_t M, int64_t N) {
   grid_dependency_wait();
   grid_launch_dependents();
@@ -119,11 +118,10 @@ __global__ void __launch_bounds__(256)
   uint2 w[kRows];
 #pragma unroll
   for (int r = 0; r < kRows; ++r)
-    w[r] = in_n && p.m0 + r < M ? __ldg(reinterpret_cast<const uint2*>(codes + (p.m0 + r) * ldq + n))
-                                : make_uint2(0u, 0u);
+    w[r] = in_n && p.m0 + r < M ? load8(codes + (p.m0 + r) * ldq + n) : make_uint2(0u, 0u);
   const int64_t m = p.m0 + (lane & 7);
   const int64_t g = n / kCkptGroup;  // (its last lanes may be past N)
-  const float mine = g * kCkptGroup < N && m < M ? __ldg(scales + g * lds + m) : 0.f;
+  const float mine = g * kCkptGroup < N && m < M ? scales[g * lds + m] : 0.f;
   with_activation(act, [&](auto a) {
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
@@ -139,8 +137,8 @@ __global__ void __launch_bounds__(256)
 }
 
 __global__ void __launch_bounds__(256)
-    ckpt8_load_kernel(const int8_t* __restrict__ codes, int64_t ldq, const float* __restrict__ scales, int64_t lds,
-                      int act, uint16_t* __restrict__ y, int64_t ldy, int64_t M, int64_t N) {
+    ckpt8_load_kernel(const int8_t* codes, int64_t ldq, const float* scales, int64_t lds,
+                      int act, uint16_t* y, int64_t ldy, int64_t M, int64_t N) {
   grid_dependency_wait();
   grid_launch_dependents();
   Piece p;

@@ -12,7 +12,7 @@ namespace {
 // columns per lane.
 template <bool BACKWARD>
 __global__ void __launch_bounds__(256)
-    linear_empty_kernel(uint16_t* __restrict__ C, int64_t ldc, int64_t M, int64_t N, const LinEpi e) {
+    linear_empty_kernel(uint16_t* C, int64_t ldc, int64_t M, int64_t N, const LinEpi e) {
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31;
@@ -41,15 +41,6 @@ __global__ void __launch_bounds__(256)
 }
 
 // ------------------------------------------------------------ few rows of X
-
-// Loads of weights that this launch reads once: past L1, which keeps X.
-__device__ __forceinline__ uint4 load_once16(const uint16_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
 
 // D (16×8, FP32) += A (16×16) · B (16×8).
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -112,13 +103,13 @@ __global__ void __launch_bounds__(WARPS * 32) linear_rows_kernel(const RowsArgs 
   auto load = [&](const uint16_t* row, int k, bool weights) {
     if constexpr (VEC) {
       if (k >= p.K) return make_uint4(0u, 0u, 0u, 0u);
-      return weights ? load_once16(row + k) : __ldg(reinterpret_cast<const uint4*>(row + k));
+      return weights ? load16_once(row + k) : load16(row + k);  // (L1 keeps X)
     } else {
       uint32_t v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = k + 2 * i < p.K ? __ldg(row + k + 2 * i) : 0u;
-        const uint32_t hi = k + 2 * i + 1 < p.K ? __ldg(row + k + 2 * i + 1) : 0u;
+        const uint32_t lo = k + 2 * i < p.K ? row[k + 2 * i] : 0u;
+        const uint32_t hi = k + 2 * i + 1 < p.K ? row[k + 2 * i + 1] : 0u;
         v[i] = lo | hi << 16;
       }
       return make_uint4(v[0], v[1], v[2], v[3]);

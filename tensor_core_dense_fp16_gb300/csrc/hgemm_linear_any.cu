@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1)
     float* row_scale = turn + 32 * (Cfg::TURN_COLS + 1);
     float* row_inv = row_scale + 32;
     auto bias_at = [&](int64_t n) {
-      return !BACKWARD && e.bias && n < p.N ? __half2float(__ushort_as_half(__ldg(e.bias + n))) : 0.f;
+      return !BACKWARD && e.bias && n < p.N ? __half2float(__ushort_as_half(e.bias[n])) : 0.f;
     };
     int acc = 0;
     uint32_t acc_phase = 0;

@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(192, 1)
   const int f = f0 + q * 32 + lane;  // this epilogue thread's feature
   const bool in_f = f < p.N;
   const float bias =
-      !BACKWARD && warp >= 2 && p.epi.bias && in_f ? __half2float(__ushort_as_half(__ldg(p.epi.bias + f))) : 0.f;
+      !BACKWARD && warp >= 2 && p.epi.bias && in_f ? __half2float(__ushort_as_half(p.epi.bias[f])) : 0.f;
 
   if (warp == 0) {
     if (elect_one()) {

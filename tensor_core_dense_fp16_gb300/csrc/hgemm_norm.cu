@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(512, 1) layernorm_backward_ring_kernel(const N
   for (int i = 0; i < NV; ++i) {
     const int c = (t + i * G) * 8;
     gamma[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (c < D) gamma[i] = __ldg(reinterpret_cast<const uint4*>(a.gamma + c));
+    if (c < D) gamma[i] = *reinterpret_cast<const uint4*>(a.gamma + c);
 #pragma unroll
     for (int k = 0; k < 4; ++k) dgamma[i][k] = dbeta[i][k] = 0;  // a pair of +0
   }

@@ -142,10 +142,10 @@ __device__ __forceinline__ void prefetch_c_row(const EpiArgs& e, const uint16_t*
 __device__ __forceinline__ uint4 load_bias8(const uint16_t* bias, int64_t col0, int64_t N) {
   if (!bias || col0 >= N) return make_uint4(0u, 0u, 0u, 0u);
   if ((reinterpret_cast<uintptr_t>(bias) & 15u) == 0 && col0 + 8 <= N)
-    return __ldg(reinterpret_cast<const uint4*>(bias + col0));
+    return *reinterpret_cast<const uint4*>(bias + col0);
   uint16_t h[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) h[i] = col0 + i < N ? __ldg(bias + col0 + i) : static_cast<uint16_t>(0);
+  for (int i = 0; i < 8; ++i) h[i] = col0 + i < N ? bias[col0 + i] : static_cast<uint16_t>(0);
   return make_uint4(h[0] | (static_cast<uint32_t>(h[1]) << 16), h[2] | (static_cast<uint32_t>(h[3]) << 16),
                     h[4] | (static_cast<uint32_t>(h[5]) << 16), h[6] | (static_cast<uint32_t>(h[7]) << 16));
 }

@@ -309,6 +309,34 @@ __device__ __forceinline__ void tmem_ld_32x32b_x4(uint32_t taddr, float (&r)[4])
       : "memory");
 }
 
+// ------------------------------------------------------- global loads
+
+// Loads that stay in the order and place in which they are written, so that
+// all of a batch are under way before the first is used. Not the non-coherent
+// path (ld.global.nc, __ldg): that one needs memory which nobody writes while
+// the kernel lives, and a kernel that starts early shares some of its life with
+// the launch that writes its operands.
+__device__ __forceinline__ uint4 load16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 load8(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+// The same for what this launch reads once: past L1.
+__device__ __forceinline__ uint4 load16_once(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 // ------------------------------------------------- pairs of FP32 values
 
 // Two FP32 values in one 64-bit register pair; the instructions below treat

@@ -10,8 +10,6 @@ from gpu_helpers import torch_cuda
 
 pytestmark = pytest.mark.gpu
 
-HALF_ULP = 2.0 ** -11
-
 
 # whole numbers small enough that every sum is exact in FP32
 def whole(rng, torch, *shape):
@@ -42,3 +40,56 @@ def test_sums_beside_their_product(M, N, K):
     assert tc.hgemm_device_status() == tc.HGEMM_OK
     for i, g in enumerate(got):
         assert torch.equal(g.double(), wants[i % 3] + (old.double() if i % 2 == 1 else 0)), i
+
+
+# the two kernels that ask L2 for weights ahead of their wait, and the others
+@pytest.mark.parametrize("M,N,K", [(1, 1024, 2048), (5, 264, 520), (3, 65, 77), (24, 2048, 2048), (100, 520, 4104),
+                                   (40, 2051, 1001), (300, 264, 520), (2048, 2048, 256)])
+def test_operands_written_just_before(M, N, K):
+    """Weights and rows written by the launch ahead, another value every time."""
+    torch = torch_cuda()
+    rng = np.random.default_rng(M + N + K)
+    xs, ws, bs = ([whole(rng, torch, *s) for _ in range(3)] for s in ((M, K), (N, K), (N,)))
+    wants = [x.double() @ w.double().t() + b.double() for x, w, b in zip(xs, ws, bs)]
+    x, w, b = (torch.empty_like(t[0]) for t in (xs, ws, bs))
+    y = torch.empty((M, N), dtype=torch.float16, device="cuda")
+    got = []
+    for i in range(15):
+        b.copy_(bs[i % 3])
+        # the last launch ahead is the one that writes the rows, or the weights
+        for dst, src in ((x, xs), (w, ws))[:: 1 if i % 2 else -1]:
+            dst.copy_(src[i % 3])
+        tc.hgemm_linear(x, K, w, K, b, tc.HGEMM_ACT_NONE, None, 0, y, N, M, N, K)
+        got.append(y.clone())
+        x.fill_(float("nan"))
+        w.fill_(float("nan"))
+    assert tc.hgemm_device_status() == tc.HGEMM_OK
+    for i, g in enumerate(got):
+        assert torch.equal(g.double(), wants[i % 3].half().double()), i
+
+
+def test_a_chain_of_early_starts():
+    """Each launch's output is the next one's operand, as X, as W and in 8 bits,
+    with kernels that start early on both sides."""
+    torch = torch_cuda()
+    rng = np.random.default_rng(3)
+    d = 1024
+    f16 = dict(dtype=torch.float16, device="cuda")
+    eye = torch.eye(d, **f16)
+    q, s = torch.empty((d, d), dtype=torch.int8, device="cuda"), torch.empty((d // 64, d), device="cuda")
+    one = torch.ones(d, **f16)
+    for i in range(10):
+        src = whole(rng, torch, d, d)
+        want = torch.layer_norm(src[:8].double(), (d,), eps=1e-5)
+        w, back, x, y = (torch.empty((d, d), **f16) for _ in range(4))
+        tc.hgemm_linear(src, d, eye, d, None, 0, None, 0, w, d, d, d, d)       # w = src, one wave of tiles
+        tc.hgemm_linear(eye, d, w, d, None, 0, None, 0, x, d, 8, d, d)         # 8 rows: x = srcᵀ's first rows
+        tc.hgemm_ckpt8_save(w, d, q, d, s, d, d, d)
+        tc.hgemm_ckpt8_load(q, d, s, d, 0, back, d, d, d)
+        tc.hgemm_layernorm_forward(w, d, one, one - 1, 1e-5, y, d, None, None, 8, d)
+        w.fill_(float("nan"))
+        assert torch.equal(x[:8], src.t()[:8])
+        # (values 0, 1 and 2 of 2: 127, 64 and 0 steps)
+        assert (back.double() - src.double()).abs().max() <= 1 / 127
+        assert (y[:8].double() - want).abs().max() <= 2.0 ** -9 * want.abs().max()
+    assert tc.hgemm_device_status() == tc.HGEMM_OK

@@ -50,3 +50,16 @@ def test_sums_beside_a_product_read_behind_a_fence_from_l2():
         # dy and the old sums, and nothing else in global memory
         assert not re.search(r"\bdy\s*\[|\*\s*\(?\s*dy\b|\bout\s*\[[^\]]*\]\s*\+|\*o\s*\+", body), name
         assert "ld_gpu_f32(" in body, name
+
+
+BLOCK = ("hgemm_linear.cu", "hgemm_linear_any.cu", "hgemm_linear_small.cu", "hgemm_linear_wave.cu", "hgemm_norm.cu",
+         "hgemm_ckpt8.cu", "linear_epilogue.cuh", "kernel_common.cuh")
+
+
+def test_no_operand_is_read_through_the_non_coherent_path():
+    """That path needs memory which nobody writes while the kernel lives, and
+    these kernels start while the launch before them may still write."""
+    for name in BLOCK:
+        text = code(sources()[name])
+        for what in (r"__ldg", r"ld\.global\.nc", r"const\s+\w+\s*\*\s*__restrict__"):
+            assert not re.search(what, text), (name, what)
