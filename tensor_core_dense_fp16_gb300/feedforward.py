@@ -98,6 +98,12 @@ class FeedForward:
 
     def backward(self, dy, s: Saved) -> FeedForwardGradients:
         m, d, f = self._rows(dy, "dy"), self.D, self.F
+        # what was saved is read by dy's sizes
+        for name, t, shape in (("x", s.x, (m, d)), ("mean", s.mean, (m,)), ("rstd", s.rstd, (m,)),
+                               ("codes", s.codes, (m, f)),
+                               ("scales", s.scales, (-(-f // tc.HGEMM_CKPT8_GROUP), m))):
+            if tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"saved {name} must be {shape} and contiguous for this dy, got {tuple(t.shape)}")
         # through the second product and the activation; a = f(u) comes with it
         du, a = self._half(m, f), self._half(m, f)
         tc.hgemm_linear_dgrad(dy, d, self.w2, f, s.codes, f, s.scales, max(m, 1), self.act, du, f, a, f, m, d, f)
