@@ -518,6 +518,8 @@ def hgemm_layernorm_backward(dY, lddy: int, X, ldx: int, gamma, mean, rstd, R, l
                              stream=None) -> None:
     """dX, dgamma and dbeta of a layer norm, R added to dX (see hgemm.h); the
     workspace's size defaults to the tensor's bytes."""
+    if workspace is not None and type(workspace) is not int and not getattr(workspace, "is_cuda", False):
+        raise ValueError("workspace must be a CUDA tensor")
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size() if hasattr(workspace, "numel") else 0
     _raise_on((_lib or load()).hgemm_layernorm_backward(

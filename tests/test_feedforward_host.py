@@ -1,6 +1,9 @@
 """Argument checks of the feed-forward block (CPU: no computing call is made)."""
 
+import numpy as np
 import pytest
+
+import tensor_core_dense_fp16_gb300 as tc
 
 torch = pytest.importorskip("torch")
 
@@ -46,3 +49,11 @@ def test_rows_and_weights_are_checked():
         FeedForward(half(D), half(D), half(D, F).t(), half(F), half(D, F), half(D))
     with pytest.raises(KeyError):
         FeedForward(half(D), half(D), half(F, D), half(F), half(D, F), half(D), act="tanh")
+
+
+@pytest.mark.parametrize("workspace", [torch.zeros(1 << 20, dtype=torch.uint8), np.zeros(1 << 20, np.uint8)])
+def test_a_workspace_in_host_memory_is_refused(workspace):
+    a = [0x10000000 * (i + 1) for i in range(10)]
+    with pytest.raises(ValueError, match="workspace"):
+        tc.hgemm_layernorm_backward(a[0], 64, a[1], 64, a[2], a[3], a[4], None, 0, a[5], 64, a[6], a[7], workspace, 0,
+                                    64, stream=0)
