@@ -287,7 +287,9 @@ __global__ void __launch_bounds__(512, 1) layernorm_backward_ring_kernel(const N
     const uint4* sdy = reinterpret_cast<const uint4*>(ring + static_cast<uint32_t>(stage) * stage_bytes + row_bytes);
     const uint4* sres =
         reinterpret_cast<const uint4*>(ring + static_cast<uint32_t>(stage) * stage_bytes + 2 * row_bytes);
-    const f32x2 scale = pair_of(rs), shift = pair_of(-mu * rs);
+    // (x̂ from the difference: x·rstd − mean·rstd loses its digits in a row far
+    // from zero)
+    const f32x2 scale = pair_of(rs), shift = pair_of(-mu);
     f32x2 p1 = 0, p2 = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -299,7 +301,7 @@ __global__ void __launch_bounds__(512, 1) layernorm_backward_ring_kernel(const N
         unpack8(gamma[i], g);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const f32x2 xh = fma2(x[k], scale, shift), gy = mul2(dy[k], g[k]);
+          const f32x2 xh = mul2(add2(x[k], shift), scale), gy = mul2(dy[k], g[k]);
           p1 = add2(p1, gy);
           p2 = fma2(gy, xh, p2);
           dgamma[i][k] = fma2(dy[k], xh, dgamma[i][k]);
@@ -336,7 +338,7 @@ __global__ void __launch_bounds__(512, 1) layernorm_backward_ring_kernel(const N
       const int64_t ahead = m + (stages - 1) * step;
       if (ahead < a.M && !*abort_flag) copy_row(ahead, stage == 0 ? stages - 1 : stage - 1);
     }
-    const f32x2 k1 = pair_of(-rs * (s1 * inv_d)), k2 = pair_of(-rs * (s2 * inv_d));
+    const f32x2 k1 = pair_of(-rs * (s1 * inv_d)), k2 = pair_of(-rs * (s2 * inv_d) * rs);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = t + i * G;
@@ -347,7 +349,7 @@ __global__ void __launch_bounds__(512, 1) layernorm_backward_ring_kernel(const N
         unpack8(gamma[i], g);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          x[k] = fma2(mul2(dy[k], g[k]), scale, fma2(fma2(x[k], scale, shift), k2, k1));
+          x[k] = fma2(mul2(dy[k], g[k]), scale, fma2(add2(x[k], shift), k2, k1));
         if (RES) {
           unpack8(sres[v], dy);
 #pragma unroll
