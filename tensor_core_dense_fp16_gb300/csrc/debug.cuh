@@ -6,8 +6,8 @@
 // to be 16-byte aligned (8 FP16 elements), every TMEM load to stay inside the
 // 512 columns, and the kernels that address global memory themselves (the
 // generic, substitution and elementwise kernels, the fused epilogue's reads
-// of C and the bias) check each computed index against the extent it must
-// stay in. A failed check records a code in its translation unit's debug
+// of C and the bias, the feed-forward block's operators) check each computed
+// index against the extent it must stay in. A failed check records a code in its translation unit's debug
 // word and SKIPS the access (a copy that is skipped leaves its barrier
 // short, so the waiting side runs into its bounded wait and the kernel
 // leaves with the watchdog code set): no trap, no fault. The host reads and
@@ -112,6 +112,15 @@ __device__ __forceinline__ bool dbg_smem(uint32_t addr, uint32_t bytes) {
     *out = nullptr;                          \
     return cudaSuccess;                      \
   }
+#endif
+
+#ifdef __CUDACC__
+// Elements n .. n + count - 1 of a row of N, at p, accessed `bytes` at a time.
+__device__ __forceinline__ bool dbg_row([[maybe_unused]] const void* p, [[maybe_unused]] int64_t n,
+                                        [[maybe_unused]] int count, [[maybe_unused]] int64_t N,
+                                        [[maybe_unused]] int bytes) {
+  return HG_DBG_INDEX(n, N) && HG_DBG_INDEX(n + count - 1, N) && HG_DBG_ALIGN(p, bytes);
+}
 #endif
 
 }  // namespace hg

@@ -45,7 +45,8 @@ __global__ void __launch_bounds__(256)
   uint4 v[kRows];
 #pragma unroll
   for (int r = 0; r < kRows; ++r)
-    v[r] = in_n && p.m0 + r < M ? load16(x + (p.m0 + r) * ldx + n) : make_uint4(0u, 0u, 0u, 0u);
+    v[r] = in_n && p.m0 + r < M && dbg_row(x + (p.m0 + r) * ldx + n, n, 8, N, 16) ? load16(x + (p.m0 + r) * ldx + n)
+                                                                                  : make_uint4(0u, 0u, 0u, 0u);
   float mine = 0.f;  // lane 8g + r keeps the scale of group g, row r
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
@@ -63,13 +64,13 @@ __global__ void __launch_bounds__(256)
     float scale, inv;
     ckpt_scale(bits, scale, inv);
     if ((lane & 7) == r) mine = scale;
-    if (in_n && p.m0 + r < M)
+    if (in_n && p.m0 + r < M && dbg_row(codes + (p.m0 + r) * ldq + n, n, 8, N, 8))
       *reinterpret_cast<uint2*>(codes + (p.m0 + r) * ldq + n) =
           make_uint2(ckpt_word(u[0], u[1], inv), ckpt_word(u[2], u[3], inv));
   }
   const int64_t m = p.m0 + (lane & 7);
   const int64_t g = n / kCkptGroup;  // (its last lanes may be past N)
-  if (g * kCkptGroup < N && m < M) scales[g * lds + m] = mine;
+  if (g * kCkptGroup < N && m < M && HG_DBG_INDEX(m, lds)) scales[g * lds + m] = mine;
 }
 
 // Any pitch and alignment: one group per warp, two columns per lane.
@@ -102,7 +103,8 @@ __global__ void __launch_bounds__(256)
         codes[(p.m0 + r) * ldq + n] = static_cast<int8_t>(inv == 0.f ? 0u : ckpt_code(u[r][i], inv));
     }
   }
-  if (lane < kRows && p.m0 + lane < M) scales[p.n0 / kCkptGroup * lds + p.m0 + lane] = mine;
+  if (lane < kRows && p.m0 + lane < M && HG_DBG_INDEX(p.n0, N) && HG_DBG_INDEX(p.m0 + lane, lds))
+    scales[p.n0 / kCkptGroup * lds + p.m0 + lane] = mine;
 }
 
 __global__ void __launch_bounds__(256)
@@ -118,10 +120,12 @@ __global__ void __launch_bounds__(256)
   uint2 w[kRows];
 #pragma unroll
   for (int r = 0; r < kRows; ++r)
-    w[r] = in_n && p.m0 + r < M ? load8(codes + (p.m0 + r) * ldq + n) : make_uint2(0u, 0u);
+    w[r] = in_n && p.m0 + r < M && dbg_row(codes + (p.m0 + r) * ldq + n, n, 8, N, 8)
+               ? load8(codes + (p.m0 + r) * ldq + n)
+               : make_uint2(0u, 0u);
   const int64_t m = p.m0 + (lane & 7);
   const int64_t g = n / kCkptGroup;  // (its last lanes may be past N)
-  const float mine = g * kCkptGroup < N && m < M ? scales[g * lds + m] : 0.f;
+  const float mine = g * kCkptGroup < N && m < M && HG_DBG_INDEX(m, lds) ? scales[g * lds + m] : 0.f;
   with_activation(act, [&](auto a) {
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
@@ -131,7 +135,8 @@ __global__ void __launch_bounds__(256)
       for (int i = 0; i < 4; ++i)
         activate<decltype(a)::value, false>(
             mul2(ckpt_pair((i < 2 ? w[r].x : w[r].y) ^ 0x80808080u, i & 1), pair_of(scale)), f[i], df);
-      if (in_n && p.m0 + r < M) *reinterpret_cast<uint4*>(y + (p.m0 + r) * ldy + n) = pack8(f);
+      if (in_n && p.m0 + r < M && dbg_row(y + (p.m0 + r) * ldy + n, n, 8, N, 16))
+        *reinterpret_cast<uint4*>(y + (p.m0 + r) * ldy + n) = pack8(f);
     }
   });
 }
@@ -153,7 +158,7 @@ __global__ void __launch_bounds__(256)
       c[r][i] = n < N && p.m0 + r < M ? codes[(p.m0 + r) * ldq + n] : static_cast<int8_t>(0);
     }
   const int64_t m = p.m0 + (lane & 7);
-  const float mine = m < M ? scales[p.n0 / kCkptGroup * lds + m] : 0.f;
+  const float mine = m < M && HG_DBG_INDEX(p.n0, N) && HG_DBG_INDEX(m, lds) ? scales[p.n0 / kCkptGroup * lds + m] : 0.f;
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
     const float scale = __shfl_sync(0xffffffffu, mine, r);

@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(256)
     }
     for (int i = 0; i < 2; ++i) {
       const int64_t n = g * kCkptGroup + lane + 32 * i;
-      if (n < N) lin_scalar<BACKWARD>(e, u[i], m, n, scale, inv, C + m * ldc + n);
+      if (n < N && HG_DBG_INDEX(m, M)) lin_scalar<BACKWARD>(e, u[i], m, n, scale, inv, C + m * ldc + n);
     }
   }
 }
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(WARPS * 32) linear_rows_kernel(const RowsArgs 
   const uint16_t* w1 = p.W + static_cast<int64_t>(min(n0 + g + 8, p.N - 1)) * p.ldw;
   auto load = [&](const uint16_t* row, int k, bool weights) {
     if constexpr (VEC) {
-      if (k >= p.K) return make_uint4(0u, 0u, 0u, 0u);
+      if (k >= p.K || !dbg_row(row + k, k, 8, p.K, 16)) return make_uint4(0u, 0u, 0u, 0u);
       return weights ? load16_once(row + k) : load16(row + k);  // (L1 keeps X)
     } else {
       uint32_t v[4];
@@ -157,7 +157,8 @@ __global__ void __launch_bounds__(WARPS * 32) linear_rows_kernel(const RowsArgs 
 #pragma unroll
     for (int w = 1; w < WARPS; ++w) u += part[w][m][f];
     if (p.epi.bias) u += __half2float(__ushort_as_half(p.epi.bias[n0 + f]));
-    lin_scalar<false>(p.epi, u, m, n0 + f, 0.f, 0.f, p.Y + m * p.ldy + n0 + f);
+    if (HG_DBG_INDEX(n0 + f, p.N) && HG_DBG_INDEX(m, p.M))
+      lin_scalar<false>(p.epi, u, m, n0 + f, 0.f, 0.f, p.Y + m * p.ldy + n0 + f);
   }
 }
 
@@ -223,9 +224,11 @@ __global__ void __launch_bounds__(kSumThreads)
       for (int k = 0; k < kUnroll; ++k) {
         const int64_t row = m + k * down;
         if constexpr (VEC == 8)
-          *reinterpret_cast<uint4*>(v[k]) = row < m1 ? ld_gpu_16(dy + row * ld + n0 + c) : make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(v[k]) = row < m1 && dbg_row(dy + row * ld + n0 + c, n0 + c, 8, N, 16)
+                                                ? ld_gpu_16(dy + row * ld + n0 + c)
+                                                : make_uint4(0u, 0u, 0u, 0u);
         else
-          v[k][0] = row < m1 ? ld_gpu_u16(dy + row * ld + n0 + c) : static_cast<uint16_t>(0);
+          v[k][0] = row < m1 && dbg_row(dy, n0 + c, 1, N, 2) ? ld_gpu_u16(dy + row * ld + n0 + c) : static_cast<uint16_t>(0);
       }
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k)
@@ -282,7 +285,8 @@ __global__ void __launch_bounds__(kThinThreads)
       uint4 v[kUnroll];
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k)
-        v[k] = m + k * STEP < m1 ? ld_gpu_16(p + (m + k * STEP) * ld) : make_uint4(0u, 0u, 0u, 0u);
+        v[k] = m + k * STEP < m1 && dbg_row(p + (m + k * STEP) * ld, n, 8, N, 16) ? ld_gpu_16(p + (m + k * STEP) * ld)
+                                                                                  : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) add8(sum, v[k]);
     }

@@ -122,10 +122,20 @@ __device__ __forceinline__ int any_shift(const uint16_t* segment) {
   return static_cast<int>(reinterpret_cast<uintptr_t>(segment) >> 1) & 7;
 }
 
+// The checking build: a piece lies between the 16 bytes in which the matrix
+// begins and its end.
+__device__ __forceinline__ bool any_inside([[maybe_unused]] const AnyOperand& o, [[maybe_unused]] const uint16_t* at,
+                                           [[maybe_unused]] int elements) {
+  [[maybe_unused]] const uint16_t* begin = o.p - any_shift(o.p);
+  return HG_DBG_ALIGN(at, 16) && HG_DBG_INDEX(at - begin, o.end - begin) &&
+         HG_DBG_INDEX(at + elements - 1 - begin, o.end - begin);
+}
+
 // One aligned piece at an edge on its way into the warp's buffer: what is past
 // the matrix's last element is not read and becomes zeros.
 __device__ __forceinline__ void any_copy_edge(const AnyOperand& o, const uint16_t* at, uint32_t dst) {
   const int elements = any_clamp(o.end - at, 8);
+  if (elements > 0 && !any_inside(o, at, elements)) return;
   cp_async_16(dst, elements > 0 ? at : o.p - any_shift(o.p), 2 * elements);
 }
 
@@ -188,7 +198,8 @@ __device__ __noinline__ void any_columns(const LinearProduct& p, const float* tu
   const int r0 = lane >> 4;
   const int64_t m = m0 + r0;
   // rows of this lane that are inside: i < count
-  const int count = n < p.N ? any_clamp((p.M - m + 1) / 2, 16) : 0;
+  int count = n < p.N ? any_clamp((p.M - m + 1) / 2, 16) : 0;
+  if (count > 0 && !(HG_DBG_INDEX(n, p.N) && HG_DBG_INDEX(m + 2 * (count - 1), p.M))) count = 0;
   turn += r0 * PITCH + (lane & 15);
   row_scale += r0;
   row_inv += r0;
@@ -398,9 +409,9 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1)
             const int i = lane + 32 * c;
             const bool of_a = i < Cfg::PIECES / 2;
             if (i < Cfg::PIECES) {
-              if (whole)
-                cp_async_16(smem_u32(dst + 32 * 16 * c), at[c], 16);
-              else
+              if (whole) {
+                if (any_inside(of_a ? oa : ob, at[c], 8)) cp_async_16(smem_u32(dst + 32 * 16 * c), at[c], 16);
+              } else
                 any_copy_edge(of_a ? oa : ob, at[c], smem_u32(dst + 32 * 16 * c));
             }
             at[c] += of_a ? step_a : step_b;
@@ -588,7 +599,7 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1)
 #pragma unroll
           for (int r = lane >> 3; r < 32; r += 4) {
             const int64_t m = u.m0 + q * 32 + r;
-            if (m < p.M && n < p.N)
+            if (m < p.M && n < p.N && dbg_row(p.C + m * p.ldc + n, n, 8, p.N, 16))
               *reinterpret_cast<uint4*>(p.C + m * p.ldc + n) =
                   *reinterpret_cast<const uint4*>(box + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
           }
@@ -598,7 +609,7 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1)
         if (e.codes) {
           float* s = e.scales + col0 / kCkptGroup * e.lds + gi;
           if constexpr (BACKWARD) {
-            if (gi < p.M) scale = *s;
+            if (gi < p.M && HG_DBG_INDEX(gi, e.lds)) scale = *s;
           } else {
             // (columns past N hold 0: zeros in the tile and no bias)
             float top = 0.f;
@@ -611,7 +622,7 @@ __global__ void __launch_bounds__(AnyCfg::THREADS, 1)
                 top = max_abs3(top, v[j] + bias_at(col0 + c + j), v[j + 1] + bias_at(col0 + c + j + 1));
             }
             ckpt_scale(magnitude_bits(top), scale, inv);
-            if (gi < p.M) *s = scale;
+            if (gi < p.M && HG_DBG_INDEX(gi, e.lds)) *s = scale;
           }
         }
         row_scale[lane] = scale;

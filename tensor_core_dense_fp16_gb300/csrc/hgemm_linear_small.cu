@@ -72,6 +72,7 @@ __device__ __forceinline__ RowSide<R> fetch_rows(const SmallArgs& p, int64_t m, 
     s.side[i] = 0u;
     s.scale[i] = 0.f;
   }
+  if (count > 0 && !(HG_DBG_INDEX(f, p.N) && HG_DBG_INDEX(m + (count < R ? count : R) - 1, p.M))) count = 0;
   if (BACKWARD && e.codes) {
     const int8_t* q = e.codes + m * e.ldq + f;
     const float* scale = e.scales + f / kCkptGroup * e.lds + m;
@@ -97,6 +98,7 @@ __device__ __forceinline__ void put_rows(const SmallArgs& p, const float (&sum)[
   const LinEpi& e = p.epi;
   const uint32_t(&side)[R] = s.side;
   const float(&scale)[R] = s.scale;
+  if (count > 0 && !(HG_DBG_INDEX(f, p.N) && HG_DBG_INDEX(m + (count < R ? count : R) - 1, p.M))) count = 0;
   uint16_t* y = p.Y + m * p.ldy + f;
   uint16_t* h = e.h + m * e.ldh + f;
   with_activation(!BACKWARD || e.codes ? e.act : HGEMM_ACT_NONE, [&](auto a) {

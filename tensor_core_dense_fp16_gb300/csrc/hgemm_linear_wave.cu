@@ -87,7 +87,7 @@ __device__ __forceinline__ void sum_rows(const TcArgs& p, uint8_t* smem, uint32_
     if (lane < 8) part[(t >> 5) * kMnBox + chunk * 8 + i] = v[i];
   }
   named_bar_sync(1, 32 * Cfg::EPI_WARPS);
-  if (t < kMnBox && first + t < p.M) {
+  if (t < kMnBox && first + t < p.M && HG_DBG_INDEX(box, 2)) {
     float total = 0.f;
 #pragma unroll
     for (int w = 0; w < Cfg::EPI_WARPS; ++w) total += part[w * kMnBox + t];

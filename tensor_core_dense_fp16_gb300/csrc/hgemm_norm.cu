@@ -100,7 +100,10 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) layernorm_forward_kernel(co
   auto col = [&](int i, int k) { return VEC ? (t + i * G) * 8 + k : (i * 8 + k) * G + t; };
   auto load = [&](const uint16_t* p, int i, float (&f)[8]) {
     if constexpr (VEC) {
-      unpack8(col(i, 0) < D ? *reinterpret_cast<const uint4*>(p + col(i, 0)) : make_uint4(0u, 0u, 0u, 0u), f);
+      unpack8(col(i, 0) < D && dbg_row(p + col(i, 0), col(i, 0), 8, D, 16)
+                  ? *reinterpret_cast<const uint4*>(p + col(i, 0))
+                  : make_uint4(0u, 0u, 0u, 0u),
+              f);
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k) f[k] = col(i, k) < D ? half_at(p, col(i, k)) : 0.f;
@@ -136,14 +139,15 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) layernorm_forward_kernel(co
     for (int k = 0; k < 8; ++k) g[k] = fmaf((x[i][k] - mu) * rs, g[k], b[k]);
     uint16_t* y = a.y + m * a.ldy;
     if constexpr (VEC) {
-      if (col(i, 0) < D) *reinterpret_cast<uint4*>(y + col(i, 0)) = pack8f(g);
+      if (col(i, 0) < D && dbg_row(y + col(i, 0), col(i, 0), 8, D, 16))
+        *reinterpret_cast<uint4*>(y + col(i, 0)) = pack8f(g);
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         if (col(i, k) < D) y[col(i, k)] = __half_as_ushort(__float2half_rn(g[k]));
     }
   }
-  if (t == 0 && a.mean) {
+  if (t == 0 && a.mean && HG_DBG_INDEX(m, a.M)) {
     a.mean[m] = mu;
     a.rstd[m] = rs;
   }
@@ -260,7 +264,7 @@ __global__ void __launch_bounds__(512, 1) layernorm_backward_ring_kernel(const N
   for (int i = 0; i < NV; ++i) {
     const int c = (t + i * G) * 8;
     gamma[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (c < D) gamma[i] = *reinterpret_cast<const uint4*>(a.gamma + c);
+    if (c < D && dbg_row(a.gamma + c, c, 8, D, 16)) gamma[i] = *reinterpret_cast<const uint4*>(a.gamma + c);
 #pragma unroll
     for (int k = 0; k < 4; ++k) dgamma[i][k] = dbeta[i][k] = 0;  // a pair of +0
   }
@@ -355,7 +359,8 @@ __global__ void __launch_bounds__(512, 1) layernorm_backward_ring_kernel(const N
 #pragma unroll
           for (int k = 0; k < 4; ++k) x[k] = add2(x[k], dy[k]);
         }
-        *reinterpret_cast<uint4*>(a.y + m * a.ldy + v * 8) = pack8(x);
+        if (dbg_row(a.y + m * a.ldy + v * 8, v * 8, 8, D, 16))
+          *reinterpret_cast<uint4*>(a.y + m * a.ldy + v * 8) = pack8(x);
       }
     }
     mu = next_mu;
@@ -377,6 +382,7 @@ __global__ void __launch_bounds__(512, 1) layernorm_backward_ring_kernel(const N
     return;
   }
   // The CTA's partial sums: the groups in order.
+  if (!HG_DBG_INDEX(blockIdx.x, kMaxPartials) || !HG_DBG_ALIGN(a.work, 16)) return;
   float* out = a.work + static_cast<int64_t>(blockIdx.x) * 2 * D;
   if constexpr (Cfg::GROUPS > 1) {
     // [group][2][NV·8·G] in the ring
@@ -459,7 +465,7 @@ __global__ void __launch_bounds__(kThreads) layernorm_partials_kernel(const Norm
   s[0][r][c] = dg;
   s[1][r][c] = db;
   __syncthreads();
-  if (r == 0 && d < a.D) {
+  if (r == 0 && d < a.D && HG_DBG_INDEX(blockIdx.y, kMaxPartials)) {
     for (int i = 1; i < 8; ++i) {
       dg += s[0][i][c];
       db += s[1][i][c];

@@ -337,8 +337,9 @@ __device__ __forceinline__ void lin_fetch(LinSide<EPI>& s, const LinEpi& e, int 
       const uint16_t* r = e.res + m * e.ldr + n;
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        s.side[j] = m + 4 * j < M && n < N ? *reinterpret_cast<const uint4*>(r + 4 * j * e.ldr)
-                                           : make_uint4(0u, 0u, 0u, 0u);
+        s.side[j] = m + 4 * j < M && n < N && dbg_row(r + 4 * j * e.ldr, n, 8, N, 16)
+                        ? *reinterpret_cast<const uint4*>(r + 4 * j * e.ldr)
+                        : make_uint4(0u, 0u, 0u, 0u);
     }
   } else if (e.codes) {
     const int64_t m = row0 + (lane >> 2), n = x0 + 16 * (lane & 3);
@@ -350,16 +351,16 @@ __device__ __forceinline__ void lin_fetch(LinSide<EPI>& s, const LinEpi& e, int 
       const int8_t* at = q + 8 * j * e.ldq;
       if (m + 8 * j < M) {
         if (wide) {
-          s.side[j] = *reinterpret_cast<const uint4*>(at);
+          if (dbg_row(at, n, 16, N, 16)) s.side[j] = *reinterpret_cast<const uint4*>(at);
         } else {
           uint2 a = make_uint2(0u, 0u), b = a;
-          if (n < N) a = reinterpret_cast<const uint2*>(at)[0];
-          if (n + 8 < N) b = reinterpret_cast<const uint2*>(at)[1];
+          if (n < N && dbg_row(at, n, 8, N, 8)) a = reinterpret_cast<const uint2*>(at)[0];
+          if (n + 8 < N && dbg_row(at, n + 8, 8, N, 8)) b = reinterpret_cast<const uint2*>(at)[1];
           s.side[j] = make_uint4(a.x, a.y, b.x, b.y);
         }
       }
     }
-    s.scale = grow < M && x0 < N ? e.scales[x0 / kCkptGroup * e.lds + grow] : 0.f;
+    s.scale = grow < M && x0 < N && HG_DBG_INDEX(grow, e.lds) ? e.scales[x0 / kCkptGroup * e.lds + grow] : 0.f;
   }
 }
 
@@ -388,7 +389,8 @@ __device__ __forceinline__ void lin_row64(uint8_t* box, int lane, f32x2 (&v)[32]
       }
       float scale, inv;
       ckpt_scale(magnitude_bits(top), scale, inv);
-      if (grow < M) e.scales[x0 / kCkptGroup * e.lds + grow] = scale;
+      if (grow < M && HG_DBG_INDEX(x0, N) && HG_DBG_INDEX(grow, e.lds))
+        e.scales[x0 / kCkptGroup * e.lds + grow] = scale;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         *box_chunk64(box, lane, j) =
@@ -404,10 +406,10 @@ __device__ __forceinline__ void lin_row64(uint8_t* box, int lane, f32x2 (&v)[32]
         int8_t* at = q + 8 * j * e.ldq;
         if (m + 8 * j < M) {
           if (wide) {
-            *reinterpret_cast<uint4*>(at) = w;
+            if (dbg_row(at, n, 16, N, 16)) *reinterpret_cast<uint4*>(at) = w;
           } else {
-            if (n < N) reinterpret_cast<uint2*>(at)[0] = make_uint2(w.x, w.y);
-            if (n + 8 < N) reinterpret_cast<uint2*>(at)[1] = make_uint2(w.z, w.w);
+            if (n < N && dbg_row(at, n, 8, N, 8)) reinterpret_cast<uint2*>(at)[0] = make_uint2(w.x, w.y);
+            if (n + 8 < N && dbg_row(at, n + 8, 8, N, 8)) reinterpret_cast<uint2*>(at)[1] = make_uint2(w.z, w.w);
           }
         }
       }
@@ -460,7 +462,8 @@ __device__ __forceinline__ void lin_row64(uint8_t* box, int lane, f32x2 (&v)[32]
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const uint4 w = *box_chunk128(box, 4 * j + (lane >> 3), lane & 7);
-        if (m + 4 * j < M && n < N) *reinterpret_cast<uint4*>(h + 4 * j * e.ldh) = w;
+        if (m + 4 * j < M && n < N && dbg_row(h + 4 * j * e.ldh, n, 8, N, 16))
+          *reinterpret_cast<uint4*>(h + 4 * j * e.ldh) = w;
       }
       __syncwarp();
     }

@@ -63,3 +63,25 @@ def test_no_operand_is_read_through_the_non_coherent_path():
         text = code(sources()[name])
         for what in (r"__ldg", r"ld\.global\.nc", r"const\s+\w+\s*\*\s*__restrict__"):
             assert not re.search(what, text), (name, what)
+
+
+# what addresses global memory itself, by file
+ADDRESSING = {
+    "linear_epilogue.cuh": ("lin_fetch", "lin_row64"),
+    "hgemm_linear.cu": ("linear_empty_kernel", "linear_rows_kernel", "column_sums_kernel", "column_sums_thin_kernel"),
+    "hgemm_linear_small.cu": ("fetch_rows", "put_rows"),
+    "hgemm_linear_any.cu": ("any_columns", "any_copy_edge", "linear_any_kernel"),
+    "hgemm_linear_wave.cu": ("sum_rows",),
+    "hgemm_norm.cu": ("layernorm_forward_kernel", "layernorm_backward_ring_kernel", "layernorm_partials_kernel"),
+    "hgemm_ckpt8.cu": ("ckpt8_save_vec_kernel", "ckpt8_save_kernel", "ckpt8_load_vec_kernel", "ckpt8_load_kernel"),
+}
+
+
+def test_the_checking_build_checks_what_addresses_global_memory():
+    """Without a check in it, a kernel passes the checking build whatever its
+    indices are."""
+    files = sources()
+    for name, functions in ADDRESSING.items():
+        for f in functions:
+            body = kernel(code(files[name]), f)
+            assert re.search(r"HG_DBG_(INDEX|ALIGN)\(|dbg_row\(|any_inside\(", body), (name, f)
