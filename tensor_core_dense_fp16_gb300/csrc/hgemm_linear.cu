@@ -3,6 +3,7 @@
 // with the epilogues of linear_epilogue.cuh.
 #include "debug.cuh"
 #include "linear_epilogue.cuh"
+#include "linear_rows.h"
 #include "ptx.cuh"
 
 namespace hg {
@@ -77,20 +78,20 @@ struct RowsArgs {
   LinEpi epi;
 };
 
-constexpr int kRowsFeatures = 16;
 template <int MT, int WARPS, bool VEC>
 __global__ void __launch_bounds__(WARPS * 32) linear_rows_kernel(const RowsArgs p) {
-  constexpr int AHEAD = MT == 1 ? 4 : 2;  // pieces in flight per warp, 64 bytes of each feature
+  constexpr int AHEAD = MT == 1 ? kRowsAhead : 2;  // pieces in flight per warp, 64 bytes of each feature
+  static_assert(WARPS <= kRowsWarps, "the walk along K fits");
   constexpr int PITCH = kRowsFeatures + 1;
   __shared__ float part[WARPS][8 * MT][PITCH];
   // The first weights, four lines per thread, into L2 while the previous launch
   // on the stream ends (only asked for: whatever it still writes there is read
   // after the wait). A token through 2048→8192→2048, two launches: 16.4 us
   // without, 14.4 with.
-  const int lines = (p.K + 63) / 64;
+  const int lines = rows_lines(p.K);
   for (int i = threadIdx.x; i < kRowsFeatures * lines && i < 4 * WARPS * 32; i += WARPS * 32) {
     const int f = static_cast<int>(blockIdx.x) * kRowsFeatures + i / lines;
-    if (f < p.N) prefetch_l2(p.W + f * p.ldw + i % lines * 64);
+    if (f < p.N) prefetch_l2(p.W + f * p.ldw + static_cast<int64_t>(i % lines) * 64);
   }
   grid_dependency_wait();
   grid_launch_dependents();
@@ -100,16 +101,16 @@ __global__ void __launch_bounds__(WARPS * 32) linear_rows_kernel(const RowsArgs 
   // features past N are computed as copies of the last one and not stored
   const uint16_t* w0 = p.W + static_cast<int64_t>(min(n0 + g, p.N - 1)) * p.ldw;
   const uint16_t* w1 = p.W + static_cast<int64_t>(min(n0 + g + 8, p.N - 1)) * p.ldw;
-  auto load = [&](const uint16_t* row, int k, bool weights) {
+  auto load = [&](const uint16_t* row, RowsK k, bool weights) {
     if constexpr (VEC) {
-      if (k >= p.K || !dbg_row(row + k, k, 8, p.K, 16)) return make_uint4(0u, 0u, 0u, 0u);
+      if (!rows_inside(k, p.K) || !dbg_row(row + k, k, 8, p.K, 16)) return make_uint4(0u, 0u, 0u, 0u);
       return weights ? load16_once(row + k) : load16(row + k);  // (L1 keeps X)
     } else {
       uint32_t v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = k + 2 * i < p.K ? row[k + 2 * i] : 0u;
-        const uint32_t hi = k + 2 * i + 1 < p.K ? row[k + 2 * i + 1] : 0u;
+        const uint32_t lo = rows_inside(k + 2 * i, p.K) ? row[k + 2 * i] : 0u;
+        const uint32_t hi = rows_inside(k + 2 * i + 1, p.K) ? row[k + 2 * i + 1] : 0u;
         v[i] = lo | hi << 16;
       }
       return make_uint4(v[0], v[1], v[2], v[3]);
@@ -119,7 +120,7 @@ __global__ void __launch_bounds__(WARPS * 32) linear_rows_kernel(const RowsArgs 
   // AHEAD pieces in turn: as soon as one has been multiplied, its registers
   // take the piece AHEAD further on
   uint4 a0[AHEAD], a1[AHEAD], b[AHEAD][MT];
-  auto fetch = [&](int u, int k) {
+  auto fetch = [&](int u, RowsK k) {
     a0[u] = load(w0, k, true);
     a1[u] = load(w1, k, true);
 #pragma unroll
@@ -128,10 +129,10 @@ __global__ void __launch_bounds__(WARPS * 32) linear_rows_kernel(const RowsArgs 
       b[u][i] = m < p.M ? load(p.X + m * p.ldx, k, false) : make_uint4(0u, 0u, 0u, 0u);
     }
   };
-  int k0 = warp * 32 + 8 * t;
+  RowsK k0 = rows_begin(warp, t);
 #pragma unroll
-  for (int u = 0; u < AHEAD; ++u) fetch(u, k0 + u * WARPS * 32);
-  for (; k0 - 8 * t < p.K; k0 += AHEAD * WARPS * 32) {
+  for (int u = 0; u < AHEAD; ++u) fetch(u, rows_on(k0, u, WARPS));
+  for (; rows_inside(k0 - 8 * t, p.K); k0 = rows_on(k0, AHEAD, WARPS)) {
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) {
 #pragma unroll
@@ -139,7 +140,7 @@ __global__ void __launch_bounds__(WARPS * 32) linear_rows_kernel(const RowsArgs 
         mma_16816(acc[i], a0[u].x, a1[u].x, a0[u].y, a1[u].y, b[u][i].x, b[u][i].y);
         mma_16816(acc[i], a0[u].z, a1[u].z, a0[u].w, a1[u].w, b[u][i].z, b[u][i].w);
       }
-      fetch(u, k0 + (AHEAD + u) * WARPS * 32);
+      fetch(u, rows_on(k0, AHEAD + u, WARPS));
     }
   }
 #pragma unroll
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(WARPS * 32) linear_rows_kernel(const RowsArgs 
 
 template <int MT, int WARPS>
 cudaError_t rows_with(const RowsArgs& p, bool vec, cudaStream_t stream) {
-  PdlLaunch l(dim3(static_cast<unsigned>((p.N + kRowsFeatures - 1) / kRowsFeatures)), dim3(WARPS * 32), 0, stream);
+  PdlLaunch l(dim3(static_cast<unsigned>(rows_blocks(p.N))), dim3(WARPS * 32), 0, stream);
   return cudaLaunchKernelEx(&l.cfg, vec ? linear_rows_kernel<MT, WARPS, true> : linear_rows_kernel<MT, WARPS, false>,
                             p);
 }
@@ -175,8 +176,7 @@ cudaError_t rows_tiles(const RowsArgs& p, bool vec, cudaStream_t stream) {
   // blocks resident at once; four pieces or more per warp. One row, us with 4,
   // 8 and 16 warps (weights not asked of L2 ahead): 8192×2048 8.0, 9.1, 11.0; 4096×4096 10.8, 8.1, 9.2;
   // 2048×8192 18.6, 11.1, 8.3; 1024×1024 3.3, 2.3, 2.4.
-  const int64_t blocks = (p.N + kRowsFeatures - 1) / kRowsFeatures;
-  const int pieces = (p.K + 31) / 32;
+  const int64_t blocks = rows_blocks(p.N), pieces = rows_pieces(p.K);
   if (blocks >= 384 || pieces < 32) return rows_with<MT, 4>(p, vec, stream);
   if (blocks >= 192 || pieces < 64) return rows_with<MT, 8>(p, vec, stream);
   return rows_with<MT, 16>(p, vec, stream);

@@ -27,6 +27,7 @@
 #include "internal.h"
 #include "kernel_common.cuh"
 #include "linear_epilogue.cuh"
+#include "linear_rows.h"
 #include "ptx.cuh"
 
 namespace hg {
@@ -378,7 +379,7 @@ cudaError_t launch_with(const CUtensorMap& w, const CUtensorMap& x, const SmallA
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_done[dev] = true;
   }
-  const unsigned tiles = static_cast<unsigned>((a.N + Cfg::BM - 1) / Cfg::BM * a.row_tiles);
+  const unsigned tiles = static_cast<unsigned>(tiles_of(a.N, Cfg::BM) * a.row_tiles);
   PdlLaunch l(dim3(tiles * static_cast<unsigned>(a.split)), dim3(Cfg::THREADS), Cfg::SMEM_BYTES, stream);
   l.cluster(static_cast<unsigned>(a.split));
   return cudaLaunchKernelEx(&l.cfg, kern, w, x, a);
