@@ -739,31 +739,43 @@ int trmm_pipe(int dev, TrmmPipe** out) {
 namespace hg {
 
 // Whether the turned-around product for few rows or small outputs computes p,
-// and is the faster kernel. Measured (us, this kernel | the next one):
+// and is the faster kernel. Measured (us, this kernel | the next one), weights
+// from memory:
 //   forward, 9 to 32 rows, against the kernel of matrix fragments: 16 rows
-//   4096×4096 9.6 | 11.3, 8192×8192 24.3 | 32.6, but 32 rows 1024×1024 4.7 | 3.8
-//   (so: from 2^21 weights on);
-//   more rows, against the clusters of 128×64 tiles: 128 rows 2048×8192 14.1 |
-//   22.5, 4096×4096 12.9 | 13.6, 9800×264, more than one wave, 7.0 | 11.5, but 64
-//   rows 8192×2048 10.6 | 9.9, 1024×1024 5.9 | 5.0 (so: where K is long, or the
-//   output wide; and where rows of many weights start between lines: 48 rows
-//   3000×1000 6.7 | 13.8, though 1000×1000 6.2 | 5.6);
-//   input gradient, against the same, 64 rows over 8192 features 12.7 | 21.2, 128
-//   rows 15.9 | 21.5, 32 rows over 1024 5.2 | 5.7, but 128 rows over 4096 15.5 |
-//   13.6, 64 rows over 1024 6.8 | 5.1;
-//   weight gradient, against the same: 16384 rows 512×512 16.7 | 32.0, 5000 rows
-//   200×304 10.5 | 16.2, 8192 rows 768×768 (36 tiles) 15.7 | 17.6, but 4096 rows
-//   1024×1024 (64 tiles) 14.3 | 11.1, 2048 rows 512×512 9.2 | 6.5.
+//   2048×2048 5.7 | 4.0, 2048×4096 6.7 | 5.7, 4096×4096 9.0 | 9.8, 8192×2048 8.6 |
+//   11.6 (but 2048×8192 9.8 | 9.0); 32 rows 1024×4096 6.4 | 6.7, 2048×2048 6.1 | 5.1,
+//   4096×2048 6.9 | 7.4, 2048×4096 7.2 | 7.6 (so: from 2^24 weights on, or 2^23 for
+//   more than 16 rows);
+//   more rows, against one wave of 128×64 tiles: 64 rows 1024×2048 6.4 | 7.4,
+//   2048×2048 7.1 | 7.6, 1024×4096 7.2 | 11.8, but 2048×1024 6.0 | 5.5, 8192×2048 10.2 |
+//   9.5; 128 rows 2048×4096 10.9 | 12.4, 4096×4096 12.7 | 12.8, but 2048×2048 9.4 |
+//   7.8; 9800×264, more than one wave, 6.9 | 9.9 (so: where K is long, or the
+//   output wide; and where rows of many weights begin inside lines: 64 rows
+//   6000×1000 8.7 | 10.7, though 4000×1000 7.4 | 7.0);
+//   input gradient, against the same or split K: 32 rows over 1024 features to
+//   1024 4.8 | 5.4; 64 rows over 2048 to 1024 6.7 | 7.9, over 4096 to 4096 10.9 | 12.7,
+//   but over 1024 to 1024 6.4 | 5.5, over 2048 to 8192 12.2 | 10.3; 128 rows over 4096
+//   to 1024 10.5 | 11.4, over 8192 to 2048 15.1 | 19.0, but over 2048 to 1024 9.5 |
+//   8.2, over 8192 to 4096 20.1 | 18.7, to 8192 35.3 | 29.7;
+//   weight gradient with the bias's, against the same: 16384 rows 512×512 17.2 |
+//   25.9, 8192 rows 13.9 | 17.5, 5000 rows 200×304 12.4 | 16.0, but 4096 rows 512×512
+//   13.1 | 11.1, 8192 rows 768×768 (36 tiles) 21.5 | 18.6.
 bool linear_small_suits(const LinearProduct& p, int num_sms) {
   auto rows = [](const void* q, int64_t ld) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0 && ld % 8 == 0; };
   if (p.K == 0 || !rows(p.A, p.lda) || !rows(p.B, p.ldb)) return false;
-  if (p.a_mn) return p.K >= 4096 && (p.M + 127) / 128 * ((p.N + 127) / 128) <= 36;
+  if (p.a_mn) {
+    const int64_t tiles = (p.M + 127) / 128 * ((p.N + 127) / 128);
+    return p.K >= 4096 && p.K >= 256 * tiles + 1024 && tiles <= 36;
+  }
   if (p.M > kLinearSmall) return false;
-  if (p.epi.backward) return p.M <= 32 || p.K > 4096 || (p.M <= 64 && p.K > 2048);
+  if (p.epi.backward)
+    return p.M <= 32 || (p.M <= 64 ? p.K >= 2048 && p.N <= 2 * p.K : p.K > 2048 && 3 * p.N <= p.K);
+  // (neither few-row kernel keeps 8-bit forms: those rows go to the tiles, 16
+  // rows 1024×1024 5.3, 8192×2048 16.5, 32 rows 9.8)
   if (p.epi.codes || p.M <= kLinearFragmentRows) return false;
-  if (p.M <= kLinearRows) return p.N * p.K >= int64_t(1) << 21;
-  if (p.M <= 64 && p.ldb % 32 != 0 && p.N * p.K >= int64_t(1) << 21) return true;
-  return p.K > 2048 || p.N > int64_t(kNarrowBN) * num_sms;
+  if (p.M <= kLinearRows) return p.N * p.K >= int64_t(p.M <= 16 ? 1 << 24 : 1 << 23);
+  if (p.M <= 64 && p.ldb % 64 != 0 && p.N * p.K >= int64_t(1) << 22) return true;
+  return p.K > (p.M <= 64 ? 2047 : 2048) || p.N > int64_t(kNarrowBN) * num_sms;
 }
 
 int run_linear_small(const LinearProduct& p, const DeviceState& dev, cudaStream_t stream) {
@@ -815,8 +827,9 @@ int run_linear_small(const LinearProduct& p, const DeviceState& dev, cudaStream_
 // 12.2, 10.7 | 10.7; 1000×1000 (pitch 1000) of 1000 7.4 | 7.8, 9.0 | 9.4, 8.5 |
 // 7.7, 8.4 | 9.1, of 2504 13.5 | 11.1, 16.4 | 13.3, 17.3 | 12.2, 17.2 | 13.7;
 // 2048×512 of 8192 19.3 | 15.4, 20.2 | 17.2, 19.1 | 16.3. (The kernels of larger
-// outputs take 1000^3 in 7.8, 11.7, 9.7 and 10.8.) Up to 128 rows split K would
-// leave half of its 256-row tiles empty.
+// outputs take 1000^3 in 7.8, 11.7, 9.7 and 10.8.) Up to 128 rows half of split
+// K's 256-row tiles is empty, and wide outputs stay here: 128 rows' input
+// gradient over 8192 to 8192 29.7 | 32.3, but to 4096 22.8 | 18.7.
 bool linear_wave_suits(const LinearProduct& p, bool sums, Gemm* g, const DeviceState& dev) {
   if (p.M == 0 || p.N == 0 || p.K == 0) return false;
   if ((p.M + kTcBM - 1) / kTcBM * ((p.N + kNarrowBN - 1) / kNarrowBN) > dev.num_sms) return false;
@@ -825,7 +838,7 @@ bool linear_wave_suits(const LinearProduct& p, bool sums, Gemm* g, const DeviceS
   };
   // A's pieces are twice as many as B's
   const int64_t per_block = 2 * requests(p.A, p.lda, p.a_mn) + requests(p.B, p.ldb, p.b_mn) + (sums ? 1 : 0);
-  if (p.M <= kTcBM || (p.K + kTcBK - 1) / kTcBK * per_block <= 192) return true;
+  if ((p.M <= kTcBM && p.N > 4096) || (p.K + kTcBK - 1) / kTcBK * per_block <= 192) return true;
   int split = 1, tile_n = kPairBN;
   g->split_k = true;
   if (choose_path(*g, dev.prof, true, &split, &tile_n) == HGEMM_PATH_SKINNY) return false;

@@ -93,3 +93,28 @@ def test_a_chain_of_early_starts():
         assert (back.double() - src.double()).abs().max() <= 1 / 127
         assert (y[:8].double() - want).abs().max() <= 2.0 ** -9 * want.abs().max()
     assert tc.hgemm_device_status() == tc.HGEMM_OK
+
+
+@pytest.mark.parametrize("what", ["forward", "backward", "weight"])
+def test_few_rows_and_small_weights_time_out(what):
+    """The waits of the turned-around product are bounded in all its forms."""
+    torch = torch_cuda()
+    half = lambda *s: torch.ones(s, dtype=torch.float16, device="cuda")  # noqa: E731
+    call = {"forward": lambda: tc.hgemm_linear(half(64, 4096), 4096, half(512, 4096), 4096, None, 2, None, 0,
+                                               half(64, 512), 512, 64, 512, 4096),
+            "backward": lambda: tc.hgemm_linear_dgrad(half(64, 4096), 4096, half(4096, 512), 512, None, 0, None, 0, 0,
+                                                      half(64, 512), 512, None, 0, 64, 4096, 512),
+            "weight": lambda: tc.hgemm_linear_wgrad(half(8192, 128), 128, half(8192, 136), 136, half(128, 136), 136, None,
+                                                    False, 8192, 128, 136)}[what]
+    torch.cuda.synchronize()
+    assert tc.hgemm_device_status() == tc.HGEMM_OK
+    tc.hgemm_set_wait_timeout(20_000_000)
+    tc.hgemm_debug_inject(tc.HGEMM_INJECT_DROP_ARRIVAL)
+    try:
+        call()
+        assert tc.hgemm_device_status() == tc.HGEMM_ERR_TIMEOUT
+    finally:
+        tc.hgemm_debug_inject(tc.HGEMM_INJECT_NONE)
+        tc.hgemm_set_wait_timeout(0)
+    call()
+    assert tc.hgemm_device_status() == tc.HGEMM_OK
