@@ -596,7 +596,6 @@ int run_tc_wide(const Gemm& g, const hg::EpiArgs& epi, const DeviceState& dev,
   args.epi = epi;
   args.C = static_cast<const uint16_t*>(g.c_src ? g.c_src : C);  // C_old, for a fused epilogue
   args.ldc = g.c_src ? g.ld_src : g.ldc;
-  if (g.lin) args.lin = *g.lin;
   args.a_mn = g.a_mn ? 1 : 0;
   args.b_mn = g.b_mn ? 1 : 0;
   cudaError_t e = hg::launch_tc_wide(ma, mb, mc, args, stream);

@@ -3,9 +3,10 @@
 //
 // Both are bound by memory: 2 bytes read and 1.06 written per value, or the
 // other way round (16384×8192: saved in 73 us, 5.7 TB/s, loaded in 60, 6.8 TB/s, and
-// with GELU in 63; a copy moves 6.8 TB/s). A warp takes 8 rows of a few groups at once, so that it
-// has eight independent loads in flight per lane and so that the scales of 8
-// rows, neighbours in memory, form one 32-byte sector per group.
+// with GELU in 63; a copy moves 6.8 TB/s; 16384×8191, one or two bytes at a time,
+// 175 and 109). A warp takes 8 rows of a few groups at once, so that it has
+// eight independent loads in flight per lane and so that the scales of 8 rows,
+// neighbours in memory, form one 32-byte sector per group.
 #include "debug.cuh"
 #include "linear_epilogue.cuh"
 #include "ptx.cuh"

@@ -174,8 +174,8 @@ template <int MT>
 cudaError_t rows_tiles(const RowsArgs& p, bool vec, cudaStream_t stream) {
   // About 2048 warps in all, 13 per SM: enough loads under way, and all
   // blocks resident at once; four pieces or more per warp. One row, us with 4,
-  // 8 and 16 warps (weights not asked of L2 ahead): 8192×2048 8.0, 9.1, 11.0; 4096×4096 10.8, 8.1, 9.2;
-  // 2048×8192 18.6, 11.1, 8.3; 1024×1024 3.3, 2.3, 2.4.
+  // 8 and 16 warps: 8192×2048 7.3, 7.7, 11.3; 4096×4096 9.5, 6.6, 8.5; 2048×8192
+  // 14.9, 9.9, 7.4; 1024×1024 2.4, 2.1, 2.3.
   const int64_t blocks = rows_blocks(p.N), pieces = rows_pieces(p.K);
   if (blocks >= 384 || pieces < 32) return rows_with<MT, 4>(p, vec, stream);
   if (blocks >= 192 || pieces < 64) return rows_with<MT, 8>(p, vec, stream);
@@ -187,9 +187,9 @@ cudaError_t rows_tiles(const RowsArgs& p, bool vec, cudaStream_t stream) {
 // neighbouring columns each, the others down the rows, kUnroll rows in
 // flight per thread. The threads of a column are added in order through
 // shared memory, and the CTAs in rank order through distributed shared memory
-// by rank 0. Bound by reading dY once (8192×8192 25.9 us, 5.2 TB/s); a strip is
-// as wide as leaves enough CTAs, because the longer a row's piece the better
-// memory delivers it.
+// by rank 0. Bound by reading dY once (8192×8192 26.0 us, 5.2 TB/s; 8192×1001,
+// two bytes at a time, 16.1); a strip is as wide as leaves enough CTAs, because
+// the longer a row's piece the better memory delivers it.
 //
 // beside: the launch before this one on the stream is the product with the
 // same dY, and the two may run at the same time, the sums on SMs that the

@@ -15,10 +15,10 @@
 // is the same in every K block (a block is 128 bytes on, or 64 pitches), so a
 // lane keeps its pointers and its shifts for a whole output tile. Bound by
 // the loaders' instructions: a K block takes them 1.3 us (8192×2049 outputs of
-// a contraction of 2047, GELU and residual: 371 us; 1001^3 46 us, 20 of them
-// the epilogue of the one wave of tiles). Where only the outputs are odd, one
-// thread loads the tiles by TMA instead and four of the loader warps join the
-// epilogue (2000×2001, contraction 2000: 38 us, by the loader warps 102).
+// a contraction of 2047, GELU and residual: 371 us, where 8192×2048 of 2048 takes
+// the aligned kernels 49; 1001^3 41). Where only the outputs are odd, one thread
+// loads the tiles by TMA instead and four of the loader warps join the epilogue
+// (2000×2001, contraction 2000: 38 us, by the loader warps 102).
 // Nothing past a matrix's last element is read, and before its first one at
 // most the rest of the same aligned 16 bytes; what a tile has outside the
 // matrix is zeros.

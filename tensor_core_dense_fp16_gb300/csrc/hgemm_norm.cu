@@ -2,9 +2,9 @@
 // are in hgemm.h). Both are bound by memory: forward reads and writes 2
 // bytes per value, backward reads 4 (6 with the residual branch) and writes 2.
 // 16384 rows of 8192: forward 85 us, 6.3 TB/s, backward with the residual
-// branch 172 us, 6.25 TB/s, 93 and 92% of a copy's rate; of 4096 42 and 83; of
-// 1024 (32768 rows) 23 and 48, 85%. Rows that 16-byte accesses cannot describe
-// (16384 of 5001: 216 and 452 us) move two bytes at a time and are bound by the
+// branch 174 us, 6.2 TB/s, 93 and 91% of a copy's rate; of 4096 43 and 83; of
+// 1024 (32768 rows) 23 and 47, 85%. Rows that 16-byte accesses cannot describe
+// (16384 of 5001: 216 and 455 us) move two bytes at a time and are bound by the
 // number of those accesses.
 #include <atomic>
 

@@ -54,9 +54,10 @@ struct LinEpi {
   int64_t ldh;
 };
 
-// The operands' order in memory, a template parameter of the pair and split-K
-// kernels: a branch on it between the copies and between the matrix
-// instructions takes them out of uniform registers (see elect_one).
+// The operands' order in memory, a template parameter of the pair, wide and
+// split-K kernels: a branch on it between the copies and between the matrix
+// instructions costs time in both (the wave kernel's copies 0.155 us a block
+// with it, 0.115 without).
 enum Layout {
   kLayoutK,    // both K-contiguous
   kLayoutBn,   // A K-contiguous, B N-contiguous: a linear layer's input gradient
@@ -286,7 +287,6 @@ struct SmallArgs {
 cudaError_t launch_linear_small(const CUtensorMap& w, const CUtensorMap& x, const SmallArgs& a, cudaStream_t stream);
 // How many clusters of `split` CTAs the device holds at once.
 int linear_small_clusters(int split, int num_sms);
-cudaError_t launch_linear_small(const CUtensorMap& w, const CUtensorMap& x, const SmallArgs& a, cudaStream_t stream);
 // The kernel for operands and outputs of any pitch and alignment; K > 0.
 // ma, mb: tensor maps of the operands (boxes of 128 rows, MN-major 64 by 64),
 // or null where there can be none.

@@ -56,9 +56,7 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t byt
 constexpr uint32_t kSuspendHintNs = 1000000;
 
 // True in one lane of the converged warp, always the same one. The warps that
-// issue copies and MMAs branch on this and not on a lane number: the compiler
-// then knows that one thread runs the branch and hands the instructions their
-// operands from uniform registers without a loop over the lanes (128×64 tiles,
+// issue copies and MMAs branch on this and not on a lane number (128×64 tiles,
 // a block of 64 of the contraction: 400 cycles for copies and MMAs issued by
 // lane 0, 220 this way, which is what the copies take).
 __device__ __forceinline__ bool elect_one() {
