@@ -517,6 +517,172 @@ HGEMM_API int hgemm_ckpt8_load(const int8_t *codes, int64_t ldq, const float *sc
                      hgemm_half_t *Y, int64_t ldy, int64_t M, int64_t N, cudaStream_t stream);
 
 /*
+ * The norms around a block, with its gate and the residual's scale. The
+ * residual stream X and a block's output Y, both M×D, give the next residual
+ * stream and, normalised, the next block's input:
+ *
+ *     Z = alpha·X + gate ⊙ N_post(Y)        H = N_pre(Z)
+ *
+ * over rows of D values, N(v) = (v − μ)·ρ·gamma + beta, with
+ *   HGEMM_NORM_LAYER  μ the row's mean, ρ = 1/√(variance + eps)
+ *   HGEMM_NORM_RMS    μ = 0, ρ = 1/√(mean(v²) + eps)
+ *   HGEMM_NORM_NONE   no norm: N_post(Y) = Y, and no H
+ * gate, gamma and beta hold D FP16 values each; gate NULL is 1, beta NULL is 0.
+ */
+#define HGEMM_NORM_NONE 0
+#define HGEMM_NORM_LAYER 1
+#define HGEMM_NORM_RMS 2
+
+/*
+ * hgemm_residual_norm_forward — Z and H. H is the norm of the FP32 Z, before
+ * its rounding. post, pre: HGEMM_NORM_* behind the block and in front of the
+ * next; with HGEMM_NORM_NONE its gamma and beta are NULL, and H is NULL with
+ * pre NONE. stats: 4·M FP32 values, or NULL: stats[m] and stats[M + m] receive
+ * μ and ρ of Y's row m, stats[2·M + m] and stats[3·M + m] those of Z's; a
+ * NONE norm's are left as they are. eps ≥ 0, alpha finite. Z may be X and H
+ * may be Y (same pitch). Same return values as hgemm_linear.
+ */
+HGEMM_API int hgemm_residual_norm_forward(const hgemm_half_t *X, int64_t ldx, float alpha, const hgemm_half_t *Y,
+                                int64_t ldy, const hgemm_half_t *gate, int post, const hgemm_half_t *post_gamma,
+                                const hgemm_half_t *post_beta, int pre, const hgemm_half_t *pre_gamma,
+                                const hgemm_half_t *pre_beta, float eps, hgemm_half_t *Z, int64_t ldz,
+                                hgemm_half_t *H, int64_t ldh, float *stats, int64_t M, int64_t D,
+                                cudaStream_t stream);
+
+/*
+ * hgemm_residual_norm_backward — from dZ, the gradient that reaches Z along the
+ * residual stream (NULL: 0), and dH, that of H (NULL with pre NONE). With
+ * v̂ = (v − μ)·ρ by stats, as forward left them, and
+ * P(g, v̂) = g − mean(g) − v̂·mean(g·v̂) over a row (RMS: without mean(g)):
+ *
+ *     dz = dZ + ρ_z·P(dH·pre_gamma, ẑ)
+ *     dX = alpha·dz
+ *     dY = ρ_y·P(gate·dz·post_gamma, ŷ)           (post NONE: gate·dz)
+ *     dgate       = Σ_m dz ⊙ N_post(Y)
+ *     dpost_gamma = Σ_m gate·dz ⊙ ŷ,  dpost_beta = Σ_m gate·dz
+ *     dpre_gamma  = Σ_m dH ⊙ ẑ,       dpre_beta  = Σ_m dH
+ *
+ * The five sums are D FP32 values each, or NULL where they are not wanted; one
+ * of a vector that forward does not have must be NULL (dpost_beta and dpre_beta
+ * need the norm, not the beta). dX may be dZ and dY may be dH (same pitch).
+ * workspace: caller-owned, 16-byte aligned, at least
+ * hgemm_residual_norm_backward_workspace_size(M, D) bytes, not used by other
+ * work until the stream has passed this call. The order of every sum is fixed.
+ * M = 0: the sums are 0. Same return values.
+ */
+HGEMM_API size_t hgemm_residual_norm_backward_workspace_size(int64_t M, int64_t D);
+HGEMM_API int hgemm_residual_norm_backward(const hgemm_half_t *dZ, int64_t lddz, const hgemm_half_t *dH, int64_t lddh,
+                                 const hgemm_half_t *Z, int64_t ldz, const hgemm_half_t *Y, int64_t ldy, float alpha,
+                                 const hgemm_half_t *gate, int post, const hgemm_half_t *post_gamma,
+                                 const hgemm_half_t *post_beta, int pre, const hgemm_half_t *pre_gamma,
+                                 const float *stats, hgemm_half_t *dX, int64_t lddx, hgemm_half_t *dY, int64_t lddy,
+                                 float *dgate, float *dpost_gamma, float *dpost_beta, float *dpre_gamma,
+                                 float *dpre_beta, void *workspace, size_t workspace_bytes, int64_t M, int64_t D,
+                                 cudaStream_t stream);
+
+/*
+ * hgemm_adamw — one AdamW step over many tensors. For each value p with
+ * gradient g and states m, v (FP32 operations, β1, β2 and 1 − β rounded to
+ * FP32; products and sums of the states are rounded one by one):
+ *
+ *     g ← g·grad_scale
+ *     m ← β1·m + (1 − β1)·g          v ← β2·v + (1 − β2)·g²
+ *     p ← p·(1 − lr·weight_decay) − lr·(m/(1 − β1^step)) / (√(v/(1 − β2^step)) + eps)
+ *
+ * A tensor has n values:
+ *   weight     FP16, or NULL: with master, written as master rounded, not read
+ *   master     FP32, or NULL: then weight is read and rounded back
+ *   grad       HGEMM_TYPE_F16 or HGEMM_TYPE_F32, by grad_type
+ *   m, v       the states. m_scales and v_scales NULL: FP32. Otherwise a byte
+ *              a value, and ⌈n/64⌉ FP32 scales each: every 64 consecutive
+ *              values share them.
+ *     m: the 8-bit form above (signed whole numbers, s = max|m|/127).
+ *     v: s = max v, and r = v·(1/s) is kept in a float of 5 exponent and 3
+ *        fraction bits: code c > 0 stands for 2^e·(1 + f/8)·s with 8·e + f =
+ *        c − 255, rounded to nearest (halves up), so that 255 is s itself; r
+ *        below the least, 1.25·2^-32, is kept as that (c = 1), 0 as 0. A
+ *        value's error is at most r/16.
+ *     A group whose largest magnitude is below 2^-100 has s = 0 and codes 0,
+ *     one that holds an infinity or a NaN s = NaN and codes 0. The step itself
+ *     uses m and v before they are kept.
+ *   weight_decay
+ * A state of zeros is all zero bytes in either form. `tensors` is read during
+ * the call only; `count` is any number, and n = 0 is nothing to do. Each
+ * tensor's arrays must not overlap one another (HGEMM_ERR_ALIAS); those of
+ * different tensors must not either, which hgemm_adamw_check looks for and a
+ * step does not. lr, eps and grad_scale are finite, 0 ≤ β < 1, step ≥ 1, eps ≥ 0.
+ * dynamic, in device memory, or NULL: its lr, grad_scale and step are taken in
+ * place of the arguments' when the work runs (a step ≤ 0 counts as 1), and with
+ * skip ≠ 0 nothing is written: what changes from step to step under one
+ * captured graph. 4-byte aligned (codes and FP16: as their type). Same return
+ * values as hgemm_linear.
+ */
+#define HGEMM_TYPE_F16 0
+#define HGEMM_TYPE_F32 1
+typedef struct {
+  hgemm_half_t *weight;
+  float *master;
+  const void *grad;
+  void *m, *v;
+  float *m_scales, *v_scales;
+  int64_t n;
+  float weight_decay;
+  int32_t grad_type;
+} hgemm_adamw_tensor;
+typedef struct {
+  float lr, grad_scale;
+  int32_t step, skip;
+} hgemm_adamw_dynamic;
+HGEMM_API int hgemm_adamw(const hgemm_adamw_tensor *tensors, int64_t count, double lr, double beta1, double beta2,
+                double eps, int64_t step, double grad_scale, const hgemm_adamw_dynamic *dynamic,
+                cudaStream_t stream);
+/* hgemm_adamw_check — hgemm_adamw's argument checks, and that no tensor's
+ * arrays overlap another's outputs (gradients may be shared). Host logic. */
+HGEMM_API int hgemm_adamw_check(const hgemm_adamw_tensor *tensors, int64_t count);
+/*
+ * hgemm_adamw_load — 8-bit states read back: m_out and v_out receive n FP32
+ * values (either may be NULL with its codes and scales). Tensors that lie one
+ * behind the other in whole groups of 64 are read by one call. Same return
+ * values.
+ */
+HGEMM_API int hgemm_adamw_load(const int8_t *m, const float *m_scales, const uint8_t *v, const float *v_scales,
+                     float *m_out, float *v_out, int64_t n, cudaStream_t stream);
+
+/*
+ * hgemm_experts — a mixture-of-experts feed-forward layer for few tokens. X is
+ * M×D, M ≤ HGEMM_EXPERTS_MAX_TOKENS. For each row x:
+ *
+ *     l = Wr·x                     E FP32 logits, Wr E×D
+ *     the k largest l_e            ties to the lowest e; a NaN is below every number
+ *     s_e                          normalize: softmax over the k; else over all E
+ *     h_e = f(W1_e·x + b1_e)       gated 0: W1_e F×D;
+ *         = f(g) ⊙ u               gated 1: W1_e 2F×D, (g, u) = W1_e·x + b1_e, g the first F
+ *     Y = Σ s_e·(W2_e·h_e + b2_e) + R        W2_e D×F
+ *
+ * W1 holds the experts one behind the other, E·F (or 2·E·F) rows of pitch
+ * ldw1, W2 E·D rows of pitch ldw2; b1 E×F (2F), b2 E×D, without gaps, or NULL.
+ * R is M×D or NULL; R = Y (same pitch) adds in place. h is rounded to FP16.
+ * chosen (M×k, the experts from the largest logit down) and share (M×k, s)
+ * receive the router's choice, or are NULL.
+ * 1 ≤ k ≤ min(E, HGEMM_EXPERTS_MAX_CHOICES), E ≤ HGEMM_EXPERTS_MAX, D and F ≤
+ * HGEMM_EXPERTS_MAX_WIDTH.
+ * F = 0: h is empty. workspace: caller-owned, 16-byte aligned, at least
+ * hgemm_experts_workspace_size(M, D, F, E, k) bytes (0 for sizes that a call
+ * refuses), not used by other work until the stream has passed this call. The
+ * order of every sum is fixed. Same return values as hgemm_linear.
+ */
+#define HGEMM_EXPERTS_MAX_TOKENS 64
+#define HGEMM_EXPERTS_MAX_CHOICES 16
+#define HGEMM_EXPERTS_MAX 512
+#define HGEMM_EXPERTS_MAX_WIDTH (1 << 20)
+HGEMM_API size_t hgemm_experts_workspace_size(int64_t M, int64_t D, int64_t F, int64_t E, int64_t k);
+HGEMM_API int hgemm_experts(const hgemm_half_t *X, int64_t ldx, const hgemm_half_t *Wr, int64_t ldwr,
+                  const hgemm_half_t *W1, int64_t ldw1, const hgemm_half_t *b1, const hgemm_half_t *W2, int64_t ldw2,
+                  const hgemm_half_t *b2, int act, int gated, int64_t k, int normalize, const hgemm_half_t *R,
+                  int64_t ldr, hgemm_half_t *Y, int64_t ldy, int32_t *chosen, float *share, void *workspace,
+                  size_t workspace_bytes, int64_t M, int64_t D, int64_t F, int64_t E, cudaStream_t stream);
+
+/*
  * hgemm_host — the same product for operands held in HOST memory.
  *
  * Copies hA -> dA (M*K values) and hB -> dB (N*K values), computes

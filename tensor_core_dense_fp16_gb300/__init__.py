@@ -38,6 +38,11 @@ __all__ = [
     "hgemm_layernorm_backward", "hgemm_layernorm_backward_workspace_size", "hgemm_ckpt8_save", "hgemm_ckpt8_load",
     "HGEMM_ACT_NONE", "HGEMM_ACT_RELU", "HGEMM_ACT_GELU", "HGEMM_ACT_SILU", "HGEMM_ACT_GELU_ERF",
     "HGEMM_CKPT8_GROUP",
+    "hgemm_residual_norm_forward", "hgemm_residual_norm_backward", "hgemm_residual_norm_backward_workspace_size",
+    "HGEMM_NORM_NONE", "HGEMM_NORM_LAYER", "HGEMM_NORM_RMS",
+    "hgemm_adamw", "hgemm_adamw_check", "hgemm_adamw_tensors", "hgemm_adamw_dynamic", "hgemm_adamw_load", "AdamwTensors", "HGEMM_TYPE_F16",
+    "HGEMM_TYPE_F32", "hgemm_experts", "hgemm_experts_workspace_size", "HGEMM_EXPERTS_MAX_TOKENS",
+    "HGEMM_EXPERTS_MAX_CHOICES", "HGEMM_EXPERTS_MAX", "HGEMM_EXPERTS_MAX_WIDTH",
 ]
 
 HGEMM_OK = 0
@@ -68,6 +73,18 @@ HGEMM_ACT_GELU = 2
 HGEMM_ACT_SILU = 3
 HGEMM_ACT_GELU_ERF = 4
 HGEMM_CKPT8_GROUP = 64
+
+HGEMM_NORM_NONE = 0
+HGEMM_NORM_LAYER = 1
+HGEMM_NORM_RMS = 2
+
+HGEMM_TYPE_F16 = 0
+HGEMM_TYPE_F32 = 1
+
+HGEMM_EXPERTS_MAX_TOKENS = 64
+HGEMM_EXPERTS_MAX_CHOICES = 16
+HGEMM_EXPERTS_MAX = 512
+HGEMM_EXPERTS_MAX_WIDTH = 1 << 20
 
 HGEMM_PATH_NONE = 0
 HGEMM_PATH_ZERO = 1
@@ -179,6 +196,23 @@ def load():
         getattr(lib, name).restype = i32
     lib.hgemm_layernorm_backward_workspace_size.argtypes = [i64, i64]
     lib.hgemm_layernorm_backward_workspace_size.restype = ctypes.c_size_t
+    f64, size = ctypes.c_double, ctypes.c_size_t
+    lib.hgemm_residual_norm_forward.argtypes = [vp, i64, f32, vp, i64, vp, i32, vp, vp, i32, vp, vp, f32, vp, i64, vp,
+                                                i64, vp, i64, i64, vp]
+    lib.hgemm_residual_norm_backward.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, f32, vp, i32, vp, vp, i32, vp, vp,
+                                                 vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, size, i64, i64, vp]
+    lib.hgemm_adamw.argtypes = [vp, i64, f64, f64, f64, f64, i64, f64, vp, vp]
+    lib.hgemm_adamw_check.argtypes = [vp, i64]
+    lib.hgemm_adamw_load.argtypes = [vp, vp, vp, vp, vp, vp, i64, vp]
+    lib.hgemm_experts.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, i64, vp, i32, i32, i64, i32, vp, i64, vp, i64, vp,
+                                  vp, vp, size, i64, i64, i64, i64, vp]
+    for name in ("hgemm_residual_norm_forward", "hgemm_residual_norm_backward", "hgemm_adamw", "hgemm_adamw_check",
+                 "hgemm_adamw_load", "hgemm_experts"):
+        getattr(lib, name).restype = i32
+    lib.hgemm_residual_norm_backward_workspace_size.argtypes = [i64, i64]
+    lib.hgemm_residual_norm_backward_workspace_size.restype = size
+    lib.hgemm_experts_workspace_size.argtypes = [i64, i64, i64, i64, i64]
+    lib.hgemm_experts_workspace_size.restype = size
     for name in ("hgemm_debug_build", "hgemm_debug_code", "hgemm_debug_selftest", "hgemm_trsm_last_schedule"):
         getattr(lib, name).argtypes = []
         getattr(lib, name).restype = i32
@@ -456,7 +490,7 @@ def matmul(a, b_cols, out=None, stream=None):
 
 # ------------------------------------------- the feed-forward block's operators
 
-_F16, _F32, _I8 = "torch.float16", "torch.float32", "torch.int8"
+_F16, _F32, _I8, _U8 = "torch.float16", "torch.float32", "torch.int8", "torch.uint8"
 _dtypes: dict = {}  # torch's dtype objects and their names
 
 
@@ -541,3 +575,166 @@ def hgemm_ckpt8_load(codes, ldq: int, scales, lds: int, act: int, Y, ldy: int, M
     _raise_on((_lib or load()).hgemm_ckpt8_load(
         _dev(codes, _I8, "codes"), ldq, _dev(scales, _F32, "scales"), lds, act, _dev(Y, _F16, "Y"), ldy, M, N,
         _stream(stream)), "hgemm_ckpt8_load")
+
+
+def _workspace(workspace, workspace_bytes):
+    if workspace is not None and type(workspace) is not int and not getattr(workspace, "is_cuda", False):
+        raise ValueError("workspace must be a CUDA tensor")
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size() if hasattr(workspace, "numel") else 0
+    return _ptr(workspace), workspace_bytes
+
+
+def hgemm_residual_norm_forward(X, ldx, alpha: float, Y, ldy, gate, post: int, post_gamma, post_beta, pre: int,
+                                pre_gamma, pre_beta, eps: float, Z, ldz, H, ldh, stats, M: int, D: int,
+                                stream=None) -> None:
+    """Z = alpha·X + gate ⊙ N_post(Y) and H = N_pre(Z); the norms are HGEMM_NORM_* (see hgemm.h)."""
+    _raise_on((_lib or load()).hgemm_residual_norm_forward(
+        _dev(X, _F16, "X"), ldx, alpha, _dev(Y, _F16, "Y"), ldy, _dev(gate, _F16, "gate"), post,
+        _dev(post_gamma, _F16, "post_gamma"), _dev(post_beta, _F16, "post_beta"), pre,
+        _dev(pre_gamma, _F16, "pre_gamma"), _dev(pre_beta, _F16, "pre_beta"), eps, _dev(Z, _F16, "Z"), ldz,
+        _dev(H, _F16, "H"), ldh, _dev(stats, _F32, "stats"), M, D, _stream(stream)), "hgemm_residual_norm_forward")
+
+
+def hgemm_residual_norm_backward_workspace_size(M: int, D: int) -> int:
+    """Bytes of device workspace hgemm_residual_norm_backward needs."""
+    return int(load().hgemm_residual_norm_backward_workspace_size(M, D))
+
+
+def hgemm_residual_norm_backward(dZ, lddz, dH, lddh, Z, ldz, Y, ldy, alpha: float, gate, post: int, post_gamma,
+                                 post_beta, pre: int, pre_gamma, stats, dX, lddx, dY, lddy, dgate, dpost_gamma,
+                                 dpost_beta, dpre_gamma, dpre_beta, workspace, M: int, D: int,
+                                 workspace_bytes: int | None = None, stream=None) -> None:
+    """dX, dY and the vectors' gradients of hgemm_residual_norm_forward (see
+    hgemm.h); the workspace's size defaults to the tensor's bytes."""
+    ws, nbytes = _workspace(workspace, workspace_bytes)
+    _raise_on((_lib or load()).hgemm_residual_norm_backward(
+        _dev(dZ, _F16, "dZ"), lddz, _dev(dH, _F16, "dH"), lddh, _dev(Z, _F16, "Z"), ldz, _dev(Y, _F16, "Y"), ldy,
+        alpha, _dev(gate, _F16, "gate"), post, _dev(post_gamma, _F16, "post_gamma"),
+        _dev(post_beta, _F16, "post_beta"), pre, _dev(pre_gamma, _F16, "pre_gamma"), _dev(stats, _F32, "stats"),
+        _dev(dX, _F16, "dX"), lddx, _dev(dY, _F16, "dY"), lddy, _dev(dgate, _F32, "dgate"),
+        _dev(dpost_gamma, _F32, "dpost_gamma"), _dev(dpost_beta, _F32, "dpost_beta"),
+        _dev(dpre_gamma, _F32, "dpre_gamma"), _dev(dpre_beta, _F32, "dpre_beta"), ws, nbytes, M, D, _stream(stream)),
+        "hgemm_residual_norm_backward")
+
+
+# ---------------------------------------------------------------- the optimizer
+
+class _AdamwTensor(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("master", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("m", ctypes.c_void_p), ("v", ctypes.c_void_p), ("m_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("n", ctypes.c_int64), ("weight_decay", ctypes.c_float),
+                ("grad_type", ctypes.c_int32)]
+
+
+class AdamwTensors:
+    """The table of tensors that hgemm_adamw steps: their addresses, and the
+    tensors themselves so that they stay alive."""
+
+    def __init__(self, table, keep):
+        self.table, self.keep = table, keep
+
+
+_ADAMW_FIELDS = {"weight", "master", "grad", "m", "v", "m_scales", "v_scales", "weight_decay"}
+
+
+def hgemm_adamw_tensors(tensors) -> AdamwTensors:
+    """The table for hgemm_adamw from dicts of CUDA tensors: ``grad`` (float16
+    or float32), ``weight`` (float16) and ``master`` (float32) or either, the
+    states ``m`` and ``v`` (float32; or int8 and uint8 with ``m_scales`` and
+    ``v_scales``, float32, one per 64 values), and ``weight_decay`` (0 where not
+    given). Made once for a program's tensors; all contiguous, of equal size, on
+    one device, and none may share memory with another's outputs."""
+    tensors = list(tensors)
+    rows, device = [], None
+    for i, t in enumerate(tensors):
+        get = t.get
+        grad, ms, vs = get("grad"), get("m_scales"), get("v_scales")
+        if not t.keys() <= _ADAMW_FIELDS:
+            raise TypeError(f"tensor {i}: unknown {sorted(set(t) - _ADAMW_FIELDS)}")
+        for name in ("grad", "m", "v"):
+            if get(name) is None:
+                raise ValueError(f"tensor {i}: {name} is missing")
+        eight = ms is not None or vs is not None
+        n = grad.numel()
+        half_grad = (_dtypes.get(grad.dtype) or str(grad.dtype)) == _F16
+        row = []
+        for name, dtype, size in (("weight", _F16, n), ("master", _F32, n), ("grad", _F16 if half_grad else _F32, n),
+                                  ("m", _I8 if eight else _F32, n), ("v", _U8 if eight else _F32, n),
+                                  ("m_scales", _F32, -(-n // HGEMM_CKPT8_GROUP)),
+                                  ("v_scales", _F32, -(-n // HGEMM_CKPT8_GROUP))):
+            x = get(name)
+            if x is None:
+                row.append(None)
+                continue
+            row.append(_dev(x, dtype, name))
+            if x.numel() != size:
+                raise ValueError(f"tensor {i}: {name} must have {size} values, got {x.numel()}")
+            if not x.is_contiguous():
+                raise ValueError(f"tensor {i}: {name} must be contiguous")
+            at = x.get_device()
+            if at != device:
+                if device is not None:
+                    raise ValueError(f"tensor {i}: {name} must be on cuda:{device}, got cuda:{at}")
+                device = at
+        rows.append((*row, n, get("weight_decay", 0.0), HGEMM_TYPE_F16 if half_grad else HGEMM_TYPE_F32))
+    plan = AdamwTensors((_AdamwTensor * len(rows))(*rows), tensors)
+    hgemm_adamw_check(plan)
+    return plan
+
+
+def hgemm_adamw_check(tensors: AdamwTensors) -> None:
+    """Raises where hgemm_adamw would refuse a tensor, and where one's arrays
+    overlap another's outputs (hgemm_adamw_tensors has called it)."""
+    _raise_on((_lib or load()).hgemm_adamw_check(tensors.table, len(tensors.table)), "hgemm_adamw_check")
+
+
+def hgemm_adamw_dynamic(lr: float, grad_scale: float, step: int, skip: bool = False):
+    """The 16 bytes of an hgemm_adamw_dynamic as a host tensor of bytes, to be
+    copied to the device tensor that a captured step reads."""
+    import struct
+    import torch
+    return torch.frombuffer(bytearray(struct.pack("=ffii", lr, grad_scale, step, 1 if skip else 0)), dtype=torch.uint8)
+
+
+def hgemm_adamw(tensors: AdamwTensors, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+                step: int = 1, grad_scale: float = 1.0, dynamic=None, stream=None) -> None:
+    """One AdamW step over the tensors of hgemm_adamw_tensors (see hgemm.h).
+    dynamic: 16 device bytes (hgemm_adamw_dynamic's) that are read when the step
+    runs, or None."""
+    if dynamic is not None and type(dynamic) is not int:
+        if not getattr(dynamic, "is_cuda", False):
+            raise ValueError("dynamic must be a CUDA tensor")
+        if dynamic.numel() * dynamic.element_size() < 16 or not dynamic.is_contiguous():
+            raise ValueError("dynamic must have 16 bytes, contiguous")
+    _raise_on((_lib or load()).hgemm_adamw(tensors.table, len(tensors.table), lr, beta1, beta2, eps, step, grad_scale,
+                                           _ptr(dynamic), _stream(stream)), "hgemm_adamw")
+
+
+def hgemm_adamw_load(m, m_scales, v, v_scales, m_out, v_out, n: int, stream=None) -> None:
+    """8-bit states read back as float32 (see hgemm.h)."""
+    _raise_on((_lib or load()).hgemm_adamw_load(
+        _dev(m, _I8, "m"), _dev(m_scales, _F32, "m_scales"), _dev(v, _U8, "v"),
+        _dev(v_scales, _F32, "v_scales"), _dev(m_out, _F32, "m_out"), _dev(v_out, _F32, "v_out"), n, _stream(stream)),
+        "hgemm_adamw_load")
+
+
+# ------------------------------------------------------------ mixture of experts
+
+def hgemm_experts_workspace_size(M: int, D: int, F: int, E: int, k: int) -> int:
+    """Bytes of device workspace hgemm_experts needs."""
+    return int(load().hgemm_experts_workspace_size(M, D, F, E, k))
+
+
+def hgemm_experts(X, ldx, Wr, ldwr, W1, ldw1, b1, W2, ldw2, b2, act: int, gated: bool, k: int, normalize: bool, R, ldr,
+                  Y, ldy, chosen, share, workspace, M: int, D: int, F: int, E: int,
+                  workspace_bytes: int | None = None, stream=None) -> None:
+    """Y = Σ s·(W2·f(W1·x + b1) + b2) + R over the k experts of E that the
+    router Wr chooses for each of M tokens (see hgemm.h); the workspace's size
+    defaults to the tensor's bytes."""
+    ws, nbytes = _workspace(workspace, workspace_bytes)
+    _raise_on((_lib or load()).hgemm_experts(
+        _dev(X, _F16, "X"), ldx, _dev(Wr, _F16, "Wr"), ldwr, _dev(W1, _F16, "W1"), ldw1, _dev(b1, _F16, "b1"),
+        _dev(W2, _F16, "W2"), ldw2, _dev(b2, _F16, "b2"), act, 1 if gated else 0, k, 1 if normalize else 0,
+        _dev(R, _F16, "R"), ldr, _dev(Y, _F16, "Y"), ldy, _dev(chosen, "torch.int32", "chosen"),
+        _dev(share, _F32, "share"), ws, nbytes, M, D, F, E, _stream(stream)), "hgemm_experts")

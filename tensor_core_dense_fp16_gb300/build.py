@@ -29,8 +29,10 @@ DEBUG_DIR = os.path.join(OUT_DIR, "debug")
 DEBUG_LIB = os.path.join(DEBUG_DIR, "libhgemm.so")
 SOURCES = ["hgemm_api.cu", "hgemm_tc.cu", "hgemm_tc2.cu", "hgemm_tc2w.cu", "hgemm_skinny.cu", "hgemm_generic.cu", "hgemm_trsm.cu",
            "hgemm_trileaf.cu", "hgemm_trsm_chain.cu", "hgemm_block_api.cu", "hgemm_linear.cu", "hgemm_norm.cu",
-           "hgemm_ckpt8.cu", "hgemm_linear_any.cu", "hgemm_linear_small.cu", "hgemm_linear_wave.cu"]
-HEADERS = ["ptx.cuh", "internal.h", "kernel_common.cuh", "debug.cuh", "trsm_chain.h", "linear_epilogue.cuh", "linear_rows.h"]
+           "hgemm_ckpt8.cu", "hgemm_linear_any.cu", "hgemm_linear_small.cu", "hgemm_linear_wave.cu",
+           "hgemm_residual_norm.cu", "hgemm_adamw.cu", "hgemm_experts.cu"]
+HEADERS = ["ptx.cuh", "internal.h", "kernel_common.cuh", "debug.cuh", "trsm_chain.h", "linear_epilogue.cuh", "linear_rows.h",
+           "row_sums.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",

@@ -75,7 +75,9 @@ cudaError_t debug_words(int* (&out)[hg::kDebugWords]) {
                                                       hg::debug_word_trileaf, hg::debug_word_chain,
                                                       hg::debug_word_linear,  hg::debug_word_norm,
                                                       hg::debug_word_ckpt8,   hg::debug_word_linear_any,
-                                                      hg::debug_word_linear_small, hg::debug_word_linear_wave};
+                                                      hg::debug_word_linear_small, hg::debug_word_linear_wave,
+                                                      hg::debug_word_residual_norm, hg::debug_word_adamw,
+                                                      hg::debug_word_experts};
   for (int i = 0; i < hg::kDebugWords; ++i) {
     const cudaError_t e = get[i](&out[i]);
     if (e != cudaSuccess) return e;

@@ -1,7 +1,9 @@
 // hgemm_block_api.cu — the C ABI of the feed-forward block's operators
 // declared in include/hgemm.h: argument checks and dispatch.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <new>
 
 #include "hgemm.h"
 #include "internal.h"
@@ -217,6 +219,300 @@ int hgemm_ckpt8_load(const int8_t* codes, int64_t ldq, const float* scales, int6
   const int rc = hg::call_device(&dev);
   if (rc != HGEMM_OK) return rc;
   return hg::cuda_status(hg::launch_ckpt8_load(codes, ldq, scales, lds, act, Y, ldy, M, N, stream));
+}
+
+namespace {
+
+bool norm_kind_ok(int kind, const void* gamma, const void* beta) {
+  if (kind == HGEMM_NORM_NONE) return !gamma && !beta;
+  return kind == HGEMM_NORM_LAYER || kind == HGEMM_NORM_RMS;
+}
+
+Span vec_or_none(const void* p, int64_t n, int size) { return p ? vec(p, n, size) : kNone; }
+
+}  // namespace
+
+int hgemm_residual_norm_forward(const hgemm_half_t* X, int64_t ldx, float alpha, const hgemm_half_t* Y, int64_t ldy,
+                                const hgemm_half_t* gate, int post, const hgemm_half_t* post_gamma,
+                                const hgemm_half_t* post_beta, int pre, const hgemm_half_t* pre_gamma,
+                                const hgemm_half_t* pre_beta, float eps, hgemm_half_t* Z, int64_t ldz,
+                                hgemm_half_t* H, int64_t ldh, float* stats, int64_t M, int64_t D,
+                                cudaStream_t stream) {
+  if (!dims_ok(M, D) || !(eps >= 0.f) || std::isinf(eps) || !std::isfinite(alpha)) return HGEMM_ERR_INVALID_ARG;
+  if (!norm_kind_ok(post, post_gamma, post_beta) || !norm_kind_ok(pre, pre_gamma, pre_beta) ||
+      (pre == HGEMM_NORM_NONE && H))
+    return HGEMM_ERR_INVALID_ARG;
+  const Span x = half_matrix(X, M, D, ldx), y = half_matrix(Y, M, D, ldy), z = half_matrix(Z, M, D, ldz);
+  const Span h = pre ? half_matrix(H, M, D, ldh) : kNone;
+  const Span g = vec_or_none(gate, D, 2), pg = post ? vec(post_gamma, D, 2) : kNone, pb = vec_or_none(post_beta, D, 2);
+  const Span qg = pre ? vec(pre_gamma, D, 2) : kNone, qb = vec_or_none(pre_beta, D, 2);
+  const Span st = stats ? Span{stats, 4, M, M, 4} : kNone;
+  for (const Span& v : {x, y, z, h, g, pg, pb, qg, qb, st})
+    if (!span_ok(v)) return HGEMM_ERR_INVALID_ARG;
+  for (const Span& o : {z, h, st})
+    for (const Span& v : {g, pg, pb, qg, qb})
+      if (overlap(o, v)) return HGEMM_ERR_ALIAS;
+  if ((overlap(z, x) && !same(z, x)) || overlap(z, y) || (overlap(h, y) && !same(h, y)) || overlap(h, x))
+    return HGEMM_ERR_ALIAS;
+  if (overlap(st, x) || overlap(st, y) || overlap(z, h) || overlap(z, st) || overlap(h, st)) return HGEMM_ERR_ALIAS;
+  if (M == 0 || D == 0) return HGEMM_OK;
+  hg::CallDevice dev;
+  const int rc = hg::call_device(&dev);
+  if (rc != HGEMM_OK) return rc;
+  const hg::ResidualNormArgs a{X,   ldx,       alpha,    Y,   ldy, gate, post, post_gamma, post_beta, pre,
+                               pre_gamma, pre_beta, eps, Z,   ldz, H,    ldh,  stats,      M,         D};
+  return hg::cuda_status(hg::launch_residual_norm_forward(a, dev.num_sms, stream));
+}
+
+size_t hgemm_residual_norm_backward_workspace_size(int64_t M, int64_t D) {
+  if (!dims_ok(M, D) || D == 0) return 0;
+  return hg::residual_norm_backward_workspace(M, D);
+}
+
+int hgemm_residual_norm_backward(const hgemm_half_t* dZ, int64_t lddz, const hgemm_half_t* dH, int64_t lddh,
+                                 const hgemm_half_t* Z, int64_t ldz, const hgemm_half_t* Y, int64_t ldy, float alpha,
+                                 const hgemm_half_t* gate, int post, const hgemm_half_t* post_gamma,
+                                 const hgemm_half_t* post_beta, int pre, const hgemm_half_t* pre_gamma,
+                                 const float* stats, hgemm_half_t* dX, int64_t lddx, hgemm_half_t* dY, int64_t lddy,
+                                 float* dgate, float* dpost_gamma, float* dpost_beta, float* dpre_gamma,
+                                 float* dpre_beta, void* workspace, size_t workspace_bytes, int64_t M, int64_t D,
+                                 cudaStream_t stream) {
+  if (!dims_ok(M, D) || !std::isfinite(alpha)) return HGEMM_ERR_INVALID_ARG;
+  if (!norm_kind_ok(post, post_gamma, post_beta) || !norm_kind_ok(pre, pre_gamma, nullptr))
+    return HGEMM_ERR_INVALID_ARG;
+  if ((!pre && (dH || dpre_gamma || dpre_beta)) || (!post && (dpost_gamma || dpost_beta)) || (!gate && dgate))
+    return HGEMM_ERR_INVALID_ARG;
+  const Span dz = dZ ? half_matrix(dZ, M, D, lddz) : kNone, dh = pre ? half_matrix(dH, M, D, lddh) : kNone;
+  const Span z = half_matrix(Z, M, D, ldz), y = half_matrix(Y, M, D, ldy);
+  const Span dx = half_matrix(dX, M, D, lddx), dy = half_matrix(dY, M, D, lddy);
+  const Span g = vec_or_none(gate, D, 2), pg = post ? vec(post_gamma, D, 2) : kNone, pb = vec_or_none(post_beta, D, 2);
+  const Span qg = pre ? vec(pre_gamma, D, 2) : kNone;
+  const Span st = pre || post ? Span{stats, 4, M, M, 4} : kNone;
+  const Span sums[5] = {vec_or_none(dgate, D, 4), vec_or_none(dpost_gamma, D, 4), vec_or_none(dpost_beta, D, 4),
+                        vec_or_none(dpre_gamma, D, 4), vec_or_none(dpre_beta, D, 4)};
+  for (const Span& v : {dz, dh, z, y, dx, dy, g, pg, pb, qg, st})
+    if (!span_ok(v)) return HGEMM_ERR_INVALID_ARG;
+  for (const Span& v : sums)
+    if (!span_ok(v)) return HGEMM_ERR_INVALID_ARG;
+  const size_t need = hgemm_residual_norm_backward_workspace_size(M, D);
+  if (D > 0 && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15u)))
+    return HGEMM_ERR_INVALID_ARG;
+  const Span ws = vec(workspace, static_cast<int64_t>(need), 1);
+  for (const Span& o : {dx, dy, ws, sums[0], sums[1], sums[2], sums[3], sums[4]})
+    for (const Span& v : {z, y, g, pg, pb, qg, st})
+      if (overlap(o, v)) return HGEMM_ERR_ALIAS;
+  if ((overlap(dx, dz) && !same(dx, dz)) || overlap(dx, dh) || (overlap(dy, dh) && !same(dy, dh)) || overlap(dy, dz))
+    return HGEMM_ERR_ALIAS;
+  if (overlap(dx, dy) || overlap(dx, ws) || overlap(dy, ws) || overlap(dz, ws) || overlap(dh, ws))
+    return HGEMM_ERR_ALIAS;
+  for (int i = 0; i < 5; ++i) {
+    for (const Span& v : {dz, dh, dx, dy, ws})
+      if (overlap(sums[i], v)) return HGEMM_ERR_ALIAS;
+    for (int j = 0; j < i; ++j)
+      if (overlap(sums[i], sums[j])) return HGEMM_ERR_ALIAS;
+  }
+  if (D == 0) return HGEMM_OK;
+  hg::CallDevice dev;
+  const int rc = hg::call_device(&dev);
+  if (rc != HGEMM_OK) return rc;
+  hg::ResidualNormBackArgs a{};
+  a.dz = dZ, a.lddz = lddz, a.dh = dH, a.lddh = lddh, a.z = Z, a.ldz = ldz, a.y = Y, a.ldy = ldy, a.alpha = alpha;
+  a.gate = gate, a.post = post, a.post_gamma = post_gamma, a.post_beta = post_beta, a.pre = pre;
+  a.pre_gamma = pre_gamma, a.stats = stats, a.dx = dX, a.lddx = lddx, a.dy = dY, a.lddy = lddy;
+  a.dgate = dgate, a.dpost_gamma = dpost_gamma, a.dpost_beta = dpost_beta;
+  a.dpre_gamma = dpre_gamma, a.dpre_beta = dpre_beta;
+  a.partials = static_cast<float*>(workspace), a.M = M, a.D = D;
+  a.status = dev.status, a.timeout_ns = dev.timeout_ns, a.inject = dev.inject;
+  return hg::cuda_status(hg::launch_residual_norm_backward(a, dev.num_sms, stream));
+}
+
+namespace {
+
+// The arrays of one tensor, outputs first: weight, master, m, v, their scales,
+// then the gradient.
+constexpr int kAdamwOutputs = 6;
+int adamw_spans(const hgemm_adamw_tensor& t, Span (&s)[kAdamwOutputs + 1]) {
+  if (t.n < 0 || t.n > HGEMM_MAX_DIM || (t.grad_type != HGEMM_TYPE_F16 && t.grad_type != HGEMM_TYPE_F32) ||
+      !std::isfinite(t.weight_decay) || !t.m_scales != !t.v_scales)
+    return HGEMM_ERR_INVALID_ARG;
+  if (t.n > 0 && !t.weight && !t.master) return HGEMM_ERR_INVALID_ARG;
+  const int state = t.m_scales ? 1 : 4;
+  s[0] = vec_or_none(t.weight, t.n, 2);
+  s[1] = vec_or_none(t.master, t.n, 4);
+  s[2] = vec(t.m, t.n, state);
+  s[3] = vec(t.v, t.n, state);
+  s[4] = vec_or_none(t.m_scales, groups_of(t.n), 4);
+  s[5] = vec_or_none(t.v_scales, groups_of(t.n), 4);
+  s[6] = vec(t.grad, t.n, t.grad_type == HGEMM_TYPE_F32 ? 4 : 2);
+  for (const Span& v : s)
+    if (!span_ok(v)) return HGEMM_ERR_INVALID_ARG;
+  for (int i = 0; i < kAdamwOutputs; ++i)
+    for (int j = i + 1; j <= kAdamwOutputs; ++j)
+      if (overlap(s[i], s[j])) return HGEMM_ERR_ALIAS;
+  return HGEMM_OK;
+}
+
+struct Range {
+  uintptr_t begin, end;
+  bool output;
+};
+
+}  // namespace
+
+int hgemm_adamw_check(const hgemm_adamw_tensor* tensors, int64_t count) {
+  if (count < 0 || (count > 0 && !tensors)) return HGEMM_ERR_INVALID_ARG;
+  if (count > HGEMM_MAX_DIM) return HGEMM_ERR_INVALID_ARG;
+  Range* all = new (std::nothrow) Range[static_cast<size_t>(count) * (kAdamwOutputs + 1) + 1];
+  if (!all) return HGEMM_ERR_INVALID_ARG;
+  size_t n = 0;
+  int rc = HGEMM_OK;
+  for (int64_t i = 0; i < count && rc == HGEMM_OK; ++i) {
+    Span s[kAdamwOutputs + 1];
+    rc = adamw_spans(tensors[i], s);
+    for (int j = 0; j <= kAdamwOutputs && rc == HGEMM_OK; ++j)
+      if (s[j].p && !s[j].empty()) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(s[j].p);
+        all[n++] = Range{at, at + static_cast<uintptr_t>(s[j].bytes()), j < kAdamwOutputs};
+      }
+  }
+  if (rc == HGEMM_OK) {
+    std::sort(all, all + n, [](const Range& a, const Range& b) { return a.begin < b.begin; });
+    // the furthest ends so far, of any array and of outputs
+    uintptr_t any = 0, outputs = 0;
+    for (size_t i = 0; i < n && rc == HGEMM_OK; ++i) {
+      if (all[i].begin < (all[i].output ? any : outputs)) rc = HGEMM_ERR_ALIAS;
+      any = std::max(any, all[i].end);
+      if (all[i].output) outputs = std::max(outputs, all[i].end);
+    }
+  }
+  delete[] all;
+  return rc;
+}
+
+int hgemm_adamw(const hgemm_adamw_tensor* tensors, int64_t count, double lr, double beta1, double beta2, double eps,
+                int64_t step, double grad_scale, const hgemm_adamw_dynamic* dynamic, cudaStream_t stream) {
+  if (count < 0 || count > HGEMM_MAX_DIM || (count > 0 && !tensors)) return HGEMM_ERR_INVALID_ARG;
+  if (!std::isfinite(lr) || !(beta1 >= 0 && beta1 < 1) || !(beta2 >= 0 && beta2 < 1) || !(eps >= 0) ||
+      std::isinf(eps) || step < 1 || !std::isfinite(grad_scale) || (reinterpret_cast<uintptr_t>(dynamic) & 3u))
+    return HGEMM_ERR_INVALID_ARG;
+  bool any = false;
+  for (int64_t i = 0; i < count; ++i) {
+    Span s[kAdamwOutputs + 1];
+    const int rc = adamw_spans(tensors[i], s);
+    if (rc != HGEMM_OK) return rc;
+    if (dynamic)
+      for (const Span& v : s)
+        if (overlap(v, Span{dynamic, 1, 1, 1, static_cast<int>(sizeof(*dynamic))})) return HGEMM_ERR_ALIAS;
+    any = any || tensors[i].n > 0;
+  }
+  if (!any) return HGEMM_OK;
+  hg::CallDevice dev;
+  int rc = hg::call_device(&dev);
+  if (rc != HGEMM_OK) return rc;
+  const double t = static_cast<double>(step);
+  hg::AdamwStep s{};
+  s.beta1 = static_cast<float>(beta1), s.rest1 = static_cast<float>(1.0 - beta1);
+  s.beta2 = static_cast<float>(beta2), s.rest2 = static_cast<float>(1.0 - beta2);
+  s.eps = static_cast<float>(eps), s.gscale = static_cast<float>(grad_scale), s.lr = static_cast<float>(lr);
+  s.a = static_cast<float>(lr / (1.0 - std::pow(beta1, t)));
+  s.b = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(beta2, t)));
+  s.ln1 = static_cast<float>(std::log(beta1)), s.ln2 = static_cast<float>(std::log(beta2));
+  s.dynamic = dynamic;
+  auto aligned = [](const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; };
+  hg::AdamwEntry e[hg::kAdamwTensors];
+  int n = 0;
+  uint32_t chunks = 0;
+  for (int64_t i = 0; i <= count; ++i) {
+    if (n == hg::kAdamwTensors || (i == count && n > 0)) {
+      if ((rc = hg::cuda_status(hg::launch_adamw(e, n, chunks, s, dev.num_sms, stream))) != HGEMM_OK) return rc;
+      n = 0;
+      chunks = 0;
+    }
+    if (i == count || tensors[i].n == 0) continue;
+    const hgemm_adamw_tensor& x = tensors[i];
+    const uintptr_t state = x.m_scales ? 8 : 16;
+    const bool vec8 = x.n % 8 == 0 && aligned(x.weight, 16) && aligned(x.master, 16) && aligned(x.grad, 16) &&
+                      aligned(x.m, state) && aligned(x.v, state);
+    e[n++] = hg::AdamwEntry{x.weight, x.master, x.grad, x.m, x.v, x.m_scales, x.v_scales, x.n, x.weight_decay,
+                            static_cast<float>(1.0 - lr * x.weight_decay), chunks,
+                            static_cast<int16_t>(x.grad_type), static_cast<int16_t>(vec8)};
+    chunks += static_cast<uint32_t>((x.n + hg::kAdamwChunk - 1) / hg::kAdamwChunk);
+  }
+  return HGEMM_OK;
+}
+
+int hgemm_adamw_load(const int8_t* m, const float* m_scales, const uint8_t* v, const float* v_scales, float* m_out,
+                     float* v_out, int64_t n, cudaStream_t stream) {
+  if (n < 0 || n > kPitchLimit) return HGEMM_ERR_INVALID_ARG;
+  if (!m != !m_scales || !m != !m_out || !v != !v_scales || !v != !v_out || (n > 0 && !m && !v))
+    return HGEMM_ERR_INVALID_ARG;
+  const Span in[4] = {vec_or_none(m, n, 1), vec_or_none(m_scales, groups_of(n), 4), vec_or_none(v, n, 1),
+                      vec_or_none(v_scales, groups_of(n), 4)};
+  const Span mo = vec_or_none(m_out, n, 4), vo = vec_or_none(v_out, n, 4);
+  for (const Span& x : {in[0], in[1], in[2], in[3], mo, vo})
+    if (!span_ok(x)) return HGEMM_ERR_INVALID_ARG;
+  for (const Span& x : in)
+    if (overlap(mo, x) || overlap(vo, x)) return HGEMM_ERR_ALIAS;
+  if (overlap(mo, vo)) return HGEMM_ERR_ALIAS;
+  if (n == 0) return HGEMM_OK;
+  hg::CallDevice dev;
+  const int rc = hg::call_device(&dev);
+  if (rc != HGEMM_OK) return rc;
+  return hg::cuda_status(hg::launch_adamw_load(m, m_scales, v, v_scales, m_out, v_out, n, dev.num_sms, stream));
+}
+
+namespace {
+
+bool experts_sizes_ok(int64_t M, int64_t D, int64_t F, int64_t E, int64_t k) {
+  return M >= 0 && M <= HGEMM_EXPERTS_MAX_TOKENS && D >= 0 && D <= HGEMM_EXPERTS_MAX_WIDTH && F >= 0 &&
+         F <= HGEMM_EXPERTS_MAX_WIDTH && E >= 1 && E <= HGEMM_EXPERTS_MAX && k >= 1 && k <= E &&
+         k <= HGEMM_EXPERTS_MAX_CHOICES;
+}
+
+}  // namespace
+
+size_t hgemm_experts_workspace_size(int64_t M, int64_t D, int64_t F, int64_t E, int64_t k) {
+  if (!experts_sizes_ok(M, D, F, E, k)) return 0;
+  return hg::experts_workspace(M, D, F, k);
+}
+
+int hgemm_experts(const hgemm_half_t* X, int64_t ldx, const hgemm_half_t* Wr, int64_t ldwr, const hgemm_half_t* W1,
+                  int64_t ldw1, const hgemm_half_t* b1, const hgemm_half_t* W2, int64_t ldw2, const hgemm_half_t* b2,
+                  int act, int gated, int64_t k, int normalize, const hgemm_half_t* R, int64_t ldr, hgemm_half_t* Y,
+                  int64_t ldy, int32_t* chosen, float* share, void* workspace, size_t workspace_bytes, int64_t M,
+                  int64_t D, int64_t F, int64_t E, cudaStream_t stream) {
+  if (!experts_sizes_ok(M, D, F, E, k) || act < HGEMM_ACT_NONE || act > HGEMM_ACT_GELU_ERF || (gated & ~1) ||
+      (normalize & ~1))
+    return HGEMM_ERR_INVALID_ARG;
+  const int64_t up = gated ? 2 * F : F;
+  const Span x = half_matrix(X, M, D, ldx), wr = half_matrix(Wr, E, D, ldwr), y = half_matrix(Y, M, D, ldy);
+  const Span w1 = half_matrix(W1, E * up, D, ldw1), w2 = half_matrix(W2, E * D, F, ldw2);
+  const Span v1 = vec_or_none(b1, E * up, 2), v2 = vec_or_none(b2, E * D, 2);
+  const Span r = R ? half_matrix(R, M, D, ldr) : kNone;
+  const Span c = vec_or_none(chosen, M * k, 4), s = vec_or_none(share, M * k, 4);
+  for (const Span& v : {x, wr, w1, w2, v1, v2, r, y, c, s})
+    if (!span_ok(v)) return HGEMM_ERR_INVALID_ARG;
+  const size_t need = hg::experts_workspace(M, D, F, k);
+  if (M > 0 && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15u)))
+    return HGEMM_ERR_INVALID_ARG;
+  const Span ws = vec(workspace, static_cast<int64_t>(need), 1);
+  for (const Span& o : {y, c, s, ws})
+    for (const Span& v : {x, wr, w1, w2, v1, v2})
+      if (overlap(o, v)) return HGEMM_ERR_ALIAS;
+  if ((overlap(y, r) && !same(y, r)) || overlap(c, r) || overlap(s, r) || overlap(ws, r)) return HGEMM_ERR_ALIAS;
+  if (overlap(y, c) || overlap(y, s) || overlap(y, ws) || overlap(c, s) || overlap(c, ws) || overlap(s, ws))
+    return HGEMM_ERR_ALIAS;
+  if (M == 0) return HGEMM_OK;
+  hg::CallDevice dev;
+  const int rc = hg::call_device(&dev);
+  if (rc != HGEMM_OK) return rc;
+  hg::ExpertsArgs a{};
+  a.X = X, a.ldx = ldx, a.Wr = Wr, a.ldwr = ldwr, a.W1 = W1, a.ldw1 = ldw1, a.b1 = b1, a.W2 = W2, a.ldw2 = ldw2;
+  a.b2 = b2, a.act = act, a.gated = gated != 0, a.normalize = normalize != 0, a.R = R, a.ldr = ldr, a.Y = Y;
+  a.ldy = ldy, a.chosen = chosen, a.share = share;
+  a.M = static_cast<int>(M), a.D = static_cast<int>(D), a.F = static_cast<int>(F), a.E = static_cast<int>(E);
+  a.k = static_cast<int>(k);
+  return hg::cuda_status(hg::launch_experts(a, workspace, dev.num_sms, stream));
 }
 
 }  // extern "C"

@@ -7,6 +7,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "hgemm.h"
+
 namespace hg {
 
 // Watchdog codes written to the device status word by a wait that gave up.
@@ -328,6 +330,118 @@ cudaError_t launch_ckpt8_save(const uint16_t* x, int64_t ldx, int8_t* codes, int
 cudaError_t launch_ckpt8_load(const int8_t* codes, int64_t ldq, const float* scales, int64_t lds, int act,
                               uint16_t* y, int64_t ldy, int64_t M, int64_t N, cudaStream_t stream);
 
+// The norms around a block; kinds are HGEMM_NORM_*, absent vectors null.
+struct ResidualNormArgs {
+  const uint16_t* x;
+  int64_t ldx;
+  float alpha;
+  const uint16_t* y;
+  int64_t ldy;
+  const uint16_t* gate;
+  int post;
+  const uint16_t *post_gamma, *post_beta;
+  int pre;
+  const uint16_t *pre_gamma, *pre_beta;
+  float eps;
+  uint16_t* z;
+  int64_t ldz;
+  uint16_t* h;
+  int64_t ldh;
+  float* stats;  // [4][M], or null
+  int64_t M, D;
+};
+cudaError_t launch_residual_norm_forward(const ResidualNormArgs& a, int num_sms, cudaStream_t stream);
+
+// At most this many partial sums of the vectors' gradients.
+constexpr int kResidualNormPartials = 160;
+struct ResidualNormBackArgs {
+  const uint16_t* dz;  // or null
+  int64_t lddz;
+  const uint16_t* dh;
+  int64_t lddh;
+  const uint16_t* z;
+  int64_t ldz;
+  const uint16_t* y;
+  int64_t ldy;
+  float alpha;
+  const uint16_t* gate;
+  int post;
+  const uint16_t *post_gamma, *post_beta;
+  int pre;
+  const uint16_t* pre_gamma;
+  const float* stats;
+  uint16_t* dx;
+  int64_t lddx;
+  uint16_t* dy;
+  int64_t lddy;
+  float *dgate, *dpost_gamma, *dpost_beta, *dpre_gamma, *dpre_beta;  // each or null
+  float* partials;  // the workspace: [partial][4][D], or fewer partials and
+  float* means;     // four means for each of the rows m0 .. m1-1
+  int64_t M, D, m0, m1;
+  int* status;  // device watchdog word
+  unsigned long long timeout_ns;
+  int inject;   // HGEMM_INJECT_* (testing the watchdog)
+};
+cudaError_t launch_residual_norm_backward(ResidualNormBackArgs a, int num_sms, cudaStream_t stream);
+size_t residual_norm_backward_workspace(int64_t M, int64_t D);
+
+// One tensor of an AdamW step (hgemm_adamw_tensor), and where its chunks of
+// kAdamwChunk values begin in the launch's numbering.
+constexpr int kAdamwChunk = 2048;
+constexpr int kAdamwTensors = 384;  // of one launch, its parameters at most 32764 bytes
+struct AdamwEntry {
+  uint16_t* weight;
+  float* master;
+  const void* grad;
+  void *m, *v;
+  float *ms, *vs;
+  int64_t n;
+  float decay, keep;  // weight_decay and 1 − lr·weight_decay
+  uint32_t chunk0;
+  int16_t grad_type;
+  int16_t vec;        // n and the pointers let eight values be moved at once
+};
+struct AdamwStep {
+  float beta1, rest1, beta2, rest2, eps;  // rest: 1 − β
+  float gscale, lr, a, b;                 // a = lr/(1 − β1^step), b = 1/√(1 − β2^step)
+  float ln1, ln2;                         // ln β, for a step number that the device holds
+  const hgemm_adamw_dynamic* dynamic;     // or null
+};
+cudaError_t launch_adamw(const AdamwEntry* t, int count, uint32_t chunks, const AdamwStep& step, int num_sms,
+                         cudaStream_t stream);
+cudaError_t launch_adamw_load(const int8_t* m, const float* ms, const uint8_t* v, const float* vs, float* m_out,
+                              float* v_out, int64_t n, int num_sms, cudaStream_t stream);
+
+struct ExpertsArgs {
+  const uint16_t* X;
+  int64_t ldx;
+  const uint16_t* Wr;
+  int64_t ldwr;
+  const uint16_t* W1;
+  int64_t ldw1;
+  const uint16_t* b1;
+  const uint16_t* W2;
+  int64_t ldw2;
+  const uint16_t* b2;
+  int act;
+  bool gated, normalize;
+  const uint16_t* R;
+  int64_t ldr;
+  uint16_t* Y;
+  int64_t ldy;
+  int* chosen;   // M×k, or null
+  float* share;
+  int M, D, F, E, k;
+  // the workspace's parts
+  int* ws_chosen;
+  float* ws_share;
+  uint16_t* ws_h;  // M·k rows
+  int64_t ldh;
+  float* ws_out;   // M·k rows
+  int64_t ldo;
+};
+cudaError_t launch_experts(ExpertsArgs a, void* workspace, int num_sms, cudaStream_t stream);
+size_t experts_workspace(int64_t M, int64_t D, int64_t F, int64_t k);
 
 // Address of the device watchdog word on the current device.
 cudaError_t status_word_address(int** addr);
@@ -348,7 +462,10 @@ cudaError_t debug_word_ckpt8(int** out);
 cudaError_t debug_word_linear_any(int** out);
 cudaError_t debug_word_linear_small(int** out);
 cudaError_t debug_word_linear_wave(int** out);
-constexpr int kDebugWords = 14;
+cudaError_t debug_word_residual_norm(int** out);
+cudaError_t debug_word_adamw(int** out);
+cudaError_t debug_word_experts(int** out);
+constexpr int kDebugWords = 17;
 
 // Co-residency limits of the cluster kernels on one device, measured once
 // (or nominal GB300 figures when no device has been queried).
