@@ -553,7 +553,8 @@ HGEMM_API int hgemm_residual_norm_forward(const hgemm_half_t *X, int64_t ldx, fl
  * hgemm_residual_norm_backward — from dZ, the gradient that reaches Z along the
  * residual stream (NULL: 0), and dH, that of H (NULL with pre NONE). With
  * v̂ = (v − μ)·ρ by stats, as forward left them, and
- * P(g, v̂) = g − mean(g) − v̂·mean(g·v̂) over a row (RMS: without mean(g)):
+ * P(g, v̂) = g − mean(g) − v̂·mean(g·v̂) over a row (RMS: μ = 0, whatever stats
+ * holds, and P without mean(g)):
  *
  *     dz = dZ + ρ_z·P(dH·pre_gamma, ẑ)
  *     dX = alpha·dz

@@ -2,6 +2,8 @@
 // residual's scale, forward and backward (the formulas are in hgemm.h). Both
 // are bound by memory: forward reads 4 bytes per value and writes 4, backward
 // reads 8 and writes 4.
+#include <atomic>
+
 #include <cuda_fp16.h>
 
 #include "debug.cuh"
@@ -20,9 +22,177 @@ __device__ __forceinline__ float half_or(const uint16_t* p, int64_t i, float oth
   return p ? half_at(p, i) : otherwise;
 }
 
+// ------------------------------------------------------------------ forward
+
+// What a warp knows of its row's values: their number, their sum and their
+// squares' sum around their mean (or, RMS, around 0).
+struct Part {
+  float n, sum, sq;
+};
+
+// μ and ρ of a row from the moments of the G threads that hold it, V values
+// each, `in` telling which of them are in the row. A layer norm's squares are
+// summed around each warp's own mean, and the warps' joined by the distances
+// of their means: Σ(v − μ)² = Σ_w [Σ(v − μ_w)² + n_w·(μ_w − μ)²], which keeps
+// its digits in a row far from zero and takes one exchange between the warps
+// where a second pass around the row's mean takes two.
+template <int G, int V, typename In>
+__device__ __forceinline__ void row_moments(bool layer, int D, float eps, Part* parts, const float (&v)[V], In in,
+                                            float& mu, float& rho) {
+  const int lane = threadIdx.x & 31;
+  Part p{0.f, 0.f, 0.f};
+  float center = 0.f;
+  if (layer) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (in(i)) {
+        p.sum += v[i];
+        ++n;
+      }
+    p.sum = warp_sum(p.sum);
+    p.n = static_cast<float>(__reduce_add_sync(0xffffffffu, n));
+    center = p.n > 0.f ? p.sum / p.n : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (in(i)) {
+      const float c = v[i] - center;
+      p.sq = fmaf(c, c, p.sq);
+    }
+  p.sq = warp_sum(p.sq);
+  const float inv = 1.f / static_cast<float>(D);
+  if constexpr (G > 32) {
+    if (lane == 0) parts[threadIdx.x >> 5] = p;
+    __syncthreads();
+    float sum = 0.f, sq = 0.f;
+    if (layer) {
+#pragma unroll
+      for (int w = 0; w < G / 32; ++w) sum += parts[w].sum;
+      mu = sum * inv;
+#pragma unroll
+      for (int w = 0; w < G / 32; ++w) {
+        const Part q = parts[w];
+        const float off = q.n > 0.f ? q.sum / q.n - mu : 0.f;
+        sq += fmaf(q.n * off, off, q.sq);
+      }
+    } else {
+      mu = 0.f;
+#pragma unroll
+      for (int w = 0; w < G / 32; ++w) sq += parts[w].sq;
+    }
+    p.sq = sq;
+  } else {
+    mu = layer ? center : 0.f;
+  }
+  rho = rsqrtf(p.sq * inv + eps);
+}
+
+// G threads per row, which they hold in registers (8·NV values each); one
+// read and one write. VEC: the row in 16-byte pieces; otherwise value by
+// value, neighbouring threads on neighbouring values. Blocks of max(G, 128)
+// threads.
+template <int G, int NV, bool VEC>
+__global__ void __launch_bounds__(G < 128 ? 128 : G) residual_norm_rows_kernel(const ResidualNormArgs a) {
+  constexpr int THREADS = G < 128 ? 128 : G, V = 8 * NV;
+  __shared__ Part parts[2][THREADS / 32];
+  const int t = threadIdx.x % G;
+  const int64_t m = static_cast<int64_t>(blockIdx.x) * (THREADS / G) + threadIdx.x / G;
+  const int D = static_cast<int>(a.D);
+  // the column of a thread's value i
+  auto col = [&](int i) { return VEC ? (t + i / 8 * G) * 8 + i % 8 : i * G + t; };
+  auto in = [&](int i) { return col(VEC ? i / 8 * 8 : i) < D; };
+  auto load = [&](const uint16_t* p, int j, float (&f)[8], float otherwise) {
+    if constexpr (VEC) {
+      const int c = col(8 * j);
+      if (c < D && dbg_row(p + c, c, 8, D, 16)) unpack8(load16(p + c), f);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] = in(8 * j + k) ? half_at(p, col(8 * j + k)) : otherwise;
+    }
+  };
+  auto store = [&](uint16_t* p, int j, const float (&f)[8]) {
+    if constexpr (VEC) {
+      const int c = col(8 * j);
+      if (c < D && dbg_row(p + c, c, 8, D, 16)) *reinterpret_cast<uint4*>(p + c) = pack8f(f);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (in(8 * j + k)) p[col(8 * j + k)] = __half_as_ushort(__float2half_rn(f[k]));
+    }
+  };
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (G < 128 && m >= a.M) return;  // whole warps; larger groups have a block of their own
+  float v[V];                       // y, then z
+  float x[NV][8];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    float f[8] = {};
+    load(a.y + m * a.ldy, j, f, 0.f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[8 * j + k] = f[k];
+  }
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[j][k] = 0.f;
+    load(a.x + m * a.ldx, j, x[j], 0.f);
+  }
+  float my = 0.f, ry = 1.f, mz = 0.f, rz = 1.f;
+  if (a.post) row_moments<G, V>(a.post == HGEMM_NORM_LAYER, D, a.eps, parts[0], v, in, my, ry);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    float f[8] = {}, z[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) z[k] = v[8 * j + k];
+    if (a.post) {
+      load(a.post_gamma, j, f, 0.f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) z[k] = (z[k] - my) * ry * f[k];
+      if (a.post_beta) {
+        load(a.post_beta, j, f, 0.f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) z[k] += f[k];
+      }
+    }
+    if (a.gate) {
+      load(a.gate, j, f, 0.f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) z[k] *= f[k];
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[8 * j + k] = z[k] = fmaf(a.alpha, x[j][k], z[k]);
+    store(a.z + m * a.ldz, j, z);
+  }
+  if (a.pre) {
+    row_moments<G, V>(a.pre == HGEMM_NORM_LAYER, D, a.eps, parts[1], v, in, mz, rz);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float f[8] = {}, h[8];
+      load(a.pre_gamma, j, f, 0.f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) h[k] = (v[8 * j + k] - mz) * rz * f[k];
+      if (a.pre_beta) {
+        load(a.pre_beta, j, f, 0.f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) h[k] += f[k];
+      }
+      store(a.h + m * a.ldh, j, h);
+    }
+  }
+  if (t == 0 && a.stats && HG_DBG_INDEX(m, a.M)) {
+    if (a.post) a.stats[m] = my, a.stats[a.M + m] = ry;
+    if (a.pre) a.stats[2 * a.M + m] = mz, a.stats[3 * a.M + m] = rz;
+  }
+}
+
+// Rows too long for registers: a block per row, which it reads once per sum
+// (from L1 or L2 after the first).
+
 // μ and ρ of a row's values v(d), d = threadIdx.x, + kThreads, ...
 template <typename Value>
-__device__ __forceinline__ void row_moments(int kind, int64_t D, float eps, float* s, Value v, float& mu, float& rho) {
+__device__ __forceinline__ void long_row_moments(int kind, int64_t D, float eps, float* s, Value v, float& mu, float& rho) {
   const float n = static_cast<float>(D);
   mu = 0.f;
   if (kind == HGEMM_NORM_LAYER) {
@@ -38,9 +208,7 @@ __device__ __forceinline__ void row_moments(int kind, int64_t D, float eps, floa
   rho = rsqrtf(group_sum<kThreads>(sq, s) / n + eps);
 }
 
-// Any length, pitch and alignment: a block per row, which it reads once per
-// sum (from L1 or L2 after the first).
-__global__ void __launch_bounds__(kThreads) residual_norm_forward_kernel(const ResidualNormArgs a) {
+__global__ void __launch_bounds__(kThreads) residual_norm_long_kernel(const ResidualNormArgs a) {
   __shared__ float s[kThreads / 32];
   grid_dependency_wait();
   grid_launch_dependents();
@@ -48,13 +216,13 @@ __global__ void __launch_bounds__(kThreads) residual_norm_forward_kernel(const R
     if (!HG_DBG_INDEX(m, a.M)) return;
     const uint16_t *x = a.x + m * a.ldx, *y = a.y + m * a.ldy;
     float my = 0.f, ry = 1.f, mz = 0.f, rz = 1.f;
-    if (a.post) row_moments(a.post, a.D, a.eps, s, [&](int64_t d) { return half_at(y, d); }, my, ry);
+    if (a.post) long_row_moments(a.post, a.D, a.eps, s, [&](int64_t d) { return half_at(y, d); }, my, ry);
     auto z = [&](int64_t d) {
       float n = half_at(y, d);
       if (a.post) n = fmaf((n - my) * ry, half_at(a.post_gamma, d), half_or(a.post_beta, d, 0.f));
       return fmaf(a.alpha, half_at(x, d), n * half_or(a.gate, d, 1.f));
     };
-    if (a.pre) row_moments(a.pre, a.D, a.eps, s, z, mz, rz);
+    if (a.pre) long_row_moments(a.pre, a.D, a.eps, s, z, mz, rz);
     __syncthreads();  // (Z may be X and H may be Y) the row has been read
     for (int64_t d = threadIdx.x; d < a.D; d += kThreads) {
       const float v = z(d);
@@ -72,6 +240,393 @@ __global__ void __launch_bounds__(kThreads) residual_norm_forward_kernel(const R
 
 // ----------------------------------------------------------------- backward
 
+// Persistent CTAs of 512 threads, one per SM, in groups of G threads; group j
+// of a CTA owns a row at a time. Rows arrive by bulk copies, several ahead, in
+// a ring per group: dZ, dH, Z and Y, as far as there are any. A thread owns
+// the same 16 columns of every row, so the column sums add up in its
+// registers; at the end the groups of a CTA are added in order through shared
+// memory and the CTA writes one partial sum of each.
+//
+// Per row: pass 1 gives every sum along the row, one exchange between the
+// group's warps, pass 2 gives dX, dY and the columns' terms. That one exchange
+// is enough because dz is linear in a1 and a2: with t = dZ + ρ_z·g,
+// Σ w·dz = Σ w·t − ρ_z·(a1·Σw + a2·Σ w·ẑ), and the same with w·ŷ for w. Pass 1
+// of a row runs before pass 2 of the row before it, so that the exchange has
+// the time of a pass. Both passes read shared memory, which keeps the
+// registers for the column sums. The barrier of the exchange also frees the
+// stage of the row before: every thread of the group has finished its pass 2
+// by then, and the group's first thread copies a row into it.
+//
+// FULL: a layer norm, or a beta's gradient, is among what is wanted: four
+// column sums and the sums along the row that only these need. RMS norms
+// without betas do without, which leaves registers to run both passes in.
+struct RingPlan {
+  uint32_t dz, dh, z, y;  // where a row of each lies in a stage
+  uint32_t stage_bytes;
+  int stages;
+  bool need_y;            // the norm behind the block or the gate's gradient reads Y
+  bool empty;             // nothing to copy: neither dZ nor dH, nor Y
+};
+
+template <int G_>
+struct RingCfg {
+  static constexpr int G = G_, NV = 2;
+  static constexpr int THREADS = 512;
+  static constexpr int GROUPS = THREADS / G;
+  static constexpr int WARPS = G / 32;  // per group
+  static constexpr int MAX_STAGES = 8;
+  static constexpr int RING_BYTES = 200 * 1024;  // of the CTA
+  static constexpr int OFF_BAR = RING_BYTES;
+  static constexpr int OFF_EXCHANGE = OFF_BAR + GROUPS * MAX_STAGES * 8;
+  static constexpr int OFF_MISC = OFF_EXCHANGE + 2 * (THREADS / 32) * 32;  // two buffers of eight sums per warp
+  static constexpr int SMEM_BYTES = OFF_MISC + 16;
+  static_assert(SMEM_BYTES <= 232448 - 1024, "fits an SM");
+  static_assert(THREADS * 8 * NV * 4 * 4 <= RING_BYTES, "the groups' sums fit the ring");
+};
+
+// N sums (4 or 8) over a warp: while more than one is left, a lane sends the
+// half of them that its partner goes on with; 9 shuffles for eight. Lane l
+// leaves with the sum of v[l % N] over all lanes.
+template <int N>
+__device__ __forceinline__ float warp_sums(float (&v)[N]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1) {
+    const bool upper = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float mine = upper ? v[i + o] : v[i], other = upper ? v[i] : v[i + o];
+      v[i] = mine + __shfl_xor_sync(0xffffffffu, other, o);
+    }
+  }
+  float r = v[0];
+#pragma unroll
+  for (int o = N; o < 32; o <<= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+  return r;
+}
+
+__device__ __forceinline__ float pair_sum(f32x2 v) {
+  float lo, hi;
+  unpair(v, lo, hi);
+  return lo + hi;
+}
+
+// A row's statistics, and where it lies in shared memory.
+struct RingRow {
+  float my, ry, mz, rz;
+  const uint8_t* at;
+};
+
+template <int G, bool POST, bool PRE, bool FULL>
+__global__ void __launch_bounds__(512, 1) residual_norm_ring_kernel(const ResidualNormBackArgs a, const RingPlan plan) {
+  using Cfg = RingCfg<G>;
+  constexpr int NV = Cfg::NV;
+  constexpr int SUMS = FULL ? 8 : 4;
+  extern __shared__ __align__(128) uint8_t ring_smem[];
+  const int group = threadIdx.x / G, t = threadIdx.x % G;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int D = static_cast<int>(a.D), stages = plan.stages;
+  const uint32_t row_bytes = static_cast<uint32_t>(D) * 2u;
+  uint8_t* ring = ring_smem + static_cast<uint32_t>(group * stages) * plan.stage_bytes;
+  const uint32_t ring_addr = smem_u32(ring);
+  const uint32_t bar0 = smem_u32(ring_smem + Cfg::OFF_BAR) + static_cast<uint32_t>(group * Cfg::MAX_STAGES * 8);
+  float* exchange = reinterpret_cast<float*>(ring_smem + Cfg::OFF_EXCHANGE);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(ring_smem + Cfg::OFF_MISC);
+  const Watchdog wd{abort_flag, a.status, a.timeout_ns};
+
+  if (threadIdx.x == 0) *abort_flag = 0;
+  if (t == 0) {
+    for (int i = 0; i < stages; ++i) mbar_init(bar0 + 8u * i, 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * Cfg::GROUPS + group;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * Cfg::GROUPS;
+  int copied = 0;  // rows the group's first thread has issued
+  auto copy_row = [&](int64_t m, int stage) {
+    if (plan.empty) return;
+    ++copied;
+    const uint32_t bar = bar0 + 8u * stage, dst = ring_addr + static_cast<uint32_t>(stage) * plan.stage_bytes;
+    if (!(a.inject == 1 && copied == 1))  // testing aid: withhold one arrival
+      mbar_arrive_expect_tx(bar, plan.stage_bytes);
+    if (a.dz) bulk_load(dst + plan.dz, a.dz + m * a.lddz, row_bytes, bar);
+    if (PRE) {
+      bulk_load(dst + plan.dh, a.dh + m * a.lddh, row_bytes, bar);
+      bulk_load(dst + plan.z, a.z + m * a.ldz, row_bytes, bar);
+    }
+    if (POST || plan.need_y) bulk_load(dst + plan.y, a.y + m * a.ldy, row_bytes, bar);
+  };
+  if (t == 0)
+    for (int i = 0; i < stages - 1; ++i)
+      if (first + i * step < a.M) copy_row(first + i * step, i);
+
+  // w = gate·post_gamma, and the norm in front's gamma; the sums dz·ŷ, dz,
+  // dH·ẑ and dH of this thread's columns
+  f32x2 w[NV][4];
+  uint4 gamma[NV];
+  f32x2 s1[NV][4], s0[NV][4], t1[NV][4], t0[NV][4];
+  float sum_w = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (t + i * G) * 8;
+    gamma[i] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      w[i][k] = pair_of(c < D ? 1.f : 0.f);
+      s1[i][k] = s0[i][k] = t1[i][k] = t0[i][k] = 0;  // a pair of +0
+    }
+    if (c < D) {
+      f32x2 f[4];
+      if (PRE && dbg_row(a.pre_gamma + c, c, 8, D, 16)) gamma[i] = load16(a.pre_gamma + c);
+      if (a.gate && dbg_row(a.gate + c, c, 8, D, 16)) unpack8(load16(a.gate + c), w[i]);
+      if (POST && dbg_row(a.post_gamma + c, c, 8, D, 16)) {
+        unpack8(load16(a.post_gamma + c), f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[i][k] = mul2(w[i][k], f[k]);
+      }
+    }
+    if constexpr (FULL) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sum_w += pair_sum(w[i][k]);
+    }
+  }
+
+  const float inv_d = 1.f / static_cast<float>(D);
+  const bool layer_y = POST && a.post == HGEMM_NORM_LAYER, layer_z = PRE && a.pre == HGEMM_NORM_LAYER;
+  int stage = 0;  // of the next row that pass 1 takes
+  uint32_t phase = 0;
+  auto fetch_stats = [&](int64_t m) {
+    RingRow r{0.f, 1.f, 0.f, 1.f, nullptr};
+    if (m < a.M) {
+      if (POST) r.ry = a.stats[a.M + m];
+      if (layer_y) r.my = a.stats[m];
+      if (PRE) r.rz = a.stats[3 * a.M + m];
+      if (layer_z) r.mz = a.stats[2 * a.M + m];
+    }
+    return r;
+  };
+  // The sums along a row, over this warp's columns, into the exchange:
+  // Σ g·ẑ, w·ŷ·t, w·ŷ·ẑ, and FULL Σ g, w·t, w·ẑ, w·ŷ, w.
+  auto pass1 = [&](RingRow& r, int flip) {
+    // A wait that gives up has raised the abort flag: no more copies are
+    // issued, later waits give up at once, and the loop runs out on what the
+    // ring holds, so that every thread still reaches every barrier.
+    if (!plan.empty) (void)wait_phase(bar0 + 8u * stage, phase, wd, kWdRows);
+    r.at = ring + static_cast<uint32_t>(stage) * plan.stage_bytes;
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+    if constexpr (POST || PRE) {
+      // (v̂ from the difference: v·ρ − μ·ρ loses its digits in a row far from zero)
+      const f32x2 scale_z = pair_of(r.rz), shift_z = pair_of(-r.mz), scale_y = pair_of(r.ry), shift_y = pair_of(-r.my);
+      f32x2 p[7] = {0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int v = t + i * G;
+        if (v * 8 < D) {
+          f32x2 z[4], tt[4], y[4], g[4];
+          if (POST && a.dz) {
+            unpack8(reinterpret_cast<const uint4*>(r.at + plan.dz)[v], tt);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tt[k] = 0;
+          }
+          if constexpr (PRE) {
+            f32x2 q[4];
+            unpack8(reinterpret_cast<const uint4*>(r.at + plan.z)[v], z);
+            unpack8(reinterpret_cast<const uint4*>(r.at + plan.dh)[v], g);
+            unpack8(gamma[i], q);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if constexpr (FULL) z[k] = add2(z[k], shift_z);
+              z[k] = mul2(z[k], scale_z);
+              g[k] = mul2(g[k], q[k]);
+              p[0] = fma2(g[k], z[k], p[0]);
+              if constexpr (FULL) p[3] = add2(p[3], g[k]);
+              tt[k] = fma2(g[k], scale_z, tt[k]);
+            }
+          }
+          if constexpr (POST) {
+            unpack8(reinterpret_cast<const uint4*>(r.at + plan.y)[v], y);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if constexpr (FULL) y[k] = add2(y[k], shift_y);
+              y[k] = mul2(mul2(y[k], scale_y), w[i][k]);  // w·ŷ
+              p[1] = fma2(y[k], tt[k], p[1]);
+              if constexpr (FULL) p[4] = fma2(w[i][k], tt[k], p[4]);
+              if constexpr (PRE) {
+                p[2] = fma2(y[k], z[k], p[2]);
+                if constexpr (FULL) {
+                  p[5] = fma2(w[i][k], z[k], p[5]);
+                  p[6] = add2(p[6], y[k]);
+                }
+              }
+            }
+          }
+        }
+      }
+      float sums[SUMS];
+#pragma unroll
+      for (int i = 0; i < (FULL ? 7 : 3); ++i) sums[i] = pair_sum(p[i]);
+      sums[SUMS - 1] = sum_w;
+      const float mine = warp_sums(sums);
+      if (lane < SUMS) exchange[(flip * (Cfg::THREADS / 32) + warp) * 8 + lane] = mine;
+    }
+  };
+
+  RingRow row = fetch_stats(first), next = fetch_stats(first + step);
+  int flip = 0;
+  if (first < a.M) pass1(row, 0);
+  for (int64_t m = first; m < a.M; m += step) {
+    if constexpr (Cfg::WARPS > 1)
+      named_bar_sync(1 + group, G);
+    else
+      __syncwarp();
+    if (t == 0) {
+      // the stage of the row before this one is free: the group is past it
+      const int64_t ahead = m + (stages - 1) * step;
+      const int into = stage == 0 ? stages - 1 : stage - 1;  // this row's
+      if (ahead < a.M && !*abort_flag) copy_row(ahead, into == 0 ? stages - 1 : into - 1);
+    }
+    float mine = 0.f;
+    if constexpr (POST || PRE) {
+      const float* ex = exchange + (flip * (Cfg::THREADS / 32) + group * Cfg::WARPS) * 8 + lane % SUMS;
+#pragma unroll
+      for (int i = 0; i < Cfg::WARPS; ++i) mine += ex[i * 8];
+    }
+    flip ^= 1;  // the other buffer next: nobody writes this one before everybody has read it
+    const RingRow after = fetch_stats(m + 2 * step);
+    if (m + step < a.M) pass1(next, flip);
+
+    float sums[SUMS];
+    mine *= inv_d;
+#pragma unroll
+    for (int i = 0; i < SUMS; ++i) sums[i] = __shfl_sync(0xffffffffu, mine, i);
+    const float a1 = FULL && layer_z ? sums[SUMS - 5] : 0.f, a2 = sums[0];
+    float b1 = 0.f, b2 = sums[1] - row.rz * (a2 * sums[2]);
+    if constexpr (FULL) {
+      if (layer_y) b1 = sums[SUMS - 4] - row.rz * (a1 * sums[SUMS - 1] + a2 * sums[SUMS - 3]);
+      b2 -= row.rz * (a1 * sums[SUMS - 2]);
+    }
+    // dz = dZ + ρ_z·g + ẑ·k2 + k1;  dY = ρ_y·w·dz + ŷ·l2 + l1
+    const f32x2 scale_z = pair_of(row.rz), shift_z = pair_of(-row.mz);
+    const f32x2 scale_y = pair_of(row.ry), shift_y = pair_of(-row.my);
+    const f32x2 k1 = pair_of(-row.rz * a1), k2 = pair_of(-row.rz * a2);
+    const f32x2 l1 = pair_of(-row.ry * b1), l2 = pair_of(-row.ry * b2), alpha = pair_of(a.alpha);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = t + i * G;
+      if (v * 8 < D) {
+        f32x2 dz[4], z[4], g[4];
+        if (a.dz) {
+          unpack8(reinterpret_cast<const uint4*>(row.at + plan.dz)[v], dz);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) dz[k] = 0;
+        }
+        if constexpr (PRE) {
+          f32x2 q[4];
+          unpack8(reinterpret_cast<const uint4*>(row.at + plan.z)[v], z);
+          unpack8(reinterpret_cast<const uint4*>(row.at + plan.dh)[v], g);
+          unpack8(gamma[i], q);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if constexpr (FULL) z[k] = add2(z[k], shift_z);
+            z[k] = mul2(z[k], scale_z);
+            t1[i][k] = fma2(g[k], z[k], t1[i][k]);
+            if constexpr (FULL) {
+              t0[i][k] = add2(t0[i][k], g[k]);
+              z[k] = fma2(z[k], k2, k1);
+            } else {
+              z[k] = mul2(z[k], k2);
+            }
+            dz[k] = add2(dz[k], fma2(mul2(g[k], q[k]), scale_z, z[k]));
+          }
+        }
+        const int64_t c = v * 8;
+        if (POST || plan.need_y) unpack8(reinterpret_cast<const uint4*>(row.at + plan.y)[v], z);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          g[k] = mul2(w[i][k], dz[k]);
+          if (POST || plan.need_y) {
+            if constexpr (POST) {
+              if constexpr (FULL) z[k] = add2(z[k], shift_y);
+              z[k] = mul2(z[k], scale_y);
+            }
+            s1[i][k] = fma2(dz[k], z[k], s1[i][k]);
+          }
+          if constexpr (POST) {
+            if constexpr (FULL) {
+              s0[i][k] = add2(s0[i][k], dz[k]);
+              z[k] = fma2(z[k], l2, l1);
+            } else {
+              z[k] = mul2(z[k], l2);
+            }
+            g[k] = fma2(g[k], scale_y, z[k]);
+          }
+          dz[k] = mul2(dz[k], alpha);
+        }
+        if (dbg_row(a.dx + m * a.lddx + c, c, 8, D, 16)) *reinterpret_cast<uint4*>(a.dx + m * a.lddx + c) = pack8(dz);
+        if (dbg_row(a.dy + m * a.lddy + c, c, 8, D, 16)) *reinterpret_cast<uint4*>(a.dy + m * a.lddy + c) = pack8(g);
+      }
+    }
+    row = next;
+    next = after;
+  }
+
+  // Every copy has landed, each waited for before its row, unless a wait gave
+  // up: the last copy into each stage lands before the CTA leaves.
+  __syncthreads();
+  if (*abort_flag) {
+    if (t == 0)
+      for (int i = copied > stages ? copied - stages : 0; i < copied; ++i)
+        wait_drain(bar0 + 8u * (i % stages), static_cast<uint32_t>(i / stages) & 1u, wd);
+    __syncthreads();
+    return;
+  }
+  // The CTA's partial sums: the groups in order, four sums one after another
+  // through [group][2·8·G] in the ring.
+  if (!HG_DBG_INDEX(blockIdx.x, kResidualNormPartials) || !HG_DBG_ALIGN(a.partials, 16)) return;
+  float* out = a.partials + static_cast<int64_t>(blockIdx.x) * 4 * D;
+  auto write_sums = [&](const f32x2 (&s)[NV][4], int which) {
+    if constexpr (Cfg::GROUPS > 1) {
+      float* all = reinterpret_cast<float*>(ring_smem) + which * (Cfg::THREADS * 8 * NV);
+      float* mine = all + group * (NV * 8 * G);
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          *reinterpret_cast<ulonglong2*>(mine + (t + i * G) * 8 + 4 * k) = make_ulonglong2(s[i][2 * k], s[i][2 * k + 1]);
+      __syncthreads();
+      for (int c = threadIdx.x; c < D; c += Cfg::THREADS) {
+        float v = 0.f;
+#pragma unroll
+        for (int j = 0; j < Cfg::GROUPS; ++j) v += all[j * (NV * 8 * G) + c];
+        out[static_cast<int64_t>(which) * D + c] = v;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (t + i * G) * 8;
+        if (c < D) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            *reinterpret_cast<ulonglong2*>(out + static_cast<int64_t>(which) * D + c + 4 * k) =
+                make_ulonglong2(s[i][2 * k], s[i][2 * k + 1]);
+        }
+      }
+    }
+  };
+  write_sums(s1, 0);
+  if constexpr (FULL) write_sums(s0, 1);
+  write_sums(t1, 2);
+  if constexpr (FULL) write_sums(t0, 3);
+}
+
 // What the gradients of a value need of its row: the statistics and the four
 // means a1 = mean(g), a2 = mean(g·ẑ) (g = dH·γ), b1 = mean(w·dz),
 // b2 = mean(w·dz·ŷ) (w = gate·γ'), a layer norm's a1 and b1 0 for an RMS norm.
@@ -81,8 +636,10 @@ struct BackRow {
 
 __device__ __forceinline__ BackRow back_row(const ResidualNormBackArgs& a, int64_t m) {
   BackRow r{0.f, 1.f, 0.f, 1.f, 0.f, 0.f, 0.f, 0.f};
-  if (a.post) r.my = a.stats[m], r.ry = a.stats[a.M + m];
-  if (a.pre) r.mz = a.stats[2 * a.M + m], r.rz = a.stats[3 * a.M + m];
+  if (a.post) r.ry = a.stats[a.M + m];
+  if (a.post == HGEMM_NORM_LAYER) r.my = a.stats[m];
+  if (a.pre) r.rz = a.stats[3 * a.M + m];
+  if (a.pre == HGEMM_NORM_LAYER) r.mz = a.stats[2 * a.M + m];
   return r;
 }
 
@@ -197,7 +754,8 @@ __global__ void __launch_bounds__(kThreads) residual_norm_backward_kernel(const 
 
 // The vectors' gradients from `count` partial sums, in a fixed order: 32
 // columns per block, 8 threads down each.
-__global__ void __launch_bounds__(kThreads) residual_norm_sums_kernel(const ResidualNormBackArgs a, int count) {
+__global__ void __launch_bounds__(kThreads)
+    residual_norm_sums_kernel(const ResidualNormBackArgs a, int count, bool full) {
   __shared__ float s[4][8][33];
   grid_dependency_wait();
   grid_launch_dependents();
@@ -207,7 +765,8 @@ __global__ void __launch_bounds__(kThreads) residual_norm_sums_kernel(const Resi
   if (d < a.D)
     for (int i = r; i < count; i += 8)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] += a.partials[(static_cast<int64_t>(i) * 4 + j) * a.D + d];
+      for (int j = 0; j < 4; ++j)
+        if (full || j % 2 == 0) v[j] += a.partials[(static_cast<int64_t>(i) * 4 + j) * a.D + d];
 #pragma unroll
   for (int j = 0; j < 4; ++j) s[j][r][c] = v[j];
   __syncthreads();
@@ -224,11 +783,91 @@ __global__ void __launch_bounds__(kThreads) residual_norm_sums_kernel(const Resi
   if (a.dpre_beta) a.dpre_beta[d] = v[3];
 }
 
+template <int G, int NV>
+cudaError_t forward_with(const ResidualNormArgs& a, bool vec, cudaStream_t stream) {
+  constexpr int THREADS = G < 128 ? 128 : G;
+  const int64_t blocks = (a.M + THREADS / G - 1) / (THREADS / G);  // at most 2^31 − 1 rows
+  PdlLaunch l(dim3(static_cast<unsigned>(blocks)), dim3(THREADS), 0, stream);
+  return cudaLaunchKernelEx(&l.cfg,
+                            vec ? residual_norm_rows_kernel<G, NV, true> : residual_norm_rows_kernel<G, NV, false>, a);
+}
+
+template <int G>
+cudaError_t forward_group(const ResidualNormArgs& a, bool vec, cudaStream_t stream) {
+  const int64_t nv = (a.D + 8 * G - 1) / (8 * G);
+  if (nv <= 1) return forward_with<G, 1>(a, vec, stream);
+  if (nv <= 2) return forward_with<G, 2>(a, vec, stream);
+  return forward_with<G, 4>(a, vec, stream);
+}
+
+template <int G, bool POST, bool PRE, bool FULL>
+cudaError_t ring_with(const ResidualNormBackArgs& a, const RingPlan& plan, int grid, cudaStream_t stream) {
+  static std::atomic<bool> attr_done[64];
+  auto kern = residual_norm_ring_kernel<G, POST, PRE, FULL>;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !attr_done[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RingCfg<G>::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_done[dev] = true;
+  }
+  PdlLaunch l(dim3(static_cast<unsigned>(grid)), dim3(RingCfg<G>::THREADS), RingCfg<G>::SMEM_BYTES, stream);
+  return cudaLaunchKernelEx(&l.cfg, kern, a, plan);
+}
+
+// Whether a call needs the column sums of dz and dH, or a layer norm's means.
+bool ring_full(const ResidualNormBackArgs& a) {
+  return a.post == HGEMM_NORM_LAYER || a.pre == HGEMM_NORM_LAYER || a.dpost_beta || a.dpre_beta ||
+         (a.dgate && a.post_beta);
+}
+
+// The ring kernel with G threads per row; *partials: how many it leaves.
+template <int G>
+cudaError_t ring_group(const ResidualNormBackArgs& a, int num_sms, int* partials, cudaStream_t stream) {
+  using Cfg = RingCfg<G>;
+  const int64_t want = (a.M + Cfg::GROUPS - 1) / Cfg::GROUPS;
+  const int most = num_sms < kResidualNormPartials ? num_sms : kResidualNormPartials;
+  const int grid = static_cast<int>(want < most ? want : most);
+  RingPlan plan{};
+  const uint32_t row = static_cast<uint32_t>(a.D) * 2u;
+  plan.need_y = a.post || a.dgate;
+  uint32_t at = 0;
+  if (a.dz) plan.dz = at, at += row;
+  if (a.pre) plan.dh = at, plan.z = at + row, at += 2 * row;
+  if (plan.need_y) plan.y = at, at += row;
+  plan.stage_bytes = at;
+  if (at == 0) plan.stage_bytes = row;  // neither dZ nor dH: nothing is copied
+  const uint32_t stages = Cfg::RING_BYTES / (plan.stage_bytes * Cfg::GROUPS);
+  plan.stages = static_cast<int>(stages > Cfg::MAX_STAGES ? Cfg::MAX_STAGES : stages);
+  plan.empty = at == 0;
+  *partials = grid;
+  if (!a.post && !a.pre) return ring_with<G, false, false, false>(a, plan, grid, stream);
+  if (ring_full(a)) {
+    if (!a.post) return ring_with<G, false, true, true>(a, plan, grid, stream);
+    return a.pre ? ring_with<G, true, true, true>(a, plan, grid, stream)
+                 : ring_with<G, true, false, true>(a, plan, grid, stream);
+  }
+  if (!a.post) return ring_with<G, false, true, false>(a, plan, grid, stream);
+  return a.pre ? ring_with<G, true, true, false>(a, plan, grid, stream)
+               : ring_with<G, true, false, false>(a, plan, grid, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_residual_norm_forward(const ResidualNormArgs& a, int num_sms, cudaStream_t stream) {
+  const bool vec = a.D % 8 == 0 && rows16(a.x, a.ldx) && rows16(a.y, a.ldy) && rows16(a.z, a.ldz) &&
+                   rows16(a.h, a.pre ? a.ldh : 8) && rows16(a.gate, 8) && rows16(a.post_gamma, 8) &&
+                   rows16(a.post_beta, 8) && rows16(a.pre_gamma, 8) && rows16(a.pre_beta, 8);
+  // Enough threads per row to hold it, 16 values each; when the rows do not
+  // fill the GPU, as many as have a piece of it.
+  const int64_t each = a.M > 4 * static_cast<int64_t>(num_sms) ? 16 : 8;
+  if (a.D <= 32 * each) return forward_group<32>(a, vec, stream);
+  if (a.D <= 128 * each) return forward_group<128>(a, vec, stream);
+  if (a.D <= 256 * each) return forward_group<256>(a, vec, stream);
+  if (a.D <= 512 * 32) return forward_group<512>(a, vec, stream);
   PdlLaunch l(dim3(rows_grid(a.M)), dim3(kThreads), 0, stream);
-  return cudaLaunchKernelEx(&l.cfg, residual_norm_forward_kernel, a);
+  return cudaLaunchKernelEx(&l.cfg, residual_norm_long_kernel, a);
 }
 
 // Partial sums; the kernels for any row keep theirs in the first kSlices, and
@@ -242,7 +881,20 @@ cudaError_t launch_residual_norm_backward(ResidualNormBackArgs a, int num_sms, c
   const int64_t pitch = (a.D + 3) / 4 * 4, most = (kResidualNormPartials - kSlices) * pitch;
   a.means = a.partials + 4 * kSlices * pitch;
   int partials = 0;
-  for (a.m0 = 0; a.m0 < a.M; a.m0 = a.m1) {
+  const bool ring = a.D % 8 == 0 && a.D <= 8192 && (!a.dz || rows16(a.dz, a.lddz)) &&
+                    (!a.pre || (rows16(a.dh, a.lddh) && rows16(a.z, a.ldz) && rows16(a.pre_gamma, 8))) &&
+                    rows16(a.y, a.ldy) && rows16(a.dx, a.lddx) && rows16(a.dy, a.lddy) && rows16(a.gate, 8) &&
+                    rows16(a.post_gamma, 8);
+  if (a.M > 0 && ring) {
+    e = a.D <= 512    ? ring_group<32>(a, num_sms, &partials, stream)
+        : a.D <= 1024 ? ring_group<64>(a, num_sms, &partials, stream)
+        : a.D <= 2048 ? ring_group<128>(a, num_sms, &partials, stream)
+        : a.D <= 4096 ? ring_group<256>(a, num_sms, &partials, stream)
+                      : ring_group<512>(a, num_sms, &partials, stream);
+    if (e != cudaSuccess) return e;
+    a.m0 = a.M;
+  }
+  for (; a.m0 < a.M; a.m0 = a.m1) {
     a.m1 = a.m0 + most < a.M ? a.m0 + most : a.M;
     PdlLaunch r(dim3(rows_grid(a.m1 - a.m0)), dim3(kThreads), 0, stream);
     if ((e = cudaLaunchKernelEx(&r.cfg, residual_norm_means_kernel, a)) != cudaSuccess) return e;
@@ -253,7 +905,7 @@ cudaError_t launch_residual_norm_backward(ResidualNormBackArgs a, int num_sms, c
   }
   if (!a.dgate && !a.dpost_gamma && !a.dpost_beta && !a.dpre_gamma && !a.dpre_beta) return e;
   PdlLaunch l(dim3(static_cast<unsigned>((a.D + 31) / 32)), dim3(kThreads), 0, stream);
-  return cudaLaunchKernelEx(&l.cfg, residual_norm_sums_kernel, a, partials);
+  return cudaLaunchKernelEx(&l.cfg, residual_norm_sums_kernel, a, partials, !ring || ring_full(a));
 }
 
 // The -DHGEMM_DEBUG build's check word of this file (null otherwise).
