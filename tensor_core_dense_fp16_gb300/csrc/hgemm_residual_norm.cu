@@ -102,14 +102,18 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) residual_norm_rows_kernel(c
   // the column of a thread's value i
   auto col = [&](int i) { return VEC ? (t + i / 8 * G) * 8 + i % 8 : i * G + t; };
   auto in = [&](int i) { return col(VEC ? i / 8 * 8 : i) < D; };
-  auto load = [&](const uint16_t* p, int j, float (&f)[8], float otherwise) {
+  auto load = [&](const uint16_t* p, int j) {
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
     if constexpr (VEC) {
       const int c = col(8 * j);
-      if (c < D && dbg_row(p + c, c, 8, D, 16)) unpack8(load16(p + c), f);
+      if (c < D && dbg_row(p + c, c, 8, D, 16)) v = load16(p + c);
     } else {
+      uint32_t w[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] = in(8 * j + k) ? half_at(p, col(8 * j + k)) : otherwise;
+      for (int k = 0; k < 8; ++k) w[k] = in(8 * j + k) ? p[col(8 * j + k)] : 0u;
+      v = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
     }
+    return v;
   };
   auto store = [&](uint16_t* p, int j, const float (&f)[8]) {
     if constexpr (VEC) {
@@ -125,56 +129,54 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) residual_norm_rows_kernel(c
   grid_launch_dependents();
   if (G < 128 && m >= a.M) return;  // whole warps; larger groups have a block of their own
   float v[V];                       // y, then z
-  float x[NV][8];
+  uint4 x[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) x[j] = load(a.y + m * a.ldy, j);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    float f[8] = {};
-    load(a.y + m * a.ldy, j, f, 0.f);
+    float f[8];
+    unpack8(x[j], f);
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[8 * j + k] = f[k];
-  }
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) x[j][k] = 0.f;
-    load(a.x + m * a.ldx, j, x[j], 0.f);
+    x[j] = load(a.x + m * a.ldx, j);
   }
   float my = 0.f, ry = 1.f, mz = 0.f, rz = 1.f;
   if (a.post) row_moments<G, V>(a.post == HGEMM_NORM_LAYER, D, a.eps, parts[0], v, in, my, ry);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    float f[8] = {}, z[8];
+    float f[8], z[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) z[k] = v[8 * j + k];
     if (a.post) {
-      load(a.post_gamma, j, f, 0.f);
+      unpack8(load(a.post_gamma, j), f);
 #pragma unroll
       for (int k = 0; k < 8; ++k) z[k] = (z[k] - my) * ry * f[k];
       if (a.post_beta) {
-        load(a.post_beta, j, f, 0.f);
+        unpack8(load(a.post_beta, j), f);
 #pragma unroll
         for (int k = 0; k < 8; ++k) z[k] += f[k];
       }
     }
     if (a.gate) {
-      load(a.gate, j, f, 0.f);
+      unpack8(load(a.gate, j), f);
 #pragma unroll
       for (int k = 0; k < 8; ++k) z[k] *= f[k];
     }
+    unpack8(x[j], f);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[8 * j + k] = z[k] = fmaf(a.alpha, x[j][k], z[k]);
+    for (int k = 0; k < 8; ++k) v[8 * j + k] = z[k] = fmaf(a.alpha, f[k], z[k]);
     store(a.z + m * a.ldz, j, z);
   }
   if (a.pre) {
     row_moments<G, V>(a.pre == HGEMM_NORM_LAYER, D, a.eps, parts[1], v, in, mz, rz);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      float f[8] = {}, h[8];
-      load(a.pre_gamma, j, f, 0.f);
+      float f[8], h[8];
+      unpack8(load(a.pre_gamma, j), f);
 #pragma unroll
       for (int k = 0; k < 8; ++k) h[k] = (v[8 * j + k] - mz) * rz * f[k];
       if (a.pre_beta) {
-        load(a.pre_beta, j, f, 0.f);
+        unpack8(load(a.pre_beta, j), f);
 #pragma unroll
         for (int k = 0; k < 8; ++k) h[k] += f[k];
       }
@@ -859,9 +861,11 @@ cudaError_t launch_residual_norm_forward(const ResidualNormArgs& a, int num_sms,
   const bool vec = a.D % 8 == 0 && rows16(a.x, a.ldx) && rows16(a.y, a.ldy) && rows16(a.z, a.ldz) &&
                    rows16(a.h, a.pre ? a.ldh : 8) && rows16(a.gate, 8) && rows16(a.post_gamma, 8) &&
                    rows16(a.post_beta, 8) && rows16(a.pre_gamma, 8) && rows16(a.pre_beta, 8);
-  // Enough threads per row to hold it, 16 values each; when the rows do not
-  // fill the GPU, as many as have a piece of it.
-  const int64_t each = a.M > 4 * static_cast<int64_t>(num_sms) ? 16 : 8;
+  // Enough threads per row to hold it, 32 values each at most (16384 rows of
+  // 4096: 128 threads 85 us, 256 threads of 16 values 93, 512 of 8 154); when
+  // the rows do not fill the GPU, as many as have a piece of it, which is
+  // faster for a single row.
+  const int64_t each = a.M > 4 * static_cast<int64_t>(num_sms) ? 32 : 8;
   if (a.D <= 32 * each) return forward_group<32>(a, vec, stream);
   if (a.D <= 128 * each) return forward_group<128>(a, vec, stream);
   if (a.D <= 256 * each) return forward_group<256>(a, vec, stream);
