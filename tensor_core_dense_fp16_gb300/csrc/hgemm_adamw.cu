@@ -24,13 +24,14 @@ template <int MAX>
 struct AdamwTable {
   AdamwStep step;
   int count;
-  uint32_t chunks;
+  int per;          // chunks of a block's step
+  uint32_t chunks;  // steps
   AdamwEntry t[MAX];
 };
 
 __device__ __forceinline__ float sqrt_approx(float x) {
   float y;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -51,16 +52,18 @@ __device__ __forceinline__ void second_scale(uint32_t top_bits, float& scale, fl
   }
 }
 
-// The upper 12 bits of an FP32 number in (0, 1] (8 of exponent, 3 of fraction)
-// rounded at the 20th, counted from 1's.
+// The upper 12 bits of an FP32 number r in (0, 1] (8 of exponent, 3 of fraction
+// and the leading 0) rounded at the 20th, counted from 1's; at least 1 where r
+// is not 0. (r = v·(1/top) is at most 1 + 2^-23, whose code is 255.) The caller
+// takes 0 in place of all codes of a group whose inv is 0.
 __device__ __forceinline__ uint32_t second_code(float v, float inv) {
-  const float r = __fmul_rn(v, inv);
-  const int c = 255 + (static_cast<int>(__float_as_uint(r) - kOneBits + 0x80000u) >> 20);
-  return r > 0.f ? static_cast<uint32_t>(min(max(c, 1), 255)) : 0u;
+  const uint32_t r = __float_as_uint(__fmul_rn(v, inv));
+  const int c = static_cast<int>(r + ((255u << 20) + 0x80000u - kOneBits)) >> 20;
+  return static_cast<uint32_t>(max(c, static_cast<int>(min(r, 1u))));
 }
 
 __device__ __forceinline__ float second_value(uint32_t code, float scale) {
-  const float r = code ? __uint_as_float(kOneBits - ((255u - code) << 20)) : 0.f;
+  const float r = code ? __uint_as_float((code << 20) + (kOneBits - (255u << 20))) : 0.f;
   return __fmul_rn(r, scale);
 }
 
@@ -188,7 +191,7 @@ __device__ __forceinline__ void adamw_eight(const AdamwEntry& t, const AdamwStep
                                             int64_t first) {
   const int64_t n = t.n;
   const bool in = first < n;  // VEC: all eight, n is a multiple of 8
-  const bool eight = t.ms != nullptr;
+  const bool eight = !VEC && t.ms != nullptr;  // (VEC: adamw_bytes)
   float g[8] = {}, m[8] = {}, v[8] = {}, p[8] = {};
   if (in && HG_DBG_INDEX(VEC ? first + 7 : first, n)) {
     if (t.grad_type == 0)
@@ -253,8 +256,121 @@ __device__ __forceinline__ void adamw_eight(const AdamwEntry& t, const AdamwStep
   }
 }
 
+// The same for 8-bit states moved eight at a time, the path of large tensors:
+// `count` chunks from `first` on, the next one's loads under way while one is
+// computed. The form's conversions cost as many instructions as its bytes
+// save: the three quotients of a group are one division, each in a lane of its
+// own.
+template <bool G32, bool MASTER>
+struct Packed {
+  uint2 m, v;
+  float sm, sv;
+  uint4 g[G32 ? 2 : 1], p[MASTER ? 2 : 1];
+};
+
+template <bool WIDE>
+__device__ __forceinline__ void unpack_wide(const uint4 (&w)[WIDE ? 2 : 1], float (&f)[8]) {
+  if constexpr (WIDE) {
+    f[0] = __uint_as_float(w[0].x), f[1] = __uint_as_float(w[0].y), f[2] = __uint_as_float(w[0].z);
+    f[3] = __uint_as_float(w[0].w), f[4] = __uint_as_float(w[1].x), f[5] = __uint_as_float(w[1].y);
+    f[6] = __uint_as_float(w[1].z), f[7] = __uint_as_float(w[1].w);
+  } else {
+    unpack8(w[0], f);
+  }
+}
+
+template <bool G32, bool MASTER>
+__device__ __forceinline__ void adamw_bytes(const AdamwEntry& t, const AdamwStep& s, const Scalars& c, float keep,
+                                            int64_t first, int count) {
+  const int64_t n = t.n;
+  uint8_t *tm = static_cast<uint8_t*>(t.m), *tv = static_cast<uint8_t*>(t.v);
+  auto load = [&](int64_t i) {
+    const int64_t at = i < n ? i : 0;  // (past the end: anything, not stored)
+    Packed<G32, MASTER> r{};
+    if (!HG_DBG_INDEX(at + 7, n)) return r;
+    r.m = load8(tm + at);
+    r.v = load8(tv + at);
+    r.sm = t.ms[at / kCkptGroup];
+    r.sv = t.vs[at / kCkptGroup];
+    const uint8_t* g = static_cast<const uint8_t*>(t.grad) + at * (G32 ? 4 : 2);
+    const uint8_t* p = MASTER ? reinterpret_cast<const uint8_t*>(t.master) + at * 4
+                              : reinterpret_cast<const uint8_t*>(t.weight) + at * 2;
+    r.g[0] = load16(g);
+    if (G32) r.g[G32 ? 1 : 0] = load16(g + 16);
+    r.p[0] = load16(p);
+    if (MASTER) r.p[MASTER ? 1 : 0] = load16(p + 16);
+    return r;
+  };
+  const int lane = threadIdx.x & 31, role = lane & 7;
+  Packed<G32, MASTER> next = load(first);
+  // (whole warps: a chunk's first value decides)
+  for (int i = 0; i < count && first - 8 * static_cast<int>(threadIdx.x) < n; ++i, first += kChunk) {
+    const Packed<G32, MASTER> r = next;
+    if (i + 1 < count) next = load(first + kChunk);
+    const bool in = first < n;  // all eight, n is a multiple of 8
+    float g[8], p[8], m[8], v[8];
+    unpack_wide<G32>(r.g, g);
+    unpack_wide<MASTER>(r.p, p);
+    float top_m = 0.f, top_v = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+      unpair(ckpt_pair((k < 4 ? r.m.x : r.m.y) ^ 0x80808080u, (k & 3) / 2), m[k], m[k + 1]);
+#pragma unroll
+      for (int j = k; j < k + 2; ++j) {
+        m[j] = __fmul_rn(m[j], r.sm);
+        v[j] = second_value(__byte_perm(j < 4 ? r.v.x : r.v.y, 0u, 0x4440u + (j & 3)), r.sv);
+        adamw_value(s, c, keep, g[j], m[j], v[j], p[j]);
+      }
+      top_m = max_abs3(top_m, m[k], m[k + 1]);
+      top_v = max_abs3(top_v, v[k], v[k + 1]);
+    }
+    if (in) {
+      if (MASTER) store_f32<true>(t.master, first, n, p);
+      if (!MASTER || t.weight) store_f16<true>(t.weight, first, n, p);
+    }
+    // (a group lies whole in or past the tensor's last eight; what is past is not counted)
+    uint32_t bits_m = in ? magnitude_bits(top_m) : 0u, bits_v = in ? magnitude_bits(top_v) : 0u;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) {
+      bits_m = max(bits_m, __shfl_xor_sync(0xffffffffu, bits_m, o));
+      bits_v = max(bits_v, __shfl_xor_sync(0xffffffffu, bits_v, o));
+    }
+    // lane 0 of a group's eight: max|m|/127, lane 1: 127/max|m|, lane 2: 1/max v
+    top_m = __uint_as_float(bits_m);
+    top_v = __uint_as_float(bits_v);
+    const float q =
+        __fdiv_rn(role == 0 ? top_m : role == 1 ? 127.f : 1.f, role == 0 ? 127.f : role == 1 ? top_m : top_v);
+    const float inv_m = __shfl_sync(0xffffffffu, q, (lane & 24) | 1);
+    const float inv_v = __shfl_sync(0xffffffffu, q, (lane & 24) | 2);
+    // (no infinity or NaN, and not below 2^-100)
+    const bool keep_m = bits_m < 0x7F800000u && top_m >= 7.888609e-31f;
+    const bool keep_v = bits_v < 0x7F800000u && top_v >= 7.888609e-31f;
+    uint32_t wm[2], wv[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t cm[4], cv[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        cm[k] = ckpt_code(m[4 * h + k], inv_m);
+        cv[k] = second_code(v[4 * h + k], inv_v);
+      }
+      wm[h] = __byte_perm(__byte_perm(cm[0], cm[1], 0x0040u), __byte_perm(cm[2], cm[3], 0x0040u), 0x5410u);
+      wv[h] = __byte_perm(__byte_perm(cv[0], cv[1], 0x0040u), __byte_perm(cv[2], cv[3], 0x0040u), 0x5410u);
+    }
+    if (in) {
+      *reinterpret_cast<uint2*>(tm + first) = keep_m ? make_uint2(wm[0], wm[1]) : make_uint2(0u, 0u);
+      *reinterpret_cast<uint2*>(tv + first) = keep_v ? make_uint2(wv[0], wv[1]) : make_uint2(0u, 0u);
+      if (role == 0) {
+        const float nan = __uint_as_float(0x7FFFFFFFu);
+        t.ms[first / kCkptGroup] = keep_m ? q : bits_m >= 0x7F800000u ? nan : 0.f;
+        t.vs[first / kCkptGroup] = keep_v ? top_v : bits_v >= 0x7F800000u ? nan : 0.f;
+      }
+    }
+  }
+}
+
 template <int MAX>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamwTable<MAX> table) {
+__global__ void __launch_bounds__(kThreads, 3) adamw_kernel(const __grid_constant__ AdamwTable<MAX> table) {
   grid_dependency_wait();
   grid_launch_dependents();
   const AdamwStep& s = table.step;
@@ -278,12 +394,24 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
         hi = mid - 1;
     }
     const AdamwEntry& t = table.t[lo];
-    const int64_t base = static_cast<int64_t>(chunk - t.chunk0) * kChunk;
+    int64_t first = static_cast<int64_t>(chunk - t.chunk0) * kChunk * table.per;
     const float keep = c.dynamic ? fmaf(-c.lr, t.decay, 1.f) : t.keep;
-    if (t.vec)
-      adamw_eight<true>(t, s, c, keep, base + 8 * static_cast<int>(threadIdx.x));
-    else
-      adamw_eight<false>(t, s, c, keep, base + (threadIdx.x >> 5) * 256 + (threadIdx.x & 31));
+    if (t.vec && t.ms) {
+      first += 8 * static_cast<int>(threadIdx.x);
+      if (t.grad_type == 0)
+        t.master ? adamw_bytes<false, true>(t, s, c, keep, first, table.per)
+                 : adamw_bytes<false, false>(t, s, c, keep, first, table.per);
+      else
+        t.master ? adamw_bytes<true, true>(t, s, c, keep, first, table.per)
+                 : adamw_bytes<true, false>(t, s, c, keep, first, table.per);
+      continue;
+    }
+    for (int i = 0; i < table.per && first < t.n; ++i, first += kChunk) {
+      if (t.vec)
+        adamw_eight<true>(t, s, c, keep, first + 8 * static_cast<int>(threadIdx.x));
+      else
+        adamw_eight<false>(t, s, c, keep, first + (threadIdx.x >> 5) * 256 + (threadIdx.x & 31));
+    }
   }
 }
 
@@ -293,24 +421,73 @@ cudaError_t adamw_with(const AdamwEntry* t, int count, uint32_t chunks, const Ad
   AdamwTable<MAX> table;
   table.step = step;
   table.count = count;
+  // Eight chunks a step where that leaves every block a few steps: the search
+  // for the tensor and its addresses are paid for once (100 M values with
+  // 8-bit states, and read back: 467 us with one, 373 with four, 359 with eight;
+  // 33.6 M with FP32 states 144, 141, 143). More blocks than fit at once balance
+  // better than one wave of them (FP32 states: 160 us with 3 an SM, 143 with 16).
+  table.per = chunks >= static_cast<uint32_t>(num_sms) * 32u ? 8 : 1;
+  chunks = 0;
+  for (int i = 0; i < count; ++i) {
+    table.t[i] = t[i];
+    table.t[i].chunk0 = chunks;
+    const int64_t step_values = static_cast<int64_t>(kChunk) * table.per;
+    chunks += static_cast<uint32_t>((t[i].n + step_values - 1) / step_values);
+  }
   table.chunks = chunks;
-  for (int i = 0; i < count; ++i) table.t[i] = t[i];
-  const uint32_t most = static_cast<uint32_t>(num_sms) * 8u;
+  const uint32_t most = static_cast<uint32_t>(num_sms) * 16u;
   PdlLaunch l(dim3(chunks < most ? chunks : most), dim3(kThreads), 0, stream);
   return cudaLaunchKernelEx(&l.cfg, adamw_kernel<MAX>, table);
 }
 
-// One value per thread.
+// Four neighbouring values per thread and step where VEC, else one.
+template <bool VEC>
 __global__ void __launch_bounds__(kThreads)
     adamw_load_kernel(const int8_t* m, const float* ms, const uint8_t* v, const float* vs, float* m_out, float* v_out,
                       int64_t n) {
+  constexpr int EACH = VEC ? 4 : 1, AHEAD = VEC ? 4 : 1;
   grid_dependency_wait();
   grid_launch_dependents();
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n; i += step) {
-    if (!HG_DBG_INDEX(i, n)) return;
-    if (m) m_out[i] = __fmul_rn(static_cast<float>(m[i]), ms[i / kCkptGroup]);
-    if (v) v_out[i] = second_value(v[i], vs[i / kCkptGroup]);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads * EACH;
+  const int64_t begin = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * EACH;
+  for (int64_t i0 = begin; i0 < n; i0 += AHEAD * step) {
+    uint32_t cm[AHEAD], cv[AHEAD];
+    float sm[AHEAD], sv[AHEAD];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      const int64_t i = i0 + j * step;
+      if (i >= n || !HG_DBG_INDEX(i + EACH - 1, n)) break;
+      if (m) {
+        cm[j] = VEC ? *reinterpret_cast<const uint32_t*>(m + i) : static_cast<uint8_t>(m[i]);
+        sm[j] = ms[i / kCkptGroup];
+      }
+      if (v) {
+        cv[j] = VEC ? *reinterpret_cast<const uint32_t*>(v + i) : v[i];
+        sv[j] = vs[i / kCkptGroup];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      const int64_t i = i0 + j * step;
+      if (i >= n) break;
+      float f[4];
+      if (m) {
+#pragma unroll
+        for (int k = 0; k < EACH; ++k) f[k] = __fmul_rn(static_cast<float>(static_cast<int8_t>(cm[j] >> (8 * k))), sm[j]);
+        if constexpr (VEC)
+          *reinterpret_cast<float4*>(m_out + i) = make_float4(f[0], f[1], f[2], f[3]);
+        else
+          m_out[i] = f[0];
+      }
+      if (v) {
+#pragma unroll
+        for (int k = 0; k < EACH; ++k) f[k] = second_value((cv[j] >> (8 * k)) & 0xFFu, sv[j]);
+        if constexpr (VEC)
+          *reinterpret_cast<float4*>(v_out + i) = make_float4(f[0], f[1], f[2], f[3]);
+        else
+          v_out[i] = f[0];
+      }
+    }
   }
 }
 
@@ -324,9 +501,13 @@ cudaError_t launch_adamw(const AdamwEntry* t, int count, uint32_t chunks, const 
 
 cudaError_t launch_adamw_load(const int8_t* m, const float* ms, const uint8_t* v, const float* vs, float* m_out,
                               float* v_out, int64_t n, int num_sms, cudaStream_t stream) {
-  const int64_t want = (n + kThreads - 1) / kThreads, most = static_cast<int64_t>(num_sms) * 8;
+  auto aligned = [](const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; };
+  const bool vec = n % 4 == 0 && aligned(m, 4) && aligned(v, 4) && aligned(m_out, 16) && aligned(v_out, 16);
+  const int64_t per = kThreads * (vec ? 4 : 1);
+  const int64_t want = (n + per - 1) / per, most = static_cast<int64_t>(num_sms) * 8;
   PdlLaunch l(dim3(static_cast<unsigned>(want < most ? want : most)), dim3(kThreads), 0, stream);
-  return cudaLaunchKernelEx(&l.cfg, adamw_load_kernel, m, ms, v, vs, m_out, v_out, n);
+  return cudaLaunchKernelEx(&l.cfg, vec ? adamw_load_kernel<true> : adamw_load_kernel<false>, m, ms, v, vs, m_out, v_out,
+                            n);
 }
 
 // The -DHGEMM_DEBUG build's check word of this file (null otherwise).
