@@ -473,7 +473,7 @@ bool experts_sizes_ok(int64_t M, int64_t D, int64_t F, int64_t E, int64_t k) {
 
 size_t hgemm_experts_workspace_size(int64_t M, int64_t D, int64_t F, int64_t E, int64_t k) {
   if (!experts_sizes_ok(M, D, F, E, k)) return 0;
-  return hg::experts_workspace(M, D, F, k);
+  return hg::experts_workspace(M, D, F, E, k);
 }
 
 int hgemm_experts(const hgemm_half_t* X, int64_t ldx, const hgemm_half_t* Wr, int64_t ldwr, const hgemm_half_t* W1,
@@ -492,7 +492,7 @@ int hgemm_experts(const hgemm_half_t* X, int64_t ldx, const hgemm_half_t* Wr, in
   const Span c = vec_or_none(chosen, M * k, 4), s = vec_or_none(share, M * k, 4);
   for (const Span& v : {x, wr, w1, w2, v1, v2, r, y, c, s})
     if (!span_ok(v)) return HGEMM_ERR_INVALID_ARG;
-  const size_t need = hg::experts_workspace(M, D, F, k);
+  const size_t need = hg::experts_workspace(M, D, F, E, k);
   if (M > 0 && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15u)))
     return HGEMM_ERR_INVALID_ARG;
   const Span ws = vec(workspace, static_cast<int64_t>(need), 1);

@@ -11,6 +11,8 @@
 // interleaved pieces of K and their sums are added in order through shared
 // memory. Work is numbered over the experts that some token chose, so that
 // only their weights are read, each by one block.
+#include <atomic>
+
 #include <cuda_fp16.h>
 
 #include "debug.cuh"
@@ -89,38 +91,65 @@ __device__ __forceinline__ void choose(const float* logits, int E, int k, bool n
   share = __fdiv_rn(share, warp_sum(sum));
 }
 
-// A block per token: a warp per logit, then the choice.
+// A cluster of CTAs per token: a warp per logit, the logits gathered in the
+// first CTA, which chooses. The launch is bound by its latencies: a lane asks
+// for eight pieces of a row at once.
 template <bool VEC>
 __global__ void __launch_bounds__(kThreads) experts_router_kernel(const ExpertsArgs a) {
   __shared__ float logits[kMost];
+  if (a.router_ctas > 1) cluster_sync();  // the first CTA is there
   grid_dependency_wait();
   grid_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, m = blockIdx.x;
-  if (!HG_DBG_INDEX(m, a.M)) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int ctas = a.router_ctas, rank = blockIdx.x % ctas, m = blockIdx.x / ctas;
+  const uint32_t gather = mapa_shared(smem_u32(logits), 0);
   const uint16_t* x = a.X + m * a.ldx;
-  for (int e = warp; e < a.E; e += kWarps) {
+  for (int e = rank * kWarps + warp; e < a.E; e += ctas * kWarps) {
     const uint16_t* w = a.Wr + e * a.ldwr;
     float sum = 0.f;
     if constexpr (VEC) {
-      for (int64_t d = 8 * lane; d < a.D; d += 256) {
-        float p[8], q[8];
-        unpack8(load16(x + d), p);
-        unpack8(load16(w + d), q);
+      constexpr int AHEAD = 8;
+      for (int d0 = 8 * lane; d0 < a.D; d0 += 256 * AHEAD) {
+        uint4 p[AHEAD], q[AHEAD];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum = fmaf(p[i], q[i], sum);
+        for (int j = 0; j < AHEAD; ++j) {
+          const int d = d0 + 256 * j;
+          p[j] = q[j] = make_uint4(0u, 0u, 0u, 0u);
+          if (d < a.D && dbg_row(w + d, d, 8, a.D, 16)) {
+            p[j] = load16(x + d);
+            q[j] = load16(w + d);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+          float f[8], h[8];
+          unpack8(p[j], f);
+          unpack8(q[j], h);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum = fmaf(f[i], h[i], sum);
+        }
       }
     } else {
-      for (int64_t d = lane; d < a.D; d += 32) sum = fmaf(half_at(x, d), half_at(w, d), sum);
+#pragma unroll 8
+      for (int d = lane; d < a.D; d += 32) sum = fmaf(half_at(x, d), half_at(w, d), sum);
     }
     sum = warp_sum(sum);
-    if (lane == 0) logits[e] = sum;
+    if (lane == 0 && HG_DBG_INDEX(e, kMost)) {
+      if (ctas == 1)
+        logits[e] = sum;
+      else
+        st_cluster_f32(gather + 4u * static_cast<uint32_t>(e), sum);
+    }
   }
-  __syncthreads();
-  if (warp > 0) return;
+  if (ctas == 1)
+    __syncthreads();
+  else
+    cluster_sync();
+  if (rank > 0 || warp > 0) return;
   int e;
   float share;
   choose(logits, a.E, a.k, a.normalize, e, share);
-  if (lane < a.k) {
+  if (lane < a.k && HG_DBG_INDEX(m, a.M)) {
     const int at = m * a.k + lane;
     a.ws_chosen[at] = e;
     a.ws_share[at] = share;
@@ -131,154 +160,246 @@ __global__ void __launch_bounds__(kThreads) experts_router_kernel(const ExpertsA
 
 // ------------------------------------------------------------------ products
 
-// Which experts some token chose, and who chose the one at hand. A slot is a
-// choice, m·k + j.
+// Who chose which expert. A slot is a choice, m·k + j; an entry a run of at
+// most 8·MT slots that chose the same expert, whose weights are read once for
+// it. Experts come in order, and within one the tokens.
+constexpr int kSlots = kTokens * HGEMM_EXPERTS_MAX_CHOICES;
+constexpr int kEntries = kMost + kSlots / 8;  // a partly filled one per expert, and full ones
 struct Routing {
-  int chosen[kTokens * HGEMM_EXPERTS_MAX_CHOICES];
-  int active[kMost];  // the chosen experts, in order
-  int count;
-  int slots[kTokens];  // the slots that chose the expert at hand, in order
-  int rows;
+  unsigned long long tokens[kMost];  // a bit per token that chose the expert
+  uint16_t list[kSlots];             // the slots, by entry
+  uint16_t first[kMost];             // where an expert's slots begin in it
+  struct {
+    uint16_t expert, first;
+    int count;
+  } entry[kEntries];
+  int entries;
 };
 
-__device__ __forceinline__ void find_active(Routing& r, const ExpertsArgs& a) {
-  for (int e = threadIdx.x; e < a.E; e += kThreads) r.active[e] = 0;
+template <int MT>
+__device__ __forceinline__ void find_entries(Routing& r, const ExpertsArgs& a) {
+  for (int e = threadIdx.x; e < a.E; e += kThreads) r.tokens[e] = 0;
   __syncthreads();
-  for (int i = threadIdx.x; i < a.M * a.k; i += kThreads) {
-    r.chosen[i] = a.ws_chosen[i];
-    r.active[r.chosen[i]] = 1;
-  }
-  __syncthreads();
-  if (threadIdx.x < 32) {  // in place: what is written lies before what is read
-    int n = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 32) {
-      const int e = e0 + static_cast<int>(threadIdx.x);
-      const bool is = e < a.E && r.active[e];
-      const uint32_t all = __ballot_sync(0xffffffffu, is);
-      if (is) r.active[n + __popc(all & ((1u << threadIdx.x) - 1u))] = e;
-      n += __popc(all);
-      __syncwarp();
-    }
-    if (threadIdx.x == 0) r.count = n;
-  }
-  __syncthreads();
-}
-
-__device__ __forceinline__ void find_slots(Routing& r, const ExpertsArgs& a, int expert) {
+  const int slots = a.M * a.k;
+  for (int i = threadIdx.x; i < slots; i += kThreads)
+    atomicOr(&r.tokens[ld_gpu_s32(a.ws_chosen + i)], 1ull << (i / a.k));
   __syncthreads();
   if (threadIdx.x < 32) {
-    int n = 0;
-    for (int i0 = 0; i0 < a.M * a.k; i0 += 32) {
-      const int i = i0 + static_cast<int>(threadIdx.x);
-      const bool is = i < a.M * a.k && r.chosen[i] == expert;
-      const uint32_t all = __ballot_sync(0xffffffffu, is);
-      if (is) r.slots[n + __popc(all & ((1u << threadIdx.x) - 1u))] = i;
-      n += __popc(all);
+    const int lane = threadIdx.x;
+    int at = 0, n = 0;  // slots and entries of the experts before
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+      const int e = e0 + lane;
+      const int count = e < a.E ? __popcll(r.tokens[e]) : 0;
+      const int runs = (count + 8 * MT - 1) / (8 * MT);
+      int both = count | runs << 16, sum = both;  // (1024 slots, 640 entries at most)
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
+      }
+      const int all = __shfl_sync(0xffffffffu, sum, 31);
+      const int first = at + ((sum - both) & 0xFFFF), entry = n + ((sum - both) >> 16);
+      if (count > 0) {
+        r.first[e] = static_cast<uint16_t>(first);
+        for (int j = 0; j < runs; ++j) {
+          r.entry[entry + j].expert = static_cast<uint16_t>(e);
+          r.entry[entry + j].first = static_cast<uint16_t>(first + 8 * MT * j);
+          r.entry[entry + j].count = min(count - 8 * MT * j, 8 * MT);
+        }
+      }
+      at += all & 0xFFFF;
+      n += all >> 16;
     }
-    if (threadIdx.x == 0) r.rows = n;
+    if (lane == 0) r.entries = n;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < slots; i += kThreads) {
+    const int e = ld_gpu_s32(a.ws_chosen + i);
+    r.list[r.first[e] + __popcll(r.tokens[e] & ((1ull << (i / a.k)) - 1))] = static_cast<uint16_t>(i);
   }
   __syncthreads();
 }
 
 template <bool VEC>
-__device__ __forceinline__ uint4 load_piece(const uint16_t* row, int k, int K, bool once) {
+__device__ __forceinline__ uint4 load_piece(const uint16_t* row, int k, int K, bool weights) {
   if constexpr (VEC) {
     if (k >= K || !dbg_row(row + k, k, 8, K, 16)) return make_uint4(0u, 0u, 0u, 0u);
-    return once ? load16_once(row + k) : load16(row + k);
+    return weights ? ld_gpu_16(row + k) : load16(row + k);  // (L1 keeps the tokens)
   } else {
     uint32_t v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = k + 2 * i < K ? row[k + 2 * i] : 0u;
-      const uint32_t hi = k + 2 * i + 1 < K ? row[k + 2 * i + 1] : 0u;
+      const uint32_t lo = k + 2 * i < K ? (weights ? ld_gpu_u16(row + k + 2 * i) : row[k + 2 * i]) : 0u;
+      const uint32_t hi = k + 2 * i + 1 < K ? (weights ? ld_gpu_u16(row + k + 2 * i + 1) : row[k + 2 * i + 1]) : 0u;
       v[i] = lo | hi << 16;
     }
     return make_uint4(v[0], v[1], v[2], v[3]);
   }
 }
 
-// FIRST: unit u of an expert is features 8u .. 8u+7 and their gates (gated) or
-// 16u .. 16u+15, and H is written; else outputs 16u .. 16u+15 and the slots'
-// FP32 outputs are. MT tiles of 8 tokens.
+// FIRST: a unit of work is features 8u .. 8u+7 and their gates (gated) or
+// 16u .. 16u+15 of an entry's expert, and H is written; else outputs 16u ..
+// 16u+15 over one of `splits` runs of F, and the slots' FP32 partial outputs
+// are. Units are dealt to the blocks in turn. A warp's pieces of all its units
+// form one sequence, AHEAD of which are under way at any time, so that the next
+// unit's weights are on their way while one is added up. The second product
+// starts on its weights before the first has ended: who chose what is known
+// since the router, and only the tokens' values have to be waited for.
+template <int MT>
+struct ProductCfg {
+  static constexpr int AHEAD = MT == 1 ? 4 : MT == 2 ? 3 : 2;
+  static constexpr int PART = kWarps * 8 * MT * 17;  // floats of one buffer of partial sums
+  static constexpr int SMEM_BYTES = 2 * PART * 4 + static_cast<int>(sizeof(Routing));
+};
+
 template <int MT, bool FIRST, bool VEC>
-__global__ void __launch_bounds__(kThreads) experts_product_kernel(const ExpertsArgs a) {
-  __shared__ Routing r;
-  __shared__ float part[kWarps][8 * MT][17];
-  grid_dependency_wait();
-  grid_launch_dependents();
-  find_active(r, a);
+__global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) experts_product_kernel(const ExpertsArgs a) {
+  constexpr int AHEAD = ProductCfg<MT>::AHEAD;
+  extern __shared__ __align__(16) uint8_t experts_smem[];
+  float* parts = reinterpret_cast<float*>(experts_smem);
+  Routing& r = *reinterpret_cast<Routing*>(experts_smem + 2 * ProductCfg<MT>::PART * 4);
+  if constexpr (FIRST) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+  } else {
+    fence_gpu();
+  }
+  find_entries<MT>(r, a);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const int K = FIRST ? a.D : a.F;
+  const int K = FIRST ? a.D : a.F, rows = FIRST ? a.F : a.D;
   const bool gated = FIRST && a.gated;
   const int per = gated ? 8 : 16;  // outputs of a unit
-  const int rows = FIRST ? a.F : a.D;
-  const int units = (rows + per - 1) / per;
-  const int total = r.count * units;
+  const int blocks = (rows + per - 1) / per, splits = FIRST ? 1 : a.splits;
+  const int run = FIRST ? K : a.run;  // of K, of one split
+  const int steps = (run + kWarps * kPiece - 1) / (kWarps * kPiece);
+  const int units = r.entries * splits * blocks;
+  const int mine = units > static_cast<int>(blockIdx.x) ? (units - static_cast<int>(blockIdx.x) - 1) / static_cast<int>(gridDim.x) + 1 : 0;
   const uint16_t* W = FIRST ? a.W1 : a.W2;
   const int64_t ldw = FIRST ? a.ldw1 : a.ldw2;
-  const int64_t expert_rows = FIRST && gated ? 2 * static_cast<int64_t>(a.F) : rows;
-  int held = -1;
-  for (int u = blockIdx.x; u < total; u += gridDim.x) {
-    const int at = u / units, n0 = (u - at * units) * per;
-    if (at != held) {
-      find_slots(r, a, r.active[at]);
-      held = at;
-    }
-    const int expert = r.active[at], count = r.rows;
+  const int64_t expert_rows = gated ? 2 * static_cast<int64_t>(rows) : rows;
+
+  struct Unit {
+    int entry, split, n0;
+  };
+  auto unit_of = [&](int i) {
+    const int u = static_cast<int>(blockIdx.x) + i * static_cast<int>(gridDim.x);
+    const int at = u / blocks;
+    return Unit{at / splits, at % splits, (u - at * blocks) * per};
+  };
+
+  // What is fetched: step fs of the block's unit fi.
+  int fi = 0, fs = 0, fk = 0, fend = 0;
+  const uint16_t *w0 = nullptr, *w1 = nullptr, *x[MT];
+  auto begin_unit = [&]() {
+    const Unit u = unit_of(fi);
+    const auto& e = r.entry[u.entry];
     // rows past the end are computed as copies of the last one and not stored
-    const uint16_t* base = W + expert * expert_rows * ldw;
-    const int64_t row0 = min(n0 + g, rows - 1);
-    const int64_t row1 = gated ? row0 + a.F : min(n0 + g + 8, rows - 1);
-    const uint16_t *w0 = base + row0 * ldw, *w1 = base + row1 * ldw;
-    const uint16_t* x[MT];
+    const uint16_t* base = W + e.expert * expert_rows * ldw;
+    const int row0 = min(u.n0 + g, rows - 1), row1 = min(u.n0 + g + 8, rows - 1);
+    w0 = base + row0 * ldw;
+    w1 = base + (gated ? row0 + static_cast<int64_t>(rows) : row1) * ldw;
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      const int slot = 8 * i + g < count ? r.slots[8 * i + g] : -1;
+      const int slot = 8 * i + g < e.count ? r.list[e.first + 8 * i + g] : -1;
       x[i] = slot < 0 ? nullptr : FIRST ? a.X + slot / a.k * a.ldx : a.ws_h + slot * a.ldh;
     }
-    float acc[MT][4] = {};
-    for (int k = warp * kPiece + 8 * t; k - 8 * t < K; k += kWarps * kPiece) {
-      const uint4 a0 = load_piece<VEC>(w0, k, K, true), a1 = load_piece<VEC>(w1, k, K, true);
+    fk = u.split * run + warp * kPiece + 8 * t;
+    fend = min(u.split * run + run, K);
+    fs = 0;
+  };
+  uint4 a0[AHEAD], a1[AHEAD], b[AHEAD][MT];
+  auto fetch_tokens = [&](int j, int k) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        if (8 * i >= count) break;
-        const uint4 b = x[i] ? load_piece<VEC>(x[i], k, K, false) : make_uint4(0u, 0u, 0u, 0u);
-        mma_16816(acc[i], a0.x, a1.x, a0.y, a1.y, b.x, b.y);
-        mma_16816(acc[i], a0.z, a1.z, a0.w, a1.w, b.z, b.w);
+    for (int i = 0; i < MT; ++i)
+      b[j][i] = x[i] ? load_piece<VEC>(x[i], k, fend, false) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  auto fetch = [&](int j, bool tokens) {
+    if (fi >= mine) return;
+    a0[j] = load_piece<VEC>(w0, fk, fend, true);
+    a1[j] = load_piece<VEC>(w1, fk, fend, true);
+    if (tokens) fetch_tokens(j, fk);
+    fk += kWarps * kPiece;
+    if (++fs == steps && ++fi < mine) begin_unit();
+  };
+  if constexpr (FIRST) {
+    if (mine > 0) begin_unit();
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) fetch(j, true);
+  } else {
+    if (mine > 0) begin_unit();
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) fetch(j, false);
+    grid_dependency_wait();
+    grid_launch_dependents();
+    fi = 0;
+    if (mine > 0) begin_unit();
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j)
+      if (fi < mine) {
+        fetch_tokens(j, fk);
+        fk += kWarps * kPiece;
+        if (++fs == steps && ++fi < mine) begin_unit();
       }
-    }
-    __syncthreads();  // the unit before has been added up
+  }
+
+  float acc[MT][4] = {};
+  int ci = 0, cs = 0;
+  auto finish_unit = [&]() {
+    const Unit u = unit_of(ci);
+    const auto& e = r.entry[u.entry];
+    float* part = parts + (ci & 1) * ProductCfg<MT>::PART + warp * (8 * MT * 17);
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      part[warp][8 * i + 2 * t][g] = acc[i][0];
-      part[warp][8 * i + 2 * t + 1][g] = acc[i][1];
-      part[warp][8 * i + 2 * t][g + 8] = acc[i][2];
-      part[warp][8 * i + 2 * t + 1][g + 8] = acc[i][3];
+      part[(8 * i + 2 * t) * 17 + g] = acc[i][0];
+      part[(8 * i + 2 * t + 1) * 17 + g] = acc[i][1];
+      part[(8 * i + 2 * t) * 17 + g + 8] = acc[i][2];
+      part[(8 * i + 2 * t + 1) * 17 + g + 8] = acc[i][3];
+      acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
     }
+    // (the other buffer next: it has been read by all who pass this barrier)
     __syncthreads();
-    for (int i = threadIdx.x; i < count * per; i += kThreads) {
-      const int row = i / per, f = i - row * per, n = n0 + f;
+    part = parts + (ci & 1) * ProductCfg<MT>::PART;
+    for (int i = threadIdx.x; i < e.count * per; i += kThreads) {
+      const int row = i / per, f = i - row * per, n = u.n0 + f;
       if (n >= rows) continue;
-      const int slot = r.slots[row];
-      float v = part[0][row][f];
+      const int slot = r.list[e.first + row];
+      auto sum = [&](int at) {
+        float v = part[row * 17 + at];
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) v += part[w][row][f];
+        for (int w = 1; w < kWarps; ++w) v += part[w * (8 * MT * 17) + row * 17 + at];
+        return v;
+      };
+      float v = sum(f);
       if constexpr (FIRST) {
-        const uint16_t* b = a.b1 ? a.b1 + expert * expert_rows : nullptr;
-        if (b) v += half_at(b, n);
+        const uint16_t* bias = a.b1 ? a.b1 + e.expert * expert_rows : nullptr;
+        if (bias) v += half_at(bias, n);
         v = activate(v, a.act);
         if (gated) {
-          float up = part[0][row][f + 8];
-#pragma unroll
-          for (int w = 1; w < kWarps; ++w) up += part[w][row][f + 8];
-          if (b) up += half_at(b, a.F + n);
+          float up = sum(f + 8);
+          if (bias) up += half_at(bias, rows + n);
           v *= up;
         }
         if (HG_DBG_INDEX(n, a.F)) a.ws_h[slot * a.ldh + n] = __half_as_ushort(__float2half_rn(v));
       } else {
-        if (HG_DBG_INDEX(n, a.D)) a.ws_out[slot * a.ldo + n] = v;
+        if (HG_DBG_INDEX(n, a.D))
+          a.ws_out[(static_cast<int64_t>(u.split) * a.M * a.k + slot) * a.ldo + n] = v;
       }
+    }
+    ++ci;
+    cs = 0;
+  };
+  while (ci < mine) {
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      if (ci >= mine) break;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        mma_16816(acc[i], a0[j].x, a1[j].x, a0[j].y, a1[j].y, b[j][i].x, b[j][i].y);
+        mma_16816(acc[i], a0[j].z, a1[j].z, a0[j].w, a1[j].w, b[j][i].z, b[j][i].w);
+      }
+      fetch(j, true);
+      if (++cs == steps) finish_unit();
     }
   }
 }
@@ -293,7 +414,8 @@ __global__ void __launch_bounds__(kThreads) experts_sum_kernel(const ExpertsArgs
   float y = a.R ? half_at(a.R, m * a.ldr + d) : 0.f;
   for (int j = 0; j < a.k; ++j) {
     const int slot = m * a.k + j;
-    float v = a.F > 0 ? a.ws_out[slot * a.ldo + d] : 0.f;
+    float v = 0.f;
+    for (int i = 0; i < a.splits; ++i) v += a.ws_out[(static_cast<int64_t>(i) * a.M * a.k + slot) * a.ldo + d];
     if (a.b2) v += half_at(a.b2, static_cast<int64_t>(a.ws_chosen[slot]) * a.D + d);
     y = fmaf(a.ws_share[slot], v, y);
   }
@@ -302,26 +424,66 @@ __global__ void __launch_bounds__(kThreads) experts_sum_kernel(const ExpertsArgs
 
 template <int MT, bool FIRST>
 cudaError_t product_with(const ExpertsArgs& a, bool vec, int num_sms, cudaStream_t stream) {
-  PdlLaunch l(dim3(static_cast<unsigned>(num_sms * 3)), dim3(kThreads), 0, stream);
-  return cudaLaunchKernelEx(&l.cfg, vec ? experts_product_kernel<MT, FIRST, true> : experts_product_kernel<MT, FIRST, false>,
-                            a);
+  static std::atomic<bool> attr_done[64];
+  constexpr int SMEM = ProductCfg<MT>::SMEM_BYTES;
+  auto kern = vec ? experts_product_kernel<MT, FIRST, true> : experts_product_kernel<MT, FIRST, false>;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !attr_done[dev]) {
+    for (auto k : {experts_product_kernel<MT, FIRST, true>, experts_product_kernel<MT, FIRST, false>})
+      if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM)) != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_done[dev] = true;
+  }
+  PdlLaunch l(dim3(static_cast<unsigned>(num_sms * (MT == 1 ? 3 : 2))), dim3(kThreads), SMEM, stream);
+  return cudaLaunchKernelEx(&l.cfg, kern, a);
+}
+
+// Tiles of eight tokens that share a read of an expert's weights: as many as an
+// expert is likely to have. More tokens than that read them again, from L2.
+int token_tiles(const ExpertsArgs& a) {
+  if (a.M <= 8) return 1;
+  return a.M * a.k > 12 * a.E ? 4 : 2;
 }
 
 template <bool FIRST>
 cudaError_t product(const ExpertsArgs& a, bool vec, int num_sms, cudaStream_t stream) {
-  if (a.M <= 8) return product_with<1, FIRST>(a, vec, num_sms, stream);
-  if (a.M <= 16) return product_with<2, FIRST>(a, vec, num_sms, stream);
-  if (a.M <= 32) return product_with<4, FIRST>(a, vec, num_sms, stream);
-  return product_with<8, FIRST>(a, vec, num_sms, stream);
+  switch (token_tiles(a)) {
+    case 1:
+      return product_with<1, FIRST>(a, vec, num_sms, stream);
+    case 2:
+      return product_with<2, FIRST>(a, vec, num_sms, stream);
+    default:
+      return product_with<4, FIRST>(a, vec, num_sms, stream);
+  }
 }
 
 int64_t align16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 
+// The second product's runs of F: enough units to keep every block busy for a
+// few of them, and two steps of the warps each at least.
+constexpr int kUnits = 2048;
+constexpr int kMaxSplits = 16;
+constexpr int kStep = kWarps * kPiece;
+int run_of(int64_t M, int64_t D, int64_t F, int64_t E, int64_t k, int* splits) {
+  const int64_t experts = M * k < E ? M * k : E, blocks = (D + 15) / 16;
+  int64_t want = experts * blocks > 0 ? (kUnits + experts * blocks - 1) / (experts * blocks) : 1;
+  const int64_t most = F / (2 * kStep);
+  want = want > kMaxSplits ? kMaxSplits : want;
+  want = want > most ? most : want;
+  want = want < 1 ? 1 : want;
+  const int64_t run = ((F + want - 1) / want + kStep - 1) / kStep * kStep;
+  *splits = static_cast<int>(run > 0 ? (F + run - 1) / run : 0);
+  return static_cast<int>(run);
+}
+
 }  // namespace
 
 // The choice, its shares, H (rows of whole 16 bytes) and the slots' outputs.
-size_t experts_workspace(int64_t M, int64_t D, int64_t F, int64_t k) {
-  return static_cast<size_t>(2 * align16(4 * M * k) + M * k * align16(2 * F) + M * k * align16(4 * D));
+size_t experts_workspace(int64_t M, int64_t D, int64_t F, int64_t E, int64_t k) {
+  int splits;
+  run_of(M, D, F, E, k, &splits);
+  return static_cast<size_t>(2 * align16(4 * M * k) + M * k * align16(2 * F) + splits * M * k * align16(4 * D));
 }
 
 cudaError_t launch_experts(ExpertsArgs a, void* workspace, int num_sms, cudaStream_t stream) {
@@ -333,16 +495,20 @@ cudaError_t launch_experts(ExpertsArgs a, void* workspace, int num_sms, cudaStre
   a.ldh = align16(2 * static_cast<int64_t>(a.F)) / 2;
   a.ws_out = reinterpret_cast<float*>(ws += slots * a.ldh * 2);
   a.ldo = align16(4 * static_cast<int64_t>(a.D)) / 4;
+  a.run = run_of(a.M, a.D, a.F, a.E, a.k, &a.splits);
   const bool vec_x = a.D % 8 == 0 && rows16(a.X, a.ldx);
   const bool vec_r = vec_x && rows16(a.Wr, a.ldwr), vec1 = vec_x && rows16(a.W1, a.ldw1);
   const bool vec2 = a.F % 8 == 0 && rows16(a.W2, a.ldw2);
   cudaError_t e;
   {
-    PdlLaunch l(dim3(static_cast<unsigned>(a.M)), dim3(kThreads), 0, stream);
+    // a warp per logit, up to eight CTAs of eight
+    a.router_ctas = a.E <= kWarps ? 1 : a.E <= 2 * kWarps ? 2 : a.E <= 4 * kWarps ? 4 : 8;
+    PdlLaunch l(dim3(static_cast<unsigned>(a.M * a.router_ctas)), dim3(kThreads), 0, stream);
+    if (a.router_ctas > 1) l.cluster(static_cast<unsigned>(a.router_ctas));
     e = cudaLaunchKernelEx(&l.cfg, vec_r ? experts_router_kernel<true> : experts_router_kernel<false>, a);
     if (e != cudaSuccess) return e;
   }
-  if (a.F > 0) {
+  if (a.F > 0 && a.D > 0) {
     if ((e = product<true>(a, vec1, num_sms, stream)) != cudaSuccess) return e;
     if ((e = product<false>(a, vec2, num_sms, stream)) != cudaSuccess) return e;
   }

@@ -437,11 +437,13 @@ struct ExpertsArgs {
   float* ws_share;
   uint16_t* ws_h;  // M·k rows
   int64_t ldh;
-  float* ws_out;   // M·k rows
+  float* ws_out;   // [splits][M·k] rows
   int64_t ldo;
+  int splits, run;  // the second product's runs of F, and their length
+  int router_ctas;  // a cluster of the router
 };
 cudaError_t launch_experts(ExpertsArgs a, void* workspace, int num_sms, cudaStream_t stream);
-size_t experts_workspace(int64_t M, int64_t D, int64_t F, int64_t k);
+size_t experts_workspace(int64_t M, int64_t D, int64_t F, int64_t E, int64_t k);
 
 // Address of the device watchdog word on the current device.
 cudaError_t status_word_address(int** addr);
