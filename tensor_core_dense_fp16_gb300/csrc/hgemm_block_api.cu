@@ -512,6 +512,7 @@ int hgemm_experts(const hgemm_half_t* X, int64_t ldx, const hgemm_half_t* Wr, in
   a.ldy = ldy, a.chosen = chosen, a.share = share;
   a.M = static_cast<int>(M), a.D = static_cast<int>(D), a.F = static_cast<int>(F), a.E = static_cast<int>(E);
   a.k = static_cast<int>(k);
+  a.status = dev.status, a.timeout_ns = dev.timeout_ns, a.inject = dev.inject;
   return hg::cuda_status(hg::launch_experts(a, workspace, dev.num_sms, stream));
 }
 

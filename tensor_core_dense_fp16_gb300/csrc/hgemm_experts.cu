@@ -168,6 +168,7 @@ constexpr int kEntries = kMost + kSlots / 8;  // a partly filled one per expert,
 struct Routing {
   unsigned long long tokens[kMost];  // a bit per token that chose the expert
   uint16_t list[kSlots];             // the slots, by entry
+  uint16_t token[kSlots];            // and their tokens
   uint16_t first[kMost];             // where an expert's slots begin in it
   struct {
     uint16_t expert, first;
@@ -178,11 +179,18 @@ struct Routing {
 
 template <int MT>
 __device__ __forceinline__ void find_entries(Routing& r, const ExpertsArgs& a) {
-  for (int e = threadIdx.x; e < a.E; e += kThreads) r.tokens[e] = 0;
-  __syncthreads();
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) r.tokens[e] = 0;
   const int slots = a.M * a.k;
-  for (int i = threadIdx.x; i < slots; i += kThreads)
-    atomicOr(&r.tokens[ld_gpu_s32(a.ws_chosen + i)], 1ull << (i / a.k));
+  int chosen[kSlots / kThreads];
+#pragma unroll
+  for (int j = 0; j < kSlots / kThreads; ++j) {
+    const int i = static_cast<int>(threadIdx.x) + j * kThreads;
+    chosen[j] = threadIdx.x < kThreads && i < slots ? ld_gpu_s32(a.ws_chosen + i) : -1;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kSlots / kThreads; ++j)
+    if (chosen[j] >= 0) atomicOr(&r.tokens[chosen[j]], 1ull << ((static_cast<int>(threadIdx.x) + j * kThreads) / a.k));
   __syncthreads();
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
@@ -213,28 +221,57 @@ __device__ __forceinline__ void find_entries(Routing& r, const ExpertsArgs& a) {
     if (lane == 0) r.entries = n;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < slots; i += kThreads) {
-    const int e = ld_gpu_s32(a.ws_chosen + i);
-    r.list[r.first[e] + __popcll(r.tokens[e] & ((1ull << (i / a.k)) - 1))] = static_cast<uint16_t>(i);
+#pragma unroll
+  for (int j = 0; j < kSlots / kThreads; ++j) {
+    const int i = static_cast<int>(threadIdx.x) + j * kThreads, e = chosen[j];
+    if (e < 0) continue;
+    const int token = i / a.k, at = r.first[e] + __popcll(r.tokens[e] & ((1ull << token) - 1));
+    r.list[at] = static_cast<uint16_t>(i);
+    r.token[at] = static_cast<uint16_t>(token);
   }
   __syncthreads();
 }
 
-template <bool VEC>
-__device__ __forceinline__ uint4 load_piece(const uint16_t* row, int k, int K, bool weights) {
-  if constexpr (VEC) {
-    if (k >= K || !dbg_row(row + k, k, 8, K, 16)) return make_uint4(0u, 0u, 0u, 0u);
-    return weights ? ld_gpu_16(row + k) : load16(row + k);  // (L1 keeps the tokens)
-  } else {
-    uint32_t v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = k + 2 * i < K ? (weights ? ld_gpu_u16(row + k + 2 * i) : row[k + 2 * i]) : 0u;
-      const uint32_t hi = k + 2 * i + 1 < K ? (weights ? ld_gpu_u16(row + k + 2 * i + 1) : row[k + 2 * i + 1]) : 0u;
-      v[i] = lo | hi << 16;
+// What becomes of the sums of one unit: outputs n0 .. n0+per-1 of an entry's
+// slots, `sum(row, column)` over the block's warps. By the threads t of T.
+template <bool FIRST, typename Entry, typename Sum>
+__device__ __forceinline__ void put_unit(const ExpertsArgs& a, const Routing& r, const Entry& e, int split, int n0,
+                                         int per, int rows, int t, int T, Sum sum) {
+  for (int i = t; i < e.count * per; i += T) {
+    const int row = i / per, f = i - row * per, n = n0 + f;
+    if (n >= rows) continue;
+    const int slot = r.list[e.first + row];
+    float v = sum(row, f);
+    if constexpr (FIRST) {
+      const uint16_t* bias = a.b1 ? a.b1 + e.expert * (a.gated ? 2 : 1) * static_cast<int64_t>(rows) : nullptr;
+      if (bias) v += half_at(bias, n);
+      v = activate(v, a.act);
+      if (a.gated) {
+        float up = sum(row, f + 8);
+        if (bias) up += half_at(bias, rows + n);
+        v *= up;
+      }
+      if (HG_DBG_INDEX(n, a.F)) a.ws_h[slot * a.ldh + n] = __half_as_ushort(__float2half_rn(v));
+    } else {
+      if (HG_DBG_INDEX(n, a.D)) a.ws_out[(static_cast<int64_t>(split) * a.M * a.k + slot) * a.ldo + n] = v;
     }
-    return make_uint4(v[0], v[1], v[2], v[3]);
   }
+}
+
+// The 16 bytes at k of a row of any alignment, what lies at or past K zero.
+__device__ __forceinline__ uint4 load_piece(const uint16_t* row, int k, int K, bool weights) {
+  uint32_t v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t h[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int at = k + 2 * i + j;
+      h[j] = at < K && HG_DBG_INDEX(at, K) ? (weights ? ld_gpu_u16(row + at) : row[at]) : 0u;
+    }
+    v[i] = h[0] | h[1] << 16;
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
 // FIRST: a unit of work is features 8u .. 8u+7 and their gates (gated) or
@@ -252,10 +289,10 @@ struct ProductCfg {
   static constexpr int SMEM_BYTES = 2 * PART * 4 + static_cast<int>(sizeof(Routing));
 };
 
-template <int MT, bool FIRST, bool VEC>
+template <int MT, bool FIRST>
 __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) experts_product_kernel(const ExpertsArgs a) {
   constexpr int AHEAD = ProductCfg<MT>::AHEAD;
-  extern __shared__ __align__(16) uint8_t experts_smem[];
+  extern __shared__ __align__(128) uint8_t experts_smem[];
   float* parts = reinterpret_cast<float*>(experts_smem);
   Routing& r = *reinterpret_cast<Routing*>(experts_smem + 2 * ProductCfg<MT>::PART * 4);
   if constexpr (FIRST) {
@@ -312,12 +349,12 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) experts_product_ker
   auto fetch_tokens = [&](int j, int k) {
 #pragma unroll
     for (int i = 0; i < MT; ++i)
-      b[j][i] = x[i] ? load_piece<VEC>(x[i], k, fend, false) : make_uint4(0u, 0u, 0u, 0u);
+      b[j][i] = x[i] ? load_piece(x[i], k, fend, false) : make_uint4(0u, 0u, 0u, 0u);
   };
   auto fetch = [&](int j, bool tokens) {
     if (fi >= mine) return;
-    a0[j] = load_piece<VEC>(w0, fk, fend, true);
-    a1[j] = load_piece<VEC>(w1, fk, fend, true);
+    a0[j] = load_piece(w0, fk, fend, true);
+    a1[j] = load_piece(w1, fk, fend, true);
     if (tokens) fetch_tokens(j, fk);
     fk += kWarps * kPiece;
     if (++fs == steps && ++fi < mine) begin_unit();
@@ -360,32 +397,12 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) experts_product_ker
     // (the other buffer next: it has been read by all who pass this barrier)
     __syncthreads();
     part = parts + (ci & 1) * ProductCfg<MT>::PART;
-    for (int i = threadIdx.x; i < e.count * per; i += kThreads) {
-      const int row = i / per, f = i - row * per, n = u.n0 + f;
-      if (n >= rows) continue;
-      const int slot = r.list[e.first + row];
-      auto sum = [&](int at) {
-        float v = part[row * 17 + at];
+    put_unit<FIRST>(a, r, e, u.split, u.n0, per, rows, threadIdx.x, kThreads, [&](int row, int column) {
+      float v = part[row * 17 + column];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) v += part[w * (8 * MT * 17) + row * 17 + at];
-        return v;
-      };
-      float v = sum(f);
-      if constexpr (FIRST) {
-        const uint16_t* bias = a.b1 ? a.b1 + e.expert * expert_rows : nullptr;
-        if (bias) v += half_at(bias, n);
-        v = activate(v, a.act);
-        if (gated) {
-          float up = sum(f + 8);
-          if (bias) up += half_at(bias, rows + n);
-          v *= up;
-        }
-        if (HG_DBG_INDEX(n, a.F)) a.ws_h[slot * a.ldh + n] = __half_as_ushort(__float2half_rn(v));
-      } else {
-        if (HG_DBG_INDEX(n, a.D))
-          a.ws_out[(static_cast<int64_t>(u.split) * a.M * a.k + slot) * a.ldo + n] = v;
-      }
-    }
+      for (int w = 1; w < kWarps; ++w) v += part[w * (8 * MT * 17) + row * 17 + column];
+      return v;
+    });
     ++ci;
     cs = 0;
   };
@@ -404,46 +421,316 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) experts_product_ker
   }
 }
 
-// Y = Σ s·(output + b2) + R, the choices in order.
+// The same products for rows that 16-byte copies can describe. Eight warps
+// multiply and a ninth adds their sums up, so that none of the eight waits for
+// the others at a unit's end. A lane's pieces pass through a queue of its own
+// in shared memory, filled by asynchronous copies: registers hold four pieces
+// at most before a warp's scoreboards, six, make it wait for the youngest load
+// instead of the oldest. What a lane copies only that lane reads, so that
+// nothing but its own copies is waited for. A step is two pieces, 64 values of
+// K per warp and 128 bytes of a row.
+template <int MT>
+struct QueueCfg {
+  static constexpr int CTAS = MT == 4 ? 1 : 2;  // per SM
+  static constexpr int DEPTH = MT == 1 ? 2 : MT == 2 ? 2 : 3;
+  static constexpr int BUFFERS = MT == 1 ? 4 : 2;    // of partial sums
+  static constexpr int SLOT = (2 + MT) * 1024;       // of a warp: a step's rows and tokens
+  static constexpr int PART = kWarps * 8 * MT * 17;  // floats of one buffer
+  static constexpr int OFF_ROUTING = BUFFERS * PART * 4;
+  static constexpr int OFF_BAR = (OFF_ROUTING + static_cast<int>(sizeof(Routing)) + 15) / 16 * 16;
+  static constexpr int OFF_MISC = OFF_BAR + 2 * 8 * BUFFERS;
+  static constexpr int OFF_QUEUE = (OFF_MISC + 4 + 15) / 16 * 16;
+  static constexpr int SMEM_BYTES = OFF_QUEUE + kWarps * DEPTH * SLOT;
+  static_assert(CTAS * (SMEM_BYTES + 1024) <= 233472, "the CTAs fit an SM");
+};
+
+template <int MT, bool FIRST>
+__global__ void __launch_bounds__(kThreads + 32, QueueCfg<MT>::CTAS) experts_queue_kernel(const ExpertsArgs a) {
+  using Cfg = QueueCfg<MT>;
+  constexpr int DEPTH = Cfg::DEPTH, STEP = kWarps * 2 * kPiece;  // values of K per step
+  extern __shared__ __align__(128) uint8_t experts_smem[];
+  float* parts = reinterpret_cast<float*>(experts_smem);
+  Routing& r = *reinterpret_cast<Routing*>(experts_smem + Cfg::OFF_ROUTING);
+  const uint32_t full0 = smem_u32(experts_smem + Cfg::OFF_BAR), empty0 = full0 + 8u * Cfg::BUFFERS;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(experts_smem + Cfg::OFF_MISC);
+  const Watchdog wd{abort_flag, a.status, a.timeout_ns};
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < Cfg::BUFFERS; ++i) {
+      mbar_init(full0 + 8u * i, kWarps);
+      mbar_init(empty0 + 8u * i, 1);
+    }
+  }
+  if constexpr (FIRST) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+  } else {
+    fence_gpu();
+  }
+  find_entries<MT>(r, a);  // (its barriers publish these)
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int K = FIRST ? a.D : a.F, rows = FIRST ? a.F : a.D;
+  const bool gated = FIRST && a.gated;
+  const int per = gated ? 8 : 16;  // outputs of a unit
+  const int blocks = (rows + per - 1) / per, splits = FIRST ? 1 : a.splits;
+  const int run = FIRST ? K : a.run;  // of K, of one split
+  // The block's units, every gridDim.x-th of blocks × splits × entries, without
+  // a division from one to the next: a warp that does not multiply does not
+  // refill its queue either (M = 1, D 2048, F 16384: 66 us with, XXX without).
+  const int entries = r.entries;
+  const int block_step = static_cast<int>(gridDim.x) % blocks, rest = static_cast<int>(gridDim.x) / blocks;
+  const int split_step = rest % splits, entry_step = rest / splits;
+  struct Unit {
+    int block, split, entry;
+  };
+  const Unit first{static_cast<int>(blockIdx.x) % blocks, static_cast<int>(blockIdx.x) / blocks % splits,
+                   static_cast<int>(blockIdx.x) / blocks / splits};
+  auto advance = [&](Unit& u) {
+    u.block += block_step;
+    u.split += split_step;
+    u.entry += entry_step;
+    if (u.block >= blocks) u.block -= blocks, ++u.split;
+    if (u.split >= splits) u.split -= splits, ++u.entry;
+  };
+  // (of K: at least one value)
+  auto k_end = [&](const Unit& u) { return min(u.split * run + run, K); };
+  auto steps_of = [&](const Unit& u) { return (k_end(u) - u.split * run + STEP - 1) / STEP; };
+  int buffer = 0;
+  uint32_t phase = 0;
+  auto next_buffer = [&]() {
+    if (++buffer == Cfg::BUFFERS) {
+      buffer = 0;
+      phase ^= 1u;
+    }
+  };
+
+  if (warp == kWarps) {
+    // ---- the warp that adds up. (A wait that gives up has raised the abort
+    // flag: later waits give up at once, and the loops run out.)
+    if constexpr (!FIRST) {
+      grid_dependency_wait();
+      grid_launch_dependents();
+    }
+    for (Unit u = first; u.entry < entries; advance(u)) {
+      (void)wait_phase(full0 + 8u * buffer, phase, wd, kWdReduce);
+      const float* part = parts + buffer * Cfg::PART;
+      put_unit<FIRST>(a, r, r.entry[u.entry], u.split, u.block * per, per, rows, lane, 32, [&](int row, int column) {
+        float v = part[row * 17 + column];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) v += part[w * (8 * MT * 17) + row * 17 + column];
+        return v;
+      });
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty0 + 8u * buffer);
+      next_buffer();
+    }
+    return;
+  }
+
+  // ---- the eight warps that multiply
+  const int g = lane >> 2, t = lane & 3;
+  const uint16_t* W = FIRST ? a.W1 : a.W2;
+  const int64_t ldw = FIRST ? a.ldw1 : a.ldw2;
+  const int64_t expert_rows = gated ? 2 * static_cast<int64_t>(rows) : rows;
+  uint8_t* queue = experts_smem + Cfg::OFF_QUEUE + warp * (DEPTH * Cfg::SLOT) + 16 * lane;
+  const uint32_t queue_addr = smem_u32(queue);
+  // What is copied next: unit fu, fsteps steps of it left, the next at fk of
+  // these rows.
+  Unit fu = first;
+  int fsteps = 0, fk = 0, fend = 0;
+  const uint16_t *w0 = nullptr, *w1 = nullptr, *x[MT];
+  auto begin_unit = [&]() {
+    if (fu.entry >= entries) return;
+    const auto& e = r.entry[fu.entry];
+    const int n0 = fu.block * per;
+    fk = fu.split * run + warp * 2 * kPiece + 8 * t;
+    fend = k_end(fu);
+    fsteps = steps_of(fu);
+    // rows past the end are computed as copies of the last one and not stored
+    const uint16_t* base = W + e.expert * expert_rows * ldw + fk;
+    const int row0 = min(n0 + g, rows - 1), row1 = min(n0 + g + 8, rows - 1);
+    w0 = base + row0 * ldw;
+    w1 = base + (gated ? row0 + static_cast<int64_t>(rows) : row1) * ldw;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const int row = e.first + 8 * i + g;
+      x[i] = 8 * i + g >= e.count ? nullptr : (FIRST ? a.X + r.token[row] * a.ldx : a.ws_h + r.list[row] * a.ldh) + fk;
+    }
+  };
+  // (past the end zeros; where there is no token nothing: a column of its own)
+  auto copy = [&](uint32_t to, const uint16_t* p, bool weights) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const bool in = fk + kPiece * i < fend && dbg_row(p + kPiece * i, fk + kPiece * i, 8, fend, 16);
+      if (weights)
+        cp_async_16(to + 512u * i, in ? p + kPiece * i : W, in ? 16 : 0);
+      else
+        cp_async_16_shared(to + 512u * i, in ? p + kPiece * i : W, in ? 16 : 0);
+    }
+  };
+  auto copy_weights = [&](int into) {
+    const uint32_t to = queue_addr + static_cast<uint32_t>(into * Cfg::SLOT);
+    copy(to, w0, true);
+    copy(to + 1024, w1, true);
+  };
+  auto copy_tokens = [&](int into) {
+    const uint32_t to = queue_addr + static_cast<uint32_t>(into * Cfg::SLOT) + 2048;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+      if (x[i]) copy(to + 1024u * i, x[i], false);
+  };
+  auto next_step = [&]() {
+    if (--fsteps > 0) {
+      fk += STEP;
+      w0 += STEP;
+      w1 += STEP;
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        if (x[i]) x[i] += STEP;
+    } else {
+      advance(fu);
+      begin_unit();
+    }
+  };
+  begin_unit();
+  if constexpr (!FIRST) {
+    // the first steps' weights, before the tokens' values are there
+    for (int j = 0; j < DEPTH && fu.entry < entries; ++j) {
+      copy_weights(j);
+      next_step();
+    }
+    grid_dependency_wait();
+    grid_launch_dependents();
+    fu = first;
+    begin_unit();
+  }
+  for (int j = 0; j < DEPTH; ++j) {
+    if (fu.entry < entries) {
+      if (FIRST) copy_weights(j);
+      copy_tokens(j);
+      next_step();
+    }
+    cp_async_commit();
+  }
+
+  int slot = 0, done = 0;
+  for (Unit u = first; u.entry < entries; advance(u)) {
+    const int steps = steps_of(u), count = r.entry[u.entry].count;
+    float acc[MT][4] = {};
+    for (int s = 0; s < steps; ++s) {
+      cp_async_wait<DEPTH - 1>();
+      const uint4* at = reinterpret_cast<const uint4*>(queue + slot * Cfg::SLOT);  // 512 bytes: 32 of these
+      uint4 p[2][2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        p[i][0] = at[32 * i];
+        p[i][1] = at[64 + 32 * i];
+      }
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        if (8 * j >= count) break;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint4 b = at[128 + 64 * j + 32 * i];
+          mma_16816(acc[j], p[i][0].x, p[i][1].x, p[i][0].y, p[i][1].y, b.x, b.y);
+          mma_16816(acc[j], p[i][0].z, p[i][1].z, p[i][0].w, p[i][1].w, b.z, b.w);
+        }
+      }
+      if (fu.entry < entries) {
+        copy_weights(slot);
+        copy_tokens(slot);
+        next_step();
+      }
+      cp_async_commit();
+      if (++slot == DEPTH) slot = 0;
+    }
+    if (done++ >= Cfg::BUFFERS) (void)wait_phase(empty0 + 8u * buffer, phase ^ 1u, wd, kWdReduce);
+    float* part = parts + buffer * Cfg::PART + warp * (8 * MT * 17);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      float* q = part + (8 * i + 2 * t) * 17 + g;
+      q[0] = acc[i][0];
+      q[17] = acc[i][1];
+      q[8] = acc[i][2];
+      q[17 + 8] = acc[i][3];
+    }
+    __syncwarp();
+    if (lane == 0 && !(a.inject == 1 && done == 1 && warp == 0))  // testing aid: withhold one arrival
+      mbar_arrive(full0 + 8u * buffer);
+    next_buffer();
+  }
+  cp_async_wait<0>();  // (nothing is under way any more but empty groups)
+}
+
+// Y = Σ s·(output + b2) + R, the choices in order, a choice's runs of F in
+// order. A thread asks for four choices' values at once.
 __global__ void __launch_bounds__(kThreads) experts_sum_kernel(const ExpertsArgs a) {
   grid_dependency_wait();
   grid_launch_dependents();
   const int m = blockIdx.y;
   const int64_t d = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   if (d >= a.D || !HG_DBG_INDEX(m, a.M)) return;
-  float y = a.R ? half_at(a.R, m * a.ldr + d) : 0.f;
-  for (int j = 0; j < a.k; ++j) {
-    const int slot = m * a.k + j;
-    float v = 0.f;
-    for (int i = 0; i < a.splits; ++i) v += a.ws_out[(static_cast<int64_t>(i) * a.M * a.k + slot) * a.ldo + d];
-    if (a.b2) v += half_at(a.b2, static_cast<int64_t>(a.ws_chosen[slot]) * a.D + d);
-    y = fmaf(a.ws_share[slot], v, y);
+  const float residual = a.R ? half_at(a.R, m * a.ldr + d) : 0.f;
+  const float* out = a.ws_out + static_cast<int64_t>(m) * a.k * a.ldo + d;
+  const int64_t split = static_cast<int64_t>(a.M) * a.k * a.ldo;
+  float y = 0.f;
+  for (int j0 = 0; j0 < a.k; j0 += 4) {
+    float v[4], s[4], bias[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = s[j] = bias[j] = 0.f;
+      if (j0 + j >= a.k) continue;
+      const int slot = m * a.k + j0 + j;
+      s[j] = a.ws_share[slot];
+      if (a.b2) bias[j] = half_at(a.b2, static_cast<int64_t>(a.ws_chosen[slot]) * a.D + d);
+    }
+#pragma unroll 4
+    for (int i = 0; i < a.splits; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j0 + j < a.k) v[j] += out[i * split + (j0 + j) * a.ldo];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j0 + j < a.k) y = fmaf(s[j], v[j] + bias[j], y);
   }
-  a.Y[m * a.ldy + d] = __half_as_ushort(__float2half_rn(y));
+  a.Y[m * a.ldy + d] = __half_as_ushort(__float2half_rn(y + residual));
+}
+
+template <typename Kernel>
+cudaError_t allow_smem(Kernel kern, int bytes, std::atomic<bool> (&done)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !done[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+  }
+  return e;
 }
 
 template <int MT, bool FIRST>
 cudaError_t product_with(const ExpertsArgs& a, bool vec, int num_sms, cudaStream_t stream) {
-  static std::atomic<bool> attr_done[64];
-  constexpr int SMEM = ProductCfg<MT>::SMEM_BYTES;
-  auto kern = vec ? experts_product_kernel<MT, FIRST, true> : experts_product_kernel<MT, FIRST, false>;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || !attr_done[dev]) {
-    for (auto k : {experts_product_kernel<MT, FIRST, true>, experts_product_kernel<MT, FIRST, false>})
-      if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM)) != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) attr_done[dev] = true;
+  static std::atomic<bool> done[2][64];
+  cudaError_t e;
+  if (vec) {
+    using Cfg = QueueCfg<MT>;
+    auto kern = experts_queue_kernel<MT, FIRST>;
+    if ((e = allow_smem(kern, Cfg::SMEM_BYTES, done[0])) != cudaSuccess) return e;
+    PdlLaunch l(dim3(static_cast<unsigned>(num_sms * Cfg::CTAS)), dim3(kThreads + 32), Cfg::SMEM_BYTES, stream);
+    return cudaLaunchKernelEx(&l.cfg, kern, a);
   }
-  PdlLaunch l(dim3(static_cast<unsigned>(num_sms * (MT == 1 ? 3 : 2))), dim3(kThreads), SMEM, stream);
+  auto kern = experts_product_kernel<MT, FIRST>;
+  if ((e = allow_smem(kern, ProductCfg<MT>::SMEM_BYTES, done[1])) != cudaSuccess) return e;
+  PdlLaunch l(dim3(static_cast<unsigned>(num_sms * (MT == 1 ? 3 : 2))), dim3(kThreads), ProductCfg<MT>::SMEM_BYTES,
+              stream);
   return cudaLaunchKernelEx(&l.cfg, kern, a);
 }
 
 // Tiles of eight tokens that share a read of an expert's weights: as many as an
 // expert is likely to have. More tokens than that read them again, from L2.
 int token_tiles(const ExpertsArgs& a) {
-  if (a.M <= 8) return 1;
-  return a.M * a.k > 12 * a.E ? 4 : 2;
+  if (a.M <= 8 || a.M * a.k <= 8 * a.E) return 1;
+  return a.M * a.k > 16 * a.E ? 4 : 2;
 }
 
 template <bool FIRST>
@@ -461,14 +748,14 @@ cudaError_t product(const ExpertsArgs& a, bool vec, int num_sms, cudaStream_t st
 int64_t align16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 
 // The second product's runs of F: enough units to keep every block busy for a
-// few of them, and two steps of the warps each at least.
-constexpr int kUnits = 2048;
+// few of them, and a step of the warps each at least.
+constexpr int kUnits = 1024;
 constexpr int kMaxSplits = 16;
-constexpr int kStep = kWarps * kPiece;
+constexpr int kStep = kWarps * 2 * kPiece;
 int run_of(int64_t M, int64_t D, int64_t F, int64_t E, int64_t k, int* splits) {
   const int64_t experts = M * k < E ? M * k : E, blocks = (D + 15) / 16;
   int64_t want = experts * blocks > 0 ? (kUnits + experts * blocks - 1) / (experts * blocks) : 1;
-  const int64_t most = F / (2 * kStep);
+  const int64_t most = F / kStep;
   want = want > kMaxSplits ? kMaxSplits : want;
   want = want > most ? most : want;
   want = want < 1 ? 1 : want;

@@ -441,6 +441,9 @@ struct ExpertsArgs {
   int64_t ldo;
   int splits, run;  // the second product's runs of F, and their length
   int router_ctas;  // a cluster of the router
+  int* status;      // device watchdog word
+  unsigned long long timeout_ns;
+  int inject;       // HGEMM_INJECT_* (testing the watchdog)
 };
 cudaError_t launch_experts(ExpertsArgs a, void* workspace, int num_sms, cudaStream_t stream);
 size_t experts_workspace(int64_t M, int64_t D, int64_t F, int64_t E, int64_t k);

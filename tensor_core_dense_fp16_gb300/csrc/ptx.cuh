@@ -172,6 +172,11 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, int s
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes)
                : "memory");
 }
+// The same through L1, for what other copies of this SM read again.
+__device__ __forceinline__ void cp_async_16_shared(uint32_t dst, const void *src, int src_bytes) {
+  if (!HG_DBG_SMEM(dst, 16) || !HG_DBG_ALIGN(src, 16)) return;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Waits until at most N of this thread's committed copy groups are pending.
 template <int N>
