@@ -190,7 +190,7 @@ template <bool VEC>
 __device__ __forceinline__ void adamw_eight(const AdamwEntry& t, const AdamwStep& s, const Scalars& c, float keep,
                                             int64_t first) {
   const int64_t n = t.n;
-  const bool in = first < n;  // VEC: all eight, n is a multiple of 8
+  const bool in = first < n;  // VEC: all eight, the chunks hold whole eights
   const bool eight = !VEC && t.ms != nullptr;  // (VEC: adamw_bytes)
   float g[8] = {}, m[8] = {}, v[8] = {}, p[8] = {};
   if (in && HG_DBG_INDEX(VEC ? first + 7 : first, n)) {
@@ -282,7 +282,7 @@ __device__ __forceinline__ void unpack_wide(const uint4 (&w)[WIDE ? 2 : 1], floa
 template <bool G32, bool MASTER>
 __device__ __forceinline__ void adamw_bytes(const AdamwEntry& t, const AdamwStep& s, const Scalars& c, float keep,
                                             int64_t first, int count) {
-  const int64_t n = t.n;
+  const int64_t n = t.n;  // a multiple of 8, or past all these chunks
   uint8_t *tm = static_cast<uint8_t*>(t.m), *tv = static_cast<uint8_t*>(t.v);
   auto load = [&](int64_t i) {
     const int64_t at = i < n ? i : 0;  // (past the end: anything, not stored)
@@ -303,11 +303,10 @@ __device__ __forceinline__ void adamw_bytes(const AdamwEntry& t, const AdamwStep
   };
   const int lane = threadIdx.x & 31, role = lane & 7;
   Packed<G32, MASTER> next = load(first);
-  // (whole warps: a chunk's first value decides)
-  for (int i = 0; i < count && first - 8 * static_cast<int>(threadIdx.x) < n; ++i, first += kChunk) {
+  for (int i = 0; i < count; ++i, first += kChunk) {
     const Packed<G32, MASTER> r = next;
     if (i + 1 < count) next = load(first + kChunk);
-    const bool in = first < n;  // all eight, n is a multiple of 8
+    const bool in = first < n;  // all eight
     float g[8], p[8], m[8], v[8];
     unpack_wide<G32>(r.g, g);
     unpack_wide<MASTER>(r.p, p);
@@ -396,22 +395,25 @@ __global__ void __launch_bounds__(kThreads, 3) adamw_kernel(const __grid_constan
     const AdamwEntry& t = table.t[lo];
     int64_t first = static_cast<int64_t>(chunk - t.chunk0) * kChunk * table.per;
     const float keep = c.dynamic ? fmaf(-c.lr, t.decay, 1.f) : t.keep;
-    if (t.vec && t.ms) {
-      first += 8 * static_cast<int>(threadIdx.x);
-      if (t.grad_type == 0)
-        t.master ? adamw_bytes<false, true>(t, s, c, keep, first, table.per)
-                 : adamw_bytes<false, false>(t, s, c, keep, first, table.per);
-      else
-        t.master ? adamw_bytes<true, true>(t, s, c, keep, first, table.per)
-                 : adamw_bytes<true, false>(t, s, c, keep, first, table.per);
-      continue;
+    // Chunks of whole eights where the pointers allow it; a tensor whose size is
+    // no multiple of eight ends in a chunk moved value by value.
+    const int64_t whole = !t.vec ? 0 : t.n % 8 == 0 ? t.n : t.n / kChunk * kChunk;
+    int done = 0;
+    if (first < whole) {
+      const int64_t left = (whole - first + kChunk - 1) / kChunk;
+      done = left < table.per ? static_cast<int>(left) : table.per;
+      const int64_t at = first + 8 * static_cast<int>(threadIdx.x);
+      if (!t.ms) {
+        for (int i = 0; i < done; ++i) adamw_eight<true>(t, s, c, keep, at + i * kChunk);
+      } else if (t.grad_type == 0) {
+        t.master ? adamw_bytes<false, true>(t, s, c, keep, at, done) : adamw_bytes<false, false>(t, s, c, keep, at, done);
+      } else {
+        t.master ? adamw_bytes<true, true>(t, s, c, keep, at, done) : adamw_bytes<true, false>(t, s, c, keep, at, done);
+      }
     }
-    for (int i = 0; i < table.per && first < t.n; ++i, first += kChunk) {
-      if (t.vec)
-        adamw_eight<true>(t, s, c, keep, first + 8 * static_cast<int>(threadIdx.x));
-      else
-        adamw_eight<false>(t, s, c, keep, first + (threadIdx.x >> 5) * 256 + (threadIdx.x & 31));
-    }
+    first += static_cast<int64_t>(done) * kChunk;
+    for (int i = done; i < table.per && first < t.n; ++i, first += kChunk)
+      adamw_eight<false>(t, s, c, keep, first + (threadIdx.x >> 5) * 256 + (threadIdx.x & 31));
   }
 }
 

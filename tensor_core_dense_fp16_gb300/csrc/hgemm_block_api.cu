@@ -431,7 +431,7 @@ int hgemm_adamw(const hgemm_adamw_tensor* tensors, int64_t count, double lr, dou
     if (i == count || tensors[i].n == 0) continue;
     const hgemm_adamw_tensor& x = tensors[i];
     const uintptr_t state = x.m_scales ? 8 : 16;
-    const bool vec8 = x.n % 8 == 0 && aligned(x.weight, 16) && aligned(x.master, 16) && aligned(x.grad, 16) &&
+    const bool vec8 = aligned(x.weight, 16) && aligned(x.master, 16) && aligned(x.grad, 16) &&
                       aligned(x.m, state) && aligned(x.v, state);
     e[n++] = hg::AdamwEntry{x.weight, x.master, x.grad, x.m, x.v, x.m_scales, x.v_scales, x.n, x.weight_decay,
                             static_cast<float>(1.0 - lr * x.weight_decay), chunks,

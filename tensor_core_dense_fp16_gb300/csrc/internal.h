@@ -399,7 +399,7 @@ struct AdamwEntry {
   float decay, keep;  // weight_decay and 1 − lr·weight_decay
   uint32_t chunk0;
   int16_t grad_type;
-  int16_t vec;        // n and the pointers let eight values be moved at once
+  int16_t vec;        // the pointers let eight values be moved at once
 };
 struct AdamwStep {
   float beta1, rest1, beta2, rest2, eps;  // rest: 1 − β
