@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(kThreads + 32, QueueCfg<MT>::CTAS) experts_que
   const int run = FIRST ? K : a.run;  // of K, of one split
   // The block's units, every gridDim.x-th of blocks × splits × entries, without
   // a division from one to the next: a warp that does not multiply does not
-  // refill its queue either (M = 1, D 2048, F 16384: 66 us with, XXX without).
+  // refill its queue either.
   const int entries = r.entries;
   const int block_step = static_cast<int>(gridDim.x) % blocks, rest = static_cast<int>(gridDim.x) / blocks;
   const int split_step = rest % splits, entry_step = rest / splits;

@@ -24,166 +24,188 @@ __device__ __forceinline__ float half_or(const uint16_t* p, int64_t i, float oth
 
 // ------------------------------------------------------------------ forward
 
-// What a warp knows of its row's values: their number, their sum and their
-// squares' sum around their mean (or, RMS, around 0).
-struct Part {
-  float n, sum, sq;
-};
-
-// μ and ρ of a row from the moments of the G threads that hold it, V values
-// each, `in` telling which of them are in the row. A layer norm's squares are
-// summed around each warp's own mean, and the warps' joined by the distances
-// of their means: Σ(v − μ)² = Σ_w [Σ(v − μ_w)² + n_w·(μ_w − μ)²], which keeps
-// its digits in a row far from zero and takes one exchange between the warps
-// where a second pass around the row's mean takes two.
-template <int G, int V, typename In>
-__device__ __forceinline__ void row_moments(bool layer, int D, float eps, Part* parts, const float (&v)[V], In in,
-                                            float& mu, float& rho) {
-  const int lane = threadIdx.x & 31;
-  Part p{0.f, 0.f, 0.f};
-  float center = 0.f;
-  if (layer) {
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (in(i)) {
-        p.sum += v[i];
-        ++n;
-      }
-    p.sum = warp_sum(p.sum);
-    p.n = static_cast<float>(__reduce_add_sync(0xffffffffu, n));
-    center = p.n > 0.f ? p.sum / p.n : 0.f;
-  }
-#pragma unroll
-  for (int i = 0; i < V; ++i)
-    if (in(i)) {
-      const float c = v[i] - center;
-      p.sq = fmaf(c, c, p.sq);
-    }
-  p.sq = warp_sum(p.sq);
-  const float inv = 1.f / static_cast<float>(D);
-  if constexpr (G > 32) {
-    if (lane == 0) parts[threadIdx.x >> 5] = p;
-    __syncthreads();
-    float sum = 0.f, sq = 0.f;
-    if (layer) {
-#pragma unroll
-      for (int w = 0; w < G / 32; ++w) sum += parts[w].sum;
-      mu = sum * inv;
-#pragma unroll
-      for (int w = 0; w < G / 32; ++w) {
-        const Part q = parts[w];
-        const float off = q.n > 0.f ? q.sum / q.n - mu : 0.f;
-        sq += fmaf(q.n * off, off, q.sq);
-      }
-    } else {
-      mu = 0.f;
-#pragma unroll
-      for (int w = 0; w < G / 32; ++w) sq += parts[w].sq;
-    }
-    p.sq = sq;
-  } else {
-    mu = layer ? center : 0.f;
-  }
-  rho = rsqrtf(p.sq * inv + eps);
+__device__ __forceinline__ float pair_sum(f32x2 v) {
+  float lo, hi;
+  unpair(v, lo, hi);
+  return lo + hi;
 }
 
-// G threads per row, which they hold in registers (8·NV values each); one
-// read and one write. VEC: the row in 16-byte pieces; otherwise value by
-// value, neighbouring threads on neighbouring values. Blocks of max(G, 128)
-// threads.
+// What a warp knows of its row's values: their mean (RMS: 0) and the sum of
+// the squares around it.
+struct Part {
+  float mean, sq;
+};
+
+// The values a thread holds, 8·NV in pairs; those past the row's end are 0.
+// VEC: the row in 16-byte pieces; otherwise value by value, neighbouring
+// threads on neighbouring values.
 template <int G, int NV, bool VEC>
-__global__ void __launch_bounds__(G < 128 ? 128 : G) residual_norm_rows_kernel(const ResidualNormArgs a) {
-  constexpr int THREADS = G < 128 ? 128 : G, V = 8 * NV;
-  __shared__ Part parts[2][THREADS / 32];
-  const int t = threadIdx.x % G;
-  const int64_t m = static_cast<int64_t>(blockIdx.x) * (THREADS / G) + threadIdx.x / G;
-  const int D = static_cast<int>(a.D);
-  // the column of a thread's value i
-  auto col = [&](int i) { return VEC ? (t + i / 8 * G) * 8 + i % 8 : i * G + t; };
-  auto in = [&](int i) { return col(VEC ? i / 8 * 8 : i) < D; };
-  auto load = [&](const uint16_t* p, int j) {
+struct RowPiece {
+  int t, D;
+  // the column of value k of piece j
+  __device__ int col(int j, int k) const { return VEC ? (t + j * G) * 8 + k : (8 * j + k) * G + t; }
+  __device__ bool in(int j, int k) const { return col(j, VEC ? 0 : k) < D; }
+  // How many of the row's values this thread's warp holds.
+  __device__ int of_warp() const {
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int k = 0; k < (VEC ? 1 : 8); ++k) n += __popc(__ballot_sync(0xffffffffu, in(j, k)));
+    return VEC ? 8 * n : n;
+  }
+  __device__ uint4 load(const uint16_t* p, int j) const {
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
     if constexpr (VEC) {
-      const int c = col(8 * j);
+      const int c = col(j, 0);
       if (c < D && dbg_row(p + c, c, 8, D, 16)) v = load16(p + c);
     } else {
       uint32_t w[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) w[k] = in(8 * j + k) ? p[col(8 * j + k)] : 0u;
+      for (int k = 0; k < 8; ++k) w[k] = in(j, k) ? p[col(j, k)] : 0u;
       v = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
     }
     return v;
-  };
-  auto store = [&](uint16_t* p, int j, const float (&f)[8]) {
+  }
+  __device__ void store(uint16_t* p, int j, const float (&f)[8]) const {
+    const uint4 v = pack8f(f);
     if constexpr (VEC) {
-      const int c = col(8 * j);
-      if (c < D && dbg_row(p + c, c, 8, D, 16)) *reinterpret_cast<uint4*>(p + c) = pack8f(f);
+      const int c = col(j, 0);
+      if (c < D && dbg_row(p + c, c, 8, D, 16)) *reinterpret_cast<uint4*>(p + c) = v;
     } else {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (in(8 * j + k)) p[col(8 * j + k)] = __half_as_ushort(__float2half_rn(f[k]));
+        if (in(j, k)) p[col(j, k)] = static_cast<uint16_t>(w[k / 2] >> (16 * (k & 1)));
     }
-  };
+  }
+};
+
+// μ and ρ of a row from the moments of the G threads that hold it; `n` of its
+// values lie in this warp, counts[w] in warp w. A layer norm's squares are
+// summed around each warp's own mean, and the warps' joined by the distances
+// of their means: Σ(v − μ)² = Σ_w [Σ(v − μ_w)² + n_w·(μ_w − μ)²], which keeps
+// its digits in a row far from zero and takes one exchange between the warps
+// where a second pass around the row's mean takes two.
+template <int G, int NV, bool VEC>
+__device__ __forceinline__ void row_moments(bool layer, const RowPiece<G, NV, VEC>& piece, float eps, float n,
+                                            const float* counts, Part* parts, const float (&v)[NV][8], float& mu,
+                                            float& rho) {
+  Part p{0.f, 0.f};
+  if (layer) {
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += v[j][k];
+    p.mean = n > 0.f ? warp_sum(s) / n : 0.f;
+  }
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    float sq = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float c = VEC || piece.in(j, k) ? v[j][k] - p.mean : 0.f;
+      sq = fmaf(c, c, sq);
+    }
+    if (piece.in(j, 0)) p.sq += sq;
+  }
+  p.sq = warp_sum(p.sq);
+  const float inv = 1.f / static_cast<float>(piece.D);
+  mu = p.mean;
+  if constexpr (G > 32) {
+    if ((threadIdx.x & 31) == 0) parts[threadIdx.x >> 5] = p;
+    __syncthreads();
+    float sum = 0.f, total = 0.f;
+    if (layer) {
+#pragma unroll
+      for (int w = 0; w < G / 32; ++w) sum = fmaf(counts[w], parts[w].mean, sum);
+      mu = sum * inv;
+#pragma unroll
+      for (int w = 0; w < G / 32; ++w) {
+        const Part q = parts[w];
+        total += fmaf(counts[w] * (q.mean - mu), q.mean - mu, q.sq);
+      }
+    } else {
+#pragma unroll
+      for (int w = 0; w < G / 32; ++w) total += parts[w].sq;
+    }
+    p.sq = total;
+  }
+  rho = rsqrtf(p.sq * inv + eps);
+}
+
+// G threads per row, which they hold in registers; one read and one write.
+// Blocks of max(G, 128) threads. (At least 768 threads to an SM where a thread
+// holds 32 values: 16384 rows of 8192, RMS norms: 169 us, and 194 with the
+// registers that the compiler takes without the bound.)
+template <int G, int NV, bool VEC>
+__global__ void __launch_bounds__(G < 128 ? 128 : G, NV == 4 && G < 512 ? 768 / (G < 128 ? 128 : G) : 1)
+    residual_norm_rows_kernel(const ResidualNormArgs a) {
+  constexpr int THREADS = G < 128 ? 128 : G;
+  __shared__ Part parts[2][THREADS / 32];
+  __shared__ float counts[THREADS / 32];
+  const RowPiece<G, NV, VEC> piece{static_cast<int>(threadIdx.x % G), static_cast<int>(a.D)};
+  const int64_t m = static_cast<int64_t>(blockIdx.x) * (THREADS / G) + threadIdx.x / G;
+  float n = 0.f;
+  if (a.post == HGEMM_NORM_LAYER || a.pre == HGEMM_NORM_LAYER) {
+    n = static_cast<float>(piece.of_warp());
+    if ((threadIdx.x & 31) == 0) counts[threadIdx.x >> 5] = n;  // (read behind the exchanges' barriers)
+  }
   grid_dependency_wait();
   grid_launch_dependents();
   if (G < 128 && m >= a.M) return;  // whole warps; larger groups have a block of their own
-  float v[V];                       // y, then z
+  float v[NV][8];                   // y, then z
   uint4 x[NV];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) x[j] = load(a.y + m * a.ldy, j);
+  for (int j = 0; j < NV; ++j) x[j] = piece.load(a.y + m * a.ldy, j);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    unpack8(x[j], v[j]);
+    x[j] = piece.load(a.x + m * a.ldx, j);
+  }
+  float my = 0.f, ry = 1.f, mz = 0.f, rz = 1.f;
+  if (a.post) row_moments(a.post == HGEMM_NORM_LAYER, piece, a.eps, n, counts, parts[0], v, my, ry);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     float f[8];
-    unpack8(x[j], f);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[8 * j + k] = f[k];
-    x[j] = load(a.x + m * a.ldx, j);
-  }
-  float my = 0.f, ry = 1.f, mz = 0.f, rz = 1.f;
-  if (a.post) row_moments<G, V>(a.post == HGEMM_NORM_LAYER, D, a.eps, parts[0], v, in, my, ry);
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    float f[8], z[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) z[k] = v[8 * j + k];
     if (a.post) {
-      unpack8(load(a.post_gamma, j), f);
+      unpack8(piece.load(a.post_gamma, j), f);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) z[k] = (z[k] - my) * ry * f[k];
+      for (int k = 0; k < 8; ++k) v[j][k] = (v[j][k] - my) * ry * f[k];
       if (a.post_beta) {
-        unpack8(load(a.post_beta, j), f);
+        unpack8(piece.load(a.post_beta, j), f);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) z[k] += f[k];
+        for (int k = 0; k < 8; ++k) v[j][k] += f[k];
       }
     }
     if (a.gate) {
-      unpack8(load(a.gate, j), f);
+      unpack8(piece.load(a.gate, j), f);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) z[k] *= f[k];
+      for (int k = 0; k < 8; ++k) v[j][k] *= f[k];
     }
     unpack8(x[j], f);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[8 * j + k] = z[k] = fmaf(a.alpha, f[k], z[k]);
-    store(a.z + m * a.ldz, j, z);
+    for (int k = 0; k < 8; ++k) v[j][k] = fmaf(a.alpha, f[k], v[j][k]);
+    piece.store(a.z + m * a.ldz, j, v[j]);
   }
   if (a.pre) {
-    row_moments<G, V>(a.pre == HGEMM_NORM_LAYER, D, a.eps, parts[1], v, in, mz, rz);
+    row_moments(a.pre == HGEMM_NORM_LAYER, piece, a.eps, n, counts, parts[1], v, mz, rz);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      float f[8], h[8];
-      unpack8(load(a.pre_gamma, j), f);
+      float f[8];
+      unpack8(piece.load(a.pre_gamma, j), f);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) h[k] = (v[8 * j + k] - mz) * rz * f[k];
+      for (int k = 0; k < 8; ++k) v[j][k] = (v[j][k] - mz) * rz * f[k];
       if (a.pre_beta) {
-        unpack8(load(a.pre_beta, j), f);
+        unpack8(piece.load(a.pre_beta, j), f);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) h[k] += f[k];
+        for (int k = 0; k < 8; ++k) v[j][k] += f[k];
       }
-      store(a.h + m * a.ldh, j, h);
+      piece.store(a.h + m * a.ldh, j, v[j]);
     }
   }
-  if (t == 0 && a.stats && HG_DBG_INDEX(m, a.M)) {
+  if (piece.t == 0 && a.stats && HG_DBG_INDEX(m, a.M)) {
     if (a.post) a.stats[m] = my, a.stats[a.M + m] = ry;
     if (a.pre) a.stats[2 * a.M + m] = mz, a.stats[3 * a.M + m] = rz;
   }
@@ -277,12 +299,13 @@ struct RingCfg {
   static constexpr int GROUPS = THREADS / G;
   static constexpr int WARPS = G / 32;  // per group
   static constexpr int MAX_STAGES = 8;
-  static constexpr int RING_BYTES = 200 * 1024;  // of the CTA
-  static constexpr int OFF_BAR = RING_BYTES;
+  static constexpr int RING_BYTES = 192 * 1024;  // of the CTA
+  static constexpr int OFF_W = RING_BYTES;       // FULL: gate·post_gamma of up to 8192 columns
+  static constexpr int OFF_BAR = OFF_W + THREADS * 8 * NV * 4;
   static constexpr int OFF_EXCHANGE = OFF_BAR + GROUPS * MAX_STAGES * 8;
   static constexpr int OFF_MISC = OFF_EXCHANGE + 2 * (THREADS / 32) * 32;  // two buffers of eight sums per warp
   static constexpr int SMEM_BYTES = OFF_MISC + 16;
-  static_assert(SMEM_BYTES <= 232448 - 1024, "fits an SM");
+  static_assert(SMEM_BYTES <= 232448, "fits a CTA");
   static_assert(THREADS * 8 * NV * 4 * 4 <= RING_BYTES, "the groups' sums fit the ring");
 };
 
@@ -305,12 +328,6 @@ __device__ __forceinline__ float warp_sums(float (&v)[N]) {
 #pragma unroll
   for (int o = N; o < 32; o <<= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
   return r;
-}
-
-__device__ __forceinline__ float pair_sum(f32x2 v) {
-  float lo, hi;
-  unpair(v, lo, hi);
-  return lo + hi;
 }
 
 // A row's statistics, and where it lies in shared memory.
@@ -367,34 +384,54 @@ __global__ void __launch_bounds__(512, 1) residual_norm_ring_kernel(const Residu
 
   // w = gate·post_gamma, and the norm in front's gamma; the sums dz·ŷ, dz,
   // dH·ẑ and dH of this thread's columns
-  f32x2 w[NV][4];
+  // (FULL keeps w in shared memory: its sums leave too few registers)
+  f32x2 w[FULL ? 1 : NV][4];
   uint4 gamma[NV];
+  ulonglong2* shared_w = reinterpret_cast<ulonglong2*>(ring_smem + Cfg::OFF_W);
   f32x2 s1[NV][4], s0[NV][4], t1[NV][4], t0[NV][4];
   float sum_w = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (t + i * G) * 8;
     gamma[i] = make_uint4(0u, 0u, 0u, 0u);
+    f32x2 v[4], f[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      w[i][k] = pair_of(c < D ? 1.f : 0.f);
+      v[k] = pair_of(c < D ? 1.f : 0.f);
       s1[i][k] = s0[i][k] = t1[i][k] = t0[i][k] = 0;  // a pair of +0
     }
     if (c < D) {
-      f32x2 f[4];
       if (PRE && dbg_row(a.pre_gamma + c, c, 8, D, 16)) gamma[i] = load16(a.pre_gamma + c);
-      if (a.gate && dbg_row(a.gate + c, c, 8, D, 16)) unpack8(load16(a.gate + c), w[i]);
+      if (a.gate && dbg_row(a.gate + c, c, 8, D, 16)) unpack8(load16(a.gate + c), v);
       if (POST && dbg_row(a.post_gamma + c, c, 8, D, 16)) {
         unpack8(load16(a.post_gamma + c), f);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) w[i][k] = mul2(w[i][k], f[k]);
+        for (int k = 0; k < 4; ++k) v[k] = mul2(v[k], f[k]);
       }
     }
     if constexpr (FULL) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) sum_w += pair_sum(w[i][k]);
+      for (int k = 0; k < 4; ++k) sum_w += pair_sum(v[k]);
+      if (group == 0) {
+        shared_w[(t + i * G) * 2] = make_ulonglong2(v[0], v[1]);
+        shared_w[(t + i * G) * 2 + 1] = make_ulonglong2(v[2], v[3]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[i][k] = v[k];
     }
   }
+  if constexpr (FULL) __syncthreads();
+  // w of a thread's piece i
+  auto weights = [&](int i, f32x2 (&v)[4]) {
+    if constexpr (FULL) {
+      const ulonglong2 lo = shared_w[(t + i * G) * 2], hi = shared_w[(t + i * G) * 2 + 1];
+      v[0] = lo.x, v[1] = lo.y, v[2] = hi.x, v[3] = hi.y;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = w[i][k];
+    }
+  };
 
   const float inv_d = 1.f / static_cast<float>(D);
   const bool layer_y = POST && a.post == HGEMM_NORM_LAYER, layer_z = PRE && a.pre == HGEMM_NORM_LAYER;
@@ -453,17 +490,19 @@ __global__ void __launch_bounds__(512, 1) residual_norm_ring_kernel(const Residu
             }
           }
           if constexpr (POST) {
+            f32x2 wv[4];
+            weights(i, wv);
             unpack8(reinterpret_cast<const uint4*>(r.at + plan.y)[v], y);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               if constexpr (FULL) y[k] = add2(y[k], shift_y);
-              y[k] = mul2(mul2(y[k], scale_y), w[i][k]);  // w·ŷ
+              y[k] = mul2(mul2(y[k], scale_y), wv[k]);  // w·ŷ
               p[1] = fma2(y[k], tt[k], p[1]);
-              if constexpr (FULL) p[4] = fma2(w[i][k], tt[k], p[4]);
+              if constexpr (FULL) p[4] = fma2(wv[k], tt[k], p[4]);
               if constexpr (PRE) {
                 p[2] = fma2(y[k], z[k], p[2]);
                 if constexpr (FULL) {
-                  p[5] = fma2(w[i][k], z[k], p[5]);
+                  p[5] = fma2(wv[k], z[k], p[5]);
                   p[6] = add2(p[6], y[k]);
                 }
               }
@@ -551,9 +590,10 @@ __global__ void __launch_bounds__(512, 1) residual_norm_ring_kernel(const Residu
         }
         const int64_t c = v * 8;
         if (POST || plan.need_y) unpack8(reinterpret_cast<const uint4*>(row.at + plan.y)[v], z);
+        weights(i, g);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          g[k] = mul2(w[i][k], dz[k]);
+          g[k] = mul2(g[k], dz[k]);
           if (POST || plan.need_y) {
             if constexpr (POST) {
               if constexpr (FULL) z[k] = add2(z[k], shift_y);
@@ -660,8 +700,9 @@ __device__ __forceinline__ float back_yh(const ResidualNormBackArgs& a, const Ba
   return (half_at(a.y, m * a.ldy + d) - r.my) * r.ry;
 }
 
-// Any length, pitch and alignment, for the rows m0 .. m1-1 whose means the
-// workspace holds. First the four means of every row ...
+// Rows that bulk copies cannot describe, or longer than the ring takes: rows
+// m0 .. m1-1, whose means the workspace holds. First the four means of every
+// row ...
 __global__ void __launch_bounds__(kThreads) residual_norm_means_kernel(const ResidualNormBackArgs a) {
   __shared__ float s[kThreads / 32];
   grid_dependency_wait();
@@ -755,34 +796,51 @@ __global__ void __launch_bounds__(kThreads) residual_norm_backward_kernel(const 
 }
 
 // The vectors' gradients from `count` partial sums, in a fixed order: 32
-// columns per block, 8 threads down each.
-__global__ void __launch_bounds__(kThreads)
+// columns per block, 32 threads down each, whose few loads are all under way at
+// once (1000 rows of 1000: 13.4 us for the whole pass with 8 threads and their
+// loads one after another, 10.9 this way).
+constexpr int kSumThreads = 1024;
+__global__ void __launch_bounds__(kSumThreads)
     residual_norm_sums_kernel(const ResidualNormBackArgs a, int count, bool full) {
-  __shared__ float s[4][8][33];
+  constexpr int EACH = (kResidualNormPartials + 31) / 32;
+  __shared__ float s[4][32][33];
   grid_dependency_wait();
   grid_launch_dependents();
   const int c = threadIdx.x & 31, r = threadIdx.x >> 5;
   const int64_t d = static_cast<int64_t>(blockIdx.x) * 32 + c;
-  float v[4] = {};
-  if (d < a.D)
-    for (int i = r; i < count; i += 8)
+  float p[EACH][4] = {};
+  if (d < a.D) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (full || j % 2 == 0) v[j] += a.partials[(static_cast<int64_t>(i) * 4 + j) * a.D + d];
+    for (int i = 0; i < EACH; ++i)
+      if (r + 32 * i < count) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) s[j][r][c] = v[j];
+        for (int j = 0; j < 4; ++j)
+          if (full || j % 2 == 0) p[i][j] = a.partials[(static_cast<int64_t>(r + 32 * i) * 4 + j) * a.D + d];
+      }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) v += p[i][j];
+    s[j][r][c] = v;
+  }
   __syncthreads();
-  if (r != 0 || d >= a.D || !HG_DBG_INDEX(d, a.D)) return;
+  if (r >= 4) return;
+  // warp j: the sum j of the 32 columns, then all four by warp 0
+  float v = 0.f;
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    for (int i = 1; i < 8; ++i) v[j] += s[j][i][c];
+  for (int i = 0; i < 32; ++i) v += s[r][i][c];
+  s[r][0][c] = v;  // (its own column's sums are read)
+  named_bar_sync(1, 128);
+  if (r != 0 || d >= a.D || !HG_DBG_INDEX(d, a.D)) return;
+  const float s1 = s[0][0][c], s0 = s[1][0][c], t1 = s[2][0][c], t0 = s[3][0][c];
   const float gate = half_or(a.gate, d, 1.f);
-  if (a.dgate)
-    a.dgate[d] = a.post ? fmaf(half_at(a.post_gamma, d), v[0], half_or(a.post_beta, d, 0.f) * v[1]) : v[0];
-  if (a.dpost_gamma) a.dpost_gamma[d] = gate * v[0];
-  if (a.dpost_beta) a.dpost_beta[d] = gate * v[1];
-  if (a.dpre_gamma) a.dpre_gamma[d] = v[2];
-  if (a.dpre_beta) a.dpre_beta[d] = v[3];
+  if (a.dgate) a.dgate[d] = a.post ? fmaf(half_at(a.post_gamma, d), s1, half_or(a.post_beta, d, 0.f) * s0) : s1;
+  if (a.dpost_gamma) a.dpost_gamma[d] = gate * s1;
+  if (a.dpost_beta) a.dpost_beta[d] = gate * s0;
+  if (a.dpre_gamma) a.dpre_gamma[d] = t1;
+  if (a.dpre_beta) a.dpre_beta[d] = t0;
 }
 
 template <int G, int NV>
@@ -802,18 +860,24 @@ cudaError_t forward_group(const ResidualNormArgs& a, bool vec, cudaStream_t stre
   return forward_with<G, 4>(a, vec, stream);
 }
 
-template <int G, bool POST, bool PRE, bool FULL>
-cudaError_t ring_with(const ResidualNormBackArgs& a, const RingPlan& plan, int grid, cudaStream_t stream) {
-  static std::atomic<bool> attr_done[64];
-  auto kern = residual_norm_ring_kernel<G, POST, PRE, FULL>;
+template <typename Kernel>
+cudaError_t allow_smem(Kernel kern, int bytes, std::atomic<bool> (&done)[64]) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || !attr_done[dev]) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RingCfg<G>::SMEM_BYTES);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) attr_done[dev] = true;
+  if (dev < 0 || dev >= 64 || !done[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
   }
+  return e;
+}
+
+template <int G, bool POST, bool PRE, bool FULL>
+cudaError_t ring_with(const ResidualNormBackArgs& a, const RingPlan& plan, int grid, cudaStream_t stream) {
+  static std::atomic<bool> done[64];
+  auto kern = residual_norm_ring_kernel<G, POST, PRE, FULL>;
+  const cudaError_t e = allow_smem(kern, RingCfg<G>::SMEM_BYTES, done);
+  if (e != cudaSuccess) return e;
   PdlLaunch l(dim3(static_cast<unsigned>(grid)), dim3(RingCfg<G>::THREADS), RingCfg<G>::SMEM_BYTES, stream);
   return cudaLaunchKernelEx(&l.cfg, kern, a, plan);
 }
@@ -908,7 +972,7 @@ cudaError_t launch_residual_norm_backward(ResidualNormBackArgs a, int num_sms, c
     partials = kSlices;
   }
   if (!a.dgate && !a.dpost_gamma && !a.dpost_beta && !a.dpre_gamma && !a.dpre_beta) return e;
-  PdlLaunch l(dim3(static_cast<unsigned>((a.D + 31) / 32)), dim3(kThreads), 0, stream);
+  PdlLaunch l(dim3(static_cast<unsigned>((a.D + 31) / 32)), dim3(kSumThreads), 0, stream);
   return cudaLaunchKernelEx(&l.cfg, residual_norm_sums_kernel, a, partials, !ring || ring_full(a));
 }
 
