@@ -43,38 +43,37 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
 
 // -------------------------------------------------------------------- router
 
-// An order of FP32 logits as whole numbers: larger logit, larger number; a NaN
-// below every number (0), and ties, by the lower half, to the lowest index.
-__device__ __forceinline__ unsigned long long order_key(float l, int e) {
+// An order of FP32 logits as whole numbers: larger logit, larger number, and a
+// NaN below every number. 0 is left for what has been chosen.
+__device__ __forceinline__ uint32_t order_key(float l) {
   const uint32_t b = __float_as_uint(l == 0.f ? 0.f : l);  // (−0 is +0)
-  const uint32_t up = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-  return (static_cast<unsigned long long>(l != l ? 0u : up) << 32) | static_cast<uint32_t>(~e);
-}
-
-__device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const unsigned long long w = __shfl_xor_sync(0xffffffffu, v, o);
-    v = w > v ? w : v;
-  }
-  return v;
+  return l != l ? 1u : (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
 // The k largest of the E logits in shared memory, by one warp: lane j < k
-// leaves with choice j and its share.
+// leaves with choice j and its share. A lane holds every 32nd logit; a round is
+// two reductions, the largest and the lowest index that has it.
 __device__ __forceinline__ void choose(const float* logits, int E, int k, bool normalize, int& mine, float& share) {
   const int lane = threadIdx.x & 31;
-  unsigned long long last = ~0ull;
+  uint32_t key[kMost / 32];
+#pragma unroll
+  for (int i = 0; i < kMost / 32; ++i) key[i] = lane + 32 * i < E ? order_key(logits[lane + 32 * i]) : 0u;
   float chosen = 0.f, top = 0.f;
   mine = 0;
   for (int j = 0; j < k; ++j) {
-    unsigned long long best = 0;
-    for (int e = lane; e < E; e += 32) {
-      const unsigned long long key = order_key(logits[e], e);
-      if (key < last && key > best) best = key;
-    }
-    last = best = warp_max(best);
-    const int e = static_cast<int>(~static_cast<uint32_t>(best));
+    uint32_t best = 0u;
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < kMost / 32; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        at = lane + 32 * i;
+      }
+    const uint32_t most = __reduce_max_sync(0xffffffffu, best);
+    const int e = __reduce_min_sync(0xffffffffu, best == most ? at : kMost);
+#pragma unroll
+    for (int i = 0; i < kMost / 32; ++i)
+      if (e == lane + 32 * i) key[i] = 0u;
     if (j == 0) top = logits[e];
     if (lane == j) {
       mine = e;
@@ -111,17 +110,18 @@ __global__ void __launch_bounds__(kThreads) experts_router_kernel(const ExpertsA
       constexpr int AHEAD = 8;
       for (int d0 = 8 * lane; d0 < a.D; d0 += 256 * AHEAD) {
         uint4 p[AHEAD], q[AHEAD];
+        // (unconditional, or the compiler waits for one pair before it asks for
+        // the next; in place of pieces past the end the row's first, not summed)
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) {
-          const int d = d0 + 256 * j;
-          p[j] = q[j] = make_uint4(0u, 0u, 0u, 0u);
-          if (d < a.D && dbg_row(w + d, d, 8, a.D, 16)) {
-            p[j] = load16(x + d);
-            q[j] = load16(w + d);
-          }
+          const int d = d0 + 256 * j < a.D ? d0 + 256 * j : 0;
+          if (!dbg_row(w + d, d, 8, a.D, 16)) return;
+          p[j] = load16(x + d);
+          q[j] = load16(w + d);
         }
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) {
+          if (d0 + 256 * j >= a.D) break;
           float f[8], h[8];
           unpack8(p[j], f);
           unpack8(q[j], h);
