@@ -258,183 +258,39 @@ __device__ __forceinline__ void put_unit(const ExpertsArgs& a, const Routing& r,
   }
 }
 
-// The 16 bytes at k of a row of any alignment, what lies at or past K zero.
-__device__ __forceinline__ uint4 load_piece(const uint16_t* row, int k, int K, bool weights) {
-  uint32_t v[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t h[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int at = k + 2 * i + j;
-      h[j] = at < K && HG_DBG_INDEX(at, K) ? (weights ? ld_gpu_u16(row + at) : row[at]) : 0u;
-    }
-    v[i] = h[0] | h[1] << 16;
-  }
-  return make_uint4(v[0], v[1], v[2], v[3]);
-}
-
 // FIRST: a unit of work is features 8u .. 8u+7 and their gates (gated) or
 // 16u .. 16u+15 of an entry's expert, and H is written; else outputs 16u ..
 // 16u+15 over one of `splits` runs of F, and the slots' FP32 partial outputs
-// are. Units are dealt to the blocks in turn. A warp's pieces of all its units
-// form one sequence, AHEAD of which are under way at any time, so that the next
-// unit's weights are on their way while one is added up. The second product
-// starts on its weights before the first has ended: who chose what is known
-// since the router, and only the tokens' values have to be waited for.
-template <int MT>
-struct ProductCfg {
-  static constexpr int AHEAD = MT == 1 ? 4 : MT == 2 ? 3 : 2;
-  static constexpr int PART = kWarps * 8 * MT * 17;  // floats of one buffer of partial sums
-  static constexpr int SMEM_BYTES = 2 * PART * 4 + static_cast<int>(sizeof(Routing));
-};
-
-template <int MT, bool FIRST>
-__global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) experts_product_kernel(const ExpertsArgs a) {
-  constexpr int AHEAD = ProductCfg<MT>::AHEAD;
-  extern __shared__ __align__(128) uint8_t experts_smem[];
-  float* parts = reinterpret_cast<float*>(experts_smem);
-  Routing& r = *reinterpret_cast<Routing*>(experts_smem + 2 * ProductCfg<MT>::PART * 4);
-  if constexpr (FIRST) {
-    grid_dependency_wait();
-    grid_launch_dependents();
-  } else {
-    fence_gpu();
-  }
-  find_entries<MT>(r, a);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = lane >> 2, t = lane & 3;
-  const int K = FIRST ? a.D : a.F, rows = FIRST ? a.F : a.D;
-  const bool gated = FIRST && a.gated;
-  const int per = gated ? 8 : 16;  // outputs of a unit
-  const int blocks = (rows + per - 1) / per, splits = FIRST ? 1 : a.splits;
-  const int run = FIRST ? K : a.run;  // of K, of one split
-  const int steps = (run + kWarps * kPiece - 1) / (kWarps * kPiece);
-  const int units = r.entries * splits * blocks;
-  const int mine = units > static_cast<int>(blockIdx.x) ? (units - static_cast<int>(blockIdx.x) - 1) / static_cast<int>(gridDim.x) + 1 : 0;
-  const uint16_t* W = FIRST ? a.W1 : a.W2;
-  const int64_t ldw = FIRST ? a.ldw1 : a.ldw2;
-  const int64_t expert_rows = gated ? 2 * static_cast<int64_t>(rows) : rows;
-
-  struct Unit {
-    int entry, split, n0;
-  };
-  auto unit_of = [&](int i) {
-    const int u = static_cast<int>(blockIdx.x) + i * static_cast<int>(gridDim.x);
-    const int at = u / blocks;
-    return Unit{at / splits, at % splits, (u - at * blocks) * per};
-  };
-
-  // What is fetched: step fs of the block's unit fi.
-  int fi = 0, fs = 0, fk = 0, fend = 0;
-  const uint16_t *w0 = nullptr, *w1 = nullptr, *x[MT];
-  auto begin_unit = [&]() {
-    const Unit u = unit_of(fi);
-    const auto& e = r.entry[u.entry];
-    // rows past the end are computed as copies of the last one and not stored
-    const uint16_t* base = W + e.expert * expert_rows * ldw;
-    const int row0 = min(u.n0 + g, rows - 1), row1 = min(u.n0 + g + 8, rows - 1);
-    w0 = base + row0 * ldw;
-    w1 = base + (gated ? row0 + static_cast<int64_t>(rows) : row1) * ldw;
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const int slot = 8 * i + g < e.count ? r.list[e.first + 8 * i + g] : -1;
-      x[i] = slot < 0 ? nullptr : FIRST ? a.X + slot / a.k * a.ldx : a.ws_h + slot * a.ldh;
-    }
-    fk = u.split * run + warp * kPiece + 8 * t;
-    fend = min(u.split * run + run, K);
-    fs = 0;
-  };
-  uint4 a0[AHEAD], a1[AHEAD], b[AHEAD][MT];
-  auto fetch_tokens = [&](int j, int k) {
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-      b[j][i] = x[i] ? load_piece(x[i], k, fend, false) : make_uint4(0u, 0u, 0u, 0u);
-  };
-  auto fetch = [&](int j, bool tokens) {
-    if (fi >= mine) return;
-    a0[j] = load_piece(w0, fk, fend, true);
-    a1[j] = load_piece(w1, fk, fend, true);
-    if (tokens) fetch_tokens(j, fk);
-    fk += kWarps * kPiece;
-    if (++fs == steps && ++fi < mine) begin_unit();
-  };
-  if constexpr (FIRST) {
-    if (mine > 0) begin_unit();
-#pragma unroll
-    for (int j = 0; j < AHEAD; ++j) fetch(j, true);
-  } else {
-    if (mine > 0) begin_unit();
-#pragma unroll
-    for (int j = 0; j < AHEAD; ++j) fetch(j, false);
-    grid_dependency_wait();
-    grid_launch_dependents();
-    fi = 0;
-    if (mine > 0) begin_unit();
-#pragma unroll
-    for (int j = 0; j < AHEAD; ++j)
-      if (fi < mine) {
-        fetch_tokens(j, fk);
-        fk += kWarps * kPiece;
-        if (++fs == steps && ++fi < mine) begin_unit();
-      }
-  }
-
-  float acc[MT][4] = {};
-  int ci = 0, cs = 0;
-  auto finish_unit = [&]() {
-    const Unit u = unit_of(ci);
-    const auto& e = r.entry[u.entry];
-    float* part = parts + (ci & 1) * ProductCfg<MT>::PART + warp * (8 * MT * 17);
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      part[(8 * i + 2 * t) * 17 + g] = acc[i][0];
-      part[(8 * i + 2 * t + 1) * 17 + g] = acc[i][1];
-      part[(8 * i + 2 * t) * 17 + g + 8] = acc[i][2];
-      part[(8 * i + 2 * t + 1) * 17 + g + 8] = acc[i][3];
-      acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-    }
-    // (the other buffer next: it has been read by all who pass this barrier)
-    __syncthreads();
-    part = parts + (ci & 1) * ProductCfg<MT>::PART;
-    put_unit<FIRST>(a, r, e, u.split, u.n0, per, rows, threadIdx.x, kThreads, [&](int row, int column) {
-      float v = part[row * 17 + column];
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) v += part[w * (8 * MT * 17) + row * 17 + column];
-      return v;
-    });
-    ++ci;
-    cs = 0;
-  };
-  while (ci < mine) {
-#pragma unroll
-    for (int j = 0; j < AHEAD; ++j) {
-      if (ci >= mine) break;
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        mma_16816(acc[i], a0[j].x, a1[j].x, a0[j].y, a1[j].y, b[j][i].x, b[j][i].y);
-        mma_16816(acc[i], a0[j].z, a1[j].z, a0[j].w, a1[j].w, b[j][i].z, b[j][i].w);
-      }
-      fetch(j, true);
-      if (++cs == steps) finish_unit();
-    }
-  }
-}
-
-// The same products for rows that 16-byte copies can describe. Eight warps
-// multiply and a ninth adds their sums up, so that none of the eight waits for
-// the others at a unit's end. A lane's pieces pass through a queue of its own
-// in shared memory, filled by asynchronous copies: registers hold four pieces
-// at most before a warp's scoreboards, six, make it wait for the youngest load
-// instead of the oldest. What a lane copies only that lane reads, so that
-// nothing but its own copies is waited for. A step is two pieces, 64 values of
-// K per warp and 128 bytes of a row.
-template <int MT>
+// are. Units are dealt to the blocks in turn.
+//
+// Eight warps multiply and a ninth adds their sums up, so that none of the
+// eight waits for the others at a unit's end. A lane's pieces pass through a
+// queue of its own in shared memory, filled by asynchronous copies: registers
+// hold four pieces at most before a warp's scoreboards, six, make it wait for
+// the youngest load instead of the oldest (24 tokens, 8 of 64 experts: 176 us
+// that way, 136 with the queue; 347 with bulk copies of 1 KB, of which an SM
+// starts one in some 125 cycles). A step is two pieces, 64 values of K per warp
+// and 128 bytes of a row. A warp's steps of all its units form one sequence, so
+// that the next unit's weights are on their way while one is added up. The
+// second product starts on its weights before the first has ended: who chose
+// what is known since the router, and only the tokens' values have to be waited
+// for. Tokens are copied through L1: every block wants the same few rows, and
+// the L2 lines of one token's row, asked for by all of them, held the first
+// product to 4.4 TB/s (6.9 through L1).
+//
+// ANY: rows that begin at any even address. The copies are of the aligned 16
+// bytes that a piece lies in, its row's last ones cut at the end (the rest is
+// zeros), and a ninth to a row's eight; a lane takes its piece out of its own
+// and its neighbour's by the row's distance from alignment. (The first copy of
+// a row may begin up to 14 bytes before it, within the 16 that hold its first
+// value and so within the same allocation.)
+template <int MT, bool ANY>
 struct QueueCfg {
   static constexpr int CTAS = MT == 4 ? 1 : 2;  // per SM
   static constexpr int DEPTH = MT == 1 ? 2 : MT == 2 ? 2 : 3;
   static constexpr int BUFFERS = MT == 1 ? 4 : 2;    // of partial sums
-  static constexpr int SLOT = (2 + MT) * 1024;       // of a warp: a step's rows and tokens
+  static constexpr int ROWS = 1024 + (ANY ? 128 : 0);  // of a warp: a step of eight rows
+  static constexpr int SLOT = (2 + MT) * ROWS;         // 16 rows of weights, and the tokens
   static constexpr int PART = kWarps * 8 * MT * 17;  // floats of one buffer
   static constexpr int OFF_ROUTING = BUFFERS * PART * 4;
   static constexpr int OFF_BAR = (OFF_ROUTING + static_cast<int>(sizeof(Routing)) + 15) / 16 * 16;
@@ -444,9 +300,21 @@ struct QueueCfg {
   static_assert(CTAS * (SMEM_BYTES + 1024) <= 233472, "the CTAs fit an SM");
 };
 
-template <int MT, bool FIRST>
-__global__ void __launch_bounds__(kThreads + 32, QueueCfg<MT>::CTAS) experts_queue_kernel(const ExpertsArgs a) {
-  using Cfg = QueueCfg<MT>;
+// The 16 bytes that begin s bytes (even) into two times 16.
+__device__ __forceinline__ uint4 shifted(uint4 lo, uint4 hi, uint32_t s) {
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+  for (int j = 0; j < 6; ++j) w[j] = s & 8u ? w[j + 2] : w[j];
+#pragma unroll
+  for (int j = 0; j < 5; ++j) w[j] = s & 4u ? w[j + 1] : w[j];
+  const uint32_t bits = (s & 2u) * 8u;
+  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                    __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+
+template <int MT, bool FIRST, bool ANY>
+__global__ void __launch_bounds__(kThreads + 32, QueueCfg<MT, ANY>::CTAS) experts_queue_kernel(const ExpertsArgs a) {
+  using Cfg = QueueCfg<MT, ANY>;
   constexpr int DEPTH = Cfg::DEPTH, STEP = kWarps * 2 * kPiece;  // values of K per step
   extern __shared__ __align__(128) uint8_t experts_smem[];
   float* parts = reinterpret_cast<float*>(experts_smem);
@@ -558,26 +426,50 @@ __global__ void __launch_bounds__(kThreads + 32, QueueCfg<MT>::CTAS) experts_que
     }
   };
   // (past the end zeros; where there is no token nothing: a column of its own)
+  auto copy_16 = [&](uint32_t to, const void* p, int bytes, bool weights) {
+    if (weights)
+      cp_async_16(to, p, bytes);
+    else
+      cp_async_16_shared(to, p, bytes);
+  };
   auto copy = [&](uint32_t to, const uint16_t* p, bool weights) {
+    if constexpr (ANY) {
+      const uintptr_t at = reinterpret_cast<uintptr_t>(p) & ~static_cast<uintptr_t>(15);
+      // bytes from here to the end of the row's part
+      const int left = static_cast<int>(reinterpret_cast<uintptr_t>(p + (fend - fk)) - at);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const bool in = fk + kPiece * i < fend && dbg_row(p + kPiece * i, fk + kPiece * i, 8, fend, 16);
-      if (weights)
-        cp_async_16(to + 512u * i, in ? p + kPiece * i : W, in ? 16 : 0);
-      else
-        cp_async_16_shared(to + 512u * i, in ? p + kPiece * i : W, in ? 16 : 0);
+      for (int i = 0; i < 3; ++i) {
+        if (i == 2 && t != 3) continue;  // the ninth
+        const int from = i == 2 ? 80 : 64 * i, bytes = min(max(left - from, 0), 16);
+        if (!HG_DBG_INDEX(bytes, 17)) continue;
+        copy_16(to + (i == 2 ? 1024u + 16u * g - 16u * lane : 512u * i),
+                bytes > 0 ? reinterpret_cast<const void*>(at + from) : a.ws_h, bytes, weights);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const bool in = fk + kPiece * i < fend && dbg_row(p + kPiece * i, fk + kPiece * i, 8, fend, 16);
+        copy_16(to + 512u * i, in ? p + kPiece * i : a.ws_h, in ? 16 : 0, weights);
+      }
     }
   };
   auto copy_weights = [&](int into) {
     const uint32_t to = queue_addr + static_cast<uint32_t>(into * Cfg::SLOT);
     copy(to, w0, true);
-    copy(to + 1024, w1, true);
+    copy(to + Cfg::ROWS, w1, true);
   };
   auto copy_tokens = [&](int into) {
-    const uint32_t to = queue_addr + static_cast<uint32_t>(into * Cfg::SLOT) + 2048;
+    const uint32_t to = queue_addr + static_cast<uint32_t>(into * Cfg::SLOT + 2 * Cfg::ROWS);
 #pragma unroll
     for (int i = 0; i < MT; ++i)
-      if (x[i]) copy(to + 1024u * i, x[i], false);
+      if (x[i]) copy(to + static_cast<uint32_t>(Cfg::ROWS) * i, x[i], false);
+  };
+  // Piece i of the rows at `at`, their distance from alignment `off`.
+  auto piece_of = [&](const uint8_t* at, int i, uint32_t off) {
+    const uint4 lo = *reinterpret_cast<const uint4*>(at + 512 * i);
+    if constexpr (!ANY) return lo;
+    const int next = t < 3 ? 512 * i + 16 : i == 0 ? 512 - 48 : 1024 + 16 * g - 16 * lane;
+    return shifted(lo, *reinterpret_cast<const uint4*>(at + next), off);
   };
   auto next_step = [&]() {
     if (--fsteps > 0) {
@@ -615,27 +507,45 @@ __global__ void __launch_bounds__(kThreads + 32, QueueCfg<MT>::CTAS) experts_que
 
   int slot = 0, done = 0;
   for (Unit u = first; u.entry < entries; advance(u)) {
-    const int steps = steps_of(u), count = r.entry[u.entry].count;
+    const int steps = steps_of(u);
+    const auto& e = r.entry[u.entry];
+    const int count = e.count;
+    uint32_t off0 = 0, off1 = 0, off[MT] = {};
+    if constexpr (ANY) {
+      // (whole steps further on a row's distance is the same)
+      auto distance = [](const uint16_t* p) { return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u; };
+      const int n0 = u.block * per, row0 = min(n0 + g, rows - 1), row1 = min(n0 + g + 8, rows - 1);
+      const uint16_t* base = W + e.expert * expert_rows * ldw;
+      off0 = distance(base + row0 * ldw);
+      off1 = distance(base + (gated ? row0 + static_cast<int64_t>(rows) : row1) * ldw);
+      if constexpr (FIRST) {  // (H's rows are aligned)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+          if (8 * i + g < count) off[i] = distance(a.X + r.token[e.first + 8 * i + g] * a.ldx);
+      }
+    }
     float acc[MT][4] = {};
     for (int s = 0; s < steps; ++s) {
       cp_async_wait<DEPTH - 1>();
-      const uint4* at = reinterpret_cast<const uint4*>(queue + slot * Cfg::SLOT);  // 512 bytes: 32 of these
+      if (ANY) __syncwarp();
+      const uint8_t* at = queue + slot * Cfg::SLOT;
       uint4 p[2][2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        p[i][0] = at[32 * i];
-        p[i][1] = at[64 + 32 * i];
+        p[i][0] = piece_of(at, i, off0);
+        p[i][1] = piece_of(at + Cfg::ROWS, i, off1);
       }
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
         if (8 * j >= count) break;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint4 b = at[128 + 64 * j + 32 * i];
+          const uint4 b = piece_of(at + (2 + j) * Cfg::ROWS, i, off[j]);
           mma_16816(acc[j], p[i][0].x, p[i][1].x, p[i][0].y, p[i][1].y, b.x, b.y);
           mma_16816(acc[j], p[i][0].z, p[i][1].z, p[i][0].w, p[i][1].w, b.z, b.w);
         }
       }
+      if (ANY) __syncwarp();  // the neighbours have read theirs
       if (fu.entry < entries) {
         copy_weights(slot);
         copy_tokens(slot);
@@ -708,21 +618,14 @@ cudaError_t allow_smem(Kernel kern, int bytes, std::atomic<bool> (&done)[64]) {
   return e;
 }
 
-template <int MT, bool FIRST>
-cudaError_t product_with(const ExpertsArgs& a, bool vec, int num_sms, cudaStream_t stream) {
-  static std::atomic<bool> done[2][64];
-  cudaError_t e;
-  if (vec) {
-    using Cfg = QueueCfg<MT>;
-    auto kern = experts_queue_kernel<MT, FIRST>;
-    if ((e = allow_smem(kern, Cfg::SMEM_BYTES, done[0])) != cudaSuccess) return e;
-    PdlLaunch l(dim3(static_cast<unsigned>(num_sms * Cfg::CTAS)), dim3(kThreads + 32), Cfg::SMEM_BYTES, stream);
-    return cudaLaunchKernelEx(&l.cfg, kern, a);
-  }
-  auto kern = experts_product_kernel<MT, FIRST>;
-  if ((e = allow_smem(kern, ProductCfg<MT>::SMEM_BYTES, done[1])) != cudaSuccess) return e;
-  PdlLaunch l(dim3(static_cast<unsigned>(num_sms * (MT == 1 ? 3 : 2))), dim3(kThreads), ProductCfg<MT>::SMEM_BYTES,
-              stream);
+template <int MT, bool FIRST, bool ANY>
+cudaError_t product_with(const ExpertsArgs& a, int num_sms, cudaStream_t stream) {
+  using Cfg = QueueCfg<MT, ANY>;
+  static std::atomic<bool> done[64];
+  auto kern = experts_queue_kernel<MT, FIRST, ANY>;
+  const cudaError_t e = allow_smem(kern, Cfg::SMEM_BYTES, done);
+  if (e != cudaSuccess) return e;
+  PdlLaunch l(dim3(static_cast<unsigned>(num_sms * Cfg::CTAS)), dim3(kThreads + 32), Cfg::SMEM_BYTES, stream);
   return cudaLaunchKernelEx(&l.cfg, kern, a);
 }
 
@@ -733,16 +636,21 @@ int token_tiles(const ExpertsArgs& a) {
   return a.M * a.k > 16 * a.E ? 4 : 2;
 }
 
-template <bool FIRST>
-cudaError_t product(const ExpertsArgs& a, bool vec, int num_sms, cudaStream_t stream) {
+template <bool FIRST, bool ANY>
+cudaError_t product_tiles(const ExpertsArgs& a, int num_sms, cudaStream_t stream) {
   switch (token_tiles(a)) {
     case 1:
-      return product_with<1, FIRST>(a, vec, num_sms, stream);
+      return product_with<1, FIRST, ANY>(a, num_sms, stream);
     case 2:
-      return product_with<2, FIRST>(a, vec, num_sms, stream);
+      return product_with<2, FIRST, ANY>(a, num_sms, stream);
     default:
-      return product_with<4, FIRST>(a, vec, num_sms, stream);
+      return product_with<4, FIRST, ANY>(a, num_sms, stream);
   }
+}
+
+template <bool FIRST>
+cudaError_t product(const ExpertsArgs& a, bool vec, int num_sms, cudaStream_t stream) {
+  return vec ? product_tiles<FIRST, false>(a, num_sms, stream) : product_tiles<FIRST, true>(a, num_sms, stream);
 }
 
 int64_t align16(int64_t bytes) { return (bytes + 15) / 16 * 16; }

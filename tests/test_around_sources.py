@@ -13,8 +13,7 @@ ADDRESSING = {
                                "residual_norm_sums_kernel", "residual_norm_means_kernel",
                                "residual_norm_partials_kernel", "residual_norm_backward_kernel"),
     "hgemm_adamw.cu": ("adamw_eight", "adamw_bytes", "adamw_load_kernel"),
-    "hgemm_experts.cu": ("experts_router_kernel", "load_piece", "put_unit", "experts_queue_kernel",
-                         "experts_sum_kernel"),
+    "hgemm_experts.cu": ("experts_router_kernel", "put_unit", "experts_queue_kernel", "experts_sum_kernel"),
 }
 
 
@@ -50,12 +49,10 @@ def test_what_is_read_before_the_wait_goes_past_l1():
     """The second product's routing and weights are read before its wait, behind
     a fence, with accesses that go to L2."""
     text = code(sources()["hgemm_experts.cu"])
-    for k in ("experts_product_kernel", "experts_queue_kernel"):
-        body = kernel(text, k)
-        assert "fence_gpu()" in body[:body.index("find_entries<")]
+    queue = kernel(text, "experts_queue_kernel")
+    assert "fence_gpu()" in queue[:queue.index("find_entries<")]
     entries = kernel(text, "find_entries")
     assert "ld_gpu_s32(a.ws_chosen" in entries and "a.ws_chosen[" not in entries
-    queue = kernel(text, "experts_queue_kernel")
-    assert "copy(to, w0, true)" in queue and "cp_async_16(to" in queue
+    assert "copy(to, w0, true)" in queue and "copy(to + Cfg::ROWS, w1, true)" in queue
+    assert re.search(r"if \(weights\)\s*cp_async_16\(to, p, bytes\);", queue)
     assert ".cg" in kernel(code(sources()["ptx.cuh"]), "cp_async_16")
-    assert "weights ? ld_gpu_u16(" in kernel(text, "load_piece")
