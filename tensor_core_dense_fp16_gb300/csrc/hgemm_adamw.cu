@@ -15,7 +15,7 @@ namespace hg {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChunk = kAdamwChunk;  // values of a block's step: 8 per thread, whole groups
+constexpr int kChunk = 2048;  // values that a block moves at once: 8 per thread, whole groups
 static_assert(kChunk == kThreads * 8 && kChunk % kCkptGroup == 0, "a group lies in one warp's values");
 
 // The tensors travel as the launch's parameters: nothing has to be copied
@@ -418,27 +418,27 @@ __global__ void __launch_bounds__(kThreads, 3) adamw_kernel(const __grid_constan
 }
 
 template <int MAX>
-cudaError_t adamw_with(const AdamwEntry* t, int count, uint32_t chunks, const AdamwStep& step, int num_sms,
-                       cudaStream_t stream) {
+cudaError_t adamw_with(const AdamwEntry* t, int count, const AdamwStep& step, int num_sms, cudaStream_t stream) {
   AdamwTable<MAX> table;
   table.step = step;
   table.count = count;
+  auto steps_of = [](const AdamwEntry& x, int64_t values) { return static_cast<uint32_t>((x.n + values - 1) / values); };
+  uint32_t chunks = 0;  // (384 tensors of 2^31 values are 2^29 of them)
+  for (int i = 0; i < count; ++i) chunks += steps_of(t[i], kChunk);
   // Eight chunks a step where that leaves every block a few steps: the search
   // for the tensor and its addresses are paid for once (100 M values with
   // 8-bit states, and read back: 467 us with one, 373 with four, 359 with eight;
   // 33.6 M with FP32 states 144, 141, 143). More blocks than fit at once balance
   // better than one wave of them (FP32 states: 160 us with 3 an SM, 143 with 16).
   table.per = chunks >= static_cast<uint32_t>(num_sms) * 32u ? 8 : 1;
-  chunks = 0;
+  table.chunks = 0;
   for (int i = 0; i < count; ++i) {
     table.t[i] = t[i];
-    table.t[i].chunk0 = chunks;
-    const int64_t step_values = static_cast<int64_t>(kChunk) * table.per;
-    chunks += static_cast<uint32_t>((t[i].n + step_values - 1) / step_values);
+    table.t[i].chunk0 = table.chunks;
+    table.chunks += steps_of(t[i], static_cast<int64_t>(kChunk) * table.per);
   }
-  table.chunks = chunks;
   const uint32_t most = static_cast<uint32_t>(num_sms) * 16u;
-  PdlLaunch l(dim3(chunks < most ? chunks : most), dim3(kThreads), 0, stream);
+  PdlLaunch l(dim3(table.chunks < most ? table.chunks : most), dim3(kThreads), 0, stream);
   return cudaLaunchKernelEx(&l.cfg, adamw_kernel<MAX>, table);
 }
 
@@ -495,10 +495,9 @@ __global__ void __launch_bounds__(kThreads)
 
 }  // namespace
 
-cudaError_t launch_adamw(const AdamwEntry* t, int count, uint32_t chunks, const AdamwStep& step, int num_sms,
-                         cudaStream_t stream) {
-  if (count <= 16) return adamw_with<16>(t, count, chunks, step, num_sms, stream);
-  return adamw_with<kAdamwTensors>(t, count, chunks, step, num_sms, stream);
+cudaError_t launch_adamw(const AdamwEntry* t, int count, const AdamwStep& step, int num_sms, cudaStream_t stream) {
+  if (count <= 16) return adamw_with<16>(t, count, step, num_sms, stream);
+  return adamw_with<kAdamwTensors>(t, count, step, num_sms, stream);
 }
 
 cudaError_t launch_adamw_load(const int8_t* m, const float* ms, const uint8_t* v, const float* vs, float* m_out,

@@ -421,12 +421,10 @@ int hgemm_adamw(const hgemm_adamw_tensor* tensors, int64_t count, double lr, dou
   auto aligned = [](const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; };
   hg::AdamwEntry e[hg::kAdamwTensors];
   int n = 0;
-  uint32_t chunks = 0;
   for (int64_t i = 0; i <= count; ++i) {
     if (n == hg::kAdamwTensors || (i == count && n > 0)) {
-      if ((rc = hg::cuda_status(hg::launch_adamw(e, n, chunks, s, dev.num_sms, stream))) != HGEMM_OK) return rc;
+      if ((rc = hg::cuda_status(hg::launch_adamw(e, n, s, dev.num_sms, stream))) != HGEMM_OK) return rc;
       n = 0;
-      chunks = 0;
     }
     if (i == count || tensors[i].n == 0) continue;
     const hgemm_adamw_tensor& x = tensors[i];
@@ -434,9 +432,8 @@ int hgemm_adamw(const hgemm_adamw_tensor* tensors, int64_t count, double lr, dou
     const bool vec8 = aligned(x.weight, 16) && aligned(x.master, 16) && aligned(x.grad, 16) &&
                       aligned(x.m, state) && aligned(x.v, state);
     e[n++] = hg::AdamwEntry{x.weight, x.master, x.grad, x.m, x.v, x.m_scales, x.v_scales, x.n, x.weight_decay,
-                            static_cast<float>(1.0 - lr * x.weight_decay), chunks,
+                            static_cast<float>(1.0 - lr * x.weight_decay), 0u,
                             static_cast<int16_t>(x.grad_type), static_cast<int16_t>(vec8)};
-    chunks += static_cast<uint32_t>((x.n + hg::kAdamwChunk - 1) / hg::kAdamwChunk);
   }
   return HGEMM_OK;
 }

@@ -3,6 +3,7 @@
 // are bound by memory: forward reads 4 bytes per value and writes 4, backward
 // reads 8 and writes 4.
 #include <atomic>
+#include <type_traits>
 
 #include <cuda_fp16.h>
 
@@ -685,53 +686,115 @@ __device__ __forceinline__ BackRow back_row(const ResidualNormBackArgs& a, int64
   return r;
 }
 
-// dz of one value.
-__device__ __forceinline__ float back_dz(const ResidualNormBackArgs& a, const BackRow& r, int64_t m, int64_t d) {
-  float v = a.dz ? half_at(a.dz, m * a.lddz + d) : 0.f;
-  if (a.pre) {
-    const float g = half_at(a.dh, m * a.lddh + d) * half_at(a.pre_gamma, d);
-    const float zh = (half_at(a.z, m * a.ldz + d) - r.mz) * r.rz;
-    v = fmaf(r.rz, g - r.a1 - zh * r.a2, v);
+// N of a row's values per thread, kThreads apart from column d on, their loads
+// all under way at once. KIND: which operands there are.
+template <bool POST_, bool PRE_, bool DZ_>
+struct BackKind {
+  static constexpr bool POST = POST_, PRE = PRE_, DZ = DZ_;
+};
+
+template <int N>
+struct BackValues {
+  float dz[N], dh[N], z[N], y[N], gamma[N], gate[N], w[N];
+};
+
+template <typename Kind, int N>
+__device__ __forceinline__ BackValues<N> back_values(const ResidualNormBackArgs& a, int64_t m, int64_t d) {
+  BackValues<N> v;
+  const uint16_t *dz = a.dz + m * a.lddz + d, *dh = a.dh + m * a.lddh + d, *z = a.z + m * a.ldz + d;
+  const uint16_t* y = a.y + m * a.ldy + d;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    v.dz[i] = Kind::DZ ? half_at(dz, i * kThreads) : 0.f;
+    v.dh[i] = Kind::PRE ? half_at(dh, i * kThreads) : 0.f;
+    v.z[i] = Kind::PRE ? half_at(z, i * kThreads) : 0.f;
+    v.y[i] = half_at(y, i * kThreads);
+    v.gamma[i] = Kind::PRE ? half_at(a.pre_gamma, d + i * kThreads) : 0.f;
+    v.w[i] = Kind::POST ? half_at(a.post_gamma, d + i * kThreads) : 0.f;
+    v.gate[i] = 1.f;
   }
+  if (a.gate) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v.gate[i] = half_at(a.gate, d + i * kThreads);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) v.w[i] *= v.gate[i];
   return v;
 }
 
-__device__ __forceinline__ float back_yh(const ResidualNormBackArgs& a, const BackRow& r, int64_t m, int64_t d) {
-  return (half_at(a.y, m * a.ldy + d) - r.my) * r.ry;
+// body(values, column of the first, how many) over a row's columns.
+template <typename Kind, typename Body>
+__device__ __forceinline__ void each_back_value(const ResidualNormBackArgs& a, int64_t m, Body body) {
+  constexpr int N = 4;
+  int64_t d = threadIdx.x;
+  for (; d + (N - 1) * kThreads < a.D; d += N * kThreads) {
+    const BackValues<N> v = back_values<Kind, N>(a, m, d);
+    body(v, d, std::integral_constant<int, N>{});
+  }
+  for (; d < a.D; d += kThreads) {
+    const BackValues<1> v = back_values<Kind, 1>(a, m, d);
+    body(v, d, std::integral_constant<int, 1>{});
+  }
+}
+
+// dz of one value.
+template <typename Kind>
+__device__ __forceinline__ float back_dz(const BackRow& r, float dz, float dh, float z, float gamma) {
+  return Kind::PRE ? fmaf(r.rz, dh * gamma - r.a1 - (z - r.mz) * r.rz * r.a2, dz) : dz;
 }
 
 // Rows that bulk copies cannot describe, or longer than the ring takes: rows
 // m0 .. m1-1, whose means the workspace holds. First the four means of every
-// row ...
+// row, from the ring's sums ...
+template <typename Kind>
 __global__ void __launch_bounds__(kThreads) residual_norm_means_kernel(const ResidualNormBackArgs a) {
-  __shared__ float s[kThreads / 32];
+  __shared__ float s[kThreads / 32][8];
   grid_dependency_wait();
   grid_launch_dependents();
-  const float n = static_cast<float>(a.D);
+  const float inv_d = 1.f / static_cast<float>(a.D);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int64_t m = a.m0 + blockIdx.x; m < a.m1; m += gridDim.x) {
     if (!HG_DBG_INDEX(m, a.M)) return;
-    BackRow r = back_row(a, m);
-    float s1 = 0.f, s2 = 0.f;
-    if (a.pre) {
-      for (int64_t d = threadIdx.x; d < a.D; d += kThreads) {
-        const float g = half_at(a.dh, m * a.lddh + d) * half_at(a.pre_gamma, d);
-        s1 += g;
-        s2 = fmaf(g, (half_at(a.z, m * a.ldz + d) - r.mz) * r.rz, s2);
+    const BackRow r = back_row(a, m);
+    float sums[8] = {};
+    each_back_value<Kind>(a, m, [&](const auto& v, int64_t, auto n) {
+#pragma unroll
+      for (int i = 0; i < decltype(n)::value; ++i) {
+        const float zh = (v.z[i] - r.mz) * r.rz, g = v.dh[i] * v.gamma[i];
+        const float t = fmaf(g, r.rz, v.dz[i]), wy = (v.y[i] - r.my) * r.ry * v.w[i];
+        if (Kind::PRE) {
+          sums[0] = fmaf(g, zh, sums[0]);
+          sums[3] += g;
+        }
+        if (Kind::POST) {
+          sums[1] = fmaf(wy, t, sums[1]);
+          sums[4] = fmaf(v.w[i], t, sums[4]);
+        }
+        if (Kind::PRE && Kind::POST) {
+          sums[2] = fmaf(wy, zh, sums[2]);
+          sums[5] = fmaf(v.w[i], zh, sums[5]);
+          sums[6] += wy;
+          sums[7] += v.w[i];
+        }
       }
-      if (a.pre == HGEMM_NORM_LAYER) r.a1 = group_sum<kThreads>(s1, s) / n;
-      r.a2 = group_sum<kThreads>(s2, s) / n;
-    }
-    if (a.post) {
-      s1 = s2 = 0.f;
-      for (int64_t d = threadIdx.x; d < a.D; d += kThreads) {
-        const float w = half_or(a.gate, d, 1.f) * half_at(a.post_gamma, d) * back_dz(a, r, m, d);
-        s1 += w;
-        s2 = fmaf(w, back_yh(a, r, m, d), s2);
+    });
+    const float mine = warp_sums(sums);  // lane l: sum l & 7
+    __syncthreads();                     // the row before has been read
+    if (lane < 8) s[warp][lane] = mine;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        sums[j] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) sums[j] += s[w][j];
+        sums[j] *= inv_d;
       }
-      if (a.post == HGEMM_NORM_LAYER) r.b1 = group_sum<kThreads>(s1, s) / n;
-      r.b2 = group_sum<kThreads>(s2, s) / n;
+      const float a1 = a.pre == HGEMM_NORM_LAYER ? sums[3] : 0.f, a2 = a.pre ? sums[0] : 0.f;
+      const float b1 = a.post == HGEMM_NORM_LAYER ? sums[4] - r.rz * (a1 * sums[7] + a2 * sums[5]) : 0.f;
+      const float b2 = a.post ? sums[1] - r.rz * (a1 * sums[6] + a2 * sums[2]) : 0.f;
+      reinterpret_cast<float4*>(a.means)[m - a.m0] = make_float4(a1, a2, b1, b2);
     }
-    if (threadIdx.x == 0) reinterpret_cast<float4*>(a.means)[m - a.m0] = make_float4(r.a1, r.a2, r.b1, r.b2);
   }
 }
 
@@ -743,55 +806,77 @@ __device__ __forceinline__ BackRow back_row_means(const ResidualNormBackArgs& a,
 }
 
 // ... then partial sums down the columns (dX may be dZ and dY may be dH):
-// S1 = Σ dz·ŷ, S0 = Σ dz, T1 = Σ dH·ẑ, T0 = Σ dH ...
-constexpr int kSlices = 32;
+// S1 = Σ dz·ŷ, S0 = Σ dz, T1 = Σ dH·ẑ, T0 = Σ dH. Four columns a thread, 32
+// apart, which share a row's statistics and means ...
+constexpr int kSlices = 80, kSumColumns = 128;
+template <typename Kind>
 __global__ void __launch_bounds__(kThreads) residual_norm_partials_kernel(const ResidualNormBackArgs a) {
   __shared__ float s[4][8][33];
   grid_dependency_wait();
   grid_launch_dependents();
   const int c = threadIdx.x & 31, row = threadIdx.x >> 5;
-  const int64_t d = static_cast<int64_t>(blockIdx.x) * 32 + c;
-  float v[4] = {};
-  if (d < a.D) {
-    for (int64_t m = a.m0 + blockIdx.y * 8 + row; m < a.m1; m += 8 * kSlices) {
-      const BackRow r = back_row_means(a, m);
-      const float dz = back_dz(a, r, m, d);
-      v[0] = fmaf(dz, back_yh(a, r, m, d), v[0]);
-      v[1] += dz;
-      if (a.pre) {
-        const float dh = half_at(a.dh, m * a.lddh + d);
-        v[2] = fmaf(dh, (half_at(a.z, m * a.ldz + d) - r.mz) * r.rz, v[2]);
-        v[3] += dh;
+  const int64_t d = static_cast<int64_t>(blockIdx.x) * kSumColumns + c;
+  float v[4][4] = {}, gamma[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) gamma[k] = Kind::PRE && d + 32 * k < a.D ? half_at(a.pre_gamma, d + 32 * k) : 0.f;
+  for (int64_t m = a.m0 + blockIdx.y * 8 + row; m < a.m1; m += 8 * kSlices) {
+    const BackRow r = back_row_means(a, m);
+    float dz[4] = {}, dh[4] = {}, z[4] = {}, y[4] = {};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (d + 32 * k < a.D) {
+        if (Kind::DZ) dz[k] = half_at(a.dz, m * a.lddz + d + 32 * k);
+        if (Kind::PRE) dh[k] = half_at(a.dh, m * a.lddh + d + 32 * k);
+        if (Kind::PRE) z[k] = half_at(a.z, m * a.ldz + d + 32 * k);
+        y[k] = half_at(a.y, m * a.ldy + d + 32 * k);
+      }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float g = back_dz<Kind>(r, dz[k], dh[k], z[k], gamma[k]);
+      v[k][0] = fmaf(g, (y[k] - r.my) * r.ry, v[k][0]);
+      v[k][1] += g;
+      if (Kind::PRE) {
+        v[k][2] = fmaf(dh[k], (z[k] - r.mz) * r.rz, v[k][2]);
+        v[k][3] += dh[k];
       }
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) s[i][row][c] = v[i];
-  __syncthreads();
-  if (row == 0 && d < a.D && HG_DBG_INDEX(blockIdx.y, kResidualNormPartials)) {
+  for (int k = 0; k < 4; ++k) {
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      for (int j = 1; j < 8; ++j) v[i] += s[i][j][c];
-      float* out = a.partials + (static_cast<int64_t>(blockIdx.y) * 4 + i) * a.D + d;
-      *out = a.m0 > 0 ? *out + v[i] : v[i];
+    for (int i = 0; i < 4; ++i) s[i][row][c] = v[k][i];
+    __syncthreads();
+    // warp i < 4: the sum i
+    if (row < 4 && d + 32 * k < a.D && HG_DBG_INDEX(blockIdx.y, kResidualNormPartials)) {
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum += s[row][j][c];
+      float* out = a.partials + (static_cast<int64_t>(blockIdx.y) * 4 + row) * a.D + d + 32 * k;
+      *out = a.m0 > 0 ? *out + sum : sum;
     }
   }
 }
 
 // ... then dX and dY.
+template <typename Kind>
 __global__ void __launch_bounds__(kThreads) residual_norm_backward_kernel(const ResidualNormBackArgs a) {
   grid_dependency_wait();
   grid_launch_dependents();
   for (int64_t m = a.m0 + blockIdx.x; m < a.m1; m += gridDim.x) {
     if (!HG_DBG_INDEX(m, a.M)) return;
     const BackRow r = back_row_means(a, m);
-    for (int64_t d = threadIdx.x; d < a.D; d += kThreads) {
-      const float dz = back_dz(a, r, m, d), gate = half_or(a.gate, d, 1.f);
-      float dy = gate * dz;
-      if (a.post) dy = r.ry * (dy * half_at(a.post_gamma, d) - r.b1 - back_yh(a, r, m, d) * r.b2);
-      a.dx[m * a.lddx + d] = __half_as_ushort(__float2half_rn(a.alpha * dz));
-      a.dy[m * a.lddy + d] = __half_as_ushort(__float2half_rn(dy));
-    }
+    each_back_value<Kind>(a, m, [&](const auto& v, int64_t d, auto n) {
+#pragma unroll
+      for (int i = 0; i < decltype(n)::value; ++i) {
+        const int64_t c = d + i * kThreads;
+        const float dz = back_dz<Kind>(r, v.dz[i], v.dh[i], v.z[i], v.gamma[i]);
+        const float dy =
+            Kind::POST ? r.ry * (v.w[i] * dz - r.b1 - (v.y[i] - r.my) * r.ry * r.b2) : v.gate[i] * dz;
+        a.dx[m * a.lddx + c] = __half_as_ushort(__float2half_rn(a.alpha * dz));
+        a.dy[m * a.lddy + c] = __half_as_ushort(__float2half_rn(dy));
+      }
+    });
   }
 }
 
@@ -919,6 +1004,21 @@ cudaError_t ring_group(const ResidualNormBackArgs& a, int num_sms, int* partials
                : ring_with<G, true, false, false>(a, plan, grid, stream);
 }
 
+template <typename Kind>
+cudaError_t any_rows_of(const ResidualNormBackArgs& a, cudaStream_t stream) {
+  cudaError_t e;
+  PdlLaunch r(dim3(rows_grid(a.m1 - a.m0)), dim3(kThreads), 0, stream);
+  if ((e = cudaLaunchKernelEx(&r.cfg, residual_norm_means_kernel<Kind>, a)) != cudaSuccess) return e;
+  PdlLaunch p(dim3(static_cast<unsigned>((a.D + kSumColumns - 1) / kSumColumns), kSlices), dim3(kThreads), 0, stream);
+  if ((e = cudaLaunchKernelEx(&p.cfg, residual_norm_partials_kernel<Kind>, a)) != cudaSuccess) return e;
+  return cudaLaunchKernelEx(&r.cfg, residual_norm_backward_kernel<Kind>, a);
+}
+
+template <bool POST, bool PRE>
+cudaError_t any_rows(const ResidualNormBackArgs& a, cudaStream_t stream) {
+  return a.dz ? any_rows_of<BackKind<POST, PRE, true>>(a, stream) : any_rows_of<BackKind<POST, PRE, false>>(a, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_residual_norm_forward(const ResidualNormArgs& a, int num_sms, cudaStream_t stream) {
@@ -964,11 +1064,9 @@ cudaError_t launch_residual_norm_backward(ResidualNormBackArgs a, int num_sms, c
   }
   for (; a.m0 < a.M; a.m0 = a.m1) {
     a.m1 = a.m0 + most < a.M ? a.m0 + most : a.M;
-    PdlLaunch r(dim3(rows_grid(a.m1 - a.m0)), dim3(kThreads), 0, stream);
-    if ((e = cudaLaunchKernelEx(&r.cfg, residual_norm_means_kernel, a)) != cudaSuccess) return e;
-    PdlLaunch p(dim3(static_cast<unsigned>((a.D + 31) / 32), kSlices), dim3(kThreads), 0, stream);
-    if ((e = cudaLaunchKernelEx(&p.cfg, residual_norm_partials_kernel, a)) != cudaSuccess) return e;
-    if ((e = cudaLaunchKernelEx(&r.cfg, residual_norm_backward_kernel, a)) != cudaSuccess) return e;
+    e = a.post ? (a.pre ? any_rows<true, true>(a, stream) : any_rows<true, false>(a, stream))
+               : (a.pre ? any_rows<false, true>(a, stream) : any_rows<false, false>(a, stream));
+    if (e != cudaSuccess) return e;
     partials = kSlices;
   }
   if (!a.dgate && !a.dpost_gamma && !a.dpost_beta && !a.dpre_gamma && !a.dpre_beta) return e;

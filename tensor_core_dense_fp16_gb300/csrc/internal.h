@@ -385,9 +385,8 @@ struct ResidualNormBackArgs {
 cudaError_t launch_residual_norm_backward(ResidualNormBackArgs a, int num_sms, cudaStream_t stream);
 size_t residual_norm_backward_workspace(int64_t M, int64_t D);
 
-// One tensor of an AdamW step (hgemm_adamw_tensor), and where its chunks of
-// kAdamwChunk values begin in the launch's numbering.
-constexpr int kAdamwChunk = 2048;
+// One tensor of an AdamW step (hgemm_adamw_tensor), and where it begins in the
+// launch's numbering of work (set by the launch).
 constexpr int kAdamwTensors = 384;  // of one launch, its parameters at most 32764 bytes
 struct AdamwEntry {
   uint16_t* weight;
@@ -407,8 +406,7 @@ struct AdamwStep {
   float ln1, ln2;                         // ln β, for a step number that the device holds
   const hgemm_adamw_dynamic* dynamic;     // or null
 };
-cudaError_t launch_adamw(const AdamwEntry* t, int count, uint32_t chunks, const AdamwStep& step, int num_sms,
-                         cudaStream_t stream);
+cudaError_t launch_adamw(const AdamwEntry* t, int count, const AdamwStep& step, int num_sms, cudaStream_t stream);
 cudaError_t launch_adamw_load(const int8_t* m, const float* ms, const uint8_t* v, const float* vs, float* m_out,
                               float* v_out, int64_t n, int num_sms, cudaStream_t stream);
 
