@@ -645,38 +645,43 @@ def hgemm_adamw_tensors(tensors) -> AdamwTensors:
     ``v_scales``, float32, one per 64 values), and ``weight_decay`` (0 where not
     given). Made once for a program's tensors; all contiguous, of equal size, on
     one device, and none may share memory with another's outputs."""
+    import torch
+    f16, f32, i8, u8 = torch.float16, torch.float32, torch.int8, torch.uint8
     tensors = list(tensors)
     rows, device = [], None
     for i, t in enumerate(tensors):
         get = t.get
-        grad, ms, vs = get("grad"), get("m_scales"), get("v_scales")
+        grad = get("grad")
         if not t.keys() <= _ADAMW_FIELDS:
             raise TypeError(f"tensor {i}: unknown {sorted(set(t) - _ADAMW_FIELDS)}")
         for name in ("grad", "m", "v"):
             if get(name) is None:
                 raise ValueError(f"tensor {i}: {name} is missing")
-        eight = ms is not None or vs is not None
-        n = grad.numel()
-        half_grad = (_dtypes.get(grad.dtype) or str(grad.dtype)) == _F16
+        eight = get("m_scales") is not None or get("v_scales") is not None
+        n, groups = grad.numel(), 0
+        if eight:
+            groups = -(-n // HGEMM_CKPT8_GROUP)
+        half_grad = grad.dtype is f16
         row = []
-        for name, dtype, size in (("weight", _F16, n), ("master", _F32, n), ("grad", _F16 if half_grad else _F32, n),
-                                  ("m", _I8 if eight else _F32, n), ("v", _U8 if eight else _F32, n),
-                                  ("m_scales", _F32, -(-n // HGEMM_CKPT8_GROUP)),
-                                  ("v_scales", _F32, -(-n // HGEMM_CKPT8_GROUP))):
+        for name, dtype, size in (("weight", f16, n), ("master", f32, n), ("grad", f16 if half_grad else f32, n),
+                                  ("m", i8 if eight else f32, n), ("v", u8 if eight else f32, n),
+                                  ("m_scales", f32, groups), ("v_scales", f32, groups)):
             x = get(name)
             if x is None:
                 row.append(None)
                 continue
-            row.append(_dev(x, dtype, name))
-            if x.numel() != size:
-                raise ValueError(f"tensor {i}: {name} must have {size} values, got {x.numel()}")
-            if not x.is_contiguous():
-                raise ValueError(f"tensor {i}: {name} must be contiguous")
+            if x.dtype is not dtype:
+                raise TypeError(f"tensor {i}: {name} must be {dtype}, got {x.dtype}")
             at = x.get_device()
             if at != device:
+                if at < 0:
+                    raise ValueError(f"tensor {i}: {name} must be a CUDA tensor")
                 if device is not None:
                     raise ValueError(f"tensor {i}: {name} must be on cuda:{device}, got cuda:{at}")
                 device = at
+            if x.numel() != size or not x.is_contiguous():
+                raise ValueError(f"tensor {i}: {name} must be {size} values, contiguous, got {tuple(x.shape)}")
+            row.append(x.data_ptr())
         rows.append((*row, n, get("weight_decay", 0.0), HGEMM_TYPE_F16 if half_grad else HGEMM_TYPE_F32))
     plan = AdamwTensors((_AdamwTensor * len(rows))(*rows), tensors)
     hgemm_adamw_check(plan)

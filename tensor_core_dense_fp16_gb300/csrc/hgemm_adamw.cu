@@ -496,7 +496,10 @@ __global__ void __launch_bounds__(kThreads)
 }  // namespace
 
 cudaError_t launch_adamw(const AdamwEntry* t, int count, const AdamwStep& step, int num_sms, cudaStream_t stream) {
+  // (the parameters' bytes cost a launch time: 72 tensors of 4096, 6.8 us in the
+  // largest table, 6.1 in the middle one)
   if (count <= 16) return adamw_with<16>(t, count, step, num_sms, stream);
+  if (count <= 96) return adamw_with<96>(t, count, step, num_sms, stream);
   return adamw_with<kAdamwTensors>(t, count, step, num_sms, stream);
 }
 
