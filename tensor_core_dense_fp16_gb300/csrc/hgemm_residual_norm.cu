@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kThreads) residual_norm_long_kernel(const Resi
 // the time of a pass. Both passes read shared memory, which keeps the
 // registers for the column sums. The barrier of the exchange also frees the
 // stage of the row before: every thread of the group has finished its pass 2
-// by then, and the group's first thread copies a row into it.
+// by then, and a row is copied into it.
 //
 // FULL: a layer norm, or a beta's gradient, is among what is wanted: four
 // column sums and the sums along the row that only these need. RMS norms
@@ -301,7 +301,9 @@ struct RingCfg {
   static constexpr int WARPS = G / 32;  // per group
   static constexpr int MAX_STAGES = 8;
   static constexpr int RING_BYTES = 192 * 1024;  // of the CTA
-  static constexpr int OFF_W = RING_BYTES;       // FULL: gate·post_gamma of up to 8192 columns
+  static constexpr int OFF_W = RING_BYTES;       // FULL: gate·post_gamma of up to 8192 columns,
+  static constexpr bool SHARED_GAMMA = 2 * G <= THREADS;
+  static constexpr int OFF_GAMMA = OFF_W + G * 8 * NV * 4;  // with pre_gamma behind it where there is room
   static constexpr int OFF_BAR = OFF_W + THREADS * 8 * NV * 4;
   static constexpr int OFF_EXCHANGE = OFF_BAR + GROUPS * MAX_STAGES * 8;
   static constexpr int OFF_MISC = OFF_EXCHANGE + 2 * (THREADS / 32) * 32;  // two buffers of eight sums per warp
@@ -331,10 +333,20 @@ __device__ __forceinline__ float warp_sums(float (&v)[N]) {
   return r;
 }
 
-// A row's statistics, and where it lies in shared memory.
+// A row's statistics (mean and 1/σ of Y, then of Z), and where it lies in the
+// ring. LANES: one to a lane (lane % 4), handed out by a shuffle, and an offset
+// in place of an address: two registers in place of six for each of the three
+// rows under way.
+template <bool LANES>
 struct RingRow {
-  float my, ry, mz, rz;
-  const uint8_t* at;
+  float stat[LANES ? 1 : 4];
+  std::conditional_t<LANES, uint32_t, const uint8_t*> at;
+  __device__ float of(int i) const {
+    if constexpr (LANES)
+      return __shfl_sync(0xffffffffu, stat[0], i);
+    else
+      return stat[i];
+  }
 };
 
 template <int G, bool POST, bool PRE, bool FULL>
@@ -365,30 +377,44 @@ __global__ void __launch_bounds__(512, 1) residual_norm_ring_kernel(const Residu
 
   const int64_t first = static_cast<int64_t>(blockIdx.x) * Cfg::GROUPS + group;
   const int64_t step = static_cast<int64_t>(gridDim.x) * Cfg::GROUPS;
-  int copied = 0;  // rows the group's first thread has issued
+  // With all sums of both norms the arithmetic is what a row waits for: the
+  // first lanes of four warps issue its copies, an operand each, since one
+  // thread's hold its warp up, and then the group (layer norms, 16384×4096: 191
+  // µs by one thread, 168 by four). Elsewhere memory is, and one thread is
+  // faster (RMS norms 122 and 124, one layer norm 123 and 136), with the
+  // statistics in registers.
+  constexpr bool BUSY = FULL && POST && PRE;
+  constexpr int COPIERS = !BUSY ? 1 : Cfg::WARPS < 4 ? Cfg::WARPS : 4;
+  const bool copier = lane == 0 && t < 32 * COPIERS;
+  int copied = 0;  // rows that this thread has issued copies of
   auto copy_row = [&](int64_t m, int stage) {
     if (plan.empty) return;
     ++copied;
     const uint32_t bar = bar0 + 8u * stage, dst = ring_addr + static_cast<uint32_t>(stage) * plan.stage_bytes;
-    if (!(a.inject == 1 && copied == 1))  // testing aid: withhold one arrival
+    const int who = COPIERS == 1 ? 0 : t / 32;
+    if (t == 0 && !(a.inject == 1 && copied == 1))  // testing aid: withhold one arrival
       mbar_arrive_expect_tx(bar, plan.stage_bytes);
-    if (a.dz) bulk_load(dst + plan.dz, a.dz + m * a.lddz, row_bytes, bar);
+    if (a.dz && who == 0) bulk_load(dst + plan.dz, a.dz + m * a.lddz, row_bytes, bar);
     if (PRE) {
-      bulk_load(dst + plan.dh, a.dh + m * a.lddh, row_bytes, bar);
-      bulk_load(dst + plan.z, a.z + m * a.ldz, row_bytes, bar);
+      if (who == 1 % COPIERS) bulk_load(dst + plan.dh, a.dh + m * a.lddh, row_bytes, bar);
+      if (who == 2 % COPIERS) bulk_load(dst + plan.z, a.z + m * a.ldz, row_bytes, bar);
     }
-    if (POST || plan.need_y) bulk_load(dst + plan.y, a.y + m * a.ldy, row_bytes, bar);
+    if ((POST || plan.need_y) && who == 3 % COPIERS) bulk_load(dst + plan.y, a.y + m * a.ldy, row_bytes, bar);
   };
-  if (t == 0)
+  if (copier)
     for (int i = 0; i < stages - 1; ++i)
       if (first + i * step < a.M) copy_row(first + i * step, i);
 
   // w = gate·post_gamma, and the norm in front's gamma; the sums dz·ŷ, dz,
   // dH·ẑ and dH of this thread's columns
-  // (FULL keeps w in shared memory: its sums leave too few registers)
+  // (FULL keeps w in shared memory, and pre_gamma where there is room for it:
+  // its sums leave too few registers. Layer norms, 16384×4096: 207 µs with gamma
+  // in registers, 195 this way.)
+  constexpr bool SHARED_GAMMA = FULL && PRE && Cfg::SHARED_GAMMA;
   f32x2 w[FULL ? 1 : NV][4];
   uint4 gamma[NV];
   ulonglong2* shared_w = reinterpret_cast<ulonglong2*>(ring_smem + Cfg::OFF_W);
+  ulonglong2* shared_gamma = reinterpret_cast<ulonglong2*>(ring_smem + Cfg::OFF_GAMMA);
   f32x2 s1[NV][4], s0[NV][4], t1[NV][4], t0[NV][4];
   float sum_w = 0.f;
 #pragma unroll
@@ -416,6 +442,11 @@ __global__ void __launch_bounds__(512, 1) residual_norm_ring_kernel(const Residu
       if (group == 0) {
         shared_w[(t + i * G) * 2] = make_ulonglong2(v[0], v[1]);
         shared_w[(t + i * G) * 2 + 1] = make_ulonglong2(v[2], v[3]);
+        if constexpr (SHARED_GAMMA) {
+          unpack8(gamma[i], f);
+          shared_gamma[(t + i * G) * 2] = make_ulonglong2(f[0], f[1]);
+          shared_gamma[(t + i * G) * 2 + 1] = make_ulonglong2(f[2], f[3]);
+        }
       }
     } else {
 #pragma unroll
@@ -433,36 +464,57 @@ __global__ void __launch_bounds__(512, 1) residual_norm_ring_kernel(const Residu
       for (int k = 0; k < 4; ++k) v[k] = w[i][k];
     }
   };
+  auto gammas = [&](int i, f32x2 (&v)[4]) {
+    if constexpr (SHARED_GAMMA) {
+      const ulonglong2 lo = shared_gamma[(t + i * G) * 2], hi = shared_gamma[(t + i * G) * 2 + 1];
+      v[0] = lo.x, v[1] = lo.y, v[2] = hi.x, v[3] = hi.y;
+    } else {
+      unpack8(gamma[i], v);
+    }
+  };
 
   const float inv_d = 1.f / static_cast<float>(D);
   const bool layer_y = POST && a.post == HGEMM_NORM_LAYER, layer_z = PRE && a.pre == HGEMM_NORM_LAYER;
   int stage = 0;  // of the next row that pass 1 takes
   uint32_t phase = 0;
   auto fetch_stats = [&](int64_t m) {
-    RingRow r{0.f, 1.f, 0.f, 1.f, nullptr};
-    if (m < a.M) {
-      if (POST) r.ry = a.stats[a.M + m];
-      if (layer_y) r.my = a.stats[m];
-      if (PRE) r.rz = a.stats[3 * a.M + m];
-      if (layer_z) r.mz = a.stats[2 * a.M + m];
+    RingRow<BUSY> r;
+    r.at = 0;
+#pragma unroll
+    for (int i = 0; i < (BUSY ? 1 : 4); ++i) {
+      const int which = BUSY ? lane & 3 : i;
+      const bool known = which == 0 ? layer_y : which == 1 ? POST : which == 2 ? layer_z : PRE;
+      r.stat[i] = static_cast<float>(which & 1);
+      if (known && m < a.M) r.stat[i] = a.stats[which * a.M + m];
     }
     return r;
   };
+  auto in_ring = [&](const RingRow<BUSY>& r) -> const uint8_t* {
+    if constexpr (BUSY)
+      return ring + r.at;
+    else
+      return r.at;
+  };
   // The sums along a row, over this warp's columns, into the exchange:
   // Σ g·ẑ, w·ŷ·t, w·ŷ·ẑ, and FULL Σ g, w·t, w·ẑ, w·ŷ, w.
-  auto pass1 = [&](RingRow& r, int flip) {
+  auto pass1 = [&](RingRow<BUSY>& r, int flip) {
     // A wait that gives up has raised the abort flag: no more copies are
     // issued, later waits give up at once, and the loop runs out on what the
     // ring holds, so that every thread still reaches every barrier.
     if (!plan.empty) (void)wait_phase(bar0 + 8u * stage, phase, wd, kWdRows);
-    r.at = ring + static_cast<uint32_t>(stage) * plan.stage_bytes;
+    if constexpr (BUSY)
+      r.at = static_cast<uint32_t>(stage) * plan.stage_bytes;
+    else
+      r.at = ring + static_cast<uint32_t>(stage) * plan.stage_bytes;
     if (++stage == stages) {
       stage = 0;
       phase ^= 1u;
     }
     if constexpr (POST || PRE) {
       // (v̂ from the difference: v·ρ − μ·ρ loses its digits in a row far from zero)
-      const f32x2 scale_z = pair_of(r.rz), shift_z = pair_of(-r.mz), scale_y = pair_of(r.ry), shift_y = pair_of(-r.my);
+      const f32x2 scale_z = pair_of(r.of(3)), shift_z = pair_of(-r.of(2));
+      const f32x2 scale_y = pair_of(r.of(1)), shift_y = pair_of(-r.of(0));
+      const uint8_t* at = in_ring(r);
       f32x2 p[7] = {0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -470,16 +522,16 @@ __global__ void __launch_bounds__(512, 1) residual_norm_ring_kernel(const Residu
         if (v * 8 < D) {
           f32x2 z[4], tt[4], y[4], g[4];
           if (POST && a.dz) {
-            unpack8(reinterpret_cast<const uint4*>(r.at + plan.dz)[v], tt);
+            unpack8(reinterpret_cast<const uint4*>(at + plan.dz)[v], tt);
           } else {
 #pragma unroll
             for (int k = 0; k < 4; ++k) tt[k] = 0;
           }
           if constexpr (PRE) {
             f32x2 q[4];
-            unpack8(reinterpret_cast<const uint4*>(r.at + plan.z)[v], z);
-            unpack8(reinterpret_cast<const uint4*>(r.at + plan.dh)[v], g);
-            unpack8(gamma[i], q);
+            unpack8(reinterpret_cast<const uint4*>(at + plan.z)[v], z);
+            unpack8(reinterpret_cast<const uint4*>(at + plan.dh)[v], g);
+            gammas(i, q);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               if constexpr (FULL) z[k] = add2(z[k], shift_z);
@@ -493,7 +545,7 @@ __global__ void __launch_bounds__(512, 1) residual_norm_ring_kernel(const Residu
           if constexpr (POST) {
             f32x2 wv[4];
             weights(i, wv);
-            unpack8(reinterpret_cast<const uint4*>(r.at + plan.y)[v], y);
+            unpack8(reinterpret_cast<const uint4*>(at + plan.y)[v], y);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               if constexpr (FULL) y[k] = add2(y[k], shift_y);
@@ -520,7 +572,7 @@ __global__ void __launch_bounds__(512, 1) residual_norm_ring_kernel(const Residu
     }
   };
 
-  RingRow row = fetch_stats(first), next = fetch_stats(first + step);
+  RingRow<BUSY> row = fetch_stats(first), next = fetch_stats(first + step);
   int flip = 0;
   if (first < a.M) pass1(row, 0);
   for (int64_t m = first; m < a.M; m += step) {
@@ -528,7 +580,7 @@ __global__ void __launch_bounds__(512, 1) residual_norm_ring_kernel(const Residu
       named_bar_sync(1 + group, G);
     else
       __syncwarp();
-    if (t == 0) {
+    if (copier) {
       // the stage of the row before this one is free: the group is past it
       const int64_t ahead = m + (stages - 1) * step;
       const int into = stage == 0 ? stages - 1 : stage - 1;  // this row's
@@ -541,40 +593,42 @@ __global__ void __launch_bounds__(512, 1) residual_norm_ring_kernel(const Residu
       for (int i = 0; i < Cfg::WARPS; ++i) mine += ex[i * 8];
     }
     flip ^= 1;  // the other buffer next: nobody writes this one before everybody has read it
-    const RingRow after = fetch_stats(m + 2 * step);
+    const RingRow<BUSY> after = fetch_stats(m + 2 * step);
     if (m + step < a.M) pass1(next, flip);
 
     float sums[SUMS];
     mine *= inv_d;
 #pragma unroll
     for (int i = 0; i < SUMS; ++i) sums[i] = __shfl_sync(0xffffffffu, mine, i);
+    const float my = row.of(0), ry = row.of(1), mz = row.of(2), rz = row.of(3);
+    const uint8_t* at = in_ring(row);
     const float a1 = FULL && layer_z ? sums[SUMS - 5] : 0.f, a2 = sums[0];
-    float b1 = 0.f, b2 = sums[1] - row.rz * (a2 * sums[2]);
+    float b1 = 0.f, b2 = sums[1] - rz * (a2 * sums[2]);
     if constexpr (FULL) {
-      if (layer_y) b1 = sums[SUMS - 4] - row.rz * (a1 * sums[SUMS - 1] + a2 * sums[SUMS - 3]);
-      b2 -= row.rz * (a1 * sums[SUMS - 2]);
+      if (layer_y) b1 = sums[SUMS - 4] - rz * (a1 * sums[SUMS - 1] + a2 * sums[SUMS - 3]);
+      b2 -= rz * (a1 * sums[SUMS - 2]);
     }
     // dz = dZ + ρ_z·g + ẑ·k2 + k1;  dY = ρ_y·w·dz + ŷ·l2 + l1
-    const f32x2 scale_z = pair_of(row.rz), shift_z = pair_of(-row.mz);
-    const f32x2 scale_y = pair_of(row.ry), shift_y = pair_of(-row.my);
-    const f32x2 k1 = pair_of(-row.rz * a1), k2 = pair_of(-row.rz * a2);
-    const f32x2 l1 = pair_of(-row.ry * b1), l2 = pair_of(-row.ry * b2), alpha = pair_of(a.alpha);
+    const f32x2 scale_z = pair_of(rz), shift_z = pair_of(-mz);
+    const f32x2 scale_y = pair_of(ry), shift_y = pair_of(-my);
+    const f32x2 k1 = pair_of(-rz * a1), k2 = pair_of(-rz * a2);
+    const f32x2 l1 = pair_of(-ry * b1), l2 = pair_of(-ry * b2), alpha = pair_of(a.alpha);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = t + i * G;
       if (v * 8 < D) {
         f32x2 dz[4], z[4], g[4];
         if (a.dz) {
-          unpack8(reinterpret_cast<const uint4*>(row.at + plan.dz)[v], dz);
+          unpack8(reinterpret_cast<const uint4*>(at + plan.dz)[v], dz);
         } else {
 #pragma unroll
           for (int k = 0; k < 4; ++k) dz[k] = 0;
         }
         if constexpr (PRE) {
           f32x2 q[4];
-          unpack8(reinterpret_cast<const uint4*>(row.at + plan.z)[v], z);
-          unpack8(reinterpret_cast<const uint4*>(row.at + plan.dh)[v], g);
-          unpack8(gamma[i], q);
+          unpack8(reinterpret_cast<const uint4*>(at + plan.z)[v], z);
+          unpack8(reinterpret_cast<const uint4*>(at + plan.dh)[v], g);
+          gammas(i, q);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             if constexpr (FULL) z[k] = add2(z[k], shift_z);
@@ -590,7 +644,7 @@ __global__ void __launch_bounds__(512, 1) residual_norm_ring_kernel(const Residu
           }
         }
         const int64_t c = v * 8;
-        if (POST || plan.need_y) unpack8(reinterpret_cast<const uint4*>(row.at + plan.y)[v], z);
+        if (POST || plan.need_y) unpack8(reinterpret_cast<const uint4*>(at + plan.y)[v], z);
         weights(i, g);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -622,10 +676,11 @@ __global__ void __launch_bounds__(512, 1) residual_norm_ring_kernel(const Residu
   }
 
   // Every copy has landed, each waited for before its row, unless a wait gave
-  // up: the last copy into each stage lands before the CTA leaves.
+  // up: the last copy into each stage lands before the CTA leaves. (A thread
+  // that saw the flag before another has issued fewer; each waits for its own.)
   __syncthreads();
   if (*abort_flag) {
-    if (t == 0)
+    if (copier)
       for (int i = copied > stages ? copied - stages : 0; i < copied; ++i)
         wait_drain(bar0 + 8u * (i % stages), static_cast<uint32_t>(i / stages) & 1u, wd);
     __syncthreads();
