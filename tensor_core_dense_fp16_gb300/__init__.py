@@ -648,7 +648,7 @@ def hgemm_adamw_tensors(tensors) -> AdamwTensors:
     import torch
     f16, f32, i8, u8 = torch.float16, torch.float32, torch.int8, torch.uint8
     tensors = list(tensors)
-    rows, device = [], None
+    rows, keep, device = [], [], None
     for i, t in enumerate(tensors):
         get = t.get
         grad = get("grad")
@@ -682,8 +682,9 @@ def hgemm_adamw_tensors(tensors) -> AdamwTensors:
             if x.numel() != size or not x.is_contiguous():
                 raise ValueError(f"tensor {i}: {name} must be {size} values, contiguous, got {tuple(x.shape)}")
             row.append(x.data_ptr())
+            keep.append(x)
         rows.append((*row, n, get("weight_decay", 0.0), HGEMM_TYPE_F16 if half_grad else HGEMM_TYPE_F32))
-    plan = AdamwTensors((_AdamwTensor * len(rows))(*rows), tensors)
+    plan = AdamwTensors((_AdamwTensor * len(rows))(*rows), keep)
     hgemm_adamw_check(plan)
     return plan
 

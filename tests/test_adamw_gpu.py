@@ -274,6 +274,24 @@ def test_load(n, offset):
     same(a[5].get(), ref.kept_v(v, vs), "v")
 
 
+def test_a_table_keeps_its_tensors():
+    """The caller's dicts may be changed for the next table: a gradient that the
+    first one points to stays alive with it."""
+    import gc
+    import weakref
+    torch = torch_cuda()
+    t = {"grad": torch.zeros(64, dtype=torch.float16, device="cuda"), "master": torch.zeros(64, device="cuda"),
+         "m": torch.zeros(64, device="cuda"), "v": torch.zeros(64, device="cuda")}
+    held = weakref.ref(t["grad"])
+    first = tc.hgemm_adamw_tensors([t])
+    t["grad"] = torch.zeros(64, dtype=torch.float16, device="cuda")
+    gc.collect()
+    assert held() is not None
+    del first
+    gc.collect()
+    assert held() is None
+
+
 def test_refusals():
     torch = torch_cuda()
     f, h = torch.zeros(128, device="cuda"), torch.zeros(128, dtype=torch.float16, device="cuda")
