@@ -420,9 +420,9 @@ class AdamW:
         dynamic: see hgemm_adamw."""
         for name, t in zip(self.names, self.tensors):
             t["grad"] = gradients[name]
-        self.steps += 1
-        tc.hgemm_adamw(tc.hgemm_adamw_tensors(self.tensors), self.lr, self.beta1, self.beta2, self.eps, self.steps,
+        tc.hgemm_adamw(tc.hgemm_adamw_tensors(self.tensors), self.lr, self.beta1, self.beta2, self.eps, self.steps + 1,
                        grad_scale, dynamic, stream)
+        self.steps += 1  # (a refused step is none)
 
 
 def main() -> None:

@@ -233,6 +233,25 @@ def test_tokens_through_experts_between_norms(m):
     assert off(nxt, norm64(z64, rms, g3.double(), None)) < 4e-3
 
 
+def test_a_refused_step_is_not_counted():
+    from tensor_core_dense_fp16_gb300.feedforward import AdamW
+    torch = torch_cuda()
+    p = torch.ones(64, dtype=torch.float16, device="cuda")
+    g = torch.full((64,), 0.01, dtype=torch.float16, device="cuda")
+    one, other = AdamW({"p": p.clone()}, lr=0.1), AdamW({"p": p.clone()}, lr=0.1)
+    for bad in (g[:32], g.double()):
+        with pytest.raises((ValueError, TypeError)):
+            one.step({"p": bad})
+    with pytest.raises(Exception):
+        one.step({"p": g}, grad_scale=float("inf"))
+    for o in (one, other):
+        o.step({"p": g})
+        o.step({"p": g})
+    done()
+    assert one.steps == 2
+    assert torch.equal(one.tensors[0]["master"], other.tensors[0]["master"])
+
+
 def test_layers_are_checked():
     torch = torch_cuda()
     from tensor_core_dense_fp16_gb300.feedforward import AdamW, ExpertFeedForward, FeedForward, FeedForwardStack
