@@ -2,7 +2,9 @@
 // states read back (hgemm_adamw, hgemm_adamw_load; the formulas and the 8-bit
 // forms are in hgemm.h). Bound by memory: with FP32 states, a master copy, an
 // FP16 gradient and weight 28 bytes per value, with 8-bit states and no master
-// 10.25.
+// 10.25. Measured: 33.6 M values with FP32 states and master 139 us (6.8 TB/s, a
+// copy's rate); 100.8 M with 8-bit states 183 us (5.6 TB/s, issue slots 71%),
+// read back 153 us (6.7 TB/s).
 #include <cuda_fp16.h>
 
 #include "debug.cuh"
@@ -56,16 +58,18 @@ __device__ __forceinline__ void second_scale(uint32_t top_bits, float& scale, fl
 // and the leading 0) rounded at the 20th, counted from 1's; at least 1 where r
 // is not 0. (r = v·(1/top) is at most 1 + 2^-23, whose code is 255.) The caller
 // takes 0 in place of all codes of a group whose inv is 0.
-__device__ __forceinline__ uint32_t second_code(float v, float inv) {
-  const uint32_t r = __float_as_uint(__fmul_rn(v, inv));
+__device__ __forceinline__ uint32_t second_code(float v_over_top) {
+  const uint32_t r = __float_as_uint(v_over_top);
   const int c = static_cast<int>(r + ((255u << 20) + 0x80000u - kOneBits)) >> 20;
   return static_cast<uint32_t>(max(c, static_cast<int>(min(r, 1u))));
 }
 
-__device__ __forceinline__ float second_value(uint32_t code, float scale) {
-  const float r = code ? __uint_as_float((code << 20) + (kOneBits - (255u << 20))) : 0.f;
-  return __fmul_rn(r, scale);
+// What a code stands for, in units of the group's largest.
+__device__ __forceinline__ float second_unit(uint32_t code) {
+  return code ? __uint_as_float((code << 20) + (kOneBits - (255u << 20))) : 0.f;
 }
+
+__device__ __forceinline__ float second_value(uint32_t code, float scale) { return __fmul_rn(second_unit(code), scale); }
 
 // ------------------------------------------------------------------ the step
 
@@ -232,7 +236,7 @@ __device__ __forceinline__ void adamw_eight(const AdamwEntry& t, const AdamwStep
 #pragma unroll
       for (int j = i; j < (VEC ? 8 : i + 2); ++j) {
         qm[j] = inv_m == 0.f ? 0u : ckpt_code(m[j], inv_m);
-        qv[j] = inv_v == 0.f ? 0u : second_code(v[j], inv_v);
+        qv[j] = inv_v == 0.f ? 0u : second_code(__fmul_rn(v[j], inv_v));
       }
       const int lane = threadIdx.x & 31;
       const int64_t at = VEC ? first : first - lane + 32 * i;  // a value of the group
@@ -269,11 +273,12 @@ struct Packed {
 };
 
 template <bool WIDE>
-__device__ __forceinline__ void unpack_wide(const uint4 (&w)[WIDE ? 2 : 1], float (&f)[8]) {
+__device__ __forceinline__ void unpack_wide(const uint4 (&w)[WIDE ? 2 : 1], f32x2 (&f)[4]) {
   if constexpr (WIDE) {
-    f[0] = __uint_as_float(w[0].x), f[1] = __uint_as_float(w[0].y), f[2] = __uint_as_float(w[0].z);
-    f[3] = __uint_as_float(w[0].w), f[4] = __uint_as_float(w[1].x), f[5] = __uint_as_float(w[1].y);
-    f[6] = __uint_as_float(w[1].z), f[7] = __uint_as_float(w[1].w);
+    f[0] = pair_of(__uint_as_float(w[0].x), __uint_as_float(w[0].y));
+    f[1] = pair_of(__uint_as_float(w[0].z), __uint_as_float(w[0].w));
+    f[2] = pair_of(__uint_as_float(w[1].x), __uint_as_float(w[1].y));
+    f[3] = pair_of(__uint_as_float(w[1].z), __uint_as_float(w[1].w));
   } else {
     unpack8(w[0], f);
   }
@@ -307,25 +312,38 @@ __device__ __forceinline__ void adamw_bytes(const AdamwEntry& t, const AdamwStep
     const Packed<G32, MASTER> r = next;
     if (i + 1 < count) next = load(first + kChunk);
     const bool in = first < n;  // all eight
-    float g[8], p[8], m[8], v[8];
+    // Two values at a time. product2 is a product rounded by itself: a packed
+    // product and sum would be contracted into one rounding.
+    const f32x2 none = pair_of(s.minus_zero);
+    auto product2 = [&](f32x2 x, f32x2 y) { return fma2(x, y, none); };
+    f32x2 g[4], p[4], m[4], v[4];
     unpack_wide<G32>(r.g, g);
     unpack_wide<MASTER>(r.p, p);
     float top_m = 0.f, top_v = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; k += 2) {
-      unpair(ckpt_pair((k < 4 ? r.m.x : r.m.y) ^ 0x80808080u, (k & 3) / 2), m[k], m[k + 1]);
-#pragma unroll
-      for (int j = k; j < k + 2; ++j) {
-        m[j] = __fmul_rn(m[j], r.sm);
-        v[j] = second_value(__byte_perm(j < 4 ? r.v.x : r.v.y, 0u, 0x4440u + (j & 3)), r.sv);
-        adamw_value(s, c, keep, g[j], m[j], v[j], p[j]);
-      }
-      top_m = max_abs3(top_m, m[k], m[k + 1]);
-      top_v = max_abs3(top_v, v[k], v[k + 1]);
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t code = k < 2 ? r.v.x : r.v.y;
+      m[k] = mul2(ckpt_pair((k < 2 ? r.m.x : r.m.y) ^ 0x80808080u, k & 1), pair_of(r.sm));
+      v[k] = mul2(pair_of(second_unit(__byte_perm(code, 0u, 0x4440u + 2 * (k & 1))),
+                          second_unit(__byte_perm(code, 0u, 0x4441u + 2 * (k & 1)))),
+                  pair_of(r.sv));
+      g[k] = mul2(g[k], pair_of(c.gscale));
+      m[k] = add2(product2(m[k], pair_of(s.beta1)), product2(g[k], pair_of(s.rest1)));
+      v[k] = add2(product2(v[k], pair_of(s.beta2)), product2(product2(g[k], g[k]), pair_of(s.rest2)));
+      float a, b;
+      unpair(v[k], a, b);
+      top_v = max_abs3(top_v, a, b);
+      unpair(fma2(pair_of(sqrt_approx(a), sqrt_approx(b)), pair_of(c.b), pair_of(s.eps)), a, b);
+      p[k] = fma2(p[k], pair_of(keep), mul2(mul2(m[k], pair_of(-c.a)), pair_of(rcp_approx(a), rcp_approx(b))));
+      unpair(m[k], a, b);
+      top_m = max_abs3(top_m, a, b);
     }
     if (in) {
-      if (MASTER) store_f32<true>(t.master, first, n, p);
-      if (!MASTER || t.weight) store_f16<true>(t.weight, first, n, p);
+      if (MASTER) {
+        *reinterpret_cast<ulonglong2*>(t.master + first) = make_ulonglong2(p[0], p[1]);
+        *reinterpret_cast<ulonglong2*>(t.master + first + 4) = make_ulonglong2(p[2], p[3]);
+      }
+      if (!MASTER || t.weight) *reinterpret_cast<uint4*>(t.weight + first) = pack8(p);
     }
     // (a group lies whole in or past the tensor's last eight; what is past is not counted)
     uint32_t bits_m = in ? magnitude_bits(top_m) : 0u, bits_v = in ? magnitude_bits(top_v) : 0u;
@@ -349,9 +367,14 @@ __device__ __forceinline__ void adamw_bytes(const AdamwEntry& t, const AdamwStep
     for (int h = 0; h < 2; ++h) {
       uint32_t cm[4], cv[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        cm[k] = ckpt_code(m[4 * h + k], inv_m);
-        cv[k] = second_code(v[4 * h + k], inv_v);
+      for (int k = 0; k < 2; ++k) {
+        float a, b;
+        unpair(add2(product2(m[2 * h + k], pair_of(inv_m)), pair_of(12582912.f)), a, b);
+        cm[2 * k] = __float_as_uint(a);  // (ckpt_code)
+        cm[2 * k + 1] = __float_as_uint(b);
+        unpair(product2(v[2 * h + k], pair_of(inv_v)), a, b);
+        cv[2 * k] = second_code(a);
+        cv[2 * k + 1] = second_code(b);
       }
       wm[h] = __byte_perm(__byte_perm(cm[0], cm[1], 0x0040u), __byte_perm(cm[2], cm[3], 0x0040u), 0x5410u);
       wv[h] = __byte_perm(__byte_perm(cv[0], cv[1], 0x0040u), __byte_perm(cv[2], cv[3], 0x0040u), 0x5410u);
@@ -425,19 +448,29 @@ cudaError_t adamw_with(const AdamwEntry* t, int count, const AdamwStep& step, in
   auto steps_of = [](const AdamwEntry& x, int64_t values) { return static_cast<uint32_t>((x.n + values - 1) / values); };
   uint32_t chunks = 0;  // (384 tensors of 2^31 values are 2^29 of them)
   for (int i = 0; i < count; ++i) chunks += steps_of(t[i], kChunk);
-  // Eight chunks a step where that leaves every block a few steps: the search
-  // for the tensor and its addresses are paid for once (100 M values with
-  // 8-bit states, and read back: 467 us with one, 373 with four, 359 with eight;
-  // 33.6 M with FP32 states 144, 141, 143). More blocks than fit at once balance
-  // better than one wave of them (FP32 states: 160 us with 3 an SM, 143 with 16).
-  table.per = chunks >= static_cast<uint32_t>(num_sms) * 32u ? 8 : 1;
+  // A step of several chunks pays once for the search for the tensor and for
+  // its addresses, and 8-bit states load the next chunk while one is computed;
+  // too few steps leave blocks without one. 8-bit states, microseconds with 1, 2,
+  // 4 and 8: 2.6 M values 8.9, 7.9, 8.2, 10.3; 5.2 M 15.9, 13.0, 12.6, 14.0;
+  // 10.4 M 30, 23.2, 21.0, 21.8; 21 M 65, 50, 44, 42; 100 M 274, 213, 191, 182.
+  // FP32 states and master: 2.6 M 11.1, 12.8, 13.5, 15.6; 10.4 M 47.9, 46.3, 46.5,
+  // 52.4; 100 M 422, 413, 413, 419.
+  bool eight = false;
+  for (int i = 0; i < count; ++i) eight = eight || t[i].ms;
+  const uint32_t each = chunks / static_cast<uint32_t>(num_sms);
+  if (eight)
+    table.per = each >= 64 ? 8 : each >= 16 ? 4 : each >= 3 ? 2 : 1;
+  else
+    table.per = each >= 16 ? 2 : 1;
   table.chunks = 0;
   for (int i = 0; i < count; ++i) {
     table.t[i] = t[i];
     table.t[i].chunk0 = table.chunks;
     table.chunks += steps_of(t[i], static_cast<int64_t>(kChunk) * table.per);
   }
-  const uint32_t most = static_cast<uint32_t>(num_sms) * 16u;
+  // More blocks than fit at once balance better than few waves of them (100 M
+  // values with 8-bit states: 189 us with 16 an SM, 183 with 32 or 64).
+  const uint32_t most = static_cast<uint32_t>(num_sms) * 64u;
   PdlLaunch l(dim3(table.chunks < most ? table.chunks : most), dim3(kThreads), 0, stream);
   return cudaLaunchKernelEx(&l.cfg, adamw_kernel<MAX>, table);
 }
@@ -507,8 +540,10 @@ cudaError_t launch_adamw_load(const int8_t* m, const float* ms, const uint8_t* v
                               float* v_out, int64_t n, int num_sms, cudaStream_t stream) {
   auto aligned = [](const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; };
   const bool vec = n % 4 == 0 && aligned(m, 4) && aligned(v, 4) && aligned(m_out, 16) && aligned(v_out, 16);
-  const int64_t per = kThreads * (vec ? 4 : 1);
-  const int64_t want = (n + per - 1) / per, most = static_cast<int64_t>(num_sms) * 8;
+  const int64_t per = kThreads * (vec ? 16 : 1);
+  // (four pieces a thread, and blocks that balance: 100.8 M values 168 us with 8
+  // an SM, 155 with 32, 153 with 64; a block to every piece costs 6.2 M values 2.5 us)
+  const int64_t want = (n + per - 1) / per, most = static_cast<int64_t>(num_sms) * 64;
   PdlLaunch l(dim3(static_cast<unsigned>(want < most ? want : most)), dim3(kThreads), 0, stream);
   return cudaLaunchKernelEx(&l.cfg, vec ? adamw_load_kernel<true> : adamw_load_kernel<false>, m, ms, v, vs, m_out, v_out,
                             n);

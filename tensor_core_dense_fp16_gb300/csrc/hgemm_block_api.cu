@@ -417,6 +417,7 @@ int hgemm_adamw(const hgemm_adamw_tensor* tensors, int64_t count, double lr, dou
   s.a = static_cast<float>(lr / (1.0 - std::pow(beta1, t)));
   s.b = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(beta2, t)));
   s.ln1 = static_cast<float>(std::log(beta1)), s.ln2 = static_cast<float>(std::log(beta2));
+  s.minus_zero = -0.f;
   s.dynamic = dynamic;
   auto aligned = [](const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; };
   hg::AdamwEntry e[hg::kAdamwTensors];

@@ -404,6 +404,7 @@ struct AdamwStep {
   float beta1, rest1, beta2, rest2, eps;  // rest: 1 − β
   float gscale, lr, a, b;                 // a = lr/(1 − β1^step), b = 1/√(1 − β2^step)
   float ln1, ln2;                         // ln β, for a step number that the device holds
+  float minus_zero;                       // −0, which no compiler folds into what it is added to
   const hgemm_adamw_dynamic* dynamic;     // or null
 };
 cudaError_t launch_adamw(const AdamwEntry* t, int count, const AdamwStep& step, int num_sms, cudaStream_t stream);

@@ -274,6 +274,16 @@ def test_load(n, offset):
     same(a[5].get(), ref.kept_v(v, vs), "v")
 
 
+@pytest.mark.parametrize("bits,sizes", [(8, (1000003, 2048, 64 * 900 + 8, 5)), (8, (4000000, 1, 1200007, 5000, 65)),
+                                        (8, (20000001, 777, 100000)), (32, (5000009, 3, 300000, 2049))])
+def test_several_chunks_a_step(bits, sizes):
+    """Tables large enough for steps of two, four and eight chunks, whose
+    tensors end inside one."""
+    tensors = [make(n, bits, master=i % 2 == 0, grad="float32" if i % 3 == 2 else "float16")
+               for i, n in enumerate(sizes)]
+    run(tensors)
+
+
 def test_a_table_keeps_its_tensors():
     """The caller's dicts may be changed for the next table: a gradient that the
     first one points to stays alive with it."""
