@@ -166,6 +166,15 @@ def test_more_rows_than_a_pass_of_any_grid():
     run_backward(70000, 9, "layer", "rms")
 
 
+@pytest.mark.parametrize("m,d", [(3800, 1000), (1900, 1800), (1000, 4096), (1400, 2200), (520, 8192), (200, 16384)])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_several_waves_of_rows(m, d, kind):
+    """More rows than the GPU holds at once, in rows of every number of threads."""
+    run_forward(m, d, kind, kind, pad=8)
+    if d <= 8192:
+        run_backward(m, d, kind, kind, pad=8)
+
+
 def test_no_rows():
     torch = torch_cuda()
     h = torch.zeros(64, dtype=torch.float16, device="cuda")
