@@ -631,8 +631,29 @@ class AdamwTensors:
     """The table of tensors that hgemm_adamw steps: their addresses, and the
     tensors themselves so that they stay alive."""
 
-    def __init__(self, table, keep):
-        self.table, self.keep = table, keep
+    def __init__(self, table, keep, grads, device):
+        self.table, self.keep, self.grads, self.device = table, keep, grads, device
+
+    def set_gradients(self, grads) -> None:
+        """Other gradients (float16 or float32) in place of the table's, in its
+        order, checked as hgemm_adamw_tensors checks them: what a step without
+        kept gradients changes. A refused call changes nothing."""
+        import torch
+        f16, f32 = torch.float16, torch.float32
+        grads, table = list(grads), type(self.table).from_buffer_copy(self.table)
+        if len(grads) != len(table):
+            raise ValueError(f"{len(table)} gradients are needed, got {len(grads)}")
+        for i, (row, g) in enumerate(zip(table, grads)):
+            dtype = g.dtype
+            if dtype is not f16 and dtype is not f32:
+                raise TypeError(f"tensor {i}: grad must be float16 or float32, got {dtype}")
+            if g.get_device() != self.device:
+                raise ValueError(f"tensor {i}: grad must be on cuda:{self.device}, got {g.device}")
+            if g.numel() != row.n or not g.is_contiguous():
+                raise ValueError(f"tensor {i}: grad must be {row.n} values, contiguous, got {tuple(g.shape)}")
+            row.grad, row.grad_type = g.data_ptr(), HGEMM_TYPE_F16 if dtype is f16 else HGEMM_TYPE_F32
+        _raise_on((_lib or load()).hgemm_adamw_check(table, len(table)), "hgemm_adamw_check")
+        self.table, self.grads = table, grads
 
 
 _ADAMW_FIELDS = {"weight", "master", "grad", "m", "v", "m_scales", "v_scales", "weight_decay"}
@@ -643,7 +664,8 @@ def hgemm_adamw_tensors(tensors) -> AdamwTensors:
     or float32), ``weight`` (float16) and ``master`` (float32) or either, the
     states ``m`` and ``v`` (float32; or int8 and uint8 with ``m_scales`` and
     ``v_scales``, float32, one per 64 values), and ``weight_decay`` (0 where not
-    given). Made once for a program's tensors; all contiguous, of equal size, on
+    given). Made once for a program's tensors (set_gradients takes a later step's
+    gradients); all contiguous, of equal size, on
     one device, and none may share memory with another's outputs."""
     import torch
     f16, f32, i8, u8 = torch.float16, torch.float32, torch.int8, torch.uint8
@@ -682,9 +704,10 @@ def hgemm_adamw_tensors(tensors) -> AdamwTensors:
             if x.numel() != size or not x.is_contiguous():
                 raise ValueError(f"tensor {i}: {name} must be {size} values, contiguous, got {tuple(x.shape)}")
             row.append(x.data_ptr())
-            keep.append(x)
+            if name != "grad":
+                keep.append(x)
         rows.append((*row, n, get("weight_decay", 0.0), HGEMM_TYPE_F16 if half_grad else HGEMM_TYPE_F32))
-    plan = AdamwTensors((_AdamwTensor * len(rows))(*rows), keep)
+    plan = AdamwTensors((_AdamwTensor * len(rows))(*rows), keep, [t["grad"] for t in tensors], device)
     hgemm_adamw_check(plan)
     return plan
 

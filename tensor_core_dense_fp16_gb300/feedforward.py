@@ -397,7 +397,7 @@ class AdamW:
         if bits not in (8, 32):
             raise ValueError(f"bits must be 8 or 32, got {bits}")
         self.lr, self.beta1, self.beta2, self.eps, self.steps = lr, beta1, beta2, eps, 0
-        self.names, self.tensors = list(parameters), []
+        self.names, self.tensors, self.plan = list(parameters), [], None
         for name in self.names:
             p = parameters[name]
             n = p.numel()
@@ -405,7 +405,7 @@ class AdamW:
             def zeros(dtype, size=n, like=p):
                 return torch.zeros(size, dtype=dtype, device=like.device)
 
-            t = {"weight": p, "grad": p, "master": p.float() if master else None,
+            t = {"weight": p, "master": p.float() if master else None,
                  "weight_decay": weight_decay if (p.dim() > 1 if decay is None else name in decay) else 0.0}
             if bits == 8:
                 groups = -(-n // tc.HGEMM_CKPT8_GROUP)
@@ -418,10 +418,14 @@ class AdamW:
     def step(self, gradients, grad_scale: float = 1.0, dynamic=None, stream=None) -> None:
         """One step with the gradients of these names (float16 or float32).
         dynamic: see hgemm_adamw."""
-        for name, t in zip(self.names, self.tensors):
-            t["grad"] = gradients[name]
-        tc.hgemm_adamw(tc.hgemm_adamw_tensors(self.tensors), self.lr, self.beta1, self.beta2, self.eps, self.steps + 1,
-                       grad_scale, dynamic, stream)
+        grads = [gradients[name] for name in self.names]
+        # (a parameter may have been given other storage since)
+        if self.plan is None or any((row.weight or 0) != t["weight"].data_ptr()
+                                    for row, t in zip(self.plan.table, self.tensors)):
+            self.plan = tc.hgemm_adamw_tensors({**t, "grad": g} for t, g in zip(self.tensors, grads))
+        else:
+            self.plan.set_gradients(grads)
+        tc.hgemm_adamw(self.plan, self.lr, self.beta1, self.beta2, self.eps, self.steps + 1, grad_scale, dynamic, stream)
         self.steps += 1  # (a refused step is none)
 
 

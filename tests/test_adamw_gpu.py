@@ -302,6 +302,33 @@ def test_a_table_keeps_its_tensors():
     assert held() is None
 
 
+def test_other_gradients_in_a_table():
+    """set_gradients steps as a table of the new gradients does, of the other
+    type too; what it refuses leaves the table as it was."""
+    torch = torch_cuda()
+    tensors = [make(1000, 8), make(5000, 32, grad="float32"), make(77, 32, master=False)]
+    plan = table(tensors)
+    run_with = [Array((a["grad"].host * 0.5).astype("float32" if i == 0 else "float16"))
+                for i, (a, _) in enumerate(tensors)]
+    good = [a.tensor for a in run_with]
+    for bad, error in (([good[0], good[1]], ValueError), ([good[0], good[1], good[2][:70]], ValueError),
+                       ([good[0], good[1], good[2].double()], TypeError), ([good[0], good[1], good[2].cpu()], ValueError),
+                       ([good[0], good[1], tensors[2][0]["weight"].tensor], tc.HgemmError)):
+        before, grads = bytes(plan.table), plan.grads
+        with pytest.raises(error):
+            plan.set_gradients(bad)
+        assert bytes(plan.table) == before and plan.grads is grads
+    plan.set_gradients(good)
+    for (t, _), g in zip(tensors, run_with):
+        t["grad"] = g
+    tc.hgemm_adamw(plan, step=3, **HYPER)
+    done()
+    check_step(tensors, 3)
+    empty = tc.hgemm_adamw_tensors([])
+    empty.set_gradients([])
+    tc.hgemm_adamw(empty, 1e-3)
+
+
 def test_refusals():
     torch = torch_cuda()
     f, h = torch.zeros(128, device="cuda"), torch.zeros(128, dtype=torch.float16, device="cuda")

@@ -252,6 +252,29 @@ def test_a_refused_step_is_not_counted():
     assert torch.equal(one.tensors[0]["master"], other.tensors[0]["master"])
 
 
+def test_parameters_with_other_storage_and_gradients():
+    """A parameter whose storage is replaced between steps is stepped where it
+    is now; gradients may be of another type at every step."""
+    from tensor_core_dense_fp16_gb300.feedforward import AdamW
+    torch = torch_cuda()
+    g = torch.Generator(device="cuda").manual_seed(5)
+    start = torch.randn(40, 64, generator=g, device="cuda").half()
+    grads = [0.01 * torch.randn(40, 64, generator=g, device="cuda") for _ in range(3)]
+    grads[1] = grads[1].half()
+    p, q, none = start.clone(), start.clone(), torch.empty(0, dtype=torch.float16, device="cuda")
+    one = AdamW({"none": none, "p": p}, lr=0.1, bits=8, master=False)
+    other = AdamW({"none": none, "p": q}, lr=0.1, bits=8, master=False)
+    for grad in grads:
+        old = p.data
+        p.data = old.clone()
+        old.fill_(7)
+        one.step({"none": none.clone(), "p": grad})
+        other.step({"none": none.clone(), "p": grad.clone()})
+        done()
+        assert torch.equal(p, q) and (old == 7).all()
+    assert not torch.equal(p, start)
+
+
 def test_layers_are_checked():
     torch = torch_cuda()
     from tensor_core_dense_fp16_gb300.feedforward import AdamW, ExpertFeedForward, FeedForward, FeedForwardStack
