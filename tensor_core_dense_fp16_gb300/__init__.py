@@ -631,7 +631,7 @@ class AdamwTensors:
     """The table of tensors that hgemm_adamw steps: their addresses, and the
     tensors themselves so that they stay alive."""
 
-    def __init__(self, table, keep, grads, device):
+    def __init__(self, table, keep, grads=(), device=None):
         self.table, self.keep, self.grads, self.device = table, keep, grads, device
 
     def set_gradients(self, grads) -> None:
