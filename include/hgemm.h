@@ -663,7 +663,9 @@ HGEMM_API int hgemm_adamw_load(const int8_t *m, const float *m_scales, const uin
  *
  * W1 holds the experts one behind the other, E·F (or 2·E·F) rows of pitch
  * ldw1, W2 E·D rows of pitch ldw2; b1 E×F (2F), b2 E×D, without gaps, or NULL.
- * R is M×D or NULL; R = Y (same pitch) adds in place. h is rounded to FP16.
+ * R is M×D or NULL; R = Y (same pitch) adds in place. h is kept as two
+ * FP16 numbers, its rounding and what that leaves out: within 2^-23 of itself or
+ * 2^-25, whichever is more; from 65520 on it is infinite.
  * chosen (M×k, the experts from the largest logit down) and share (M×k, s)
  * receive the router's choice, or are NULL.
  * 1 ≤ k ≤ min(E, HGEMM_EXPERTS_MAX_CHOICES), E ≤ HGEMM_EXPERTS_MAX, D and F ≤

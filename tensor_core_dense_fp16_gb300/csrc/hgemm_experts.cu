@@ -251,7 +251,14 @@ __device__ __forceinline__ void put_unit(const ExpertsArgs& a, const Routing& r,
         if (bias) up += half_at(bias, rows + n);
         v *= up;
       }
-      if (HG_DBG_INDEX(n, a.F)) a.ws_h[slot * a.ldh + n] = __half_as_ushort(__float2half_rn(v));
+      // In two parts, v's FP16 value and that of what it leaves out: within 2^-23
+      // of v or 2^-25; from 65520 on infinite, with no rest.
+      const __half upper = __float2half_rn(v);
+      const float rest = __hisinf(upper) ? 0.f : v - __half2float(upper);
+      if (HG_DBG_INDEX(n, a.F)) {
+        a.ws_h[2 * slot * a.ldh + n] = __half_as_ushort(upper);
+        a.ws_h[(2 * slot + 1) * a.ldh + n] = __half_as_ushort(__float2half_rn(rest));
+      }
     } else {
       if (HG_DBG_INDEX(n, a.D)) a.ws_out[(static_cast<int64_t>(split) * a.M * a.k + slot) * a.ldo + n] = v;
     }
@@ -268,15 +275,15 @@ __device__ __forceinline__ void put_unit(const ExpertsArgs& a, const Routing& r,
 // queue of its own in shared memory, filled by asynchronous copies: registers
 // hold four pieces at most before a warp's scoreboards, six, make it wait for
 // the youngest load instead of the oldest (24 tokens, 8 of 64 experts: 176 us
-// that way, 136 with the queue; 347 with bulk copies of 1 KB, of which an SM
-// starts one in some 125 cycles). A step is two pieces, 64 values of K per warp
+// that way, 136 with the queue, both with h in 11 bits; 347 with bulk copies of
+// 1 KB, of which an SM starts one in some 125 cycles). A step is two pieces, 64 values of K per warp
 // and 128 bytes of a row. A warp's steps of all its units form one sequence, so
 // that the next unit's weights are on their way while one is added up. The
 // second product starts on its weights before the first has ended: who chose
 // what is known since the router, and only the tokens' values have to be waited
 // for. Tokens are copied through L1: every block wants the same few rows, and
 // the L2 lines of one token's row, asked for by all of them, held the first
-// product to 4.4 TB/s (6.9 through L1).
+// product to 4.4 TB/s (5.3 through L1: 134 MB in 25 us, launched by itself).
 //
 // ANY: rows that begin at any even address. The copies are of the aligned 16
 // bytes that a piece lies in, its row's last ones cut at the end (the rest is
@@ -284,13 +291,22 @@ __device__ __forceinline__ void put_unit(const ExpertsArgs& a, const Routing& r,
 // and its neighbour's by the row's distance from alignment. (The first copy of
 // a row may begin up to 14 bytes before it, within the 16 that hold its first
 // value and so within the same allocation.)
-template <int MT, bool ANY>
+//
+// The second product's tokens are pairs of rows, H's upper parts and what they
+// leave out, both multiplied by the weights that are there anyway and summed by
+// themselves. A tile of eight columns takes the pairs of up to four tokens, so
+// that an entry of so few needs no second one, and its sums are the same (24
+// tokens 2048 -> 1025, rows at any address: 203 us with two tiles, 197 with one;
+// aligned rows within 1%). With H in 11 bits one token through 2 of 8 experts
+// took 47.2 us in place of 48.7, 24 tokens through 8 of 64 139.6 of 142.8.
+template <int MT, bool FIRST, bool ANY>
 struct QueueCfg {
-  static constexpr int CTAS = MT == 4 ? 1 : 2;  // per SM
-  static constexpr int DEPTH = MT == 1 ? 2 : MT == 2 ? 2 : 3;
+  static constexpr int TILES = FIRST ? MT : 2 * MT;  // of eight rows, a step's tokens
+  static constexpr int CTAS = TILES < 4 ? 2 : 1;     // per SM
+  static constexpr int DEPTH = TILES < 4 ? 2 : FIRST || ANY ? 3 : 4;
   static constexpr int BUFFERS = MT == 1 ? 4 : 2;    // of partial sums
   static constexpr int ROWS = 1024 + (ANY ? 128 : 0);  // of a warp: a step of eight rows
-  static constexpr int SLOT = (2 + MT) * ROWS;         // 16 rows of weights, and the tokens
+  static constexpr int SLOT = (2 + TILES) * ROWS;      // 16 rows of weights, and the tokens
   static constexpr int PART = kWarps * 8 * MT * 17;  // floats of one buffer
   static constexpr int OFF_ROUTING = BUFFERS * PART * 4;
   static constexpr int OFF_BAR = (OFF_ROUTING + static_cast<int>(sizeof(Routing)) + 15) / 16 * 16;
@@ -313,8 +329,8 @@ __device__ __forceinline__ uint4 shifted(uint4 lo, uint4 hi, uint32_t s) {
 }
 
 template <int MT, bool FIRST, bool ANY>
-__global__ void __launch_bounds__(kThreads + 32, QueueCfg<MT, ANY>::CTAS) experts_queue_kernel(const ExpertsArgs a) {
-  using Cfg = QueueCfg<MT, ANY>;
+__global__ void __launch_bounds__(kThreads + 32, QueueCfg<MT, FIRST, ANY>::CTAS) experts_queue_kernel(const ExpertsArgs a) {
+  using Cfg = QueueCfg<MT, FIRST, ANY>;
   constexpr int DEPTH = Cfg::DEPTH, STEP = kWarps * 2 * kPiece;  // values of K per step
   extern __shared__ __align__(128) uint8_t experts_smem[];
   float* parts = reinterpret_cast<float*>(experts_smem);
@@ -406,10 +422,14 @@ __global__ void __launch_bounds__(kThreads + 32, QueueCfg<MT, ANY>::CTAS) expert
   // these rows.
   Unit fu = first;
   int fsteps = 0, fk = 0, fend = 0;
+  bool fpaired = false;
   const uint16_t *w0 = nullptr, *w1 = nullptr, *x[MT];
+  // Whether an entry's upper parts and rests share a tile, in columns 0-3 and 4-7.
+  auto paired = [](int count) { return !FIRST && MT == 1 && count <= 4; };
   auto begin_unit = [&]() {
     if (fu.entry >= entries) return;
     const auto& e = r.entry[fu.entry];
+    fpaired = paired(e.count);
     const int n0 = fu.block * per;
     fk = fu.split * run + warp * 2 * kPiece + 8 * t;
     fend = k_end(fu);
@@ -421,8 +441,9 @@ __global__ void __launch_bounds__(kThreads + 32, QueueCfg<MT, ANY>::CTAS) expert
     w1 = base + (gated ? row0 + static_cast<int64_t>(rows) : row1) * ldw;
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      const int row = e.first + 8 * i + g;
-      x[i] = 8 * i + g >= e.count ? nullptr : (FIRST ? a.X + r.token[row] * a.ldx : a.ws_h + r.list[row] * a.ldh) + fk;
+      const int token = fpaired ? g & 3 : 8 * i + g, row = e.first + token, rest = fpaired ? g >> 2 : 0;
+      x[i] = token >= e.count ? nullptr
+                              : (FIRST ? a.X + r.token[row] * a.ldx : a.ws_h + (2 * r.list[row] + rest) * a.ldh) + fk;
     }
   };
   // (past the end zeros; where there is no token nothing: a column of its own)
@@ -462,7 +483,10 @@ __global__ void __launch_bounds__(kThreads + 32, QueueCfg<MT, ANY>::CTAS) expert
     const uint32_t to = queue_addr + static_cast<uint32_t>(into * Cfg::SLOT + 2 * Cfg::ROWS);
 #pragma unroll
     for (int i = 0; i < MT; ++i)
-      if (x[i]) copy(to + static_cast<uint32_t>(Cfg::ROWS) * i, x[i], false);
+      if (x[i]) {
+        copy(to + static_cast<uint32_t>(Cfg::ROWS) * i, x[i], false);
+        if (!FIRST && !fpaired) copy(to + static_cast<uint32_t>(Cfg::ROWS) * (MT + i), x[i] + a.ldh, false);
+      }
   };
   // Piece i of the rows at `at`, their distance from alignment `off`.
   auto piece_of = [&](const uint8_t* at, int i, uint32_t off) {
@@ -524,7 +548,8 @@ __global__ void __launch_bounds__(kThreads + 32, QueueCfg<MT, ANY>::CTAS) expert
           if (8 * i + g < count) off[i] = distance(a.X + r.token[e.first + 8 * i + g] * a.ldx);
       }
     }
-    float acc[MT][4] = {};
+    const bool pair = paired(count);
+    float acc[Cfg::TILES][4] = {};
     for (int s = 0; s < steps; ++s) {
       cp_async_wait<DEPTH - 1>();
       if (ANY) __syncwarp();
@@ -536,11 +561,11 @@ __global__ void __launch_bounds__(kThreads + 32, QueueCfg<MT, ANY>::CTAS) expert
         p[i][1] = piece_of(at + Cfg::ROWS, i, off1);
       }
 #pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        if (8 * j >= count) break;
+      for (int j = 0; j < Cfg::TILES; ++j) {
+        if (8 * (j % MT) >= count || (j >= MT && pair)) continue;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint4 b = piece_of(at + (2 + j) * Cfg::ROWS, i, off[j]);
+          const uint4 b = piece_of(at + (2 + j) * Cfg::ROWS, i, off[j % MT]);
           mma_16816(acc[j], p[i][0].x, p[i][1].x, p[i][0].y, p[i][1].y, b.x, b.y);
           mma_16816(acc[j], p[i][0].z, p[i][1].z, p[i][0].w, p[i][1].w, b.z, b.w);
         }
@@ -553,6 +578,16 @@ __global__ void __launch_bounds__(kThreads + 32, QueueCfg<MT, ANY>::CTAS) expert
       }
       cp_async_commit();
       if (++slot == DEPTH) slot = 0;
+    }
+    if constexpr (!FIRST) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          // (columns 2t, 2t + 1 of a fragment's lane t; those four further are lane t + 2's)
+          const float rest = pair ? __shfl_down_sync(0xffffffffu, acc[i][k], 2) : acc[MT + i][k];
+          acc[i][k] += rest;
+        }
     }
     if (done++ >= Cfg::BUFFERS) (void)wait_phase(empty0 + 8u * buffer, phase ^ 1u, wd, kWdReduce);
     float* part = parts + buffer * Cfg::PART + warp * (8 * MT * 17);
@@ -620,7 +655,7 @@ cudaError_t allow_smem(Kernel kern, int bytes, std::atomic<bool> (&done)[64]) {
 
 template <int MT, bool FIRST, bool ANY>
 cudaError_t product_with(const ExpertsArgs& a, int num_sms, cudaStream_t stream) {
-  using Cfg = QueueCfg<MT, ANY>;
+  using Cfg = QueueCfg<MT, FIRST, ANY>;
   static std::atomic<bool> done[64];
   auto kern = experts_queue_kernel<MT, FIRST, ANY>;
   const cudaError_t e = allow_smem(kern, Cfg::SMEM_BYTES, done);
@@ -638,14 +673,17 @@ int token_tiles(const ExpertsArgs& a) {
 
 template <bool FIRST, bool ANY>
 cudaError_t product_tiles(const ExpertsArgs& a, int num_sms, cudaStream_t stream) {
-  switch (token_tiles(a)) {
-    case 1:
-      return product_with<1, FIRST, ANY>(a, num_sms, stream);
-    case 2:
-      return product_with<2, FIRST, ANY>(a, num_sms, stream);
-    default:
-      return product_with<4, FIRST, ANY>(a, num_sms, stream);
+  const int tiles = token_tiles(a);
+  if constexpr (FIRST) {
+    if (tiles == 4) return product_with<4, FIRST, ANY>(a, num_sms, stream);
+    if (tiles == 2) return product_with<2, FIRST, ANY>(a, num_sms, stream);
+  } else {
+    // Half as many: its tokens are pairs of rows, and tiles for all of them leave
+    // an SM one block (40 tokens, 5 of 16 experts, 2048 -> 2048: 134 us with as
+    // many as in the first product, 111 with half; 64 tokens, 4 of 8: 82 and 81).
+    if (tiles == 4) return product_with<2, FIRST, ANY>(a, num_sms, stream);
   }
+  return product_with<1, FIRST, ANY>(a, num_sms, stream);
 }
 
 template <bool FIRST>
@@ -674,11 +712,12 @@ int run_of(int64_t M, int64_t D, int64_t F, int64_t E, int64_t k, int* splits) {
 
 }  // namespace
 
-// The choice, its shares, H (rows of whole 16 bytes) and the slots' outputs.
+// The choice, its shares, H (two rows of whole 16 bytes a slot) and the slots'
+// outputs.
 size_t experts_workspace(int64_t M, int64_t D, int64_t F, int64_t E, int64_t k) {
   int splits;
   run_of(M, D, F, E, k, &splits);
-  return static_cast<size_t>(2 * align16(4 * M * k) + M * k * align16(2 * F) + splits * M * k * align16(4 * D));
+  return static_cast<size_t>(2 * align16(4 * M * k) + 2 * M * k * align16(2 * F) + splits * M * k * align16(4 * D));
 }
 
 cudaError_t launch_experts(ExpertsArgs a, void* workspace, int num_sms, cudaStream_t stream) {
@@ -688,7 +727,7 @@ cudaError_t launch_experts(ExpertsArgs a, void* workspace, int num_sms, cudaStre
   a.ws_share = reinterpret_cast<float*>(ws += align16(4 * slots));
   a.ws_h = reinterpret_cast<uint16_t*>(ws += align16(4 * slots));
   a.ldh = align16(2 * static_cast<int64_t>(a.F)) / 2;
-  a.ws_out = reinterpret_cast<float*>(ws += slots * a.ldh * 2);
+  a.ws_out = reinterpret_cast<float*>(ws += slots * a.ldh * 4);
   a.ldo = align16(4 * static_cast<int64_t>(a.D)) / 4;
   a.run = run_of(a.M, a.D, a.F, a.E, a.k, &a.splits);
   const bool vec_x = a.D % 8 == 0 && rows16(a.X, a.ldx);

@@ -434,7 +434,7 @@ struct ExpertsArgs {
   // the workspace's parts
   int* ws_chosen;
   float* ws_share;
-  uint16_t* ws_h;  // M·k rows
+  uint16_t* ws_h;  // M·k pairs of rows, upper parts and what they leave out
   int64_t ldh;
   float* ws_out;   // [splits][M·k] rows
   int64_t ldo;
