@@ -672,7 +672,8 @@ HGEMM_API int hgemm_adamw_load(const int8_t *m, const float *m_scales, const uin
  * HGEMM_EXPERTS_MAX_WIDTH.
  * F = 0: h is empty. workspace: caller-owned, 16-byte aligned, at least
  * hgemm_experts_workspace_size(M, D, F, E, k) bytes (0 for sizes that a call
- * refuses), not used by other work until the stream has passed this call. The
+ * refuses; enough for every call of fewer tokens too), not used by other work
+ * until the stream has passed this call. The
  * order of every sum is fixed. Same return values as hgemm_linear.
  */
 #define HGEMM_EXPERTS_MAX_TOKENS 64

@@ -471,7 +471,11 @@ bool experts_sizes_ok(int64_t M, int64_t D, int64_t F, int64_t E, int64_t k) {
 
 size_t hgemm_experts_workspace_size(int64_t M, int64_t D, int64_t F, int64_t E, int64_t k) {
   if (!experts_sizes_ok(M, D, F, E, k)) return 0;
-  return hg::experts_workspace(M, D, F, E, k);
+  // The most that any number of tokens up to M takes: fewer tokens may be cut
+  // into more runs of F.
+  size_t most = 0;
+  for (int64_t m = 0; m <= M; ++m) most = std::max(most, hg::experts_workspace(m, D, F, E, k));
+  return most;
 }
 
 int hgemm_experts(const hgemm_half_t* X, int64_t ldx, const hgemm_half_t* Wr, int64_t ldwr, const hgemm_half_t* W1,
