@@ -638,6 +638,26 @@ typedef struct {
 HGEMM_API int hgemm_adamw(const hgemm_adamw_tensor *tensors, int64_t count, double lr, double beta1, double beta2,
                 double eps, int64_t step, double grad_scale, const hgemm_adamw_dynamic *dynamic,
                 cudaStream_t stream);
+/*
+ * hgemm_adamw_rounded — hgemm_adamw with a choice of how 8-bit states are rounded:
+ *   HGEMM_ROUND_NEAREST  as above, which hgemm_adamw does. For a step or a few:
+ *        carried over many, a state that moves by less than half a code a step
+ *        is rounded back to the code it came from and stops following its
+ *        gradients (v at β2 = 0.999 moves by tenths of a percent a step, and
+ *        its codes are 6 to 12 percent apart).
+ *   HGEMM_ROUND_RANDOM   what training takes: up with the probability of what
+ *        lies above the lower of the two codes, so that a kept state's mean is
+ *        the formula's. A group's scale and largest value are kept as above.
+ *        The random number of a value is computed from its index in its tensor
+ *        and the step's number (dynamic's, where that is given): equal calls
+ *        give equal results, and alignment and order of the tensors do not
+ *        matter. FP32 states are as in hgemm_adamw.
+ */
+#define HGEMM_ROUND_NEAREST 0
+#define HGEMM_ROUND_RANDOM 1
+HGEMM_API int hgemm_adamw_rounded(const hgemm_adamw_tensor *tensors, int64_t count, double lr, double beta1,
+                        double beta2, double eps, int64_t step, double grad_scale, int rounding,
+                        const hgemm_adamw_dynamic *dynamic, cudaStream_t stream);
 /* hgemm_adamw_check — hgemm_adamw's argument checks, and that no tensor's
  * arrays overlap another's outputs (gradients may be shared). Host logic. */
 HGEMM_API int hgemm_adamw_check(const hgemm_adamw_tensor *tensors, int64_t count);

@@ -41,7 +41,7 @@ __all__ = [
     "hgemm_residual_norm_forward", "hgemm_residual_norm_backward", "hgemm_residual_norm_backward_workspace_size",
     "HGEMM_NORM_NONE", "HGEMM_NORM_LAYER", "HGEMM_NORM_RMS",
     "hgemm_adamw", "hgemm_adamw_check", "hgemm_adamw_tensors", "hgemm_adamw_dynamic", "hgemm_adamw_load", "AdamwTensors", "HGEMM_TYPE_F16",
-    "HGEMM_TYPE_F32", "hgemm_experts", "hgemm_experts_workspace_size", "HGEMM_EXPERTS_MAX_TOKENS",
+    "HGEMM_TYPE_F32", "HGEMM_ROUND_NEAREST", "HGEMM_ROUND_RANDOM", "hgemm_experts", "hgemm_experts_workspace_size", "HGEMM_EXPERTS_MAX_TOKENS",
     "HGEMM_EXPERTS_MAX_CHOICES", "HGEMM_EXPERTS_MAX", "HGEMM_EXPERTS_MAX_WIDTH",
 ]
 
@@ -80,6 +80,9 @@ HGEMM_NORM_RMS = 2
 
 HGEMM_TYPE_F16 = 0
 HGEMM_TYPE_F32 = 1
+
+HGEMM_ROUND_NEAREST = 0
+HGEMM_ROUND_RANDOM = 1
 
 HGEMM_EXPERTS_MAX_TOKENS = 64
 HGEMM_EXPERTS_MAX_CHOICES = 16
@@ -202,12 +205,13 @@ def load():
     lib.hgemm_residual_norm_backward.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, f32, vp, i32, vp, vp, i32, vp, vp,
                                                  vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, size, i64, i64, vp]
     lib.hgemm_adamw.argtypes = [vp, i64, f64, f64, f64, f64, i64, f64, vp, vp]
+    lib.hgemm_adamw_rounded.argtypes = [vp, i64, f64, f64, f64, f64, i64, f64, i32, vp, vp]
     lib.hgemm_adamw_check.argtypes = [vp, i64]
     lib.hgemm_adamw_load.argtypes = [vp, vp, vp, vp, vp, vp, i64, vp]
     lib.hgemm_experts.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, i64, vp, i32, i32, i64, i32, vp, i64, vp, i64, vp,
                                   vp, vp, size, i64, i64, i64, i64, vp]
-    for name in ("hgemm_residual_norm_forward", "hgemm_residual_norm_backward", "hgemm_adamw", "hgemm_adamw_check",
-                 "hgemm_adamw_load", "hgemm_experts"):
+    for name in ("hgemm_residual_norm_forward", "hgemm_residual_norm_backward", "hgemm_adamw", "hgemm_adamw_rounded",
+                 "hgemm_adamw_check", "hgemm_adamw_load", "hgemm_experts"):
         getattr(lib, name).restype = i32
     lib.hgemm_residual_norm_backward_workspace_size.argtypes = [i64, i64]
     lib.hgemm_residual_norm_backward_workspace_size.restype = size
@@ -727,17 +731,21 @@ def hgemm_adamw_dynamic(lr: float, grad_scale: float, step: int, skip: bool = Fa
 
 
 def hgemm_adamw(tensors: AdamwTensors, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
-                step: int = 1, grad_scale: float = 1.0, dynamic=None, stream=None) -> None:
+                step: int = 1, grad_scale: float = 1.0, dynamic=None, stream=None,
+                rounding: int = HGEMM_ROUND_NEAREST) -> None:
     """One AdamW step over the tensors of hgemm_adamw_tensors (see hgemm.h).
     dynamic: 16 device bytes (hgemm_adamw_dynamic's) that are read when the step
-    runs, or None."""
+    runs, or None. rounding: of 8-bit states, HGEMM_ROUND_RANDOM where they are
+    carried over many steps (to the nearest code they stop following their
+    gradients)."""
     if dynamic is not None and type(dynamic) is not int:
         if not getattr(dynamic, "is_cuda", False):
             raise ValueError("dynamic must be a CUDA tensor")
         if dynamic.numel() * dynamic.element_size() < 16 or not dynamic.is_contiguous():
             raise ValueError("dynamic must have 16 bytes, contiguous")
-    _raise_on((_lib or load()).hgemm_adamw(tensors.table, len(tensors.table), lr, beta1, beta2, eps, step, grad_scale,
-                                           _ptr(dynamic), _stream(stream)), "hgemm_adamw")
+    _raise_on((_lib or load()).hgemm_adamw_rounded(tensors.table, len(tensors.table), lr, beta1, beta2, eps, step,
+                                                   grad_scale, rounding, _ptr(dynamic), _stream(stream)),
+              "hgemm_adamw")
 
 
 def hgemm_adamw_load(m, m_scales, v, v_scales, m_out, v_out, n: int, stream=None) -> None:

@@ -4,7 +4,7 @@
 // FP16 gradient and weight 28 bytes per value, with 8-bit states and no master
 // 10.25. Measured: 33.6 M values with FP32 states and master 139 us (6.8 TB/s, a
 // copy's rate); 100.8 M with 8-bit states 183 us (5.6 TB/s, issue slots 71%),
-// read back 153 us (6.7 TB/s).
+// rounded at random 192, read back 153 us (6.7 TB/s).
 #include <cuda_fp16.h>
 
 #include "debug.cuh"
@@ -56,13 +56,19 @@ __device__ __forceinline__ void second_scale(uint32_t top_bits, float& scale, fl
 
 // The upper 12 bits of an FP32 number r in (0, 1] (8 of exponent, 3 of fraction
 // and the leading 0) rounded at the 20th, counted from 1's; at least 1 where r
-// is not 0. (r = v·(1/top) is at most 1 + 2^-23, whose code is 255.) The caller
-// takes 0 in place of all codes of a group whose inv is 0.
-__device__ __forceinline__ uint32_t second_code(float v_over_top) {
+// is not 0. `add` goes to the 20 bits that are cut off: half of them rounds to
+// nearest, a random number below 2^20 up with the probability of the rest (r is
+// linear in its bits between two codes). r = v·(1/top) is at most 1 + 2^-23,
+// whose code is 255. The caller takes 0 in place of all codes of a group whose
+// inv is 0.
+template <bool RANDOM>
+__device__ __forceinline__ uint32_t second_code(float v_over_top, uint32_t add) {
   const uint32_t r = __float_as_uint(v_over_top);
-  const int c = static_cast<int>(r + ((255u << 20) + 0x80000u - kOneBits)) >> 20;
+  int c = static_cast<int>(r + add + ((255u << 20) - kOneBits)) >> 20;
+  if (RANDOM) c = min(c, 255);
   return static_cast<uint32_t>(max(c, static_cast<int>(min(r, 1u))));
 }
+constexpr uint32_t kHalfCode = 0x80000u;
 
 // What a code stands for, in units of the group's largest.
 __device__ __forceinline__ float second_unit(uint32_t code) {
@@ -71,11 +77,46 @@ __device__ __forceinline__ float second_unit(uint32_t code) {
 
 __device__ __forceinline__ float second_value(uint32_t code, float scale) { return __fmul_rn(second_unit(code), scale); }
 
+// ----------------------------------------------------------- random rounding
+
+// 32 bits from 32, a bijection: shifts and products with odd numbers (the first
+// bits of √2's and √3's fractions), after which a bit that changes changes each
+// other with probability 0.497 to 0.503.
+__device__ __forceinline__ uint32_t mixed(uint32_t x) {
+  x = (x ^ (x >> 16)) * 0x6A09E667u;
+  x = (x ^ (x >> 15)) * 0xBB67AE85u;
+  return x ^ (x >> 16);
+}
+
+// The random bits of value i of a tensor in the step whose number gave `key`:
+// one mixed number for eight values, times a power of an odd number (the golden
+// section's bits) each. The upper 20 round v, the lower 12 m: over steps and
+// over values both are even, and neighbours' are independent of one another
+// within 1%.
+constexpr uint32_t kGolden = 0x9E3779B1u;
+__device__ __forceinline__ uint32_t eight_bits(uint32_t key, int64_t i) {
+  return mixed(static_cast<uint32_t>(i >> 3) + key);
+}
+
+// A number in (1, 2) from the lower 12 bits, in the middle of its 4096th part.
+__device__ __forceinline__ float one_and(uint32_t bits) {
+  return __uint_as_float(0x3F800400u | ((bits & 0xFFFu) << 11));
+}
+
+// floor(m·inv + u) as the low byte, from 1 + u: adding 1.5·2^23 − 1 and rounding
+// down leaves the whole number in the low bits. |m·inv| is at most 127 + 2^-15
+// and u lies 2^-13 from 0 and 1, so that no code passes 127.
+constexpr float kFloorMagic = 12582911.f;
+__device__ __forceinline__ uint32_t random_code(float m, float inv, float one_and_u) {
+  return __float_as_uint(__fadd_rd(__fmaf_rn(m, inv, one_and_u), kFloorMagic));
+}
+
 // ------------------------------------------------------------------ the step
 
 struct Scalars {
   float gscale, a, b, lr;
   bool dynamic;
+  uint32_t key;  // of random rounding
 };
 
 // One value: the states (each product and sum rounded, so that the kept codes
@@ -190,7 +231,7 @@ __device__ __forceinline__ uint32_t group_top(const float (&f)[8], int i) {
 }
 
 // Eight values of a tensor. All lanes of a warp come here together.
-template <bool VEC>
+template <bool VEC, bool RANDOM>
 __device__ __forceinline__ void adamw_eight(const AdamwEntry& t, const AdamwStep& s, const Scalars& c, float keep,
                                             int64_t first) {
   const int64_t n = t.n;
@@ -228,6 +269,9 @@ __device__ __forceinline__ void adamw_eight(const AdamwEntry& t, const AdamwStep
   if (eight) {
     __syncwarp();  // the group's scales have been read
     uint32_t qm[8], qv[8];
+    uint32_t power = 1u;  // (a thread's values have the same place in their eights)
+    if (RANDOM)
+      for (int i = static_cast<int>(first & 7); i > 0; --i) power *= kGolden;
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
       float scale_m, inv_m, scale_v, inv_v;
@@ -235,8 +279,9 @@ __device__ __forceinline__ void adamw_eight(const AdamwEntry& t, const AdamwStep
       second_scale(group_top<VEC>(v, i), scale_v, inv_v);
 #pragma unroll
       for (int j = i; j < (VEC ? 8 : i + 2); ++j) {
-        qm[j] = inv_m == 0.f ? 0u : ckpt_code(m[j], inv_m);
-        qv[j] = inv_v == 0.f ? 0u : second_code(__fmul_rn(v[j], inv_v));
+        const uint32_t bits = RANDOM ? eight_bits(c.key, value_at<VEC>(first, j)) * power : 0u;
+        qm[j] = inv_m == 0.f ? 0u : RANDOM ? random_code(m[j], inv_m, one_and(bits)) : ckpt_code(m[j], inv_m);
+        qv[j] = inv_v == 0.f ? 0u : second_code<RANDOM>(__fmul_rn(v[j], inv_v), RANDOM ? bits >> 12 : kHalfCode);
       }
       const int lane = threadIdx.x & 31;
       const int64_t at = VEC ? first : first - lane + 32 * i;  // a value of the group
@@ -284,7 +329,7 @@ __device__ __forceinline__ void unpack_wide(const uint4 (&w)[WIDE ? 2 : 1], f32x
   }
 }
 
-template <bool G32, bool MASTER>
+template <bool RANDOM, bool G32, bool MASTER>
 __device__ __forceinline__ void adamw_bytes(const AdamwEntry& t, const AdamwStep& s, const Scalars& c, float keep,
                                             int64_t first, int count) {
   const int64_t n = t.n;  // a multiple of 8, or past all these chunks
@@ -363,18 +408,26 @@ __device__ __forceinline__ void adamw_bytes(const AdamwEntry& t, const AdamwStep
     const bool keep_m = bits_m < 0x7F800000u && top_m >= 7.888609e-31f;
     const bool keep_v = bits_v < 0x7F800000u && top_v >= 7.888609e-31f;
     uint32_t wm[2], wv[2];
+    uint32_t bits = RANDOM ? eight_bits(c.key, first) : 0u;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t cm[4], cv[4];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         float a, b;
-        unpair(add2(product2(m[2 * h + k], pair_of(inv_m)), pair_of(12582912.f)), a, b);
-        cm[2 * k] = __float_as_uint(a);  // (ckpt_code)
+        const uint32_t other = bits * kGolden;
+        if constexpr (RANDOM)  // (random_code)
+          unpair(add2_down(fma2(m[2 * h + k], pair_of(inv_m), pair_of(one_and(bits), one_and(other))),
+                           pair_of(kFloorMagic)),
+                 a, b);
+        else  // (ckpt_code)
+          unpair(add2(product2(m[2 * h + k], pair_of(inv_m)), pair_of(12582912.f)), a, b);
+        cm[2 * k] = __float_as_uint(a);
         cm[2 * k + 1] = __float_as_uint(b);
         unpair(product2(v[2 * h + k], pair_of(inv_v)), a, b);
-        cv[2 * k] = second_code(a);
-        cv[2 * k + 1] = second_code(b);
+        cv[2 * k] = second_code<RANDOM>(a, RANDOM ? bits >> 12 : kHalfCode);
+        cv[2 * k + 1] = second_code<RANDOM>(b, RANDOM ? other >> 12 : kHalfCode);
+        bits = other * kGolden;
       }
       wm[h] = __byte_perm(__byte_perm(cm[0], cm[1], 0x0040u), __byte_perm(cm[2], cm[3], 0x0040u), 0x5410u);
       wv[h] = __byte_perm(__byte_perm(cv[0], cv[1], 0x0040u), __byte_perm(cv[2], cv[3], 0x0040u), 0x5410u);
@@ -391,12 +444,12 @@ __device__ __forceinline__ void adamw_bytes(const AdamwEntry& t, const AdamwStep
   }
 }
 
-template <int MAX>
+template <int MAX, bool RANDOM>
 __global__ void __launch_bounds__(kThreads, 3) adamw_kernel(const __grid_constant__ AdamwTable<MAX> table) {
   grid_dependency_wait();
   grid_launch_dependents();
   const AdamwStep& s = table.step;
-  Scalars c{s.gscale, s.a, s.b, s.lr, s.dynamic != nullptr};
+  Scalars c{s.gscale, s.a, s.b, s.lr, s.dynamic != nullptr, s.number};
   if (c.dynamic) {
     const hgemm_adamw_dynamic d = *s.dynamic;
     if (d.skip) return;
@@ -405,7 +458,9 @@ __global__ void __launch_bounds__(kThreads, 3) adamw_kernel(const __grid_constan
     c.lr = d.lr;
     c.a = d.lr / -expm1f(step * s.ln1);
     c.b = rsqrtf(-expm1f(step * s.ln2));
+    c.key = static_cast<uint32_t>(max(d.step, 1));
   }
+  if (RANDOM) c.key = mixed(c.key);
   for (uint32_t chunk = blockIdx.x; chunk < table.chunks; chunk += gridDim.x) {
     int lo = 0, hi = table.count - 1;  // the last tensor that begins at or before the chunk
     while (lo < hi) {
@@ -427,21 +482,24 @@ __global__ void __launch_bounds__(kThreads, 3) adamw_kernel(const __grid_constan
       done = left < table.per ? static_cast<int>(left) : table.per;
       const int64_t at = first + 8 * static_cast<int>(threadIdx.x);
       if (!t.ms) {
-        for (int i = 0; i < done; ++i) adamw_eight<true>(t, s, c, keep, at + i * kChunk);
+        for (int i = 0; i < done; ++i) adamw_eight<true, RANDOM>(t, s, c, keep, at + i * kChunk);
       } else if (t.grad_type == 0) {
-        t.master ? adamw_bytes<false, true>(t, s, c, keep, at, done) : adamw_bytes<false, false>(t, s, c, keep, at, done);
+        t.master ? adamw_bytes<RANDOM, false, true>(t, s, c, keep, at, done)
+                 : adamw_bytes<RANDOM, false, false>(t, s, c, keep, at, done);
       } else {
-        t.master ? adamw_bytes<true, true>(t, s, c, keep, at, done) : adamw_bytes<true, false>(t, s, c, keep, at, done);
+        t.master ? adamw_bytes<RANDOM, true, true>(t, s, c, keep, at, done)
+                 : adamw_bytes<RANDOM, true, false>(t, s, c, keep, at, done);
       }
     }
     first += static_cast<int64_t>(done) * kChunk;
     for (int i = done; i < table.per && first < t.n; ++i, first += kChunk)
-      adamw_eight<false>(t, s, c, keep, first + (threadIdx.x >> 5) * 256 + (threadIdx.x & 31));
+      adamw_eight<false, RANDOM>(t, s, c, keep, first + (threadIdx.x >> 5) * 256 + (threadIdx.x & 31));
   }
 }
 
 template <int MAX>
-cudaError_t adamw_with(const AdamwEntry* t, int count, const AdamwStep& step, int num_sms, cudaStream_t stream) {
+cudaError_t adamw_with(const AdamwEntry* t, int count, const AdamwStep& step, bool random, int num_sms,
+                       cudaStream_t stream) {
   AdamwTable<MAX> table;
   table.step = step;
   table.count = count;
@@ -472,7 +530,7 @@ cudaError_t adamw_with(const AdamwEntry* t, int count, const AdamwStep& step, in
   // values with 8-bit states: 189 us with 16 an SM, 183 with 32 or 64).
   const uint32_t most = static_cast<uint32_t>(num_sms) * 64u;
   PdlLaunch l(dim3(table.chunks < most ? table.chunks : most), dim3(kThreads), 0, stream);
-  return cudaLaunchKernelEx(&l.cfg, adamw_kernel<MAX>, table);
+  return cudaLaunchKernelEx(&l.cfg, random && eight ? adamw_kernel<MAX, true> : adamw_kernel<MAX, false>, table);
 }
 
 // Four neighbouring values per thread and step where VEC, else one.
@@ -528,12 +586,13 @@ __global__ void __launch_bounds__(kThreads)
 
 }  // namespace
 
-cudaError_t launch_adamw(const AdamwEntry* t, int count, const AdamwStep& step, int num_sms, cudaStream_t stream) {
+cudaError_t launch_adamw(const AdamwEntry* t, int count, const AdamwStep& step, bool random, int num_sms,
+                         cudaStream_t stream) {
   // (the parameters' bytes cost a launch time: 72 tensors of 4096, 6.8 us in the
   // largest table, 6.1 in the middle one)
-  if (count <= 16) return adamw_with<16>(t, count, step, num_sms, stream);
-  if (count <= 96) return adamw_with<96>(t, count, step, num_sms, stream);
-  return adamw_with<kAdamwTensors>(t, count, step, num_sms, stream);
+  if (count <= 16) return adamw_with<16>(t, count, step, random, num_sms, stream);
+  if (count <= 96) return adamw_with<96>(t, count, step, random, num_sms, stream);
+  return adamw_with<kAdamwTensors>(t, count, step, random, num_sms, stream);
 }
 
 cudaError_t launch_adamw_load(const int8_t* m, const float* ms, const uint8_t* v, const float* vs, float* m_out,

@@ -391,6 +391,14 @@ int hgemm_adamw_check(const hgemm_adamw_tensor* tensors, int64_t count) {
 
 int hgemm_adamw(const hgemm_adamw_tensor* tensors, int64_t count, double lr, double beta1, double beta2, double eps,
                 int64_t step, double grad_scale, const hgemm_adamw_dynamic* dynamic, cudaStream_t stream) {
+  return hgemm_adamw_rounded(tensors, count, lr, beta1, beta2, eps, step, grad_scale, HGEMM_ROUND_NEAREST, dynamic,
+                             stream);
+}
+
+int hgemm_adamw_rounded(const hgemm_adamw_tensor* tensors, int64_t count, double lr, double beta1, double beta2,
+                        double eps, int64_t step, double grad_scale, int rounding, const hgemm_adamw_dynamic* dynamic,
+                        cudaStream_t stream) {
+  if (rounding != HGEMM_ROUND_NEAREST && rounding != HGEMM_ROUND_RANDOM) return HGEMM_ERR_INVALID_ARG;
   if (count < 0 || count > HGEMM_MAX_DIM || (count > 0 && !tensors)) return HGEMM_ERR_INVALID_ARG;
   if (!std::isfinite(lr) || !(beta1 >= 0 && beta1 < 1) || !(beta2 >= 0 && beta2 < 1) || !(eps >= 0) ||
       std::isinf(eps) || step < 1 || !std::isfinite(grad_scale) || (reinterpret_cast<uintptr_t>(dynamic) & 3u))
@@ -419,12 +427,13 @@ int hgemm_adamw(const hgemm_adamw_tensor* tensors, int64_t count, double lr, dou
   s.ln1 = static_cast<float>(std::log(beta1)), s.ln2 = static_cast<float>(std::log(beta2));
   s.minus_zero = -0.f;
   s.dynamic = dynamic;
+  s.number = static_cast<uint32_t>(step);
   auto aligned = [](const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; };
   hg::AdamwEntry e[hg::kAdamwTensors];
   int n = 0;
   for (int64_t i = 0; i <= count; ++i) {
     if (n == hg::kAdamwTensors || (i == count && n > 0)) {
-      if ((rc = hg::cuda_status(hg::launch_adamw(e, n, s, dev.num_sms, stream))) != HGEMM_OK) return rc;
+      if ((rc = hg::cuda_status(hg::launch_adamw(e, n, s, rounding == HGEMM_ROUND_RANDOM, dev.num_sms, stream))) != HGEMM_OK) return rc;
       n = 0;
     }
     if (i == count || tensors[i].n == 0) continue;

@@ -406,8 +406,11 @@ struct AdamwStep {
   float ln1, ln2;                         // ln β, for a step number that the device holds
   float minus_zero;                       // −0, which no compiler folds into what it is added to
   const hgemm_adamw_dynamic* dynamic;     // or null
+  uint32_t number;                        // the step's, for random rounding
 };
-cudaError_t launch_adamw(const AdamwEntry* t, int count, const AdamwStep& step, int num_sms, cudaStream_t stream);
+// random: 8-bit states are rounded at random (HGEMM_ROUND_RANDOM).
+cudaError_t launch_adamw(const AdamwEntry* t, int count, const AdamwStep& step, bool random, int num_sms,
+                         cudaStream_t stream);
 cudaError_t launch_adamw_load(const int8_t* m, const float* ms, const uint8_t* v, const float* vs, float* m_out,
                               float* v_out, int64_t n, int num_sms, cudaStream_t stream);
 

@@ -389,7 +389,9 @@ class AdamW:
         optimizer.step(block.backward(dy, saved).named())
 
     weight_decay goes to parameters of two dimensions alone, unless `decay`
-    names which."""
+    names which. 8-bit states are rounded at random, by the values' indexes and
+    the step's number, so that they follow their gradients over many steps and
+    equal runs are equal."""
 
     def __init__(self, parameters, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
                  weight_decay: float = 0.01, bits: int = 32, master: bool = True, decay=None):
@@ -425,7 +427,8 @@ class AdamW:
             self.plan = tc.hgemm_adamw_tensors({**t, "grad": g} for t, g in zip(self.tensors, grads))
         else:
             self.plan.set_gradients(grads)
-        tc.hgemm_adamw(self.plan, self.lr, self.beta1, self.beta2, self.eps, self.steps + 1, grad_scale, dynamic, stream)
+        tc.hgemm_adamw(self.plan, self.lr, self.beta1, self.beta2, self.eps, self.steps + 1, grad_scale, dynamic, stream,
+                       tc.HGEMM_ROUND_RANDOM)
         self.steps += 1  # (a refused step is none)
 
 
