@@ -26,6 +26,7 @@ its optimizer's, and a token through the block and through experts.
 
 from __future__ import annotations
 
+import operator
 from dataclasses import dataclass
 from typing import Any
 
@@ -391,7 +392,14 @@ class AdamW:
     weight_decay goes to parameters of two dimensions alone, unless `decay`
     names which. 8-bit states are rounded at random, by the values' indexes and
     the step's number, so that they follow their gradients over many steps and
-    equal runs are equal."""
+    equal runs are equal.
+
+    `tensors` holds a dict of what hgemm_adamw_tensors takes for each of `names`,
+    without the gradient. Its states, master copies and weight_decay may be
+    replaced or given other values between steps (a checkpoint, a schedule), and
+    `steps` counts the steps so far. With master copies a step reads those and
+    overwrites the weights: who sets weights sets them too. Under a captured
+    graph a step's learning rate, number and scale come from `dynamic`."""
 
     def __init__(self, parameters, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
                  weight_decay: float = 0.01, bits: int = 32, master: bool = True, decay=None):
@@ -399,7 +407,7 @@ class AdamW:
         if bits not in (8, 32):
             raise ValueError(f"bits must be 8 or 32, got {bits}")
         self.lr, self.beta1, self.beta2, self.eps, self.steps = lr, beta1, beta2, eps, 0
-        self.names, self.tensors, self.plan = list(parameters), [], None
+        self.names, self.tensors, self.plan, self._held = list(parameters), [], None, None
         for name in self.names:
             p = parameters[name]
             n = p.numel()
@@ -421,15 +429,32 @@ class AdamW:
         """One step with the gradients of these names (float16 or float32).
         dynamic: see hgemm_adamw."""
         grads = [gradients[name] for name in self.names]
-        # (a parameter may have been given other storage since)
-        if self.plan is None or any((row.weight or 0) != t["weight"].data_ptr()
-                                    for row, t in zip(self.plan.table, self.tensors)):
-            self.plan = tc.hgemm_adamw_tensors({**t, "grad": g} for t, g in zip(self.tensors, grads))
-        else:
+        if self.plan is not None and self._unchanged():
             self.plan.set_gradients(grads)
+        else:
+            self.plan = tc.hgemm_adamw_tensors({**t, "grad": g} for t, g in zip(self.tensors, grads))
+            held, decays = self._entries()
+            self._held = held, self._addresses(held), decays
         tc.hgemm_adamw(self.plan, self.lr, self.beta1, self.beta2, self.eps, self.steps + 1, grad_scale, dynamic, stream,
                        tc.HGEMM_ROUND_RANDOM)
         self.steps += 1  # (a refused step is none)
+
+    def _entries(self):
+        """What a table holds of `tensors`: the tensors, in order, and the decays."""
+        return ([t.get(n) for t in self.tensors for n in ("weight", "master", "m", "v", "m_scales", "v_scales")],
+                [t.get("weight_decay", 0.0) for t in self.tensors])
+
+    @staticmethod
+    def _addresses(held):
+        return [None if x is None else x.data_ptr() for x in held]
+
+    def _unchanged(self) -> bool:
+        """Whether the table says what `tensors` does: the same tensors, where
+        they were, and the same decays."""
+        held, at, decays = self._held
+        now, now_decays = self._entries()
+        return (now_decays == decays and len(now) == len(held) and all(map(operator.is_, now, held))
+                and self._addresses(held) == at)
 
 
 def main() -> None:
