@@ -633,7 +633,8 @@ class _AdamwTensor(ctypes.Structure):
 
 class AdamwTensors:
     """The table of tensors that hgemm_adamw steps: their addresses, and the
-    tensors themselves so that they stay alive."""
+    tensors themselves so that they stay alive. device: the CUDA device's number
+    that gradients must be on; None: the first gradient's."""
 
     def __init__(self, table, keep, grads=(), device=None):
         self.table, self.keep, self.grads, self.device = table, keep, grads, device
@@ -647,12 +648,16 @@ class AdamwTensors:
         grads, table = list(grads), type(self.table).from_buffer_copy(self.table)
         if len(grads) != len(table):
             raise ValueError(f"{len(table)} gradients are needed, got {len(grads)}")
+        device = self.device
         for i, (row, g) in enumerate(zip(table, grads)):
             dtype = g.dtype
             if dtype is not f16 and dtype is not f32:
                 raise TypeError(f"tensor {i}: grad must be float16 or float32, got {dtype}")
-            if g.get_device() != self.device:
-                raise ValueError(f"tensor {i}: grad must be on cuda:{self.device}, got {g.device}")
+            at = g.get_device()  # (−1 of a tensor on the host)
+            if device is None:
+                device = at
+            if at != device or at < 0:
+                raise ValueError(f"tensor {i}: grad must be on {'cuda' if device < 0 else f'cuda:{device}'}, got {g.device}")
             if g.numel() != row.n or not g.is_contiguous():
                 raise ValueError(f"tensor {i}: grad must be {row.n} values, contiguous, got {tuple(g.shape)}")
             row.grad, row.grad_type = g.data_ptr(), HGEMM_TYPE_F16 if dtype is f16 else HGEMM_TYPE_F32
