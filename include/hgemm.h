@@ -601,8 +601,8 @@ HGEMM_API int hgemm_residual_norm_backward(const hgemm_half_t *dZ, int64_t lddz,
  *     v: s = max v, and r = v·(1/s) is kept in a float of 5 exponent and 3
  *        fraction bits: code c > 0 stands for 2^e·(1 + f/8)·s with 8·e + f =
  *        c − 255, rounded to nearest (halves up), so that 255 is s itself; r
- *        below the least, 1.25·2^-32, is kept as that (c = 1), 0 as 0. A
- *        value's error is at most r/16.
+ *        below the least, 1.25·2^-32, is kept as that (c = 1), 0 as 0. An
+ *        error is at most r/16, of an r below the least code at most that code.
  *     A group whose largest magnitude is below 2^-100 has s = 0 and codes 0,
  *     one that holds an infinity or a NaN s = NaN and codes 0. The step itself
  *     uses m and v before they are kept.
