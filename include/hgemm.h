@@ -612,7 +612,8 @@ HGEMM_API int hgemm_residual_norm_backward(const hgemm_half_t *dZ, int64_t lddz,
  * tensor's arrays must not overlap one another (HGEMM_ERR_ALIAS); those of
  * different tensors must not either, which hgemm_adamw_check looks for and a
  * step does not. A v below 2^-126 counts as 0 under the root, which only eps = 0
- * shows. lr, eps and grad_scale are finite, 0 ≤ β < 1, step ≥ 1, eps ≥ 0.
+ * shows; an eps above 0 and below 2^-126 counts as that. lr, eps and grad_scale
+ * are finite, 0 ≤ β < 1, step ≥ 1, eps ≥ 0.
  * dynamic, in device memory, or NULL: its lr, grad_scale and step are taken in
  * place of the arguments' when the work runs (a step ≤ 0 counts as 1), and with
  * skip ≠ 0 nothing is written: what changes from step to step under one
