@@ -462,7 +462,11 @@ __global__ void __launch_bounds__(kThreads + 32, QueueCfg<MT, FIRST, ANY>::CTAS)
       for (int i = 0; i < 3; ++i) {
         if (i == 2 && t != 3) continue;  // the ninth
         const int from = i == 2 ? 80 : 64 * i, bytes = min(max(left - from, 0), 16);
-        if (!HG_DBG_INDEX(bytes, 17)) continue;
+        // (its first value's index in the row: at most seven before it, of the row's first 16 bytes)
+        if (bytes > 0 && !HG_DBG_INDEX(fk + static_cast<int>(static_cast<int64_t>(at + from) -
+                                                             reinterpret_cast<int64_t>(p)) / 2 + 7,
+                                       fend + 7))
+          continue;
         copy_16(to + (i == 2 ? 1024u + 16u * g - 16u * lane : 512u * i),
                 bytes > 0 ? reinterpret_cast<const void*>(at + from) : a.ws_h, bytes, weights);
       }
