@@ -125,3 +125,23 @@ def test_a_state_that_does_not_fit_is_refused():
         opt.step(gradients(1))
     equal(one, other)
     assert torch.cuda.is_available()
+
+
+def test_tensors_of_another_device_than_the_current_one():
+    """The step runs on the current device: a table that says another is refused
+    before anything is launched."""
+    torch = torch_cuda()
+    t = {"grad": torch.ones(64, device="cuda"), "master": torch.ones(64, device="cuda"),
+         "m": torch.zeros(64, device="cuda"), "v": torch.zeros(64, device="cuda")}
+    plan = tc.hgemm_adamw_tensors([t])
+    assert plan.device == torch.cuda.current_device()
+    plan.device += 1
+    for stream in (None, torch.cuda.Stream(), 0):
+        with pytest.raises(ValueError, match="current device"):
+            tc.hgemm_adamw(plan, 0.1, stream=stream)
+    done()
+    assert (t["master"] == 1).all() and (t["m"] == 0).all()
+    plan.device -= 1
+    tc.hgemm_adamw(plan, 0.1)
+    done()
+    assert (t["master"] != 1).all()
