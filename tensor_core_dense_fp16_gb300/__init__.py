@@ -40,7 +40,7 @@ __all__ = [
     "HGEMM_CKPT8_GROUP",
     "hgemm_residual_norm_forward", "hgemm_residual_norm_backward", "hgemm_residual_norm_backward_workspace_size",
     "HGEMM_NORM_NONE", "HGEMM_NORM_LAYER", "HGEMM_NORM_RMS",
-    "hgemm_adamw", "hgemm_adamw_check", "hgemm_adamw_tensors", "hgemm_adamw_dynamic", "hgemm_adamw_load", "AdamwTensors", "HGEMM_TYPE_F16",
+    "hgemm_adamw", "hgemm_adamw_rounded", "hgemm_adamw_check", "hgemm_adamw_tensors", "hgemm_adamw_dynamic", "hgemm_adamw_load", "AdamwTensors", "HGEMM_TYPE_F16",
     "HGEMM_TYPE_F32", "HGEMM_ROUND_NEAREST", "HGEMM_ROUND_RANDOM", "hgemm_experts", "hgemm_experts_workspace_size", "HGEMM_EXPERTS_MAX_TOKENS",
     "HGEMM_EXPERTS_MAX_CHOICES", "HGEMM_EXPERTS_MAX", "HGEMM_EXPERTS_MAX_WIDTH",
 ]
@@ -736,13 +736,19 @@ def hgemm_adamw_dynamic(lr: float, grad_scale: float, step: int, skip: bool = Fa
 
 
 def hgemm_adamw(tensors: AdamwTensors, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
-                step: int = 1, grad_scale: float = 1.0, dynamic=None, stream=None,
-                rounding: int = HGEMM_ROUND_NEAREST) -> None:
-    """One AdamW step over the tensors of hgemm_adamw_tensors (see hgemm.h).
-    dynamic: 16 device bytes (hgemm_adamw_dynamic's) that are read when the step
-    runs, or None. rounding: of 8-bit states, HGEMM_ROUND_RANDOM where they are
-    carried over many steps (to the nearest code they stop following their
-    gradients)."""
+                step: int = 1, grad_scale: float = 1.0, dynamic=None, stream=None) -> None:
+    """One AdamW step over the tensors of hgemm_adamw_tensors (see hgemm.h), 8-bit
+    states rounded to nearest: carried over many steps they stop following their
+    gradients, where hgemm_adamw_rounded is for. dynamic: 16 device bytes
+    (hgemm_adamw_dynamic's) that are read when the step runs, or None."""
+    hgemm_adamw_rounded(tensors, lr, beta1, beta2, eps, step, grad_scale, HGEMM_ROUND_NEAREST, dynamic, stream)
+
+
+def hgemm_adamw_rounded(tensors: AdamwTensors, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+                        step: int = 1, grad_scale: float = 1.0, rounding: int = HGEMM_ROUND_RANDOM, dynamic=None,
+                        stream=None) -> None:
+    """hgemm_adamw with a choice of how 8-bit states are rounded, HGEMM_ROUND_*:
+    at random is what training takes (see hgemm.h)."""
     if dynamic is not None and type(dynamic) is not int:
         if not getattr(dynamic, "is_cuda", False):
             raise ValueError("dynamic must be a CUDA tensor")
@@ -755,7 +761,7 @@ def hgemm_adamw(tensors: AdamwTensors, lr: float, beta1: float = 0.9, beta2: flo
                              f"cuda:{torch.cuda.current_device()}")
     _raise_on((_lib or load()).hgemm_adamw_rounded(tensors.table, len(tensors.table), lr, beta1, beta2, eps, step,
                                                    grad_scale, rounding, _ptr(dynamic), _stream(stream)),
-              "hgemm_adamw")
+              "hgemm_adamw_rounded")
 
 
 def hgemm_adamw_load(m, m_scales, v, v_scales, m_out, v_out, n: int, stream=None) -> None:

@@ -435,8 +435,8 @@ class AdamW:
             self.plan = tc.hgemm_adamw_tensors({**t, "grad": g} for t, g in zip(self.tensors, grads))
             held, decays = self._entries()
             self._held = held, self._addresses(held), decays
-        tc.hgemm_adamw(self.plan, self.lr, self.beta1, self.beta2, self.eps, self.steps + 1, grad_scale, dynamic, stream,
-                       tc.HGEMM_ROUND_RANDOM)
+        tc.hgemm_adamw_rounded(self.plan, self.lr, self.beta1, self.beta2, self.eps, self.steps + 1, grad_scale,
+                               tc.HGEMM_ROUND_RANDOM, dynamic, stream)
         self.steps += 1  # (a refused step is none)
 
     def _entries(self):

@@ -29,7 +29,7 @@ def test_refusals(lib):
     for rounding in (-1, 2):
         assert call(empty, rounding) == BAD
     with pytest.raises(tc.HgemmError):
-        tc.hgemm_adamw(tc.AdamwTensors(table(), []), 1e-3, stream=0, rounding=2)
+        tc.hgemm_adamw_rounded(tc.AdamwTensors(table(), []), 1e-3, stream=0, rounding=2)
 
 
 def test_constants_match_the_header():

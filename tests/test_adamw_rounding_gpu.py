@@ -35,7 +35,7 @@ def check_states(tensors, step, grad_scale=1.0, forms=rounded):
 
 
 def run(tensors, step=3, grad_scale=1.0, stream=None):
-    tc.hgemm_adamw(table(tensors), step=step, grad_scale=grad_scale, stream=stream, rounding=RANDOM, **HYPER)
+    tc.hgemm_adamw_rounded(table(tensors), step=step, grad_scale=grad_scale, stream=stream, rounding=RANDOM, **HYPER)
     torch_cuda().cuda.synchronize()
     done()
     check_states(tensors, step, grad_scale)
@@ -84,7 +84,7 @@ def test_zero_infinite_and_nan_groups_and_values_at_the_ends():
         t[name + "_scales"] = Array(np.zeros_like(t[name + "_scales"].host))
     t["grad"] = Array(g)
     for step in range(1, 40):
-        tc.hgemm_adamw(table([(t, d)]), step=step, rounding=RANDOM, **HYPER)
+        tc.hgemm_adamw_rounded(table([(t, d)]), step=step, rounding=RANDOM, **HYPER)
         done()
         check_states([(t, d)], step)
         m, v = t["m"].get(), t["v"].get()
@@ -104,7 +104,7 @@ def test_a_graph_takes_the_devices_step_number():
     with torch.cuda.stream(side):
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph, stream=side):
-            tc.hgemm_adamw(plan, 123.0, 0.9, 0.999, 1e-8, dynamic=device, rounding=RANDOM)
+            tc.hgemm_adamw_rounded(plan, 123.0, 0.9, 0.999, 1e-8, dynamic=device, rounding=RANDOM)
     for step in (1, 2, 70000):
         device.copy_(tc.hgemm_adamw_dynamic(1e-2, 1.0, step))
         graph.replay()
@@ -148,7 +148,7 @@ def test_the_random_numbers_are_even(step):
         g[::64] = 1
         t["grad"] = g
         t = {k: Array(a) for k, a in t.items()}
-        tc.hgemm_adamw(table([(t, 0.0)]), step=step, rounding=RANDOM, **HYPER)
+        tc.hgemm_adamw_rounded(table([(t, 0.0)]), step=step, rounding=RANDOM, **HYPER)
         done()
         codes = t[name].get().astype(np.int64).reshape(-1, 64)[:, 1:]
         assert ((codes == code) | (codes == code + 1)).all()
