@@ -262,7 +262,10 @@ class FeedForward:
 class FeedForwardStack:
     """Blocks one behind the other: what lies between two of them, the norm
     behind the first with its gate and residual scale and the norm in front of
-    the second, is one pass over the rows each way.
+    the second, is one pass over the rows each way. Forward a block's input is
+    the norm of the stream in 32 bits; backward, for w1's gradient, that of the
+    stream as it is kept, rounded to FP16, which is as near as FP16 gradients
+    are.
 
         stack = FeedForwardStack(blocks)
         y = stack(x)
