@@ -652,7 +652,8 @@ HGEMM_API int hgemm_adamw(const hgemm_adamw_tensor *tensors, int64_t count, doub
  *        The random number of a value is computed from its index in its tensor
  *        and the step's number (dynamic's, where that is given): equal calls
  *        give equal results, and alignment and order of the tensors do not
- *        matter. FP32 states are as in hgemm_adamw.
+ *        matter. (A captured step without dynamic has the same number, and rounds
+ *        the same way, at every replay.) FP32 states are as in hgemm_adamw.
  */
 #define HGEMM_ROUND_NEAREST 0
 #define HGEMM_ROUND_RANDOM 1

@@ -754,11 +754,12 @@ def hgemm_adamw_rounded(tensors: AdamwTensors, lr: float, beta1: float = 0.9, be
             raise ValueError("dynamic must be a CUDA tensor")
         if dynamic.numel() * dynamic.element_size() < 16 or not dynamic.is_contiguous():
             raise ValueError("dynamic must have 16 bytes, contiguous")
-    if tensors.device is not None and len(tensors.table):
-        torch = _torch or _import_torch()
-        if tensors.device != torch.cuda.current_device():
-            raise ValueError(f"the tensors are on cuda:{tensors.device}, the current device is "
-                             f"cuda:{torch.cuda.current_device()}")
+    if tensors.device is not None or stream is None:
+        current = (_torch or _import_torch()).cuda.current_device()
+        if tensors.device is not None and tensors.device != current:
+            raise ValueError(f"the tensors are on cuda:{tensors.device}, the current device is cuda:{current}")
+        if stream is None:
+            stream = int(_raw_current_stream(current))
     _raise_on((_lib or load()).hgemm_adamw_rounded(tensors.table, len(tensors.table), lr, beta1, beta2, eps, step,
                                                    grad_scale, rounding, _ptr(dynamic), _stream(stream)),
               "hgemm_adamw_rounded")
