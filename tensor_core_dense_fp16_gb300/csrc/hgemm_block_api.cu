@@ -422,8 +422,9 @@ int hgemm_adamw_rounded(const hgemm_adamw_tensor* tensors, int64_t count, double
   hg::AdamwStep s{};
   s.beta1 = static_cast<float>(beta1), s.rest1 = static_cast<float>(1.0 - beta1);
   s.beta2 = static_cast<float>(beta2), s.rest2 = static_cast<float>(1.0 - beta2);
-  // (the step's reciprocal takes a denominator below 2^-126 for 0, and a value without a gradient gave 0/0)
-  s.eps = eps > 0 ? std::max(static_cast<float>(eps), FLT_MIN) : 0.f, s.gscale = static_cast<float>(grad_scale), s.lr = static_cast<float>(lr);
+  // (the step's reciprocal takes a denominator below 2^-126 for 0, and a value without a gradient would be 0/0)
+  s.eps = eps > 0 ? std::max(static_cast<float>(eps), FLT_MIN) : 0.f;
+  s.gscale = static_cast<float>(grad_scale), s.lr = static_cast<float>(lr);
   s.a = static_cast<float>(lr / (1.0 - std::pow(beta1, t)));
   s.b = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(beta2, t)));
   s.ln1 = static_cast<float>(std::log(beta1)), s.ln2 = static_cast<float>(std::log(beta2));
@@ -435,7 +436,8 @@ int hgemm_adamw_rounded(const hgemm_adamw_tensor* tensors, int64_t count, double
   int n = 0;
   for (int64_t i = 0; i <= count; ++i) {
     if (n == hg::kAdamwTensors || (i == count && n > 0)) {
-      if ((rc = hg::cuda_status(hg::launch_adamw(e, n, s, rounding == HGEMM_ROUND_RANDOM, dev.num_sms, stream))) != HGEMM_OK) return rc;
+      rc = hg::cuda_status(hg::launch_adamw(e, n, s, rounding == HGEMM_ROUND_RANDOM, dev.num_sms, stream));
+      if (rc != HGEMM_OK) return rc;
       n = 0;
     }
     if (i == count || tensors[i].n == 0) continue;

@@ -165,21 +165,26 @@ __global__ void __launch_bounds__(kThreads) experts_router_kernel(const ExpertsA
 // it. Experts come in order, and within one the tokens.
 constexpr int kSlots = kTokens * HGEMM_EXPERTS_MAX_CHOICES;
 constexpr int kEntries = kMost + kSlots / 8;  // a partly filled one per expert, and full ones
+struct Entry {
+  uint32_t expert : 16, first : 10, count : 6;
+};
+static_assert(kMost <= 1 << 16 && kSlots <= 1 << 10, "an entry's parts");
+template <bool FIRST>
 struct Routing {
-  unsigned long long tokens[kMost];  // a bit per token that chose the expert
-  uint16_t list[kSlots];             // the slots, by entry
-  uint16_t token[kSlots];            // and their tokens
-  uint16_t first[kMost];             // where an expert's slots begin in it
-  struct {
-    uint16_t expert, first;
-    int count;
-  } entry[kEntries];
+  uint16_t list[kSlots];               // the slots, by entry
+  uint16_t token[FIRST ? kSlots : 1];  // and their tokens
+  Entry entry[kEntries];
   int entries;
 };
+// What only finding them needs, in the room of the partial sums.
+struct RoutingScratch {
+  unsigned long long tokens[kMost];  // a bit per token that chose the expert
+  uint16_t first[kMost];             // where an expert's slots begin in the list
+};
 
-template <int MT>
-__device__ __forceinline__ void find_entries(Routing& r, const ExpertsArgs& a) {
-  for (int e = threadIdx.x; e < a.E; e += blockDim.x) r.tokens[e] = 0;
+template <int MT, bool FIRST>
+__device__ __forceinline__ void find_entries(Routing<FIRST>& r, RoutingScratch& s, const ExpertsArgs& a) {
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) s.tokens[e] = 0;
   const int slots = a.M * a.k;
   int chosen[kSlots / kThreads];
 #pragma unroll
@@ -190,14 +195,14 @@ __device__ __forceinline__ void find_entries(Routing& r, const ExpertsArgs& a) {
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < kSlots / kThreads; ++j)
-    if (chosen[j] >= 0) atomicOr(&r.tokens[chosen[j]], 1ull << ((static_cast<int>(threadIdx.x) + j * kThreads) / a.k));
+    if (chosen[j] >= 0) atomicOr(&s.tokens[chosen[j]], 1ull << ((static_cast<int>(threadIdx.x) + j * kThreads) / a.k));
   __syncthreads();
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
     int at = 0, n = 0;  // slots and entries of the experts before
     for (int e0 = 0; e0 < a.E; e0 += 32) {
       const int e = e0 + lane;
-      const int count = e < a.E ? __popcll(r.tokens[e]) : 0;
+      const int count = e < a.E ? __popcll(s.tokens[e]) : 0;
       const int runs = (count + 8 * MT - 1) / (8 * MT);
       int both = count | runs << 16, sum = both;  // (1024 slots, 640 entries at most)
 #pragma unroll
@@ -208,12 +213,10 @@ __device__ __forceinline__ void find_entries(Routing& r, const ExpertsArgs& a) {
       const int all = __shfl_sync(0xffffffffu, sum, 31);
       const int first = at + ((sum - both) & 0xFFFF), entry = n + ((sum - both) >> 16);
       if (count > 0) {
-        r.first[e] = static_cast<uint16_t>(first);
-        for (int j = 0; j < runs; ++j) {
-          r.entry[entry + j].expert = static_cast<uint16_t>(e);
-          r.entry[entry + j].first = static_cast<uint16_t>(first + 8 * MT * j);
-          r.entry[entry + j].count = min(count - 8 * MT * j, 8 * MT);
-        }
+        s.first[e] = static_cast<uint16_t>(first);
+        for (int j = 0; j < runs; ++j)
+          r.entry[entry + j] = Entry{static_cast<uint32_t>(e), static_cast<uint32_t>(first + 8 * MT * j),
+                                     static_cast<uint32_t>(min(count - 8 * MT * j, 8 * MT))};
       }
       at += all & 0xFFFF;
       n += all >> 16;
@@ -225,17 +228,17 @@ __device__ __forceinline__ void find_entries(Routing& r, const ExpertsArgs& a) {
   for (int j = 0; j < kSlots / kThreads; ++j) {
     const int i = static_cast<int>(threadIdx.x) + j * kThreads, e = chosen[j];
     if (e < 0) continue;
-    const int token = i / a.k, at = r.first[e] + __popcll(r.tokens[e] & ((1ull << token) - 1));
+    const int token = i / a.k, at = s.first[e] + __popcll(s.tokens[e] & ((1ull << token) - 1));
     r.list[at] = static_cast<uint16_t>(i);
-    r.token[at] = static_cast<uint16_t>(token);
+    if (FIRST) r.token[at] = static_cast<uint16_t>(token);
   }
   __syncthreads();
 }
 
 // What becomes of the sums of one unit: outputs n0 .. n0+per-1 of an entry's
 // slots, `sum(row, column)` over the block's warps. By the threads t of T.
-template <bool FIRST, typename Entry, typename Sum>
-__device__ __forceinline__ void put_unit(const ExpertsArgs& a, const Routing& r, const Entry& e, int split, int n0,
+template <bool FIRST, typename Sum>
+__device__ __forceinline__ void put_unit(const ExpertsArgs& a, const Routing<FIRST>& r, const Entry& e, int split, int n0,
                                          int per, int rows, int t, int T, Sum sum) {
   for (int i = t; i < e.count * per; i += T) {
     const int row = i / per, f = i - row * per, n = n0 + f;
@@ -275,8 +278,8 @@ __device__ __forceinline__ void put_unit(const ExpertsArgs& a, const Routing& r,
 // queue of its own in shared memory, filled by asynchronous copies: registers
 // hold four pieces at most before a warp's scoreboards, six, make it wait for
 // the youngest load instead of the oldest (24 tokens, 8 of 64 experts: 176 us
-// that way, 136 with the queue, both with h in 11 bits; 347 with bulk copies of
-// 1 KB, of which an SM starts one in some 125 cycles). A step is two pieces, 64 values of K per warp
+// that way, 136 with the queue; 347 with bulk copies of 1 KB, of which an SM
+// starts one in some 125 cycles). A step is two pieces, 64 values of K per warp
 // and 128 bytes of a row. A warp's steps of all its units form one sequence, so
 // that the next unit's weights are on their way while one is added up. The
 // second product starts on its weights before the first has ended: who chose
@@ -297,22 +300,29 @@ __device__ __forceinline__ void put_unit(const ExpertsArgs& a, const Routing& r,
 // themselves. A tile of eight columns takes the pairs of up to four tokens, so
 // that an entry of so few needs no second one, and its sums are the same (24
 // tokens 2048 -> 1025, rows at any address: 203 us with two tiles, 197 with one;
-// aligned rows within 1%). With H in 11 bits one token through 2 of 8 experts
-// took 47.2 us in place of 48.7, 24 tokens through 8 of 64 139.6 of 142.8.
+// aligned rows within 1%).
 template <int MT, bool FIRST, bool ANY>
 struct QueueCfg {
   static constexpr int TILES = FIRST ? MT : 2 * MT;  // of eight rows, a step's tokens
   static constexpr int CTAS = TILES < 4 ? 2 : 1;     // per SM
-  static constexpr int DEPTH = TILES < 4 ? 2 : FIRST || ANY ? 3 : 4;
-  static constexpr int BUFFERS = MT == 1 ? 4 : 2;    // of partial sums
+  static constexpr int DEPTH = TILES < 4 ? 2 : 3;
+  static constexpr int BUFFERS = 2;                  // of partial sums
   static constexpr int ROWS = 1024 + (ANY ? 128 : 0);  // of a warp: a step of eight rows
   static constexpr int SLOT = (2 + TILES) * ROWS;      // 16 rows of weights, and the tokens
   static constexpr int PART = kWarps * 8 * MT * 17;  // floats of one buffer
   static constexpr int OFF_ROUTING = BUFFERS * PART * 4;
-  static constexpr int OFF_BAR = (OFF_ROUTING + static_cast<int>(sizeof(Routing)) + 15) / 16 * 16;
+  static constexpr int OFF_BAR = (OFF_ROUTING + static_cast<int>(sizeof(Routing<FIRST>)) + 15) / 16 * 16;
   static constexpr int OFF_MISC = OFF_BAR + 2 * 8 * BUFFERS;
   static constexpr int OFF_QUEUE = (OFF_MISC + 4 + 15) / 16 * 16;
-  static constexpr int SMEM_BYTES = OFF_QUEUE + kWarps * DEPTH * SLOT;
+  static_assert(sizeof(RoutingScratch) <= OFF_ROUTING, "fits the partial sums' room");
+  // Enough that no further CTA fits: units are dealt out to CTAS on each SM, and
+  // an SM that takes one more leaves another idle (one token 52 us in place of
+  // 46.5). And no more than it takes: what is left of an SM's memory is L1, where
+  // the tokens are, and both products' launches divide it alike, or an SM has to
+  // run dry between them. (With four buffers of partial sums and the scratch of
+  // the routing beside them one token took 48.7 us, 24 tokens 142.5.)
+  static constexpr int NEEDED = OFF_QUEUE + kWarps * DEPTH * SLOT, LEAST = 233472 / (CTAS + 1) - 1024 + 16;
+  static constexpr int SMEM_BYTES = NEEDED > LEAST ? NEEDED : LEAST;
   static_assert(CTAS * (SMEM_BYTES + 1024) <= 233472, "the CTAs fit an SM");
 };
 
@@ -334,7 +344,7 @@ __global__ void __launch_bounds__(kThreads + 32, QueueCfg<MT, FIRST, ANY>::CTAS)
   constexpr int DEPTH = Cfg::DEPTH, STEP = kWarps * 2 * kPiece;  // values of K per step
   extern __shared__ __align__(128) uint8_t experts_smem[];
   float* parts = reinterpret_cast<float*>(experts_smem);
-  Routing& r = *reinterpret_cast<Routing*>(experts_smem + Cfg::OFF_ROUTING);
+  Routing<FIRST>& r = *reinterpret_cast<Routing<FIRST>*>(experts_smem + Cfg::OFF_ROUTING);
   const uint32_t full0 = smem_u32(experts_smem + Cfg::OFF_BAR), empty0 = full0 + 8u * Cfg::BUFFERS;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(experts_smem + Cfg::OFF_MISC);
   const Watchdog wd{abort_flag, a.status, a.timeout_ns};
@@ -351,7 +361,7 @@ __global__ void __launch_bounds__(kThreads + 32, QueueCfg<MT, FIRST, ANY>::CTAS)
   } else {
     fence_gpu();
   }
-  find_entries<MT>(r, a);  // (its barriers publish these)
+  find_entries<MT>(r, *reinterpret_cast<RoutingScratch*>(experts_smem), a);  // (its barriers publish these)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int K = FIRST ? a.D : a.F, rows = FIRST ? a.F : a.D;
   const bool gated = FIRST && a.gated;
@@ -684,7 +694,7 @@ cudaError_t product_tiles(const ExpertsArgs& a, int num_sms, cudaStream_t stream
   } else {
     // Half as many: its tokens are pairs of rows, and tiles for all of them leave
     // an SM one block (40 tokens, 5 of 16 experts, 2048 -> 2048: 134 us with as
-    // many as in the first product, 111 with half; 64 tokens, 4 of 8: 82 and 81).
+    // many as in the first product, 110 with half; 64 tokens, 4 of 8: 82 and 77.5).
     if (tiles == 4) return product_with<2, FIRST, ANY>(a, num_sms, stream);
   }
   return product_with<1, FIRST, ANY>(a, num_sms, stream);
