@@ -286,7 +286,7 @@ __device__ __forceinline__ void put_unit(const ExpertsArgs& a, const Routing<FIR
 // what is known since the router, and only the tokens' values have to be waited
 // for. Tokens are copied through L1: every block wants the same few rows, and
 // the L2 lines of one token's row, asked for by all of them, held the first
-// product to 4.4 TB/s (5.3 through L1: 134 MB in 25 us, launched by itself).
+// product to 4.4 TB/s (5.3 through L1, launched by itself).
 //
 // ANY: rows that begin at any even address. The copies are of the aligned 16
 // bytes that a piece lies in, its row's last ones cut at the end (the rest is
